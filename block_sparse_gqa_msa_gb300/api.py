@@ -10,6 +10,7 @@ Names follow the C ABI: msa_build_plan, msa_forward, msa_backward.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -27,6 +28,7 @@ STATUS = {
     0: "MSA_OK", 1: "MSA_ERR_INVALID_ARG", 2: "MSA_ERR_UNSUPPORTED", 3: "MSA_ERR_ALIGNMENT",
     4: "MSA_ERR_WORKSPACE", 5: "MSA_ERR_CUDA", 6: "MSA_ERR_BAD_Q2K", 7: "MSA_ERR_BAD_OFFSETS",
     8: "MSA_ERR_TIMEOUT", 9: "MSA_ERR_CAPACITY", 10: "MSA_ERR_RANGE",
+    11: "MSA_ERR_BAD_PAGE",
 }
 MSA_OK = 0
 
@@ -60,6 +62,26 @@ class MsaPlanOptions(ctypes.Structure):
                 ("reserved", ctypes.c_int32 * 4)]
 
 
+class MsaPagedCacheStruct(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_stride", ctypes.c_int64 * 3),
+                ("v_stride", ctypes.c_int64 * 3), ("num_pages", ctypes.c_int64),
+                ("page_size", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("status", ctypes.c_void_p)]
+
+
+class MsaPagedIndexStruct(ctypes.Structure):
+    _fields_ = [("keys", ctypes.c_void_p), ("key_stride", ctypes.c_int64 * 3),
+                ("means", ctypes.c_void_p), ("num_pages", ctypes.c_int64),
+                ("page_size", ctypes.c_int32), ("heads", ctypes.c_int32), ("dim", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("status", ctypes.c_void_p)]
+
+
+class MsaPageTableStruct(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_void_p), ("stride", ctypes.c_int64), ("rows", ctypes.c_int32),
+                ("width", ctypes.c_int32)]
+
+
 DQ_ACCUM = {"f16": 0, "bf16": 1, "f32": 2}
 O_ACCUM = {"f32": 0, "bf16": 1}
 
@@ -73,6 +95,9 @@ _I32 = ctypes.c_int32
 _SZ = ctypes.c_size_t
 _F = ctypes.c_float
 _PLAN = ctypes.POINTER(MsaPlanStruct)
+_CACHE = ctypes.POINTER(MsaPagedCacheStruct)
+_INDEX = ctypes.POINTER(MsaPagedIndexStruct)
+_TABLE = ctypes.POINTER(MsaPageTableStruct)
 
 SIGNATURES = {
     "msa_status_string": ([_I32], ctypes.c_char_p),
@@ -98,6 +123,13 @@ SIGNATURES = {
     "msa_unpack_bshd": ([_P, _I32, _I32, _I32, _P, _P, _P, _P], _I32),
     "msa_select_workspace_bytes": ([_I64, _I32, _I32, ctypes.POINTER(_SZ)], _I32),
     "msa_select_blocks": ([_P, _P, _I64, _I32, _P, _I32, _I32, _P, _P, _SZ, _P], _I32),
+    "msa_paged_read_status": ([_P, _P], _I32),
+    "msa_paged_append": ([_CACHE, _TABLE, _P, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _I32, _P,
+                          _I32, _I32, _P, _P, _P], _I32),
+    "msa_paged_index": ([_INDEX, _TABLE, _P, _P, _I64, _P, _I64, _P], _I32),
+    "msa_paged_select": ([_INDEX, _TABLE, _P, _P, _I32, _P, _P], _I32),
+    "msa_paged_decode_workspace_bytes": ([_CACHE, _I32, _I32, ctypes.POINTER(_SZ)], _I32),
+    "msa_paged_decode": ([_CACHE, _TABLE, _P, _P, _I32, _F, _P, _P, _P, _P, _SZ, _P], _I32),
 }
 
 
@@ -406,3 +438,288 @@ def msa_select_blocks(iq: torch.Tensor, ik: torch.Tensor, doc_offsets: torch.Ten
                                    1 if force_local else 0, _ptr(q2k), _ptr(workspace),
                                    workspace.numel(), _stream(stream)), "msa_select_blocks")
     return q2k
+
+
+# ---------------------------------------------------------------- paged cache (serving)
+BLOCK = 128
+PAGED_DTYPES = {torch.bfloat16: 0, torch.float16: 1}
+
+
+def _pool(x, name: str, dtypes):
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not x.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if x.dtype not in dtypes:
+        raise TypeError(f"{name} must be one of {tuple(dtypes)}, got {x.dtype}")
+    if x.dim() != 4 or x.numel() == 0:
+        raise ValueError(f"{name} must be [num_pages, page_size, heads, dim]")
+    if x.stride(3) != 1:
+        raise ValueError(f"{name}: a head's channels must be contiguous")
+    # outermost first, every dimension must step over all that the inner ones cover
+    covered = x.shape[3]
+    for stride, n in sorted((x.stride(i), x.shape[i]) for i in range(3)):
+        if n > 1 and stride < covered:
+            raise ValueError(f"{name}: elements overlap (strides {x.stride()})")
+        covered = max(covered, stride * n)
+
+
+def _pool_strides(x):
+    # the stride of a dimension of one element means nothing; any valid one will do
+    return (_I64 * 3)(*(x.stride(i) if x.shape[i] > 1 else x.shape[3] for i in range(3)))
+
+
+class PagedCache:
+    """Keys and values in pages: two tensors [num_pages, page_size, kv_heads,
+    head_dim], bf16 or fp16, any strides with contiguous channels (so pages
+    may also lie head-major).  page_size is a power of two up to 1024,
+    head_dim 64 or 128.  Holds the tensors and a device status word."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor):
+        _pool(k, "k", PAGED_DTYPES)
+        _pool(v, "v", (k.dtype,))
+        if k.shape != v.shape:
+            raise ValueError(f"k {tuple(k.shape)} and v {tuple(v.shape)} must have one shape")
+        if k.device != v.device:
+            raise ValueError("k and v must be on one device")
+        self.k, self.v = k, v
+        self.device, self.dtype = k.device, k.dtype
+        self.num_pages, self.page_size, self.kv_heads, self.head_dim = map(int, k.shape)
+        self.status = torch.zeros(1, dtype=torch.int64, device=k.device)
+        self.struct = MsaPagedCacheStruct(
+            k=k.data_ptr(), v=v.data_ptr(), k_stride=_pool_strides(k), v_stride=_pool_strides(v),
+            num_pages=self.num_pages, page_size=self.page_size, kv_heads=self.kv_heads,
+            head_dim=self.head_dim, dtype=PAGED_DTYPES[k.dtype], status=self.status.data_ptr())
+        # the library's own check of the cache, before the first call
+        paged_decode_workspace_bytes(self, 1, self.kv_heads)
+
+    def ref(self):
+        return ctypes.byref(self.struct)
+
+
+def paged_means_shape(num_pages: int, page_size: int, heads: int, dim: int):
+    """Shape of the block means that belong to index keys in pages."""
+    return num_pages * max(1, page_size // BLOCK), heads, dim
+
+
+class PagedIndex:
+    """Index keys in pages, bf16 [num_pages, page_size, heads, dim] (strides
+    as for PagedCache), and the fp32 means of their 128-key blocks
+    (``paged_means_shape``, contiguous).  Holds both and a status word."""
+
+    def __init__(self, keys: torch.Tensor, means: torch.Tensor):
+        _pool(keys, "keys", (torch.bfloat16,))
+        shape = paged_means_shape(*map(int, keys.shape))
+        _need(means, "means", torch.float32, shape)
+        if keys.device != means.device:
+            raise ValueError("keys and means must be on one device")
+        self.keys, self.means, self.device = keys, means, keys.device
+        self.num_pages, self.page_size, self.heads, self.dim = map(int, keys.shape)
+        self.status = torch.zeros(1, dtype=torch.int64, device=keys.device)
+        self.struct = MsaPagedIndexStruct(
+            keys=keys.data_ptr(), key_stride=_pool_strides(keys), means=means.data_ptr(),
+            num_pages=self.num_pages, page_size=self.page_size, heads=self.heads, dim=self.dim,
+            reserved=0, status=self.status.data_ptr())
+
+    def ref(self):
+        return ctypes.byref(self.struct)
+
+
+def _on(device, **tensors):
+    """Every tensor given is on the cache's device, which is the current one."""
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"the cache is on {device}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} must be on {device}, got {t.device}")
+
+
+def _table(page_table: torch.Tensor) -> MsaPageTableStruct:
+    if not isinstance(page_table, torch.Tensor):
+        raise TypeError("page_table must be a torch.Tensor")
+    if page_table.dtype != torch.int32:
+        raise TypeError(f"page_table must be torch.int32, got {page_table.dtype}")
+    if page_table.dim() != 2 or page_table.numel() == 0:
+        raise ValueError("page_table must be [rows, pages of a row]")
+    rows, width = page_table.shape
+    stride = page_table.stride(0) if rows > 1 else width
+    if (width > 1 and page_table.stride(1) != 1) or stride < width:
+        raise ValueError("page_table: a row's entries must be contiguous, rows must not overlap")
+    return MsaPageTableStruct(pages=page_table.data_ptr(), stride=stride, rows=rows, width=width)
+
+
+def _tokens(x, name: str, dtype, heads: int | None, dim: int):
+    """Token stride of [T, heads, dim] with contiguous tokens."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if x.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {x.dtype}")
+    if x.dim() != 3 or x.shape[2] != dim or (heads is not None and x.shape[1] != heads):
+        raise ValueError(f"{name} must be [T, {heads if heads is not None else 'heads'}, {dim}], "
+                         f"got {tuple(x.shape)}")
+    h = x.shape[1]
+    if x.stride(2) != 1 or (h > 1 and x.stride(1) != dim):
+        raise ValueError(f"{name}: a token's heads must be contiguous")
+    return x.stride(0) if x.shape[0] > 1 else h * dim
+
+
+def _on_stream(stream):
+    """Context in which what a call allocates belongs to the stream it runs on."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def paged_decode_workspace_bytes(cache: PagedCache, rows: int, q_heads: int) -> int:
+    n = _SZ(0)
+    _check(lib().msa_paged_decode_workspace_bytes(cache.ref(), rows, q_heads, ctypes.byref(n)),
+           "msa_paged_decode_workspace_bytes")
+    return int(n.value)
+
+
+def msa_paged_read_status(cache, stream=None, clear: bool = False) -> int:
+    """Synchronising read of the status word of a PagedCache or PagedIndex (0 =
+    OK; the lowest-numbered status otherwise).  ``clear`` resets the word."""
+    code = int(lib().msa_paged_read_status(_ptr(cache.status), _stream(stream)))
+    if clear:
+        with _on_stream(stream):
+            cache.status.zero_()
+    return code
+
+
+def msa_paged_append(cache: PagedCache, k: torch.Tensor, v: torch.Tensor,
+                     page_table: torch.Tensor, row_offsets: torch.Tensor,
+                     start_pos: torch.Tensor, inv_freq: torch.Tensor | None = None,
+                     interleaved: bool = False, q: torch.Tensor | None = None,
+                     q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None,
+                     stream=None):
+    """New tokens into the cache, keys (and queries) rotated by position.
+
+    k, v: [T, kv_heads, head_dim] and q: [T, q_heads, head_dim] of the cache's
+    type, each token contiguous, any token stride (slices of one projection
+    will do).  Row r owns tokens row_offsets[r] .. row_offsets[r+1]-1 (int32
+    [rows + 1]), at positions from start_pos[r] (int32 [rows]) on; tokens at
+    row_offsets[rows] and behind are padding and left alone.  page_table:
+    int32 [rows, width].  inv_freq: fp32 [rotary_dim / 2], or None for no
+    rotation; pairs are channels (i, i + rotary_dim / 2), or (2 i, 2 i + 1)
+    when ``interleaved``.  Returns (q_out, k_out): the rotated queries (None
+    without q; q itself may be given as q_out) and, where a k_out [T,
+    kv_heads, head_dim] is given, the rotated keys.  Padding rows of both are
+    left as they were.  Not differentiable."""
+    dt, dim = cache.dtype, cache.head_dim
+    table = _table(page_table)
+    rows = table.rows
+    ks = _tokens(k, "k", dt, cache.kv_heads, dim)
+    vs = _tokens(v, "v", dt, cache.kv_heads, dim)
+    T = k.shape[0]
+    if v.shape[0] != T:
+        raise ValueError(f"k has {T} tokens, v {v.shape[0]}")
+    _need(row_offsets, "row_offsets", torch.int32, (rows + 1,))
+    _need(start_pos, "start_pos", torch.int32, (rows,))
+    qs = heads = rot = 0
+    if q is not None:
+        qs = _tokens(q, "q", dt, None, dim)
+        heads = q.shape[1]
+        if q.shape[0] != T:
+            raise ValueError(f"k has {T} tokens, q {q.shape[0]}")
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    if inv_freq is not None:
+        rot = 2 * inv_freq.numel()
+        _need(inv_freq, "inv_freq", torch.float32, (rot // 2,))
+    _on(cache.device, k=k, v=v, q=q, page_table=page_table, row_offsets=row_offsets,
+        start_pos=start_pos, inv_freq=inv_freq, q_out=q_out, k_out=k_out)
+    if q is not None:
+        if q_out is None:
+            with _on_stream(stream):
+                q_out = torch.empty((T, heads, dim), dtype=dt, device=cache.device)
+        _need(q_out, "q_out", dt, (T, heads, dim))
+    if k_out is not None:
+        _need(k_out, "k_out", dt, (T, cache.kv_heads, dim))
+    _check(lib().msa_paged_append(
+        cache.ref(), ctypes.byref(table), row_offsets.data_ptr(), start_pos.data_ptr(), T,
+        k.data_ptr(), ks, v.data_ptr(), vs, None if q is None else q.data_ptr(), qs, heads,
+        None if inv_freq is None else inv_freq.data_ptr(), rot, 1 if interleaved else 0,
+        None if q_out is None else q_out.data_ptr(), None if k_out is None else k_out.data_ptr(),
+        _stream(stream)), "msa_paged_append")
+    return q_out, k_out
+
+
+def msa_paged_index(index: PagedIndex, ik: torch.Tensor, page_table: torch.Tensor,
+                    row_offsets: torch.Tensor, start_pos: torch.Tensor, stream=None) -> None:
+    """New tokens' index keys (bf16 [T, heads, dim], each token contiguous)
+    into their pages, and the means of the blocks they fall in.  Rows,
+    positions and padding as for ``msa_paged_append``."""
+    table = _table(page_table)
+    s = _tokens(ik, "ik", torch.bfloat16, index.heads, index.dim)
+    _need(row_offsets, "row_offsets", torch.int32, (table.rows + 1,))
+    _need(start_pos, "start_pos", torch.int32, (table.rows,))
+    _on(index.device, ik=ik, page_table=page_table, row_offsets=row_offsets, start_pos=start_pos)
+    _check(lib().msa_paged_index(index.ref(), ctypes.byref(table), row_offsets.data_ptr(),
+                                 start_pos.data_ptr(), ik.shape[0], ik.data_ptr(), s,
+                                 _stream(stream)), "msa_paged_index")
+
+
+def msa_paged_select(index: PagedIndex, iq: torch.Tensor, page_table: torch.Tensor,
+                     kv_len: torch.Tensor, force_local: bool = True,
+                     q2k: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """q2k int32 [heads, rows, 16] for the newest token of each row from its
+    index query (bf16 [rows, heads, dim]) and the cached block means; the
+    rules of ``msa_select_blocks``.  kv_len: int32 [rows], the new token
+    included, 0 for a row that is not in use."""
+    table = _table(page_table)
+    rows = table.rows
+    _need(iq, "iq", torch.bfloat16, (rows, index.heads, index.dim))
+    _need(kv_len, "kv_len", torch.int32, (rows,))
+    _on(index.device, iq=iq, page_table=page_table, kv_len=kv_len, q2k=q2k)
+    if q2k is None:
+        with _on_stream(stream):
+            q2k = torch.empty((index.heads, rows, TOPK), dtype=torch.int32, device=index.device)
+    _need(q2k, "q2k", torch.int32, (index.heads, rows, TOPK))
+    _check(lib().msa_paged_select(index.ref(), ctypes.byref(table), kv_len.data_ptr(),
+                                  iq.data_ptr(), 1 if force_local else 0, q2k.data_ptr(),
+                                  _stream(stream)), "msa_paged_select")
+    return q2k
+
+
+def msa_paged_decode(cache: PagedCache, q: torch.Tensor, page_table: torch.Tensor,
+                     kv_len: torch.Tensor, softmax_scale: float,
+                     q2k: torch.Tensor | None = None, o: torch.Tensor | None = None,
+                     lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                     stream=None):
+    """Attention of one token of each row over the cache: (O [rows, q_heads,
+    head_dim], LSE fp32 [rows, q_heads]).
+
+    q: [rows, q_heads, head_dim] of the cache's type, up to 16 query heads a
+    key head; kv_len: int32 [rows], keys that each row attends (0: none, O = 0
+    and LSE = -inf); q2k: int32 [kv_heads, rows, 16], or None for every key.
+    A workspace serves one call at a time.  Not differentiable."""
+    table = _table(page_table)
+    rows = table.rows
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be [rows, q_heads, head_dim]")
+    heads = q.shape[1]
+    shape = (rows, heads, cache.head_dim)
+    _need(q, "q", cache.dtype, shape)
+    _need(kv_len, "kv_len", torch.int32, (rows,))
+    if q2k is not None:
+        _need(q2k, "q2k", torch.int32, (cache.kv_heads, rows, TOPK))
+    _on(cache.device, q=q, page_table=page_table, kv_len=kv_len, q2k=q2k, o=o, lse=lse,
+        workspace=workspace)
+    if o is None or lse is None or workspace is None:
+        with _on_stream(stream):
+            if o is None:
+                o = torch.empty_like(q)
+            if lse is None:
+                lse = torch.empty((rows, heads), dtype=torch.float32, device=q.device)
+            if workspace is None:
+                workspace = torch.empty(paged_decode_workspace_bytes(cache, rows, heads),
+                                        dtype=torch.uint8, device=q.device)
+    _need(o, "o", cache.dtype, shape)
+    _need(lse, "lse", torch.float32, (rows, heads))
+    _need(workspace, "workspace", torch.uint8, (workspace.numel(),))
+    _check(lib().msa_paged_decode(
+        cache.ref(), ctypes.byref(table), kv_len.data_ptr(), q.data_ptr(), heads,
+        float(softmax_scale), None if q2k is None else q2k.data_ptr(), o.data_ptr(),
+        lse.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream(stream)),
+        "msa_paged_decode")
+    return o, lse

@@ -64,9 +64,12 @@ typedef enum msa_status {
   MSA_ERR_BAD_OFFSETS = 7,  /* device: doc_offsets not 0 < ... strictly up .. T */
   MSA_ERR_TIMEOUT = 8,      /* device: a bounded pipeline wait gave up         */
   MSA_ERR_CAPACITY = 9,     /* device: a plan table exceeded its capacity      */
-  MSA_ERR_RANGE = 10        /* device warning: the last backward's 16-bit dQ
+  MSA_ERR_RANGE = 10,       /* device warning: the last backward's 16-bit dQ
                                pool overflowed (dQ holds inf / nan); rerun it
                                with MSA_DQ_ACCUM_BF16 or MSA_DQ_ACCUM_F32      */
+  MSA_ERR_BAD_PAGE = 11     /* device: a page-table entry that is needed lies
+                               outside the pool, or a position or a length
+                               outside its row of the page table              */
 } msa_status;
 
 /* Human-readable name of a status code (static string). */
@@ -347,6 +350,181 @@ msa_status msa_select_blocks(const void* iq, const void* ik, int64_t T, int32_t 
                              const int32_t* doc_offsets, int32_t num_docs, int32_t force_local,
                              int32_t* q2k, void* workspace, size_t workspace_bytes,
                              msa_stream_t stream);
+
+/*
+ * Serving: a paged key-value cache
+ * --------------------------------
+ * A model trained with this attention is run token by token from a cache in
+ * pages.  A step of a batch of rows (sequences) is
+ *
+ *   msa_paged_append   rotate the new tokens' keys (and queries) by their
+ *                      positions, write keys and values into the cache
+ *   msa_paged_index    write the new tokens' index keys, renew block means
+ *   msa_paged_select   the top-16 blocks of each row's newest token (q2k)
+ *   msa_paged_decode   attention of each row's newest token over the cache:
+ *                      over all keys, or over the blocks of q2k
+ *
+ * A prompt goes through append and index in one call for all its tokens; the
+ * rotated queries and keys that append hands back go through
+ * msa_select_blocks, msa_build_plan and msa_forward.
+ *
+ * Rows and pages.  Token j of row r lives in page page_table[r][j / S], slot
+ * j % S, S the page size.  A row's table entries past its tokens are never
+ * read.  Pages may be shared between rows for reading.  A page id outside
+ * [0, num_pages) that is needed, a position or length outside the row's
+ * table, sets MSA_ERR_BAD_PAGE in the status word and what it concerns is
+ * left out as each call says; nothing outside the given buffers is touched.
+ *
+ * Status.  `status` is a device word of the caller's, zero at first, to which
+ * the calls OR (1 << msa_status) (msa_paged_read_status reads it); it is
+ * never cleared by the library, and no call does less because it is set.
+ *
+ * Calls are asynchronous on the stream, allocate nothing and can be captured
+ * into a CUDA graph; sizes that change from step to step (positions, lengths)
+ * are read on the device.  Inputs and outputs must not overlap except where a
+ * call says so.
+ */
+typedef enum msa_dtype { MSA_BF16 = 0, MSA_F16 = 1 } msa_dtype;
+
+/* Keys and values in pages, each [num_pages][page_size][kv_heads][head_dim]
+ * with the given strides (in elements: of a page, of a token in a page, of a
+ * head; a head's channels are contiguous), so head-major pages work as well.
+ * page_size is a power of two up to 1024, kv_heads 1 .. 64, head_dim 64 or
+ * 128; strides are positive multiples of 8, k and v 16-byte aligned. */
+typedef struct msa_paged_cache {
+  void* k;
+  void* v;
+  int64_t k_stride[3];
+  int64_t v_stride[3];
+  int64_t num_pages;
+  int32_t page_size;
+  int32_t kv_heads;
+  int32_t head_dim;
+  int32_t dtype;       /* an msa_dtype */
+  int64_t* status;     /* device word */
+} msa_paged_cache;
+
+/* Index keys in pages, bf16 [num_pages][page_size][heads][dim] with strides
+ * as above (dim 8, 16, .. 128; heads 1 .. 64; page_size a power of two up to
+ * 1024), and the means of 128-key blocks, fp32 [slots][heads][dim]
+ * contiguous, slots = num_pages * max(1, page_size / 128).  A block's mean is
+ * kept with the page of the last key it has so far: slot = page id, or for
+ * pages of more than 128 tokens page id * (page_size / 128) + block in page.
+ * Rows that share a page thus share the means of the blocks that end in it. */
+typedef struct msa_paged_index_cache {
+  void* keys;
+  int64_t key_stride[3];
+  float* means;
+  int64_t num_pages;
+  int32_t page_size;
+  int32_t heads;
+  int32_t dim;
+  int32_t reserved;
+  int64_t* status;
+} msa_paged_index_cache;
+
+/* Page table of a call: int32 [rows][width] device, rows `stride` entries
+ * apart (stride >= width); 1 <= rows <= 65536, 1 <= width,
+ * width * page_size <= 2^30. */
+typedef struct msa_page_table {
+  const int32_t* pages;
+  int64_t stride;
+  int32_t rows;
+  int32_t width;
+} msa_page_table;
+
+/* Synchronises the stream and returns the lowest-numbered status set in the
+ * device word (MSA_OK if none). */
+msa_status msa_paged_read_status(const int64_t* status, msa_stream_t stream);
+
+/*
+ * Append.  The call's tokens are compact: row r owns tokens row_offsets[r]
+ * .. row_offsets[r+1]-1, which go to positions start_pos[r], start_pos[r]+1,
+ * ...  Tokens at row_offsets[rows] and behind (padding of a captured batch)
+ * are skipped: nothing is read for them nor written.
+ *   k, v   [T][kv_heads][head_dim] of the cache's type, tokens k_stride /
+ *          v_stride elements apart (multiples of 8)
+ *   q      [T][q_heads][head_dim] or NULL, tokens q_stride elements apart
+ *   inv_freq fp32 [rotary_dim / 2] device, or NULL for no rotation
+ *          (rotary_dim is then ignored); rotary_dim a multiple of 16, at most
+ *          head_dim
+ *   interleaved 0: channel i pairs with i + rotary_dim / 2; 1: 2 i with 2 i + 1
+ *   q_out  contiguous [T][q_heads][head_dim], rotated q (required with q; may
+ *          be q itself when q is contiguous)
+ *   k_out  contiguous [T][kv_heads][head_dim] rotated keys, or NULL
+ * Pair i of a token at position p turns by p * inv_freq[i] (the product and
+ * its reduction in 64 bits, the rotation in 32, one rounding); channels from
+ * rotary_dim on are copied.  A token whose place is bad is skipped
+ * (MSA_ERR_BAD_PAGE); offsets that do not start at 0, decrease or pass T set
+ * MSA_ERR_BAD_OFFSETS, and tokens that no row owns are skipped.  Two tokens
+ * of one call must not have the same place.  1 <= T <= 2^20.
+ */
+msa_status msa_paged_append(const msa_paged_cache* cache, const msa_page_table* table,
+                            const int32_t* row_offsets, const int32_t* start_pos, int64_t T,
+                            const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                            const void* q, int64_t q_stride, int32_t q_heads,
+                            const float* inv_freq, int32_t rotary_dim, int32_t interleaved,
+                            void* q_out, void* k_out, msa_stream_t stream);
+
+/*
+ * Index keys of new tokens (tokens, rows and padding as for append):
+ *   ik  bf16 [T][heads][dim], tokens ik_stride elements apart (a multiple of 8)
+ * Writes them into their pages and the mean of every block that got a token:
+ * the fp32 sum of the block's keys up to the row's last new token, in
+ * order of position, divided by their number - the summary that
+ * msa_select_blocks forms.  A block one of whose pages is bad is left out
+ * with all its tokens (MSA_ERR_BAD_PAGE).
+ */
+msa_status msa_paged_index(const msa_paged_index_cache* cache, const msa_page_table* table,
+                           const int32_t* row_offsets, const int32_t* start_pos, int64_t T,
+                           const void* ik, int64_t ik_stride, msa_stream_t stream);
+
+/*
+ * Block selection for one new token of each row, the one at kv_len[r] - 1:
+ * scores, candidates, force_local and ties as for msa_select_blocks, with the
+ * same fp32 operations in the same order, so that both calls choose the same
+ * blocks for the same keys.
+ *   iq      bf16 [rows][heads][dim] contiguous; finite
+ *   kv_len  int32 [rows] device, tokens of each row, the new one included;
+ *           0 marks a row that is not in use (its slots are all -1)
+ *   q2k     int32 [heads][rows][16] (written)
+ * The means of the scored blocks must be there (msa_paged_index).  A block
+ * whose page is bad is not chosen (MSA_ERR_BAD_PAGE); a row with a bad length
+ * gets -1 in all slots.
+ */
+msa_status msa_paged_select(const msa_paged_index_cache* cache, const msa_page_table* table,
+                            const int32_t* kv_len, const void* iq, int32_t force_local,
+                            int32_t* q2k, msa_stream_t stream);
+
+/* Bytes of decode workspace for `rows` rows and q_heads query heads (host
+ * only; an upper bound for every device of this kind). */
+msa_status msa_paged_decode_workspace_bytes(const msa_paged_cache* cache, int32_t rows,
+                                            int32_t q_heads, size_t* bytes);
+
+/*
+ * Attention of one token of each row over the cache.
+ *   q       [rows][q_heads][head_dim] contiguous, of the cache's type;
+ *           q_heads = kv_heads * n, 1 <= n <= 16; query head h reads key head
+ *           h / n
+ *   kv_len  int32 [rows] device: row r attends keys 0 .. kv_len[r]-1 (the
+ *           new token's key, at kv_len[r]-1, has been appended)
+ *   q2k     int32 [kv_heads][rows][16] device, or NULL: of these keys only
+ *           those whose block (key / 128) is in the set q2k[g][r][:], -1 = an
+ *           unused slot.  Other values outside [0, blocks of the row) set
+ *           MSA_ERR_BAD_Q2K and are left out.
+ *   o       [rows][q_heads][head_dim] contiguous, of the cache's type
+ *   lse     fp32 [rows][q_heads] natural log
+ *   workspace  device, 16-byte aligned, >= msa_paged_decode_workspace_bytes;
+ *           needs no initialisation; calls that may overlap in time need one
+ *           each
+ * A row that sees no key (kv_len 0, no slot used) gets O = 0, LSE = -inf; so
+ * does a row whose length is bad.  Keys in a bad page are left out.  What
+ * lies in a page past a row's length does not matter, whatever it is.
+ */
+msa_status msa_paged_decode(const msa_paged_cache* cache, const msa_page_table* table,
+                            const int32_t* kv_len, const void* q, int32_t q_heads,
+                            float softmax_scale, const int32_t* q2k, void* o, float* lse,
+                            void* workspace, size_t workspace_bytes, msa_stream_t stream);
 
 /*
  * Kernel timing for benchmarks.  While enabled, every kernel the library

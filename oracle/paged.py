@@ -1,0 +1,147 @@
+"""The paged-cache operators in fp64, written out row by row - TEST
+INFRASTRUCTURE (used by the tests only; the product never imports it).
+
+Definitions (include/msa.h, section "Serving: a paged key-value cache").
+Caches are float64 arrays [pages, page_size, heads, dim]; token j of row r is
+cache[table[r, j // page_size], j % page_size].  All arguments are numpy
+arrays (or ints), all results float64.
+"""
+from __future__ import annotations
+
+import numpy as np
+
+BLOCK, SLOTS = 128, 16
+
+
+def gather(cache, table_row, lo: int, hi: int) -> np.ndarray:
+    """Tokens lo .. hi-1 of a row, [hi - lo, heads, dim]."""
+    j = np.arange(lo, hi)
+    return cache[np.asarray(table_row)[j // cache.shape[1]], j % cache.shape[1]]
+
+
+def rotate(x, pos, inv_freq, interleaved: bool) -> np.ndarray:
+    """x [n, heads, dim] at positions pos [n]: pair i turns by pos * inv_freq[i]."""
+    y = np.array(x, dtype=np.float64)
+    half = len(inv_freq)
+    for i in range(half):
+        a, b = (2 * i, 2 * i + 1) if interleaved else (i, i + half)
+        angle = np.asarray(pos, dtype=np.float64)[:, None] * float(inv_freq[i])
+        c, s = np.cos(angle), np.sin(angle)
+        u, v = np.array(x[..., a], np.float64), np.array(x[..., b], np.float64)
+        y[..., a], y[..., b] = u * c - v * s, v * c + u * s
+    return y
+
+
+def append(k_cache, v_cache, k, v, table, offs, start, inv_freq=None, interleaved=False, q=None):
+    """(k_cache, v_cache, q_rot, k_rot) after the call; rows of q_rot and k_rot
+    that no row owns are NaN (not written)."""
+    kc, vc = k_cache.copy(), v_cache.copy()
+    S = kc.shape[1]
+    freq = [] if inv_freq is None else inv_freq
+    k_rot = np.full(k.shape, np.nan)
+    q_rot = None if q is None else np.full(q.shape, np.nan)
+    for r in range(len(start)):
+        for t in range(offs[r], offs[r + 1]):
+            p = int(start[r]) + t - int(offs[r])
+            k_rot[t] = rotate(k[t:t + 1], [p], freq, interleaved)[0]
+            if q is not None:
+                q_rot[t] = rotate(q[t:t + 1], [p], freq, interleaved)[0]
+            kc[table[r, p // S], p % S] = k_rot[t]
+            vc[table[r, p // S], p % S] = v[t]
+    return kc, vc, q_rot, k_rot
+
+
+def mean_slot(page: int, last: int, S: int) -> int:
+    """Where the mean of the block whose last key is at position ``last`` is kept."""
+    return page if S <= BLOCK else page * (S // BLOCK) + last % S // BLOCK
+
+
+def index(keys, means, ik, table, offs, start):
+    """(keys, means) after the call."""
+    keys, means = keys.copy(), means.copy()
+    S = keys.shape[1]
+    for r in range(len(start)):
+        p0, p1 = int(start[r]), int(start[r]) + int(offs[r + 1]) - int(offs[r])
+        for p in range(p0, p1):
+            keys[table[r, p // S], p % S] = ik[offs[r] + p - p0]
+        if p1 == p0:
+            continue
+        for b in range(p0 // BLOCK, (p1 - 1) // BLOCK + 1):
+            end = min(b * BLOCK + BLOCK, p1)
+            at = mean_slot(table[r, (end - 1) // S], end - 1, S)
+            means[at] = gather(keys, table[r], b * BLOCK, end).mean(0)
+    return keys, means
+
+
+def visible(n: int, slots=None) -> np.ndarray:
+    """Positions that a row of n keys sees: all, or those in the slots' blocks."""
+    j = np.arange(n)
+    return j if slots is None else j[np.isin(j // BLOCK, [int(x) for x in slots if x != -1])]
+
+
+def decode(k_cache, v_cache, q, table, lens, scale, q2k=None):
+    """(O [rows, heads, dim], LSE [rows, heads])."""
+    rows, heads, dim = q.shape
+    kv = k_cache.shape[2]
+    share = heads // kv
+    O = np.zeros((rows, heads, dim))
+    L = np.full((rows, heads), -np.inf)
+    for r in range(rows):
+        n = int(lens[r])
+        if n == 0:
+            continue
+        K, V = gather(k_cache, table[r], 0, n), gather(v_cache, table[r], 0, n)
+        for g in range(kv):
+            j = visible(n, None if q2k is None else q2k[g, r])
+            if j.size == 0:
+                continue
+            h = slice(g * share, (g + 1) * share)
+            s = scale * (q[r, h] @ K[j, g].T)
+            top = s.max(1, keepdims=True)
+            p = np.exp(s - top)
+            z = p.sum(1, keepdims=True)
+            O[r, h] = (p / z) @ V[j, g]
+            L[r, h] = (top + np.log(z))[:, 0]
+    return O, L
+
+
+def decode_bounds(k_cache, v_cache, q, table, lens, scale, step: float, tiny: float, q2k=None):
+    """Element-wise error bounds (O, LSE) of a kernel that keeps scores and
+    states in fp32 and rounds weights and output once to a type of relative
+    half step ``step`` and smallest half step ``tiny``.
+
+    u = 2^-24.  A score is a chain of dim fp32 products and sums and one
+    scaling (of a constant rounded twice): |ds| <= (dim + 4) u scale sum |q||k|.
+    2^x and the differences x - m add 8 u and 2 u |x - m|, |x - m| <= 2 max|s|
+    / ln 2 + |ds|; a rescaling of the state (one at most for each 16 keys, and
+    one for each join, 400 at most) adds 4 u, a sum over n keys n u.  So
+    a weight and the normaliser are each off by e (relative), O by twice that
+    times sum p|v|; the weight's rounding adds step * sum p|v| (and tiny for
+    each weight below the normal range, against a largest weight of 1), the
+    output's step * |O| + tiny.  LSE: e, plus the sum's and logarithm's roundings."""
+    u = 2.0 ** -24
+    O, L = decode(k_cache, v_cache, q, table, lens, scale, q2k)
+    BO, BL = np.zeros_like(O), np.zeros_like(L)
+    rows, heads, dim = q.shape
+    share = heads // k_cache.shape[2]
+    for r in range(rows):
+        n = int(lens[r])
+        if n == 0:
+            continue
+        K, V = gather(k_cache, table[r], 0, n), gather(v_cache, table[r], 0, n)
+        for g in range(k_cache.shape[2]):
+            j = visible(n, None if q2k is None else q2k[g, r])
+            if j.size == 0:
+                continue
+            h = slice(g * share, (g + 1) * share)
+            s = scale * (q[r, h] @ K[j, g].T)
+            ds = (dim + 4) * u * scale * (np.abs(q[r, h]) @ np.abs(K[j, g]).T).max(1)
+            biggest = np.abs(s).max(1)
+            m = j.size
+            e = ds + u * (8 + 4 * biggest) + u * (4 * (m / 16 + 400) + m)
+            p = np.exp(s - L[r, h][:, None])
+            pv = p @ np.abs(V[j, g])
+            BO[r, h] = ((2 * e + step) * 1.01)[:, None] * pv + step * np.abs(O[r, h]) + tiny \
+                + m * tiny * np.abs(V[j, g]).max() * np.exp(s.max(1) - L[r, h])[:, None]
+            BL[r, h] = 1.01 * e + 4 * u * (np.abs(L[r, h]) + biggest + np.log(m) + 1)
+    return O, L, BO, BL

@@ -1,0 +1,701 @@
+"""The paged-cache operators on the GPU against their fp64 statement
+(oracle/paged.py), and against the training path where both compute the same.
+
+Error bounds are element-wise and derived (u = 2^-24, h = half a step of the
+cache's type relative to the value: bf16 2^-8, fp16 2^-11):
+  rotation  an angle's turns are rounded once to fp32 (2 f <= 1: pi 2^-25) and
+            sine and cosine are good to 2 u: 2^-22 absolute; with the products'
+            and the sum's roundings d = 2^-21 (|x| + |y|), then h (|result| + d)
+  means     n - 1 sums and a division: (n + 1) u mean|x|
+  attention oracle.paged.decode_bounds
+"""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from block_sparse_gqa_msa_gb300 import api, inputs
+from oracle import paged
+from tests.helpers import check_lse, check_o
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+U = 2.0 ** -24
+BF, FP = torch.bfloat16, torch.float16
+HALF = {BF: 2.0 ** -8, FP: 2.0 ** -11}
+TINY = {BF: 2.0 ** -134, FP: 2.0 ** -25}  # half the smallest step
+
+
+def _np(x):
+    return x.detach().double().cpu().numpy()
+
+
+def _i32(x):
+    return torch.as_tensor(np.asarray(x), dtype=torch.int32, device=DEV)
+
+
+def _pages(rng, lens, S, spare=3, width=None):
+    """(pool size, table [rows, width] with -1 where a row has no page)."""
+    need = [-(-n // S) for n in lens]
+    pool = sum(need) + spare
+    order = rng.permutation(pool)
+    table = np.full((len(lens), width or max(max(need), 1) + 2), -1, dtype=np.int64)
+    at = 0
+    for r, n in enumerate(need):
+        table[r, :n] = order[at:at + n]
+        at += n
+    return pool, table
+
+
+def _randn(gen, shape, dtype=torch.float32):
+    return torch.randn(shape, generator=gen, device=DEV).to(dtype)
+
+
+def _pool(gen, pool, S, heads, dim, dtype, head_major=False):
+    if head_major:
+        return _randn(gen, (pool, heads, S, dim), dtype).transpose(1, 2)
+    return _randn(gen, (pool, S, heads, dim), dtype)
+
+
+def _gen(seed):
+    return torch.Generator(device=DEV).manual_seed(seed)
+
+
+def _within(got, ref, bound, what):
+    over = np.abs(got - ref) - bound
+    assert not np.isnan(got).any(), f"{what}: NaN"
+    worst = np.unravel_index(np.argmax(over), over.shape)
+    assert over[worst] <= 0, (f"{what}: {got[worst]} for {ref[worst]} at {worst}, bound "
+                              f"{bound[worst]:.3e}")
+
+
+def _rot_bound(x, ref, rot, inter, dt):
+    """Bound of a rotated tensor; channels past rot are copied exactly."""
+    part = np.array(x)
+    half = rot // 2
+    if inter:
+        part[..., 0:rot:2], part[..., 1:rot:2] = x[..., 1:rot:2], x[..., 0:rot:2]
+    else:
+        part[..., :half], part[..., half:rot] = x[..., half:rot], x[..., :half]
+    d = 2.0 ** -21 * (np.abs(x) + np.abs(part))
+    b = HALF[dt] * (np.abs(ref) + d) + d + TINY[dt]
+    b[..., rot:] = 0
+    return b
+
+
+# ------------------------------------------------------------------ append
+def _append_case(dt, dim, kv, heads, S, rot, inter, fresh, start, pad, seed, head_major=False,
+                 fused=False, theta=10000.0):
+    rng, gen = np.random.default_rng(seed), _gen(seed)
+    pool, table = _pages(rng, [f + s for f, s in zip(fresh, start)], S)
+    offs = np.concatenate([[0], np.cumsum(fresh)])
+    T = int(offs[-1]) + pad
+    kc, vc = (_pool(gen, pool, S, kv, dim, dt, head_major) for _ in range(2))
+    if fused:  # one projection's output, sliced
+        qkv = _randn(gen, (T, heads + 2 * kv, dim), dt)
+        q, k, v = qkv[:, :heads], qkv[:, heads:heads + kv], qkv[:, heads + kv:]
+    else:
+        q, k, v = (_randn(gen, (T, h, dim), dt) for h in (heads, kv, kv))
+    freq = torch.tensor(theta ** (-np.arange(0, rot, 2) / max(rot, 1)), dtype=torch.float32,
+                        device=DEV) if rot else None
+    ref = paged.append(_np(kc), _np(vc), _np(k), _np(v), table, offs, start,
+                       None if freq is None else _np(freq), inter, _np(q))
+    cache = api.PagedCache(kc, vc)
+    k_out = torch.full((T, kv, dim), 7.0, dtype=dt, device=DEV)
+    q_out = torch.full((T, heads, dim), 7.0, dtype=dt, device=DEV)
+    before = _np(kc)
+    api.msa_paged_append(cache, k, v, _i32(table), _i32(offs), _i32(start), inv_freq=freq,
+                         interleaved=inter, q=q, q_out=q_out, k_out=k_out)
+    torch.cuda.synchronize()
+    assert api.msa_paged_read_status(cache) == 0
+    kc2, vc2, q_ref, k_ref = ref
+    n = int(offs[-1])
+    assert (_np(q_out)[n:] == 7).all() and (_np(k_out)[n:] == 7).all()
+    _within(_np(q_out)[:n], q_ref[:n], _rot_bound(_np(q)[:n], q_ref[:n], rot, inter, dt), "q")
+    _within(_np(k_out)[:n], k_ref[:n], _rot_bound(_np(k)[:n], k_ref[:n], rot, inter, dt), "k")
+    assert np.array_equal(_np(vc), vc2)
+    # the cache holds exactly the rotated keys handed back, and is unchanged elsewhere
+    want = before
+    for r in range(len(start)):
+        for t in range(offs[r], offs[r + 1]):
+            p = start[r] + t - offs[r]
+            want[table[r, p // S], p % S] = _np(k_out)[t]
+    assert np.array_equal(_np(kc), want)
+
+
+@pytest.mark.parametrize("dt,dim,kv,heads,S,rot,inter,fused,head_major", [
+    (BF, 128, 4, 64, 128, 64, False, False, False),
+    (BF, 128, 4, 64, 16, 128, True, True, False),
+    (FP, 64, 8, 24, 32, 64, False, False, True),
+    (FP, 128, 1, 7, 1, 32, True, True, True),
+    (BF, 64, 3, 3, 1024, 16, False, True, False),
+    (BF, 128, 2, 2, 64, 0, False, False, False),
+])
+def test_append_matches_fp64(dt, dim, kv, heads, S, rot, inter, fused, head_major):
+    _append_case(dt, dim, kv, heads, S, rot, inter, [1, 0, 130, 3, 17], [5, 9, 0, 1000, 127], 4,
+                 seed=S + rot, fused=fused, head_major=head_major)
+
+
+def test_append_one_token_per_row_many_rows():
+    rng = np.random.default_rng(5)
+    start = rng.integers(0, 40, 1500).tolist()
+    fresh = (rng.random(1500) < 0.9).astype(int).tolist()
+    _append_case(BF, 64, 1, 2, 8, 32, False, fresh, start, 1, seed=6)
+
+
+def test_append_one_token():
+    _append_case(BF, 128, 4, 64, 64, 64, False, [1], [0], 0, seed=7)
+    _append_case(FP, 128, 4, 64, 64, 64, True, [1], [777], 0, seed=8)
+
+
+def test_append_wide_tokens_take_several_rounds():
+    _append_case(BF, 128, 64, 256, 16, 128, False, [3], [2], 0, seed=9)
+
+
+def test_append_far_positions():
+    # every entry of the table names the same few pages: only the last position is written
+    S, pos = 1024, [1_000_003, 99_999_999]
+    gen = _gen(11)
+    kc, vc = (_pool(gen, 4, S, 2, 128, BF) for _ in range(2))
+    q, k, v = (_randn(gen, (2, h, 128), BF) for h in (4, 2, 2))
+    width = max(pos) // S + 1
+    table = torch.zeros(2, width, dtype=torch.int32, device=DEV)
+    table[1] = 3
+    freq = torch.tensor(5e6 ** (-np.arange(0, 128, 2) / 128), dtype=torch.float32, device=DEV)
+    cache = api.PagedCache(kc, vc)
+    q_out, _ = api.msa_paged_append(cache, k, v, table, _i32([0, 1, 2]), _i32(pos), inv_freq=freq,
+                                    q=q)
+    torch.cuda.synchronize()
+    assert api.msa_paged_read_status(cache) == 0
+    ref = paged.rotate(_np(q), pos, _np(freq), False)
+    _within(_np(q_out), ref, _rot_bound(_np(q), ref, 128, False, BF), "q")
+    ref = paged.rotate(_np(k), pos, _np(freq), False)
+    for r, pg in ((0, 0), (1, 3)):
+        _within(_np(kc[pg, pos[r] % S]), ref[r], _rot_bound(_np(k[r]), ref[r], 128, False, BF), "k")
+        assert torch.equal(vc[pg, pos[r] % S], v[r])
+
+
+def test_append_in_place_and_without_queries():
+    gen = _gen(12)
+    kc, vc = (_pool(gen, 6, 16, 2, 64, BF) for _ in range(2))
+    q, k, v = (_randn(gen, (5, h, 64), BF) for h in (6, 2, 2))
+    freq = torch.rand(16, generator=gen, device=DEV)
+    args = (_i32([[1, 2], [4, 0]]), _i32([0, 3, 5]), _i32([0, 14]))
+    cache = api.PagedCache(kc, vc)
+    want, _ = api.msa_paged_append(cache, k, v, *args, inv_freq=freq, q=q)
+    k1 = kc.clone()
+    kc.zero_()
+    none, _ = api.msa_paged_append(cache, k, v, *args, inv_freq=freq)
+    got, _ = api.msa_paged_append(cache, k, v, *args, inv_freq=freq, q=q, q_out=q)
+    torch.cuda.synchronize()
+    assert none is None and got is q and torch.equal(q, want)
+    touched = kc.abs().sum((2, 3)) > 0
+    assert torch.equal(kc[touched], k1[touched]) and int(touched.sum()) == 5
+
+
+def test_append_bad_places_are_skipped():
+    gen = _gen(13)
+    kc, vc = (_pool(gen, 4, 16, 2, 64, FP) for _ in range(2))
+    k, v = (_randn(gen, (6, 2, 64), FP) for _ in range(2))
+    cache = api.PagedCache(kc, vc)
+    before = kc.clone()
+    table = _i32([[0, -1], [4, 1], [2, 3]])
+    # row 0: positions 15 (page 0), 16 (no page); row 1: 0 (page 4 of 4), 16 is fine;
+    # row 2: 31 (page 3), 32 (past the table)
+    k_out = torch.full((6, 2, 64), 9.0, dtype=FP, device=DEV)
+    api.msa_paged_append(cache, k, v, table, _i32([0, 2, 4, 6]), _i32([15, 15, 31]), k_out=k_out)
+    assert api.msa_paged_read_status(cache, clear=True) == 11
+    assert api.msa_paged_read_status(cache) == 0
+    ok = [0, 3, 4]
+    for t, (pg, slot) in zip(ok, ((0, 15), (1, 0), (3, 15))):
+        assert torch.equal(kc[pg, slot], k[t]) and torch.equal(vc[pg, slot], v[t])
+        before[pg, slot] = k[t]
+        assert torch.equal(k_out[t], k[t])
+    assert torch.equal(kc, before)
+    assert (k_out[[1, 2, 5]] == 9).all()
+    # a negative position, and offsets that decrease or pass T
+    api.msa_paged_append(cache, k[:1], v[:1], table[:1], _i32([0, 1]), _i32([-1]))
+    assert api.msa_paged_read_status(cache, clear=True) == 11 and torch.equal(kc, before)
+    for offs in ([0, 2, 1, 6], [0, 2, 4, 7], [1, 2, 4, 6]):
+        api.msa_paged_append(cache, k, v, _i32([[0], [1], [2]]), _i32(offs), _i32([0, 0, 0]))
+        assert api.msa_paged_read_status(cache, clear=True) == 7
+
+
+# ------------------------------------------------------------------ index
+@pytest.mark.parametrize("S,heads,dim,head_major", [(128, 4, 64, False), (16, 4, 128, False),
+                                                    (1, 3, 8, False), (512, 4, 32, True),
+                                                    (64, 5, 120, True)])
+def test_index_matches_fp64(S, heads, dim, head_major):
+    rng, gen = np.random.default_rng(S), _gen(S)
+    steps = [([0, 5, 130, 300, 1], [0, 0, 0, 0, 0]), ([1, 0, 1, 1, 1], [0, 5, 130, 300, 1]),
+             ([400, 1, 126, 90, 0], [1, 5, 131, 301, 2])]
+    final = [401, 6, 257, 391, 2]
+    pool, table = _pages(rng, final, S)
+    keys = _pool(gen, pool, S, heads, dim, BF, head_major)
+    means = torch.full(api.paged_means_shape(pool, S, heads, dim), 3.0, device=DEV)
+    index = api.PagedIndex(keys, means)
+    for fresh, start in steps:
+        offs = np.concatenate([[0], np.cumsum(fresh)])
+        ik = _randn(gen, (int(offs[-1]) + 2, heads + 1, dim), BF)[:, :heads]
+        k0, m0 = _np(keys), _np(means)
+        k_ref, m_ref = paged.index(k0, m0, _np(ik), table, offs, start)
+        api.msa_paged_index(index, ik, _i32(table), _i32(offs), _i32(start))
+        torch.cuda.synchronize()
+        assert np.array_equal(_np(keys), k_ref)
+        m_abs = paged.index(np.abs(k0), np.abs(m0), np.abs(_np(ik)), table, offs, start)[1]
+        bound = 129 * U * m_abs
+        bound[m_ref == m0] = 0  # not touched
+        _within(_np(means), m_ref, bound, "means")
+    assert api.msa_paged_read_status(index) == 0
+
+
+def test_index_long_prompts():
+    rng, gen = np.random.default_rng(1), _gen(1)
+    fresh, start, S = [5000, 1, 3333], [77, 128, 0], 64
+    pool, table = _pages(rng, [f + s for f, s in zip(fresh, start)], S)
+    offs = np.concatenate([[0], np.cumsum(fresh)])
+    ik = _randn(gen, (int(offs[-1]), 4, 64), BF)
+    keys = _pool(gen, pool, S, 4, 64, BF)
+    index = api.PagedIndex(keys, torch.zeros(api.paged_means_shape(pool, S, 4, 64), device=DEV))
+    k0, m0 = _np(keys), _np(index.means)
+    k_ref, m_ref = paged.index(k0, m0, _np(ik), table, offs, start)
+    m_abs = paged.index(np.abs(k0), m0, np.abs(_np(ik)), table, offs, start)[1]
+    api.msa_paged_index(index, ik, _i32(table), _i32(offs), _i32(start))
+    torch.cuda.synchronize()
+    assert np.array_equal(_np(keys), k_ref)
+    _within(_np(index.means), m_ref, 129 * U * m_abs, "means")
+    assert api.msa_paged_read_status(index) == 0
+
+
+def test_index_bad_pages_leave_the_block_out():
+    gen = _gen(2)
+    keys = _pool(gen, 4, 64, 4, 8, BF)
+    before = keys.clone()
+    index = api.PagedIndex(keys, torch.zeros(4, 4, 8, device=DEV))
+    ik = _randn(gen, (130, 4, 8), BF)
+    # block 0 (pages 0, 9 of 4) is left out, block 1 (page 2) is not
+    api.msa_paged_index(index, ik, _i32([[0, 9, 2]]), _i32([0, 130]), _i32([0]))
+    assert api.msa_paged_read_status(index, clear=True) == 11
+    before[2, :2] = ik[128:]
+    assert torch.equal(keys, before)
+    assert torch.equal(index.means[2], ik[128:].float().sum(0) / 2)
+    assert (index.means[[0, 1, 3]] == 0).all()
+    api.msa_paged_index(index, ik[:1], _i32([[0, 1]]), _i32([0, 1]), _i32([128]))
+    assert api.msa_paged_read_status(index, clear=True) == 11
+    api.msa_paged_index(index, ik[:1], _i32([[0, 1]]), _i32([0, 1]), _i32([-3]))
+    assert api.msa_paged_read_status(index, clear=True) == 11 and torch.equal(keys, before)
+
+
+# ------------------------------------------------------------------ select
+def _filled_index(lens, S, dim, seed, heads=4):
+    rng, gen = np.random.default_rng(seed), _gen(seed)
+    pool, table = _pages(rng, lens, S)
+    offs = np.concatenate([[0], np.cumsum(lens)])
+    ik = _randn(gen, (int(offs[-1]), heads, dim), BF)
+    keys = torch.zeros(pool, S, heads, dim, dtype=BF, device=DEV)
+    index = api.PagedIndex(keys, torch.full(api.paged_means_shape(pool, S, heads, dim),
+                                            float("nan"), device=DEV))
+    api.msa_paged_index(index, ik, _i32(table), _i32(offs), _i32([0] * len(lens)))
+    return index, table, offs, ik, _randn(gen, ik.shape, BF)
+
+
+@pytest.mark.parametrize("lens,S,dim,force", [
+    ([2500, 300, 3100, 129, 1], 64, 64, True),
+    ([2500, 300, 3100, 129, 1], 16, 64, False),
+    ([2049, 2048, 2176, 2177], 128, 128, False),
+    ([40000, 5000], 512, 32, False),
+    ([150000], 128, 64, True),
+    ([600000], 1024, 8, False),
+])
+def test_select_equals_the_training_selection(lens, S, dim, force):
+    """Bit for bit: the same sums and products in the same order."""
+    index, table, offs, ik, iq = _filled_index(lens, S, dim, sum(lens) + S)
+    ref = api.msa_select_blocks(iq, ik, _i32(offs), force_local=force)
+    last = torch.as_tensor(offs[1:] - 1, device=DEV)
+    got = api.msa_paged_select(index, iq[last].contiguous(), _i32(table), _i32(lens),
+                               force_local=force)
+    torch.cuda.synchronize()
+    assert torch.equal(got, ref[:, last])
+    assert api.msa_paged_read_status(index) == 0
+    if force:  # the own block is kept without a score: any shorter length as well
+        rng = np.random.default_rng(3)
+        cut = np.array([rng.integers(1, n + 1) for n in lens])
+        at = torch.as_tensor(offs[:-1] + cut - 1, device=DEV)
+        got = api.msa_paged_select(index, iq[at].contiguous(), _i32(table), _i32(cut))
+        assert torch.equal(got, ref[:, at])
+
+
+def test_select_ties_go_to_the_lowest_block():
+    n = 128 * 40
+    gen = _gen(4)
+    pool, table = _pages(np.random.default_rng(4), [n], 128)
+    index = api.PagedIndex(torch.zeros(pool, 128, 4, 8, dtype=BF, device=DEV),
+                           torch.zeros(pool, 4, 8, device=DEV))
+    iq = _randn(gen, (1, 4, 8), BF)
+    got = api.msa_paged_select(index, iq, _i32(table), _i32([n]), force_local=False)
+    assert got.cpu().tolist() == [[list(range(16))]] * 4
+    index.means[torch.as_tensor(table[0, 1::2].copy(), device=DEV).clamp(min=0)] = -0.0
+    got = api.msa_paged_select(index, -iq.abs(), _i32(table), _i32([n]), force_local=False)
+    assert got.cpu().tolist() == [[list(range(16))]] * 4
+    got = api.msa_paged_select(index, iq, _i32(table), _i32([n]), force_local=True)
+    assert got.cpu().tolist() == [[list(range(15)) + [39]]] * 4
+
+
+def test_select_unused_rows_bad_lengths_and_pages():
+    lens = [2600, 2600, 2600, 2600]
+    index, table, offs, ik, iq = _filled_index(lens, 128, 16, 5)
+    last = torch.as_tensor(offs[1:] - 1, device=DEV)
+    q = iq[last].contiguous()
+    good = api.msa_paged_select(index, q, _i32(table), _i32(lens)).cpu().numpy()
+    assert api.msa_paged_read_status(index) == 0
+    table = table.copy()
+    table[2, 4:] = -1       # only blocks 0 .. 3 have a page
+    got = api.msa_paged_select(index, q, _i32(table), _i32([0, 2600, 2600, 128 * 99])).cpu().numpy()
+    assert api.msa_paged_read_status(index, clear=True) == 11
+    assert (got[:, 0] == -1).all() and np.array_equal(got[:, 1], good[:, 1])
+    assert (got[:, 3] == -1).all()
+    for h in range(4):  # the blocks with a page, and the two that are always kept
+        assert got[h, 2].tolist() == [0, 1, 2, 3, 20] + [-1] * 11
+
+
+# ------------------------------------------------------------------ decode
+def _decode_case(dt, dim, kv, share, S, lens, sparse, seed, head_major=False, poison=True,
+                 scale=None, spread=1.0):
+    rng, gen = np.random.default_rng(seed), _gen(seed)
+    pool, table = _pages(rng, lens, S)
+    kc, vc = (_pool(gen, pool, S, kv, dim, dt, head_major) for _ in range(2))
+    q = (_randn(gen, (len(lens), kv * share, dim)) * spread).to(dt)
+    q2k = None
+    if sparse:
+        q2k = np.full((kv, len(lens), 16), -1, dtype=np.int64)
+        for g in range(kv):
+            for r, n in enumerate(lens):
+                nb = -(-n // 128)
+                if nb == 0 or rng.random() < 0.1:
+                    continue  # no slot used
+                pick = rng.permutation(nb)[:rng.integers(1, 17)]
+                if rng.random() < 0.7:
+                    pick = np.unique(np.append(pick, nb - 1))[-16:]
+                slots = rng.permutation(16)[:len(pick)]
+                q2k[g, r, slots] = pick
+                free = [i for i in range(16) if i not in slots]
+                if free and rng.random() < 0.5:
+                    q2k[g, r, free[0]] = pick[0]  # the same block twice counts once
+    scale = scale or dim ** -0.5
+    ref = paged.decode_bounds(_np(kc), _np(vc), _np(q), table, lens, scale, HALF[dt], TINY[dt], q2k)
+    if poison:  # whatever lies where no row has a key must not matter
+        used = np.zeros((pool, S), dtype=bool)
+        for r, n in enumerate(lens):
+            j = np.arange(n)
+            used[table[r, j // S], j % S] = True
+        free = torch.as_tensor(~used, device=DEV)
+        for c, bad in ((kc, float("nan")), (vc, float("inf"))):
+            c[free] = bad
+    cache = api.PagedCache(kc, vc)
+    o, lse = api.msa_paged_decode(cache, q, _i32(table), _i32(lens), scale,
+                                  q2k=None if q2k is None else _i32(q2k))
+    torch.cuda.synchronize()
+    assert api.msa_paged_read_status(cache) == 0
+    O, L, BO, BL = ref
+    fin = np.isfinite(L)
+    got = _np(lse)
+    assert np.array_equal(got == -np.inf, ~fin)
+    _within(np.where(fin, got, 0), np.where(fin, L, 0), BL, "LSE")
+    _within(_np(o), O, BO, "O")
+    assert (_np(o)[~fin] == 0).all()
+    o2, lse2 = api.msa_paged_decode(cache, q, _i32(table), _i32(lens), scale,
+                                    q2k=None if q2k is None else _i32(q2k))
+    assert torch.equal(o, o2) and torch.equal(lse, lse2), "not the same twice"
+
+
+EDGES = [0, 1, 2, 15, 16, 17, 63, 64, 65, 127, 128, 129, 191, 300, 1000]
+
+
+@pytest.mark.parametrize("dt,dim,kv,share,S,head_major", [
+    (BF, 128, 4, 16, 128, False),
+    (BF, 128, 4, 16, 16, True),
+    (FP, 64, 8, 3, 32, False),
+    (FP, 128, 2, 7, 64, True),
+    (BF, 64, 1, 1, 1, False),
+    (BF, 64, 3, 8, 8, False),
+    (FP, 128, 1, 9, 1024, False),
+    (BF, 128, 2, 16, 4, True),
+])
+@pytest.mark.parametrize("sparse", [False, True])
+def test_decode_matches_fp64(dt, dim, kv, share, S, head_major, sparse):
+    _decode_case(dt, dim, kv, share, S, EDGES, sparse, seed=S + dim + share,
+                 head_major=head_major)
+
+
+@pytest.mark.parametrize("n", [1, 64, 65, 128, 1000, 2500])
+@pytest.mark.parametrize("sparse", [False, True])
+def test_decode_one_row(n, sparse):
+    _decode_case(BF, 128, 4, 16, 64, [n], sparse, seed=n)
+
+
+def test_decode_row_without_keys_alone():
+    _decode_case(BF, 128, 4, 16, 64, [0], False, seed=1)
+    _decode_case(FP, 64, 1, 2, 64, [0, 0], True, seed=2)
+
+
+def test_decode_many_rows():
+    rng = np.random.default_rng(8)
+    _decode_case(BF, 64, 2, 4, 16, rng.integers(0, 200, 700).tolist(), False, seed=8)
+    _decode_case(BF, 128, 4, 16, 32, rng.integers(0, 700, 90).tolist(), True, seed=9)
+
+
+def test_decode_one_long_row_split_over_all_ctas():
+    _decode_case(BF, 128, 1, 16, 128, [90001], False, seed=10)
+    _decode_case(FP, 64, 2, 5, 256, [70000, 3], False, seed=11)
+
+
+def test_decode_sparse_in_long_rows():
+    _decode_case(BF, 128, 4, 16, 128, [40000, 17, 9000], True, seed=12)
+
+
+def test_decode_peaked_and_growing_scores():
+    # large scores: the running maximum moves often, most weights vanish
+    _decode_case(BF, 128, 2, 16, 64, [700, 129], False, seed=13, spread=30.0)
+    _decode_case(FP, 64, 2, 4, 64, [700, 129], False, seed=14, spread=12.0)
+
+
+def test_decode_bad_slots_pages_and_lengths():
+    rng, gen = np.random.default_rng(15), _gen(15)
+    lens = [300, 300, 300, 300, 300]
+    pool, table = _pages(rng, lens, 16)
+    kc, vc = (_pool(gen, pool, 16, 2, 64, BF) for _ in range(2))
+    q = _randn(gen, (5, 8, 64), BF)
+    cache = api.PagedCache(kc, vc)
+    q2k = np.full((2, 5, 16), -1)
+    q2k[:, :, 2], q2k[:, :, 9] = 0, 2
+    bad = q2k.copy()
+    bad[0, 1, 0], bad[1, 1, 5], bad[:, 2, 15] = 3, -2, 2 ** 31 - 1
+    good = api.msa_paged_decode(cache, q, _i32(table), _i32(lens), 0.125, q2k=_i32(q2k))
+    assert api.msa_paged_read_status(cache) == 0
+    got = api.msa_paged_decode(cache, q, _i32(table), _i32(lens), 0.125, q2k=_i32(bad))
+    assert api.msa_paged_read_status(cache, clear=True) == 6
+    assert torch.equal(got[0], good[0]) and torch.equal(got[1], good[1])
+    # row 3's second page is bad: as if its keys were not there; rows 0 and 4: bad lengths
+    broken = table.copy()
+    broken[3, 1] = pool
+    wrong = [-1, 300, 300, 300, 16 * table.shape[1] + 1]
+    for slots in (None, q2k):
+        got = api.msa_paged_decode(cache, q, _i32(broken), _i32(wrong), 0.125,
+                                   q2k=None if slots is None else _i32(slots))
+        assert api.msa_paged_read_status(cache, clear=True) == 11
+        for r in (0, 4):
+            assert (got[0][r] == 0).all() and (got[1][r] == -float("inf")).all()
+        # positions 16 .. 31 moved out of the row
+        j = [x for x in range(300) if not 16 <= x < 32]
+        for g in range(2):
+            see = [x for x in j if slots is None or x // 128 in (0, 2)]
+            K = np.stack([_np(kc[table[3, x // 16], x % 16, g]) for x in see])
+            s = 0.125 * _np(q[3, 4 * g:4 * g + 4]) @ K.T
+            L = np.log(np.exp(s).sum(1))
+            assert np.abs(_np(got[1][3, 4 * g:4 * g + 4]) - L).max() < 1e-4
+        ok = [1, 2]
+        full = api.msa_paged_decode(cache, q, _i32(table), _i32(lens), 0.125,
+                                    q2k=None if slots is None else _i32(slots))
+        # the split of the keys over CTAs differs with the lengths: equal up to rounding
+        assert (full[1][ok] - got[1][ok]).abs().max() < 1e-5
+
+
+def test_decode_on_another_stream_and_into_given_tensors():
+    gen = _gen(16)
+    pool, table = _pages(np.random.default_rng(16), [500, 90], 32)
+    kc, vc = (_pool(gen, pool, 32, 4, 128, BF) for _ in range(2))
+    q = _randn(gen, (2, 64, 128), BF)
+    cache = api.PagedCache(kc, vc)
+    t, n = _i32(table), _i32([500, 90])
+    want = api.msa_paged_decode(cache, q, t, n, 0.1)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = api.msa_paged_decode(cache, q, t, n, 0.1, stream=side)
+    side.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    o, lse = torch.full_like(want[0], 5.0), torch.full_like(want[1], 5.0)
+    ws = torch.full((api.paged_decode_workspace_bytes(cache, 2, 64),), 255, dtype=torch.uint8,
+                    device=DEV)
+    got = api.msa_paged_decode(cache, q, t, n, 0.1, o=o, lse=lse, workspace=ws)
+    assert got[0] is o and torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
+def test_binding_refuses_mismatches():
+    gen = _gen(17)
+    kc, vc = (_pool(gen, 4, 16, 2, 64, BF) for _ in range(2))
+    cache = api.PagedCache(kc, vc)
+    t, n, q = _i32([[0, 1]]), _i32([20]), _randn(gen, (1, 8, 64), BF)
+    for kw in (dict(q=q.half()), dict(q=q[:, :, :32]), dict(q=q[0]), dict(n=_i32([20, 3])),
+               dict(n=n.long()), dict(n=n.cpu()), dict(t=t.cpu()), dict(q2k=_i32([[0] * 16])),
+               dict(o=torch.empty(1, 8, 64, device=DEV)), dict(lse=q[:, :, 0].double()),
+               dict(workspace=torch.empty(8, dtype=torch.uint8, device=DEV)),
+               dict(scale=0.0), dict(q=_randn(gen, (1, 7, 64), BF)),
+               dict(q=_randn(gen, (1, 34, 64), BF))):
+        a = {**dict(q=q, t=t, n=n, scale=0.1), **kw}
+        with pytest.raises((TypeError, ValueError, api.MSAError)):
+            api.msa_paged_decode(cache, a["q"], a["t"], a["n"], a["scale"], q2k=a.get("q2k"),
+                                 o=a.get("o"), lse=a.get("lse"), workspace=a.get("workspace"))
+    with pytest.raises(ValueError):
+        api.PagedCache(kc, vc[:3])
+    with pytest.raises(TypeError):
+        api.PagedCache(kc, vc.half())
+    with pytest.raises(ValueError):
+        api.PagedCache(kc[:1].expand(4, 16, 2, 64), vc)
+    with pytest.raises(api.MSAError):
+        api.PagedCache(kc[:, :12], vc[:, :12])
+    with pytest.raises(api.MSAError):
+        api.PagedCache(kc[..., :32], vc[..., :32])
+    assert api.msa_paged_read_status(cache) == 0
+
+
+# ------------------------------------------------------------------ together
+def test_prompt_then_steps_as_served():
+    """A prompt through append, index and the training path's forward, then
+    token by token: every step's output must be what the training path and
+    the fp64 oracle give for that token of the whole document."""
+    rng, gen = np.random.default_rng(21), _gen(21)
+    lens, steps, S, dim = [2300, 129, 700], 4, 64, 64
+    full = [n + steps for n in lens]
+    pool, table = _pages(rng, full, S)
+    t = _i32(table)
+    offs_full = np.concatenate([[0], np.cumsum(full)])
+    T = int(offs_full[-1])
+    q, k, v = (_randn(gen, (T, h, 128), BF) for h in (64, 4, 4))
+    iq, ik = (_randn(gen, (T, 4, dim), BF) for _ in range(2))
+    freq = torch.tensor(10000.0 ** (-np.arange(0, 64, 2) / 64), dtype=torch.float32, device=DEV)
+    scale = 128 ** -0.5
+
+    cache = api.PagedCache(*(torch.zeros(pool, S, 4, 128, dtype=BF, device=DEV) for _ in range(2)))
+    index = api.PagedIndex(torch.zeros(pool, S, 4, dim, dtype=BF, device=DEV),
+                           torch.zeros(api.paged_means_shape(pool, S, 4, dim), device=DEV))
+    q_rot, k_rot = torch.empty_like(q), torch.empty_like(k)
+
+    def tokens(begin, end):  # each row's tokens begin[r] .. end[r]-1
+        return torch.as_tensor(np.concatenate([np.arange(offs_full[r] + begin[r],
+                                                         offs_full[r] + end[r])
+                                               for r in range(3)]), device=DEV)
+
+    def feed(begin, end):
+        at = tokens(begin, end)
+        offs = _i32(np.concatenate([[0], np.cumsum(np.array(end) - np.array(begin))]))
+        k_out = torch.empty(len(at), 4, 128, dtype=BF, device=DEV)
+        qr, kr = api.msa_paged_append(cache, k[at], v[at], t, offs, _i32(begin), inv_freq=freq,
+                                      q=q[at], k_out=k_out)
+        api.msa_paged_index(index, ik[at], t, offs, _i32(begin))
+        q_rot[at], k_rot[at] = qr, kr
+        return qr
+
+    # the prompt: handed-back queries and keys through the training path
+    qr = feed([0, 0, 0], lens)
+    at = tokens([0, 0, 0], lens)
+    offs = _i32(np.concatenate([[0], np.cumsum(lens)]))
+    q2k = api.msa_select_blocks(iq[at], ik[at], offs)
+    plan = api.msa_build_plan(q2k, offs)
+    o, lse = api.msa_forward(plan, qr, k_rot[at], v[at], scale)
+    last = (offs[1:] - 1).long()
+    got = api.msa_paged_decode(cache, qr[last].contiguous(), t, _i32(lens), scale,
+                               q2k=q2k[:, last].contiguous())
+    torch.cuda.synchronize()
+    check_o(_np(got[0]), _np(o[last]))
+    check_lse(_np(got[1]), _np(lse[last]))
+
+    # then step by step
+    served = []
+    for i in range(steps):
+        n = [x + i for x in lens]
+        qr = feed(n, [x + 1 for x in n])
+        at = tokens(n, [x + 1 for x in n])
+        chosen = api.msa_paged_select(index, iq[at], t, _i32([x + 1 for x in n]))
+        served.append((at, chosen, api.msa_paged_decode(cache, qr, t, _i32([x + 1 for x in n]),
+                                                        scale, q2k=chosen)))
+    torch.cuda.synchronize()
+    assert api.msa_paged_read_status(cache) == 0 and api.msa_paged_read_status(index) == 0
+
+    offs = _i32(offs_full)
+    q2k = api.msa_select_blocks(iq, ik, offs)
+    plan = api.msa_build_plan(q2k, offs)
+    o, lse = api.msa_forward(plan, q_rot, k_rot, v, scale)
+    P = oracle.Problem(q_rot.cpu(), k_rot.cpu(), v.cpu(), q2k.cpu().numpy(),
+                       offs_full.astype(np.int32), scale)
+    for at, chosen, (so, sl) in served:
+        assert torch.equal(chosen, q2k[:, at])
+        check_o(_np(so), _np(o[at]))
+        check_lse(_np(sl), _np(lse[at]))
+        O, L = P.forward(at.cpu().numpy())
+        check_o(_np(so), O)
+        check_lse(_np(sl), L)
+
+
+def test_a_step_captured_and_replayed():
+    """One step in a CUDA graph, replayed with other lengths, tables and
+    inputs, some rows not in use; a second graph of another batch size beside
+    it; every replay equals the eager calls."""
+    rng, gen = np.random.default_rng(22), _gen(22)
+    S, dim, most = 32, 32, 4000
+    pool = 900
+    cache = api.PagedCache(*(_pool(gen, pool, S, 4, 128, BF) for _ in range(2)))
+    index = api.PagedIndex(_pool(gen, pool, S, 4, dim, BF),
+                           _randn(gen, api.paged_means_shape(pool, S, 4, dim)))
+    freq = torch.rand(32, generator=gen, device=DEV)
+
+    def state(rows):
+        return dict(q=torch.zeros(rows, 64, 128, dtype=BF, device=DEV),
+                    k=torch.zeros(rows, 4, 128, dtype=BF, device=DEV),
+                    v=torch.zeros(rows, 4, 128, dtype=BF, device=DEV),
+                    iq=torch.zeros(rows, 4, dim, dtype=BF, device=DEV),
+                    ik=torch.zeros(rows, 4, dim, dtype=BF, device=DEV),
+                    t=torch.zeros(rows, -(-most // S), dtype=torch.int32, device=DEV),
+                    offs=torch.zeros(rows + 1, dtype=torch.int32, device=DEV),
+                    start=torch.zeros(rows, dtype=torch.int32, device=DEV),
+                    n=torch.zeros(rows, dtype=torch.int32, device=DEV))
+
+    def step(s):
+        qr, _ = api.msa_paged_append(cache, s["k"], s["v"], s["t"], s["offs"], s["start"],
+                                     inv_freq=freq, q=s["q"], q_out=s.get("qr"))
+        api.msa_paged_index(index, s["ik"], s["t"], s["offs"], s["start"])
+        chosen = api.msa_paged_select(index, s["iq"], s["t"], s["n"])
+        return (chosen, *api.msa_paged_decode(cache, qr, s["t"], s["n"], 0.09, q2k=chosen))
+
+    graphs = []
+    for rows in (5, 3):
+        s = state(rows)
+        s["qr"] = torch.zeros(rows, 64, 128, dtype=BF, device=DEV)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            step(s)
+        torch.cuda.current_stream().wait_stream(side)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = step(s)
+        graphs.append((rows, s, g, out))
+    for turn in range(4):
+        for rows, s, g, out in graphs:
+            order, at = rng.permutation(pool), 0
+            used = int(rng.integers(1, rows + 1))
+            new = state(rows)
+            start = np.zeros(rows, int)
+            start[:used] = rng.integers(0, most - 1, used)
+            new["start"].copy_(_i32(start))
+            new["n"][:used] = _i32(start[:used] + 1)
+            new["offs"].copy_(_i32(np.minimum(np.arange(rows + 1), used)))
+            new["t"].fill_(-1)
+            for r in range(used):
+                np_ = start[r] // S + 1
+                new["t"][r, :np_] = _i32(order[at:at + np_])
+                at += np_
+            for x in ("q", "k", "v", "iq", "ik"):
+                new[x].copy_(_randn(gen, new[x].shape, BF))
+            for x in new:
+                s[x].copy_(new[x])
+            saved = [x.clone() for x in (cache.k, cache.v, index.keys, index.means)]
+            g.replay()
+            torch.cuda.synchronize()
+            for x, y in zip((cache.k, cache.v, index.keys, index.means), saved):
+                x.copy_(y)
+            eager = step(s)
+            for x, y in zip(out, eager):
+                assert torch.equal(x, y)
+            assert (out[0][:, used:] == -1).all() and (out[1][used:] == 0).all()
+            assert (out[2][used:] == -float("inf")).all()
+    assert api.msa_paged_read_status(cache) == 0 and api.msa_paged_read_status(index) == 0
