@@ -10,7 +10,6 @@ Names follow the C ABI: msa_build_plan, msa_forward, msa_backward.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 import threading
@@ -136,6 +135,8 @@ SIGNATURES = {
 def lib():
     """The loaded libmsa (built in-tree by build.py); raises MSAError if absent."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -154,9 +155,11 @@ def _check(code: int, what: str):
         raise MSAError(code, what)
 
 
-def _stream(stream) -> ctypes.c_void_p:
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+def _stream(stream) -> int:
+    if stream is None:
+        # the current stream's handle without a Stream object (4 us of a call)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream
 
 
 def _ptr(t: torch.Tensor) -> ctypes.c_void_p:
@@ -490,11 +493,12 @@ class PagedCache:
             k=k.data_ptr(), v=v.data_ptr(), k_stride=_pool_strides(k), v_stride=_pool_strides(v),
             num_pages=self.num_pages, page_size=self.page_size, kv_heads=self.kv_heads,
             head_dim=self.head_dim, dtype=PAGED_DTYPES[k.dtype], status=self.status.data_ptr())
+        self._ref = ctypes.byref(self.struct)
         # the library's own check of the cache, before the first call
         paged_decode_workspace_bytes(self, 1, self.kv_heads)
 
     def ref(self):
-        return ctypes.byref(self.struct)
+        return self._ref
 
 
 def paged_means_shape(num_pages: int, page_size: int, heads: int, dim: int):
@@ -520,53 +524,71 @@ class PagedIndex:
             keys=keys.data_ptr(), key_stride=_pool_strides(keys), means=means.data_ptr(),
             num_pages=self.num_pages, page_size=self.page_size, heads=self.heads, dim=self.dim,
             reserved=0, status=self.status.data_ptr())
+        self._ref = ctypes.byref(self.struct)
 
     def ref(self):
-        return ctypes.byref(self.struct)
+        return self._ref
 
 
-def _on(device, **tensors):
-    """Every tensor given is on the cache's device, which is the current one."""
-    if device.index != torch.cuda.current_device():
+def _current(device):
+    if device.index != torch._C._cuda_getDevice():
         raise ValueError(f"the cache is on {device}, the current device is "
                          f"cuda:{torch.cuda.current_device()}")
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} must be on {device}, got {t.device}")
 
 
-def _table(page_table: torch.Tensor) -> MsaPageTableStruct:
+def _arg(t, name: str, dtype, shape, device) -> int:
+    """Address of a contiguous tensor of this type and shape on the cache's device."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.device == device and t.is_contiguous()):
+        _need(t, name, dtype, shape)
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    return t.data_ptr()
+
+
+def _table(page_table: torch.Tensor, device) -> MsaPageTableStruct:
     if not isinstance(page_table, torch.Tensor):
         raise TypeError("page_table must be a torch.Tensor")
-    if page_table.dtype != torch.int32:
+    if page_table.dtype is not torch.int32:
         raise TypeError(f"page_table must be torch.int32, got {page_table.dtype}")
+    if page_table.device != device:
+        raise ValueError(f"page_table must be on {device}, got {page_table.device}")
     if page_table.dim() != 2 or page_table.numel() == 0:
         raise ValueError("page_table must be [rows, pages of a row]")
     rows, width = page_table.shape
-    stride = page_table.stride(0) if rows > 1 else width
-    if (width > 1 and page_table.stride(1) != 1) or stride < width:
+    stride, step = page_table.stride()
+    if rows == 1:
+        stride = width
+    if (width > 1 and step != 1) or stride < width:
         raise ValueError("page_table: a row's entries must be contiguous, rows must not overlap")
-    return MsaPageTableStruct(pages=page_table.data_ptr(), stride=stride, rows=rows, width=width)
+    return MsaPageTableStruct(page_table.data_ptr(), stride, rows, width)
 
 
-def _tokens(x, name: str, dtype, heads: int | None, dim: int):
+def _tokens(x, name: str, dtype, tokens: int | None, heads: int | None, dim: int, device) -> int:
     """Token stride of [T, heads, dim] with contiguous tokens."""
     if not isinstance(x, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if x.dtype != dtype:
+    if x.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {x.dtype}")
-    if x.dim() != 3 or x.shape[2] != dim or (heads is not None and x.shape[1] != heads):
-        raise ValueError(f"{name} must be [T, {heads if heads is not None else 'heads'}, {dim}], "
-                         f"got {tuple(x.shape)}")
-    h = x.shape[1]
-    if x.stride(2) != 1 or (h > 1 and x.stride(1) != dim):
+    if x.device != device:
+        raise ValueError(f"{name} must be on {device}, got {x.device}")
+    shape = x.shape
+    if (len(shape) != 3 or shape[2] != dim or (heads is not None and shape[1] != heads)
+            or (tokens is not None and shape[0] != tokens)):
+        raise ValueError(f"{name} must be [{'T' if tokens is None else tokens}, "
+                         f"{'heads' if heads is None else heads}, {dim}], got {tuple(shape)}")
+    st, sh, sd = x.stride()
+    h = shape[1]
+    if sd != 1 or (h > 1 and sh != dim):
         raise ValueError(f"{name}: a token's heads must be contiguous")
-    return x.stride(0) if x.shape[0] > 1 else h * dim
+    return st if shape[0] > 1 else h * dim
 
 
-def _on_stream(stream):
-    """Context in which what a call allocates belongs to the stream it runs on."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+def _empty(shape, dtype, device, stream):
+    """What a call allocates belongs to the stream that it runs on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def paged_decode_workspace_bytes(cache: PagedCache, rows: int, q_heads: int) -> int:
@@ -581,7 +603,7 @@ def msa_paged_read_status(cache, stream=None, clear: bool = False) -> int:
     OK; the lowest-numbered status otherwise).  ``clear`` resets the word."""
     code = int(lib().msa_paged_read_status(_ptr(cache.status), _stream(stream)))
     if clear:
-        with _on_stream(stream):
+        with torch.cuda.stream(stream):  # the current one if None
             cache.status.zero_()
     return code
 
@@ -605,42 +627,34 @@ def msa_paged_append(cache: PagedCache, k: torch.Tensor, v: torch.Tensor,
     without q; q itself may be given as q_out) and, where a k_out [T,
     kv_heads, head_dim] is given, the rotated keys.  Padding rows of both are
     left as they were.  Not differentiable."""
-    dt, dim = cache.dtype, cache.head_dim
-    table = _table(page_table)
+    device, dt, dim, kv = cache.device, cache.dtype, cache.head_dim, cache.kv_heads
+    _current(device)
+    table = _table(page_table, device)
     rows = table.rows
-    ks = _tokens(k, "k", dt, cache.kv_heads, dim)
-    vs = _tokens(v, "v", dt, cache.kv_heads, dim)
+    ks = _tokens(k, "k", dt, None, kv, dim, device)
     T = k.shape[0]
-    if v.shape[0] != T:
-        raise ValueError(f"k has {T} tokens, v {v.shape[0]}")
-    _need(row_offsets, "row_offsets", torch.int32, (rows + 1,))
-    _need(start_pos, "start_pos", torch.int32, (rows,))
+    vs = _tokens(v, "v", dt, T, kv, dim, device)
+    offs = _arg(row_offsets, "row_offsets", torch.int32, (rows + 1,), device)
+    start = _arg(start_pos, "start_pos", torch.int32, (rows,), device)
     qs = heads = rot = 0
+    qp = qo = ko = freq = None
     if q is not None:
-        qs = _tokens(q, "q", dt, None, dim)
-        heads = q.shape[1]
-        if q.shape[0] != T:
-            raise ValueError(f"k has {T} tokens, q {q.shape[0]}")
+        qs = _tokens(q, "q", dt, T, None, dim, device)
+        qp, heads = q.data_ptr(), q.shape[1]
+        if q_out is None:
+            q_out = _empty((T, heads, dim), dt, device, stream)
+        qo = _arg(q_out, "q_out", dt, (T, heads, dim), device)
     elif q_out is not None:
         raise ValueError("q_out needs q")
     if inv_freq is not None:
         rot = 2 * inv_freq.numel()
-        _need(inv_freq, "inv_freq", torch.float32, (rot // 2,))
-    _on(cache.device, k=k, v=v, q=q, page_table=page_table, row_offsets=row_offsets,
-        start_pos=start_pos, inv_freq=inv_freq, q_out=q_out, k_out=k_out)
-    if q is not None:
-        if q_out is None:
-            with _on_stream(stream):
-                q_out = torch.empty((T, heads, dim), dtype=dt, device=cache.device)
-        _need(q_out, "q_out", dt, (T, heads, dim))
+        freq = _arg(inv_freq, "inv_freq", torch.float32, (rot // 2,), device)
     if k_out is not None:
-        _need(k_out, "k_out", dt, (T, cache.kv_heads, dim))
+        ko = _arg(k_out, "k_out", dt, (T, kv, dim), device)
     _check(lib().msa_paged_append(
-        cache.ref(), ctypes.byref(table), row_offsets.data_ptr(), start_pos.data_ptr(), T,
-        k.data_ptr(), ks, v.data_ptr(), vs, None if q is None else q.data_ptr(), qs, heads,
-        None if inv_freq is None else inv_freq.data_ptr(), rot, 1 if interleaved else 0,
-        None if q_out is None else q_out.data_ptr(), None if k_out is None else k_out.data_ptr(),
-        _stream(stream)), "msa_paged_append")
+        cache._ref, ctypes.byref(table), offs, start, T, k.data_ptr(), ks, v.data_ptr(), vs, qp,
+        qs, heads, freq, rot, 1 if interleaved else 0, qo, ko, _stream(stream)),
+        "msa_paged_append")
     return q_out, k_out
 
 
@@ -649,14 +663,14 @@ def msa_paged_index(index: PagedIndex, ik: torch.Tensor, page_table: torch.Tenso
     """New tokens' index keys (bf16 [T, heads, dim], each token contiguous)
     into their pages, and the means of the blocks they fall in.  Rows,
     positions and padding as for ``msa_paged_append``."""
-    table = _table(page_table)
-    s = _tokens(ik, "ik", torch.bfloat16, index.heads, index.dim)
-    _need(row_offsets, "row_offsets", torch.int32, (table.rows + 1,))
-    _need(start_pos, "start_pos", torch.int32, (table.rows,))
-    _on(index.device, ik=ik, page_table=page_table, row_offsets=row_offsets, start_pos=start_pos)
-    _check(lib().msa_paged_index(index.ref(), ctypes.byref(table), row_offsets.data_ptr(),
-                                 start_pos.data_ptr(), ik.shape[0], ik.data_ptr(), s,
-                                 _stream(stream)), "msa_paged_index")
+    device = index.device
+    _current(device)
+    table = _table(page_table, device)
+    s = _tokens(ik, "ik", torch.bfloat16, None, index.heads, index.dim, device)
+    offs = _arg(row_offsets, "row_offsets", torch.int32, (table.rows + 1,), device)
+    start = _arg(start_pos, "start_pos", torch.int32, (table.rows,), device)
+    _check(lib().msa_paged_index(index._ref, ctypes.byref(table), offs, start, ik.shape[0],
+                                 ik.data_ptr(), s, _stream(stream)), "msa_paged_index")
 
 
 def msa_paged_select(index: PagedIndex, iq: torch.Tensor, page_table: torch.Tensor,
@@ -666,18 +680,18 @@ def msa_paged_select(index: PagedIndex, iq: torch.Tensor, page_table: torch.Tens
     index query (bf16 [rows, heads, dim]) and the cached block means; the
     rules of ``msa_select_blocks``.  kv_len: int32 [rows], the new token
     included, 0 for a row that is not in use."""
-    table = _table(page_table)
+    device, heads = index.device, index.heads
+    _current(device)
+    table = _table(page_table, device)
     rows = table.rows
-    _need(iq, "iq", torch.bfloat16, (rows, index.heads, index.dim))
-    _need(kv_len, "kv_len", torch.int32, (rows,))
-    _on(index.device, iq=iq, page_table=page_table, kv_len=kv_len, q2k=q2k)
+    qp = _arg(iq, "iq", torch.bfloat16, (rows, heads, index.dim), device)
+    lens = _arg(kv_len, "kv_len", torch.int32, (rows,), device)
     if q2k is None:
-        with _on_stream(stream):
-            q2k = torch.empty((index.heads, rows, TOPK), dtype=torch.int32, device=index.device)
-    _need(q2k, "q2k", torch.int32, (index.heads, rows, TOPK))
-    _check(lib().msa_paged_select(index.ref(), ctypes.byref(table), kv_len.data_ptr(),
-                                  iq.data_ptr(), 1 if force_local else 0, q2k.data_ptr(),
-                                  _stream(stream)), "msa_paged_select")
+        q2k = _empty((heads, rows, TOPK), torch.int32, device, stream)
+    out = _arg(q2k, "q2k", torch.int32, (heads, rows, TOPK), device)
+    _check(lib().msa_paged_select(index._ref, ctypes.byref(table), lens, qp,
+                                  1 if force_local else 0, out, _stream(stream)),
+           "msa_paged_select")
     return q2k
 
 
@@ -693,33 +707,31 @@ def msa_paged_decode(cache: PagedCache, q: torch.Tensor, page_table: torch.Tenso
     key head; kv_len: int32 [rows], keys that each row attends (0: none, O = 0
     and LSE = -inf); q2k: int32 [kv_heads, rows, 16], or None for every key.
     A workspace serves one call at a time.  Not differentiable."""
-    table = _table(page_table)
+    device = cache.device
+    _current(device)
+    table = _table(page_table, device)
     rows = table.rows
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
-        raise ValueError("q must be [rows, q_heads, head_dim]")
+        raise ValueError("q must be a [rows, q_heads, head_dim] tensor")
     heads = q.shape[1]
     shape = (rows, heads, cache.head_dim)
-    _need(q, "q", cache.dtype, shape)
-    _need(kv_len, "kv_len", torch.int32, (rows,))
+    qp = _arg(q, "q", cache.dtype, shape, device)
+    lens = _arg(kv_len, "kv_len", torch.int32, (rows,), device)
+    slots = None
     if q2k is not None:
-        _need(q2k, "q2k", torch.int32, (cache.kv_heads, rows, TOPK))
-    _on(cache.device, q=q, page_table=page_table, kv_len=kv_len, q2k=q2k, o=o, lse=lse,
-        workspace=workspace)
-    if o is None or lse is None or workspace is None:
-        with _on_stream(stream):
-            if o is None:
-                o = torch.empty_like(q)
-            if lse is None:
-                lse = torch.empty((rows, heads), dtype=torch.float32, device=q.device)
-            if workspace is None:
-                workspace = torch.empty(paged_decode_workspace_bytes(cache, rows, heads),
-                                        dtype=torch.uint8, device=q.device)
-    _need(o, "o", cache.dtype, shape)
-    _need(lse, "lse", torch.float32, (rows, heads))
-    _need(workspace, "workspace", torch.uint8, (workspace.numel(),))
+        slots = _arg(q2k, "q2k", torch.int32, (cache.kv_heads, rows, TOPK), device)
+    if o is None:
+        o = _empty(shape, cache.dtype, device, stream)
+    if lse is None:
+        lse = _empty((rows, heads), torch.float32, device, stream)
+    if workspace is None:
+        workspace = _empty(paged_decode_workspace_bytes(cache, rows, heads), torch.uint8, device,
+                           stream)
+    nbytes = workspace.numel()
     _check(lib().msa_paged_decode(
-        cache.ref(), ctypes.byref(table), kv_len.data_ptr(), q.data_ptr(), heads,
-        float(softmax_scale), None if q2k is None else q2k.data_ptr(), o.data_ptr(),
-        lse.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream(stream)),
+        cache._ref, ctypes.byref(table), lens, qp, heads, float(softmax_scale), slots,
+        _arg(o, "o", cache.dtype, shape, device),
+        _arg(lse, "lse", torch.float32, (rows, heads), device),
+        _arg(workspace, "workspace", torch.uint8, (nbytes,), device), nbytes, _stream(stream)),
         "msa_paged_decode")
     return o, lse

@@ -7,10 +7,11 @@
 // channel.  The order is kept exactly, so a token selects the same blocks
 // here as there.
 //
-// k_paged_index   one CTA a block that got a token: it writes the block's new
-//                 keys and sums old and new ones.  Blocks are found by their
-//                 first new token (position a multiple of 128, or the row's
-//                 first).
+// k_paged_index   one CTA a block that got a token and 128 channels: it brings
+//                 the block's keys, old and new, into shared memory with all
+//                 loads in flight, writes the new ones to the cache and sums
+//                 them in order.  Blocks are found by their first new token
+//                 (position a multiple of 128, or the row's first).
 // k_paged_select  one cluster of CTAs a (row, index head): a lane scores a
 //                 block, a warp keeps the best of its blocks in a list sorted
 //                 across its lanes, and the lists are merged through shared
@@ -25,7 +26,9 @@ namespace msa {
 namespace {
 
 constexpr int kIdxThreads = 256;
-constexpr int kIdxPages = kBlock;  // pages of a block, one-token pages at most
+constexpr int kIdxSlice = 128;      // channels of one CTA
+constexpr int kIdxChunks = kIdxSlice / 8;
+constexpr int kIdxPages = kBlock;   // pages of a block, one-token pages at most
 
 struct IndexArgs {
   const __nv_bfloat16* ik;
@@ -61,114 +64,125 @@ __device__ __forceinline__ BlockStart block_start(const IndexArgs& a, int64_t t,
   return b;
 }
 
-__device__ void index_block(const IndexArgs& a, int64_t t, const BlockStart& b, int32_t* pages) {
+struct IndexSmem {
+  uint4 rows[kBlock][kIdxChunks];  // the block's keys, the CTA's channels
+  int32_t pages[kIdxPages];
+  int32_t hit[kIdxThreads];
+  int n_hits;
+};
+
+__device__ void index_block(const IndexArgs& a, int64_t t, const BlockStart& b, IndexSmem& sm) {
   const int n_old = int(b.pos & 127);
   const int64_t first = b.pos - n_old;  // position of the block's first key
   const int n = n_old + b.n_new;
   const int64_t i0 = first >> a.table.shift;
   const int np = int(((first + n - 1) >> a.table.shift) - i0) + 1;
-  __syncthreads();  // the list of the block before is no longer read
+  __syncthreads();  // the block before is done
   bool bad = b.pos < 0;
   if (!bad)
     for (int i = threadIdx.x; i < np; i += kIdxThreads) {
       const int32_t p = page_of(a.table, b.row, (i0 + i) << a.table.shift);
-      pages[i] = p;
+      sm.pages[i] = p;
       bad |= p < 0;
     }
   if (__syncthreads_or(bad)) {
     if (threadIdx.x == 0) raise_paged(a.table.status, MSA_ERR_BAD_PAGE);
     return;
   }
-  __nv_bfloat16* keys = static_cast<__nv_bfloat16*>(a.keys.base);
   const int width = a.heads * a.dim;
   const int mask = (1 << a.table.shift) - 1;
-  for (int ch = 2 * threadIdx.x; ch < width; ch += 2 * kIdxThreads) {
-    const int h = ch / a.dim, c = ch % a.dim;
-    __nv_bfloat16* col = keys + h * a.keys.head + c;
+  // A thread's chunk is the same for all its keys.
+  const int ch = blockIdx.y * kIdxSlice + int(threadIdx.x % kIdxChunks) * 8;
+  if (ch < width) {
+    __nv_bfloat16* col =
+        static_cast<__nv_bfloat16*>(a.keys.base) + (ch / a.dim) * a.keys.head + ch % a.dim;
     const __nv_bfloat16* in = a.ik + t * a.ik_stride + ch;
-    float s0 = 0.f, s1 = 0.f;
-    // 32 keys' loads in flight, then their sum in order: the adds are one
-    // chain either way, the loads need not be.
-    for (int j0 = 0; j0 < n; j0 += 32) {
-      uint32_t w[32];
+    constexpr int kStep = kIdxThreads / kIdxChunks;
+    constexpr int kEach = kBlock / kStep;
+    uint4 w[kEach];
+    uint4* at[kEach];
 #pragma unroll
-      for (int u = 0; u < 32; ++u) {
-        const int j = j0 + u;
-        w[u] = 0;
-        if (j < n) {
-          const int64_t p = first + j;
-          const __nv_bfloat16* src =
-              j < n_old ? col + pages[(p >> a.table.shift) - i0] * a.keys.page +
-                              (p & mask) * a.keys.token
-                        : in + int64_t(j - n_old) * a.ik_stride;
-          w[u] = *reinterpret_cast<const uint32_t*>(src);
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < 32; ++u) {
-        const int j = j0 + u;
-        if (j < n) {
-          const float2 f = Pair<__nv_bfloat16>::unpack(w[u]);
-          s0 += f.x;
-          s1 += f.y;
-          if (j >= n_old) {
-            const int64_t p = first + j;
-            *reinterpret_cast<uint32_t*>(col + pages[(p >> a.table.shift) - i0] * a.keys.page +
-                                         (p & mask) * a.keys.token) = w[u];
-          }
-        }
+    for (int u = 0; u < kEach; ++u) {
+      const int j = u * kStep + int(threadIdx.x / kIdxChunks);
+      if (j < n) {
+        const int64_t p = first + j;
+        at[u] = reinterpret_cast<uint4*>(
+            col + sm.pages[(p >> a.table.shift) - i0] * a.keys.page + (p & mask) * a.keys.token);
+        w[u] = j < n_old ? *at[u]
+                         : *reinterpret_cast<const uint4*>(in + int64_t(j - n_old) * a.ik_stride);
       }
     }
-    const int64_t slot = mean_slot(a.table, pages[np - 1], int32_t(first + n - 1));
-    *reinterpret_cast<float2*>(a.means + slot * width + ch) =
+#pragma unroll
+    for (int u = 0; u < kEach; ++u) {
+      const int j = u * kStep + int(threadIdx.x / kIdxChunks);
+      if (j < n) {
+        sm.rows[j][threadIdx.x % kIdxChunks] = w[u];
+        if (j >= n_old) *at[u] = w[u];
+      }
+    }
+  }
+  __syncthreads();
+  const int c = blockIdx.y * kIdxSlice + 2 * int(threadIdx.x);
+  if (2 * threadIdx.x < kIdxSlice && c < width) {
+    const uint32_t* col = reinterpret_cast<const uint32_t*>(&sm.rows[0][0]) + threadIdx.x;
+    float s0 = 0.f, s1 = 0.f;
+#pragma unroll 16
+    for (int j = 0; j < n; ++j) {
+      const float2 f = Pair<__nv_bfloat16>::unpack(col[j * (kIdxSlice / 2)]);
+      s0 += f.x;
+      s1 += f.y;
+    }
+    const int64_t slot = mean_slot(a.table, sm.pages[np - 1], int32_t(first + n - 1));
+    *reinterpret_cast<float2*>(a.means + slot * width + c) =
         make_float2(__fdiv_rn(s0, float(n)), __fdiv_rn(s1, float(n)));
   }
 }
 
 __global__ void __launch_bounds__(kIdxThreads) k_paged_index(const IndexArgs a) {
-  __shared__ int32_t pages[kIdxPages];
-  __shared__ int32_t hit[32];
-  __shared__ int n_hits;
+  __shared__ IndexSmem sm;
   grid_dep_wait();
   grid_dep_release();
-  if (blockIdx.x == 0) check_offsets(a.offs, a.table.rows, a.T, a.table.status);
+  if (blockIdx.x == 0 && blockIdx.y == 0) check_offsets(a.offs, a.table.rows, a.T, a.table.status);
   if (a.T <= gridDim.x) {  // one token a CTA
     const int64_t t = blockIdx.x;
     const BlockStart b = block_start(a, t, find_row_warp(a.offs, a.table.rows, t));
-    if (b.n_new > 0) index_block(a, t, b, pages);
+    if (b.n_new > 0) index_block(a, t, b, sm);
     return;
   }
-  for (int64_t t0 = blockIdx.x; t0 < a.T; t0 += 32ll * gridDim.x) {
+  for (int64_t t0 = blockIdx.x; t0 < a.T; t0 += int64_t(kIdxThreads) * gridDim.x) {
     __syncthreads();
-    if (threadIdx.x < 32) {
-      const int64_t t = t0 + int64_t(threadIdx.x) * gridDim.x;
-      bool starts = false;
-      if (t < a.T) {
-        int32_t lo = 0, hi = a.table.rows - 1;  // largest r with offs[r] <= t
-        while (lo < hi) {
-          const int32_t mid = (lo + hi + 1) >> 1;
-          if (a.offs[mid] <= t) lo = mid; else hi = mid - 1;
-        }
-        starts = block_start(a, t, lo).n_new > 0;
+    if (threadIdx.x == 0) sm.n_hits = 0;
+    __syncthreads();
+    const int64_t t = t0 + int64_t(threadIdx.x) * gridDim.x;
+    if (t < a.T) {
+      int32_t lo = 0, hi = a.table.rows - 1;  // largest r with offs[r] <= t
+      while (lo < hi) {
+        const int32_t mid = (lo + hi + 1) >> 1;
+        if (a.offs[mid] <= t) lo = mid; else hi = mid - 1;
       }
-      const uint32_t m = __ballot_sync(0xffffffffu, starts);
-      if (starts) hit[__popc(m & ((1u << threadIdx.x) - 1))] = int32_t(t);
-      if (threadIdx.x == 0) n_hits = __popc(m);
+      if (block_start(a, t, lo).n_new > 0) sm.hit[atomicAdd(&sm.n_hits, 1)] = int32_t(t);
     }
     __syncthreads();
-    const int n = n_hits;
+    const int n = sm.n_hits;
     for (int i = 0; i < n; ++i) {
-      const int64_t t = hit[i];
-      const BlockStart b = block_start(a, t, find_row_warp(a.offs, a.table.rows, t));
-      index_block(a, t, b, pages);
+      const int64_t t = sm.hit[i];
+      index_block(a, t, block_start(a, t, find_row_warp(a.offs, a.table.rows, t)), sm);
     }
   }
 }
 
 // ------------------------------------------------------------------ selection
-constexpr int kSelThreads = 256;
-constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kSelWarps = 4;
+constexpr int kSelThreads = kSelWarps * 32;
 constexpr int kSelMaxCluster = 8;
+// A warp's ring of slabs: 32 channels of the means of 32 blocks, a block's
+// row 16 bytes longer than its 128 so that 8 rows' 16-byte reads hit
+// different banks.
+constexpr int kSlabRow = 144;
+constexpr int kSlabBytes = 32 * kSlabRow;
+constexpr int kSlabs = 4;
+constexpr int kSelFill = 4;  // CTAs an SM
+constexpr int kSelSmem = kSelWarps * kSlabs * kSlabBytes;  // 72 KB
 
 struct SelectArgs {
   const __nv_bfloat16* iq;
@@ -219,6 +233,7 @@ __device__ __forceinline__ uint64_t sort_desc(uint64_t x, int lane) {
 
 __global__ void __launch_bounds__(kSelThreads) k_paged_select(const SelectArgs a) {
   namespace cg = cooperative_groups;
+  extern __shared__ __align__(128) uint8_t slabs[];
   __shared__ float sq[128];
   __shared__ uint64_t lists[kSelWarps][kTopK];
   __shared__ uint64_t from[kSelMaxCluster][kTopK];
@@ -242,32 +257,85 @@ __global__ void __launch_bounds__(kSelThreads) k_paged_select(const SelectArgs a
     sq[c] = __bfloat162float(a.iq[(int64_t(r) * a.heads + h) * a.dim + c]);
   __syncthreads();
   const int32_t lo = a.force ? 1 : 0, hi = a.force ? b - 1 : b;
-  uint64_t best = 0;  // the warp's best candidates, sorted over the lanes
-  for (int32_t v0 = lo + (rank * kSelWarps + warp) * 32; v0 <= hi; v0 += C * kSelThreads) {
-    const int32_t v = v0 + lane;
-    uint64_t key = 0;
+  // The warp's slabs in order: for every group of 32 blocks, its channels 32
+  // at a time.  fetch runs kSlabs - 1 slabs ahead of the sums.
+  const uint32_t ring = uint32_t(__cvta_generic_to_shared(slabs)) + warp * (kSlabs * kSlabBytes);
+  const int per = (a.dim + 31) / 32;
+  const int32_t v_step = C * kSelThreads;
+  int32_t fv = lo + (rank * kSelWarps + warp) * 32;  // first block of the group being fetched
+  int fc = 0;                                        // its next slab
+  int64_t row = -1;                                  // the lane's block in it: row of the means
+  auto locate = [&]() {
+    const int32_t v = fv + lane;
+    row = -1;
     if (v <= hi) {
       const int32_t last = min(v * kBlock + kBlock - 1, len - 1);
       const int32_t page = page_of(a.table, r, last);
-      if (page >= 0) {
-        const float4* m = reinterpret_cast<const float4*>(
-            a.means + (mean_slot(a.table, page, last) * a.heads + h) * a.dim);
-        float acc = 0.f;
-#pragma unroll 8
-        for (int c = 0; c < a.dim / 4; ++c) {
-          const float4 s = m[c];
-          acc = fmaf(sq[4 * c + 0], s.x, acc);
-          acc = fmaf(sq[4 * c + 1], s.y, acc);
-          acc = fmaf(sq[4 * c + 2], s.z, acc);
-          acc = fmaf(sq[4 * c + 3], s.w, acc);
+      if (page >= 0) row = mean_slot(a.table, page, last) * a.heads + h;
+    }
+  };
+  if (fv <= hi) locate();
+  auto fetch = [&](int stage) {
+    if (fv > hi) return;
+    const int c = fc * 32 + (lane & 7) * 4;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {  // 4 rows of 128 bytes an instruction
+      const int k = i * 4 + (lane >> 3);
+      const int64_t m = __shfl_sync(0xffffffffu, row, k);
+      const bool real = m >= 0 && c < a.dim;
+      const float* src = real ? a.means + m * a.dim + c : a.means;
+      asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(
+                       ring + stage * kSlabBytes + k * kSlabRow + (lane & 7) * 16),
+                   "l"(src), "r"(real ? 16 : 0)
+                   : "memory");
+    }
+    if (++fc == per) {
+      fc = 0;
+      fv += v_step;
+      if (fv <= hi) locate();
+    }
+  };
+  uint64_t best = 0;  // the warp's best candidates, sorted over the lanes
+  int32_t gv = fv;    // the group being summed
+  int stage = 0;
+  for (int i = 0; i < kSlabs - 1; ++i) {
+    fetch(i);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  while (gv <= hi) {
+    float acc = 0.f;
+    for (int c = 0; c < per; ++c) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kSlabs - 2) : "memory");
+      __syncwarp();
+      fetch((stage + kSlabs - 1) % kSlabs);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      const float4* m = reinterpret_cast<const float4*>(
+          slabs + warp * (kSlabs * kSlabBytes) + stage * kSlabBytes + lane * kSlabRow);
+      const int n4 = min(8, (a.dim - c * 32) / 4);
+      const float* q = sq + c * 32;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if (k < n4) {
+          const float4 s = m[k];
+          acc = fmaf(q[4 * k + 0], s.x, acc);
+          acc = fmaf(q[4 * k + 1], s.y, acc);
+          acc = fmaf(q[4 * k + 2], s.z, acc);
+          acc = fmaf(q[4 * k + 3], s.w, acc);
         }
-        key = rank_key(acc, v);
       }
+      stage = (stage + 1) % kSlabs;
+    }
+    uint64_t key = 0;
+    if (gv + lane <= hi) {
+      const int32_t v = gv + lane;
+      const int32_t last = min(v * kBlock + kBlock - 1, len - 1);
+      if (page_of(a.table, r, last) >= 0) key = rank_key(acc, v);
     }
     key = sort_desc(key, lane);
     // the larger of best[i] and key[31 - i] are the best 32 of both lists
     const uint64_t rev = __shfl_sync(0xffffffffu, key, 31 - lane);
     best = bitonic_merge<32>(max64(best, rev), lane);
+    gv += v_step;
   }
   if (lane < kTopK) lists[warp][lane] = best;
   __syncthreads();
@@ -308,13 +376,21 @@ __global__ void __launch_bounds__(kSelThreads) k_paged_select(const SelectArgs a
 }
 
 cudaError_t launch_paged_select(const SelectArgs& a, cudaStream_t s) {
-  // CTAs of a cluster: one for every 256 blocks that the table has room for.
+  // CTAs of a cluster: one for every 128 blocks that the table has room for,
+  // while the batch alone does not fill the chip.
   const int64_t room = ((int64_t(a.table.width) << a.table.shift) + kBlock - 1) / kBlock;
+  const int64_t units = int64_t(a.table.rows) * a.heads;
   int C = 1;
-  while (C < kSelMaxCluster && room > int64_t(C) * kSelThreads) C *= 2;
+  while (C < kSelMaxCluster && room > int64_t(C) * kSelThreads &&
+         units * C < int64_t(kSelFill) * device_sm_count())
+    C *= 2;
+  cudaError_t e = cudaFuncSetAttribute(k_paged_select, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       kSelSmem);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(int64_t(a.table.rows) * a.heads * C));
   cfg.blockDim = dim3(kSelThreads);
+  cfg.dynamicSmemBytes = kSelSmem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -359,12 +435,14 @@ extern "C" msa_status msa_paged_index(const msa_paged_index_cache* cache,
   a.T = T;
   a.heads = cache->heads;
   a.dim = cache->dim;
-  // An odd number of CTAs: blocks start 128 tokens apart, and an odd stride
-  // spreads them over all CTAs.
-  const int64_t most = int64_t(device_sm_count()) * 8 - 1;
+  const int slices = (a.heads * a.dim + kIdxSlice - 1) / kIdxSlice;
+  // Six CTAs an SM (their shared memory).  An odd number of them along the
+  // tokens: blocks start 128 tokens apart, and an odd stride spreads them
+  // over all CTAs.
+  const int64_t most = int64_t(device_sm_count()) * 6 / slices | 1;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   launch_begin("paged_index", s);
-  const cudaError_t e = launch_k(true, k_paged_index, dim3(unsigned(T < most ? T : most)),
+  const cudaError_t e = launch_k(true, k_paged_index, dim3(unsigned(T < most ? T : most), slices),
                                  dim3(kIdxThreads), 0, s, a);
   launch_end("paged_index", s);
   return e == cudaSuccess ? MSA_OK : MSA_ERR_CUDA;

@@ -13,6 +13,7 @@ from block_sparse_gqa_msa_gb300 import api
 from block_sparse_gqa_msa_gb300 import build as msa_build
 
 OK, INVALID, ALIGN, WORKSPACE = 0, 1, 3, 4
+CPU = torch.device("cpu")
 G = 0x10000  # an aligned address that no refused call reads
 
 
@@ -150,25 +151,29 @@ def test_binding_refuses_cpu_and_overlapping_tensors():
 
 def test_binding_checks_layouts():
     with pytest.raises(TypeError):
-        api._table(torch.zeros(2, 3, dtype=torch.int64))
+        api._table(torch.zeros(2, 3, dtype=torch.int64), CPU)
     with pytest.raises(ValueError):
-        api._table(torch.zeros(3, dtype=torch.int32))
+        api._table(torch.zeros(3, dtype=torch.int32), CPU)
     with pytest.raises(ValueError):
-        api._table(torch.zeros(3, 2, dtype=torch.int32).t())
+        api._table(torch.zeros(3, 2, dtype=torch.int32).t(), CPU)
     with pytest.raises(ValueError):
-        api._table(torch.zeros(1, 5, dtype=torch.int32).expand(4, 5))
-    t = api._table(torch.zeros(4, 9, dtype=torch.int32)[1:3, 2:7])
+        api._table(torch.zeros(1, 5, dtype=torch.int32).expand(4, 5), CPU)
+    with pytest.raises(ValueError):
+        api._table(torch.zeros(3, 2, dtype=torch.int32), torch.device("cuda:0"))
+    t = api._table(torch.zeros(4, 9, dtype=torch.int32)[1:3, 2:7], CPU)
     assert (t.rows, t.width, t.stride) == (2, 5, 9)
-    one = api._table(torch.zeros(4, 9, dtype=torch.int32)[:1, :5])
+    one = api._table(torch.zeros(4, 9, dtype=torch.int32)[:1, :5], CPU)
     assert one.stride >= one.width
     qkv = torch.zeros(5, 72, 128, dtype=torch.float16)
-    assert api._tokens(qkv[:, 64:68], "k", torch.float16, 4, 128) == 72 * 128
+    assert api._tokens(qkv[:, 64:68], "k", torch.float16, 5, 4, 128, CPU) == 72 * 128
     for x, dt, h, d in ((qkv, torch.bfloat16, 72, 128), (qkv, torch.float16, 4, 128),
                         (qkv, torch.float16, 72, 64), (qkv[0], torch.float16, 72, 128),
                         (qkv[:, ::2], torch.float16, 36, 128),
                         (qkv.transpose(1, 2), torch.float16, 128, 72)):
         with pytest.raises((TypeError, ValueError)):
-            api._tokens(x, "x", dt, h, d)
+            api._tokens(x, "x", dt, None, h, d, CPU)
+    with pytest.raises(ValueError):
+        api._tokens(qkv, "x", torch.float16, 6, 72, 128, CPU)
 
 
 @pytest.mark.skipif(shutil.which("gcc") is None, reason="needs a C compiler")
