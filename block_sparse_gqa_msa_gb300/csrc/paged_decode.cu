@@ -29,9 +29,10 @@
 // each of its CTAs leaves its (m, l, O) in the workspace and k_paged_join adds
 // them up, in order, so results do not depend on timing.
 //
-// A warp works alone on 16 keys of each tile: it fetches them with
-// asynchronous copies into its own ring of stages and never waits for
-// another warp until the segment's end.
+// A warp works alone on its share of each tile (16 keys of 128 channels, 32 of
+// 64: 8 KB of keys and values): it fetches them with asynchronous copies into
+// its own ring of stages, two stages ahead and across segment borders, and
+// waits for other warps only where a segment ends.
 #include "paged.cuh"
 
 namespace msa {
@@ -39,20 +40,24 @@ namespace {
 
 constexpr int kDecWarps = 4;
 constexpr int kDecThreads = kDecWarps * 32;
-constexpr int kWarpKeys = 16;                       // keys of a warp in a tile
-constexpr int kTileKeys = kDecWarps * kWarpKeys;    // 64
-constexpr int kTilesPerBlock = kBlock / kTileKeys;  // 2
-constexpr int kGroup = 16;                          // query heads of a tile
+constexpr int kGroup = 16;   // query heads of a matrix tile
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 template <int kDim>
 struct DecodeShape {
-  static constexpr int kRow = kDim * 2;                  // bytes of a key
-  static constexpr int kStageBytes = 2 * kWarpKeys * kRow;  // keys and values of a warp
-  static constexpr int kStages = kDim == 128 ? 3 : 6;    // 24 KB a warp
+  static constexpr int kWarpKeys = 2048 / kDim;              // keys of a warp in a tile
+  static constexpr int kTileKeys = kDecWarps * kWarpKeys;    // 64 or 128
+  static constexpr int kTilesPerBlock = kBlock / kTileKeys;  // 2 or 1
+  static constexpr int kRow = kDim * 2;                      // bytes of a key
+  static constexpr int kStageBytes = 2 * kWarpKeys * kRow;   // 8 KB
+  static constexpr int kStages = 3;
   static constexpr int kRing = kStages * kStageBytes;
-  static constexpr int kSmem = kDecWarps * kRing;        // 96 KB a CTA
+  // the warps' states meet 32 channels at a time, rows 40 floats apart
+  // (8 rows' 8-byte writes then hit all banks once)
+  static constexpr int kMergeRow = 40;
+  static constexpr int kMergeBytes = kDecWarps * kGroup * kMergeRow * 4;
+  static constexpr int kSmem = kDecWarps * kRing + kMergeBytes;  // 106 KB a CTA
 };
 
 // What a CTA leaves for the join about the unit that its run starts inside.
@@ -76,6 +81,15 @@ struct DecodeArgs {
   float* part_o;       // [2 grid][16][dim]
 };
 
+__device__ __forceinline__ float exp2_fast(float x) {  // to 2^-22, results below 2^-126 are 0
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src)
+               : "memory");
+}
 __device__ __forceinline__ void cp_async16_if(uint32_t dst, const void* src, bool real) {
   asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
                "r"(real ? 16 : 0)
@@ -124,13 +138,15 @@ __device__ __forceinline__ void mma16816<__half>(float (&d)[4], const uint32_t (
 
 // Tiles of one unit of a row of len keys (at least one, so that rows without
 // keys are written too).
+template <int kDim>
 __device__ __forceinline__ int32_t unit_tiles(int32_t len, bool sparse) {
+  using S = DecodeShape<kDim>;
   int32_t n;
   if (sparse) {
     const int32_t nb = int32_t((int64_t(len) + kBlock - 1) / kBlock);
-    n = min(nb, kTopK) * kTilesPerBlock;
+    n = min(nb, kTopK) * S::kTilesPerBlock;
   } else {
-    n = int32_t((int64_t(len) + kTileKeys - 1) / kTileKeys);
+    n = int32_t((int64_t(len) + S::kTileKeys - 1) / S::kTileKeys);
   }
   return max(n, 1);
 }
@@ -153,6 +169,7 @@ struct Place {
 // Finds the CTA's run.  Every thread sums the tiles of a stretch of rows; a
 // scan over the threads' sums gives the total and, for the one stretch that
 // holds lo, its place.
+template <int kDim>
 __device__ __forceinline__ Place find_place(const DecodeArgs& a, int64_t* sums, Place* found) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const bool sparse = a.q2k != nullptr;
@@ -169,7 +186,7 @@ __device__ __forceinline__ Place find_place(const DecodeArgs& a, int64_t* sums, 
       n = 0;
     }
     if (r == r0) first_len = n;
-    mine += int64_t(unit_tiles(n, sparse)) * a.kv_heads;
+    mine += int64_t(unit_tiles<kDim>(n, sparse)) * a.kv_heads;
   }
   int64_t incl = mine;
 #pragma unroll
@@ -196,7 +213,7 @@ __device__ __forceinline__ Place find_place(const DecodeArgs& a, int64_t* sums, 
         len = a.kv_len[r];
         if (len < 0 || len > most) len = 0;
       }
-      const int32_t tiles = unit_tiles(len, sparse);
+      const int32_t tiles = unit_tiles<kDim>(len, sparse);
       const int64_t here = int64_t(tiles) * a.kv_heads;
       if (lo < at + here) {
         Place p;
@@ -219,99 +236,203 @@ __device__ __forceinline__ Place find_place(const DecodeArgs& a, int64_t* sums, 
   return *found;
 }
 
-// One warp's keys of a stretch of tiles [i0, i1) of a unit: the fetching side.
+// A part of a unit that one CTA works on: its tiles i0 .. i1 - 1.
+struct Segment {
+  int32_t row, head, i0, i1, tiles;
+};
+constexpr int kSegQueue = 8;  // the fetch is at most kStages tiles, so segments, ahead
+
+// The fetching side of a warp: walks the run's tiles ahead of the sums and
+// leaves each segment that it enters in a queue.  All its state is the same
+// in all lanes except page and slots.
 template <typename T, int kDim>
 struct Fetch {
-  static constexpr int kChunks = kDim / 8;         // 16-byte chunks of a key
+  using S = DecodeShape<kDim>;
+  static constexpr int kChunks = kDim / 8;          // 16-byte chunks of a key
   static constexpr int kRowsAtOnce = 32 / kChunks;  // keys one copy instruction covers
-  static constexpr int kCopies = kWarpKeys / kRowsAtOnce;
+  static constexpr int kCopies = S::kWarpKeys / kRowsAtOnce;
+  static constexpr int kWhole = S::kWarpKeys == 32 ? 5 : 4;  // log2 of a warp's keys
   const DecodeArgs& a;
-  const int32_t* blocks;  // the unit's blocks (sparse), shared memory
-  int32_t n_blocks;
-  int32_t row, head, len, lane, warp;
+  int32_t* blocks;   // the unit's blocks (sparse), shared memory
+  Segment* queue;
+  int lane, warp;
+  int64_t left;      // tiles of the run after the current segment
+  int32_t row, head, len, tiles, i, i1, n_blocks, n_seg;
+  int32_t next_len, slots;  // of the next unit, loaded ahead
+  int32_t j;         // first key of the warp's part of the tile at hand, -1: none
+  int32_t page;      // its page as the table has it, unchecked
 
-  // First key of the warp's part of tile i, or -1: nothing to see there.
-  __device__ __forceinline__ int32_t first_key(int32_t i) const {
-    int32_t j;
+  __device__ __forceinline__ int32_t checked(int32_t n) const {
+    return n < 0 || n > (int64_t(a.table.width) << a.table.shift) ? 0 : n;
+  }
+  __device__ __forceinline__ void load_slots(int32_t r, int32_t h) {
+    if (a.q2k && lane < kTopK && r < a.table.rows)
+      slots = a.q2k[(int64_t(h) * a.table.rows + r) * kTopK + lane];
+  }
+  // Enters the unit (row, head) at tile i: its blocks (the distinct valid
+  // slots, in slot order), its place in the queue, and a look ahead.
+  __device__ __forceinline__ void enter() {
     if (a.q2k) {
-      const int32_t s = i / kTilesPerBlock;
-      if (s >= n_blocks) return -1;
-      j = blocks[s] * kBlock + (i % kTilesPerBlock) * kTileKeys + warp * kWarpKeys;
-    } else {
-      j = i * kTileKeys + warp * kWarpKeys;
+      const int32_t nb = int32_t((int64_t(len) + kBlock - 1) / kBlock);
+      const int32_t v = slots;
+      const bool ok = lane < kTopK && v >= 0 && v < nb;
+      if (lane < kTopK && len > 0 && v != -1 && !ok) raise_paged(a.table.status, MSA_ERR_BAD_Q2K);
+      const uint32_t same = __match_any_sync(0xffffffffu, ok ? v : -1 - lane);
+      const bool keep = ok && (__ffs(same) - 1) == lane;
+      const uint32_t m = __ballot_sync(0xffffffffu, keep);
+      n_blocks = __popc(m);
+      __syncwarp();  // the list before is read
+      if (keep) blocks[__popc(m & ((1u << lane) - 1))] = v;
     }
-    return j < len ? j : -1;
+    if (lane == 0) queue[n_seg % kSegQueue] = Segment{row, head, i, i1, tiles};
+    ++n_seg;
+    __syncwarp();
+    if (left > 0) {  // the next unit: its length, slots and queries
+      const int32_t r = head + 1 == a.kv_heads ? row + 1 : row;
+      const int32_t h = head + 1 == a.kv_heads ? 0 : head + 1;
+      next_len = a.kv_len[r];
+      load_slots(r, h);
+      if (lane * 64 < a.group * kDim)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(
+            static_cast<const T*>(a.q) + (int64_t(r) * a.kv_heads + h) * a.group * kDim +
+            lane * 64));
+    }
   }
-  // Page of key j + lane (lanes 0 .. 15), -1 past the row's end or if bad.
-  // Pages of 16 tokens and more hold all 16 keys: every lane gets that page.
-  __device__ __forceinline__ int32_t page(int32_t j) const {
-    if (j < 0) return -1;
-    if (a.table.shift >= 4) return page_of(a.table, row, j);
-    if (lane >= kWarpKeys || j + lane >= len) return -1;
-    return page_of(a.table, row, j + lane);
+  __device__ __forceinline__ void begin(const Place& p) {
+    row = p.row;
+    head = p.head;
+    len = p.len;
+    tiles = p.tiles;
+    i = int32_t(p.lo - p.unit_start);
+    const int64_t n = p.hi - p.lo;
+    i1 = int32_t(min(int64_t(tiles), i + n));
+    left = n - (i1 - i);
+    n_blocks = 0;
+    n_seg = 0;
+    slots = -1;
+    load_slots(row, head);
+    enter();
+    look();
   }
-  // Starts the copies of keys j .. j + 15 into a stage: the keys, then the
+  __device__ __forceinline__ void advance() {
+    if (i1 == 0) return;  // the run is done
+    if (++i == i1) {
+      if (left == 0) {
+        i1 = 0;
+        j = -1;
+        return;
+      }
+      if (++head == a.kv_heads) {
+        head = 0;
+        ++row;
+        len = checked(next_len);
+        tiles = unit_tiles<kDim>(len, a.q2k != nullptr);
+      }
+      i = 0;
+      i1 = int32_t(min(int64_t(tiles), left));
+      left -= i1;
+      enter();
+    }
+    look();
+  }
+  // The warp's first key in tile i and its page (loaded, not looked at yet).
+  // Where a page holds all the warp's keys every lane loads that page, else
+  // lane l the page of key j + l.
+  __device__ __forceinline__ void look() {
+    j = -1;
+    if (a.q2k) {
+      const int32_t s = i / S::kTilesPerBlock;
+      if (s < n_blocks)
+        j = blocks[s] * kBlock + (i % S::kTilesPerBlock) * S::kTileKeys + warp * S::kWarpKeys;
+    } else {
+      j = i * S::kTileKeys + warp * S::kWarpKeys;
+    }
+    if (j >= len) j = -1;
+    page = -1;
+    if (j < 0) return;
+    const int32_t* t = a.table.pages + int64_t(row) * a.table.stride;
+    if (a.table.shift >= kWhole)
+      page = t[j >> a.table.shift];
+    else if (lane < S::kWarpKeys && j + lane < len)
+      page = t[(j + lane) >> a.table.shift];
+  }
+  // Starts the copies of the tile at hand into a stage: the keys, then the
   // values; a key's 16-byte chunk c sits at c ^ (key & 7), so that the 8 rows
   // of a matrix load hit different banks.  Keys that are not there become
   // zeros (a masked key's weight is 0, and 0 times what lies there must be 0).
   // Returns the mask of the keys that are there.
-  __device__ __forceinline__ uint32_t copy(uint32_t stage, int32_t j, int32_t pg) const {
+  __device__ __forceinline__ uint32_t copy(uint32_t stage) const {
     if (j < 0) return 0;
     const int sub = lane / kChunks, c = lane % kChunks;
     const int mask = (1 << a.table.shift) - 1;
     const T* kb = static_cast<const T*>(a.k.base) + head * a.k.head + c * 8;
     const T* vb = static_cast<const T*>(a.v.base) + head * a.v.head + c * 8;
-    if (a.table.shift >= 4) {
-      if (pg < 0) return 0;
-      const int64_t slot = j & mask;
-      kb += pg * a.k.page + (slot + sub) * a.k.token;
-      vb += pg * a.v.page + (slot + sub) * a.v.token;
-      const int left = len - j;
-#pragma unroll
-      for (int i = 0; i < kCopies; ++i) {
-        const int key = i * kRowsAtOnce + sub;
-        const uint32_t dst = stage + key * (kDim * 2) + ((c ^ (key & 7)) << 4);
-        const bool real = key < left;
-        // a key past the end copies nothing; its address is the first key's
-        cp_async16_if(dst, real ? kb + int64_t(i * kRowsAtOnce) * a.k.token : kb - sub * a.k.token,
-                      real);
-        cp_async16_if(dst + kWarpKeys * kDim * 2,
-                      real ? vb + int64_t(i * kRowsAtOnce) * a.v.token : vb - sub * a.v.token,
-                      real);
+    constexpr int kValues = S::kWarpKeys * S::kRow;
+    if (a.table.shift >= kWhole) {
+      if (page < 0 || page >= a.table.num_pages) {
+        raise_paged(a.table.status, MSA_ERR_BAD_PAGE);
+        return 0;
       }
-      return left >= kWarpKeys ? 0xffffu : (1u << left) - 1;
-    }
-    const uint32_t there = __ballot_sync(0xffffffffu, pg >= 0);
+      const int64_t slot = j & mask;
+      kb += page * a.k.page + slot * a.k.token;
+      vb += page * a.v.page + slot * a.v.token;
+      const int n = len - j;
+      if (n >= S::kWarpKeys) {
 #pragma unroll
-    for (int i = 0; i < kCopies; ++i) {
-      const int key = i * kRowsAtOnce + sub;
-      const int32_t p = __shfl_sync(0xffffffffu, pg, key);
-      const uint32_t dst = stage + key * (kDim * 2) + ((c ^ (key & 7)) << 4);
+        for (int x = 0; x < kCopies; ++x) {
+          const int key = x * kRowsAtOnce + sub;
+          const uint32_t dst = stage + key * S::kRow + ((c ^ (key & 7)) << 4);
+          cp_async16(dst, kb + key * a.k.token);
+          cp_async16(dst + kValues, vb + key * a.v.token);
+        }
+        return 0xffffffffu >> (32 - S::kWarpKeys);
+      }
+#pragma unroll 4
+      for (int x = 0; x < kCopies; ++x) {
+        const int key = x * kRowsAtOnce + sub;
+        const uint32_t dst = stage + key * S::kRow + ((c ^ (key & 7)) << 4);
+        const bool real = key < n;  // else nothing is read; the address is the first key's
+        cp_async16_if(dst, kb + (real ? key : 0) * a.k.token, real);
+        cp_async16_if(dst + kValues, vb + (real ? key : 0) * a.v.token, real);
+      }
+      return (1u << n) - 1;
+    }
+    const bool due = lane < S::kWarpKeys && j + lane < len;
+    const bool good = due && page >= 0 && page < a.table.num_pages;
+    if (due && !good) raise_paged(a.table.status, MSA_ERR_BAD_PAGE);
+    const uint32_t there = __ballot_sync(0xffffffffu, good);
+#pragma unroll 4
+    for (int x = 0; x < kCopies; ++x) {
+      const int key = x * kRowsAtOnce + sub;
+      const int32_t p = __shfl_sync(0xffffffffu, good ? page : -1, key);
+      const uint32_t dst = stage + key * S::kRow + ((c ^ (key & 7)) << 4);
       const int64_t slot = (j + key) & mask;
       cp_async16_if(dst, p >= 0 ? kb + p * a.k.page + slot * a.k.token : a.k.base, p >= 0);
-      cp_async16_if(dst + kWarpKeys * kDim * 2,
-                    p >= 0 ? vb + p * a.v.page + slot * a.v.token : a.v.base, p >= 0);
+      cp_async16_if(dst + kValues, p >= 0 ? vb + p * a.v.page + slot * a.v.token : a.v.base,
+                    p >= 0);
     }
-    return there & 0xffffu;
+    return there;
   }
 };
 
 template <typename T, int kDim>
 __global__ void __launch_bounds__(kDecThreads, 2) k_paged_decode(const DecodeArgs a) {
   using S = DecodeShape<kDim>;
-  constexpr int kSteps = kDim / 16;  // k-steps of the first product
-  constexpr int kCols = kDim / 8;    // column tiles of the second
+  constexpr int kSteps = kDim / 16;            // k-steps of the first product
+  constexpr int kCols = kDim / 8;              // column tiles of the second
+  constexpr int kKeyTiles = S::kWarpKeys / 8;  // column tiles of the first
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int64_t sums[kDecWarps];
   __shared__ Place found;
   __shared__ int32_t blocks[kDecWarps][kTopK];
+  __shared__ Segment queue[kDecWarps][kSegQueue];
   __shared__ float ml[2][kDecWarps][kGroup];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r_lo = lane >> 2;  // the lane's matrix rows: r_lo and r_lo + 8
   const int col = (lane & 3) * 2;
   grid_dep_wait();
   grid_dep_release();
-  Place p = find_place(a, sums, &found);
+  const Place p = find_place<kDim>(a, sums, &found);
   if (blockIdx.x >= p.ctas) {
     if (tid == 0) a.rec[blockIdx.x] = JoinRec{0, 0};
     return;
@@ -330,50 +451,28 @@ __global__ void __launch_bounds__(kDecThreads, 2) k_paged_decode(const DecodeArg
   }
 
   const uint32_t ring = uint32_t(__cvta_generic_to_shared(smem)) + warp * S::kRing;
-  float* merge = reinterpret_cast<float*>(smem);  // [warp][16][dim], after the ring is drained
-  int64_t at = p.lo;
-  while (true) {
-    const int64_t unit_end = p.unit_start + p.tiles;
-    const int64_t seg_end = unit_end < p.hi ? unit_end : p.hi;
-    const int32_t i0 = int32_t(at - p.unit_start), i1 = int32_t(seg_end - p.unit_start);
-
-    // ---- the unit's blocks: distinct valid slots, in slot order
-    int32_t n_blocks = 0;
-    if (a.q2k) {
-      const int32_t nb = int32_t((int64_t(p.len) + kBlock - 1) / kBlock);
-      int32_t v = -1;
-      if (lane < kTopK) v = a.q2k[(int64_t(p.head) * a.table.rows + p.row) * kTopK + lane];
-      const bool ok = lane < kTopK && v >= 0 && v < nb;
-      if (lane < kTopK && p.len > 0 && v != -1 && !ok)
-        raise_paged(a.table.status, MSA_ERR_BAD_Q2K);
-      const uint32_t same = __match_any_sync(0xffffffffu, ok ? v : -1 - lane);
-      const bool keep = ok && (__ffs(same) - 1) == lane;
-      const uint32_t m = __ballot_sync(0xffffffffu, keep);
-      n_blocks = __popc(m);
-      if (keep) blocks[warp][__popc(m & ((1u << lane) - 1))] = v;
-      __syncwarp();
-    }
-    const Fetch<T, kDim> fetch{a, blocks[warp], n_blocks, p.row, p.head, p.len, lane, warp};
-
-    // ---- fill the ring
-    uint32_t there[S::kStages];  // keys that are there, by stage
+  float* merge = reinterpret_cast<float*>(smem + kDecWarps * S::kRing);
+  Fetch<T, kDim> fetch{a, blocks[warp], queue[warp], lane, warp};
+  fetch.begin(p);
+  uint32_t there[S::kStages - 1];  // of the tiles in flight: the keys that are there
 #pragma unroll
-    for (int s = 0; s < S::kStages - 1; ++s) {
-      there[s] = 0;
-      if (i0 + s < i1) {
-        const int32_t j = fetch.first_key(i0 + s);
-        there[s] = fetch.copy(ring + s * S::kStageBytes, j, fetch.page(j));
-      }
-      cp_async_commit();
-    }
-    int32_t next_j = i0 + S::kStages - 1 < i1 ? fetch.first_key(i0 + S::kStages - 1) : -1;
-    int32_t next_page = fetch.page(next_j);
+  for (int s = 0; s < S::kStages - 1; ++s) {
+    there[s] = fetch.copy(ring + s * S::kStageBytes);
+    cp_async_commit();
+    fetch.advance();
+  }
+
+  int64_t left = p.hi - p.lo;
+  int stage = 0;
+  for (int seg = 0; left > 0; ++seg) {
+    const Segment g = queue[warp][seg % kSegQueue];
+    left -= g.i1 - g.i0;
 
     // ---- the query heads as the left operand; heads past the group are zeros
     uint32_t qa[kSteps][4];
     {
       const T* q = static_cast<const T*>(a.q) +
-                   (int64_t(p.row) * a.kv_heads + p.head) * a.group * kDim + col;
+                   (int64_t(g.row) * a.kv_heads + g.head) * a.group * kDim + col;
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
         const uint32_t* lo = reinterpret_cast<const uint32_t*>(q + r_lo * kDim + s * 16);
@@ -390,104 +489,99 @@ __global__ void __launch_bounds__(kDecThreads, 2) k_paged_decode(const DecodeArg
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
 
     // ---- the keys
-    for (int32_t base = i0; base < i1; base += S::kStages) {
+#pragma unroll 1
+    for (int32_t i = g.i0; i < g.i1; ++i) {
+      cp_async_wait<S::kStages - 2>();
+      __syncwarp();
+      const uint32_t seen = there[0];
+      const uint32_t kb = ring + stage * S::kStageBytes, vb = kb + S::kWarpKeys * S::kRow;
+      // the stage freed by the last tile takes the tile kStages - 1 ahead
+      {
+        const int free = stage == 0 ? S::kStages - 1 : stage - 1;
+        stage = stage + 1 == S::kStages ? 0 : stage + 1;
 #pragma unroll
-      for (int s = 0; s < S::kStages; ++s) {
-        const int32_t i = base + s;
-        if (i >= i1) break;
-        cp_async_wait<S::kStages - 2>();
-        __syncwarp();
-        // the stage freed by the last tile takes the tile kStages - 1 ahead
-        {
-          constexpr int kLast = S::kStages - 1;
-          const int d = (s + kLast) % S::kStages;
-          const uint32_t got = fetch.copy(ring + d * S::kStageBytes, next_j, next_page);
-          cp_async_commit();
-#pragma unroll
-          for (int x = 0; x < S::kStages; ++x)
-            if (x == d) there[x] = got;
-          const int32_t in = i + S::kStages;
-          next_j = in < i1 ? fetch.first_key(in) : -1;
-          next_page = fetch.page(next_j);
-        }
-        const uint32_t seen = there[s];
-        if (seen == 0) continue;
-        const uint32_t kb = ring + s * S::kStageBytes, vb = kb + kWarpKeys * S::kRow;
+        for (int s = 0; s + 1 < S::kStages - 1; ++s) there[s] = there[s + 1];
+        there[S::kStages - 2] = fetch.copy(ring + free * S::kStageBytes);
+        cp_async_commit();
+        fetch.advance();
+      }
+      if (seen == 0) continue;
 
-        float x[2][4];
+      float x[kKeyTiles][4];
 #pragma unroll
-        for (int n = 0; n < 2; ++n) x[n][0] = x[n][1] = x[n][2] = x[n][3] = 0.f;
-        {
-          // matrices: keys 0-7 / 8-15 by channels 0-7 / 8-15 of the step
-          const int key = (lane & 7) + ((lane >> 4) << 3);
-          const uint32_t rowp = kb + key * S::kRow;
+      for (int n = 0; n < kKeyTiles; ++n) x[n][0] = x[n][1] = x[n][2] = x[n][3] = 0.f;
 #pragma unroll
-          for (int k = 0; k < kSteps; ++k) {
-            uint32_t b[4];
-            ldsm4(b, rowp + (((2 * k + ((lane >> 3) & 1)) ^ (key & 7)) << 4));
-            mma16816<T>(x[0], qa[k], b[0], b[1]);
-            mma16816<T>(x[1], qa[k], b[2], b[3]);
-          }
+      for (int n = 0; n < kKeyTiles; n += 2) {
+        // matrices: keys 0-7 / 8-15 by channels 0-7 / 8-15 of the step
+        const int key = n * 8 + (lane & 7) + ((lane >> 4) << 3);
+        const uint32_t rowp = kb + key * S::kRow;
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k) {
+          uint32_t b[4];
+          ldsm4(b, rowp + (((2 * k + ((lane >> 3) & 1)) ^ (key & 7)) << 4));
+          mma16816<T>(x[n], qa[k], b[0], b[1]);
+          mma16816<T>(x[n + 1], qa[k], b[2], b[3]);
         }
-        // scores in base 2, masked
-        float top0 = -INFINITY, top1 = -INFINITY;
+      }
+      // scores in base 2, masked
+      float top0 = -INFINITY, top1 = -INFINITY;
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
+      for (int n = 0; n < kKeyTiles; ++n) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const bool on = (seen >> (n * 8 + col + (e & 1))) & 1;
-            x[n][e] = on ? x[n][e] * a.scale_log2 : -INFINITY;
-          }
-          top0 = fmaxf(top0, fmaxf(x[n][0], x[n][1]));
-          top1 = fmaxf(top1, fmaxf(x[n][2], x[n][3]));
+        for (int e = 0; e < 4; ++e) {
+          const bool on = (seen >> (n * 8 + col + (e & 1))) & 1;
+          x[n][e] = on ? x[n][e] * a.scale_log2 : -INFINITY;
         }
-        top0 = fmaxf(top0, __shfl_xor_sync(0xffffffffu, top0, 1));
-        top1 = fmaxf(top1, __shfl_xor_sync(0xffffffffu, top1, 1));
-        top0 = fmaxf(top0, __shfl_xor_sync(0xffffffffu, top0, 2));
-        top1 = fmaxf(top1, __shfl_xor_sync(0xffffffffu, top1, 2));
-        if (__any_sync(0xffffffffu, top0 > m0 || top1 > m1)) {
-          const float n0 = fmaxf(m0, top0), n1 = fmaxf(m1, top1);
-          const float f0 = n0 == -INFINITY ? 1.f : exp2f(m0 - n0);
-          const float f1 = n1 == -INFINITY ? 1.f : exp2f(m1 - n1);
-          m0 = n0;
-          m1 = n1;
-          l0 *= f0;
-          l1 *= f1;
+        top0 = fmaxf(top0, fmaxf(x[n][0], x[n][1]));
+        top1 = fmaxf(top1, fmaxf(x[n][2], x[n][3]));
+      }
+      top0 = fmaxf(top0, __shfl_xor_sync(0xffffffffu, top0, 1));
+      top1 = fmaxf(top1, __shfl_xor_sync(0xffffffffu, top1, 1));
+      top0 = fmaxf(top0, __shfl_xor_sync(0xffffffffu, top0, 2));
+      top1 = fmaxf(top1, __shfl_xor_sync(0xffffffffu, top1, 2));
+      if (__any_sync(0xffffffffu, top0 > m0 || top1 > m1)) {
+        const float n0 = fmaxf(m0, top0), n1 = fmaxf(m1, top1);
+        const float f0 = n0 == -INFINITY ? 1.f : exp2_fast(m0 - n0);
+        const float f1 = n1 == -INFINITY ? 1.f : exp2_fast(m1 - n1);
+        m0 = n0;
+        m1 = n1;
+        l0 *= f0;
+        l1 *= f1;
 #pragma unroll
-          for (int n = 0; n < kCols; ++n) {
-            acc[n][0] *= f0;
-            acc[n][1] *= f0;
-            acc[n][2] *= f1;
-            acc[n][3] *= f1;
-          }
+        for (int n = 0; n < kCols; ++n) {
+          acc[n][0] *= f0;
+          acc[n][1] *= f0;
+          acc[n][2] *= f1;
+          acc[n][3] *= f1;
         }
-        const float z0 = m0 == -INFINITY ? 0.f : m0, z1 = m1 == -INFINITY ? 0.f : m1;
+      }
+      const float z0 = m0 == -INFINITY ? 0.f : m0, z1 = m1 == -INFINITY ? 0.f : m1;
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          x[n][0] = exp2f(x[n][0] - z0);
-          x[n][1] = exp2f(x[n][1] - z0);
-          x[n][2] = exp2f(x[n][2] - z1);
-          x[n][3] = exp2f(x[n][3] - z1);
-          l0 += x[n][0] + x[n][1];
-          l1 += x[n][2] + x[n][3];
-        }
-        const uint32_t pa[4] = {Pair<T>::pack(x[0][0], x[0][1]), Pair<T>::pack(x[0][2], x[0][3]),
-                                Pair<T>::pack(x[1][0], x[1][1]), Pair<T>::pack(x[1][2], x[1][3])};
-        {
-          // matrices: keys 0-7 / 8-15 by channels 0-7 / 8-15 of the pair of column tiles
-          const int key = lane & 15;
-          const uint32_t rowp = vb + key * S::kRow;
+      for (int n = 0; n < kKeyTiles; ++n) {
+        x[n][0] = exp2_fast(x[n][0] - z0);
+        x[n][1] = exp2_fast(x[n][1] - z0);
+        x[n][2] = exp2_fast(x[n][2] - z1);
+        x[n][3] = exp2_fast(x[n][3] - z1);
+        l0 += x[n][0] + x[n][1];
+        l1 += x[n][2] + x[n][3];
+      }
 #pragma unroll
-          for (int n = 0; n < kCols; n += 2) {
-            uint32_t b[4];
-            ldsm4_t(b, rowp + (((n + (lane >> 4)) ^ (key & 7)) << 4));
-            mma16816<T>(acc[n], pa, b[0], b[1]);
-            mma16816<T>(acc[n + 1], pa, b[2], b[3]);
-          }
+      for (int k = 0; k < kKeyTiles; k += 2) {
+        const uint32_t pa[4] = {
+            Pair<T>::pack(x[k][0], x[k][1]), Pair<T>::pack(x[k][2], x[k][3]),
+            Pair<T>::pack(x[k + 1][0], x[k + 1][1]), Pair<T>::pack(x[k + 1][2], x[k + 1][3])};
+        // matrices: keys 0-7 / 8-15 by channels 0-7 / 8-15 of the pair of column tiles
+        const int key = k * 8 + (lane & 15);
+        const uint32_t rowp = vb + key * S::kRow;
+#pragma unroll
+        for (int n = 0; n < kCols; n += 2) {
+          uint32_t b[4];
+          ldsm4_t(b, rowp + (((n + (lane >> 4)) ^ (key & 7)) << 4));
+          mma16816<T>(acc[n], pa, b[0], b[1]);
+          mma16816<T>(acc[n + 1], pa, b[2], b[3]);
         }
       }
     }
-    cp_async_wait<0>();
 
     // ---- join the warps: every state is brought to the common maximum
     l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
@@ -498,74 +592,72 @@ __global__ void __launch_bounds__(kDecThreads, 2) k_paged_decode(const DecodeArg
       ml[0][warp][r_lo] = m0;
       ml[0][warp][r_lo + 8] = m1;
     }
-    __syncthreads();  // also: every warp's ring is drained
+    __syncthreads();
     float M0 = -INFINITY, M1 = -INFINITY;
 #pragma unroll
     for (int w = 0; w < kDecWarps; ++w) {
       M0 = fmaxf(M0, ml[0][w][r_lo]);
       M1 = fmaxf(M1, ml[0][w][r_lo + 8]);
     }
-    const float f0 = m0 == -INFINITY ? 0.f : exp2f(m0 - M0);
-    const float f1 = m1 == -INFINITY ? 0.f : exp2f(m1 - M1);
+    const float f0 = m0 == -INFINITY ? 0.f : exp2_fast(m0 - M0);
+    const float f1 = m1 == -INFINITY ? 0.f : exp2_fast(m1 - M1);
     if ((lane & 3) == 0) {
       ml[1][warp][r_lo] = l0 * f0;
       ml[1][warp][r_lo + 8] = l1 * f1;
     }
-    float* mine = merge + warp * (kGroup * kDim);
+    const bool whole = g.i0 == 0 && g.i1 == g.tiles;
+    const int64_t slot = 2 * int64_t(blockIdx.x) + (g.i0 > 0 ? 0 : 1);
+    const int64_t unit = int64_t(g.row) * a.kv_heads + g.head;
+    const int h = tid / 8;  // the thread's row of the result, 4 channels of each 32
+    float M = -INFINITY, l = 0.f, inv = 0.f;
 #pragma unroll
-    for (int n = 0; n < kCols; ++n) {
-      *reinterpret_cast<float2*>(mine + r_lo * kDim + n * 8 + col) =
-          make_float2(acc[n][0] * f0, acc[n][1] * f0);
-      *reinterpret_cast<float2*>(mine + (r_lo + 8) * kDim + n * 8 + col) =
-          make_float2(acc[n][2] * f1, acc[n][3] * f1);
-    }
-    __syncthreads();
-    const bool whole = i0 == 0 && i1 == p.tiles;
-    const int64_t slot = 2 * int64_t(blockIdx.x) + (p.unit_start < p.lo ? 0 : 1);
-    const int64_t unit = int64_t(p.row) * a.kv_heads + p.head;
-    for (int e = tid * 4; e < kGroup * kDim; e += kDecThreads * 4) {
-      const int h = e / kDim;
-      float4 v = *reinterpret_cast<const float4*>(merge + e);
-      float l = ml[1][0][h];
+    for (int c = 0; c < kDim / 32; ++c) {
+      float* mine = merge + warp * (kGroup * S::kMergeRow);
 #pragma unroll
-      for (int w = 1; w < kDecWarps; ++w) {
-        const float4 u = *reinterpret_cast<const float4*>(merge + w * (kGroup * kDim) + e);
+      for (int n = 0; n < 4; ++n) {
+        const float* x = acc[c * 4 + n];
+        *reinterpret_cast<float2*>(mine + r_lo * S::kMergeRow + n * 8 + col) =
+            make_float2(x[0] * f0, x[1] * f0);
+        *reinterpret_cast<float2*>(mine + (r_lo + 8) * S::kMergeRow + n * 8 + col) =
+            make_float2(x[2] * f1, x[3] * f1);
+      }
+      __syncthreads();
+      if (c == 0) {
+#pragma unroll
+        for (int w = 0; w < kDecWarps; ++w) {
+          M = fmaxf(M, ml[0][w][h]);
+          l += ml[1][w][h];
+        }
+        inv = l == 0.f ? 0.f : 1.f / l;  // l == 0: no key was seen
+      }
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kDecWarps; ++w) {
+        const float4 u = *reinterpret_cast<const float4*>(
+            merge + (w * kGroup + h) * S::kMergeRow + (tid % 8) * 4);
         v.x += u.x;
         v.y += u.y;
         v.z += u.z;
         v.w += u.w;
-        l += ml[1][w][h];
       }
-      float M = ml[0][0][h];
-#pragma unroll
-      for (int w = 1; w < kDecWarps; ++w) M = fmaxf(M, ml[0][w][h]);
-      if (!whole) {
-        *reinterpret_cast<float4*>(a.part_o + slot * (kGroup * kDim) + e) = v;
-        if (e % kDim == 0) {
-          a.part_ml[slot * (2 * kGroup) + h] = M;
-          a.part_ml[slot * (2 * kGroup) + kGroup + h] = l;
-        }
-      } else if (h < a.group) {
-        const float inv = l == 0.f ? 0.f : 1.f / l;  // l == 0: no key was seen
-        T* o = static_cast<T*>(a.o) + (unit * a.group) * kDim + e;
-        *reinterpret_cast<uint2*>(o) =
+      const int ch = c * 32 + (tid % 8) * 4;
+      if (!whole)
+        *reinterpret_cast<float4*>(a.part_o + (slot * kGroup + h) * kDim + ch) = v;
+      else if (h < a.group)
+        *reinterpret_cast<uint2*>(static_cast<T*>(a.o) + (unit * a.group + h) * kDim + ch) =
             make_uint2(Pair<T>::pack(v.x * inv, v.y * inv), Pair<T>::pack(v.z * inv, v.w * inv));
-        if (e % kDim == 0)
-          a.lse[unit * a.group + h] = l == 0.f ? -INFINITY : kLn2 * (M + log2f(l));
-      }
+      __syncthreads();  // the buffers are read
     }
-    at = seg_end;
-    if (at >= p.hi) break;
-    __syncthreads();  // merge and ml are read; the next segment's copies may land
-    p.unit_start = at;
-    if (++p.head == a.kv_heads) {
-      p.head = 0;
-      ++p.row;
-      const int32_t n = a.kv_len[p.row];
-      p.len = n < 0 || n > (int64_t(a.table.width) << a.table.shift) ? 0 : n;
-      p.tiles = unit_tiles(p.len, a.q2k != nullptr);
+    if (tid % 8 == 0) {
+      if (!whole) {
+        a.part_ml[slot * (2 * kGroup) + h] = M;
+        a.part_ml[slot * (2 * kGroup) + kGroup + h] = l;
+      } else if (h < a.group) {
+        a.lse[unit * a.group + h] = l == 0.f ? -INFINITY : kLn2 * (M + log2f(l));
+      }
     }
   }
+  cp_async_wait<0>();
 }
 
 // Joins the parts of the units that several CTAs share.  CTA (c, y): the unit
@@ -601,7 +693,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const DecodeArgs a)
   for (int i = way; i < n; i += kJoinWays) {
     const int64_t s = slot(i);
     const float m = a.part_ml[s * (2 * kGroup) + h];
-    const float f = m == -INFINITY ? 0.f : exp2f(m - M);
+    const float f = m == -INFINITY ? 0.f : exp2_fast(m - M);
     l += f * a.part_ml[s * (2 * kGroup) + kGroup + h];
     const float* o = a.part_o + (s * kGroup + h) * kDim + lane * kPer;
 #pragma unroll
