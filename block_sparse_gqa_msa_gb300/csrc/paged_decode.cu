@@ -20,20 +20,35 @@
 // the 16 heads, where a 128-row tensor-memory tile would be seven eighths
 // empty.
 //
-// Split.  A unit is a (row, key head); its keys are cut into tiles of 64.  All
-// units' tiles, in order, are dealt out in equal runs to the CTAs (two an
-// SM), so a batch of any lengths is balanced and a single long row occupies
-// the whole chip; the run's place is found from the lengths on the device, so
-// nothing comes back to the host.  A run is cut into segments at unit
-// borders.  A unit that lies within one run is finished there; otherwise
-// each of its CTAs leaves its (m, l, O) in the workspace and k_paged_join adds
-// them up, in order, so results do not depend on timing.
+// Split.  A unit is a (row, key head); its keys are cut into tiles of 8 KB a
+// warp.  All units' tiles, in order, are dealt out in runs to the CTAs, so a
+// batch of any lengths is balanced and a single long row occupies the whole
+// chip; a run's place is found from the lengths on the device, so nothing
+// comes back to the host.  SMs do not get equal shares of the memory's
+// bandwidth (with equal runs they ended 7 % apart), so part of the tiles is
+// kept back in short runs, each a CTA of the same grid: a CTA that ends its
+// run takes the next short one over from the hardware's queue of CTAs not
+// started yet (cluster launch control), in the midst of its copies.  A run is
+// cut into segments at unit borders.  A unit that lies within one run is
+// finished there; otherwise each run leaves its (m, l, O) in the workspace
+// and k_paged_join adds them up, in order: which CTA works on a run changes
+// from call to call, the runs and the sums do not.
 //
 // A warp works alone on its share of each tile (16 keys of 128 channels, 32 of
 // 64: 8 KB of keys and values): it fetches them with asynchronous copies into
-// its own ring of stages, two stages ahead and across segment borders, and
-// waits for other warps only where a segment ends.
+// its own ring of three stages, across unit and run borders, and waits for
+// other warps only where a segment ends.  Two stages are in flight while it
+// waits, 128 KB an SM; with the third one filled before the wait as well
+// (192 KB) the same calls took 3 % longer, the requests being in each other's
+// way.
+//
+// Measured (bf16, 64 heads on 4, pages of 128 tokens): 9 rows of 65536 to
+// 131072 tokens, all keys, 1.85 GB: 271 to 279 us, 6.6 to 6.8 TB/s, as fast as
+// a plain copy; 285 without the short runs.  128 rows of 500 to 16384 tokens,
+// selected blocks, 508 MB: 91 us, 5.6 TB/s (units of 32 tiles: the chip's
+// start, 6 us, and the ends of runs and units weigh more).
 #include "paged.cuh"
+#include "sm100.cuh"
 
 namespace msa {
 namespace {
@@ -60,11 +75,13 @@ struct DecodeShape {
   static constexpr int kSmem = kDecWarps * kRing + kMergeBytes;  // 106 KB a CTA
 };
 
-// What a CTA leaves for the join about the unit that its run starts inside.
-struct JoinRec {
-  int32_t unit;   // row * kv_heads + key head
-  int32_t parts;  // CTAs after the unit's first one that hold a part of it; 0: no join here
-};
+// Runs of a call: one for each CTA that is on the chip at once (two an SM),
+// and as many short ones (a multiple of 4).  The workspace is sized without a
+// device: no GB300 has more than 160 SMs.
+constexpr int kTailShare = 12;  // one in so many tiles is kept back for the short runs
+constexpr int kTailFrom = 64;   // in calls of so many tiles a CTA and more
+constexpr int kMaxSlots = 160 * 2;
+constexpr int kMaxGrid = kMaxSlots * 2;
 
 struct DecodeArgs {
   const void* q;
@@ -76,16 +93,12 @@ struct DecodeArgs {
   float* lse;
   float scale_log2;    // scale * log2(e)
   int32_t kv_heads, group;
-  JoinRec* rec;        // [grid]
+  int32_t slots;       // first runs
+  int32_t* rec;        // [grid]: 1 + the unit that the run starts inside of; 0: it starts a unit
   float* part_ml;      // [2 grid][2][16]: m, l
   float* part_o;       // [2 grid][16][dim]
 };
 
-__device__ __forceinline__ float exp2_fast(float x) {  // to 2^-22, results below 2^-126 are 0
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src)
                : "memory");
@@ -151,100 +164,213 @@ __device__ __forceinline__ int32_t unit_tiles(int32_t len, bool sparse) {
   return max(n, 1);
 }
 
-// Start of CTA c's run of the n tiles, dealt to `ctas` <= n CTAs (so no run is
-// empty); the last CTA whose run starts before tile e is (e * ctas - 1) / n.
-__device__ __forceinline__ int64_t run_start(int64_t n, int64_t c, int64_t ctas) {
-  return n * c / ctas;
-}
-
-// A place in the list of all tiles.
-struct Place {
-  int64_t total;       // tiles of the call
-  int64_t ctas;        // CTAs they are dealt to
-  int64_t lo, hi;      // the CTA's run
-  int64_t unit_start;  // first tile of the unit that lo lies in
-  int32_t row, head, tiles, len;
+// How n tiles are dealt out to runs: by the numbers alone.  The first runs are
+// equal.  The short ones shrink in four steps, 7 : 5 : 3 : 1: the CTAs that end
+// first take the longest.  No run is empty.
+struct Deal {
+  int32_t first;    // tiles of the first runs
+  int32_t q0, r0;   // a first run's tiles, and how many runs have one more
+  int32_t step, e, r1;  // a short run's: 7, 5, 3 or 1 times step, + e, one more for r1 of them
+  int32_t c0, runs; // first runs, all runs
+  __device__ __forceinline__ Deal(int32_t n, int32_t slots, int32_t grid) {
+    const bool tail = grid > slots && n >= slots * kTailFrom;
+    first = tail ? n - n / kTailShare : n;
+    c0 = min(n, slots);
+    runs = tail ? grid : c0;
+    q0 = first / c0;
+    r0 = first - q0 * c0;
+    step = e = r1 = 0;
+    if (tail) {
+      const int32_t R = runs - c0, rest = n - first;
+      step = rest / (4 * R);
+      e = (rest - 4 * R * step) / R;
+      r1 = rest - 4 * R * step - e * R;
+    }
+  }
+  // First tile of run c (c == runs: the end of the last).
+  __device__ __forceinline__ int32_t start(int32_t c) const {
+    if (c <= c0) return q0 * c + min(c, r0);
+    const int32_t k = c - c0, R4 = (runs - c0) / 4, s = min(k / R4, 3);
+    // runs before the step, weighted: 0, 7, 12, 15 times R4
+    return first + step * (s * (8 - s) * R4 + (7 - 2 * s) * (k - s * R4)) + e * k + min(k, r1);
+  }
 };
+static_assert(kTailFrom >= kTailShare, "a tile for every short run");
 
-// Finds the CTA's run.  Every thread sums the tiles of a stretch of rows; a
-// scan over the threads' sums gives the total and, for the one stretch that
-// holds lo, its place.
+// What a CTA keeps in shared memory to find the place of a tile: the tiles
+// before each of kDecThreads stretches of rows.
+struct Prefix {
+  int32_t at[kDecThreads];
+  int32_t sums[kDecWarps];
+  int32_t total;
+  int32_t each;  // rows of a stretch
+};
+__device__ __forceinline__ int32_t checked_len(const DecodeArgs& a, int32_t n) {
+  return n < 0 || n > (int64_t(a.table.width) << a.table.shift) ? 0 : n;
+}
+// Every thread sums the tiles of a stretch of rows; a scan over the threads.
 template <int kDim>
-__device__ __forceinline__ Place find_place(const DecodeArgs& a, int64_t* sums, Place* found) {
+__device__ __forceinline__ void make_prefix(const DecodeArgs& a, Prefix& s) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const bool sparse = a.q2k != nullptr;
   const int32_t rows = a.table.rows;
   const int32_t each = (rows + kDecThreads - 1) / kDecThreads;
   const int32_t r0 = min(rows, tid * each), r1 = min(rows, r0 + each);
-  const int64_t most = int64_t(a.table.width) << a.table.shift;
-  int64_t mine = 0;
-  int32_t first_len = 0;
+  int32_t mine = 0;
   for (int32_t r = r0; r < r1; ++r) {
-    int32_t n = a.kv_len[r];
-    if (n < 0 || n > most) {
-      if (blockIdx.x == 0) raise_paged(a.table.status, MSA_ERR_BAD_PAGE);
-      n = 0;
-    }
-    if (r == r0) first_len = n;
-    mine += int64_t(unit_tiles<kDim>(n, sparse)) * a.kv_heads;
+    const int32_t n = a.kv_len[r];
+    if (checked_len(a, n) != n && blockIdx.x == 0) raise_paged(a.table.status, MSA_ERR_BAD_PAGE);
+    mine += unit_tiles<kDim>(checked_len(a, n), a.q2k != nullptr) * a.kv_heads;
   }
-  int64_t incl = mine;
+  int32_t incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+    const int32_t y = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += y;
   }
-  if (lane == 31) sums[warp] = incl;
+  if (lane == 31) s.sums[warp] = incl;
   __syncthreads();
-  int64_t total = 0, before = 0;
+  int32_t total = 0, before = 0;
 #pragma unroll
   for (int w = 0; w < kDecWarps; ++w) {
-    if (w < warp) before += sums[w];
-    total += sums[w];
+    if (w < warp) before += s.sums[w];
+    total += s.sums[w];
   }
-  int64_t at = before + incl - mine;  // tiles before the thread's rows
-  const int64_t ctas = total < gridDim.x ? total : gridDim.x;
-  const int64_t lo = run_start(total, blockIdx.x, ctas);  // total and more past the last CTA
-  if (tid == 0) found->ctas = ctas;
-  if (lo >= at && lo < at + mine) {
-    int32_t len = first_len;
-    for (int32_t r = r0; r < r1; ++r) {
-      if (r > r0) {
-        len = a.kv_len[r];
-        if (len < 0 || len > most) len = 0;
-      }
-      const int32_t tiles = unit_tiles<kDim>(len, sparse);
-      const int64_t here = int64_t(tiles) * a.kv_heads;
-      if (lo < at + here) {
-        Place p;
-        p.total = total;
-        p.ctas = ctas;
-        p.lo = lo;
-        p.hi = run_start(total, blockIdx.x + 1, ctas);
-        p.head = int32_t((lo - at) / tiles);
-        p.unit_start = at + int64_t(p.head) * tiles;
-        p.row = r;
-        p.tiles = tiles;
-        p.len = len;
-        *found = p;
-        break;
-      }
-      at += here;
-    }
+  s.at[tid] = before + incl - mine;
+  if (tid == 0) {
+    s.total = total;
+    s.each = each;
   }
   __syncthreads();
-  return *found;
+}
+
+// A tile's row, its length and the first tile of the row.  A whole warp.
+struct RowPlace {
+  int32_t row, len, tiles, start;
+};
+template <int kDim>
+__device__ __forceinline__ RowPlace locate(const DecodeArgs& a, const Prefix& s, int32_t t) {
+  const int lane = threadIdx.x & 31;
+  const bool sparse = a.q2k != nullptr;
+  int k = -1;  // the last stretch that starts at or before t
+#pragma unroll
+  for (int w = 0; w < kDecWarps; ++w)
+    k += __popc(__ballot_sync(0xffffffffu, s.at[w * 32 + lane] <= t));
+  RowPlace p;
+  p.start = s.at[k];
+  if (s.each == 1) {
+    p.row = k;
+    p.len = checked_len(a, a.kv_len[k]);
+    p.tiles = unit_tiles<kDim>(p.len, sparse);
+    return p;
+  }
+  const int32_t end = min(a.table.rows, (k + 1) * s.each);
+#pragma unroll 1
+  for (int32_t r0 = k * s.each;; r0 += 32) {
+    const int32_t r = r0 + lane;
+    const int32_t len = r < end ? checked_len(a, a.kv_len[r]) : 0;
+    const int32_t tiles = unit_tiles<kDim>(len, sparse);
+    const int32_t mine = r < end ? tiles * a.kv_heads : 0;
+    int32_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int32_t y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    const uint32_t past = __ballot_sync(0xffffffffu, p.start + incl > t);
+    if (past || r0 + 32 >= end) {
+      const int src = past ? __ffs(past) - 1 : 31;
+      p.row = min(r0 + src, end - 1);
+      p.len = __shfl_sync(0xffffffffu, len, src);
+      p.tiles = __shfl_sync(0xffffffffu, tiles, src);
+      p.start += __shfl_sync(0xffffffffu, incl - mine, src);
+      return p;
+    }
+    p.start += __shfl_sync(0xffffffffu, incl, 31);
+  }
+}
+
+// The hardware's queue of CTAs that have not started: a request takes the next
+// one off it, whose index arrives in shared memory.
+constexpr int kAnswers = 8;
+struct Queue {
+  uint4 answer[kAnswers];
+  uint64_t bar[kAnswers];
+};
+__device__ __forceinline__ void take_cta(uint32_t answer, uint32_t bar) {
+  mbar_arrive_expect_tx(bar, 16);
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 "
+      "[%0], [%1];" ::"r"(answer),
+      "r"(bar)
+      : "memory");
+}
+// The CTA taken, or -1: there was none left.
+__device__ __forceinline__ int32_t taken_cta(uint32_t answer) {
+  uint32_t ok, x;
+  asm volatile(
+      "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t"
+      "ld.shared.b128 h, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "mov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
+      : "=r"(ok), "=r"(x)
+      : "r"(answer)
+      : "memory");
+  return ok ? int32_t(x) : -1;
 }
 
 // A part of a unit that one CTA works on: its tiles i0 .. i1 - 1.
 struct Segment {
-  int32_t row, head, i0, i1, tiles;
+  int32_t run, row, head, i0, i1, tiles;
+  int32_t opens;  // the run's first
 };
-constexpr int kSegQueue = 8;  // the fetch is at most kStages tiles, so segments, ahead
+struct NextRun {
+  int32_t run, row, head, len, tiles, i, n;
+};
 
-// The fetching side of a warp: walks the run's tiles ahead of the sums and
+// The place of run c.
+template <int kDim>
+__device__ __forceinline__ void find_run(const DecodeArgs& a, const Prefix& prefix,
+                                         const Deal& deal, int32_t c, NextRun* next) {
+  const int32_t lo = deal.start(c), n = deal.start(c + 1) - lo;
+  const RowPlace p = locate<kDim>(a, prefix, lo);
+  const int32_t h = (lo - p.start) / p.tiles;
+  if ((threadIdx.x & 31) == 0)
+    *next = NextRun{c, p.row, h, p.len, p.tiles, lo - p.start - h * p.tiles, n};
+  __syncwarp();
+}
+// The same for a run taken later.  Out of line: the loop over the tiles stays short.
+template <int kDim>
+__device__ __forceinline__ void find_taken_run(const DecodeArgs& a, const Prefix& prefix, int32_t c,
+                                            NextRun* next) {
+  find_run<kDim>(a, prefix, Deal(prefix.total, a.slots, gridDim.x), c, next);
+}
+// The answer to the CTA's request number n (1, 2, ..): the run taken, or -1.
+__device__ __forceinline__ int32_t await_run(const DecodeArgs& a, Queue* ctas, uint32_t n) {
+  const int b = n % kAnswers;
+  int32_t c = -1;
+  if (mbar_wait_drain(smem_u32(&ctas->bar[b]), ((n - 1) / kAnswers) & 1))
+    c = taken_cta(smem_u32(&ctas->answer[b]));
+  else
+    raise_paged(a.table.status, MSA_ERR_TIMEOUT);
+  fence_proxy_async_smem();  // the place is written again by a later request
+  return __shfl_sync(0xffffffffu, c, 0);
+}
+constexpr int kSegQueue = 8;  // the fetch is at most 4 tiles, so segments, ahead
+// Tiles before a run's end at which the next one is asked for, and at which its
+// place is looked up: each wait on the way is hidden by the tiles in flight.
+constexpr int kAskAt = 6;
+constexpr int kFindAt = 3;
+
+// The fetching side of a warp: walks the runs' tiles ahead of the sums and
 // leaves each segment that it enters in a queue.  All its state is the same
-// in all lanes except page and slots.
+// in all lanes except page and slots.  The warps of a CTA walk the same runs:
+// warp 0 asks for the next one, all read the answer.  Answer n sits in place n
+// mod 8.  A fetch is three tiles ahead of its warp's sums, and warps meet where
+// a segment ends: where warp 0's fetch is in its run n + 8, eight tiles or
+// more past run n, its sums are past run n and have met the others' there,
+// whose fetches, ahead of their sums, have all read answer n.
 template <typename T, int kDim>
 struct Fetch {
   using S = DecodeShape<kDim>;
@@ -255,23 +381,28 @@ struct Fetch {
   const DecodeArgs& a;
   int32_t* blocks;   // the unit's blocks (sparse), shared memory
   Segment* queue;
+  const Prefix& prefix;
+  Queue* ctas;
+  NextRun* next;     // shared memory of the warp
   int lane, warp;
-  int64_t left;      // tiles of the run after the current segment
+  int32_t run;       // the run at hand
+  uint32_t n_run;    // runs found
+  bool more;         // there may be further runs
+  bool asked;        // for the next one
+  bool found;        // the next one
+  int32_t left;      // tiles of the run after the current segment
   int32_t row, head, len, tiles, i, i1, n_blocks, n_seg;
   int32_t next_len, slots;  // of the next unit, loaded ahead
   int32_t j;         // first key of the warp's part of the tile at hand, -1: none
   int32_t page;      // its page as the table has it, unchecked
 
-  __device__ __forceinline__ int32_t checked(int32_t n) const {
-    return n < 0 || n > (int64_t(a.table.width) << a.table.shift) ? 0 : n;
-  }
   __device__ __forceinline__ void load_slots(int32_t r, int32_t h) {
     if (a.q2k && lane < kTopK && r < a.table.rows)
       slots = a.q2k[(int64_t(h) * a.table.rows + r) * kTopK + lane];
   }
   // Enters the unit (row, head) at tile i: its blocks (the distinct valid
   // slots, in slot order), its place in the queue, and a look ahead.
-  __device__ __forceinline__ void enter() {
+  __device__ __forceinline__ void enter(int32_t opens) {
     if (a.q2k) {
       const int32_t nb = int32_t((int64_t(len) + kBlock - 1) / kBlock);
       const int32_t v = slots;
@@ -284,7 +415,7 @@ struct Fetch {
       __syncwarp();  // the list before is read
       if (keep) blocks[__popc(m & ((1u << lane) - 1))] = v;
     }
-    if (lane == 0) queue[n_seg % kSegQueue] = Segment{row, head, i, i1, tiles};
+    if (lane == 0) queue[n_seg % kSegQueue] = Segment{run, row, head, i, i1, tiles, opens};
     ++n_seg;
     __syncwarp();
     if (left > 0) {  // the next unit: its length, slots and queries
@@ -298,42 +429,68 @@ struct Fetch {
             lane * 64));
     }
   }
-  __device__ __forceinline__ void begin(const Place& p) {
-    row = p.row;
-    head = p.head;
-    len = p.len;
-    tiles = p.tiles;
-    i = int32_t(p.lo - p.unit_start);
-    const int64_t n = p.hi - p.lo;
-    i1 = int32_t(min(int64_t(tiles), i + n));
-    left = n - (i1 - i);
-    n_blocks = 0;
+  // Before the first tile: the run to begin is the CTA's own.
+  __device__ __forceinline__ void init(const Deal& deal) {
+    find_run<kDim>(a, prefix, deal, blockIdx.x, next);
+    n_run = 1;
     n_seg = 0;
-    slots = -1;
-    load_slots(row, head);
-    enter();
-    look();
+    more = deal.runs > deal.c0;
+    found = true;
+    left = 0;
+    i = 0;
+    i1 = 1;
+    j = -1;
   }
+  // On to the next tile: of the segment, of the run's next unit, of the next run.
   __device__ __forceinline__ void advance() {
-    if (i1 == 0) return;  // the run is done
+    if (i1 == 0) return;  // nothing is left
     if (++i == i1) {
-      if (left == 0) {
-        i1 = 0;
-        j = -1;
-        return;
+      const bool opens = left == 0;
+      if (opens) {
+        if (!found) {
+          i1 = 0;
+          j = -1;
+          return;
+        }
+        run = next->run;
+        row = next->row;
+        head = next->head;
+        len = next->len;
+        tiles = next->tiles;
+        i = next->i;
+        left = next->n;
+        load_slots(row, head);
+        n_blocks = 0;
+        asked = found = false;
+      } else {
+        if (++head == a.kv_heads) {
+          head = 0;
+          ++row;
+          len = checked_len(a, next_len);
+          tiles = unit_tiles<kDim>(len, a.q2k != nullptr);
+        }
+        i = 0;
       }
-      if (++head == a.kv_heads) {
-        head = 0;
-        ++row;
-        len = checked(next_len);
-        tiles = unit_tiles<kDim>(len, a.q2k != nullptr);
-      }
-      i = 0;
-      i1 = int32_t(min(int64_t(tiles), left));
-      left -= i1;
-      enter();
+      i1 = min(tiles, i + left);
+      left -= i1 - i;
+      enter(opens);
     }
     look();
+    if (!more) return;
+    const int32_t rest = left + (i1 - i);
+    if (!asked && rest <= kAskAt) {
+      asked = true;
+      const int b = n_run % kAnswers;
+      if (warp == 0 && lane == 0) take_cta(smem_u32(&ctas->answer[b]), smem_u32(&ctas->bar[b]));
+    }
+    if (!found && rest <= kFindAt) {
+      const int32_t c = await_run(a, ctas, n_run);
+      more = found = c >= 0;
+      if (found) {
+        ++n_run;
+        find_taken_run<kDim>(a, prefix, c, next);
+      }
+    }
   }
   // The warp's first key in tile i and its page (loaded, not looked at yet).
   // Where a page holds all the warp's keys every lane loads that page, else
@@ -387,7 +544,7 @@ struct Fetch {
         }
         return 0xffffffffu >> (32 - S::kWarpKeys);
       }
-#pragma unroll 4
+#pragma unroll 1
       for (int x = 0; x < kCopies; ++x) {
         const int key = x * kRowsAtOnce + sub;
         const uint32_t dst = stage + key * S::kRow + ((c ^ (key & 7)) << 4);
@@ -401,7 +558,7 @@ struct Fetch {
     const bool good = due && page >= 0 && page < a.table.num_pages;
     if (due && !good) raise_paged(a.table.status, MSA_ERR_BAD_PAGE);
     const uint32_t there = __ballot_sync(0xffffffffu, good);
-#pragma unroll 4
+#pragma unroll 1
     for (int x = 0; x < kCopies; ++x) {
       const int key = x * kRowsAtOnce + sub;
       const int32_t p = __shfl_sync(0xffffffffu, good ? page : -1, key);
@@ -422,8 +579,9 @@ __global__ void __launch_bounds__(kDecThreads, 2) k_paged_decode(const DecodeArg
   constexpr int kCols = kDim / 8;              // column tiles of the second
   constexpr int kKeyTiles = S::kWarpKeys / 8;  // column tiles of the first
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int64_t sums[kDecWarps];
-  __shared__ Place found;
+  __shared__ Prefix prefix;
+  __shared__ Queue ctas;
+  __shared__ NextRun next[kDecWarps];
   __shared__ int32_t blocks[kDecWarps][kTopK];
   __shared__ Segment queue[kDecWarps][kSegQueue];
   __shared__ float ml[2][kDecWarps][kGroup];
@@ -432,81 +590,71 @@ __global__ void __launch_bounds__(kDecThreads, 2) k_paged_decode(const DecodeArg
   const int col = (lane & 3) * 2;
   grid_dep_wait();
   grid_dep_release();
-  const Place p = find_place<kDim>(a, sums, &found);
-  if (blockIdx.x >= p.ctas) {
-    if (tid == 0) a.rec[blockIdx.x] = JoinRec{0, 0};
+  if (tid == 0) {
+    for (int i = 0; i < kAnswers; ++i) mbar_init(smem_u32(&ctas.bar[i]), 1);
+    fence_mbar_init();
+  }
+  make_prefix<kDim>(a, prefix);
+  const Deal deal(prefix.total, a.slots, gridDim.x);
+  if (blockIdx.x >= deal.runs) {
+    if (tid == 0) a.rec[blockIdx.x] = 0;
     return;
   }
-  if (tid == 0) {
-    // The unit that the run starts inside, for the join: the first CTA that
-    // starts inside it records how many parts follow.
-    JoinRec rec{0, 0};
-    const int64_t c = blockIdx.x;
-    if (p.unit_start < p.lo && run_start(p.total, c - 1, p.ctas) <= p.unit_start) {
-      const int64_t last = ((p.unit_start + p.tiles) * p.ctas - 1) / p.total;
-      rec.unit = p.row * a.kv_heads + p.head;
-      rec.parts = int32_t(last - c + 1);
-    }
-    a.rec[c] = rec;
-  }
 
-  const uint32_t ring = uint32_t(__cvta_generic_to_shared(smem)) + warp * S::kRing;
+  const uint32_t ring = smem_u32(smem) + warp * S::kRing;
   float* merge = reinterpret_cast<float*>(smem + kDecWarps * S::kRing);
-  Fetch<T, kDim> fetch{a, blocks[warp], queue[warp], lane, warp};
-  fetch.begin(p);
-  uint32_t there[S::kStages - 1];  // of the tiles in flight: the keys that are there
-#pragma unroll
-  for (int s = 0; s < S::kStages - 1; ++s) {
-    there[s] = fetch.copy(ring + s * S::kStageBytes);
-    cp_async_commit();
-    fetch.advance();
-  }
+  Fetch<T, kDim> fetch{a, blocks[warp], queue[warp], prefix, &ctas, &next[warp], lane, warp};
+  fetch.init(deal);
 
-  int64_t left = p.hi - p.lo;
+  uint32_t qa[kSteps][4];           // the query heads as the left operand
+  float acc[kCols][4];              // O
+  float m0, m1, l0, l1;
+  uint32_t there[S::kStages - 1] = {};  // of the tiles in flight: the keys that are there
+  Segment g;
+  int seg = 0;
+  int32_t left = 0;                 // tiles of the segment
   int stage = 0;
-  for (int seg = 0; left > 0; ++seg) {
-    const Segment g = queue[warp][seg % kSegQueue];
-    left -= g.i1 - g.i0;
-
-    // ---- the query heads as the left operand; heads past the group are zeros
-    uint32_t qa[kSteps][4];
+  // A step starts the copies of the tile kStages - 1 further, into the stage that
+  // the last step has freed, then works on its own tile.  The first steps only
+  // fill the ring (the very first has no tile yet: the run is begun in it).
+  int fill = S::kStages;
+#pragma unroll 1
+  while (true) {
+    const uint32_t kb = ring + stage * S::kStageBytes, vb = kb + S::kWarpKeys * S::kRow;
+    const uint32_t seen = there[0];
+    if (fill == 0) cp_async_wait<S::kStages - 2>();
+    __syncwarp();
     {
-      const T* q = static_cast<const T*>(a.q) +
-                   (int64_t(g.row) * a.kv_heads + g.head) * a.group * kDim + col;
+      const int free = stage == 0 ? S::kStages - 1 : stage - 1;
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        const uint32_t* lo = reinterpret_cast<const uint32_t*>(q + r_lo * kDim + s * 16);
-        const uint32_t* hi = reinterpret_cast<const uint32_t*>(q + (r_lo + 8) * kDim + s * 16);
-        qa[s][0] = r_lo < a.group ? lo[0] : 0;
-        qa[s][1] = r_lo + 8 < a.group ? hi[0] : 0;
-        qa[s][2] = r_lo < a.group ? lo[4] : 0;
-        qa[s][3] = r_lo + 8 < a.group ? hi[4] : 0;
+      for (int s = 0; s + 1 < S::kStages - 1; ++s) there[s] = there[s + 1];
+      there[S::kStages - 2] = fetch.copy(ring + free * S::kStageBytes);
+      cp_async_commit();
+      fetch.advance();
+    }
+    if (fill == 0) {
+      if (left == 0) {  // the next segment; heads past the group are zeros
+        g = queue[warp][seg % kSegQueue];
+        left = g.i1 - g.i0;
+        if (g.opens && tid == 0) a.rec[g.run] = g.i0 > 0 ? 1 + g.row * a.kv_heads + g.head : 0;
+        const T* q = static_cast<const T*>(a.q) +
+                     (int64_t(g.row) * a.kv_heads + g.head) * a.group * kDim + col;
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+          const uint32_t* lo = reinterpret_cast<const uint32_t*>(q + r_lo * kDim + s * 16);
+          const uint32_t* hi = reinterpret_cast<const uint32_t*>(q + (r_lo + 8) * kDim + s * 16);
+          qa[s][0] = r_lo < a.group ? lo[0] : 0;
+          qa[s][1] = r_lo + 8 < a.group ? hi[0] : 0;
+          qa[s][2] = r_lo < a.group ? lo[4] : 0;
+          qa[s][3] = r_lo + 8 < a.group ? hi[4] : 0;
+        }
+#pragma unroll
+        for (int n = 0; n < kCols; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
+        m0 = m1 = -INFINITY;
+        l0 = l1 = 0.f;
       }
     }
-    float acc[kCols][4];
-#pragma unroll
-    for (int n = 0; n < kCols; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
-    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
-
-    // ---- the keys
-#pragma unroll 1
-    for (int32_t i = g.i0; i < g.i1; ++i) {
-      cp_async_wait<S::kStages - 2>();
-      __syncwarp();
-      const uint32_t seen = there[0];
-      const uint32_t kb = ring + stage * S::kStageBytes, vb = kb + S::kWarpKeys * S::kRow;
-      // the stage freed by the last tile takes the tile kStages - 1 ahead
-      {
-        const int free = stage == 0 ? S::kStages - 1 : stage - 1;
-        stage = stage + 1 == S::kStages ? 0 : stage + 1;
-#pragma unroll
-        for (int s = 0; s + 1 < S::kStages - 1; ++s) there[s] = there[s + 1];
-        there[S::kStages - 2] = fetch.copy(ring + free * S::kStageBytes);
-        cp_async_commit();
-        fetch.advance();
-      }
-      if (seen == 0) continue;
-
+    if (fill == 0 && seen != 0) {
       float x[kKeyTiles][4];
 #pragma unroll
       for (int n = 0; n < kKeyTiles; ++n) x[n][0] = x[n][1] = x[n][2] = x[n][3] = 0.f;
@@ -541,8 +689,8 @@ __global__ void __launch_bounds__(kDecThreads, 2) k_paged_decode(const DecodeArg
       top1 = fmaxf(top1, __shfl_xor_sync(0xffffffffu, top1, 2));
       if (__any_sync(0xffffffffu, top0 > m0 || top1 > m1)) {
         const float n0 = fmaxf(m0, top0), n1 = fmaxf(m1, top1);
-        const float f0 = n0 == -INFINITY ? 1.f : exp2_fast(m0 - n0);
-        const float f1 = n1 == -INFINITY ? 1.f : exp2_fast(m1 - n1);
+        const float f0 = n0 == -INFINITY ? 1.f : fast_exp2(m0 - n0);
+        const float f1 = n1 == -INFINITY ? 1.f : fast_exp2(m1 - n1);
         m0 = n0;
         m1 = n1;
         l0 *= f0;
@@ -558,10 +706,10 @@ __global__ void __launch_bounds__(kDecThreads, 2) k_paged_decode(const DecodeArg
       const float z0 = m0 == -INFINITY ? 0.f : m0, z1 = m1 == -INFINITY ? 0.f : m1;
 #pragma unroll
       for (int n = 0; n < kKeyTiles; ++n) {
-        x[n][0] = exp2_fast(x[n][0] - z0);
-        x[n][1] = exp2_fast(x[n][1] - z0);
-        x[n][2] = exp2_fast(x[n][2] - z1);
-        x[n][3] = exp2_fast(x[n][3] - z1);
+        x[n][0] = fast_exp2(x[n][0] - z0);
+        x[n][1] = fast_exp2(x[n][1] - z0);
+        x[n][2] = fast_exp2(x[n][2] - z1);
+        x[n][3] = fast_exp2(x[n][3] - z1);
         l0 += x[n][0] + x[n][1];
         l1 += x[n][2] + x[n][3];
       }
@@ -582,8 +730,14 @@ __global__ void __launch_bounds__(kDecThreads, 2) k_paged_decode(const DecodeArg
         }
       }
     }
+    stage = stage + 1 == S::kStages ? 0 : stage + 1;
+    if (fill > 0) {
+      --fill;
+      continue;
+    }
+    if (--left > 0) continue;
 
-    // ---- join the warps: every state is brought to the common maximum
+    // ---- the segment's end: join the warps: every state is brought to the common maximum
     l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
     l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
     l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
@@ -599,14 +753,14 @@ __global__ void __launch_bounds__(kDecThreads, 2) k_paged_decode(const DecodeArg
       M0 = fmaxf(M0, ml[0][w][r_lo]);
       M1 = fmaxf(M1, ml[0][w][r_lo + 8]);
     }
-    const float f0 = m0 == -INFINITY ? 0.f : exp2_fast(m0 - M0);
-    const float f1 = m1 == -INFINITY ? 0.f : exp2_fast(m1 - M1);
+    const float f0 = m0 == -INFINITY ? 0.f : fast_exp2(m0 - M0);
+    const float f1 = m1 == -INFINITY ? 0.f : fast_exp2(m1 - M1);
     if ((lane & 3) == 0) {
       ml[1][warp][r_lo] = l0 * f0;
       ml[1][warp][r_lo + 8] = l1 * f1;
     }
     const bool whole = g.i0 == 0 && g.i1 == g.tiles;
-    const int64_t slot = 2 * int64_t(blockIdx.x) + (g.i0 > 0 ? 0 : 1);
+    const int64_t slot = 2 * int64_t(g.run) + (g.i0 > 0 ? 0 : 1);
     const int64_t unit = int64_t(g.row) * a.kv_heads + g.head;
     const int h = tid / 8;  // the thread's row of the result, 4 channels of each 32
     float M = -INFINITY, l = 0.f, inv = 0.f;
@@ -656,61 +810,141 @@ __global__ void __launch_bounds__(kDecThreads, 2) k_paged_decode(const DecodeArg
         a.lse[unit * a.group + h] = l == 0.f ? -INFINITY : kLn2 * (M + log2f(l));
       }
     }
+    if (++seg == fetch.n_seg) break;  // the fetch is ahead: it would have entered the next one
   }
   cp_async_wait<0>();
 }
 
-// Joins the parts of the units that several CTAs share.  CTA (c, y): the unit
-// that run c starts inside, if c is the first such run; a warp a (head, part of
-// the parts), lanes over the channels.
-constexpr int kJoinThreads = 512;
-constexpr int kJoinWays = 4;    // warps that share a head
-constexpr int kJoinHeads = kJoinThreads / 32 / kJoinWays;
+// Joins the parts of the units that several runs share.  CTA x stands for run
+// x + 1, if that run starts inside a unit; the CTAs of one unit share its
+// heads.  A warp works on a head, alone or with others that take the head's
+// parts in turn, its lanes over the channels: the parts' states are merged as
+// the keys' were, then the warps'.  The chain of dependent loads is short
+// (the records, then the parts): with few rows this kernel is a good part of
+// the call's time.
+constexpr int kJoinWarps = 16;
+constexpr int kJoinWays = kJoinWarps;  // at most, for one head
 template <typename T, int kDim>
-__global__ void __launch_bounds__(kJoinThreads) k_paged_join(const DecodeArgs a) {
+__global__ void __launch_bounds__(kJoinWarps * 32, 3) k_paged_join(const DecodeArgs a) {
   constexpr int kPer = kDim / 32;
-  __shared__ float so[kJoinThreads / 32][kDim];
-  __shared__ float sl[kJoinThreads / 32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int way = warp / kJoinHeads;
-  const int h = blockIdx.y * kJoinHeads + warp % kJoinHeads;
+  constexpr int kLoads = 4;
+  struct __align__(4 * kPer) Chunk {
+    float x[kPer];
+  };
+  __shared__ Chunk so[kJoinWarps][32];
+  __shared__ float sm[kJoinWarps], sl[kJoinWarps];
+  __shared__ int32_t before, after;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) {
+    before = 0;
+    after = INT32_MAX;
+  }
   grid_dep_wait();
   grid_dep_release();
-  const int64_t c = int64_t(blockIdx.x) + 1;
-  const JoinRec rec = a.rec[c];
-  if (rec.parts == 0 || blockIdx.y * kJoinHeads >= a.group) return;
-  const int n = rec.parts + 1;
-  // part 0: the unit's first CTA, whose run goes on past it; then the CTAs
-  // that start inside the unit
-  auto slot = [&](int i) { return i == 0 ? 2 * (c - 1) + 1 : 2 * (c - 1 + i); };
-  float M = -INFINITY;
-  for (int i = lane; i < n; i += 32) M = fmaxf(M, a.part_ml[slot(i) * (2 * kGroup) + h]);
+  // The runs that start inside the same unit: up to the nearest others.
+  const int32_t run = int32_t(blockIdx.x) + 1, runs = int32_t(gridDim.x) + 1;
+  const int32_t mark = a.rec[run];
+  constexpr int kEach = (kMaxGrid + kJoinWarps * 32 - 1) / (kJoinWarps * 32);
+  int32_t marks[kEach];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  float acc[kPer] = {};
-  float l = 0.f;
-#pragma unroll 4
-  for (int i = way; i < n; i += kJoinWays) {
-    const int64_t s = slot(i);
-    const float m = a.part_ml[s * (2 * kGroup) + h];
-    const float f = m == -INFINITY ? 0.f : exp2_fast(m - M);
-    l += f * a.part_ml[s * (2 * kGroup) + kGroup + h];
-    const float* o = a.part_o + (s * kGroup + h) * kDim + lane * kPer;
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) acc[e] += f * o[e];
+  for (int k = 0; k < kEach; ++k) {
+    const int32_t i = tid + k * (kJoinWarps * 32);
+    marks[k] = i < runs ? a.rec[i] : 0;
   }
+  if (mark <= 0 || (mark - 1) / a.kv_heads >= a.table.rows) return;
+  int32_t lo = 0, hi = runs;
 #pragma unroll
-  for (int e = 0; e < kPer; ++e) so[warp][lane * kPer + e] = acc[e];
-  if (lane == 0) sl[warp] = l;
+  for (int k = 0; k < kEach; ++k) {
+    const int32_t i = tid + k * (kJoinWarps * 32);
+    if (i < runs && marks[k] != mark) {
+      if (i < run) lo = max(lo, i); else hi = min(hi, i);
+    }
+  }
   __syncthreads();
-  if (way != 0 || h >= a.group) return;
-#pragma unroll
-  for (int w = 1; w < kJoinWays; ++w) {
-    l += sl[warp + w * kJoinHeads];
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) acc[e] += so[warp + w * kJoinHeads][lane * kPer + e];
+  lo = __reduce_max_sync(0xffffffffu, lo);
+  hi = __reduce_min_sync(0xffffffffu, hi);
+  if (lane == 0) {
+    atomicMax(&before, lo);
+    atomicMin(&after, hi);
   }
-  const int64_t out = int64_t(rec.unit) * a.group + h;
+  __syncthreads();
+  const int32_t first = before;    // the run that the unit starts in
+  const int n = after - first;     // parts; n - 1 CTAs
+  int shares = 1;                  // of the 16 heads
+  while (shares < kGroup && 2 * shares <= n - 1) shares *= 2;
+  const int share = run - first - 1;
+  if (share >= shares) return;
+  const int heads = kGroup / shares;    // of this CTA
+  const int ways = kJoinWarps / heads;  // warps of a head
+  const int way = warp % ways;
+  const int h = share * heads + warp / ways;
+  // part 0: the run that the unit starts in; then the runs that start inside it
+  float M = -INFINITY, l = 0.f, acc[kPer] = {};
+  for (int i0 = way; i0 < n; i0 += kLoads * ways) {
+    Chunk o[kLoads];
+    float m[kLoads], pl[kLoads];
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) {
+      const int i = i0 + u * ways;
+      m[u] = -INFINITY;
+      pl[u] = 0.f;
+      o[u] = Chunk{};
+      if (i < n) {
+        const int32_t s = 2 * (first + i) + (i == 0 ? 1 : 0);
+        m[u] = a.part_ml[s * (2 * kGroup) + h];
+        pl[u] = a.part_ml[s * (2 * kGroup) + kGroup + h];
+        o[u] = reinterpret_cast<const Chunk*>(a.part_o + (s * kGroup + h) * kDim)[lane];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) {
+      const float top = fmaxf(M, m[u]);
+      const float f = M == -INFINITY ? 0.f : fast_exp2(M - top);
+      const float g = m[u] == -INFINITY ? 0.f : fast_exp2(m[u] - top);
+      M = top;
+      l = l * f + pl[u] * g;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) acc[e] = acc[e] * f + o[u].x[e] * g;
+    }
+  }
+  if (ways > 1) {
+    Chunk mine;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) mine.x[e] = acc[e];
+    so[warp][lane] = mine;
+    if (lane == 0) {
+      sm[warp] = M;
+      sl[warp] = l;
+    }
+    __syncthreads();
+    if (way != 0) return;
+    // a lane a way's state, then the ways' sums with their weights
+    const float mw = lane < ways ? sm[warp + lane] : -INFINITY;
+    M = mw;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float f = mw == -INFINITY ? 0.f : fast_exp2(mw - M);
+    l = lane < ways ? sl[warp + lane] * f : 0.f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
+#pragma unroll
+    for (int w0 = 0; w0 < kJoinWays; w0 += 4) {
+      if (w0 >= ways) break;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float g = __shfl_sync(0xffffffffu, f, w0 + u);  // 0 past the ways
+        const Chunk o = so[min(warp + w0 + u, kJoinWarps - 1)][lane];
+        if (w0 + u < ways) {
+#pragma unroll
+          for (int e = 0; e < kPer; ++e) acc[e] += o.x[e] * g;
+        }
+      }
+    }
+  }
+  if (h >= a.group) return;
+  const int64_t out = int64_t(mark - 1) * a.group + h;
   const float inv = l == 0.f ? 0.f : 1.f / l;
   uint32_t* o = reinterpret_cast<uint32_t*>(static_cast<T*>(a.o) + out * kDim + lane * kPer);
 #pragma unroll
@@ -718,32 +952,33 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const DecodeArgs a)
   if (lane == 0) a.lse[out] = l == 0.f ? -INFINITY : kLn2 * (M + log2f(l));
 }
 
-int decode_grid() { return device_sm_count() * 2; }
-// The workspace is sized without a device: no GB300 has more SMs than this.
-constexpr int kMaxGrid = 160 * 2;
-
 size_t decode_workspace(int32_t dim) {
-  return align_up(sizeof(JoinRec) * kMaxGrid, 256) +
+  return align_up(sizeof(int32_t) * kMaxGrid, 256) +
          sizeof(float) * 2 * kMaxGrid * (2 * kGroup + kGroup * size_t(dim));
 }
 
 template <typename T, int kDim>
-cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t s) {
+cudaError_t launch_decode(DecodeArgs a, cudaStream_t s) {
   using S = DecodeShape<kDim>;
   auto kernel = k_paged_decode<T, kDim>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        S::kSmem);
   if (e != cudaSuccess) return e;
-  int grid = decode_grid();
-  if (grid > kMaxGrid) grid = kMaxGrid;
+  a.slots = device_sm_count() * 2;
+  if (a.slots > kMaxSlots) a.slots = kMaxSlots;
+  // Short runs only where the batch, by the room in its table, can have
+  // enough tiles for them.
+  int64_t most = (int64_t(a.table.width) << a.table.shift) / S::kTileKeys + 1;
+  if (a.q2k && most > kTopK * S::kTilesPerBlock) most = kTopK * S::kTilesPerBlock;
+  most *= int64_t(a.table.rows) * a.kv_heads;
+  const int grid = a.slots + (most >= int64_t(a.slots) * kTailFrom ? a.slots / 4 * 4 : 0);
   launch_begin("paged_decode", s);
   e = launch_k(true, kernel, dim3(unsigned(grid)), dim3(kDecThreads), S::kSmem, s, a);
   launch_end("paged_decode", s);
   if (e != cudaSuccess) return e;
   launch_begin("paged_join", s);
-  e = launch_k(true, k_paged_join<T, kDim>,
-               dim3(unsigned(grid - 1), unsigned((a.group + kJoinHeads - 1) / kJoinHeads)),
-               dim3(kJoinThreads), 0, s, a);
+  e = launch_k(true, k_paged_join<T, kDim>, dim3(unsigned(grid - 1)), dim3(kJoinWarps * 32), 0, s,
+               a);
   launch_end("paged_join", s);
   return e;
 }
@@ -780,6 +1015,9 @@ extern "C" msa_status msa_paged_decode(const msa_paged_cache* cache, const msa_p
   if (!paged_aligned(q) || !paged_aligned(o) || !paged_aligned(workspace) ||
       !paged_aligned4(kv_len) || !paged_aligned4(q2k) || !paged_aligned4(lse))
     return MSA_ERR_ALIGNMENT;
+  // tiles are counted in 32 bits
+  if (int64_t(table->rows) * cache->kv_heads * table->width * cache->page_size > (int64_t(1) << 36))
+    return MSA_ERR_INVALID_ARG;
   if (workspace_bytes < decode_workspace(cache->head_dim)) return MSA_ERR_WORKSPACE;
   st = check_device();
   if (st != MSA_OK) return st;
@@ -796,8 +1034,8 @@ extern "C" msa_status msa_paged_decode(const msa_paged_cache* cache, const msa_p
   a.kv_heads = cache->kv_heads;
   a.group = q_heads / cache->kv_heads;
   uint8_t* w = static_cast<uint8_t*>(workspace);
-  a.rec = reinterpret_cast<JoinRec*>(w);
-  w += align_up(sizeof(JoinRec) * kMaxGrid, 256);
+  a.rec = reinterpret_cast<int32_t*>(w);
+  w += align_up(sizeof(int32_t) * kMaxGrid, 256);
   a.part_ml = reinterpret_cast<float*>(w);
   a.part_o = a.part_ml + 2 * kMaxGrid * 2 * kGroup;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -459,6 +459,90 @@ def test_decode_peaked_and_growing_scores():
     _decode_case(FP, 64, 2, 4, 64, [700, 129], False, seed=14, spread=12.0)
 
 
+def _decode_shared_pages(dt, dim, kv, share, S, lens, sparse, seed):
+    """Long rows over few pages: the table names each many times, so the fp64
+    result is a sum over the pool's keys with their counts."""
+    rng, gen = np.random.default_rng(seed), _gen(seed)
+    pool = 24
+    width = -(-max(lens) // S) + 1
+    table = rng.integers(0, pool, (len(lens), width))
+    kc, vc = (_pool(gen, pool, S, kv, dim, dt) for _ in range(2))
+    q = _randn(gen, (len(lens), kv * share, dim), dt)
+    q2k = None
+    if sparse:
+        q2k = np.stack([[np.sort(rng.permutation(-(-n // 128))[:16]) for n in lens]
+                        for _ in range(kv)])
+    scale = dim ** -0.5
+    cache = api.PagedCache(kc, vc)
+    args = (cache, q, _i32(table), _i32(lens), scale, None if q2k is None else _i32(q2k))
+    o, lse = api.msa_paged_decode(*args)
+    again = [api.msa_paged_decode(*args) for _ in range(5)]
+    torch.cuda.synchronize()
+    assert api.msa_paged_read_status(cache) == 0
+    for x, y in again:
+        assert torch.equal(x, o) and torch.equal(y, lse), "not the same twice"
+    K, V, Q = _np(kc).reshape(pool * S, kv, dim), _np(vc).reshape(pool * S, kv, dim), _np(q)
+    O, L, BO, BL = (np.zeros((len(lens), kv * share) + x) for x in ((dim,), (), (dim,), ()))
+    for r, n in enumerate(lens):
+        for g in range(kv):
+            j = paged.visible(n, None if q2k is None else q2k[g, r])
+            at, count = np.unique(table[r, j // S] * S + j % S, return_counts=True)
+            h = slice(g * share, (g + 1) * share)
+            s = scale * (Q[r, h] @ K[at, g].T)
+            top = s.max(1, keepdims=True)
+            w = count * np.exp(s - top)
+            z = w.sum(1, keepdims=True)
+            O[r, h], L[r, h] = (w / z) @ V[at, g], (top + np.log(z))[:, 0]
+            # as oracle.paged.decode_bounds
+            ds = (dim + 4) * U * scale * (np.abs(Q[r, h]) @ np.abs(K[at, g]).T).max(1)
+            big = np.abs(s).max(1)
+            e = ds + U * (8 + 4 * big) + U * (4 * (j.size / 16 + 400) + j.size)
+            pv = (w / z) @ np.abs(V[at, g])
+            BO[r, h] = (1.01 * (2 * e + HALF[dt]))[:, None] * pv + HALF[dt] * np.abs(O[r, h]) \
+                + TINY[dt] + j.size * TINY[dt] * np.abs(V[at, g]).max() / z
+            BL[r, h] = 1.01 * e + 4 * U * (np.abs(L[r, h]) + big + np.log(j.size) + 1)
+    _within(_np(lse), L, BL, "LSE")
+    _within(_np(o), O, BO, "O")
+
+
+def test_decode_enough_tiles_for_the_short_runs():
+    _decode_shared_pages(BF, 128, 4, 16, 128, [330001, 5, 70000], False, seed=31)
+    _decode_shared_pages(FP, 64, 4, 5, 64, [700003], False, seed=32)
+    _decode_shared_pages(BF, 128, 4, 16, 64, [2100 + 7 * i for i in range(190)], True, seed=33)
+
+
+def test_caches_of_more_than_2_to_the_31_elements():
+    """Pages whose first element lies past 2^31 (and past 2^32 bytes)."""
+    gen, S, pool = _gen(34), 128, 33000
+    kc, vc = (torch.empty(pool, S, 4, 128, dtype=BF, device=DEV) for _ in range(2))
+    keys = torch.empty(2 * pool, S, 4, 128, dtype=BF, device=DEV)
+    used = [pool - 1, 3, pool - 2, 0]
+    n = 400
+    table = np.array([used])
+    cache = api.PagedCache(kc, vc)
+    q, k, v = (_randn(gen, (n, h, 128), BF) for h in (64, 4, 4))
+    ik, t = _randn(gen, (n, 4, 128), BF), _i32(table)
+    offs, start = _i32([0, n]), _i32([0])
+    k_out = torch.empty_like(k)
+    api.msa_paged_append(cache, k, v, t, offs, start, inv_freq=torch.rand(64, device=DEV), q=q,
+                         k_out=k_out)
+    index = api.PagedIndex(keys, torch.zeros(2 * pool, 4, 128, device=DEV))
+    api.msa_paged_index(index, ik, _i32([[2 * pool - 1, 3, 2 * pool - 2, 0]]), offs, start)
+    o, lse = api.msa_paged_decode(cache, q[:1], t, _i32([n]), 0.09)
+    torch.cuda.synchronize()
+    for i, pg in enumerate(used):
+        here = slice(128 * i, min(n, 128 * i + 128))
+        m = here.stop - here.start
+        assert torch.equal(kc[pg, :m], k_out[here]) and torch.equal(vc[pg, :m], v[here])
+    assert torch.equal(keys[2 * pool - 1], ik[:128])
+    small = np.array([[0, 1, 2, 3]])
+    K = np.stack([_np(kc[p]) for p in used])
+    V = np.stack([_np(vc[p]) for p in used])
+    O, L, BO, BL = paged.decode_bounds(K, V, _np(q[:1]), small, [n], 0.09, HALF[BF], TINY[BF])
+    _within(_np(lse), L, BL, "LSE")
+    _within(_np(o), O, BO, "O")
+
+
 def test_decode_bad_slots_pages_and_lengths():
     rng, gen = np.random.default_rng(15), _gen(15)
     lens = [300, 300, 300, 300, 300]
