@@ -961,8 +961,8 @@ template <typename T, int kDim>
 cudaError_t launch_decode(DecodeArgs a, cudaStream_t s) {
   using S = DecodeShape<kDim>;
   auto kernel = k_paged_decode<T, kDim>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       S::kSmem);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(kernel, S::kSmem, done);
   if (e != cudaSuccess) return e;
   a.slots = device_sm_count() * 2;
   if (a.slots > kMaxSlots) a.slots = kMaxSlots;

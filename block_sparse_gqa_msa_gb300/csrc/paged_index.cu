@@ -10,8 +10,8 @@
 // k_paged_index   one CTA a block that got a token and 128 channels: it brings
 //                 the block's keys, old and new, into shared memory with all
 //                 loads in flight, writes the new ones to the cache and sums
-//                 them in order.  Blocks are found by their first new token
-//                 (position a multiple of 128, or the row's first).
+//                 them in order.  Blocks are numbered over the rows and dealt
+//                 out in turn.
 // k_paged_select  one cluster of CTAs a (row, index head): a lane scores a
 //                 block, a warp keeps the best of its blocks in a list sorted
 //                 across its lanes, and the lists are merged through shared
@@ -47,48 +47,45 @@ __device__ __forceinline__ int64_t mean_slot(const PagedTable& t, int32_t page, 
   return (int64_t(page) << (t.shift - 7)) + ((last & ((1 << t.shift) - 1)) >> 7);
 }
 
-// Token t starts the new part of a block: its row, position and the number
-// of the block's new tokens (0: t does not).
-struct BlockStart {
-  int32_t row, n_new;
+// The new part of a block: its row, the first of its new tokens, that token's
+// position and their number.
+struct NewBlock {
+  int32_t row, t, n_new;
   int64_t pos;
 };
-__device__ __forceinline__ BlockStart block_start(const IndexArgs& a, int64_t t, int32_t r) {
-  BlockStart b{r, 0, 0};
-  const int32_t o0 = a.offs[r], o1 = a.offs[r + 1];
-  if (t < o0 || t >= o1) return b;
-  b.pos = int64_t(a.start[r]) + (t - o0);
-  if (t != o0 && (b.pos & 127) != 0) return b;
-  const int64_t room = 128 - (b.pos & 127);
-  b.n_new = int32_t(room < o1 - t ? room : o1 - t);
-  return b;
+// Blocks of row r that get a token (0: none, or the row's offsets or first
+// position are bad).
+__device__ __forceinline__ int32_t row_blocks(const IndexArgs& a, int32_t r) {
+  const int64_t o0 = a.offs[r], o1 = a.offs[r + 1], p = a.start[r];
+  if (o0 < 0 || o1 <= o0 || o1 > a.T) return 0;
+  if (p < 0) {
+    raise_paged(a.table.status, MSA_ERR_BAD_PAGE);
+    return 0;
+  }
+  return int32_t(((p + (o1 - o0) - 1) >> 7) - (p >> 7)) + 1;
 }
 
 struct IndexSmem {
   uint4 rows[kBlock][kIdxChunks];  // the block's keys, the CTA's channels
   int32_t pages[kIdxPages];
-  int32_t hit[kIdxThreads];
-  int n_hits;
+  int32_t sums[kIdxThreads / 32];
+  NewBlock block;
 };
 
-__device__ void index_block(const IndexArgs& a, int64_t t, const BlockStart& b, IndexSmem& sm) {
+__device__ __forceinline__ void index_block(const IndexArgs& a, IndexSmem& sm) {
+  const NewBlock b = sm.block;
   const int n_old = int(b.pos & 127);
   const int64_t first = b.pos - n_old;  // position of the block's first key
   const int n = n_old + b.n_new;
   const int64_t i0 = first >> a.table.shift;
   const int np = int(((first + n - 1) >> a.table.shift) - i0) + 1;
-  __syncthreads();  // the block before is done
-  bool bad = b.pos < 0;
-  if (!bad)
-    for (int i = threadIdx.x; i < np; i += kIdxThreads) {
-      const int32_t p = page_of(a.table, b.row, (i0 + i) << a.table.shift);
-      sm.pages[i] = p;
-      bad |= p < 0;
-    }
-  if (__syncthreads_or(bad)) {
-    if (threadIdx.x == 0) raise_paged(a.table.status, MSA_ERR_BAD_PAGE);
-    return;
+  bool bad = false;
+  for (int i = threadIdx.x; i < np; i += kIdxThreads) {
+    const int32_t p = page_of(a.table, b.row, (i0 + i) << a.table.shift);
+    sm.pages[i] = p;
+    bad |= p < 0;
   }
+  if (__syncthreads_or(bad)) return;
   const int width = a.heads * a.dim;
   const int mask = (1 << a.table.shift) - 1;
   // A thread's chunk is the same for all its keys.
@@ -96,7 +93,7 @@ __device__ void index_block(const IndexArgs& a, int64_t t, const BlockStart& b, 
   if (ch < width) {
     __nv_bfloat16* col =
         static_cast<__nv_bfloat16*>(a.keys.base) + (ch / a.dim) * a.keys.head + ch % a.dim;
-    const __nv_bfloat16* in = a.ik + t * a.ik_stride + ch;
+    const __nv_bfloat16* in = a.ik + b.t * a.ik_stride + ch;
     constexpr int kStep = kIdxThreads / kIdxChunks;
     constexpr int kEach = kBlock / kStep;
     uint4 w[kEach];
@@ -140,49 +137,59 @@ __device__ void index_block(const IndexArgs& a, int64_t t, const BlockStart& b, 
 
 __global__ void __launch_bounds__(kIdxThreads) k_paged_index(const IndexArgs a) {
   __shared__ IndexSmem sm;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   grid_dep_wait();
   grid_dep_release();
   if (blockIdx.x == 0 && blockIdx.y == 0) check_offsets(a.offs, a.table.rows, a.T, a.table.status);
-  if (a.T <= gridDim.x) {  // one token a CTA
-    const int64_t t = blockIdx.x;
-    const BlockStart b = block_start(a, t, find_row_warp(a.offs, a.table.rows, t));
-    if (b.n_new > 0) index_block(a, t, b, sm);
-    return;
+  // Blocks are numbered row by row and dealt out in turn: every thread counts
+  // those of a stretch of rows, a scan gives their places.
+  const int32_t rows = a.table.rows, each = (rows + kIdxThreads - 1) / kIdxThreads;
+  const int32_t r0 = min(rows, tid * each), r1 = min(rows, r0 + each);
+  int32_t mine = 0;
+  for (int32_t r = r0; r < r1; ++r) mine += row_blocks(a, r);
+  int32_t incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int32_t y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
   }
-  for (int64_t t0 = blockIdx.x; t0 < a.T; t0 += int64_t(kIdxThreads) * gridDim.x) {
-    __syncthreads();
-    if (threadIdx.x == 0) sm.n_hits = 0;
-    __syncthreads();
-    const int64_t t = t0 + int64_t(threadIdx.x) * gridDim.x;
-    if (t < a.T) {
-      int32_t lo = 0, hi = a.table.rows - 1;  // largest r with offs[r] <= t
-      while (lo < hi) {
-        const int32_t mid = (lo + hi + 1) >> 1;
-        if (a.offs[mid] <= t) lo = mid; else hi = mid - 1;
-      }
-      if (block_start(a, t, lo).n_new > 0) sm.hit[atomicAdd(&sm.n_hits, 1)] = int32_t(t);
+  if (lane == 31) sm.sums[warp] = incl;
+  __syncthreads();
+  int32_t total = 0, before = 0;
+#pragma unroll
+  for (int w = 0; w < kIdxThreads / 32; ++w) {
+    if (w < warp) before += sm.sums[w];
+    total += sm.sums[w];
+  }
+  before += incl - mine;
+  for (int32_t x = blockIdx.x; x < total; x += gridDim.x) {
+    if (x >= before && x < before + mine) {  // one thread: the block is in its stretch
+      int32_t k = x - before;
+      int32_t r = r0;
+      for (int32_t n; k >= (n = row_blocks(a, r)); ++r) k -= n;
+      const int32_t o0 = a.offs[r], o1 = a.offs[r + 1];
+      const int64_t p = a.start[r], first = k == 0 ? p : ((p >> 7) + k) << 7;
+      NewBlock b;
+      b.row = r;
+      b.pos = first;
+      b.t = o0 + int32_t(first - p);
+      b.n_new = int32_t(min(128 - (first & 127), int64_t(o1 - b.t)));
+      sm.block = b;
     }
     __syncthreads();
-    const int n = sm.n_hits;
-    for (int i = 0; i < n; ++i) {
-      const int64_t t = sm.hit[i];
-      index_block(a, t, block_start(a, t, find_row_warp(a.offs, a.table.rows, t)), sm);
-    }
+    index_block(a, sm);
+    __syncthreads();  // the block is done
   }
 }
 
 // ------------------------------------------------------------------ selection
-constexpr int kSelWarps = 4;
-constexpr int kSelThreads = kSelWarps * 32;
 constexpr int kSelMaxCluster = 8;
 // A warp's ring of slabs: 32 channels of the means of 32 blocks, a block's
 // row 16 bytes longer than its 128 so that 8 rows' 16-byte reads hit
 // different banks.
 constexpr int kSlabRow = 144;
 constexpr int kSlabBytes = 32 * kSlabRow;
-constexpr int kSlabs = 4;
-constexpr int kSelFill = 4;  // CTAs an SM
-constexpr int kSelSmem = kSelWarps * kSlabs * kSlabBytes;  // 72 KB
+constexpr int kSlabs = 3;
 
 struct SelectArgs {
   const __nv_bfloat16* iq;
@@ -231,10 +238,12 @@ __device__ __forceinline__ uint64_t sort_desc(uint64_t x, int lane) {
   return x;
 }
 
-__global__ void __launch_bounds__(kSelThreads) k_paged_select(const SelectArgs a) {
+template <int kSelWarps>
+__global__ void __launch_bounds__(kSelWarps * 32) k_paged_select(const SelectArgs a) {
+  constexpr int kSelThreads = kSelWarps * 32;
   namespace cg = cooperative_groups;
   extern __shared__ __align__(128) uint8_t slabs[];
-  __shared__ float sq[128];
+  __shared__ __align__(16) float sq[128];
   __shared__ uint64_t lists[kSelWarps][kTopK];
   __shared__ uint64_t from[kSelMaxCluster][kTopK];
   cg::cluster_group cluster = cg::this_cluster();
@@ -284,7 +293,7 @@ __global__ void __launch_bounds__(kSelThreads) k_paged_select(const SelectArgs a
       const int64_t m = __shfl_sync(0xffffffffu, row, k);
       const bool real = m >= 0 && c < a.dim;
       const float* src = real ? a.means + m * a.dim + c : a.means;
-      asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(
+      asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(
                        ring + stage * kSlabBytes + k * kSlabRow + (lane & 7) * 16),
                    "l"(src), "r"(real ? 16 : 0)
                    : "memory");
@@ -312,15 +321,15 @@ __global__ void __launch_bounds__(kSelThreads) k_paged_select(const SelectArgs a
       const float4* m = reinterpret_cast<const float4*>(
           slabs + warp * (kSlabs * kSlabBytes) + stage * kSlabBytes + lane * kSlabRow);
       const int n4 = min(8, (a.dim - c * 32) / 4);
-      const float* q = sq + c * 32;
+      const float4* q = reinterpret_cast<const float4*>(sq + c * 32);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         if (k < n4) {
-          const float4 s = m[k];
-          acc = fmaf(q[4 * k + 0], s.x, acc);
-          acc = fmaf(q[4 * k + 1], s.y, acc);
-          acc = fmaf(q[4 * k + 2], s.z, acc);
-          acc = fmaf(q[4 * k + 3], s.w, acc);
+          const float4 s = m[k], t = q[k];
+          acc = fmaf(t.x, s.x, acc);
+          acc = fmaf(t.y, s.y, acc);
+          acc = fmaf(t.z, s.z, acc);
+          acc = fmaf(t.w, s.w, acc);
         }
       }
       stage = (stage + 1) % kSlabs;
@@ -330,6 +339,11 @@ __global__ void __launch_bounds__(kSelThreads) k_paged_select(const SelectArgs a
       const int32_t v = gv + lane;
       const int32_t last = min(v * kBlock + kBlock - 1, len - 1);
       if (page_of(a.table, r, last) >= 0) key = rank_key(acc, v);
+    }
+    // nothing here beats the last of the kept ones: most groups of a long row
+    if (!__any_sync(0xffffffffu, key > __shfl_sync(0xffffffffu, best, kTopK - 1))) {
+      gv += v_step;
+      continue;
     }
     key = sort_desc(key, lane);
     // the larger of best[i] and key[31 - i] are the best 32 of both lists
@@ -375,33 +389,43 @@ __global__ void __launch_bounds__(kSelThreads) k_paged_select(const SelectArgs a
   if (lane < kTopK) out[place] = mine == INT32_MAX ? -1 : mine;
 }
 
-cudaError_t launch_paged_select(const SelectArgs& a, cudaStream_t s) {
-  // CTAs of a cluster: one for every 128 blocks that the table has room for,
-  // while the batch alone does not fill the chip.
-  const int64_t room = ((int64_t(a.table.width) << a.table.shift) + kBlock - 1) / kBlock;
-  const int64_t units = int64_t(a.table.rows) * a.heads;
-  int C = 1;
-  while (C < kSelMaxCluster && room > int64_t(C) * kSelThreads &&
-         units * C < int64_t(kSelFill) * device_sm_count())
-    C *= 2;
-  cudaError_t e = cudaFuncSetAttribute(k_paged_select, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       kSelSmem);
+template <int kSelWarps>
+cudaError_t launch_select_as(const SelectArgs& a, int cluster, cudaStream_t s) {
+  constexpr int kSmem = kSelWarps * kSlabs * kSlabBytes;
+  auto kernel = k_paged_select<kSelWarps>;
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(kernel, kSmem, done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(int64_t(a.table.rows) * a.heads * C));
-  cfg.blockDim = dim3(kSelThreads);
-  cfg.dynamicSmemBytes = kSelSmem;
+  cfg.gridDim = dim3(unsigned(int64_t(a.table.rows) * a.heads * cluster));
+  cfg.blockDim = dim3(kSelWarps * 32);
+  cfg.dynamicSmemBytes = kSmem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = unsigned(C);
+  attr[0].val.clusterDim.x = unsigned(cluster);
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = profiling_on() ? 1 : 2;
-  return cudaLaunchKernelEx(&cfg, k_paged_select, a);
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+cudaError_t launch_paged_select(const SelectArgs& a, cudaStream_t s) {
+  // A cluster's CTAs: one for every 128 blocks that the table has room for, while
+  // the batch leaves SMs without any (64 rows of up to 1024 blocks: 22 us with 2,
+  // 24 with 4).  Four warps a CTA, four CTAs an SM; batches that would not be on
+  // the chip at once so take two warps (256 rows of 64 blocks: 6.0 us, with
+  // four 8.8; one row of 1024: 7.1, with four 5.4).
+  const int64_t room = ((int64_t(a.table.width) << a.table.shift) + kBlock - 1) / kBlock;
+  const int64_t units = int64_t(a.table.rows) * a.heads, sms = device_sm_count();
+  int cluster = 1;
+  while (cluster < kSelMaxCluster && room > int64_t(cluster) * 128 && units * cluster < 2 * sms)
+    cluster *= 2;
+  return units * cluster > 4 * sms ? launch_select_as<2>(a, cluster, s)
+                                   : launch_select_as<4>(a, cluster, s);
 }
 
 }  // namespace
@@ -436,13 +460,15 @@ extern "C" msa_status msa_paged_index(const msa_paged_index_cache* cache,
   a.heads = cache->heads;
   a.dim = cache->dim;
   const int slices = (a.heads * a.dim + kIdxSlice - 1) / kIdxSlice;
-  // Six CTAs an SM (their shared memory).  An odd number of them along the
-  // tokens: blocks start 128 tokens apart, and an odd stride spreads them
-  // over all CTAs.
-  const int64_t most = int64_t(device_sm_count()) * 6 / slices | 1;
+  // Six CTAs an SM (their shared memory), no more than there can be blocks.
+  int64_t most = int64_t(device_sm_count()) * 6 / slices;
+  const int64_t blocks = T / kBlock + 2 * int64_t(table->rows);
+  if (most > blocks) most = blocks;
+  if (most > T) most = T;
+  if (most < 1) most = 1;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   launch_begin("paged_index", s);
-  const cudaError_t e = launch_k(true, k_paged_index, dim3(unsigned(T < most ? T : most), slices),
+  const cudaError_t e = launch_k(true, k_paged_index, dim3(unsigned(most), slices),
                                  dim3(kIdxThreads), 0, s, a);
   launch_end("paged_index", s);
   return e == cudaSuccess ? MSA_OK : MSA_ERR_CUDA;
