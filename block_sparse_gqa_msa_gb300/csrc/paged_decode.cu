@@ -47,6 +47,8 @@
 // a plain copy; 285 without the short runs.  128 rows of 500 to 16384 tokens,
 // selected blocks, 508 MB: 91 us, 5.6 TB/s (units of 32 tiles: the chip's
 // start, 6 us, and the ends of runs and units weigh more).
+#include <cooperative_groups.h>
+
 #include "paged.cuh"
 #include "sm100.cuh"
 
@@ -82,6 +84,11 @@ constexpr int kTailShare = 12;  // one in so many tiles is kept back for the sho
 constexpr int kTailFrom = 64;   // in calls of so many tiles a CTA and more
 constexpr int kMaxSlots = 160 * 2;
 constexpr int kMaxGrid = kMaxSlots * 2;
+
+// Few units (32 at 8 CTAs each fill the chip) that are not long: a cluster of
+// CTAs takes each, and no second kernel is needed.
+constexpr int kClusterCtas = 8;
+constexpr int kClusterTiles = 8;  // of a CTA at most, by the room in the table
 
 struct DecodeArgs {
   const void* q;
@@ -429,12 +436,11 @@ struct Fetch {
             lane * 64));
     }
   }
-  // Before the first tile: the run to begin is the CTA's own.
-  __device__ __forceinline__ void init(const Deal& deal) {
-    find_run<kDim>(a, prefix, deal, blockIdx.x, next);
+  // Before the first tile: the run to begin lies in *next.
+  __device__ __forceinline__ void init(bool tail) {
     n_run = 1;
     n_seg = 0;
-    more = deal.runs > deal.c0;
+    more = tail;
     found = true;
     left = 0;
     i = 0;
@@ -572,7 +578,9 @@ struct Fetch {
   }
 };
 
-template <typename T, int kDim>
+// kCluster: a cluster of CTAs takes one unit, in equal parts, and joins them in
+// its shared memory.
+template <typename T, int kDim, bool kCluster>
 __global__ void __launch_bounds__(kDecThreads, 2) k_paged_decode(const DecodeArgs a) {
   using S = DecodeShape<kDim>;
   constexpr int kSteps = kDim / 16;            // k-steps of the first product
@@ -585,26 +593,43 @@ __global__ void __launch_bounds__(kDecThreads, 2) k_paged_decode(const DecodeArg
   __shared__ int32_t blocks[kDecWarps][kTopK];
   __shared__ Segment queue[kDecWarps][kSegQueue];
   __shared__ float ml[2][kDecWarps][kGroup];
+  __shared__ float state_ml[2][kGroup];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r_lo = lane >> 2;  // the lane's matrix rows: r_lo and r_lo + 8
   const int col = (lane & 3) * 2;
   grid_dep_wait();
   grid_dep_release();
-  if (tid == 0) {
-    for (int i = 0; i < kAnswers; ++i) mbar_init(smem_u32(&ctas.bar[i]), 1);
-    fence_mbar_init();
-  }
-  make_prefix<kDim>(a, prefix);
-  const Deal deal(prefix.total, a.slots, gridDim.x);
-  if (blockIdx.x >= deal.runs) {
-    if (tid == 0) a.rec[blockIdx.x] = 0;
-    return;
+  bool tail = false;
+  if constexpr (kCluster) {
+    const int rank = blockIdx.x % kClusterCtas;
+    const int32_t unit = blockIdx.x / kClusterCtas;
+    const int32_t row = unit / a.kv_heads, n = a.kv_len[row], len = checked_len(a, n);
+    if (n != len && tid == 0) raise_paged(a.table.status, MSA_ERR_BAD_PAGE);
+    const int32_t tiles = unit_tiles<kDim>(len, a.q2k != nullptr);
+    const int32_t i0 = tiles * rank / kClusterCtas, i1 = tiles * (rank + 1) / kClusterCtas;
+    if (lane == 0) next[warp] = NextRun{0, row, unit % a.kv_heads, len, tiles, i0, i1 - i0};
+    __syncwarp();
+  } else {
+    if (tid == 0) {
+      for (int i = 0; i < kAnswers; ++i) mbar_init(smem_u32(&ctas.bar[i]), 1);
+      fence_mbar_init();
+    }
+    make_prefix<kDim>(a, prefix);
+    const Deal deal(prefix.total, a.slots, gridDim.x);
+    if (blockIdx.x >= deal.runs) {
+      if (tid == 0) a.rec[blockIdx.x] = 0;
+      return;
+    }
+    tail = deal.runs > deal.c0;
+    find_run<kDim>(a, prefix, deal, blockIdx.x, &next[warp]);
   }
 
   const uint32_t ring = smem_u32(smem) + warp * S::kRing;
   float* merge = reinterpret_cast<float*>(smem + kDecWarps * S::kRing);
+  [[maybe_unused]] float* state = reinterpret_cast<float*>(smem);  // the unit's, over the drained ring
   Fetch<T, kDim> fetch{a, blocks[warp], queue[warp], prefix, &ctas, &next[warp], lane, warp};
-  fetch.init(deal);
+  fetch.init(tail);
+  [[maybe_unused]] const bool idle = next[warp].n == 0;  // (only in a cluster)
 
   uint32_t qa[kSteps][4];           // the query heads as the left operand
   float acc[kCols][4];              // O
@@ -619,7 +644,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) k_paged_decode(const DecodeArg
   // fill the ring (the very first has no tile yet: the run is begun in it).
   int fill = S::kStages;
 #pragma unroll 1
-  while (true) {
+  while (!kCluster || !idle) {
     const uint32_t kb = ring + stage * S::kStageBytes, vb = kb + S::kWarpKeys * S::kRow;
     const uint32_t seen = there[0];
     if (fill == 0) cp_async_wait<S::kStages - 2>();
@@ -636,7 +661,8 @@ __global__ void __launch_bounds__(kDecThreads, 2) k_paged_decode(const DecodeArg
       if (left == 0) {  // the next segment; heads past the group are zeros
         g = queue[warp][seg % kSegQueue];
         left = g.i1 - g.i0;
-        if (g.opens && tid == 0) a.rec[g.run] = g.i0 > 0 ? 1 + g.row * a.kv_heads + g.head : 0;
+        if (!kCluster && g.opens && tid == 0)
+          a.rec[g.run] = g.i0 > 0 ? 1 + g.row * a.kv_heads + g.head : 0;
         const T* q = static_cast<const T*>(a.q) +
                      (int64_t(g.row) * a.kv_heads + g.head) * a.group * kDim + col;
 #pragma unroll
@@ -715,9 +741,15 @@ __global__ void __launch_bounds__(kDecThreads, 2) k_paged_decode(const DecodeArg
       }
 #pragma unroll
       for (int k = 0; k < kKeyTiles; k += 2) {
-        const uint32_t pa[4] = {
-            Pair<T>::pack(x[k][0], x[k][1]), Pair<T>::pack(x[k][2], x[k][3]),
-            Pair<T>::pack(x[k + 1][0], x[k + 1][1]), Pair<T>::pack(x[k + 1][2], x[k + 1][3])};
+        // weights as two numbers of the cache's type, the second what the first leaves
+        uint32_t pa[4], pb[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float u = x[k + (e >> 1)][(e & 1) * 2], v = x[k + (e >> 1)][(e & 1) * 2 + 1];
+          pa[e] = Pair<T>::pack(u, v);
+          const float2 r = Pair<T>::unpack(pa[e]);
+          pb[e] = Pair<T>::pack(u - r.x, v - r.y);
+        }
         // matrices: keys 0-7 / 8-15 by channels 0-7 / 8-15 of the pair of column tiles
         const int key = k * 8 + (lane & 15);
         const uint32_t rowp = vb + key * S::kRow;
@@ -727,6 +759,8 @@ __global__ void __launch_bounds__(kDecThreads, 2) k_paged_decode(const DecodeArg
           ldsm4_t(b, rowp + (((n + (lane >> 4)) ^ (key & 7)) << 4));
           mma16816<T>(acc[n], pa, b[0], b[1]);
           mma16816<T>(acc[n + 1], pa, b[2], b[3]);
+          mma16816<T>(acc[n], pb, b[0], b[1]);
+          mma16816<T>(acc[n + 1], pb, b[2], b[3]);
         }
       }
     }
@@ -759,7 +793,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) k_paged_decode(const DecodeArg
       ml[1][warp][r_lo] = l0 * f0;
       ml[1][warp][r_lo + 8] = l1 * f1;
     }
-    const bool whole = g.i0 == 0 && g.i1 == g.tiles;
+    const bool whole = !kCluster && g.i0 == 0 && g.i1 == g.tiles;
     const int64_t slot = 2 * int64_t(g.run) + (g.i0 > 0 ? 0 : 1);
     const int64_t unit = int64_t(g.row) * a.kv_heads + g.head;
     const int h = tid / 8;  // the thread's row of the result, 4 channels of each 32
@@ -795,7 +829,9 @@ __global__ void __launch_bounds__(kDecThreads, 2) k_paged_decode(const DecodeArg
         v.w += u.w;
       }
       const int ch = c * 32 + (tid % 8) * 4;
-      if (!whole)
+      if (kCluster)
+        *reinterpret_cast<float4*>(state + h * kDim + ch) = v;
+      else if (!whole)
         *reinterpret_cast<float4*>(a.part_o + (slot * kGroup + h) * kDim + ch) = v;
       else if (h < a.group)
         *reinterpret_cast<uint2*>(static_cast<T*>(a.o) + (unit * a.group + h) * kDim + ch) =
@@ -803,7 +839,10 @@ __global__ void __launch_bounds__(kDecThreads, 2) k_paged_decode(const DecodeArg
       __syncthreads();  // the buffers are read
     }
     if (tid % 8 == 0) {
-      if (!whole) {
+      if (kCluster) {
+        state_ml[0][h] = M;
+        state_ml[1][h] = l;
+      } else if (!whole) {
         a.part_ml[slot * (2 * kGroup) + h] = M;
         a.part_ml[slot * (2 * kGroup) + kGroup + h] = l;
       } else if (h < a.group) {
@@ -813,6 +852,55 @@ __global__ void __launch_bounds__(kDecThreads, 2) k_paged_decode(const DecodeArg
     if (++seg == fetch.n_seg) break;  // the fetch is ahead: it would have entered the next one
   }
   cp_async_wait<0>();
+  if constexpr (kCluster) {
+    // Every CTA joins the parts of its share of the heads, a thread a few channels.
+    namespace cg = cooperative_groups;
+    cg::cluster_group cluster = cg::this_cluster();
+    if (idle) {
+      for (int e = tid; e < kGroup * kDim; e += kDecThreads) state[e] = 0.f;
+      if (tid < kGroup) {
+        state_ml[0][tid] = -INFINITY;
+        state_ml[1][tid] = 0.f;
+      }
+    }
+    cluster.sync();
+    constexpr int kHeads = kGroup / kClusterCtas;       // of a CTA
+    constexpr int kPer = kHeads * kDim / kDecThreads;   // channels of a thread
+    const int h = int(cluster.block_rank()) * kHeads + tid / (kDecThreads / kHeads);
+    const int ch = tid % (kDecThreads / kHeads) * kPer;
+    float pm[kClusterCtas], pl[kClusterCtas], po[kClusterCtas][kPer];
+    float M = -INFINITY;
+#pragma unroll
+    for (int c = 0; c < kClusterCtas; ++c) {
+      pm[c] = *cluster.map_shared_rank(&state_ml[0][h], c);
+      pl[c] = *cluster.map_shared_rank(&state_ml[1][h], c);
+      const float* o = cluster.map_shared_rank(state + h * kDim + ch, c);
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) po[c][e] = o[e];
+      M = fmaxf(M, pm[c]);
+    }
+    float l = 0.f, o[kPer] = {};
+#pragma unroll
+    for (int c = 0; c < kClusterCtas; ++c) {
+      const float f = pm[c] == -INFINITY ? 0.f : fast_exp2(pm[c] - M);
+      l += pl[c] * f;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) o[e] += po[c][e] * f;
+    }
+    if (h < a.group) {
+      const int64_t out = int64_t(blockIdx.x / kClusterCtas) * a.group + h;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      T* dst = static_cast<T*>(a.o) + out * kDim + ch;
+      if constexpr (kPer == 2) {
+        *reinterpret_cast<uint32_t*>(dst) = Pair<T>::pack(o[0] * inv, o[1] * inv);
+      } else {
+        const uint32_t w = Pair<T>::pack(o[0] * inv, 0.f);
+        *reinterpret_cast<uint16_t*>(dst) = uint16_t(w);
+      }
+      if (ch == 0) a.lse[out] = l == 0.f ? -INFINITY : kLn2 * (M + log2f(l));
+    }
+    cluster.sync();  // nobody reads this CTA's state any more
+  }
 }
 
 // Joins the parts of the units that several runs share.  CTA x stands for run
@@ -960,18 +1048,30 @@ size_t decode_workspace(int32_t dim) {
 template <typename T, int kDim>
 cudaError_t launch_decode(DecodeArgs a, cudaStream_t s) {
   using S = DecodeShape<kDim>;
-  auto kernel = k_paged_decode<T, kDim>;
+  a.slots = device_sm_count() * 2;
+  if (a.slots > kMaxSlots) a.slots = kMaxSlots;
+  // What the room in the table allows.
+  int64_t unit = (int64_t(a.table.width) << a.table.shift) / S::kTileKeys + 1;
+  if (a.q2k && unit > kTopK * S::kTilesPerBlock) unit = kTopK * S::kTilesPerBlock;
+  const int64_t units = int64_t(a.table.rows) * a.kv_heads;
+  if (units * kClusterCtas <= a.slots && unit <= kClusterCtas * kClusterTiles) {
+    auto kernel = k_paged_decode<T, kDim, true>;
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(kernel, S::kSmem, done);
+    if (e != cudaSuccess) return e;
+    launch_begin("paged_decode", s);
+    e = launch_cluster(kernel, dim3(unsigned(units * kClusterCtas)), dim3(kDecThreads), S::kSmem,
+                       kClusterCtas, s, a);
+    launch_end("paged_decode", s);
+    return e;
+  }
+  auto kernel = k_paged_decode<T, kDim, false>;
   static std::atomic<uint64_t> done{0};
   cudaError_t e = allow_smem(kernel, S::kSmem, done);
   if (e != cudaSuccess) return e;
-  a.slots = device_sm_count() * 2;
-  if (a.slots > kMaxSlots) a.slots = kMaxSlots;
-  // Short runs only where the batch, by the room in its table, can have
-  // enough tiles for them.
-  int64_t most = (int64_t(a.table.width) << a.table.shift) / S::kTileKeys + 1;
-  if (a.q2k && most > kTopK * S::kTilesPerBlock) most = kTopK * S::kTilesPerBlock;
-  most *= int64_t(a.table.rows) * a.kv_heads;
-  const int grid = a.slots + (most >= int64_t(a.slots) * kTailFrom ? a.slots / 4 * 4 : 0);
+  // Short runs only where there can be enough tiles for them.
+  const int grid =
+      a.slots + (unit * units >= int64_t(a.slots) * kTailFrom ? a.slots / 4 * 4 : 0);
   launch_begin("paged_decode", s);
   e = launch_k(true, kernel, dim3(unsigned(grid)), dim3(kDecThreads), S::kSmem, s, a);
   launch_end("paged_decode", s);

@@ -396,21 +396,8 @@ cudaError_t launch_select_as(const SelectArgs& a, int cluster, cudaStream_t s) {
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = allow_smem(kernel, kSmem, done);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(int64_t(a.table.rows) * a.heads * cluster));
-  cfg.blockDim = dim3(kSelWarps * 32);
-  cfg.dynamicSmemBytes = kSmem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = unsigned(cluster);
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = profiling_on() ? 1 : 2;
-  return cudaLaunchKernelEx(&cfg, kernel, a);
+  return launch_cluster(kernel, dim3(unsigned(int64_t(a.table.rows) * a.heads * cluster)),
+                        dim3(kSelWarps * 32), kSmem, unsigned(cluster), s, a);
 }
 
 cudaError_t launch_paged_select(const SelectArgs& a, cudaStream_t s) {

@@ -107,8 +107,9 @@ def decode(k_cache, v_cache, q, table, lens, scale, q2k=None):
 
 def decode_bounds(k_cache, v_cache, q, table, lens, scale, step: float, tiny: float, q2k=None):
     """Element-wise error bounds (O, LSE) of a kernel that keeps scores and
-    states in fp32 and rounds weights and output once to a type of relative
-    half step ``step`` and smallest half step ``tiny``.
+    states in fp32, gives a weight as the sum of two numbers of a type of
+    relative half step ``step`` and smallest half step ``tiny`` (the second is
+    what rounding leaves over), and rounds the output to that type.
 
     u = 2^-24.  A score is a chain of dim fp32 products and sums and one
     scaling (of a constant rounded twice): |ds| <= (dim + 4) u scale sum |q||k|.
@@ -116,9 +117,9 @@ def decode_bounds(k_cache, v_cache, q, table, lens, scale, step: float, tiny: fl
     / ln 2 + |ds|; a rescaling of the state (one at most for each 16 keys, and
     one for each join, 400 at most) adds 4 u, a sum over n keys n u.  So
     a weight and the normaliser are each off by e (relative), O by twice that
-    times sum p|v|; the weight's rounding adds step * sum p|v| (and tiny for
-    each weight below the normal range, against a largest weight of 1), the
-    output's step * |O| + tiny.  LSE: e, plus the sum's and logarithm's roundings."""
+    times sum p|v|; a weight's two roundings add step^2 * sum p|v| (and tiny for
+    each weight whose rest is below the normal range, against a largest weight
+    of 1), the output's step * |O| + tiny.  LSE: e, plus the sum's and logarithm's roundings."""
     u = 2.0 ** -24
     O, L = decode(k_cache, v_cache, q, table, lens, scale, q2k)
     BO, BL = np.zeros_like(O), np.zeros_like(L)
@@ -141,7 +142,7 @@ def decode_bounds(k_cache, v_cache, q, table, lens, scale, step: float, tiny: fl
             e = ds + u * (8 + 4 * biggest) + u * (4 * (m / 16 + 400) + m)
             p = np.exp(s - L[r, h][:, None])
             pv = p @ np.abs(V[j, g])
-            BO[r, h] = ((2 * e + step) * 1.01)[:, None] * pv + step * np.abs(O[r, h]) + tiny \
+            BO[r, h] = ((2 * e + step ** 2) * 1.01)[:, None] * pv + step * np.abs(O[r, h]) + tiny \
                 + m * tiny * np.abs(V[j, g]).max() * np.exp(s.max(1) - L[r, h])[:, None]
             BL[r, h] = 1.01 * e + 4 * u * (np.abs(L[r, h]) + biggest + np.log(m) + 1)
     return O, L, BO, BL

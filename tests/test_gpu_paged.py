@@ -433,6 +433,18 @@ def test_decode_one_row(n, sparse):
     _decode_case(BF, 128, 4, 16, 64, [n], sparse, seed=n)
 
 
+@pytest.mark.parametrize("dt,dim,kv,share,S,head_major", [
+    (BF, 128, 4, 16, 128, False), (FP, 64, 2, 3, 32, True), (FP, 128, 1, 9, 16, False),
+    (BF, 64, 3, 16, 8, False),
+])
+@pytest.mark.parametrize("sparse", [False, True])
+def test_decode_few_short_rows(dt, dim, kv, share, S, head_major, sparse):
+    # one cluster of CTAs a unit; parts without a tile among them
+    for lens in ([0, 1, 129, 1000, 16], [64, 65, 513, 2100], [0], [2048]):
+        _decode_case(dt, dim, kv, share, S, lens, sparse, seed=S + dim + len(lens),
+                     head_major=head_major)
+
+
 def test_decode_row_without_keys_alone():
     _decode_case(BF, 128, 4, 16, 64, [0], False, seed=1)
     _decode_case(FP, 64, 1, 2, 64, [0, 0], True, seed=2)
@@ -498,7 +510,7 @@ def _decode_shared_pages(dt, dim, kv, share, S, lens, sparse, seed):
             big = np.abs(s).max(1)
             e = ds + U * (8 + 4 * big) + U * (4 * (j.size / 16 + 400) + j.size)
             pv = (w / z) @ np.abs(V[at, g])
-            BO[r, h] = (1.01 * (2 * e + HALF[dt]))[:, None] * pv + HALF[dt] * np.abs(O[r, h]) \
+            BO[r, h] = (1.01 * (2 * e + HALF[dt] ** 2))[:, None] * pv + HALF[dt] * np.abs(O[r, h]) \
                 + TINY[dt] + j.size * TINY[dt] * np.abs(V[at, g]).max() / z
             BL[r, h] = 1.01 * e + 4 * U * (np.abs(L[r, h]) + big + np.log(j.size) + 1)
     _within(_np(lse), L, BL, "LSE")
