@@ -407,6 +407,12 @@ struct Fetch {
     if (a.q2k && lane < kTopK && r < a.table.rows)
       slots = a.q2k[(int64_t(h) * a.table.rows + r) * kTopK + lane];
   }
+  __device__ __forceinline__ void prefetch_queries(int32_t r, int32_t h) {
+    if (lane * 64 < a.group * kDim)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(
+          static_cast<const T*>(a.q) + (int64_t(r) * a.kv_heads + h) * a.group * kDim +
+          lane * 64));
+  }
   // Enters the unit (row, head) at tile i: its blocks (the distinct valid
   // slots, in slot order), its place in the queue, and a look ahead.
   __device__ __forceinline__ void enter(int32_t opens) {
@@ -425,15 +431,13 @@ struct Fetch {
     if (lane == 0) queue[n_seg % kSegQueue] = Segment{run, row, head, i, i1, tiles, opens};
     ++n_seg;
     __syncwarp();
+    if (opens) prefetch_queries(row, head);
     if (left > 0) {  // the next unit: its length, slots and queries
       const int32_t r = head + 1 == a.kv_heads ? row + 1 : row;
       const int32_t h = head + 1 == a.kv_heads ? 0 : head + 1;
       next_len = a.kv_len[r];
       load_slots(r, h);
-      if (lane * 64 < a.group * kDim)
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(
-            static_cast<const T*>(a.q) + (int64_t(r) * a.kv_heads + h) * a.group * kDim +
-            lane * 64));
+      prefetch_queries(r, h);
     }
   }
   // Before the first tile: the run to begin lies in *next.
@@ -647,6 +651,27 @@ __global__ void __launch_bounds__(kDecThreads, 2) k_paged_decode(const DecodeArg
   while (!kCluster || !idle) {
     const uint32_t kb = ring + stage * S::kStageBytes, vb = kb + S::kWarpKeys * S::kRow;
     const uint32_t seen = there[0];
+    if (fill == 0 && left == 0) {  // the next segment; heads past the group are zeros
+      g = queue[warp][seg % kSegQueue];
+      left = g.i1 - g.i0;
+      if (!kCluster && g.opens && tid == 0)
+        a.rec[g.run] = g.i0 > 0 ? 1 + g.row * a.kv_heads + g.head : 0;
+      const T* q = static_cast<const T*>(a.q) +
+                   (int64_t(g.row) * a.kv_heads + g.head) * a.group * kDim + col;
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        const uint32_t* lo = reinterpret_cast<const uint32_t*>(q + r_lo * kDim + s * 16);
+        const uint32_t* hi = reinterpret_cast<const uint32_t*>(q + (r_lo + 8) * kDim + s * 16);
+        qa[s][0] = r_lo < a.group ? lo[0] : 0;
+        qa[s][1] = r_lo + 8 < a.group ? hi[0] : 0;
+        qa[s][2] = r_lo < a.group ? lo[4] : 0;
+        qa[s][3] = r_lo + 8 < a.group ? hi[4] : 0;
+      }
+#pragma unroll
+      for (int n = 0; n < kCols; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
+      m0 = m1 = -INFINITY;
+      l0 = l1 = 0.f;
+    }
     if (fill == 0) cp_async_wait<S::kStages - 2>();
     __syncwarp();
     {
@@ -656,29 +681,6 @@ __global__ void __launch_bounds__(kDecThreads, 2) k_paged_decode(const DecodeArg
       there[S::kStages - 2] = fetch.copy(ring + free * S::kStageBytes);
       cp_async_commit();
       fetch.advance();
-    }
-    if (fill == 0) {
-      if (left == 0) {  // the next segment; heads past the group are zeros
-        g = queue[warp][seg % kSegQueue];
-        left = g.i1 - g.i0;
-        if (!kCluster && g.opens && tid == 0)
-          a.rec[g.run] = g.i0 > 0 ? 1 + g.row * a.kv_heads + g.head : 0;
-        const T* q = static_cast<const T*>(a.q) +
-                     (int64_t(g.row) * a.kv_heads + g.head) * a.group * kDim + col;
-#pragma unroll
-        for (int s = 0; s < kSteps; ++s) {
-          const uint32_t* lo = reinterpret_cast<const uint32_t*>(q + r_lo * kDim + s * 16);
-          const uint32_t* hi = reinterpret_cast<const uint32_t*>(q + (r_lo + 8) * kDim + s * 16);
-          qa[s][0] = r_lo < a.group ? lo[0] : 0;
-          qa[s][1] = r_lo + 8 < a.group ? hi[0] : 0;
-          qa[s][2] = r_lo < a.group ? lo[4] : 0;
-          qa[s][3] = r_lo + 8 < a.group ? hi[4] : 0;
-        }
-#pragma unroll
-        for (int n = 0; n < kCols; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
-        m0 = m1 = -INFINITY;
-        l0 = l1 = 0.f;
-      }
     }
     if (fill == 0 && seen != 0) {
       float x[kKeyTiles][4];
@@ -1054,7 +1056,8 @@ cudaError_t launch_decode(DecodeArgs a, cudaStream_t s) {
   int64_t unit = (int64_t(a.table.width) << a.table.shift) / S::kTileKeys + 1;
   if (a.q2k && unit > kTopK * S::kTilesPerBlock) unit = kTopK * S::kTilesPerBlock;
   const int64_t units = int64_t(a.table.rows) * a.kv_heads;
-  if (units * kClusterCtas <= a.slots && unit <= kClusterCtas * kClusterTiles) {
+  if (units * kClusterCtas <= a.slots && unit > kClusterCtas &&
+      unit <= kClusterCtas * kClusterTiles) {
     auto kernel = k_paged_decode<T, kDim, true>;
     static std::atomic<uint64_t> done{0};
     cudaError_t e = allow_smem(kernel, S::kSmem, done);

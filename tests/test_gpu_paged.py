@@ -616,6 +616,34 @@ def test_decode_on_another_stream_and_into_given_tensors():
     assert got[0] is o and torch.equal(o, want[0]) and torch.equal(lse, want[1])
 
 
+def test_calls_at_the_same_time_on_two_streams():
+    """Two batches, each on its own stream with its own workspace, over and over
+    (long enough for the short runs, so that both take CTAs at once)."""
+    rng = np.random.default_rng(18)
+    jobs = []
+    for i, (rows, n) in enumerate(((40, 9000), (3, 120000))):
+        gen = _gen(180 + i)
+        kc, vc = (_pool(gen, 64, 128, 4, 128, BF) for _ in range(2))
+        cache = api.PagedCache(kc, vc)
+        lens = rng.integers(n // 2, n, rows)
+        args = (cache, _randn(gen, (rows, 64, 128), BF),
+                _i32(rng.integers(0, 64, (rows, -(-n // 128)))), _i32(lens), 0.09)
+        want = api.msa_paged_decode(*args)
+        ws = torch.empty(api.paged_decode_workspace_bytes(cache, rows, 64), dtype=torch.uint8,
+                         device=DEV)
+        jobs.append((cache, args, want, ws, torch.cuda.Stream(), []))
+    torch.cuda.synchronize()
+    for _ in range(12):
+        for cache, args, want, ws, stream, got in jobs:
+            with torch.cuda.stream(stream):
+                got.append(api.msa_paged_decode(*args, workspace=ws))
+    torch.cuda.synchronize()
+    for cache, args, want, ws, stream, got in jobs:
+        assert api.msa_paged_read_status(cache) == 0
+        for o, lse in got:
+            assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
 def test_binding_refuses_mismatches():
     gen = _gen(17)
     kc, vc = (_pool(gen, 4, 16, 2, 64, BF) for _ in range(2))
