@@ -85,9 +85,9 @@ constexpr int kTailFrom = 64;   // in calls of so many tiles a CTA and more
 constexpr int kMaxSlots = 160 * 2;
 constexpr int kMaxGrid = kMaxSlots * 2;
 
-// Few units (32 at 8 CTAs each fill the chip) that are not long: a cluster of
-// CTAs takes each, and no second kernel is needed.
-constexpr int kClusterCtas = 8;
+// Few units that are not long: a cluster of CTAs takes each, and no second
+// kernel is needed.
+constexpr int kMaxCluster = 8;
 constexpr int kClusterTiles = 8;  // of a CTA at most, by the room in the table
 
 struct DecodeArgs {
@@ -101,6 +101,7 @@ struct DecodeArgs {
   float scale_log2;    // scale * log2(e)
   int32_t kv_heads, group;
   int32_t slots;       // first runs
+  int32_t cluster;     // CTAs of a unit, where units are not dealt out in runs
   int32_t* rec;        // [grid]: 1 + the unit that the run starts inside of; 0: it starts a unit
   float* part_ml;      // [2 grid][2][16]: m, l
   float* part_o;       // [2 grid][16][dim]
@@ -605,12 +606,13 @@ __global__ void __launch_bounds__(kDecThreads, 2) k_paged_decode(const DecodeArg
   grid_dep_release();
   bool tail = false;
   if constexpr (kCluster) {
-    const int rank = blockIdx.x % kClusterCtas;
-    const int32_t unit = blockIdx.x / kClusterCtas;
+    const int rank = blockIdx.x % a.cluster;
+    const int32_t unit = blockIdx.x / a.cluster;
     const int32_t row = unit / a.kv_heads, n = a.kv_len[row], len = checked_len(a, n);
     if (n != len && tid == 0) raise_paged(a.table.status, MSA_ERR_BAD_PAGE);
     const int32_t tiles = unit_tiles<kDim>(len, a.q2k != nullptr);
-    const int32_t i0 = tiles * rank / kClusterCtas, i1 = tiles * (rank + 1) / kClusterCtas;
+    const int32_t i0 = int32_t(int64_t(tiles) * rank / a.cluster);
+    const int32_t i1 = int32_t(int64_t(tiles) * (rank + 1) / a.cluster);
     if (lane == 0) next[warp] = NextRun{0, row, unit % a.kv_heads, len, tiles, i0, i1 - i0};
     __syncwarp();
   } else {
@@ -866,40 +868,42 @@ __global__ void __launch_bounds__(kDecThreads, 2) k_paged_decode(const DecodeArg
       }
     }
     cluster.sync();
-    constexpr int kHeads = kGroup / kClusterCtas;       // of a CTA
-    constexpr int kPer = kHeads * kDim / kDecThreads;   // channels of a thread
-    const int h = int(cluster.block_rank()) * kHeads + tid / (kDecThreads / kHeads);
-    const int ch = tid % (kDecThreads / kHeads) * kPer;
-    float pm[kClusterCtas], pl[kClusterCtas], po[kClusterCtas][kPer];
-    float M = -INFINITY;
+    const int heads = kGroup / a.cluster, items = heads * (kDim / 4);
+    for (int it = tid; it < items; it += kDecThreads) {
+      const int h = int(cluster.block_rank()) * heads + it / (kDim / 4);
+      const int ch = it % (kDim / 4) * 4;
+      float pm[kMaxCluster], pl[kMaxCluster], M = -INFINITY;
+      float4 po[kMaxCluster];
 #pragma unroll
-    for (int c = 0; c < kClusterCtas; ++c) {
-      pm[c] = *cluster.map_shared_rank(&state_ml[0][h], c);
-      pl[c] = *cluster.map_shared_rank(&state_ml[1][h], c);
-      const float* o = cluster.map_shared_rank(state + h * kDim + ch, c);
-#pragma unroll
-      for (int e = 0; e < kPer; ++e) po[c][e] = o[e];
-      M = fmaxf(M, pm[c]);
-    }
-    float l = 0.f, o[kPer] = {};
-#pragma unroll
-    for (int c = 0; c < kClusterCtas; ++c) {
-      const float f = pm[c] == -INFINITY ? 0.f : fast_exp2(pm[c] - M);
-      l += pl[c] * f;
-#pragma unroll
-      for (int e = 0; e < kPer; ++e) o[e] += po[c][e] * f;
-    }
-    if (h < a.group) {
-      const int64_t out = int64_t(blockIdx.x / kClusterCtas) * a.group + h;
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      T* dst = static_cast<T*>(a.o) + out * kDim + ch;
-      if constexpr (kPer == 2) {
-        *reinterpret_cast<uint32_t*>(dst) = Pair<T>::pack(o[0] * inv, o[1] * inv);
-      } else {
-        const uint32_t w = Pair<T>::pack(o[0] * inv, 0.f);
-        *reinterpret_cast<uint16_t*>(dst) = uint16_t(w);
+      for (int c = 0; c < kMaxCluster; ++c) {
+        if (c < a.cluster) {
+          pm[c] = *cluster.map_shared_rank(&state_ml[0][h], c);
+          pl[c] = *cluster.map_shared_rank(&state_ml[1][h], c);
+          po[c] = *reinterpret_cast<const float4*>(
+              cluster.map_shared_rank(state + h * kDim + ch, c));
+          M = fmaxf(M, pm[c]);
+        }
       }
-      if (ch == 0) a.lse[out] = l == 0.f ? -INFINITY : kLn2 * (M + log2f(l));
+      float l = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int c = 0; c < kMaxCluster; ++c) {
+        if (c < a.cluster) {
+          const float f = pm[c] == -INFINITY ? 0.f : fast_exp2(pm[c] - M);
+          l += pl[c] * f;
+          o.x += po[c].x * f;
+          o.y += po[c].y * f;
+          o.z += po[c].z * f;
+          o.w += po[c].w * f;
+        }
+      }
+      if (h < a.group) {
+        const int64_t out = int64_t(blockIdx.x / a.cluster) * a.group + h;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        *reinterpret_cast<uint2*>(static_cast<T*>(a.o) + out * kDim + ch) =
+            make_uint2(Pair<T>::pack(o.x * inv, o.y * inv), Pair<T>::pack(o.z * inv, o.w * inv));
+        if (ch == 0) a.lse[out] = l == 0.f ? -INFINITY : kLn2 * (M + log2f(l));
+      }
     }
     cluster.sync();  // nobody reads this CTA's state any more
   }
@@ -1047,6 +1051,33 @@ size_t decode_workspace(int32_t dim) {
          sizeof(float) * 2 * kMaxGrid * (2 * kGroup + kGroup * size_t(dim));
 }
 
+// Clusters of this kernel that fit on the chip at once (GPCs of unlike size
+// leave SMs over), asked for once a device and size.
+template <typename T, int kDim>
+int cluster_room(void (*kernel)(DecodeArgs), int cluster) {
+  constexpr int kDevices = 16, kSizes = 4;
+  static std::atomic<int> known[kDevices][kSizes];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  std::atomic<int>* slot = dev < kDevices ? &known[dev][log2_of(cluster)] : nullptr;
+  if (slot && slot->load() > 0) return slot->load() - 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(cluster));
+  cfg.blockDim = dim3(kDecThreads);
+  cfg.dynamicSmemBytes = DecodeShape<kDim>::kSmem;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = unsigned(cluster);
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) return 0;
+  if (slot) slot->store(n + 1);
+  return n;
+}
+
 template <typename T, int kDim>
 cudaError_t launch_decode(DecodeArgs a, cudaStream_t s) {
   using S = DecodeShape<kDim>;
@@ -1056,21 +1087,35 @@ cudaError_t launch_decode(DecodeArgs a, cudaStream_t s) {
   int64_t unit = (int64_t(a.table.width) << a.table.shift) / S::kTileKeys + 1;
   if (a.q2k && unit > kTopK * S::kTilesPerBlock) unit = kTopK * S::kTilesPerBlock;
   const int64_t units = int64_t(a.table.rows) * a.kv_heads;
-  if (units * kClusterCtas <= a.slots && unit > kClusterCtas &&
-      unit <= kClusterCtas * kClusterTiles) {
-    auto kernel = k_paged_decode<T, kDim, true>;
-    static std::atomic<uint64_t> done{0};
-    cudaError_t e = allow_smem(kernel, S::kSmem, done);
-    if (e != cudaSuccess) return e;
+  // Clusters: as many CTAs a unit as the chip has room for at once.  Blocks make
+  // units of like length; units of all keys may differ, so those must be short.
+  // Whole units for CTAs pay only if they nearly fill the chip (64 heads on 4,
+  // 128 channels, selected blocks, with clusters / with runs and a join: 16 rows,
+  // clusters of 4, 19.2 / 23.6 us; 32 rows, of 2, 29.8 / 34.0; 76 rows, of 1,
+  // 56 / 60; but 48 rows, of 1, 49 / 44).  Clusters of 8 near the room there is
+  // get in one another's way (9 rows: 17.8 us, of 4 15.7).
+  auto clustered = k_paged_decode<T, kDim, true>;
+  static std::atomic<uint64_t> done_c{0};
+  cudaError_t e = allow_smem(clustered, S::kSmem, done_c);
+  if (e != cudaSuccess) return e;
+  int cluster = kMaxCluster;
+  while (cluster > 1 &&
+         (units * cluster * 8 > a.slots * (cluster == kMaxCluster ? 7 : 8) ||
+          units > cluster_room<T, kDim>(clustered, cluster)))
+    cluster /= 2;
+  const bool fits = cluster > 1 || (units <= a.slots && units * 4 >= a.slots * 3);
+  if (fits && unit > cluster &&
+      unit <= cluster * (a.q2k ? kTopK * S::kTilesPerBlock : kClusterTiles)) {
+    a.cluster = cluster;
     launch_begin("paged_decode", s);
-    e = launch_cluster(kernel, dim3(unsigned(units * kClusterCtas)), dim3(kDecThreads), S::kSmem,
-                       kClusterCtas, s, a);
+    e = launch_cluster(clustered, dim3(unsigned(units * cluster)), dim3(kDecThreads), S::kSmem,
+                       unsigned(cluster), s, a);
     launch_end("paged_decode", s);
     return e;
   }
   auto kernel = k_paged_decode<T, kDim, false>;
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = allow_smem(kernel, S::kSmem, done);
+  e = allow_smem(kernel, S::kSmem, done);
   if (e != cudaSuccess) return e;
   // Short runs only where there can be enough tiles for them.
   const int grid =
