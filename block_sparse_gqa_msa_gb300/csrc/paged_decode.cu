@@ -8,10 +8,11 @@
 //   O' = O 2^(m-m') + 2^(x-m') V,
 // and two such states join as M = max(m1, m2), l = l1 2^(m1-M) + l2 2^(m2-M),
 // O likewise; at the end O / l and lse = ln2 (m + log2 l).  m, l, O are 32
-// bits throughout.  The weights 2^(x-m') <= 1 are rounded to the cache's type
-// for the matrix product with V: one rounding of half a step relative to each
-// weight, independent from key to key, so it stays below the one rounding of
-// the output that follows.
+// bits throughout.  The weights 2^(x-m') <= 1 enter the product with V as the
+// sum of two numbers of the cache's type, the second what rounding to the
+// first leaves over: with one number O was 0.0021 off (relative, bf16, of
+// which the output's own rounding is 0.0017), with two 0.0017, and the second
+// product costs 1 % of the time.
 //
 // What bounds it.  Each key and value is used for 16 query heads at most:
 // 4 * 16 * D flop on 4 * D bytes, 16 flop a byte, so HBM is the bound (at 6.8
@@ -42,11 +43,16 @@
 // (192 KB) the same calls took 3 % longer, the requests being in each other's
 // way.
 //
-// Measured (bf16, 64 heads on 4, pages of 128 tokens): 9 rows of 65536 to
-// 131072 tokens, all keys, 1.85 GB: 271 to 279 us, 6.6 to 6.8 TB/s, as fast as
-// a plain copy; 285 without the short runs.  128 rows of 500 to 16384 tokens,
-// selected blocks, 508 MB: 91 us, 5.6 TB/s (units of 32 tiles: the chip's
-// start, 6 us, and the ends of runs and units weigh more).
+// Measured (bf16, 64 heads on 4, 128 channels): 9 rows of 65536 to 131072
+// tokens, all keys, 1.85 GB: 270 to 279 us, 6.6 to 6.8 TB/s, as fast as a
+// plain copy (285 without the short runs; 277 or less with head-major pages).
+// 128 rows of 500 to 16384 tokens, selected blocks, 508 MB: 91 us, 5.6 TB/s:
+// the first bytes come after 4 us, the runs end up to 8 % apart, the join
+// takes 5 us.  77 rows of up to 12000 tokens, 24 heads on 8 of 64 channels,
+// 950 MB: 151 to 165 us, 5.8 to 6.3 TB/s: a head's 128 bytes a token are read
+// alone (head-major pages: 147).  One row: 7 us for 1000 tokens, 9 for 16
+// blocks; dependent loads (length, slots, page, keys) and one join in the
+// cluster are the time.
 #include <cooperative_groups.h>
 
 #include "paged.cuh"

@@ -12,10 +12,18 @@
 //                 loads in flight, writes the new ones to the cache and sums
 //                 them in order.  Blocks are numbered over the rows and dealt
 //                 out in turn.
-// k_paged_select  one cluster of CTAs a (row, index head): a lane scores a
-//                 block, a warp keeps the best of its blocks in a list sorted
-//                 across its lanes, and the lists are merged through shared
-//                 memory, then through the cluster's.
+//                 20494 prompt tokens of 4 x 128 channels (43 MB, 6.3 us at the
+//                 copy rate): 13.4 us (44 with the block's keys summed as they
+//                 came); 96 rows' next tokens: 5 us, four dependent loads.
+// k_paged_select  one cluster of CTAs a (row, index head): a warp brings the
+//                 means of 32 blocks to shared memory 32 channels at a time
+//                 (rows coalesced), a lane scores a block, and the warp keeps
+//                 the best in a list sorted across its lanes; the lists are
+//                 merged through shared memory, then through the cluster's.
+//                 64 rows of up to 1024 blocks of 4 x 128 channels (68 MB, 10
+//                 us): 21.8 us (62 with each lane reading its block's row from
+//                 memory); the longest rows, two CTAs each, take most of it.
+//                 One row of 1024 blocks: 5.1 us.
 #include <cooperative_groups.h>
 
 #include <utility>

@@ -380,9 +380,11 @@ msa_status msa_select_blocks(const void* iq, const void* ik, int64_t T, int32_t 
  * never cleared by the library, and no call does less because it is set.
  *
  * Calls are asynchronous on the stream, allocate nothing and can be captured
- * into a CUDA graph; sizes that change from step to step (positions, lengths)
- * are read on the device.  Inputs and outputs must not overlap except where a
- * call says so.
+ * into a CUDA graph (make one such call on the device before, which loads the
+ * kernels); sizes that change from step to step (positions, lengths) are read
+ * on the device.  Inputs and outputs must not overlap except where a call says
+ * so.  Keys, values and queries that are used are finite; what lies in a page
+ * where no token has been written may be anything.
  */
 typedef enum msa_dtype { MSA_BF16 = 0, MSA_F16 = 1 } msa_dtype;
 
@@ -516,8 +518,12 @@ msa_status msa_paged_decode_workspace_bytes(const msa_paged_cache* cache, int32_
  *   o       [rows][q_heads][head_dim] contiguous, of the cache's type
  *   lse     fp32 [rows][q_heads] natural log
  *   workspace  device, 16-byte aligned, >= msa_paged_decode_workspace_bytes;
- *           needs no initialisation; calls that may overlap in time need one
- *           each
+ *           needs no initialisation; calls that may overlap in time (on two
+ *           streams, in graphs replayed side by side) need one each
+ * Results are the same from call to call on one kind of device: how the keys
+ * are split depends on the lengths and sizes alone.
+ * MSA_ERR_TIMEOUT in the status word: a bounded wait of the kernel gave up, and
+ * outputs of that call are missing.
  * A row that sees no key (kv_len 0, no slot used) gets O = 0, LSE = -inf; so
  * does a row whose length is bad.  Keys in a bad page are left out.  What
  * lies in a page past a row's length does not matter, whatever it is.

@@ -489,6 +489,14 @@ def _decode_shared_pages(dt, dim, kv, share, S, lens, sparse, seed):
     args = (cache, q, _i32(table), _i32(lens), scale, None if q2k is None else _i32(q2k))
     o, lse = api.msa_paged_decode(*args)
     again = [api.msa_paged_decode(*args) for _ in range(5)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        replayed = api.msa_paged_decode(*args)
+    for _ in range(3):
+        for x in replayed:
+            x.zero_()
+        graph.replay()
+        again.append([x.clone() for x in replayed])
     torch.cuda.synchronize()
     assert api.msa_paged_read_status(cache) == 0
     for x, y in again:
@@ -642,6 +650,35 @@ def test_calls_at_the_same_time_on_two_streams():
         assert api.msa_paged_read_status(cache) == 0
         for o, lse in got:
             assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
+def test_one_pool_for_keys_and_values_and_a_slice_of_a_table():
+    """k and v as halves of one tensor's pages, heads out of a wider pool, the
+    table a slice of a larger one: same results as with tensors of their own."""
+    rng, gen = np.random.default_rng(19), _gen(19)
+    lens, S = [333, 1, 90], 16
+    pool, table = _pages(rng, lens, S)
+    both = _randn(gen, (pool, 2, S, 6, 128), BF)
+    kc, vc = both[:, 0, :, 1:5], both[:, 1, :, 2:6]
+    big = torch.full((5, table.shape[1] + 9), -7, dtype=torch.int32, device=DEV)
+    t = big[1:4, 4:4 + table.shape[1]]
+    t.copy_(_i32(table))
+    n = _i32(lens)
+    q, k, v = (_randn(gen, (3, h, 128), BF) for h in (64, 4, 4))
+    freq = torch.rand(64, generator=gen, device=DEV)
+    own = api.PagedCache(kc.contiguous(), vc.contiguous())
+    views = api.PagedCache(kc, vc)
+    outside = both.clone()
+    for cache, tab in ((own, _i32(table)), (views, t)):
+        api.msa_paged_append(cache, k, v, tab, _i32([0, 1, 2, 3]), n - 1, inv_freq=freq)
+    torch.cuda.synchronize()
+    assert torch.equal(kc, own.k) and torch.equal(vc, own.v)
+    outside[:, 0, :, 1:5], outside[:, 1, :, 2:6] = kc, vc
+    assert torch.equal(both, outside)
+    for x, y in zip(api.msa_paged_decode(own, q, _i32(table), n, 0.1),
+                    api.msa_paged_decode(views, q, t, n, 0.1)):
+        assert torch.equal(x, y)
+    assert api.msa_paged_read_status(views) == 0
 
 
 def test_binding_refuses_mismatches():
