@@ -21,9 +21,10 @@
 //                 the best in a list sorted across its lanes; the lists are
 //                 merged through shared memory, then through the cluster's.
 //                 64 rows of up to 1024 blocks of 4 x 128 channels (68 MB, 10
-//                 us): 21.8 us (62 with each lane reading its block's row from
-//                 memory); the longest rows, two CTAs each, take most of it.
-//                 One row of 1024 blocks: 5.1 us.
+//                 us): 21.5 us (62 with each lane reading its block's row from
+//                 memory); 3 us before the first means come, the longest rows,
+//                 two CTAs each, and 3 us of merging are the rest.  One row of
+//                 1024 blocks: 5.1 us.
 #include <cooperative_groups.h>
 
 #include <utility>
@@ -270,26 +271,36 @@ __global__ void __launch_bounds__(kSelWarps * 32) k_paged_select(const SelectArg
     return;
   }
   auto started = cluster.barrier_arrive();
+  const int32_t lo = a.force ? 1 : 0, hi = a.force ? b - 1 : b;
+  const int32_t v_step = C * kSelThreads;
+  int32_t fv = lo + (rank * kSelWarps + warp) * 32;  // first block of the group being fetched
+  // The page of the lane's block in the group from v0 on, as the table has it;
+  // loaded a group ahead.
+  auto last_of = [&](int32_t v) { return min(v * kBlock + kBlock - 1, len - 1); };
+  auto load_page = [&](int32_t v0) {
+    return v0 + lane <= hi
+               ? a.table.pages[int64_t(r) * a.table.stride + (last_of(v0 + lane) >> a.table.shift)]
+               : 0;
+  };
+  int32_t next_page = load_page(fv);
   for (int c = threadIdx.x; c < a.dim; c += kSelThreads)
     sq[c] = __bfloat162float(a.iq[(int64_t(r) * a.heads + h) * a.dim + c]);
-  __syncthreads();
-  const int32_t lo = a.force ? 1 : 0, hi = a.force ? b - 1 : b;
   // The warp's slabs in order: for every group of 32 blocks, its channels 32
   // at a time.  fetch runs kSlabs - 1 slabs ahead of the sums.
   const uint32_t ring = uint32_t(__cvta_generic_to_shared(slabs)) + warp * (kSlabs * kSlabBytes);
   const int per = (a.dim + 31) / 32;
-  const int32_t v_step = C * kSelThreads;
-  int32_t fv = lo + (rank * kSelWarps + warp) * 32;  // first block of the group being fetched
-  int fc = 0;                                        // its next slab
-  int64_t row = -1;                                  // the lane's block in it: row of the means
+  int fc = 0;        // the group's next slab
+  int64_t row = -1;  // the lane's block in it: row of the means
   auto locate = [&]() {
-    const int32_t v = fv + lane;
+    const int32_t page = next_page;
     row = -1;
-    if (v <= hi) {
-      const int32_t last = min(v * kBlock + kBlock - 1, len - 1);
-      const int32_t page = page_of(a.table, r, last);
-      if (page >= 0) row = mean_slot(a.table, page, last) * a.heads + h;
+    if (fv + lane <= hi) {
+      if (page >= 0 && page < a.table.num_pages)
+        row = mean_slot(a.table, page, last_of(fv + lane)) * a.heads + h;
+      else
+        raise_paged(a.table.status, MSA_ERR_BAD_PAGE);
     }
+    next_page = load_page(fv + v_step);
   };
   if (fv <= hi) locate();
   auto fetch = [&](int stage) {
@@ -319,6 +330,7 @@ __global__ void __launch_bounds__(kSelWarps * 32) k_paged_select(const SelectArg
     fetch(i);
     asm volatile("cp.async.commit_group;" ::: "memory");
   }
+  __syncthreads();  // the query
   while (gv <= hi) {
     float acc = 0.f;
     for (int c = 0; c < per; ++c) {
