@@ -354,12 +354,6 @@ __device__ __forceinline__ void find_run(const DecodeArgs& a, const Prefix& pref
     *next = NextRun{c, p.row, h, p.len, p.tiles, lo - p.start - h * p.tiles, n};
   __syncwarp();
 }
-// The same for a run taken later.  Out of line: the loop over the tiles stays short.
-template <int kDim>
-__device__ __forceinline__ void find_taken_run(const DecodeArgs& a, const Prefix& prefix, int32_t c,
-                                            NextRun* next) {
-  find_run<kDim>(a, prefix, Deal(prefix.total, a.slots, gridDim.x), c, next);
-}
 // The answer to the CTA's request number n (1, 2, ..): the run taken, or -1.
 __device__ __forceinline__ int32_t await_run(const DecodeArgs& a, Queue* ctas, uint32_t n) {
   const int b = n % kAnswers;
@@ -371,7 +365,7 @@ __device__ __forceinline__ int32_t await_run(const DecodeArgs& a, Queue* ctas, u
   fence_proxy_async_smem();  // the place is written again by a later request
   return __shfl_sync(0xffffffffu, c, 0);
 }
-constexpr int kSegQueue = 8;  // the fetch is at most 4 tiles, so segments, ahead
+constexpr int kSegQueue = 8;  // the fetch is three tiles, so at most as many segments, ahead
 // Tiles before a run's end at which the next one is asked for, and at which its
 // place is looked up: each wait on the way is hidden by the tiles in flight.
 constexpr int kAskAt = 6;
@@ -505,7 +499,7 @@ struct Fetch {
       more = found = c >= 0;
       if (found) {
         ++n_run;
-        find_taken_run<kDim>(a, prefix, c, next);
+        find_run<kDim>(a, prefix, Deal(prefix.total, a.slots, gridDim.x), c, next);
       }
     }
   }
@@ -863,7 +857,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) k_paged_decode(const DecodeArg
   }
   cp_async_wait<0>();
   if constexpr (kCluster) {
-    // Every CTA joins the parts of its share of the heads, a thread a few channels.
+    // Every CTA joins the parts of its share of the results, a thread 4 channels.
     namespace cg = cooperative_groups;
     cg::cluster_group cluster = cg::this_cluster();
     if (idle) {
@@ -874,10 +868,9 @@ __global__ void __launch_bounds__(kDecThreads, 2) k_paged_decode(const DecodeArg
       }
     }
     cluster.sync();
-    const int heads = kGroup / a.cluster, items = heads * (kDim / 4);
-    for (int it = tid; it < items; it += kDecThreads) {
-      const int h = int(cluster.block_rank()) * heads + it / (kDim / 4);
-      const int ch = it % (kDim / 4) * 4;
+    for (int it = int(cluster.block_rank()) * kDecThreads + tid; it < kGroup * (kDim / 4);
+         it += a.cluster * kDecThreads) {
+      const int h = it / (kDim / 4), ch = it % (kDim / 4) * 4;
       float pm[kMaxCluster], pl[kMaxCluster], M = -INFINITY;
       float4 po[kMaxCluster];
 #pragma unroll
@@ -1061,11 +1054,11 @@ size_t decode_workspace(int32_t dim) {
 // leave SMs over), asked for once a device and size.
 template <typename T, int kDim>
 int cluster_room(void (*kernel)(DecodeArgs), int cluster) {
-  constexpr int kDevices = 16, kSizes = 4;
-  static std::atomic<int> known[kDevices][kSizes];
+  constexpr int kDevices = 16;
+  static std::atomic<int> known[kDevices][kMaxCluster];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  std::atomic<int>* slot = dev < kDevices ? &known[dev][log2_of(cluster)] : nullptr;
+  std::atomic<int>* slot = dev < kDevices ? &known[dev][cluster - 1] : nullptr;
   if (slot && slot->load() > 0) return slot->load() - 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(cluster));
@@ -1093,13 +1086,14 @@ cudaError_t launch_decode(DecodeArgs a, cudaStream_t s) {
   int64_t unit = (int64_t(a.table.width) << a.table.shift) / S::kTileKeys + 1;
   if (a.q2k && unit > kTopK * S::kTilesPerBlock) unit = kTopK * S::kTilesPerBlock;
   const int64_t units = int64_t(a.table.rows) * a.kv_heads;
-  // Clusters: as many CTAs a unit as the chip has room for at once.  Blocks make
-  // units of like length; units of all keys may differ, so those must be short.
-  // Whole units for CTAs pay only if they nearly fill the chip (64 heads on 4,
-  // 128 channels, selected blocks, with clusters / with runs and a join: 16 rows,
-  // clusters of 4, 19.2 / 23.6 us; 32 rows, of 2, 29.8 / 34.0; 76 rows, of 1,
-  // 56 / 60; but 48 rows, of 1, 49 / 44).  Clusters of 8 near the room there is
-  // get in one another's way (9 rows: 17.8 us, of 4 15.7).
+  // Clusters: as many CTAs a unit as the chip has room for at once, 8 at most.
+  // Blocks make units of like length; units of all keys may differ, so those
+  // must be short.  Whole units for CTAs pay only if they nearly fill the chip,
+  // and a second wave of clusters never does (64 heads on 4, 128 channels,
+  // selected blocks, with clusters / with runs and a join: 9 rows, clusters of 7,
+  // 13.9 / 19 us; 24 rows, of 3, 23.7 / 28.4; 32 rows, of 2, 29.8 / 34.0; 76 rows,
+  // of 1, 56 / 60; but 48 rows, of 1, 49 / 44, and 128 rows, of 1, 100 / 93).
+  // Clusters of 8 near the room there is get in one another's way.
   auto clustered = k_paged_decode<T, kDim, true>;
   static std::atomic<uint64_t> done_c{0};
   cudaError_t e = allow_smem(clustered, S::kSmem, done_c);
@@ -1108,7 +1102,7 @@ cudaError_t launch_decode(DecodeArgs a, cudaStream_t s) {
   while (cluster > 1 &&
          (units * cluster * 8 > a.slots * (cluster == kMaxCluster ? 7 : 8) ||
           units > cluster_room<T, kDim>(clustered, cluster)))
-    cluster /= 2;
+    --cluster;
   const bool fits = cluster > 1 || (units <= a.slots && units * 4 >= a.slots * 3);
   if (fits && unit > cluster &&
       unit <= cluster * (a.q2k ? kTopK * S::kTilesPerBlock : kClusterTiles)) {

@@ -13,8 +13,8 @@
 //                 them in order.  Blocks are numbered over the rows and dealt
 //                 out in turn.
 //                 20494 prompt tokens of 4 x 128 channels (43 MB, 6.3 us at the
-//                 copy rate): 13.4 us (44 with the block's keys summed as they
-//                 came); 96 rows' next tokens: 5 us, four dependent loads.
+//                 copy rate): 11.5 us (44 with the block's keys summed as they
+//                 came, 13.4 with them staged in registers, three CTAs an SM); 96 rows' next tokens: 5 us, four dependent loads.
 // k_paged_select  one cluster of CTAs a (row, index head): a warp brings the
 //                 means of 32 blocks to shared memory 32 channels at a time
 //                 (rows coalesced), a lane scores a block, and the warp keeps
@@ -105,26 +105,28 @@ __device__ __forceinline__ void index_block(const IndexArgs& a, IndexSmem& sm) {
     const __nv_bfloat16* in = a.ik + b.t * a.ik_stride + ch;
     constexpr int kStep = kIdxThreads / kIdxChunks;
     constexpr int kEach = kBlock / kStep;
-    uint4 w[kEach];
-    uint4* at[kEach];
+    const int j0 = int(threadIdx.x / kIdxChunks);
+    auto place = [&](int j) {
+      const int64_t p = first + j;
+      return col + sm.pages[(p >> a.table.shift) - i0] * a.keys.page + (p & mask) * a.keys.token;
+    };
 #pragma unroll
     for (int u = 0; u < kEach; ++u) {
-      const int j = u * kStep + int(threadIdx.x / kIdxChunks);
+      const int j = j0 + u * kStep;
       if (j < n) {
-        const int64_t p = first + j;
-        at[u] = reinterpret_cast<uint4*>(
-            col + sm.pages[(p >> a.table.shift) - i0] * a.keys.page + (p & mask) * a.keys.token);
-        w[u] = j < n_old ? *at[u]
-                         : *reinterpret_cast<const uint4*>(in + int64_t(j - n_old) * a.ik_stride);
+        const __nv_bfloat16* src = j < n_old ? place(j) : in + int64_t(j - n_old) * a.ik_stride;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(uint32_t(
+                         __cvta_generic_to_shared(&sm.rows[j][threadIdx.x % kIdxChunks]))),
+                     "l"(src)
+                     : "memory");
       }
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
 #pragma unroll
     for (int u = 0; u < kEach; ++u) {
-      const int j = u * kStep + int(threadIdx.x / kIdxChunks);
-      if (j < n) {
-        sm.rows[j][threadIdx.x % kIdxChunks] = w[u];
-        if (j >= n_old) *at[u] = w[u];
-      }
+      const int j = j0 + u * kStep;
+      if (j >= n_old && j < n)
+        *reinterpret_cast<uint4*>(place(j)) = sm.rows[j][threadIdx.x % kIdxChunks];
     }
   }
   __syncthreads();
