@@ -1072,7 +1072,10 @@ int cluster_room(void (*kernel)(DecodeArgs), int cluster) {
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) return 0;
+  if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+    cudaGetLastError();  // no room known: no clusters
+    return 0;
+  }
   if (slot) slot->store(n + 1);
   return n;
 }
