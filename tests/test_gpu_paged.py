@@ -454,6 +454,12 @@ def test_decode_many_rows():
     rng = np.random.default_rng(8)
     _decode_case(BF, 64, 2, 4, 16, rng.integers(0, 200, 700).tolist(), False, seed=8)
     _decode_case(BF, 128, 4, 16, 32, rng.integers(0, 700, 90).tolist(), True, seed=9)
+    # 64 channels: two heads at once, and each alone (an odd number, pages by head, blocks)
+    lens = rng.integers(0, 300, 200).tolist()
+    _decode_case(FP, 64, 4, 16, 32, lens, False, seed=40)
+    _decode_case(FP, 64, 3, 5, 32, lens, False, seed=41)
+    _decode_case(BF, 64, 2, 9, 64, lens, False, seed=42, head_major=True)
+    _decode_case(BF, 64, 4, 3, 16, lens, True, seed=43)
 
 
 def test_decode_one_long_row_split_over_all_ctas():
