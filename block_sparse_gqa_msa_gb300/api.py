@@ -155,10 +155,14 @@ def _check(code: int, what: str):
         raise MSAError(code, what)
 
 
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _stream(stream) -> int:
     if stream is None:
         # the current stream's handle without a Stream object (4 us of a call)
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        return _raw_stream(_current_device())
     return stream.cuda_stream
 
 
@@ -531,18 +535,18 @@ class PagedIndex:
 
 
 def _current(device):
-    if device.index != torch._C._cuda_getDevice():
+    if device.index != _current_device():
         raise ValueError(f"the cache is on {device}, the current device is "
                          f"cuda:{torch.cuda.current_device()}")
 
 
 def _arg(t, name: str, dtype, shape, device) -> int:
     """Address of a contiguous tensor of this type and shape on the cache's device."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
             and t.device == device and t.is_contiguous()):
-        _need(t, name, dtype, shape)
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
-    return t.data_ptr()
+        return t.data_ptr()
+    _need(t, name, dtype, shape)
+    raise ValueError(f"{name} must be on {device}, got {t.device}")
 
 
 def _table(page_table: torch.Tensor, device) -> MsaPageTableStruct:
