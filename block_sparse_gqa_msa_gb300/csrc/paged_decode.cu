@@ -95,6 +95,7 @@ constexpr int kMaxGrid = kMaxSlots * 2;
 // kernel is needed.
 constexpr int kMaxCluster = 8;
 constexpr int kClusterTiles = 8;  // of a CTA at most, by the room in the table
+constexpr int kSmallUnit = 4;     // tiles of a unit that is not worth dividing
 
 struct DecodeArgs {
   const void* q;
@@ -163,19 +164,13 @@ __device__ __forceinline__ void mma16816<__half>(float (&d)[4], const uint32_t (
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Tiles of one unit of a row of len keys (at least one, so that rows without
-// keys are written too).
+// Tiles of one unit of a row of len keys, an upper bound where blocks are
+// selected (at least one, so that rows without keys are written too).
 template <int kDim>
 __device__ __forceinline__ int32_t unit_tiles(int32_t len, bool sparse) {
   using S = DecodeShape<kDim>;
-  int32_t n;
-  if (sparse) {
-    const int32_t nb = int32_t((int64_t(len) + kBlock - 1) / kBlock);
-    n = min(nb, kTopK) * S::kTilesPerBlock;
-  } else {
-    n = int32_t((int64_t(len) + S::kTileKeys - 1) / S::kTileKeys);
-  }
-  return max(n, 1);
+  if (sparse && len > kTopK * kBlock) return kTopK * S::kTilesPerBlock;
+  return max(int32_t((int64_t(len) + S::kTileKeys - 1) / S::kTileKeys), 1);
 }
 
 // How n tiles are dealt out to runs: by the numbers alone.  The first runs are
@@ -415,7 +410,8 @@ struct Fetch {
           lane * 64));
   }
   // Enters the unit (row, head) at tile i: its blocks (the distinct valid
-  // slots, in slot order), its place in the queue, and a look ahead.
+  // slots, in slot order, but the row's last block, which may be short, at the
+  // end), its place in the queue, and a look ahead.
   __device__ __forceinline__ void enter(int32_t opens) {
     if (a.q2k) {
       const int32_t nb = int32_t((int64_t(len) + kBlock - 1) / kBlock);
@@ -425,9 +421,11 @@ struct Fetch {
       const uint32_t same = __match_any_sync(0xffffffffu, ok ? v : -1 - lane);
       const bool keep = ok && (__ffs(same) - 1) == lane;
       const uint32_t m = __ballot_sync(0xffffffffu, keep);
+      const uint32_t end = __ballot_sync(0xffffffffu, keep && v == nb - 1);
       n_blocks = __popc(m);
       __syncwarp();  // the list before is read
-      if (keep) blocks[__popc(m & ((1u << lane) - 1))] = v;
+      if (keep)
+        blocks[(end >> lane) & 1 ? n_blocks - 1 : __popc(m & ~end & ((1u << lane) - 1))] = v;
     }
     if (lane == 0) queue[n_seg % kSegQueue] = Segment{run, row, head, i, i1, tiles, opens};
     ++n_seg;
@@ -1103,12 +1101,13 @@ cudaError_t launch_decode(DecodeArgs a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   int cluster = kMaxCluster;
   while (cluster > 1 &&
-         (units * cluster * 8 > a.slots * (cluster == kMaxCluster ? 7 : 8) ||
+         (unit < 2 * cluster ||
+          units * cluster * 8 > a.slots * (cluster == kMaxCluster ? 7 : 8) ||
           units > cluster_room<T, kDim>(clustered, cluster)))
     --cluster;
-  const bool fits = cluster > 1 || (units <= a.slots && units * 4 >= a.slots * 3);
-  if (fits && unit > cluster &&
-      unit <= cluster * (a.q2k ? kTopK * S::kTilesPerBlock : kClusterTiles)) {
+  const bool fits = cluster > 1 || (units <= a.slots && (unit <= kSmallUnit ||
+                                                         units * 4 >= a.slots * 3));
+  if (fits && unit <= cluster * (a.q2k ? kTopK * S::kTilesPerBlock : kClusterTiles)) {
     a.cluster = cluster;
     launch_begin("paged_decode", s);
     e = launch_cluster(clustered, dim3(unsigned(units * cluster)), dim3(kDecThreads), S::kSmem,
