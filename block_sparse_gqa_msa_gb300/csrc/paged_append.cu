@@ -8,15 +8,17 @@
 // bits, and each result is rounded once to the cache's type.
 //
 // The work is a copy: q, k, v read once, q_out, cache (and k_out) written
-// once.  A token is one CTA: an item is 16 channels (the two halves of 8
-// pairs, or 16 that are copied), every thread loads all its items before it
-// looks for the token's row, position and page and before the angles are
-// formed, so those three dependent loads hide behind the data's.
+// once.  A token is one CTA, or up to six are where they are many and narrow
+// (launch_append).  An item is 16 channels (the two halves of 8 pairs, or 16
+// that are copied); every thread loads all its items before it looks for the
+// token's row, position and page and before the angles are formed, so those
+// three dependent loads hide behind the data's.
 //
 // Measured: 17029 prompt tokens, 64 query heads and 4 key heads of 128 bf16
-// channels, 645 MB: 95 us, 6.8 TB/s, a plain copy's rate.  One token: 2.4 us,
-// 150 tokens with 80 heads (6 MB, 0.9 us at that rate): 3.8 us: the launch and
-// the dependent loads.
+// channels, 645 MB: 95 us, 6.8 TB/s, a plain copy's rate; with 8 query heads
+// and one key head (92 MB) 23.7 us, 38.8 if each token were its own CTA.  One
+// token: 2.4 us, 150 tokens with 80 heads (6 MB, 0.9 us at that rate): 3.8 us:
+// the launch and the dependent loads.
 #include "paged.cuh"
 
 namespace msa {
@@ -24,6 +26,8 @@ namespace {
 
 constexpr int kAppThreads = 192;
 constexpr int kAppItems = 3;  // items a thread holds: 192 x 3 = 64 + 4 + 4 heads of 128 channels
+constexpr int kAppResident = 5;  // CTAs of several tokens (64 registers a thread) that an SM holds
+constexpr int kAppTokens = kAppThreads / 32;  // the most tokens of a CTA: a warp places one
 
 struct AppendArgs {
   const void *q, *k, *v;
@@ -35,7 +39,8 @@ struct AppendArgs {
   const float* inv_freq;
   int64_t T;
   int32_t q_heads, kv_heads, rot;
-  int32_t share;  // items of one CTA (a multiple of its threads)
+  int32_t share;  // items of one CTA (a multiple of its threads), where it has one token
+  int32_t group;  // tokens of one CTA, where it has several
 };
 
 // Sine and cosine of pos * f.  The turns are counted in 64 bits (an exact
@@ -47,14 +52,18 @@ __device__ __forceinline__ float2 turn_of(int64_t pos, float f) {
   return make_float2(c, s);
 }
 
-template <typename T, int kDim, bool kInter>
+template <typename T, int kDim, bool kInter, int kTokens>
 __global__ void __launch_bounds__(kAppThreads) k_paged_append(const AppendArgs a) {
   constexpr int kPer = kDim / 16;  // items of a head
-  __shared__ __align__(16) float cs[kDim / 2], sn[kDim / 2];
+  __shared__ __align__(16) float cs[kTokens][kDim / 2], sn[kTokens][kDim / 2];
+  __shared__ int64_t where[kTokens];  // the token's position
+  __shared__ int32_t where_page[kTokens];
   const int tid = threadIdx.x;
-  const int64_t t = blockIdx.x;
-  const int first = blockIdx.y * a.share;
-  const int items = min((a.q_heads + 2 * a.kv_heads) * kPer, first + a.share);
+  const int each = (a.q_heads + 2 * a.kv_heads) * kPer;  // items of a token
+  const int64_t t0 = kTokens == 1 ? blockIdx.x : int64_t(blockIdx.x) * a.group;
+  const int tokens = kTokens == 1 ? 1 : int(min(int64_t(a.group), a.T - t0));
+  const int first = kTokens == 1 ? blockIdx.y * a.share : 0;
+  const int items = kTokens == 1 ? min(each, first + a.share) : tokens * each;
   grid_dep_wait();
   grid_dep_release();
   if (blockIdx.x == 0 && blockIdx.y == 0)
@@ -67,7 +76,7 @@ __global__ void __launch_bounds__(kAppThreads) k_paged_append(const AppendArgs a
   for (int base = first; base < items; base += kAppThreads * kAppItems) {
     // Items run over the key heads, the value heads, the query heads.
     uint4 x[kAppItems], y[kAppItems];
-    int head[kAppItems], c0[kAppItems], c1[kAppItems];
+    int head[kAppItems], c0[kAppItems], c1[kAppItems], tok[kAppItems];
     bool turn[kAppItems];
 #pragma unroll
     for (int i = 0; i < kAppItems; ++i) {
@@ -76,8 +85,11 @@ __global__ void __launch_bounds__(kAppThreads) k_paged_append(const AppendArgs a
         head[i] = -1;
         continue;
       }
-      head[i] = it / kPer;
-      const int sub = it % kPer;
+      tok[i] = kTokens == 1 ? 0 : it / each;
+      const int own = it - tok[i] * each;
+      head[i] = own / kPer;
+      const int sub = own % kPer;
+      const int64_t t = t0 + tok[i];
       const bool is_v = head[i] >= a.kv_heads && head[i] < 2 * a.kv_heads;
       turn[i] = !is_v && sub * 16 < a.rot;
       // the item's two runs of 8 channels
@@ -98,35 +110,62 @@ __global__ void __launch_bounds__(kAppThreads) k_paged_append(const AppendArgs a
       x[i] = *reinterpret_cast<const uint4*>(src + c0[i]);
       y[i] = *reinterpret_cast<const uint4*>(src + c1[i]);
     }
-    if (!placed) {
+    if (kTokens > 1) {  // one round of the loop: each of the first warps places a token
+      const int w = tid / 32, lane = tid % 32;
+      if (w < tokens) {
+        const int64_t t = t0 + w;
+        const int32_t r = find_row_warp(a.offs, a.table.rows, t);
+        const int32_t o0 = a.offs[r], o1 = a.offs[r + 1];
+        if (t >= o0 && t < o1) {
+          pos = int64_t(a.start[r]) + (t - o0);
+          page = page_of(a.table, r, pos);
+          for (int i = lane; i < half; i += 32) {
+            const float2 turned = turn_of(pos, a.inv_freq[i]);
+            cs[w][i] = turned.x;
+            sn[w][i] = turned.y;
+          }
+        }
+        if (lane == 0) {
+          where[w] = pos;
+          where_page[w] = page;
+        }
+      }
+      __syncthreads();
+    } else if (!placed) {
       placed = true;
-      const int32_t r = find_row_warp(a.offs, a.table.rows, t);
+      const int32_t r = find_row_warp(a.offs, a.table.rows, t0);
       const int32_t o0 = a.offs[r], o1 = a.offs[r + 1];
-      if (t < o0 || t >= o1) return;  // padding: no row owns this token
-      pos = int64_t(a.start[r]) + (t - o0);
+      if (t0 < o0 || t0 >= o1) return;  // padding: no row owns this token
+      pos = int64_t(a.start[r]) + (t0 - o0);
       page = page_of(a.table, r, pos);
       if (page < 0) return;
       if (tid < half) {
         const float2 w = turn_of(pos, a.inv_freq[tid]);
-        cs[tid] = w.x;
-        sn[tid] = w.y;
+        cs[0][tid] = w.x;
+        sn[0][tid] = w.y;
       }
       __syncthreads();
     }
-    const int64_t slot = pos & ((int64_t(1) << a.table.shift) - 1);
 #pragma unroll
     for (int i = 0; i < kAppItems; ++i) {
       if (head[i] < 0) continue;
+      if (kTokens > 1) {
+        pos = where[tok[i]];
+        page = where_page[tok[i]];
+        if (page < 0) continue;  // padding, or no page of the cache
+      }
+      const int64_t t = t0 + tok[i];
+      const int64_t slot = pos & ((int64_t(1) << a.table.shift) - 1);
       if (turn[i]) {
         uint32_t* xw = reinterpret_cast<uint32_t*>(&x[i]);
         uint32_t* yw = reinterpret_cast<uint32_t*>(&y[i]);
         // the item's first pair: channels (p, p + half) or (2 p, 2 p + 1)
         const int p = kInter ? c0[i] / 2 : c0[i];
         float cc[8], ss[8];
-        *reinterpret_cast<float4*>(cc) = *reinterpret_cast<const float4*>(cs + p);
-        *reinterpret_cast<float4*>(cc + 4) = *reinterpret_cast<const float4*>(cs + p + 4);
-        *reinterpret_cast<float4*>(ss) = *reinterpret_cast<const float4*>(sn + p);
-        *reinterpret_cast<float4*>(ss + 4) = *reinterpret_cast<const float4*>(sn + p + 4);
+        *reinterpret_cast<float4*>(cc) = *reinterpret_cast<const float4*>(cs[tok[i]] + p);
+        *reinterpret_cast<float4*>(cc + 4) = *reinterpret_cast<const float4*>(cs[tok[i]] + p + 4);
+        *reinterpret_cast<float4*>(ss) = *reinterpret_cast<const float4*>(sn[tok[i]] + p);
+        *reinterpret_cast<float4*>(ss + 4) = *reinterpret_cast<const float4*>(sn[tok[i]] + p + 4);
         if (kInter) {
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
@@ -177,9 +216,25 @@ cudaError_t launch_append(AppendArgs a, bool inter, cudaStream_t s) {
   if (slices > rounds) slices = rounds;
   const int64_t each = (rounds + slices - 1) / slices;  // rounds of a CTA
   a.share = int32_t(each * kAppThreads);
+  // Many tokens of few heads: as many to a CTA as its items hold, but no more
+  // than bring all the CTAs to the SMs at once (one head of 64 channels: 4015
+  // tokens 10.2 -> 4.7 us, 1000 tokens 4.5 -> 3.2; 3.9 against 4.6 us for 600
+  // tokens of 10 heads of 128 if they were grouped as well).
+  const int64_t wave = int64_t(device_sm_count()) * kAppResident;
+  const int64_t group = std::min<int64_t>(
+      std::min<int64_t>(kAppTokens, kAppThreads * kAppItems / items), (a.T + wave - 1) / wave);
+  if (group > 1) {
+    a.group = int32_t(group);
+    const dim3 grid(unsigned((a.T + group - 1) / group));
+    return inter ? launch_k(true, k_paged_append<T, kDim, true, kAppTokens>, grid,
+                            dim3(kAppThreads), 0, s, a)
+                 : launch_k(true, k_paged_append<T, kDim, false, kAppTokens>, grid,
+                            dim3(kAppThreads), 0, s, a);
+  }
   const dim3 grid(unsigned(a.T), unsigned((rounds + each - 1) / each));
-  return inter ? launch_k(true, k_paged_append<T, kDim, true>, grid, dim3(kAppThreads), 0, s, a)
-               : launch_k(true, k_paged_append<T, kDim, false>, grid, dim3(kAppThreads), 0, s, a);
+  return inter
+             ? launch_k(true, k_paged_append<T, kDim, true, 1>, grid, dim3(kAppThreads), 0, s, a)
+             : launch_k(true, k_paged_append<T, kDim, false, 1>, grid, dim3(kAppThreads), 0, s, a);
 }
 
 }  // namespace

@@ -114,10 +114,6 @@ struct DecodeArgs {
   float* part_o;       // [2 grid][16][dim]
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src)
-               : "memory");
-}
 __device__ __forceinline__ void cp_async16_if(uint32_t dst, const void* src, bool real) {
   asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
                "r"(real ? 16 : 0)
@@ -543,17 +539,7 @@ struct Fetch {
       kb += page * a.k.page + slot * a.k.token;
       vb += page * a.v.page + slot * a.v.token;
       const int n = len - j;
-      if (n >= S::kWarpKeys) {
 #pragma unroll
-        for (int x = 0; x < kCopies; ++x) {
-          const int key = x * kRowsAtOnce + sub;
-          const uint32_t dst = stage + key * S::kRow + ((c ^ (key & 7)) << 4);
-          cp_async16(dst, kb + key * a.k.token);
-          cp_async16(dst + kValues, vb + key * a.v.token);
-        }
-        return 0xffffffffu >> (32 - S::kWarpKeys);
-      }
-#pragma unroll 1
       for (int x = 0; x < kCopies; ++x) {
         const int key = x * kRowsAtOnce + sub;
         const uint32_t dst = stage + key * S::kRow + ((c ^ (key & 7)) << 4);
@@ -561,7 +547,7 @@ struct Fetch {
         cp_async16_if(dst, kb + (real ? key : 0) * a.k.token, real);
         cp_async16_if(dst + kValues, vb + (real ? key : 0) * a.v.token, real);
       }
-      return (1u << n) - 1;
+      return n >= S::kWarpKeys ? 0xffffffffu >> (32 - S::kWarpKeys) : (1u << n) - 1;
     }
     const bool due = lane < S::kWarpKeys && j + lane < len;
     const bool good = due && page >= 0 && page < a.table.num_pages;

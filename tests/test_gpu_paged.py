@@ -148,6 +148,39 @@ def test_append_one_token():
     _append_case(FP, 128, 4, 64, 64, 64, True, [1], [777], 0, seed=8)
 
 
+@pytest.mark.parametrize("dt,dim,kv,heads,S,rot,inter,fused", [
+    (BF, 64, 1, 1, 64, 64, False, False), (FP, 64, 3, 3, 16, 16, True, True),
+    (BF, 128, 2, 8, 128, 64, False, True), (FP, 128, 1, 6, 8, 128, True, False)])
+def test_append_many_tokens_of_few_heads(dt, dim, kv, heads, S, rot, inter, fused):
+    # rows that begin and end anywhere in a group of tokens, empty rows, padding behind the last
+    _append_case(dt, dim, kv, heads, S, rot, inter, [1, 0, 2003, 1, 3, 0, 2501, 2], [5, 9, 0, 77, 1,
+                 3, 127, 64], 13, seed=21 + dim, fused=fused, head_major=False)
+
+
+def test_append_bad_places_among_many_tokens():
+    gen = _gen(22)
+    S, T = 16, 1600
+    kc, vc = (_pool(gen, 101, S, 1, 64, BF) for _ in range(2))
+    k, v = (_randn(gen, (T, 1, 64), BF) for _ in range(2))
+    k0, v0 = kc.clone(), vc.clone()
+    table = torch.randperm(101, generator=gen, device=DEV)[:100].to(torch.int32)[None]
+    bad = [3, 4, 50, 99]
+    table[0, bad] = _i32([-1, 101, 2**31 - 1, -2**31])
+    cache = api.PagedCache(kc, vc)
+    k_out = torch.full((T, 1, 64), 9.0, dtype=BF, device=DEV)
+    api.msa_paged_append(cache, k, v, table, _i32([0, T - 1]), _i32([1]), k_out=k_out)
+    assert api.msa_paged_read_status(cache) == 11
+    for t in range(T - 1):
+        pg, slot = divmod(t + 1, S)
+        if pg in bad:
+            assert bool((k_out[t] == 9).all())
+        else:
+            k0[table[0, pg].item(), slot], v0[table[0, pg].item(), slot] = k[t], v[t]
+    assert torch.equal(kc, k0) and torch.equal(vc, v0) and bool((k_out[T - 1] == 9).all())
+    fine = [t for t in range(T - 1) if (t + 1) // S not in bad]
+    assert torch.equal(k_out[fine], k[fine])
+
+
 def test_append_wide_tokens_take_several_rounds():
     _append_case(BF, 128, 64, 256, 16, 128, False, [3], [2], 0, seed=9)
 
