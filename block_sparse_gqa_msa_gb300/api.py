@@ -647,7 +647,9 @@ def msa_paged_append(cache: PagedCache, k: torch.Tensor, v: torch.Tensor,
         qp, heads = q.data_ptr(), q.shape[1]
         if q_out is None:
             q_out = _empty((T, heads, dim), dt, device, stream)
-        qo = _arg(q_out, "q_out", dt, (T, heads, dim), device)
+            qo = q_out.data_ptr()
+        else:
+            qo = _arg(q_out, "q_out", dt, (T, heads, dim), device)
     elif q_out is not None:
         raise ValueError("q_out needs q")
     if inv_freq is not None:
@@ -692,7 +694,9 @@ def msa_paged_select(index: PagedIndex, iq: torch.Tensor, page_table: torch.Tens
     lens = _arg(kv_len, "kv_len", torch.int32, (rows,), device)
     if q2k is None:
         q2k = _empty((heads, rows, TOPK), torch.int32, device, stream)
-    out = _arg(q2k, "q2k", torch.int32, (heads, rows, TOPK), device)
+        out = q2k.data_ptr()
+    else:
+        out = _arg(q2k, "q2k", torch.int32, (heads, rows, TOPK), device)
     _check(lib().msa_paged_select(index._ref, ctypes.byref(table), lens, qp,
                                   1 if force_local else 0, out, _stream(stream)),
            "msa_paged_select")
@@ -726,16 +730,20 @@ def msa_paged_decode(cache: PagedCache, q: torch.Tensor, page_table: torch.Tenso
         slots = _arg(q2k, "q2k", torch.int32, (cache.kv_heads, rows, TOPK), device)
     if o is None:
         o = _empty(shape, cache.dtype, device, stream)
+        op = o.data_ptr()
+    else:
+        op = _arg(o, "o", cache.dtype, shape, device)
     if lse is None:
         lse = _empty((rows, heads), torch.float32, device, stream)
+        lp = lse.data_ptr()
+    else:
+        lp = _arg(lse, "lse", torch.float32, (rows, heads), device)
     if workspace is None:
         workspace = _empty(paged_decode_workspace_bytes(cache, rows, heads), torch.uint8, device,
                            stream)
     nbytes = workspace.numel()
     _check(lib().msa_paged_decode(
-        cache._ref, ctypes.byref(table), lens, qp, heads, float(softmax_scale), slots,
-        _arg(o, "o", cache.dtype, shape, device),
-        _arg(lse, "lse", torch.float32, (rows, heads), device),
+        cache._ref, ctypes.byref(table), lens, qp, heads, float(softmax_scale), slots, op, lp,
         _arg(workspace, "workspace", torch.uint8, (nbytes,), device), nbytes, _stream(stream)),
         "msa_paged_decode")
     return o, lse
