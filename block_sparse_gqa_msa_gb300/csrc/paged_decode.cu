@@ -76,11 +76,10 @@ struct DecodeShape {
   static constexpr int kStageBytes = 2 * kWarpKeys * kRow;   // 8 KB
   static constexpr int kStages = 3;
   static constexpr int kRing = kStages * kStageBytes;
-  // the warps' states meet 32 channels at a time, rows 40 floats apart
-  // (8 rows' 8-byte writes then hit all banks once)
-  static constexpr int kMergeRow = 40;
-  static constexpr int kMergeBytes = kDecWarps * kGroup * kMergeRow * 4;
-  static constexpr int kSmem = kDecWarps * kRing + kMergeBytes;  // 106 KB a CTA
+  static constexpr int kStateBytes = kGroup * kDim * 4;      // of O in 32 bits
+  static_assert(kStateBytes <= kStageBytes, "a warp's state fits a stage");
+  static constexpr int kSmem = kDecWarps * kRing;            // 96 KB a CTA
+  static constexpr int kSmemCluster = kSmem + kStateBytes;   // 104 KB
 };
 
 // Runs of a call: one for each CTA that is on the chip at once (two an SM),
@@ -615,8 +614,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) k_paged_decode(const DecodeArg
   }
 
   const uint32_t ring = smem_u32(smem) + warp * S::kRing;
-  float* merge = reinterpret_cast<float*>(smem + kDecWarps * S::kRing);
-  [[maybe_unused]] float* state = reinterpret_cast<float*>(smem);  // the unit's, over the drained ring
+  [[maybe_unused]] float* state = reinterpret_cast<float*>(smem + S::kSmem);  // the CTA's part (cluster)
   Fetch<T, kDim> fetch{a, blocks[warp], queue[warp], prefix, &ctas, &next[warp], lane, warp};
   fetch.init(tail);
   [[maybe_unused]] const bool idle = next[warp].n == 0;  // (only in a cluster)
@@ -752,6 +750,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) k_paged_decode(const DecodeArg
         }
       }
     }
+    const int worked = stage;
     stage = stage + 1 == S::kStages ? 0 : stage + 1;
     if (fill > 0) {
       --fill;
@@ -759,7 +758,9 @@ __global__ void __launch_bounds__(kDecThreads, 2) k_paged_decode(const DecodeArg
     }
     if (--left > 0) continue;
 
-    // ---- the segment's end: join the warps: every state is brought to the common maximum
+    // ---- the segment's end: join the warps.  Each leaves its state in the stage
+    // that it has just worked on, which the next step fills: a row's 16-byte
+    // piece p sits at p ^ (2 (row & 3)), so that 4 rows' writes hit all banks.
     l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
     l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
     l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
@@ -767,54 +768,48 @@ __global__ void __launch_bounds__(kDecThreads, 2) k_paged_decode(const DecodeArg
     if ((lane & 3) == 0) {
       ml[0][warp][r_lo] = m0;
       ml[0][warp][r_lo + 8] = m1;
+      ml[1][warp][r_lo] = l0;
+      ml[1][warp][r_lo + 8] = l1;
+    }
+    uint8_t* const states = smem + worked * S::kStageBytes;  // the warps', kRing apart
+    {
+      float* mine = reinterpret_cast<float*>(states + warp * S::kRing) + (col & 2);
+      const int swz = (r_lo & 3) << 1;
+      __syncwarp();  // the stage is read
+#pragma unroll
+      for (int n = 0; n < kCols; ++n) {
+        const int at = ((2 * n + (col >> 2)) ^ swz) * 4;
+        *reinterpret_cast<float2*>(mine + r_lo * kDim + at) = make_float2(acc[n][0], acc[n][1]);
+        *reinterpret_cast<float2*>(mine + (r_lo + 8) * kDim + at) =
+            make_float2(acc[n][2], acc[n][3]);
+      }
     }
     __syncthreads();
-    float M0 = -INFINITY, M1 = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kDecWarps; ++w) {
-      M0 = fmaxf(M0, ml[0][w][r_lo]);
-      M1 = fmaxf(M1, ml[0][w][r_lo + 8]);
-    }
-    const float f0 = m0 == -INFINITY ? 0.f : fast_exp2(m0 - M0);
-    const float f1 = m1 == -INFINITY ? 0.f : fast_exp2(m1 - M1);
-    if ((lane & 3) == 0) {
-      ml[1][warp][r_lo] = l0 * f0;
-      ml[1][warp][r_lo + 8] = l1 * f1;
-    }
     const bool whole = !kCluster && g.i0 == 0 && g.i1 == g.tiles;
     const int64_t slot = 2 * int64_t(g.run) + (g.i0 > 0 ? 0 : 1);
     const int64_t unit = int64_t(g.row) * a.kv_heads + g.head;
     const int h = tid / 8;  // the thread's row of the result, 4 channels of each 32
-    float M = -INFINITY, l = 0.f, inv = 0.f;
+    float M = -INFINITY, l = 0.f, f[kDecWarps];
+#pragma unroll
+    for (int w = 0; w < kDecWarps; ++w) M = fmaxf(M, ml[0][w][h]);
+#pragma unroll
+    for (int w = 0; w < kDecWarps; ++w) {
+      const float m = ml[0][w][h];
+      f[w] = m == -INFINITY ? 0.f : fast_exp2(m - M);
+      l += ml[1][w][h] * f[w];
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;  // l == 0: no key was seen
 #pragma unroll
     for (int c = 0; c < kDim / 32; ++c) {
-      float* mine = merge + warp * (kGroup * S::kMergeRow);
-#pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        const float* x = acc[c * 4 + n];
-        *reinterpret_cast<float2*>(mine + r_lo * S::kMergeRow + n * 8 + col) =
-            make_float2(x[0] * f0, x[1] * f0);
-        *reinterpret_cast<float2*>(mine + (r_lo + 8) * S::kMergeRow + n * 8 + col) =
-            make_float2(x[2] * f1, x[3] * f1);
-      }
-      __syncthreads();
-      if (c == 0) {
-#pragma unroll
-        for (int w = 0; w < kDecWarps; ++w) {
-          M = fmaxf(M, ml[0][w][h]);
-          l += ml[1][w][h];
-        }
-        inv = l == 0.f ? 0.f : 1.f / l;  // l == 0: no key was seen
-      }
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kDecWarps; ++w) {
         const float4 u = *reinterpret_cast<const float4*>(
-            merge + (w * kGroup + h) * S::kMergeRow + (tid % 8) * 4);
-        v.x += u.x;
-        v.y += u.y;
-        v.z += u.z;
-        v.w += u.w;
+            states + w * S::kRing + h * (kDim * 4) + ((c * 8 + tid % 8) ^ ((h & 3) << 1)) * 16);
+        v.x += u.x * f[w];
+        v.y += u.y * f[w];
+        v.z += u.z * f[w];
+        v.w += u.w * f[w];
       }
       const int ch = c * 32 + (tid % 8) * 4;
       if (kCluster)
@@ -824,7 +819,6 @@ __global__ void __launch_bounds__(kDecThreads, 2) k_paged_decode(const DecodeArg
       else if (h < a.group)
         *reinterpret_cast<uint2*>(static_cast<T*>(a.o) + (unit * a.group + h) * kDim + ch) =
             make_uint2(Pair<T>::pack(v.x * inv, v.y * inv), Pair<T>::pack(v.z * inv, v.w * inv));
-      __syncthreads();  // the buffers are read
     }
     if (tid % 8 == 0) {
       if (kCluster) {
@@ -837,6 +831,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) k_paged_decode(const DecodeArg
         a.lse[unit * a.group + h] = l == 0.f ? -INFINITY : kLn2 * (M + log2f(l));
       }
     }
+    __syncthreads();  // the states are read
     if (++seg == fetch.n_seg) break;  // the fetch is ahead: it would have entered the next one
   }
   cp_async_wait<0>();
@@ -1047,7 +1042,7 @@ int cluster_room(void (*kernel)(DecodeArgs), int cluster) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(cluster));
   cfg.blockDim = dim3(kDecThreads);
-  cfg.dynamicSmemBytes = DecodeShape<kDim>::kSmem;
+  cfg.dynamicSmemBytes = DecodeShape<kDim>::kSmemCluster;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
   attr.val.clusterDim.x = unsigned(cluster);
@@ -1083,7 +1078,7 @@ cudaError_t launch_decode(DecodeArgs a, cudaStream_t s) {
   // Clusters of 8 near the room there is get in one another's way.
   auto clustered = k_paged_decode<T, kDim, true>;
   static std::atomic<uint64_t> done_c{0};
-  cudaError_t e = allow_smem(clustered, S::kSmem, done_c);
+  cudaError_t e = allow_smem(clustered, S::kSmemCluster, done_c);
   if (e != cudaSuccess) return e;
   int cluster = kMaxCluster;
   while (cluster > 1 &&
@@ -1096,8 +1091,8 @@ cudaError_t launch_decode(DecodeArgs a, cudaStream_t s) {
   if (fits && unit <= cluster * (a.q2k ? kTopK * S::kTilesPerBlock : kClusterTiles)) {
     a.cluster = cluster;
     launch_begin("paged_decode", s);
-    e = launch_cluster(clustered, dim3(unsigned(units * cluster)), dim3(kDecThreads), S::kSmem,
-                       unsigned(cluster), s, a);
+    e = launch_cluster(clustered, dim3(unsigned(units * cluster)), dim3(kDecThreads),
+                       S::kSmemCluster, unsigned(cluster), s, a);
     launch_end("paged_decode", s);
     return e;
   }
