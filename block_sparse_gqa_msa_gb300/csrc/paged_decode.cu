@@ -5,10 +5,11 @@
 // share g form the 16 rows of one matrix tile.  Over the keys in any order,
 // with running maximum m and sum l in base 2 (x = scale * log2(e) * <q, k>):
 //   m' = max(m, max x),  l' = l 2^(m-m') + sum 2^(x-m'),
-//   O' = O 2^(m-m') + 2^(x-m') V,
-// and two such states join as M = max(m1, m2), l = l1 2^(m1-M) + l2 2^(m2-M),
+//   O' = O 2^(m-m') + 2^(x-m') V
+// (any m' serves that keeps the powers in range: m stays while no x is above
+// m + 8), and two such states join as M = max(m1, m2), l = l1 2^(m1-M) + l2 2^(m2-M),
 // O likewise; at the end O / l and lse = ln2 (m + log2 l).  m, l, O are 32
-// bits throughout.  The weights 2^(x-m') <= 1 enter the product with V as the
+// bits throughout.  The weights 2^(x-m') <= 2^8 enter the product with V as the
 // sum of two numbers of the cache's type, the second what rounding to the
 // first leaves over: with one number O was 0.0021 off (relative, bf16, of
 // which the output's own rounding is 0.0017), with two 0.0017, and the second
@@ -64,6 +65,11 @@ namespace {
 constexpr int kDecWarps = 4;
 constexpr int kDecThreads = kDecWarps * 32;
 constexpr int kGroup = 16;   // query heads of a matrix tile
+// The maximum that a running state refers to is renewed only when a score is
+// above it by more than this (in base 2): weights are then up to 2^8, sums of
+// 2^30 of them far inside 32 bits, and the state is scaled a few times in a unit
+// and not in most of its first tiles.
+constexpr float kSlack = 8.f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -534,17 +540,23 @@ struct Fetch {
         raise_paged(a.table.status, MSA_ERR_BAD_PAGE);
         return 0;
       }
-      const int64_t slot = j & mask;
+      const int n = len - j;
+      const int64_t slot = (j & mask) + (sub < n ? sub : 0);
       kb += page * a.k.page + slot * a.k.token;
       vb += page * a.v.page + slot * a.v.token;
-      const int n = len - j;
+      const int64_t k_step = a.k.token * kRowsAtOnce, v_step = a.v.token * kRowsAtOnce;
+      const uint32_t lane_at = stage + sub * S::kRow + ((c ^ sub) << 4);
 #pragma unroll
       for (int x = 0; x < kCopies; ++x) {
-        const int key = x * kRowsAtOnce + sub;
-        const uint32_t dst = stage + key * S::kRow + ((c ^ (key & 7)) << 4);
-        const bool real = key < n;  // else nothing is read; the address is the first key's
-        cp_async16_if(dst, kb + (real ? key : 0) * a.k.token, real);
-        cp_async16_if(dst + kValues, vb + (real ? key : 0) * a.v.token, real);
+        const uint32_t dst =
+            (lane_at ^ (((x * kRowsAtOnce) & 7) << 4)) + x * kRowsAtOnce * S::kRow;
+        const bool real = x * kRowsAtOnce + sub < n;
+        cp_async16_if(dst, kb, real);
+        cp_async16_if(dst + kValues, vb, real);
+        if ((x + 1) * kRowsAtOnce + sub < n) {  // else nothing is read: a real key's address
+          kb += k_step;
+          vb += v_step;
+        }
       }
       return n >= S::kWarpKeys ? 0xffffffffu >> (32 - S::kWarpKeys) : (1u << n) - 1;
     }
@@ -574,7 +586,8 @@ __global__ void __launch_bounds__(kDecThreads, 2) k_paged_decode(const DecodeArg
   constexpr int kSteps = kDim / 16;            // k-steps of the first product
   constexpr int kCols = kDim / 8;              // column tiles of the second
   constexpr int kKeyTiles = S::kWarpKeys / 8;  // column tiles of the first
-  extern __shared__ __align__(128) uint8_t smem[];
+  constexpr uint32_t kAllSeen = 0xffffffffu >> (32 - S::kWarpKeys);
+  extern __shared__ __align__(256) uint8_t smem[];  // rows of keys begin on their own size
   __shared__ Prefix prefix;
   __shared__ Queue ctas;
   __shared__ NextRun next[kDecWarps];
@@ -674,32 +687,34 @@ __global__ void __launch_bounds__(kDecThreads, 2) k_paged_decode(const DecodeArg
       for (int n = 0; n < kKeyTiles; n += 2) {
         // matrices: keys 0-7 / 8-15 by channels 0-7 / 8-15 of the step
         const int key = n * 8 + (lane & 7) + ((lane >> 4) << 3);
-        const uint32_t rowp = kb + key * S::kRow;
+        const uint32_t at = kb + key * S::kRow + ((((lane >> 3) & 1) ^ (key & 7)) << 4);
 #pragma unroll
         for (int k = 0; k < kSteps; ++k) {
           uint32_t b[4];
-          ldsm4(b, rowp + (((2 * k + ((lane >> 3) & 1)) ^ (key & 7)) << 4));
+          ldsm4(b, at ^ (k << 5));
           mma16816<T>(x[n], qa[k], b[0], b[1]);
           mma16816<T>(x[n + 1], qa[k], b[2], b[3]);
         }
       }
-      // scores in base 2, masked
+      // Scores and maxima; base 2 comes with the scale.
+      if (seen != kAllSeen) {
+#pragma unroll
+        for (int n = 0; n < kKeyTiles; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (!((seen >> (n * 8 + col + (e & 1))) & 1)) x[n][e] = -INFINITY;
+      }
       float top0 = -INFINITY, top1 = -INFINITY;
 #pragma unroll
       for (int n = 0; n < kKeyTiles; ++n) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const bool on = (seen >> (n * 8 + col + (e & 1))) & 1;
-          x[n][e] = on ? x[n][e] * a.scale_log2 : -INFINITY;
-        }
         top0 = fmaxf(top0, fmaxf(x[n][0], x[n][1]));
         top1 = fmaxf(top1, fmaxf(x[n][2], x[n][3]));
       }
       top0 = fmaxf(top0, __shfl_xor_sync(0xffffffffu, top0, 1));
       top1 = fmaxf(top1, __shfl_xor_sync(0xffffffffu, top1, 1));
-      top0 = fmaxf(top0, __shfl_xor_sync(0xffffffffu, top0, 2));
-      top1 = fmaxf(top1, __shfl_xor_sync(0xffffffffu, top1, 2));
-      if (__any_sync(0xffffffffu, top0 > m0 || top1 > m1)) {
+      top0 = fmaxf(top0, __shfl_xor_sync(0xffffffffu, top0, 2)) * a.scale_log2;
+      top1 = fmaxf(top1, __shfl_xor_sync(0xffffffffu, top1, 2)) * a.scale_log2;
+      if (__any_sync(0xffffffffu, top0 > m0 + kSlack || top1 > m1 + kSlack)) {
         const float n0 = fmaxf(m0, top0), n1 = fmaxf(m1, top1);
         const float f0 = n0 == -INFINITY ? 1.f : fast_exp2(m0 - n0);
         const float f1 = n1 == -INFINITY ? 1.f : fast_exp2(m1 - n1);
@@ -715,13 +730,13 @@ __global__ void __launch_bounds__(kDecThreads, 2) k_paged_decode(const DecodeArg
           acc[n][3] *= f1;
         }
       }
-      const float z0 = m0 == -INFINITY ? 0.f : m0, z1 = m1 == -INFINITY ? 0.f : m1;
+      const float z0 = m0 == -INFINITY ? 0.f : -m0, z1 = m1 == -INFINITY ? 0.f : -m1;
 #pragma unroll
       for (int n = 0; n < kKeyTiles; ++n) {
-        x[n][0] = fast_exp2(x[n][0] - z0);
-        x[n][1] = fast_exp2(x[n][1] - z0);
-        x[n][2] = fast_exp2(x[n][2] - z1);
-        x[n][3] = fast_exp2(x[n][3] - z1);
+        x[n][0] = fast_exp2(fmaf(x[n][0], a.scale_log2, z0));
+        x[n][1] = fast_exp2(fmaf(x[n][1], a.scale_log2, z0));
+        x[n][2] = fast_exp2(fmaf(x[n][2], a.scale_log2, z1));
+        x[n][3] = fast_exp2(fmaf(x[n][3], a.scale_log2, z1));
         l0 += x[n][0] + x[n][1];
         l1 += x[n][2] + x[n][3];
       }
@@ -738,11 +753,11 @@ __global__ void __launch_bounds__(kDecThreads, 2) k_paged_decode(const DecodeArg
         }
         // matrices: keys 0-7 / 8-15 by channels 0-7 / 8-15 of the pair of column tiles
         const int key = k * 8 + (lane & 15);
-        const uint32_t rowp = vb + key * S::kRow;
+        const uint32_t at = vb + key * S::kRow + (((lane >> 4) ^ (key & 7)) << 4);
 #pragma unroll
         for (int n = 0; n < kCols; n += 2) {
           uint32_t b[4];
-          ldsm4_t(b, rowp + (((n + (lane >> 4)) ^ (key & 7)) << 4));
+          ldsm4_t(b, at ^ (n << 4));
           mma16816<T>(acc[n], pa, b[0], b[1]);
           mma16816<T>(acc[n + 1], pa, b[2], b[3]);
           mma16816<T>(acc[n], pb, b[0], b[1]);
