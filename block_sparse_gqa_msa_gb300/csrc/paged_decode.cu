@@ -114,7 +114,6 @@ struct DecodeArgs {
   int32_t kv_heads, group;
   int32_t slots;       // first runs
   int32_t cluster;     // CTAs of a unit, where units are not dealt out in runs
-  int32_t* rec;        // [grid]: 1 + the unit that the run starts inside of; 0: it starts a unit
   float* part_ml;      // [2 grid][2][16]: m, l
   float* part_o;       // [2 grid][16][dim]
 };
@@ -205,6 +204,18 @@ struct Deal {
     return first + step * (s * (8 - s) * R4 + (7 - 2 * s) * (k - s * R4)) + e * k + min(k, r1);
   }
 };
+// The run of c0 .. c1 - 1 that tile t lies in (run c0 starts at or before it).
+// A whole warp.
+__device__ __forceinline__ int32_t run_of(const Deal& deal, int32_t c0, int32_t c1, int32_t t) {
+  const int lane = threadIdx.x & 31;
+  while (c1 - c0 > 1) {
+    const int32_t step = (c1 - c0 + 31) >> 5, c = c0 + lane * step;
+    const uint32_t le = __ballot_sync(0xffffffffu, c < c1 && deal.start(c) <= t);
+    c0 += (__popc(le) - 1) * step;
+    c1 = min(c1, c0 + step);
+  }
+  return c0;
+}
 static_assert(kTailFrom >= kTailShare, "a tile for every short run");
 
 // What a CTA keeps in shared memory to find the place of a tile: the tiles
@@ -218,13 +229,14 @@ struct Prefix {
 __device__ __forceinline__ int32_t checked_len(const DecodeArgs& a, int32_t n) {
   return n < 0 || n > (int64_t(a.table.width) << a.table.shift) ? 0 : n;
 }
-// Every thread sums the tiles of a stretch of rows; a scan over the threads.
+// Every one of the first kDecThreads threads sums the tiles of a stretch of
+// rows; a scan over them.
 template <int kDim>
 __device__ __forceinline__ void make_prefix(const DecodeArgs& a, Prefix& s) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int32_t rows = a.table.rows;
   const int32_t each = (rows + kDecThreads - 1) / kDecThreads;
-  const int32_t r0 = min(rows, tid * each), r1 = min(rows, r0 + each);
+  const int32_t r0 = min(rows, tid * each), r1 = tid < kDecThreads ? min(rows, r0 + each) : r0;
   int32_t mine = 0;
   for (int32_t r = r0; r < r1; ++r) {
     const int32_t n = a.kv_len[r];
@@ -237,7 +249,7 @@ __device__ __forceinline__ void make_prefix(const DecodeArgs& a, Prefix& s) {
     const int32_t y = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += y;
   }
-  if (lane == 31) s.sums[warp] = incl;
+  if (lane == 31 && warp < kDecWarps) s.sums[warp] = incl;
   __syncthreads();
   int32_t total = 0, before = 0;
 #pragma unroll
@@ -245,7 +257,7 @@ __device__ __forceinline__ void make_prefix(const DecodeArgs& a, Prefix& s) {
     if (w < warp) before += s.sums[w];
     total += s.sums[w];
   }
-  s.at[tid] = before + incl - mine;
+  if (tid < kDecThreads) s.at[tid] = before + incl - mine;
   if (tid == 0) {
     s.total = total;
     s.each = each;
@@ -333,7 +345,6 @@ __device__ __forceinline__ int32_t taken_cta(uint32_t answer) {
 // A part of a unit that one CTA works on: its tiles i0 .. i1 - 1.
 struct Segment {
   int32_t run, row, head, i0, i1, tiles;
-  int32_t opens;  // the run's first
 };
 struct NextRun {
   int32_t run, row, head, len, tiles, i, n;
@@ -375,7 +386,7 @@ constexpr int kFindAt = 3;
 // a segment ends: where warp 0's fetch is in its run n + 8, eight tiles or
 // more past run n, its sums are past run n and have met the others' there,
 // whose fetches, ahead of their sums, have all read answer n.
-template <typename T, int kDim>
+template <typename T, int kDim, bool kCluster>
 struct Fetch {
   using S = DecodeShape<kDim>;
   static constexpr int kChunks = kDim / 8;          // 16-byte chunks of a key
@@ -413,7 +424,7 @@ struct Fetch {
   // Enters the unit (row, head) at tile i: its blocks (the distinct valid
   // slots, in slot order, but the row's last block, which may be short, at the
   // end), its place in the queue, and a look ahead.
-  __device__ __forceinline__ void enter(int32_t opens) {
+  __device__ __forceinline__ void enter(bool opens) {
     if (a.q2k) {
       const int32_t nb = int32_t((int64_t(len) + kBlock - 1) / kBlock);
       const int32_t v = slots;
@@ -428,7 +439,7 @@ struct Fetch {
       if (keep)
         blocks[(end >> lane) & 1 ? n_blocks - 1 : __popc(m & ~end & ((1u << lane) - 1))] = v;
     }
-    if (lane == 0) queue[n_seg % kSegQueue] = Segment{run, row, head, i, i1, tiles, opens};
+    if (lane == 0) queue[n_seg % kSegQueue] = Segment{run, row, head, i, i1, tiles};
     ++n_seg;
     __syncwarp();
     if (opens) prefetch_queries(row, head);
@@ -469,7 +480,7 @@ struct Fetch {
         tiles = next->tiles;
         i = next->i;
         left = next->n;
-        load_slots(row, head);
+        if (!kCluster) load_slots(row, head);  // a cluster's unit is known before its length
         n_blocks = 0;
         asked = found = false;
       } else {
@@ -598,13 +609,22 @@ __global__ void __launch_bounds__(kDecThreads, 2) k_paged_decode(const DecodeArg
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r_lo = lane >> 2;  // the lane's matrix rows: r_lo and r_lo + 8
   const int col = (lane & 3) * 2;
+  const uint32_t ring = smem_u32(smem) + warp * S::kRing;
+  [[maybe_unused]] float* state = reinterpret_cast<float*>(smem + S::kSmem);  // the CTA's part (cluster)
+  Fetch<T, kDim, kCluster> fetch{a, blocks[warp], queue[warp], prefix, &ctas, &next[warp], lane, warp};
+  if (!kCluster && tid == 0) {
+    for (int i = 0; i < kAnswers; ++i) mbar_init(smem_u32(&ctas.bar[i]), 1);
+    fence_mbar_init();
+  }
   grid_dep_wait();
   grid_dep_release();
   bool tail = false;
   if constexpr (kCluster) {
     const int rank = blockIdx.x % a.cluster;
     const int32_t unit = blockIdx.x / a.cluster;
-    const int32_t row = unit / a.kv_heads, n = a.kv_len[row], len = checked_len(a, n);
+    const int32_t row = unit / a.kv_heads, n = a.kv_len[row];
+    fetch.load_slots(row, unit % a.kv_heads);
+    const int32_t len = checked_len(a, n);
     if (n != len && tid == 0) raise_paged(a.table.status, MSA_ERR_BAD_PAGE);
     const int32_t tiles = unit_tiles<kDim>(len, a.q2k != nullptr);
     const int32_t i0 = int32_t(int64_t(tiles) * rank / a.cluster);
@@ -612,23 +632,13 @@ __global__ void __launch_bounds__(kDecThreads, 2) k_paged_decode(const DecodeArg
     if (lane == 0) next[warp] = NextRun{0, row, unit % a.kv_heads, len, tiles, i0, i1 - i0};
     __syncwarp();
   } else {
-    if (tid == 0) {
-      for (int i = 0; i < kAnswers; ++i) mbar_init(smem_u32(&ctas.bar[i]), 1);
-      fence_mbar_init();
-    }
     make_prefix<kDim>(a, prefix);
     const Deal deal(prefix.total, a.slots, gridDim.x);
-    if (blockIdx.x >= deal.runs) {
-      if (tid == 0) a.rec[blockIdx.x] = 0;
-      return;
-    }
+    if (blockIdx.x >= deal.runs) return;
     tail = deal.runs > deal.c0;
     find_run<kDim>(a, prefix, deal, blockIdx.x, &next[warp]);
   }
 
-  const uint32_t ring = smem_u32(smem) + warp * S::kRing;
-  [[maybe_unused]] float* state = reinterpret_cast<float*>(smem + S::kSmem);  // the CTA's part (cluster)
-  Fetch<T, kDim> fetch{a, blocks[warp], queue[warp], prefix, &ctas, &next[warp], lane, warp};
   fetch.init(tail);
   [[maybe_unused]] const bool idle = next[warp].n == 0;  // (only in a cluster)
 
@@ -651,8 +661,6 @@ __global__ void __launch_bounds__(kDecThreads, 2) k_paged_decode(const DecodeArg
     if (fill == 0 && left == 0) {  // the next segment; heads past the group are zeros
       g = queue[warp][seg % kSegQueue];
       left = g.i1 - g.i0;
-      if (!kCluster && g.opens && tid == 0)
-        a.rec[g.run] = g.i0 > 0 ? 1 + g.row * a.kv_heads + g.head : 0;
       const T* q = static_cast<const T*>(a.q) +
                    (int64_t(g.row) * a.kv_heads + g.head) * a.group * kDim + col;
 #pragma unroll
@@ -906,9 +914,10 @@ __global__ void __launch_bounds__(kDecThreads, 2) k_paged_decode(const DecodeArg
 // x + 1, if that run starts inside a unit; the CTAs of one unit share its
 // heads.  A warp works on a head, alone or with others that take the head's
 // parts in turn, its lanes over the channels: the parts' states are merged as
-// the keys' were, then the warps'.  The chain of dependent loads is short
-// (the records, then the parts): with few rows this kernel is a good part of
-// the call's time.
+// the keys' were, then the warps'.  With few rows this kernel is a good part of
+// the call's time, so all that follows from the lengths is worked out before
+// the wait for the runs' end.  (The lengths are there: k_paged_decode lets this
+// kernel start after its own wait for what came before.)
 constexpr int kJoinWarps = 16;
 constexpr int kJoinWays = kJoinWarps;  // at most, for one head
 template <typename T, int kDim>
@@ -920,43 +929,36 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 3) k_paged_join(const DecodeA
   };
   __shared__ Chunk so[kJoinWarps][32];
   __shared__ float sm[kJoinWarps], sl[kJoinWarps];
-  __shared__ int32_t before, after;
+  __shared__ Prefix prefix;
+  __shared__ int32_t s_first, s_parts, s_unit;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid == 0) {
-    before = 0;
-    after = INT32_MAX;
-  }
-  grid_dep_wait();
-  grid_dep_release();
-  // The runs that start inside the same unit: up to the nearest others.
-  const int32_t run = int32_t(blockIdx.x) + 1, runs = int32_t(gridDim.x) + 1;
-  const int32_t mark = a.rec[run];
-  constexpr int kEach = (kMaxGrid + kJoinWarps * 32 - 1) / (kJoinWarps * 32);
-  int32_t marks[kEach];
-#pragma unroll
-  for (int k = 0; k < kEach; ++k) {
-    const int32_t i = tid + k * (kJoinWarps * 32);
-    marks[k] = i < runs ? a.rec[i] : 0;
-  }
-  if (mark <= 0 || (mark - 1) / a.kv_heads >= a.table.rows) return;
-  int32_t lo = 0, hi = runs;
-#pragma unroll
-  for (int k = 0; k < kEach; ++k) {
-    const int32_t i = tid + k * (kJoinWarps * 32);
-    if (i < runs && marks[k] != mark) {
-      if (i < run) lo = max(lo, i); else hi = min(hi, i);
+  const int32_t run = int32_t(blockIdx.x) + 1;
+  make_prefix<kDim>(a, prefix);
+  if (warp == 0) {
+    const Deal deal(prefix.total, a.slots, int32_t(gridDim.x) + 1);
+    int32_t first = 0, parts = 0, unit = 0;
+    if (run < deal.runs) {
+      const int32_t lo = deal.start(run);
+      const RowPlace p = locate<kDim>(a, prefix, lo);
+      const int32_t head = (lo - p.start) / p.tiles, u0 = p.start + head * p.tiles;
+      if (u0 < lo) {  // the run starts inside the unit
+        unit = p.row * a.kv_heads + head;
+        first = run_of(deal, 0, run, u0);
+        parts = run_of(deal, run, deal.runs, u0 + p.tiles - 1) + 1 - first;
+      }
+    }
+    if (lane == 0) {
+      s_first = first;
+      s_parts = parts;
+      s_unit = unit;
     }
   }
   __syncthreads();
-  lo = __reduce_max_sync(0xffffffffu, lo);
-  hi = __reduce_min_sync(0xffffffffu, hi);
-  if (lane == 0) {
-    atomicMax(&before, lo);
-    atomicMin(&after, hi);
-  }
-  __syncthreads();
-  const int32_t first = before;    // the run that the unit starts in
-  const int n = after - first;     // parts; n - 1 CTAs
+  const int32_t first = s_first;  // the run that the unit starts in
+  const int n = s_parts;          // parts; n - 1 CTAs
+  grid_dep_wait();  // every CTA waits: this grid must not end before the runs
+  grid_dep_release();
+  if (n == 0) return;
   int shares = 1;                  // of the 16 heads
   while (shares < kGroup && 2 * shares <= n - 1) shares *= 2;
   const int share = run - first - 1;
@@ -1031,7 +1033,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 3) k_paged_join(const DecodeA
     }
   }
   if (h >= a.group) return;
-  const int64_t out = int64_t(mark - 1) * a.group + h;
+  const int64_t out = int64_t(s_unit) * a.group + h;
   const float inv = l == 0.f ? 0.f : 1.f / l;
   uint32_t* o = reinterpret_cast<uint32_t*>(static_cast<T*>(a.o) + out * kDim + lane * kPer);
 #pragma unroll
@@ -1040,8 +1042,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 3) k_paged_join(const DecodeA
 }
 
 size_t decode_workspace(int32_t dim) {
-  return align_up(sizeof(int32_t) * kMaxGrid, 256) +
-         sizeof(float) * 2 * kMaxGrid * (2 * kGroup + kGroup * size_t(dim));
+  return sizeof(float) * 2 * kMaxGrid * (2 * kGroup + kGroup * size_t(dim));
 }
 
 // Clusters of this kernel that fit on the chip at once (GPCs of unlike size
@@ -1179,10 +1180,7 @@ extern "C" msa_status msa_paged_decode(const msa_paged_cache* cache, const msa_p
   a.scale_log2 = softmax_scale * kLog2e;
   a.kv_heads = cache->kv_heads;
   a.group = q_heads / cache->kv_heads;
-  uint8_t* w = static_cast<uint8_t*>(workspace);
-  a.rec = reinterpret_cast<int32_t*>(w);
-  w += align_up(sizeof(int32_t) * kMaxGrid, 256);
-  a.part_ml = reinterpret_cast<float*>(w);
+  a.part_ml = static_cast<float*>(workspace);
   a.part_o = a.part_ml + 2 * kMaxGrid * 2 * kGroup;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
