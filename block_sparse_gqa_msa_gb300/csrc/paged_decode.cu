@@ -17,7 +17,7 @@
 //
 // What bounds it.  Each key and value is used for 16 query heads at most:
 // 4 * 16 * D flop on 4 * D bytes, 16 flop a byte, so HBM is the bound (at 6.8
-// TB/s 109 TFLOP/s, a few per cent of the tensor pipe) and the 16-row
+// TB/s 109 TFLOP/s, which keep the tensor pipe 28 % busy) and the 16-row
 // register-level matrix instruction has the right shape: the tile's rows are
 // the 16 heads, where a 128-row tensor-memory tile would be seven eighths
 // empty.
@@ -45,14 +45,14 @@
 // way.
 //
 // Measured (bf16, 64 heads on 4, 128 channels): 9 rows of 65536 to 131072
-// tokens, all keys, 1.85 GB: 270 to 279 us, 6.6 to 6.8 TB/s, as fast as a
+// tokens, all keys, 1.85 GB: 269 to 278 us, 6.6 to 6.9 TB/s, as fast as a
 // plain copy (285 without the short runs; 277 or less with head-major pages).
-// 128 rows of 500 to 16384 tokens, selected blocks, 508 MB: 91 us, 5.6 TB/s:
+// 128 rows of 500 to 16384 tokens, selected blocks, 508 MB: 89 us, 5.7 TB/s:
 // the first bytes come after 4 us, the runs end up to 8 % apart, the join
-// takes 5 us.  77 rows of up to 12000 tokens, 24 heads on 8 of 64 channels,
+// takes 3.5 us.  77 rows of up to 12000 tokens, 24 heads on 8 of 64 channels,
 // 950 MB: 151 to 165 us, 5.8 to 6.3 TB/s: a head's 128 bytes a token are read
-// alone (head-major pages: 147).  One row: 7 us for 1000 tokens, 9 for 16
-// blocks; dependent loads (length, slots, page, keys) and one join in the
+// alone (head-major pages: 147).  One row: 6.9 us for 1000 tokens, 8.7 for 16
+// blocks; dependent loads (length and slots, page, keys) and one join in the
 // cluster are the time.
 #include <cooperative_groups.h>
 
