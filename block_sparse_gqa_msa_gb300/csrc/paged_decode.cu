@@ -92,7 +92,9 @@ struct DecodeShape {
 // and as many short ones (a multiple of 4).  The workspace is sized without a
 // device: no GB300 has more than 160 SMs.
 constexpr int kTailShare = 12;  // one in so many tiles is kept back for the short runs
-constexpr int kTailFrom = 64;   // in calls of so many tiles a CTA and more
+// In calls of so many tiles a CTA and more (160 rows of 16 blocks, 67 tiles: 115
+// us with short runs, 112 without; 77 rows of 64-channel heads, 95: 163 and 168).
+constexpr int kTailFrom = 80;
 constexpr int kMaxSlots = 160 * 2;
 constexpr int kMaxGrid = kMaxSlots * 2;
 
@@ -918,10 +920,8 @@ __global__ void __launch_bounds__(kDecThreads, 2) k_paged_decode(const DecodeArg
 // the call's time, so all that follows from the lengths is worked out before
 // the wait for the runs' end.  (The lengths are there: k_paged_decode lets this
 // kernel start after its own wait for what came before.)
-constexpr int kJoinWarps = 16;
-constexpr int kJoinWays = kJoinWarps;  // at most, for one head
-template <typename T, int kDim>
-__global__ void __launch_bounds__(kJoinWarps * 32, 3) k_paged_join(const DecodeArgs a) {
+template <typename T, int kDim, int kJoinWarps>
+__global__ void __launch_bounds__(kJoinWarps * 32, 48 / kJoinWarps) k_paged_join(const DecodeArgs a) {
   constexpr int kPer = kDim / 32;
   constexpr int kLoads = 4;
   struct __align__(4 * kPer) Chunk {
@@ -964,81 +964,83 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 3) k_paged_join(const DecodeA
   const int share = run - first - 1;
   if (share >= shares) return;
   const int heads = kGroup / shares;    // of this CTA
-  const int ways = kJoinWarps / heads;  // warps of a head
+  const int ways = max(kJoinWarps / heads, 1);  // warps of a head
   const int way = warp % ways;
-  const int h = share * heads + warp / ways;
-  // part 0: the run that the unit starts in; then the runs that start inside it
-  float M = -INFINITY, l = 0.f, acc[kPer] = {};
-  for (int i0 = way; i0 < n; i0 += kLoads * ways) {
-    Chunk o[kLoads];
-    float m[kLoads], pl[kLoads];
+  // (one pass, but where few warps have all heads)
+  for (int h = share * heads + warp / ways; h < (share + 1) * heads; h += kJoinWarps) {
+    // part 0: the run that the unit starts in; then the runs that start inside it
+    float M = -INFINITY, l = 0.f, acc[kPer] = {};
+    for (int i0 = way; i0 < n; i0 += kLoads * ways) {
+      Chunk o[kLoads];
+      float m[kLoads], pl[kLoads];
 #pragma unroll
-    for (int u = 0; u < kLoads; ++u) {
-      const int i = i0 + u * ways;
-      m[u] = -INFINITY;
-      pl[u] = 0.f;
-      o[u] = Chunk{};
-      if (i < n) {
-        const int32_t s = 2 * (first + i) + (i == 0 ? 1 : 0);
-        m[u] = a.part_ml[s * (2 * kGroup) + h];
-        pl[u] = a.part_ml[s * (2 * kGroup) + kGroup + h];
-        o[u] = reinterpret_cast<const Chunk*>(a.part_o + (s * kGroup + h) * kDim)[lane];
+      for (int u = 0; u < kLoads; ++u) {
+        const int i = i0 + u * ways;
+        m[u] = -INFINITY;
+        pl[u] = 0.f;
+        o[u] = Chunk{};
+        if (i < n) {
+          const int32_t s = 2 * (first + i) + (i == 0 ? 1 : 0);
+          m[u] = a.part_ml[s * (2 * kGroup) + h];
+          pl[u] = a.part_ml[s * (2 * kGroup) + kGroup + h];
+          o[u] = reinterpret_cast<const Chunk*>(a.part_o + (s * kGroup + h) * kDim)[lane];
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kLoads; ++u) {
+        const float top = fmaxf(M, m[u]);
+        const float f = M == -INFINITY ? 0.f : fast_exp2(M - top);
+        const float g = m[u] == -INFINITY ? 0.f : fast_exp2(m[u] - top);
+        M = top;
+        l = l * f + pl[u] * g;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) acc[e] = acc[e] * f + o[u].x[e] * g;
       }
     }
+    if (ways > 1) {
+      Chunk mine;
 #pragma unroll
-    for (int u = 0; u < kLoads; ++u) {
-      const float top = fmaxf(M, m[u]);
-      const float f = M == -INFINITY ? 0.f : fast_exp2(M - top);
-      const float g = m[u] == -INFINITY ? 0.f : fast_exp2(m[u] - top);
-      M = top;
-      l = l * f + pl[u] * g;
+      for (int e = 0; e < kPer; ++e) mine.x[e] = acc[e];
+      so[warp][lane] = mine;
+      if (lane == 0) {
+        sm[warp] = M;
+        sl[warp] = l;
+      }
+      __syncthreads();
+      if (way != 0) return;
+      // a lane a way's state, then the ways' sums with their weights
+      const float mw = lane < ways ? sm[warp + lane] : -INFINITY;
+      M = mw;
 #pragma unroll
-      for (int e = 0; e < kPer; ++e) acc[e] = acc[e] * f + o[u].x[e] * g;
-    }
-  }
-  if (ways > 1) {
-    Chunk mine;
+      for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+      const float f = mw == -INFINITY ? 0.f : fast_exp2(mw - M);
+      l = lane < ways ? sl[warp + lane] * f : 0.f;
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) mine.x[e] = acc[e];
-    so[warp][lane] = mine;
-    if (lane == 0) {
-      sm[warp] = M;
-      sl[warp] = l;
-    }
-    __syncthreads();
-    if (way != 0) return;
-    // a lane a way's state, then the ways' sums with their weights
-    const float mw = lane < ways ? sm[warp + lane] : -INFINITY;
-    M = mw;
+      for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    const float f = mw == -INFINITY ? 0.f : fast_exp2(mw - M);
-    l = lane < ways ? sl[warp + lane] * f : 0.f;
+      for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+      for (int w0 = 0; w0 < kJoinWarps; w0 += 4) {
+        if (w0 >= ways) break;
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
+        for (int u = 0; u < 4; ++u) {
+          const float g = __shfl_sync(0xffffffffu, f, w0 + u);  // 0 past the ways
+          const Chunk o = so[min(warp + w0 + u, kJoinWarps - 1)][lane];
+          if (w0 + u < ways) {
 #pragma unroll
-    for (int w0 = 0; w0 < kJoinWays; w0 += 4) {
-      if (w0 >= ways) break;
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const float g = __shfl_sync(0xffffffffu, f, w0 + u);  // 0 past the ways
-        const Chunk o = so[min(warp + w0 + u, kJoinWarps - 1)][lane];
-        if (w0 + u < ways) {
-#pragma unroll
-          for (int e = 0; e < kPer; ++e) acc[e] += o.x[e] * g;
+            for (int e = 0; e < kPer; ++e) acc[e] += o.x[e] * g;
+          }
         }
       }
     }
-  }
-  if (h >= a.group) return;
-  const int64_t out = int64_t(s_unit) * a.group + h;
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  uint32_t* o = reinterpret_cast<uint32_t*>(static_cast<T*>(a.o) + out * kDim + lane * kPer);
+    if (h >= a.group) return;
+    const int64_t out = int64_t(s_unit) * a.group + h;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    uint32_t* o = reinterpret_cast<uint32_t*>(static_cast<T*>(a.o) + out * kDim + lane * kPer);
 #pragma unroll
-  for (int e = 0; e < kPer; e += 2) o[e / 2] = Pair<T>::pack(acc[e] * inv, acc[e + 1] * inv);
-  if (lane == 0) a.lse[out] = l == 0.f ? -INFINITY : kLn2 * (M + log2f(l));
+    for (int e = 0; e < kPer; e += 2) o[e / 2] = Pair<T>::pack(acc[e] * inv, acc[e + 1] * inv);
+    if (lane == 0) a.lse[out] = l == 0.f ? -INFINITY : kLn2 * (M + log2f(l));
+  }
 }
 
 size_t decode_workspace(int32_t dim) {
@@ -1124,8 +1126,14 @@ cudaError_t launch_decode(DecodeArgs a, cudaStream_t s) {
   launch_end("paged_decode", s);
   if (e != cudaSuccess) return e;
   launch_begin("paged_join", s);
-  e = launch_k(true, k_paged_join<T, kDim>, dim3(unsigned(grid - 1)), dim3(kJoinWarps * 32), 0, s,
-               a);
+  // All of its CTAs should be on the chip while the runs end: three an SM with
+  // 16 warps, six with 8, whose warps take two heads where a CTA has all 16
+  // (256 rows of 16 blocks: 173 us with 16 warps, 171 with 8; 128 rows, without
+  // short runs: 91 and 93).
+  e = grid > a.slots ? launch_k(true, k_paged_join<T, kDim, 8>, dim3(unsigned(grid - 1)),
+                                dim3(8 * 32), 0, s, a)
+                     : launch_k(true, k_paged_join<T, kDim, 16>, dim3(unsigned(grid - 1)),
+                                dim3(16 * 32), 0, s, a);
   launch_end("paged_join", s);
   return e;
 }
