@@ -93,7 +93,7 @@ struct DecodeShape {
 // device: no GB300 has more than 160 SMs.
 constexpr int kTailShare = 12;  // one in so many tiles is kept back for the short runs
 // In calls of so many tiles a CTA and more (160 rows of 16 blocks, 67 tiles: 115
-// us with short runs, 112 without; 77 rows of 64-channel heads, 95: 163 and 168).
+// us with short runs, 112 without; 77 rows of 64-channel heads, 95: 167 and 173).
 constexpr int kTailFrom = 80;
 constexpr int kMaxSlots = 160 * 2;
 constexpr int kMaxGrid = kMaxSlots * 2;
@@ -231,9 +231,15 @@ struct Prefix {
 __device__ __forceinline__ int32_t checked_len(const DecodeArgs& a, int32_t n) {
   return n < 0 || n > (int64_t(a.table.width) << a.table.shift) ? 0 : n;
 }
+// A length, in the kernel that starts before its wait from the second level of
+// the cache, where those that wrote it have left it.
+template <bool kEarly>
+__device__ __forceinline__ int32_t length_of(const DecodeArgs& a, int32_t r) {
+  return kEarly ? __ldcg(a.kv_len + r) : a.kv_len[r];
+}
 // Every one of the first kDecThreads threads sums the tiles of a stretch of
 // rows; a scan over them.
-template <int kDim>
+template <int kDim, bool kEarly>
 __device__ __forceinline__ void make_prefix(const DecodeArgs& a, Prefix& s) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int32_t rows = a.table.rows;
@@ -241,7 +247,7 @@ __device__ __forceinline__ void make_prefix(const DecodeArgs& a, Prefix& s) {
   const int32_t r0 = min(rows, tid * each), r1 = tid < kDecThreads ? min(rows, r0 + each) : r0;
   int32_t mine = 0;
   for (int32_t r = r0; r < r1; ++r) {
-    const int32_t n = a.kv_len[r];
+    const int32_t n = length_of<kEarly>(a, r);
     if (checked_len(a, n) != n && blockIdx.x == 0) raise_paged(a.table.status, MSA_ERR_BAD_PAGE);
     mine += unit_tiles<kDim>(checked_len(a, n), a.q2k != nullptr) * a.kv_heads;
   }
@@ -271,7 +277,7 @@ __device__ __forceinline__ void make_prefix(const DecodeArgs& a, Prefix& s) {
 struct RowPlace {
   int32_t row, len, tiles, start;
 };
-template <int kDim>
+template <int kDim, bool kEarly>
 __device__ __forceinline__ RowPlace locate(const DecodeArgs& a, const Prefix& s, int32_t t) {
   const int lane = threadIdx.x & 31;
   const bool sparse = a.q2k != nullptr;
@@ -283,7 +289,7 @@ __device__ __forceinline__ RowPlace locate(const DecodeArgs& a, const Prefix& s,
   p.start = s.at[k];
   if (s.each == 1) {
     p.row = k;
-    p.len = checked_len(a, a.kv_len[k]);
+    p.len = checked_len(a, length_of<kEarly>(a, k));
     p.tiles = unit_tiles<kDim>(p.len, sparse);
     return p;
   }
@@ -291,7 +297,7 @@ __device__ __forceinline__ RowPlace locate(const DecodeArgs& a, const Prefix& s,
 #pragma unroll 1
   for (int32_t r0 = k * s.each;; r0 += 32) {
     const int32_t r = r0 + lane;
-    const int32_t len = r < end ? checked_len(a, a.kv_len[r]) : 0;
+    const int32_t len = r < end ? checked_len(a, length_of<kEarly>(a, r)) : 0;
     const int32_t tiles = unit_tiles<kDim>(len, sparse);
     const int32_t mine = r < end ? tiles * a.kv_heads : 0;
     int32_t incl = mine;
@@ -357,7 +363,7 @@ template <int kDim>
 __device__ __forceinline__ void find_run(const DecodeArgs& a, const Prefix& prefix,
                                          const Deal& deal, int32_t c, NextRun* next) {
   const int32_t lo = deal.start(c), n = deal.start(c + 1) - lo;
-  const RowPlace p = locate<kDim>(a, prefix, lo);
+  const RowPlace p = locate<kDim, false>(a, prefix, lo);
   const int32_t h = (lo - p.start) / p.tiles;
   if ((threadIdx.x & 31) == 0)
     *next = NextRun{c, p.row, h, p.len, p.tiles, lo - p.start - h * p.tiles, n};
@@ -634,7 +640,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) k_paged_decode(const DecodeArg
     if (lane == 0) next[warp] = NextRun{0, row, unit % a.kv_heads, len, tiles, i0, i1 - i0};
     __syncwarp();
   } else {
-    make_prefix<kDim>(a, prefix);
+    make_prefix<kDim, false>(a, prefix);
     const Deal deal(prefix.total, a.slots, gridDim.x);
     if (blockIdx.x >= deal.runs) return;
     tail = deal.runs > deal.c0;
@@ -933,13 +939,13 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 48 / kJoinWarps) k_paged_join
   __shared__ int32_t s_first, s_parts, s_unit;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int32_t run = int32_t(blockIdx.x) + 1;
-  make_prefix<kDim>(a, prefix);
+  make_prefix<kDim, true>(a, prefix);
   if (warp == 0) {
     const Deal deal(prefix.total, a.slots, int32_t(gridDim.x) + 1);
     int32_t first = 0, parts = 0, unit = 0;
     if (run < deal.runs) {
       const int32_t lo = deal.start(run);
-      const RowPlace p = locate<kDim>(a, prefix, lo);
+      const RowPlace p = locate<kDim, true>(a, prefix, lo);
       const int32_t head = (lo - p.start) / p.tiles, u0 = p.start + head * p.tiles;
       if (u0 < lo) {  // the run starts inside the unit
         unit = p.row * a.kv_heads + head;

@@ -510,6 +510,55 @@ def test_decode_peaked_and_growing_scores():
     _decode_case(FP, 64, 2, 4, 64, [700, 129], False, seed=14, spread=12.0)
 
 
+@pytest.mark.parametrize("sparse", [False, True])
+def test_decode_lengths_that_the_stream_has_just_written(sparse):
+    # steps in a row, each with lengths from the kernel before it, eager and captured
+    gen = _gen(31)
+    rows, kv, S, steps = 61, 4, 64, 8
+    pool, width = 300, 72  # 4608 tokens; the longest row comes to 4376
+    kc, vc = (_pool(gen, pool, S, kv, 128, BF) for _ in range(2))
+    cache = api.PagedCache(kc, vc)
+    q = _randn(gen, (rows, kv * 16, 128), BF)
+    table = torch.randint(pool, (rows, width), generator=gen, device=DEV, dtype=torch.int32)
+    first = torch.randint(0, 2000, (rows,), generator=gen, device=DEV, dtype=torch.int32)
+    q2k = None
+    if sparse:
+        q2k = torch.arange(16, dtype=torch.int32, device=DEV).repeat(kv, rows, 1)
+        q2k[:, :, 7:] = -1
+        first += 900  # all the blocks named are there
+    ws = torch.empty(api.paged_decode_workspace_bytes(cache, rows, kv * 16), dtype=torch.uint8,
+                     device=DEV)
+    want = []
+    for i in range(steps):  # one at a time
+        lens = first + 211 * i
+        torch.cuda.synchronize()
+        want.append(api.msa_paged_decode(cache, q, table, lens, 0.09, q2k, workspace=ws))
+        torch.cuda.synchronize()
+    lens = first.clone()
+    outs = [[torch.empty_like(x) for x in w] for w in want]
+
+    def run():
+        lens.copy_(first)
+        for o, lse in outs:
+            api.msa_paged_decode(cache, q, table, lens, 0.09, q2k, o=o, lse=lse, workspace=ws)
+            lens.add_(211)
+
+    run()
+    runs = [[[x.clone() for x in p] for p in outs]]
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        run()
+    for _ in range(5):
+        graph.replay()
+        runs.append([[x.clone() for x in p] for p in outs])
+    torch.cuda.synchronize()
+    assert api.msa_paged_read_status(cache) == 0
+    for got in runs:
+        for (o, lse), (wo, wl) in zip(got, want):
+            assert torch.equal(o, wo) and torch.equal(lse, wl)
+
+
 def _decode_shared_pages(dt, dim, kv, share, S, lens, sparse, seed):
     """Long rows over few pages: the table names each many times, so the fp64
     result is a sum over the pool's keys with their counts."""
