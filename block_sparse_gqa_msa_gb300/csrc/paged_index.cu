@@ -18,13 +18,13 @@
 // k_paged_select  one cluster of CTAs a (row, index head): a warp brings the
 //                 means of 32 blocks to shared memory 32 channels at a time
 //                 (rows coalesced), a lane scores a block, and the warp keeps
-//                 the best in a list sorted across its lanes; the lists are
-//                 merged through shared memory, then through the cluster's.
+//                 the best 16 in order; the warps' lists meet in shared memory,
+//                 the CTAs' in the cluster's.  Places in a list are counted.
 //                 64 rows of up to 1024 blocks of 4 x 128 channels (68 MB, 10
 //                 us): 21.5 us (62 with each lane reading its block's row from
 //                 memory); 3 us before the first means come, the longest rows,
-//                 two CTAs each, and 3 us of merging are the rest.  One row of
-//                 1024 blocks: 5.1 us.
+//                 two CTAs each, and the lists are the rest.  One row of 1024
+//                 blocks: 5.0 us (5.2 with the lists sorted and merged).
 #include <cooperative_groups.h>
 
 #include <utility>
@@ -219,34 +219,16 @@ __device__ __forceinline__ uint64_t rank_key(float score, int32_t v) {
   u ^= (u >> 31) ? 0xffffffffu : 0x80000000u;
   return (uint64_t(u) << 32) | uint32_t(~v);
 }
-__device__ __forceinline__ uint64_t shfl_xor64(uint64_t x, int o) {
-  return __shfl_xor_sync(0xffffffffu, x, o);
-}
-__device__ __forceinline__ uint64_t max64(uint64_t a, uint64_t b) { return a > b ? a : b; }
-__device__ __forceinline__ uint64_t min64(uint64_t a, uint64_t b) { return a < b ? a : b; }
-// Sorts a bitonic sequence of kN lanes (aligned groups), largest first.
+// How many of n keys (even, 16-byte aligned, shared memory) rank before x.
 template <int kN>
-__device__ __forceinline__ uint64_t bitonic_merge(uint64_t x, int lane) {
+__device__ __forceinline__ int ranked_before(const uint64_t* keys, uint64_t x) {
+  int n = 0;
 #pragma unroll
-  for (int o = kN / 2; o > 0; o >>= 1) {
-    const uint64_t y = shfl_xor64(x, o);
-    x = (lane & o) ? min64(x, y) : max64(x, y);
+  for (int j = 0; j < kN; j += 2) {
+    const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(keys + j);
+    n += (k.x > x) + (k.y > x);
   }
-  return x;
-}
-// Sorts the 32 lanes' values, largest first.
-__device__ __forceinline__ uint64_t sort_desc(uint64_t x, int lane) {
-#pragma unroll
-  for (int k = 2; k <= 32; k <<= 1) {
-#pragma unroll
-    for (int o = k / 2; o > 0; o >>= 1) {
-      const uint64_t y = shfl_xor64(x, o);
-      const bool down = (lane & k) == 0;  // k == 32: every lane
-      const bool low = (lane & o) == 0;
-      x = (low == down) ? max64(x, y) : min64(x, y);
-    }
-  }
-  return x;
+  return n;
 }
 
 template <int kSelWarps>
@@ -255,8 +237,8 @@ __global__ void __launch_bounds__(kSelWarps * 32) k_paged_select(const SelectArg
   namespace cg = cooperative_groups;
   extern __shared__ __align__(128) uint8_t slabs[];
   __shared__ __align__(16) float sq[128];
-  __shared__ uint64_t lists[kSelWarps][kTopK];
-  __shared__ uint64_t from[kSelMaxCluster][kTopK];
+  __shared__ __align__(16) uint64_t lists[kSelWarps][kTopK];
+  __shared__ __align__(16) uint64_t from[kSelMaxCluster][kTopK];
   cg::cluster_group cluster = cg::this_cluster();
   const int C = int(cluster.num_blocks()), rank = int(cluster.block_rank());
   const int64_t unit = blockIdx.x / C;
@@ -272,6 +254,7 @@ __global__ void __launch_bounds__(kSelWarps * 32) k_paged_select(const SelectArg
       out[threadIdx.x] = int(threadIdx.x) < nb ? int(threadIdx.x) : -1;
     return;
   }
+  for (int i = threadIdx.x; i < C * kTopK; i += kSelThreads) from[0][i] = 0;
   auto started = cluster.barrier_arrive();
   const int32_t lo = a.force ? 1 : 0, hi = a.force ? b - 1 : b;
   const int32_t v_step = C * kSelThreads;
@@ -325,7 +308,7 @@ __global__ void __launch_bounds__(kSelWarps * 32) k_paged_select(const SelectArg
       if (fv <= hi) locate();
     }
   };
-  uint64_t best = 0;  // the warp's best candidates, sorted over the lanes
+  uint64_t best = 0;  // the warp's best candidates, in order, in lanes 0 .. 15
   int32_t gv = fv;    // the group being summed
   int stage = 0;
   for (int i = 0; i < kSlabs - 1; ++i) {
@@ -362,42 +345,55 @@ __global__ void __launch_bounds__(kSelWarps * 32) k_paged_select(const SelectArg
       const int32_t last = min(v * kBlock + kBlock - 1, len - 1);
       if (page_of(a.table, r, last) >= 0) key = rank_key(acc, v);
     }
-    // nothing here beats the last of the kept ones: most groups of a long row
-    if (!__any_sync(0xffffffffu, key > __shfl_sync(0xffffffffu, best, kTopK - 1))) {
-      gv += v_step;
-      continue;
-    }
-    key = sort_desc(key, lane);
-    // the larger of best[i] and key[31 - i] are the best 32 of both lists
-    const uint64_t rev = __shfl_sync(0xffffffffu, key, 31 - lane);
-    best = bitonic_merge<32>(max64(best, rev), lane);
     gv += v_step;
+    // nothing here beats the last of the kept ones: most groups of a long row
+    if (!__any_sync(0xffffffffu, key > __shfl_sync(0xffffffffu, best, kTopK - 1))) continue;
+    // Every candidate, new or kept, counts those that rank before it: its place
+    // in the new list.  (In the slab just read, which the next fetch fills: 16
+    // independent loads, where sorting and merging took 20 dependent exchanges.)
+    uint64_t* sc = reinterpret_cast<uint64_t*>(slabs + warp * (kSlabs * kSlabBytes) +
+                                               (stage + kSlabs - 1) % kSlabs * kSlabBytes);
+    __syncwarp();  // the slab is read
+    sc[lane] = key;
+    if (lane < kTopK) {
+      sc[32 + lane] = best;
+      sc[32 + kTopK + lane] = 0;
+    }
+    __syncwarp();
+    const int place = ranked_before<32 + kTopK>(sc, key);
+    const int down = ranked_before<32>(sc, best);
+    if (key != 0 && place < kTopK) sc[32 + kTopK + place] = key;
+    if (best != 0 && lane + down < kTopK) sc[32 + kTopK + lane + down] = best;
+    __syncwarp();
+    best = lane < kTopK ? sc[32 + kTopK + lane] : 0;
   }
+  // The warps' lists become the CTA's, in the first CTA of the cluster, the CTAs'
+  // the unit's, by the same count.
   if (lane < kTopK) lists[warp][lane] = best;
   __syncthreads();
-  // merge the warps' lists pairwise: lanes 0..15 hold one, lanes 16..31 idle
-  for (int n = kSelWarps / 2; n > 0; n >>= 1) {
-    uint64_t x = 0;
-    if (warp < n) {
-      x = max64(lists[warp][lane & 15], lists[warp + n][15 - (lane & 15)]);
-      x = bitonic_merge<16>(x, lane & 15);
-    }
-    __syncthreads();
-    if (warp < n && lane < kTopK) lists[warp][lane] = x;
-    __syncthreads();
-  }
   cluster.barrier_wait(std::move(started));  // every CTA's shared memory is there
+  if (threadIdx.x < kSelWarps * kTopK) {
+    const uint64_t x = lists[0][threadIdx.x];
+    const int place = ranked_before<kSelWarps * kTopK>(lists[0], x);
+    if (x != 0 && place < kTopK) *cluster.map_shared_rank(&from[rank][place], 0) = x;
+  }
+  const uint64_t* last = from[0];
   if (C > 1) {
-    if (threadIdx.x < kTopK)
-      cluster.map_shared_rank(&from[rank][threadIdx.x], 0)[0] = lists[0][threadIdx.x];
     cluster.sync();
+    if (rank != 0) return;
+    if (threadIdx.x < kTopK) lists[0][threadIdx.x] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < C * kTopK; i += kSelThreads) {
+      const uint64_t x = from[0][i];
+      int place = 0;
+      for (int k = 0; k < C; ++k) place += ranked_before<kTopK>(from[k], x);
+      if (x != 0 && place < kTopK) lists[0][place] = x;
+    }
+    last = lists[0];
   }
-  if (rank != 0 || warp != 0) return;
-  uint64_t top = lists[0][lane & 15];
-  for (int k = 1; k < C; ++k) {
-    top = max64(top, from[k][15 - (lane & 15)]);
-    top = bitonic_merge<16>(top, lane & 15);
-  }
+  __syncthreads();
+  if (warp != 0) return;
+  const uint64_t top = last[lane & 15];
   // the chosen blocks in ascending order, unused slots last
   const int need = a.force ? kTopK - 2 : kTopK;
   int32_t mine = top == 0 ? INT32_MAX : int32_t(~uint32_t(top));
