@@ -359,7 +359,7 @@ def _select(st):
     page, table = st["case"]["page"], st["table"].long()
     lens = st["lens"].long()
     n = (lens + BLOCK - 1) // BLOCK
-    v = torch.arange(max(SLOTS, -(-table.shape[1] * page // BLOCK)), device="cuda")
+    v = torch.arange(max(SLOTS, table.shape[1] * page // BLOCK), device="cuda")
     last = torch.minimum(v[None, :] * BLOCK + BLOCK - 1, lens[:, None] - 1)
     slot = _mean_slot(table.gather(1, last // page), last, page)
     score = torch.einsum("rvhd,rhd->hrv", st["means"][slot], st["iq"].float())
