@@ -6,12 +6,11 @@
 // with running maximum m and sum l in base 2 (x = scale * log2(e) * <q, k>):
 //   m' = max(m, max x),  l' = l 2^(m-m') + sum 2^(x-m'),
 //   O' = O 2^(m-m') + 2^(x-m') V
-// (any m' serves that keeps the powers in range: m stays while no x is above
-// m + 8), and two such states join as M = max(m1, m2), l = l1 2^(m1-M) + l2 2^(m2-M),
+// (any m' serves that keeps the powers in range, see kLift), and two such states join as M = max(m1, m2), l = l1 2^(m1-M) + l2 2^(m2-M),
 // O likewise; at the end O / l and lse = ln2 (m + log2 l).  m, l, O are 32
-// bits throughout.  The weights 2^(x-m') <= 2^8 enter the product with V as the
-// sum of two numbers of the cache's type, the second what rounding to the
-// first leaves over: with one number O was 0.0021 off (relative, bf16, of
+// bits throughout.  The weights 2^(x-m') enter the product with V as the sum of
+// two numbers of the cache's type, the second what rounding to the first leaves
+// over (as far as the type's smallest step lets it): with one number O was 0.0021 off (relative, bf16, of
 // which the output's own rounding is 0.0017), with two 0.0017, and the second
 // product costs 1 % of the time.
 //
@@ -65,11 +64,20 @@ namespace {
 constexpr int kDecWarps = 4;
 constexpr int kDecThreads = kDecWarps * 32;
 constexpr int kGroup = 16;   // query heads of a matrix tile
-// The maximum that a running state refers to is renewed only when a score is
-// above it by more than this (in base 2): weights are then up to 2^8, sums of
-// 2^30 of them far inside 32 bits, and the state is scaled a few times in a unit
-// and not in most of its first tiles.
-constexpr float kSlack = 8.f;
+// The m of a running state is renewed only when a score is 8 (in base 2) above
+// the maximum that it was set by, so the state is scaled a few times in a unit
+// and not in most of its first tiles.  m is set kLift below that maximum, so
+// weights are up to 2^(8 + kLift), sums of 2^30 of them far inside 32 bits.
+// bf16 has the range of 32 bits: 0.  fp16 ends at 2^16 and its half step is
+// 2^-25 at least: with m 7 lower a weight of 2^15 still fits, and what a key far
+// below the maximum gives is off by 2^-32 of the maximum's weight at most (with
+// no lift every key 17.3 nats below was lost from O and not from l, and 131072
+// such keys beside one dominant key are 0.4 % of the sum).
+constexpr float kRise = 8.f;
+template <typename T>
+constexpr float kLift = 0.f;
+template <>
+constexpr float kLift<__half> = 7.f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -730,8 +738,9 @@ __global__ void __launch_bounds__(kDecThreads, 2) k_paged_decode(const DecodeArg
       top1 = fmaxf(top1, __shfl_xor_sync(0xffffffffu, top1, 1));
       top0 = fmaxf(top0, __shfl_xor_sync(0xffffffffu, top0, 2)) * a.scale_log2;
       top1 = fmaxf(top1, __shfl_xor_sync(0xffffffffu, top1, 2)) * a.scale_log2;
-      if (__any_sync(0xffffffffu, top0 > m0 + kSlack || top1 > m1 + kSlack)) {
-        const float n0 = fmaxf(m0, top0), n1 = fmaxf(m1, top1);
+      constexpr float kAbove = kLift<T> + kRise;
+      if (__any_sync(0xffffffffu, top0 > m0 + kAbove || top1 > m1 + kAbove)) {
+        const float n0 = fmaxf(m0, top0 - kLift<T>), n1 = fmaxf(m1, top1 - kLift<T>);
         const float f0 = n0 == -INFINITY ? 1.f : fast_exp2(m0 - n0);
         const float f1 = n1 == -INFINITY ? 1.f : fast_exp2(m1 - n1);
         m0 = n0;

@@ -119,8 +119,10 @@ def decode_bounds(k_cache, v_cache, q, table, lens, scale, step: float, tiny: fl
     a weight and the normaliser are each off by e (relative), O by twice that
     times sum p|v|; a weight's two roundings add step^2 * sum p|v| (and tiny for
     each weight whose rest is below the normal range, against a largest weight
-    of 1), the output's step * |O| + tiny.  LSE: e, plus the sum's and logarithm's roundings."""
+    of 2^7 in fp16, whose range is short, and of 1 in bf16), the output's
+    step * |O| + tiny.  LSE: e, plus the sum's and logarithm's roundings."""
     u = 2.0 ** -24
+    rest = tiny * 2.0 ** -7 if tiny > 2.0 ** -100 else tiny
     O, L = decode(k_cache, v_cache, q, table, lens, scale, q2k)
     BO, BL = np.zeros_like(O), np.zeros_like(L)
     rows, heads, dim = q.shape
@@ -143,6 +145,6 @@ def decode_bounds(k_cache, v_cache, q, table, lens, scale, step: float, tiny: fl
             p = np.exp(s - L[r, h][:, None])
             pv = p @ np.abs(V[j, g])
             BO[r, h] = ((2 * e + step ** 2) * 1.01)[:, None] * pv + step * np.abs(O[r, h]) + tiny \
-                + m * tiny * np.abs(V[j, g]).max() * np.exp(s.max(1) - L[r, h])[:, None]
+                + m * rest * np.abs(V[j, g]).max() * np.exp(s.max(1) - L[r, h])[:, None]
             BL[r, h] = 1.01 * e + 4 * u * (np.abs(L[r, h]) + biggest + np.log(m) + 1)
     return O, L, BO, BL

@@ -510,6 +510,37 @@ def test_decode_peaked_and_growing_scores():
     _decode_case(FP, 64, 2, 4, 64, [700, 129], False, seed=14, spread=12.0)
 
 
+@pytest.mark.parametrize("dt,dim", [(FP, 64), (FP, 128), (BF, 128)])
+@pytest.mark.parametrize("nats", [16.0, 17.0, 18.0])
+def test_decode_keeps_the_tail_behind_a_dominant_key(dt, dim, nats):
+    """One key `nats` above all others, with a value of 0: O is what the tail
+    leaves.  Two units an SM, a run each: all of a unit's keys meet the dominant
+    one's warp or the three beside it."""
+    gen, S, n = _gen(61), 128, 16384
+    rows = 2 * torch.cuda.get_device_properties(0).multi_processor_count
+    kc, vc = (_pool(gen, 9, S, 1, dim, dt) for _ in range(2))
+    kc.mul_(0.02)
+    vc.add_(2.0)
+    q = torch.ones(rows, 4, dim, dtype=dt, device=DEV)
+    q[:, 1::2] *= 0.9375
+    scale = dim ** -0.5
+    kc[8, 0] = nats / (dim * scale)
+    vc[8, 0] = 0
+    table = torch.randint(8, (1, n // S), generator=gen, device=DEV, dtype=torch.int32)
+    table[0, 0] = 8
+    cache = api.PagedCache(kc, vc)
+    o, lse = api.msa_paged_decode(cache, q, table.expand(rows, -1).contiguous(), _i32([n] * rows),
+                                  scale)
+    torch.cuda.synchronize()
+    assert api.msa_paged_read_status(cache) == 0
+    O, L, BO, BL = paged.decode_bounds(_np(kc), _np(vc), _np(q[:1]), _np(table).astype(int), [n],
+                                       scale, HALF[dt], TINY[dt])
+    assert (BO < 0.1 * np.abs(O)).all()  # a quarter of the tail is missed if one warp's is
+    one = np.ones((rows, 1, 1))
+    _within(_np(lse), L * one[..., 0], BL * one[..., 0], "LSE")
+    _within(_np(o), O * one, BO * one, "O")
+
+
 @pytest.mark.parametrize("sparse", [False, True])
 def test_decode_lengths_that_the_stream_has_just_written(sparse):
     # steps in a row, each with lengths from the kernel before it, eager and captured
