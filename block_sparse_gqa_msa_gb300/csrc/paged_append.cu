@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(kAppThreads) k_paged_append(const AppendArgs a
         const int64_t t = t0 + w;
         const int32_t r = find_row_warp(a.offs, a.table.rows, t);
         const int32_t o0 = a.offs[r], o1 = a.offs[r + 1];
-        if (t >= o0 && t < o1) {
+        if (o0 >= 0 && t >= o0 && t < o1) {
           pos = int64_t(a.start[r]) + (t - o0);
           page = page_of(a.table, r, pos);
           for (int i = lane; i < half; i += 32) {
@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(kAppThreads) k_paged_append(const AppendArgs a
       placed = true;
       const int32_t r = find_row_warp(a.offs, a.table.rows, t0);
       const int32_t o0 = a.offs[r], o1 = a.offs[r + 1];
-      if (t0 < o0 || t0 >= o1) return;  // padding: no row owns this token
+      if (o0 < 0 || t0 < o0 || t0 >= o1) return;  // padding: no row owns this token
       pos = int64_t(a.start[r]) + (t0 - o0);
       page = page_of(a.table, r, pos);
       if (page < 0) return;

@@ -63,10 +63,10 @@ struct NewBlock {
   int64_t pos;
 };
 // Blocks of row r that get a token (0: none, or the row's offsets or first
-// position are bad).
+// position are bad; as for append, a row has no tokens past T).
 __device__ __forceinline__ int32_t row_blocks(const IndexArgs& a, int32_t r) {
-  const int64_t o0 = a.offs[r], o1 = a.offs[r + 1], p = a.start[r];
-  if (o0 < 0 || o1 <= o0 || o1 > a.T) return 0;
+  const int64_t o0 = a.offs[r], o1 = min(int64_t(a.offs[r + 1]), a.T), p = a.start[r];
+  if (o0 < 0 || o1 <= o0) return 0;
   if (p < 0) {
     raise_paged(a.table.status, MSA_ERR_BAD_PAGE);
     return 0;
@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(kIdxThreads) k_paged_index(const IndexArgs a) 
       int32_t k = x - before;
       int32_t r = r0;
       for (int32_t n; k >= (n = row_blocks(a, r)); ++r) k -= n;
-      const int32_t o0 = a.offs[r], o1 = a.offs[r + 1];
+      const int32_t o0 = a.offs[r], o1 = int32_t(min(int64_t(a.offs[r + 1]), a.T));
       const int64_t p = a.start[r], first = k == 0 ? p : ((p >> 7) + k) << 7;
       NewBlock b;
       b.row = r;

@@ -458,7 +458,10 @@ msa_status msa_paged_read_status(const int64_t* status, msa_stream_t stream);
  * its reduction in 64 bits, the rotation in 32, one rounding); channels from
  * rotary_dim on are copied.  A token whose place is bad is skipped
  * (MSA_ERR_BAD_PAGE); offsets that do not start at 0, decrease or pass T set
- * MSA_ERR_BAD_OFFSETS, and tokens that no row owns are skipped.  Two tokens
+ * MSA_ERR_BAD_OFFSETS, and tokens that no row owns are skipped: a row owns
+ * those of its tokens that lie below T, and none if its offset is negative
+ * (where offsets decrease, one token may be two rows', and which of them
+ * append takes is not defined).  Two tokens
  * of one call must not have the same place.  1 <= T <= 2^20.
  */
 msa_status msa_paged_append(const msa_paged_cache* cache, const msa_page_table* table,

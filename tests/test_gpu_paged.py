@@ -319,6 +319,40 @@ def test_index_bad_pages_leave_the_block_out():
     assert api.msa_paged_read_status(index, clear=True) == 11 and torch.equal(keys, before)
 
 
+@pytest.mark.parametrize("narrow", [False, True])
+@pytest.mark.parametrize("offs", [[0, 2, 4, 7],     # the last row ends past T
+                                  [0, 2, 9, 11],    # one before it does
+                                  [1, 2, 4, 6],     # token 0 is nobody's
+                                  [-3, 2, 4, 6]])   # nor are a row's that begins below 0
+def test_bad_offsets_leave_the_same_tokens_out_of_both_caches(offs, narrow):
+    gen, S, T = _gen(62), 16, 6
+    more = 2000 if narrow else 0  # tokens behind, so that append takes several to a thread block
+    kc, vc = (torch.zeros(8, S, 1, 64, dtype=BF, device=DEV) for _ in range(2))
+    keys = torch.zeros(8, S, 1, 64, dtype=BF, device=DEV)
+    k = _randn(gen, (T + more, 1, 64), BF)
+    first, table = [15, 3, 14], [[0, 1], [2, 3], [4, 5]]
+    owned = [(r, a, min(b, T + more)) for r, (a, b) in enumerate(zip(offs, offs[1:]))
+             if 0 <= a < T + more]
+    cache, index = api.PagedCache(kc, vc), api.PagedIndex(keys, torch.zeros(8, 1, 64, device=DEV))
+    args = (_i32(table), _i32(offs), _i32(first))
+    api.msa_paged_append(cache, k, k, *args)
+    api.msa_paged_index(index, k, *args)
+    code = 7 if offs[0] != 0 or offs[-1] > T + more else 0
+    assert api.msa_paged_read_status(cache) == code and api.msa_paged_read_status(index) == code
+    want, means = torch.zeros_like(kc), torch.zeros_like(index.means)
+    for r, a, b in owned:
+        for t in range(a, b):
+            p = first[r] + t - a
+            want[table[r][p // S], p % S] = k[t]
+        end = first[r] + b - a
+        seen = torch.cat([want[pg] for pg in table[r]])[:end]  # the keys before are zeros
+        means[table[r][(end - 1) // S]] = seen.double().sum(0).div(end).float()
+    for got in (kc, vc, keys):
+        assert torch.equal(got, want)
+    # 7 sums at most and a division, of values up to 6
+    assert (index.means - means).abs().max() <= 9 * U * 6
+
+
 # ------------------------------------------------------------------ select
 def _filled_index(lens, S, dim, seed, heads=4):
     rng, gen = np.random.default_rng(seed), _gen(seed)
