@@ -155,13 +155,18 @@ def _check(code: int, what: str):
         raise MSAError(code, what)
 
 
-_current_device = torch._C._cuda_getDevice
-_raw_stream = torch._C._cuda_getCurrentRawStream
+def _public_raw_stream(device: int) -> int:
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+# The current device, and its current stream's handle without a Stream object (4
+# us of a call), where this build of torch offers them; else the public calls.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _public_raw_stream)
 
 
 def _stream(stream) -> int:
     if stream is None:
-        # the current stream's handle without a Stream object (4 us of a call)
         return _raw_stream(_current_device())
     return stream.cuda_stream
 

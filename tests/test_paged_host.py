@@ -1,6 +1,7 @@
 """The paged-cache calls without a GPU: struct layouts, and every refusal that
 is decided on the host, in the C ABI and in the Python binding."""
 import ctypes
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -174,6 +175,24 @@ def test_binding_checks_layouts():
             api._tokens(x, "x", dt, None, h, d, CPU)
     with pytest.raises(ValueError):
         api._tokens(qkv, "x", torch.float16, 6, 72, 128, CPU)
+
+
+def test_binding_imports_without_a_cuda_build_of_torch(monkeypatch):
+    """Without torch's own bindings the module still loads and asks the public calls."""
+    for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+        monkeypatch.delattr(torch._C, name, raising=False)
+    spec = importlib.util.spec_from_file_location("api_without_cuda", api.__file__)
+    fresh = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(fresh)
+    asked = []
+
+    class Stream:
+        cuda_stream = 77
+
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device: asked.append(device) or Stream)
+    monkeypatch.setattr(fresh, "_current_device", lambda: 3)
+    assert fresh._stream(None) == 77 and asked == [3]
+    assert fresh._stream(Stream) == 77
 
 
 @pytest.mark.skipif(shutil.which("gcc") is None, reason="needs a C compiler")
