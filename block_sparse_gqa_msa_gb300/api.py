@@ -542,7 +542,7 @@ class PagedIndex:
 def _current(device):
     if device.index != _current_device():
         raise ValueError(f"the cache is on {device}, the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
+                         f"cuda:{_current_device()}")
 
 
 def _arg(t, name: str, dtype, shape, device) -> int:
@@ -609,7 +609,9 @@ def paged_decode_workspace_bytes(cache: PagedCache, rows: int, q_heads: int) -> 
 
 def msa_paged_read_status(cache, stream=None, clear: bool = False) -> int:
     """Synchronising read of the status word of a PagedCache or PagedIndex (0 =
-    OK; the lowest-numbered status otherwise).  ``clear`` resets the word."""
+    OK; the lowest-numbered status otherwise).  ``clear`` resets the word.  The
+    cache's device must be the current one, as for the calls that set it."""
+    _current(cache.device)
     code = int(lib().msa_paged_read_status(_ptr(cache.status), _stream(stream)))
     if clear:
         with torch.cuda.stream(stream):  # the current one if None

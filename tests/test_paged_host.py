@@ -177,6 +177,20 @@ def test_binding_checks_layouts():
         api._tokens(qkv, "x", torch.float16, 6, 72, 128, CPU)
 
 
+def test_status_of_a_cache_on_another_device_is_refused(monkeypatch):
+    # it would wait for the current device's stream, not for the one that the calls ran on
+    class Cache:
+        device = torch.device("cuda", 1)
+        status = torch.zeros(1, dtype=torch.int64)
+
+    monkeypatch.setattr(api, "_current_device", lambda: 0)
+    monkeypatch.setattr(api, "_raw_stream", lambda device: 0)
+    monkeypatch.setattr(api, "lib", lambda: pytest.fail("the library was called"))
+    for clear in (False, True):
+        with pytest.raises(ValueError, match="cuda:1"):
+            api.msa_paged_read_status(Cache, clear=clear)
+
+
 def test_binding_imports_without_a_cuda_build_of_torch(monkeypatch):
     """Without torch's own bindings the module still loads and asks the public calls."""
     for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
