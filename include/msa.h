@@ -443,7 +443,8 @@ msa_status msa_paged_read_status(const int64_t* status, msa_stream_t stream);
  * Append.  The call's tokens are compact: row r owns tokens row_offsets[r]
  * .. row_offsets[r+1]-1, which go to positions start_pos[r], start_pos[r]+1,
  * ...  Tokens at row_offsets[rows] and behind (padding of a captured batch)
- * are skipped: nothing is read for them nor written.
+ * are skipped: q, k and v hold T tokens, whatever the padding's values, and
+ * nothing is written for it.
  *   k, v   [T][kv_heads][head_dim] of the cache's type, tokens k_stride /
  *          v_stride elements apart (multiples of 8)
  *   q      [T][q_heads][head_dim] or NULL, tokens q_stride elements apart

@@ -181,6 +181,30 @@ def test_append_bad_places_among_many_tokens():
     assert torch.equal(k_out[fine], k[fine])
 
 
+@pytest.mark.parametrize("pad", [3, 1500])
+def test_append_padding_may_hold_anything(pad):
+    # beside few tokens and beside many (several to a thread block)
+    gen = _gen(63)
+    kc, vc = (torch.zeros(4, 16, 1, 64, dtype=FP, device=DEV) for _ in range(2))
+    q, k, v = (_randn(gen, (5 + pad, h, 64), FP) for h in (2, 1, 1))
+    for x, bad in ((q, float("nan")), (k, float("inf")), (v, float("nan"))):
+        x[5:] = bad
+    cache = api.PagedCache(kc, vc)
+    outs = [torch.full_like(x, 7.0) for x in (q, k)]
+    api.msa_paged_append(cache, k, v, _i32([[3, 1], [0, 2]]), _i32([0, 2, 5]), _i32([15, 14]),
+                         inv_freq=torch.rand(16, generator=gen, device=DEV), q=q, q_out=outs[0],
+                         k_out=outs[1])
+    assert api.msa_paged_read_status(cache) == 0
+    for x in (kc, vc, *outs):
+        assert bool(x.isfinite().all())
+    assert all(bool((x[5:] == 7).all()) for x in outs)
+    for c, new in ((kc, outs[1]), (vc, v)):
+        want = torch.zeros_like(c)
+        for t, (pg, slot) in enumerate(((3, 15), (1, 0), (0, 14), (0, 15), (2, 0))):
+            want[pg, slot] = new[t]
+        assert torch.equal(c, want)
+
+
 def test_append_wide_tokens_take_several_rounds():
     _append_case(BF, 128, 64, 256, 16, 128, False, [3], [2], 0, seed=9)
 
