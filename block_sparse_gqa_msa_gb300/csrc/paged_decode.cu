@@ -55,6 +55,7 @@
 // cluster are the time.
 #include <cooperative_groups.h>
 
+#include "asked_once.cuh"
 #include "paged.cuh"
 #include "sm100.cuh"
 
@@ -1066,30 +1067,26 @@ size_t decode_workspace(int32_t dim) {
 // leave SMs over), asked for once a device and size.
 template <typename T, int kDim>
 int cluster_room(void (*kernel)(DecodeArgs), int cluster) {
-  constexpr int kDevices = 16;
-  static std::atomic<int> known[kDevices][kMaxCluster];
+  static AskedOnce<64, kMaxCluster> known;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  std::atomic<int>* slot = dev < kDevices ? &known[dev][cluster - 1] : nullptr;
-  if (slot && slot->load() > 0) return slot->load() - 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(cluster));
-  cfg.blockDim = dim3(kDecThreads);
-  cfg.dynamicSmemBytes = DecodeShape<kDim>::kSmemCluster;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = unsigned(cluster);
-  attr.val.clusterDim.y = 1;
-  attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+  return known.get(dev, cluster - 1, [&] {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(cluster));
+    cfg.blockDim = dim3(kDecThreads);
+    cfg.dynamicSmemBytes = DecodeShape<kDim>::kSmemCluster;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = unsigned(cluster);
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess) return n;
     cudaGetLastError();  // no room known: no clusters
-    return 0;
-  }
-  if (slot) slot->store(n + 1);
-  return n;
+    return -1;
+  });
 }
 
 template <typename T, int kDim>

@@ -524,8 +524,10 @@ msa_status msa_paged_decode_workspace_bytes(const msa_paged_cache* cache, int32_
  *   workspace  device, 16-byte aligned, >= msa_paged_decode_workspace_bytes;
  *           needs no initialisation; calls that may overlap in time (on two
  *           streams, in graphs replayed side by side) need one each
- * Results are the same from call to call on one kind of device: how the keys
- * are split depends on the lengths and sizes alone.
+ * Results are the same from call to call on one device: how the keys are split
+ * depends on the lengths, the sizes (the table's width is one of them) and the
+ * device alone.  Two devices of one kind may split them differently, and results
+ * then differ by the rounding of 32-bit sums.
  * MSA_ERR_TIMEOUT in the status word: a bounded wait of the kernel gave up, and
  * outputs of that call are missing.
  * A row that sees no key (kv_len 0, no slot used) gets O = 0, LSE = -inf; so

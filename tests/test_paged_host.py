@@ -209,6 +209,32 @@ def test_binding_imports_without_a_cuda_build_of_torch(monkeypatch):
     assert fresh._stream(Stream) == 77
 
 
+@pytest.mark.skipif(shutil.which("g++") is None, reason="needs a C++ compiler")
+def test_a_question_to_the_device_is_asked_once_also_if_it_fails(tmp_path):
+    """What decides the way of a call never changes within a process."""
+    src, exe = tmp_path / "t.cpp", tmp_path / "t"
+    src.write_text("""
+#include <cstdio>
+#include "asked_once.cuh"
+static msa::AskedOnce<4, 8> known;
+int main() {
+  int asked = 0;
+  auto says = [&](int x) { return [&asked, x] { ++asked; return x; }; };
+  const int got[] = {known.get(0, 1, says(-1)), known.get(0, 1, says(9)),  // failed: 0, and stays
+                     known.get(0, 2, says(0)), known.get(0, 2, says(9)),
+                     known.get(3, 1, says(38)), known.get(3, 1, says(-1)),
+                     known.get(4, 0, says(9)), known.get(-1, 0, says(9))};
+  for (int x : got) std::printf("%d ", x);
+  std::printf("%d", asked);
+}
+""")
+    csrc = os.path.join(os.path.dirname(api.__file__), "csrc")
+    subprocess.run(["g++", "-std=c++17", "-Wall", "-Werror", "-I", csrc, str(src), "-o", str(exe)],
+                   check=True)
+    out = subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout
+    assert out.split() == "0 0 0 0 38 38 0 0 3".split()
+
+
 @pytest.mark.skipif(shutil.which("gcc") is None, reason="needs a C compiler")
 def test_paged_struct_layouts_match_header():
     mirrors = {"msa_paged_cache": api.MsaPagedCacheStruct,
