@@ -148,3 +148,78 @@ def decode_bounds(k_cache, v_cache, q, table, lens, scale, step: float, tiny: fl
                 + m * rest * np.abs(V[j, g]).max() * np.exp(s.max(1) - L[r, h])[:, None]
             BL[r, h] = 1.01 * e + 4 * u * (np.abs(L[r, h]) + biggest + np.log(m) + 1)
     return O, L, BO, BL
+
+
+# ------------------------------------------------------------------ rows that show every key
+# decode_bounds grows with the number of keys, while O over random values shrinks
+# with its root: of a long row it no longer sees a part that is missing.  Here
+# page p of the pool holds STRIPE in one channel (p + head) % dim and zeros in
+# the others, and all its keys score levels[p], so every stretch of a row is most
+# of what one channel holds.
+STRIPE = 64.0
+
+
+def striped_values(pages: int, page_size: int, heads: int, dim: int) -> np.ndarray:
+    v = np.zeros((pages, page_size, heads, dim))
+    for p in range(pages):
+        for g in range(heads):
+            v[p, :, g, (p + g) % dim] = STRIPE
+    return v
+
+
+def striped(table_row, n: int, S: int, levels, heads: int, dim: int, times=None):
+    """(O [heads, dim], LSE) of a row of n keys over such pages, in closed form;
+    times [n]: how often each key counts (once, as it should)."""
+    page = np.asarray(table_row)[np.arange(n) // S]
+    w = np.bincount(page, weights=times, minlength=len(levels)) * np.exp(levels)
+    O = np.zeros((heads, dim))
+    for g in range(heads):
+        np.add.at(O[g], (np.arange(len(levels)) + g) % dim, STRIPE * w / w.sum())
+    return O, float(np.log(w.sum()))
+
+
+def striped_bounds(O, L: float, n: int, levels, dim: int, step: float, tiny: float):
+    """Element-wise bounds (O, LSE) for such a row, q all ones.
+
+    Equal levels of 0: every weight is the same power of two, every sum a whole
+    number of them below 2^24, so sums, factors and joins are exact.  What is
+    left is 1 / l, the product with it and the output's rounding; for the LSE
+    the logarithm, its sum with the maximum (below 32 both) and the product
+    with ln 2.  Else as decode_bounds, with sum p|v| = O."""
+    u = 2.0 ** -24
+    levels = np.asarray(levels)
+    if not levels.any():
+        return (step + 4 * u) * O + tiny, 8 * u * (L + 7)
+    top = float(np.abs(levels).max())
+    e = (dim + 4) * u * top + u * (8 + 4 * top) + u * (4 * (n / 16 + 400) + n)
+    rest = tiny * 2.0 ** -7 if tiny > 2.0 ** -100 else tiny
+    small = n * rest * STRIPE * np.exp(float(levels.max()) - L)
+    return (1.01 * (2 * e + step ** 2) + step) * O + tiny + small, \
+        1.01 * e + 4 * u * (abs(L) + top + np.log(n) + 1)
+
+
+# Long rows for them: type ("bf16" or "fp16"), channels, key heads, query heads a
+# key head, page size, lengths, range of the levels (0: equal ones).
+STRIPED_CASES = {
+    "bf16, one row over all thread blocks": ("bf16", 128, 1, 16, 128, [90001], 0.0),
+    "fp16, one row over all thread blocks": ("fp16", 64, 2, 5, 256, [70000, 3, 1], 0.0),
+    "bf16, short runs": ("bf16", 128, 4, 16, 128, [330001, 5, 70000, 1], 0.0),
+    "fp16, short runs": ("fp16", 64, 4, 5, 64, [700003], 0.0),
+    "bf16, maxima that differ": ("bf16", 128, 1, 16, 128, [90001, 40000], 16.0),
+    "fp16, maxima that differ": ("fp16", 64, 2, 5, 256, [70000, 3], 8.0),
+}
+
+
+def striped_rows(case):
+    """(table [rows, width], levels [pages]): a page of the pool for each channel;
+    equal levels: in a mixed order; else each page for one stretch of the row,
+    levels rising along even rows and falling along odd ones.  A level is a whole
+    number of eighths, which a key of equal channels gives exactly."""
+    _, dim, _, _, S, lens, span = case
+    width = -(-max(lens) // S) + 1
+    i = np.arange(width)
+    if span == 0:
+        return np.stack([(i * 37 + r) % dim for r in range(len(lens))]), np.zeros(dim)
+    table = np.stack([np.minimum(i * dim // -(-n // S), dim - 1) for n in lens])
+    table[1::2] = dim - 1 - table[1::2]
+    return table, np.arange(dim) / dim * span

@@ -702,6 +702,36 @@ def _decode_shared_pages(dt, dim, kv, share, S, lens, sparse, seed):
     _within(_np(o), O, BO, "O")
 
 
+@pytest.mark.parametrize("name", paged.STRIPED_CASES)
+def test_decode_counts_every_key_of_a_long_row_once(name):
+    """Rows that show a part left out or counted twice, where random ones do not:
+    tests/test_paged_oracle.py plants both."""
+    case = paged.STRIPED_CASES[name]
+    dt, dim, kv, share, S, lens, span = case
+    dt = BF if dt == "bf16" else FP
+    table, levels = paged.striped_rows(case)
+    scale = 0.125
+    gen = _gen(64)
+    vc = torch.as_tensor(paged.striped_values(dim, S, kv, dim), device=DEV).to(dt)
+    q = torch.ones(len(lens), kv * share, dim, dtype=dt, device=DEV)
+    if span:
+        kc = torch.as_tensor(levels / (dim * scale), device=DEV).to(dt)
+        assert np.array_equal(_np(kc) * dim * scale, levels)
+        kc = kc[:, None, None, None].expand(dim, S, kv, dim).contiguous()
+    else:
+        kc, q = _pool(gen, dim, S, kv, dim, dt), torch.zeros_like(q)
+    cache = api.PagedCache(kc, vc)
+    o, lse = api.msa_paged_decode(cache, q, _i32(table), _i32(lens), scale)
+    torch.cuda.synchronize()
+    assert api.msa_paged_read_status(cache) == 0
+    for r, n in enumerate(lens):
+        O, L = paged.striped(table[r], n, S, levels, kv, dim)
+        BO, BL = paged.striped_bounds(O, L, n, levels, dim, HALF[dt], TINY[dt])
+        O, BO = (np.repeat(x, share, axis=0) for x in (O, BO))
+        _within(_np(o[r]), O, BO, f"O of row {r}")
+        _within(_np(lse[r]), np.full(kv * share, L), np.full(kv * share, BL), f"LSE of row {r}")
+
+
 def test_decode_enough_tiles_for_the_short_runs():
     _decode_shared_pages(BF, 128, 4, 16, 128, [330001, 5, 70000], False, seed=31)
     _decode_shared_pages(FP, 64, 4, 5, 64, [700003], False, seed=32)

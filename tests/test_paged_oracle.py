@@ -3,6 +3,7 @@ training oracle where both compute the same thing (no GPU)."""
 import math
 
 import numpy as np
+import pytest
 import torch
 
 import oracle
@@ -102,3 +103,37 @@ def test_decode_equal_scores_average_the_values():
     assert np.allclose(lse, math.log(3))
     o, lse = paged.decode(kc, vc, np.ones((1, 2, 4)), table, [0], 1.0)
     assert (o == 0).all() and (lse == -np.inf).all()
+
+
+def test_striped_rows_are_what_the_oracle_gives():
+    for levels in (np.zeros(8), np.arange(8) / 4):
+        table = np.array([[3, 0, 7, 7, 1, 5, 2]])
+        k = np.ones((8, 4, 2, 8)) * levels[:, None, None, None] / 8
+        v = paged.striped_values(8, 4, 2, 8)
+        for n in (1, 4, 23, 28):
+            o, lse = paged.decode(k, v, np.ones((1, 6, 8)), table, [n], 1.0)
+            O, L = paged.striped(table[0], n, 4, levels, 2, 8)
+            assert np.allclose(o[0], np.repeat(O, 3, axis=0)) and np.allclose(lse, L)
+
+
+@pytest.mark.parametrize("name", paged.STRIPED_CASES)
+@pytest.mark.parametrize("times", [0, 2])
+def test_a_part_of_a_striped_row_lost_or_counted_twice_is_out_of_bounds(name, times):
+    """Mistakes of the split over 304 thread blocks, planted here: with equal
+    levels one tile of a warp in O and in LSE, else a run in O."""
+    case = paged.STRIPED_CASES[name]
+    dt, dim, _, _, S, lens, span = case
+    step, tiny = (2.0 ** -8, 2.0 ** -134) if dt == "bf16" else (2.0 ** -11, 2.0 ** -25)
+    table, levels = paged.striped_rows(case)
+    for r, n in enumerate(lens):
+        if n < 10000:
+            continue
+        O, L = paged.striped(table[r], n, S, levels, 1, dim)
+        BO, BL = paged.striped_bounds(O, L, n, levels, dim, step, tiny)
+        part = n // 304 if span else 2048 // dim
+        for at in range(0, n - part, max(n // 150 // part, 1) * part):
+            count = np.ones(n)
+            count[at:at + part] = times
+            o, lse = paged.striped(table[r], n, S, levels, 1, dim, count)
+            assert (np.abs(o - O) > BO).any(), at
+            assert span or abs(lse - L) > BL, at
