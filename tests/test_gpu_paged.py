@@ -416,6 +416,35 @@ def test_select_equals_the_training_selection(lens, S, dim, force):
         assert torch.equal(got, ref[:, at])
 
 
+@pytest.mark.parametrize("heads,dim", [(1, 8), (3, 40), (64, 24), (5, 120), (7, 104), (2, 72)])
+@pytest.mark.parametrize("force", [False, True])
+def test_select_of_any_heads_and_channels(heads, dim, force):
+    """Against the plain statement, on means and queries whose products and sums
+    are exact in 32 bits (whole numbers of 2^-11 below 2^6), so that the choice
+    does not depend on the order of a sum."""
+    lens, S = [128 * 40 + 5, 1, 2049, 128 * 300, 0, 128 * 17], 32
+    rng, gen = np.random.default_rng(heads * dim), _gen(heads * dim)
+    pool, table = _pages(rng, lens, S)
+    grid = torch.randint(-64, 65, (pool, heads, dim), generator=gen, device=DEV).float() / 512
+    iq = (torch.randint(-16, 17, (len(lens), heads, dim), generator=gen, device=DEV) / 4.0).to(BF)
+    index = api.PagedIndex(torch.zeros(pool, S, heads, dim, dtype=BF, device=DEV), grid)
+    got = api.msa_paged_select(index, iq, _i32(table), _i32(lens), force_local=force)
+    assert api.msa_paged_read_status(index) == 0
+    want = np.full((heads, len(lens), 16), -1)
+    for r, n in enumerate(lens):
+        nb = -(-n // 128)
+        if nb == 0:
+            continue
+        last = np.minimum(np.arange(nb) * 128 + 127, n - 1)
+        score = np.einsum("vhd,hd->hv", _np(grid)[table[r, last // S]], _np(iq[r]))
+        if force:
+            score[:, [0, nb - 1]] = np.inf
+        for h in range(heads):
+            best = np.sort(np.argsort(-score[h], kind="stable")[:16])
+            want[h, r, :len(best)] = best
+    assert np.array_equal(got.cpu().numpy(), want)
+
+
 def test_select_ties_go_to_the_lowest_block():
     n = 128 * 40
     gen = _gen(4)
