@@ -575,6 +575,8 @@ def test_decode_many_rows():
     _decode_case(BF, 64, 2, 4, 16, rng.integers(0, 200, 700).tolist(), False, seed=8)
     _decode_case(BF, 128, 4, 16, 32, rng.integers(0, 700, 90).tolist(), True, seed=9)
     # 64 channels: two heads at once, and each alone (an odd number, pages by head, blocks)
+    # (the kernel reads a head's 64 channels alone in each of them: heads beside one another
+    # in a token, an odd number of them, pages by head, selected blocks)
     lens = rng.integers(0, 300, 200).tolist()
     _decode_case(FP, 64, 4, 16, 32, lens, False, seed=40)
     _decode_case(FP, 64, 3, 5, 32, lens, False, seed=41)
