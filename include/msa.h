@@ -364,9 +364,16 @@ msa_status msa_select_blocks(const void* iq, const void* ik, int64_t T, int32_t 
  *   msa_paged_decode   attention of each row's newest token over the cache:
  *                      over all keys, or over the blocks of q2k
  *
- * A prompt goes through append and index in one call for all its tokens; the
- * rotated queries and keys that append hands back go through
- * msa_select_blocks, msa_build_plan and msa_forward.
+ * A prompt goes through append and index in one call for all its tokens.  If
+ * it begins at position 0 and has the shape that these calls take (64 query and
+ * 4 key heads of 128 channels, bf16), the rotated queries and keys that append
+ * hands back go through msa_select_blocks, msa_build_plan and msa_forward.
+ * There is no call that selects or attends for all tokens of a prompt behind a
+ * cached prefix at once.  Each such token can be a row of its own in select and
+ * decode, with the same pages and its own length, once all of them have been
+ * appended and indexed; the prefix is then read once for each token.  select
+ * is right for such rows with force_local alone: the mean of a token's own
+ * block already holds the keys behind it.
  *
  * Rows and pages.  Token j of row r lives in page page_table[r][j / S], slot
  * j % S, S the page size.  A row's table entries past its tokens are never

@@ -1025,6 +1025,39 @@ def test_prompt_then_steps_as_served():
         check_lse(_np(sl), L)
 
 
+@pytest.mark.parametrize("S", [16, 64, 256])
+def test_tokens_behind_a_cached_prefix_one_row_each(S):
+    """Several new tokens of a row as rows of their own over the same pages, as the
+    header describes it: selection with force_local equals the training path's
+    for the whole document, attention its forward's, whatever the page size."""
+    gen, rng = _gen(65), np.random.default_rng(65)
+    n, cached, dim = 2900, 2437, 32  # the prefix ends inside a block; new tokens over four blocks
+    pool, table = _pages(rng, [n], S)
+    q, k, v = (_randn(gen, (n, h, 128), BF) for h in (64, 4, 4))
+    iq, ik = (_randn(gen, (n, 4, dim), BF) for _ in range(2))
+    cache = api.PagedCache(*(torch.zeros(pool, S, 4, 128, dtype=BF, device=DEV) for _ in range(2)))
+    index = api.PagedIndex(torch.zeros(pool, S, 4, dim, dtype=BF, device=DEV),
+                           torch.full(api.paged_means_shape(pool, S, 4, dim), float("nan"),
+                                      device=DEV))
+    t = _i32(table)
+    for a, b in ((0, cached), (cached, n)):
+        offs, start = _i32([0, b - a]), _i32([a])
+        api.msa_paged_append(cache, k[a:b], v[a:b], t, offs, start)
+        api.msa_paged_index(index, ik[a:b], t, offs, start)
+    new = torch.arange(cached, n, device=DEV)
+    rows, lens = t.expand(len(new), -1).contiguous(), (new + 1).int()
+    chosen = api.msa_paged_select(index, iq[new], rows, lens)
+    o, lse = api.msa_paged_decode(cache, q[new], rows, lens, 128 ** -0.5, q2k=chosen)
+    doc = _i32([0, n])
+    q2k = api.msa_select_blocks(iq, ik, doc)
+    want, want_lse = api.msa_forward(api.msa_build_plan(q2k, doc), q, k, v, 128 ** -0.5)
+    torch.cuda.synchronize()
+    assert api.msa_paged_read_status(cache) == 0 and api.msa_paged_read_status(index) == 0
+    assert torch.equal(chosen, q2k[:, new])
+    check_o(_np(o), _np(want[new]))
+    check_lse(_np(lse), _np(want_lse[new]))
+
+
 def test_a_step_captured_and_replayed():
     """One step in a CUDA graph, replayed with other lengths, tables and
     inputs, some rows not in use; a second graph of another batch size beside
