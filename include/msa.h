@@ -521,7 +521,9 @@ msa_status msa_paged_decode_workspace_bytes(const msa_paged_cache* cache, int32_
  *           h / n
  *   kv_len  int32 [rows] device: row r attends keys 0 .. kv_len[r]-1 (the
  *           new token's key, at kv_len[r]-1, has been appended)
- *           rows * kv_heads * width * page_size of the table <= 2^36
+ *           rows * kv_heads * width * page_size of the table <= 2^36; what is
+ *           launched follows the table's width, so a table much wider than the
+ *           rows need costs few short rows without q2k 1 to 2 us
  *   q2k     int32 [kv_heads][rows][16] device, or NULL: of these keys only
  *           those whose block (key / 128) is in the set q2k[g][r][:], -1 = an
  *           unused slot.  Other values outside [0, blocks of the row) set
