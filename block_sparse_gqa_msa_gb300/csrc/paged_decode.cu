@@ -49,8 +49,8 @@
 // 128 rows of 500 to 16384 tokens, selected blocks, 508 MB: 89 us, 5.7 TB/s:
 // the first bytes come after 4 us, the runs end up to 8 % apart, the join
 // takes 3.5 us.  77 rows of up to 12000 tokens, 24 heads on 8 of 64 channels,
-// 950 MB: 151 to 165 us, 5.8 to 6.3 TB/s: a head's 128 bytes a token are read
-// alone (head-major pages: 147).  One row: 6.9 us for 1000 tokens, 8.7 for 16
+// 950 MB: 149 to 165 us, 5.8 to 6.4 TB/s: a head's 128 bytes a token are read
+// alone (head-major pages: 147).  One row: 7.0 us for 1000 tokens, 8.8 for 16
 // blocks; dependent loads (length and slots, page, keys) and one join in the
 // cluster are the time.
 #include <cooperative_groups.h>

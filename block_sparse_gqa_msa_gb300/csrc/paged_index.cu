@@ -24,7 +24,8 @@
 //                 us): 21.5 us (62 with each lane reading its block's row from
 //                 memory); 3 us before the first means come, the longest rows,
 //                 two CTAs each, and the lists are the rest.  One row of 1024
-//                 blocks: 5.0 us (5.2 with the lists sorted and merged).
+//                 blocks: 4.8 to 5.0 us (5.3 with the lists sorted and merged, which made no
+//                 difference to the batch).
 #include <cooperative_groups.h>
 
 #include <utility>
@@ -420,10 +421,10 @@ cudaError_t launch_select_as(const SelectArgs& a, int cluster, cudaStream_t s) {
 
 cudaError_t launch_paged_select(const SelectArgs& a, cudaStream_t s) {
   // A cluster's CTAs: one for every 128 blocks that the table has room for, while
-  // the batch leaves SMs without any (64 rows of up to 1024 blocks: 22 us with 2,
-  // 24 with 4).  Four warps a CTA, four CTAs an SM; batches that would not be on
-  // the chip at once so take two warps (256 rows of 64 blocks: 6.0 us, with
-  // four 8.8; one row of 1024: 7.1, with four 5.4).
+  // the batch leaves SMs without any (64 rows of up to 1024 blocks: 27.3 us with 1,
+  // 21.3 with 2, 22.7 with 4).  Four warps a CTA, four CTAs an SM; batches that would not be on
+  // the chip at once so take two warps (256 rows of 64 blocks: 6.1 us, with
+  // four 9.0; one row of 1024: 6.4, with four 4.8).
   const int64_t room = ((int64_t(a.table.width) << a.table.shift) + kBlock - 1) / kBlock;
   const int64_t units = int64_t(a.table.rows) * a.heads, sms = device_sm_count();
   int cluster = 1;
