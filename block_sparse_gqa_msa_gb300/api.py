@@ -27,7 +27,7 @@ STATUS = {
     0: "MSA_OK", 1: "MSA_ERR_INVALID_ARG", 2: "MSA_ERR_UNSUPPORTED", 3: "MSA_ERR_ALIGNMENT",
     4: "MSA_ERR_WORKSPACE", 5: "MSA_ERR_CUDA", 6: "MSA_ERR_BAD_Q2K", 7: "MSA_ERR_BAD_OFFSETS",
     8: "MSA_ERR_TIMEOUT", 9: "MSA_ERR_CAPACITY", 10: "MSA_ERR_RANGE",
-    11: "MSA_ERR_BAD_PAGE",
+    11: "MSA_ERR_BAD_PAGE", 12: "MSA_ERR_BAD_TREE",
 }
 MSA_OK = 0
 
@@ -81,6 +81,17 @@ class MsaPageTableStruct(ctypes.Structure):
                 ("width", ctypes.c_int32)]
 
 
+class MsaNormRopeStruct(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("q_stride", ctypes.c_int64),
+                ("k_stride", ctypes.c_int64), ("q_weight", ctypes.c_void_p),
+                ("k_weight", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+                ("inv_freq", ctypes.c_void_p), ("T", ctypes.c_int64), ("q_heads", ctypes.c_int32),
+                ("k_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("weight_dtype", ctypes.c_int32),
+                ("eps", ctypes.c_float)]
+
+
 DQ_ACCUM = {"f16": 0, "bf16": 1, "f32": 2}
 O_ACCUM = {"f32": 0, "bf16": 1}
 
@@ -97,6 +108,7 @@ _PLAN = ctypes.POINTER(MsaPlanStruct)
 _CACHE = ctypes.POINTER(MsaPagedCacheStruct)
 _INDEX = ctypes.POINTER(MsaPagedIndexStruct)
 _TABLE = ctypes.POINTER(MsaPageTableStruct)
+_NORM = ctypes.POINTER(MsaNormRopeStruct)
 
 SIGNATURES = {
     "msa_status_string": ([_I32], ctypes.c_char_p),
@@ -129,6 +141,15 @@ SIGNATURES = {
     "msa_paged_select": ([_INDEX, _TABLE, _P, _P, _I32, _P, _P], _I32),
     "msa_paged_decode_workspace_bytes": ([_CACHE, _I32, _I32, ctypes.POINTER(_SZ)], _I32),
     "msa_paged_decode": ([_CACHE, _TABLE, _P, _P, _I32, _F, _P, _P, _P, _P, _SZ, _P], _I32),
+    "msa_norm_rope": ([_NORM, _P, _P, _P], _I32),
+    "msa_norm_rope_workspace_bytes": ([_I32, ctypes.POINTER(_SZ)], _I32),
+    "msa_norm_rope_backward": ([_NORM, _P, _P, _P, _P, _P, _P, _P, _SZ, _P], _I32),
+    "msa_paged_tree_workspace_bytes": ([_CACHE, _I32, _I64, _I32, ctypes.POINTER(_SZ)], _I32),
+    "msa_paged_tree": ([_CACHE, _TABLE, _P, _P, _P, _I64, _P, _I32, _F, _P, _P, _P, _P, _SZ, _P],
+                       _I32),
+    "msa_tree_verify": ([_P, _I64, _P, _I64, _P, _P, _P, _I32, _I64, _I32, _P, _P, _I32, _P, _P,
+                         _P, _P], _I32),
+    "msa_paged_compact": ([_CACHE, _TABLE, _P, _P, _I32, _P, _P, _P], _I32),
 }
 
 
@@ -754,3 +775,243 @@ def msa_paged_decode(cache: PagedCache, q: torch.Tensor, page_table: torch.Tenso
         _arg(workspace, "workspace", torch.uint8, (nbytes,), device), nbytes, _stream(stream)),
         "msa_paged_decode")
     return o, lse
+
+
+# ---------------------------------------------------------------- norm and rotation
+WEIGHT_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+def _norm_args(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved):
+    """The struct of a call, and its device, T, heads of q and k, head_dim, type."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be a [T, q_heads, head_dim] tensor")
+    if not q.is_cuda:
+        raise ValueError("q must be a CUDA tensor")
+    device, dt = q.device, q.dtype
+    if device.index != _current_device():
+        raise ValueError(f"q is on {device}, the current device is cuda:{_current_device()}")
+    if dt not in PAGED_DTYPES:
+        raise TypeError(f"q must be one of {tuple(PAGED_DTYPES)}, got {dt}")
+    T, heads, dim = q.shape
+    qs = _tokens(q, "q", dt, None, None, dim, device)
+    ks = _tokens(k, "k", dt, T, None, dim, device)
+    kv = k.shape[1]
+    if not isinstance(q_weight, torch.Tensor) or q_weight.dtype not in (torch.float32, dt):
+        raise TypeError(f"q_weight must be torch.float32 or {dt}")
+    wd = q_weight.dtype
+    wq = _arg(q_weight, "q_weight", wd, (dim,), device)
+    wk = _arg(k_weight, "k_weight", wd, (dim,), device)
+    rot, freq, pos = 0, None, None
+    if inv_freq is not None:
+        rot = 2 * inv_freq.numel()
+        freq = _arg(inv_freq, "inv_freq", torch.float32, (rot // 2,), device)
+        if positions is None:
+            raise ValueError("inv_freq needs positions")
+    if positions is not None:
+        pos = _arg(positions, "positions", torch.int32, (T,), device)
+    args = MsaNormRopeStruct(q.data_ptr(), k.data_ptr(), qs, ks, wq, wk, pos, freq, T, heads, kv,
+                             dim, rot, 1 if interleaved else 0, PAGED_DTYPES[dt],
+                             WEIGHT_DTYPES[wd], eps)
+    return args, device, T, heads, kv, dim, dt
+
+
+def norm_rope_workspace_bytes(head_dim: int) -> int:
+    n = _SZ(0)
+    _check(lib().msa_norm_rope_workspace_bytes(head_dim, ctypes.byref(n)),
+           "msa_norm_rope_workspace_bytes")
+    return int(n.value)
+
+
+def _out(t, name, shape, dtype, device, stream):
+    if t is None:
+        t = _empty(shape, dtype, device, stream)
+        return t, t.data_ptr()
+    return t, _arg(t, name, dtype, shape, device)
+
+
+def msa_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor,
+                  k_weight: torch.Tensor, positions: torch.Tensor | None = None,
+                  inv_freq: torch.Tensor | None = None, eps: float = 1e-6,
+                  interleaved: bool = False, q_out: torch.Tensor | None = None,
+                  k_out: torch.Tensor | None = None, stream=None):
+    """Every head of q [T, q_heads, head_dim] and k [T, k_heads, head_dim] (bf16 or
+    fp16, head_dim 64 or 128, each token contiguous, any token stride) scaled to
+    unit mean square, times its weight [head_dim] (fp32 or q's type), then rotated
+    by positions (int32 [T]) as ``msa_paged_append`` rotates; without inv_freq
+    nothing is rotated.  Returns (q_out, k_out), contiguous; q and k themselves
+    may be given for them where they are contiguous.  ``autograd.msa_norm_rope``
+    is the differentiable form."""
+    args, device, T, heads, kv, dim, dt = _norm_args(q, k, q_weight, k_weight, positions, inv_freq,
+                                                     eps, interleaved)
+    q_out, qo = _out(q_out, "q_out", (T, heads, dim), dt, device, stream)
+    k_out, ko = _out(k_out, "k_out", (T, kv, dim), dt, device, stream)
+    _check(lib().msa_norm_rope(ctypes.byref(args), qo, ko, _stream(stream)), "msa_norm_rope")
+    return q_out, k_out
+
+
+def msa_norm_rope_backward(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.Tensor,
+                           k: torch.Tensor, q_weight: torch.Tensor, k_weight: torch.Tensor,
+                           positions: torch.Tensor | None = None,
+                           inv_freq: torch.Tensor | None = None, eps: float = 1e-6,
+                           interleaved: bool = False, dq: torch.Tensor | None = None,
+                           dk: torch.Tensor | None = None,
+                           workspace: torch.Tensor | None = None, stream=None):
+    """(dq, dk, dq_weight, dk_weight) of ``msa_norm_rope`` from the gradients of its
+    results (contiguous) and what it was called with; the weights' gradients are
+    fp32.  A workspace serves one call at a time."""
+    args, device, T, heads, kv, dim, dt = _norm_args(q, k, q_weight, k_weight, positions, inv_freq,
+                                                     eps, interleaved)
+    gq = _arg(dq_out, "dq_out", dt, (T, heads, dim), device)
+    gk = _arg(dk_out, "dk_out", dt, (T, kv, dim), device)
+    dq, dqp = _out(dq, "dq", (T, heads, dim), dt, device, stream)
+    dk, dkp = _out(dk, "dk", (T, kv, dim), dt, device, stream)
+    dw = _empty((2, dim), torch.float32, device, stream)
+    if workspace is None:
+        workspace = _empty(norm_rope_workspace_bytes(dim), torch.uint8, device, stream)
+    nbytes = workspace.numel()
+    _check(lib().msa_norm_rope_backward(
+        ctypes.byref(args), gq, gk, dqp, dkp, dw.data_ptr(), dw.data_ptr() + 4 * dim,
+        _arg(workspace, "workspace", torch.uint8, (nbytes,), device), nbytes, _stream(stream)),
+        "msa_norm_rope_backward")
+    return dq, dk, dw[0], dw[1]
+
+
+# ---------------------------------------------------------------- drafted tokens
+MAX_TREE = 64
+
+
+def paged_tree_workspace_bytes(cache: PagedCache, rows: int, tokens: int, q_heads: int) -> int:
+    n = _SZ(0)
+    _check(lib().msa_paged_tree_workspace_bytes(cache.ref(), rows, tokens, q_heads,
+                                                ctypes.byref(n)),
+           "msa_paged_tree_workspace_bytes")
+    return int(n.value)
+
+
+def msa_paged_tree(cache: PagedCache, q: torch.Tensor, page_table: torch.Tensor,
+                   row_offsets: torch.Tensor, kv_len: torch.Tensor, softmax_scale: float,
+                   parents: torch.Tensor | None = None, q2k: torch.Tensor | None = None,
+                   o: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                   workspace: torch.Tensor | None = None, stream=None):
+    """Attention of each row's drafted tokens over its cached ones and over the
+    drafted tokens on their own path: (O [T, q_heads, head_dim], LSE fp32 [T,
+    q_heads]).
+
+    q: [T, q_heads, head_dim] of the cache's type, up to 16 query heads a key
+    head.  Row r owns tokens row_offsets[r] .. row_offsets[r+1]-1 (int32 [rows +
+    1]), 64 at most; its token j lies in the cache at slot kv_len[r] + j (int32
+    [rows]) and continues its token parents[j] (int32 [T], numbered within the
+    row, -1: the cached ones; None: each continues the one before).  q2k: int32
+    [kv_heads, T, 16], the blocks of the cached tokens that each token attends, or
+    None for all.  Rows of O and LSE that no row owns (padding) are left as they
+    were.  A workspace serves one call at a time.  Not differentiable."""
+    device = cache.device
+    _current(device)
+    table = _table(page_table, device)
+    rows = table.rows
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be a [T, q_heads, head_dim] tensor")
+    T, heads = q.shape[:2]
+    shape = (T, heads, cache.head_dim)
+    qp = _arg(q, "q", cache.dtype, shape, device)
+    offs = _arg(row_offsets, "row_offsets", torch.int32, (rows + 1,), device)
+    lens = _arg(kv_len, "kv_len", torch.int32, (rows,), device)
+    up = None if parents is None else _arg(parents, "parents", torch.int32, (T,), device)
+    slots = None
+    if q2k is not None:
+        slots = _arg(q2k, "q2k", torch.int32, (cache.kv_heads, T, TOPK), device)
+    o, op = _out(o, "o", shape, cache.dtype, device, stream)
+    lse, lp = _out(lse, "lse", (T, heads), torch.float32, device, stream)
+    if workspace is None:
+        workspace = _empty(paged_tree_workspace_bytes(cache, rows, T, heads), torch.uint8, device,
+                           stream)
+    nbytes = workspace.numel()
+    _check(lib().msa_paged_tree(
+        cache._ref, ctypes.byref(table), offs, lens, up, T, qp, heads, float(softmax_scale), slots,
+        op, lp, _arg(workspace, "workspace", torch.uint8, (nbytes,), device), nbytes,
+        _stream(stream)), "msa_paged_tree")
+    return o, lse
+
+
+def _probabilities(x, name: str, shape, device) -> int:
+    """Row stride of fp32 [T, vocab] with contiguous rows."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if x.dtype is not torch.float32:
+        raise TypeError(f"{name} must be torch.float32, got {x.dtype}")
+    if x.device != device:
+        raise ValueError(f"{name} must be on {device}, got {x.device}")
+    if tuple(x.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(x.shape)}")
+    stride, step = x.stride()
+    T, V = shape
+    if (V > 1 and step != 1) or (T > 1 and stride < V):
+        raise ValueError(f"{name}: a row must be contiguous, rows must not overlap")
+    return stride if T > 1 else V
+
+
+def msa_tree_verify(target: torch.Tensor, tokens: torch.Tensor, row_offsets: torch.Tensor,
+                    u: torch.Tensor, u_last: torch.Tensor, draft: torch.Tensor | None = None,
+                    parents: torch.Tensor | None = None, max_path: int = MAX_TREE,
+                    path: torch.Tensor | None = None, count: torch.Tensor | None = None,
+                    last: torch.Tensor | None = None, stream=None):
+    """Which drafted tokens of each row stay, and the token behind them: (path
+    int32 [rows, max_path], count int32 [rows], last int32 [rows]).
+
+    target: fp32 [T, vocab], row t the target's distribution behind token t; draft:
+    the drafting model's, or None for drafts that were not drawn; tokens, parents:
+    int32 [T], rows as for ``msa_paged_tree`` (a row's token 0 stands already); u:
+    fp32 [T] and u_last: fp32 [rows], random numbers of [0, 1) for the drafts and
+    for the token behind them.  path: the numbers of the tokens that stay, token 0
+    first, then -1.  The rule is msa_tree_verify's in include/msa.h."""
+    if not isinstance(target, torch.Tensor) or target.dim() != 2 or target.numel() == 0:
+        raise ValueError("target must be a [T, vocab] tensor")
+    if not target.is_cuda:
+        raise ValueError("target must be a CUDA tensor")
+    device = target.device
+    if device.index != _current_device():
+        raise ValueError(f"target is on {device}, the current device is cuda:{_current_device()}")
+    T, V = target.shape
+    ts = _probabilities(target, "target", (T, V), device)
+    ds, dp = 0, None
+    if draft is not None:
+        ds, dp = _probabilities(draft, "draft", (T, V), device), draft.data_ptr()
+    tok = _arg(tokens, "tokens", torch.int32, (T,), device)
+    up = None if parents is None else _arg(parents, "parents", torch.int32, (T,), device)
+    if not isinstance(u_last, torch.Tensor) or u_last.dim() != 1 or u_last.numel() == 0:
+        raise ValueError("u_last must be a [rows] tensor")
+    rows = u_last.shape[0]
+    ul = _arg(u_last, "u_last", torch.float32, (rows,), device)
+    un = _arg(u, "u", torch.float32, (T,), device)
+    offs = _arg(row_offsets, "row_offsets", torch.int32, (rows + 1,), device)
+    if not 1 <= max_path <= MAX_TREE:
+        raise ValueError(f"max_path must be 1 .. {MAX_TREE}, got {max_path}")
+    path, pp = _out(path, "path", (rows, max_path), torch.int32, device, stream)
+    count, cp = _out(count, "count", (rows,), torch.int32, device, stream)
+    last, lp = _out(last, "last", (rows,), torch.int32, device, stream)
+    _check(lib().msa_tree_verify(target.data_ptr(), ts, dp, ds, tok, up, offs, rows, T, V, un, ul,
+                                 max_path, pp, cp, lp, _stream(stream)), "msa_tree_verify")
+    return path, count, last
+
+
+def msa_paged_compact(cache: PagedCache, page_table: torch.Tensor, kv_len: torch.Tensor,
+                      path: torch.Tensor, count: torch.Tensor,
+                      new_len: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Moves each row's kept tokens together, behind its kv_len (int32 [rows])
+    cached ones: slot kv_len + path[r, i] to slot kv_len + i for i < count[r]
+    (path: int32 [rows, width], width <= 64, ascending; count: int32 [rows]; as
+    ``msa_tree_verify`` returns them).  Returns kv_len + count."""
+    device = cache.device
+    _current(device)
+    table = _table(page_table, device)
+    rows = table.rows
+    lens = _arg(kv_len, "kv_len", torch.int32, (rows,), device)
+    if not isinstance(path, torch.Tensor) or path.dim() != 2:
+        raise ValueError("path must be a [rows, width] tensor")
+    width = path.shape[1]
+    pp = _arg(path, "path", torch.int32, (rows, width), device)
+    cp = _arg(count, "count", torch.int32, (rows,), device)
+    new_len, np_ = _out(new_len, "new_len", (rows,), torch.int32, device, stream)
+    _check(lib().msa_paged_compact(cache._ref, ctypes.byref(table), lens, pp, width, cp, np_,
+                                   _stream(stream)), "msa_paged_compact")
+    return new_len

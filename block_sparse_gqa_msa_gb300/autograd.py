@@ -64,3 +64,35 @@ def msa_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     scale = 1.0 / math.sqrt(HEAD_DIM) if softmax_scale is None else float(softmax_scale)
     o, lse = MSAFunction.apply(q, k, v, plan, scale)
     return (o, lse) if return_lse else o
+
+
+class NormRopeFunction(torch.autograd.Function):
+    """q, k normed head by head and rotated; gradients to q, k and the weights."""
+
+    @staticmethod
+    def forward(ctx, q, k, q_weight, k_weight, positions, inv_freq, eps: float,
+                interleaved: bool):
+        q_out, k_out = api.msa_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps=eps,
+                                         interleaved=interleaved)
+        ctx.save_for_backward(q, k, q_weight, k_weight, positions, inv_freq)
+        ctx.eps, ctx.interleaved = eps, interleaved
+        return q_out, k_out
+
+    @staticmethod
+    def backward(ctx, dq_out, dk_out):
+        q, k, q_weight, k_weight, positions, inv_freq = ctx.saved_tensors
+        dq, dk, dwq, dwk = api.msa_norm_rope_backward(
+            dq_out.contiguous(), dk_out.contiguous(), q, k, q_weight, k_weight, positions,
+            inv_freq, eps=ctx.eps, interleaved=ctx.interleaved)
+        return (dq, dk, dwq.to(q_weight.dtype), dwk.to(k_weight.dtype), None, None, None, None)
+
+
+def msa_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor,
+                  k_weight: torch.Tensor, positions: torch.Tensor | None = None,
+                  inv_freq: torch.Tensor | None = None, eps: float = 1e-6,
+                  interleaved: bool = False):
+    """``api.msa_norm_rope`` with gradients to q, k and both weights: queries and
+    keys as ``msa_attention`` takes them, from a projection's output.  Returns (q,
+    k), contiguous."""
+    return NormRopeFunction.apply(q, k, q_weight, k_weight, positions, inv_freq, float(eps),
+                                  bool(interleaved))

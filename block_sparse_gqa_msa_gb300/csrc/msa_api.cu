@@ -220,6 +220,7 @@ const char* msa_status_string(msa_status s) {
     case MSA_ERR_CAPACITY: return "MSA_ERR_CAPACITY";
     case MSA_ERR_RANGE: return "MSA_ERR_RANGE";
     case MSA_ERR_BAD_PAGE: return "MSA_ERR_BAD_PAGE";
+    case MSA_ERR_BAD_TREE: return "MSA_ERR_BAD_TREE";
   }
   return "MSA_ERR_UNKNOWN";
 }

@@ -1,0 +1,478 @@
+// norm_rope.cu - norm of every query and key head with the rotation by
+// position in the same pass, and its gradient.
+//
+// Mathematics: over a head's channels n = 1 / sqrt(mean(x^2) + eps), y = x n w,
+// then pairs turn by position * inv_freq (angles in 64 bits, turn_of).  The
+// turn is orthogonal, so the gradient turns dy back, g, and then
+//   dx = n (g w - u mean(g w u)), dw = sum g u, u = x n.
+// Nothing but x is kept for it: n is formed again from the x that is read
+// anyway.
+//
+// Both are bound by HBM: x in and y out (forward), x and dy in and dx out.  A
+// lane holds 16 channels of a head (8 pairs and both of their halves), so a
+// head is 8 or 4 lanes, its sums two or three exchanges, and the rotation needs
+// none.  A warp takes a token, or a slice of its heads where tokens are few, and
+// loads several heads a lane before it works on any.  A token's angles are
+// formed once a warp.
+#include <algorithm>
+
+#include "paged.cuh"
+
+namespace msa {
+namespace {
+
+constexpr int kNormThreads = 256;
+constexpr int kBackThreads = 512;
+constexpr int kFwdBatch = 4;  // heads a lane that are loaded before the first is worked on
+constexpr int kBwdBatch = 2;
+
+struct NormArgs {
+  const void* x[2];       // queries, keys
+  const void* dy[2];      // backward
+  void* y[2];             // results, or dx
+  int64_t stride[2];
+  const void* w[2];
+  const int32_t* positions;
+  const float* inv_freq;
+  float* part;            // backward: [CTAs][2][dim]
+  float* dw[2];
+  int64_t T;
+  int32_t heads[2];
+  int32_t rot, w_type, slices, parts;
+  float eps;
+};
+
+__device__ __forceinline__ float weight_at(const void* w, int type, int i) {
+  if (type == MSA_F32) return static_cast<const float*>(w)[i];
+  if (type == MSA_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(w)[i]);
+  return __half2float(static_cast<const __half*>(w)[i]);
+}
+
+// The lane's place in a head: two runs of 8 channels.  Of a head whose halves
+// pair, run 0 holds the first and run 1 the second channels of 8 pairs, or
+// both are runs of the channels that are not turned.
+template <int kDim, bool kInter>
+struct Place {
+  int c0, c1;
+  bool turn0, turn1;
+  __device__ __forceinline__ Place(int sub, int rot) {
+    if (kInter) {
+      c0 = sub * 8;
+      c1 = c0 + kDim / 2;
+    } else if (sub * 16 < rot) {
+      c0 = sub * 8;
+      c1 = c0 + rot / 2;
+    } else {
+      c0 = rot + (sub - rot / 16) * 8;
+      c1 = c0 + (kDim - rot) / 2;
+    }
+    turn0 = c0 < rot;
+    turn1 = c1 < rot;
+  }
+};
+
+// Angles of a token, left in the warp's shared memory, then the lane's 8.
+template <int kDim, bool kInter>
+__device__ __forceinline__ void angles(const NormArgs& a, int64_t t, float2* mine,
+                                       const Place<kDim, kInter>& at, float (&c)[8],
+                                       float (&s)[8]) {
+  const int lane = threadIdx.x & 31;
+  __syncwarp();
+  if (a.rot > 0) {
+    const int64_t pos = a.positions[t];
+    for (int i = lane; i < a.rot / 2; i += 32) mine[i] = turn_of(pos, a.inv_freq[i]);
+  }
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    // pair of the lane's channels: (c0 + i, c1 + i), or 4 pairs in each run
+    const bool turned = kInter && i >= 4 ? at.turn1 : at.turn0;
+    const int pair = kInter ? (i < 4 ? at.c0 / 2 + i : at.c1 / 2 + i - 4) : at.c0 + i;
+    const float2 v = turned ? mine[pair] : make_float2(1.f, 0.f);
+    c[i] = v.x;
+    s[i] = v.y;
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void unpack8(const uint4& v, float* x) {
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(&v);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 p = Pair<T>::unpack(w[i]);
+    x[2 * i] = p.x;
+    x[2 * i + 1] = p.y;
+  }
+}
+template <typename T>
+__device__ __forceinline__ uint4 pack8(const float* x) {
+  return make_uint4(Pair<T>::pack(x[0], x[1]), Pair<T>::pack(x[2], x[3]),
+                    Pair<T>::pack(x[4], x[5]), Pair<T>::pack(x[6], x[7]));
+}
+// Turns the lane's 16 channels (run 0 in x[0..7], run 1 in x[8..15]); back: by
+// the negative angle.
+template <bool kInter, bool kBack>
+__device__ __forceinline__ void rotate16(float* x, const float (&c)[8], const float (&s)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int p = kInter ? 2 * i : i, q = kInter ? 2 * i + 1 : i + 8;
+    const float u = x[p], v = x[q], sn = kBack ? -s[i] : s[i];
+    x[p] = u * c[i] - v * sn;
+    x[q] = v * c[i] + u * sn;
+  }
+}
+template <int kLanes>
+__device__ __forceinline__ float head_sum(float v) {
+#pragma unroll
+  for (int o = 1; o < kLanes; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// A warp's item: a token and a run of its groups.  Groups are 32 / kLanes heads
+// of queries, then of keys.
+struct Groups {
+  int q, all;
+  __device__ __forceinline__ Groups(const NormArgs& a, int per)
+      : q((a.heads[0] + per - 1) / per), all(q + (a.heads[1] + per - 1) / per) {}
+};
+
+template <typename T, int kDim, bool kInter>
+__global__ void __launch_bounds__(kNormThreads, 2) k_norm_rope(const NormArgs a) {
+  constexpr int kLanes = kDim / 16, kPer = 32 / kLanes;
+  __shared__ __align__(16) float sw[2][kDim];
+  __shared__ float2 turns[kNormThreads / 32][kDim / 2];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const Place<kDim, kInter> at(lane % kLanes, a.rot);
+  const int slot = lane / kLanes;
+  const Groups groups(a, kPer);
+  grid_dep_wait();
+  grid_dep_release();
+  for (int i = threadIdx.x; i < 2 * kDim; i += kNormThreads)
+    sw[i / kDim][i % kDim] = weight_at(a.w[i / kDim], a.w_type, i % kDim);
+  __syncthreads();
+  const int64_t item = int64_t(blockIdx.x) * (kNormThreads / 32) + warp;
+  const int64_t t = item / a.slices;
+  const int slice = int(item % a.slices);
+  if (t >= a.T) return;
+  const int g0 = groups.all * slice / a.slices, g1 = groups.all * (slice + 1) / a.slices;
+  float c[8], s[8];
+  for (int g = g0; g < g1; g += kFwdBatch) {
+    uint4 u[kFwdBatch], v[kFwdBatch];
+#pragma unroll
+    for (int b = 0; b < kFwdBatch; ++b) {
+      const int kind = g + b >= groups.q;
+      const int h = (kind ? g + b - groups.q : g + b) * kPer + slot;
+      u[b] = v[b] = make_uint4(0, 0, 0, 0);
+      if (g + b < g1 && h < a.heads[kind]) {
+        const T* x = static_cast<const T*>(a.x[kind]) + t * a.stride[kind] + h * kDim;
+        u[b] = *reinterpret_cast<const uint4*>(x + at.c0);
+        v[b] = *reinterpret_cast<const uint4*>(x + at.c1);
+      }
+    }
+    if (g == g0) angles<kDim, kInter>(a, t, turns[warp], at, c, s);
+#pragma unroll
+    for (int b = 0; b < kFwdBatch; ++b) {
+      if (g + b >= g1) break;
+      const int kind = g + b >= groups.q;
+      const int h = (kind ? g + b - groups.q : g + b) * kPer + slot;
+      float x[16];
+      unpack8<T>(u[b], x);
+      unpack8<T>(v[b], x + 8);
+      float ss = 0.f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) ss = fmaf(x[i], x[i], ss);
+      const float n = rsqrtf(head_sum<kLanes>(ss) * (1.f / kDim) + a.eps);
+#pragma unroll
+      for (int i = 0; i < 16; i += 4) {
+        const float4 w = *reinterpret_cast<const float4*>(
+            &sw[kind][(i < 8 ? at.c0 + i : at.c1 + i - 8)]);
+        x[i] *= n * w.x;
+        x[i + 1] *= n * w.y;
+        x[i + 2] *= n * w.z;
+        x[i + 3] *= n * w.w;
+      }
+      rotate16<kInter, false>(x, c, s);
+      if (h < a.heads[kind]) {
+        T* y = static_cast<T*>(a.y[kind]) + (t * a.heads[kind] + h) * kDim;
+        *reinterpret_cast<uint4*>(y + at.c0) = pack8<T>(x);
+        *reinterpret_cast<uint4*>(y + at.c1) = pack8<T>(x + 8);
+      }
+    }
+  }
+}
+
+// Each CTA's sums of dw go to the workspace, k_norm_rope_join adds them up in
+// order.
+template <typename T, int kDim, bool kInter>
+__global__ void __launch_bounds__(kBackThreads, 1) k_norm_rope_back(const NormArgs a) {
+  constexpr int kLanes = kDim / 16, kPer = 32 / kLanes, kWarps = kBackThreads / 32;
+  __shared__ __align__(16) float sw[2][kDim];
+  __shared__ float2 turns[kWarps][kDim / 2];
+  __shared__ float sums[kWarps][2][kDim];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const Place<kDim, kInter> at(lane % kLanes, a.rot);
+  const int slot = lane / kLanes;
+  const Groups groups(a, kPer);
+  grid_dep_wait();
+  grid_dep_release();
+  for (int i = threadIdx.x; i < 2 * kDim; i += kBackThreads)
+    sw[i / kDim][i % kDim] = weight_at(a.w[i / kDim], a.w_type, i % kDim);
+  __syncthreads();
+  float acc[2][16] = {};
+  const int64_t items = a.T * a.slices;
+  for (int64_t item = int64_t(warp) * gridDim.x + blockIdx.x; item < items;
+       item += int64_t(gridDim.x) * kWarps) {
+    const int64_t t = item / a.slices;
+    const int slice = int(item % a.slices);
+    const int g0 = groups.all * slice / a.slices, g1 = groups.all * (slice + 1) / a.slices;
+    float c[8], s[8];
+    for (int g = g0; g < g1; g += kBwdBatch) {
+      uint4 u[kBwdBatch], v[kBwdBatch], du[kBwdBatch], dv[kBwdBatch];
+#pragma unroll
+      for (int b = 0; b < kBwdBatch; ++b) {
+        const int kind = g + b >= groups.q;
+        const int h = (kind ? g + b - groups.q : g + b) * kPer + slot;
+        u[b] = v[b] = du[b] = dv[b] = make_uint4(0, 0, 0, 0);
+        if (g + b < g1 && h < a.heads[kind]) {
+          const T* x = static_cast<const T*>(a.x[kind]) + t * a.stride[kind] + h * kDim;
+          const T* dy = static_cast<const T*>(a.dy[kind]) + (t * a.heads[kind] + h) * kDim;
+          u[b] = *reinterpret_cast<const uint4*>(x + at.c0);
+          v[b] = *reinterpret_cast<const uint4*>(x + at.c1);
+          du[b] = *reinterpret_cast<const uint4*>(dy + at.c0);
+          dv[b] = *reinterpret_cast<const uint4*>(dy + at.c1);
+        }
+      }
+      if (g == g0) angles<kDim, kInter>(a, t, turns[warp], at, c, s);
+#pragma unroll
+      for (int b = 0; b < kBwdBatch; ++b) {
+        if (g + b >= g1) break;
+        const int kind = g + b >= groups.q;
+        const int h = (kind ? g + b - groups.q : g + b) * kPer + slot;
+        float x[16], d[16];
+        unpack8<T>(u[b], x);
+        unpack8<T>(v[b], x + 8);
+        unpack8<T>(du[b], d);
+        unpack8<T>(dv[b], d + 8);
+        rotate16<kInter, true>(d, c, s);
+        float ss = 0.f, dot = 0.f;
+        float w[16];
+#pragma unroll
+        for (int i = 0; i < 16; i += 4)
+          *reinterpret_cast<float4*>(w + i) = *reinterpret_cast<const float4*>(
+              &sw[kind][(i < 8 ? at.c0 + i : at.c1 + i - 8)]);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          ss = fmaf(x[i], x[i], ss);
+          dot = fmaf(d[i] * w[i], x[i], dot);
+        }
+        const float n = rsqrtf(head_sum<kLanes>(ss) * (1.f / kDim) + a.eps);
+        // mean(g w u) with u = x n
+        const float m = head_sum<kLanes>(dot) * n * (1.f / kDim);
+        if (kind == 0) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) acc[0][i] = fmaf(d[i], x[i] * n, acc[0][i]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) acc[1][i] = fmaf(d[i], x[i] * n, acc[1][i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = n * (d[i] * w[i] - x[i] * n * m);
+        if (h < a.heads[kind]) {
+          T* y = static_cast<T*>(a.y[kind]) + (t * a.heads[kind] + h) * kDim;
+          *reinterpret_cast<uint4*>(y + at.c0) = pack8<T>(x);
+          *reinterpret_cast<uint4*>(y + at.c1) = pack8<T>(x + 8);
+        }
+      }
+    }
+  }
+  // the warp's heads, then the CTA's warps, in order
+#pragma unroll
+  for (int kind = 0; kind < 2; ++kind)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float v = acc[kind][i];
+#pragma unroll
+      for (int o = kLanes; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      if (slot == 0) sums[warp][kind][i < 8 ? at.c0 + i : at.c1 + i - 8] = v;
+    }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 2 * kDim; i += kBackThreads) {
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) v += sums[w][i / kDim][i % kDim];
+    a.part[int64_t(blockIdx.x) * 2 * kDim + i] = v;
+  }
+}
+
+constexpr int kJoinThreads = 1024;
+template <int kDim>
+__global__ void __launch_bounds__(kJoinThreads) k_norm_rope_join(const NormArgs a) {
+  constexpr int kWays = kJoinThreads / (2 * kDim);
+  __shared__ float sums[kWays][2 * kDim];
+  const int col = threadIdx.x % (2 * kDim), way = threadIdx.x / (2 * kDim);
+  grid_dep_wait();
+  grid_dep_release();
+  float v = 0.f;
+#pragma unroll 8
+  for (int p = way; p < a.parts; p += kWays) v += a.part[int64_t(p) * 2 * kDim + col];
+  sums[way][col] = v;
+  __syncthreads();
+  if (way == 0) {
+    v = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWays; ++w) v += sums[w][col];
+    a.dw[col / kDim][col % kDim] = v;
+  }
+}
+
+constexpr int kMaxParts = 160;  // CTAs of the backward: one an SM
+size_t norm_workspace(int32_t dim) { return sizeof(float) * kMaxParts * 2 * size_t(dim); }
+
+// Slices of a token's groups: enough warps to fill the chip where tokens are few.
+int32_t norm_slices(const NormArgs& a, int per, int warps_sm) {
+  const int64_t groups = (a.heads[0] + per - 1) / per + (a.heads[1] + per - 1) / per;
+  int64_t n = int64_t(device_sm_count()) * warps_sm / a.T;
+  if (n > groups) n = groups;
+  return int32_t(n < 1 ? 1 : n);
+}
+
+template <typename T, int kDim>
+cudaError_t launch_norm(NormArgs a, bool inter, cudaStream_t s) {
+  a.slices = norm_slices(a, 512 / kDim, 16);
+  const int64_t warps = a.T * a.slices, each = kNormThreads / 32;
+  const dim3 grid(unsigned((warps + each - 1) / each));
+  return inter ? launch_k(true, k_norm_rope<T, kDim, true>, grid, dim3(kNormThreads), 0, s, a)
+               : launch_k(true, k_norm_rope<T, kDim, false>, grid, dim3(kNormThreads), 0, s, a);
+}
+template <typename T, int kDim>
+cudaError_t launch_norm_back(NormArgs& a, bool inter, cudaStream_t s) {
+  a.slices = norm_slices(a, 512 / kDim, kBackThreads / 32);
+  int64_t parts = std::min(device_sm_count(), kMaxParts);
+  parts = std::min<int64_t>(parts, a.T * a.slices);
+  a.parts = int32_t(parts);
+  const dim3 grid{unsigned(parts)};
+  return inter
+             ? launch_k(true, k_norm_rope_back<T, kDim, true>, grid, dim3(kBackThreads), 0, s, a)
+             : launch_k(true, k_norm_rope_back<T, kDim, false>, grid, dim3(kBackThreads), 0, s, a);
+}
+template <int kDim>
+cudaError_t launch_norm_join(const NormArgs& a, cudaStream_t s) {
+  return launch_k(true, k_norm_rope_join<kDim>, dim3(1), dim3(kJoinThreads), 0, s, a);
+}
+
+msa_status check_norm(const msa_norm_rope_args* p, NormArgs* a) {
+  if (!p || !p->q || !p->k || !p->q_weight || !p->k_weight) return MSA_ERR_INVALID_ARG;
+  if (p->T < 1 || p->T > kMaxTokens || (p->head_dim != 64 && p->head_dim != 128) ||
+      p->q_heads < 1 || p->q_heads > 1024 || p->k_heads < 1 || p->k_heads > 1024 ||
+      (p->dtype != MSA_BF16 && p->dtype != MSA_F16) || p->weight_dtype < 0 ||
+      p->weight_dtype > MSA_F32)
+    return MSA_ERR_INVALID_ARG;
+  if (p->q_stride < int64_t(p->q_heads) * p->head_dim || p->q_stride % 8 ||
+      p->k_stride < int64_t(p->k_heads) * p->head_dim || p->k_stride % 8)
+    return MSA_ERR_INVALID_ARG;
+  if (!(p->eps >= 0.f) || p->eps > 1e30f) return MSA_ERR_INVALID_ARG;
+  if (p->inv_freq && (!p->positions || p->rotary_dim < 16 || p->rotary_dim % 16 ||
+                      p->rotary_dim > p->head_dim))
+    return MSA_ERR_INVALID_ARG;
+  const uintptr_t w = p->weight_dtype == MSA_F32 ? 3 : 1;
+  if (!paged_aligned(p->q) || !paged_aligned(p->k) || !paged_aligned4(p->positions) ||
+      !paged_aligned4(p->inv_freq) || (reinterpret_cast<uintptr_t>(p->q_weight) & w) ||
+      (reinterpret_cast<uintptr_t>(p->k_weight) & w))
+    return MSA_ERR_ALIGNMENT;
+  *a = NormArgs{};
+  a->x[0] = p->q;
+  a->x[1] = p->k;
+  a->stride[0] = p->q_stride;
+  a->stride[1] = p->k_stride;
+  a->w[0] = p->q_weight;
+  a->w[1] = p->k_weight;
+  a->positions = p->positions;
+  a->inv_freq = p->inv_freq;
+  a->T = p->T;
+  a->heads[0] = p->q_heads;
+  a->heads[1] = p->k_heads;
+  a->rot = p->inv_freq ? p->rotary_dim : 0;
+  a->w_type = p->weight_dtype;
+  a->eps = p->eps;
+  return MSA_OK;
+}
+
+}  // namespace
+}  // namespace msa
+
+using namespace msa;
+
+extern "C" msa_status msa_norm_rope(const msa_norm_rope_args* args, void* q_out, void* k_out,
+                                    msa_stream_t stream) {
+  NormArgs a;
+  msa_status st = check_norm(args, &a);
+  if (st != MSA_OK) return st;
+  if (!q_out || !k_out) return MSA_ERR_INVALID_ARG;
+  if ((q_out == args->q && args->q_stride != int64_t(args->q_heads) * args->head_dim) ||
+      (k_out == args->k && args->k_stride != int64_t(args->k_heads) * args->head_dim))
+    return MSA_ERR_INVALID_ARG;
+  if (!paged_aligned(q_out) || !paged_aligned(k_out)) return MSA_ERR_ALIGNMENT;
+  st = check_device();
+  if (st != MSA_OK) return st;
+  a.y[0] = q_out;
+  a.y[1] = k_out;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool inter = args->interleaved != 0;
+  launch_begin("norm_rope", s);
+  cudaError_t e;
+  if (args->dtype == MSA_BF16)
+    e = args->head_dim == 128 ? launch_norm<__nv_bfloat16, 128>(a, inter, s)
+                              : launch_norm<__nv_bfloat16, 64>(a, inter, s);
+  else
+    e = args->head_dim == 128 ? launch_norm<__half, 128>(a, inter, s)
+                              : launch_norm<__half, 64>(a, inter, s);
+  launch_end("norm_rope", s);
+  return e == cudaSuccess ? MSA_OK : MSA_ERR_CUDA;
+}
+
+extern "C" msa_status msa_norm_rope_workspace_bytes(int32_t head_dim, size_t* bytes) {
+  if (!bytes || (head_dim != 64 && head_dim != 128)) return MSA_ERR_INVALID_ARG;
+  *bytes = norm_workspace(head_dim);
+  return MSA_OK;
+}
+
+extern "C" msa_status msa_norm_rope_backward(const msa_norm_rope_args* args, const void* dq_out,
+                                             const void* dk_out, void* dq, void* dk,
+                                             float* dq_weight, float* dk_weight, void* workspace,
+                                             size_t workspace_bytes, msa_stream_t stream) {
+  NormArgs a;
+  msa_status st = check_norm(args, &a);
+  if (st != MSA_OK) return st;
+  if (!dq_out || !dk_out || !dq || !dk || !dq_weight || !dk_weight || !workspace)
+    return MSA_ERR_INVALID_ARG;
+  if (!paged_aligned(dq_out) || !paged_aligned(dk_out) || !paged_aligned(dq) ||
+      !paged_aligned(dk) || !paged_aligned4(dq_weight) || !paged_aligned4(dk_weight) ||
+      !paged_aligned(workspace))
+    return MSA_ERR_ALIGNMENT;
+  if (workspace_bytes < norm_workspace(args->head_dim)) return MSA_ERR_WORKSPACE;
+  st = check_device();
+  if (st != MSA_OK) return st;
+  a.dy[0] = dq_out;
+  a.dy[1] = dk_out;
+  a.y[0] = dq;
+  a.y[1] = dk;
+  a.dw[0] = dq_weight;
+  a.dw[1] = dk_weight;
+  a.part = static_cast<float*>(workspace);
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool inter = args->interleaved != 0;
+  launch_begin("norm_rope_back", s);
+  cudaError_t e;
+  if (args->dtype == MSA_BF16)
+    e = args->head_dim == 128 ? launch_norm_back<__nv_bfloat16, 128>(a, inter, s)
+                              : launch_norm_back<__nv_bfloat16, 64>(a, inter, s);
+  else
+    e = args->head_dim == 128 ? launch_norm_back<__half, 128>(a, inter, s)
+                              : launch_norm_back<__half, 64>(a, inter, s);
+  launch_end("norm_rope_back", s);
+  if (e != cudaSuccess) return MSA_ERR_CUDA;
+  launch_begin("norm_rope_join", s);
+  e = args->head_dim == 128 ? launch_norm_join<128>(a, s) : launch_norm_join<64>(a, s);
+  launch_end("norm_rope_join", s);
+  return e == cudaSuccess ? MSA_OK : MSA_ERR_CUDA;
+}

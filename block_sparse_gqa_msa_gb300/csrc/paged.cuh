@@ -1,6 +1,6 @@
-// paged.cuh - what the paged-cache kernels (append, index, select, decode)
-// share: the cache as kernel arguments, the search of a token's row, the
-// host's argument checks.
+// paged.cuh - what the paged-cache kernels (append, index, select, decode,
+// tree, compact) and the norm share: the cache as kernel arguments, the search
+// of a token's row, the rotation's angles, the host's argument checks.
 #pragma once
 #include <cuda_fp16.h>
 
@@ -78,6 +78,15 @@ __device__ __forceinline__ void check_offsets(const int32_t* offs, int32_t rows,
   for (int32_t i = threadIdx.x; i < rows; i += blockDim.x) bad |= offs[i] > offs[i + 1];
   if (threadIdx.x == 0) bad |= offs[0] != 0 || offs[rows] > T;
   if (bad) raise_paged(status, MSA_ERR_BAD_OFFSETS);
+}
+
+// Sine and cosine of pos * f.  The turns are counted in 64 bits (an exact
+// product up to position 2^29) and only their fraction is rounded to 32.
+__device__ __forceinline__ float2 turn_of(int64_t pos, float f) {
+  const double turns = double(pos) * double(f) * 0.15915494309189533577;  // 1 / (2 pi)
+  float s, c;
+  sincospif(float(2.0 * (turns - rint(turns))), &s, &c);
+  return make_float2(c, s);
 }
 
 template <typename T>

@@ -43,15 +43,6 @@ struct AppendArgs {
   int32_t group;  // tokens of one CTA, where it has several
 };
 
-// Sine and cosine of pos * f.  The turns are counted in 64 bits (an exact
-// product up to position 2^29) and only their fraction is rounded to 32.
-__device__ __forceinline__ float2 turn_of(int64_t pos, float f) {
-  const double turns = double(pos) * double(f) * 0.15915494309189533577;  // 1 / (2 pi)
-  float s, c;
-  sincospif(float(2.0 * (turns - rint(turns))), &s, &c);
-  return make_float2(c, s);
-}
-
 template <typename T, int kDim, bool kInter, int kTokens>
 __global__ void __launch_bounds__(kAppThreads) k_paged_append(const AppendArgs a) {
   constexpr int kPer = kDim / 16;  // items of a head

@@ -1,0 +1,1162 @@
+// paged_tree.cu - attention of each row's drafted tokens over the paged cache:
+// over the cached keys (all, or each token's blocks) and over the drafted tokens
+// on its own path.
+//
+// Mathematics.  The tokens of a row and the query heads that share a key head
+// are the rows of matrix tiles: with n heads a key head and N tokens, N n rows
+// against the same keys.  Over tiles of 128 keys, with a running reference m and
+// sum l in base 2 (x = scale * log2(e) * <q, k>):
+//   P = 2^(x - m), l += sum P, O += P V,
+// O and l rescaled when m has to rise (m trails the maximum by kRise at most);
+// two such states join as M = max(m1, m2), l = l1 2^(m1 - M) + l2 2^(m2 - M), O
+// likewise; at the end O / l, lse = ln2 (m + log2 l).  m, l, O are 32 bits; P is
+// rounded to the cache's type for the product with V (the tensor cores take
+// both in one type), which is off by 2^-8 (bf16) or 2^-11 (fp16) of a weight
+// at most, as the output's own rounding is of the output.
+//
+// What bounds it.  A key and its value are read once for up to 256 rows, 4 * D
+// bytes for 4 * D * rows flop: up to 256 rows HBM is the bound (at 6.8 TB/s and
+// 1.9 PFLOP/s they meet at 280), beyond that the tensor cores.
+//
+// Tiles.  A CTA holds two query tiles of 128 rows (slots A and B) against one
+// stream of key tiles, so that one slot's softmax runs while the tensor cores
+// work for the other: S_A, then P_B V of the step before, S_B, P_A V.  A row
+// with more than 256 matrix rows is several such items.  With 128 rows or fewer
+// slot B takes the same queries and every other key tile, and the two states
+// are joined in tensor memory's lanes at the end; the order of operations is the
+// same.
+//
+// Split.  All items' key tiles, in order, are dealt out in equal runs to the
+// CTAs, one an SM; a run's place is found from the lengths on the device.  Items
+// are ordered with the number of the 256-row group outermost: CTAs that read the
+// same keys for other queries then do so at about the same time, and HBM is read
+// once.  An item within one run is finished there; otherwise each run leaves its
+// (m, l, O) in the workspace and k_paged_tree_join adds them up, in order.
+//
+// Keys come by asynchronous copies of 16 bytes into the swizzled layout that the
+// tensor cores read, three tiles of keys and two of values ahead; they take
+// pages of any size and any strides, and write zeros for keys that are not
+// there.
+//
+// With q2k a first kernel (k_paged_tree_lists) makes, for each item, the list of
+// the blocks that any of its tokens chose, and which tokens did.
+#include <algorithm>
+
+#include "paged.cuh"
+#include "sm100.cuh"
+
+namespace msa {
+namespace {
+
+constexpr int kNodes = 64;         // drafted tokens of a row
+constexpr int kPairRows = 256;     // matrix rows of an item
+constexpr int kTileRows = 128;
+constexpr int kMaxRuns = 160;      // CTAs: no GB300 has more SMs
+constexpr int kSoftWarps = 8, kCopyWarps = 4;
+constexpr int kTreeThreads = 512;  // and a warp that issues products, three that wait
+// Registers of a thread: 128 at launch, 512 threads; the softmax warps take over what
+// the others give up: 256 x 192 + 256 x 64 = 512 x 128.
+constexpr int kSoftRegs = 192, kOtherRegs = 64;
+constexpr int kKStages = 3, kVStages = 2;
+constexpr float kRise = 8.f;       // and kLift: as in paged_decode.cu
+template <typename T>
+constexpr float kLift = 0.f;
+template <>
+constexpr float kLift<__half> = 7.f;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+struct TreeArgs {
+  const void* q;
+  PagedPool k, v;
+  PagedTable table;
+  const int32_t *offs, *kv_len, *parents, *q2k;
+  void* o;
+  float* lse;
+  int64_t T;
+  float scale_log2;     // scale * log2(e)
+  int32_t kv_heads, group;
+  int32_t layers;       // 256-row groups of the largest row there can be
+  int32_t* counts;      // q2k: tiles of each item [layers][rows][kv_heads]
+  int32_t* ids;         // q2k: its blocks, ascending (list_base)
+  uint64_t* who;        // q2k: the tokens that chose them
+  float* part_ml;       // [2 runs][256][2]: m, l
+  float* part_o;        // [2 runs][256][dim]
+};
+
+template <int kDim>
+struct TreeShape {
+  static constexpr uint32_t kTile = kTileRows * kDim * 2;
+  static constexpr uint32_t kQ = 0, kK = 2 * kTile, kV = kK + kKStages * kTile;
+  static constexpr uint32_t kRest = kV + kVStages * kTile;  // a TreeShared
+  static constexpr uint32_t kTmO = 256;  // columns of O_A; O_B kDim further
+};
+
+// A row as the kernels see it; n == 0: nothing to attend for.
+struct TreeRow {
+  int32_t t0, n, len;
+};
+__device__ __forceinline__ bool row_fits(const TreeArgs& a, int32_t n, int32_t len) {
+  return n <= kNodes && len >= 0 && int64_t(len) + n <= (int64_t(a.table.width) << a.table.shift);
+}
+__device__ __forceinline__ TreeRow tree_row(const TreeArgs& a, int32_t r) {
+  const int32_t o0 = a.offs[r], o1 = a.offs[r + 1], len = a.kv_len[r];
+  TreeRow v{o0, o1 - o0, len};
+  if (o0 < 0 || o1 <= o0 || o1 > a.T || !row_fits(a, o1 - o0, len)) v.n = 0;
+  return v;
+}
+__device__ __forceinline__ int32_t layer_count(const TreeArgs& a, int32_t n) {
+  return (n * a.group + kPairRows - 1) / kPairRows;
+}
+__device__ __forceinline__ int32_t dense_tiles(const TreeRow& w) {
+  return int32_t((int64_t(w.len) + w.n + kBlock - 1) / kBlock);
+}
+// First list entry of an item: 16 for each of its tokens; two items may share
+// one token of a row, hence one more for each.
+__device__ __forceinline__ int64_t list_base(const TreeArgs& a, int32_t row, int32_t layer,
+                                             int32_t g, int32_t t0) {
+  const int64_t all = a.T + 4 * int64_t(a.table.rows);
+  return (g * all + t0 + layer * kPairRows / a.group + 4 * int64_t(row) + layer) * kTopK;
+}
+
+// ------------------------------------------------------------ lists of blocks
+constexpr int kListThreads = 256;
+constexpr int kHash = 2048;  // places for up to 64 x 16 blocks
+__global__ void __launch_bounds__(kListThreads) k_paged_tree_lists(const TreeArgs a) {
+  __shared__ int32_t key[kHash];
+  __shared__ unsigned long long who[kHash];
+  __shared__ int32_t uniq[kNodes * kTopK], place[kNodes * kTopK];
+  __shared__ int32_t n_uniq;
+  const int tid = threadIdx.x, lane = tid & 31;
+  for (int i = tid; i < kHash; i += kListThreads) {
+    key[i] = -1;
+    who[i] = 0;
+  }
+  if (tid == 0) n_uniq = 0;
+  grid_dep_wait();
+  grid_dep_release();
+  const int32_t item = blockIdx.x;  // (layer * rows + row) * kv_heads + g
+  const int32_t g = item % a.kv_heads, row = item / a.kv_heads % a.table.rows;
+  const int32_t layer = item / a.kv_heads / a.table.rows;
+  const TreeRow w = tree_row(a, row);
+  if (layer >= layer_count(a, w.n)) {
+    if (tid == 0) a.counts[item] = 0;
+    return;
+  }
+  __syncthreads();
+  const int32_t j0 = layer * kPairRows / a.group;
+  const int32_t j1 = min(w.n, ((layer + 1) * kPairRows + a.group - 1) / a.group);
+  const int32_t blocks = int32_t((int64_t(w.len) + kBlock - 1) / kBlock);
+  const int32_t* slots = a.q2k + (int64_t(g) * a.T + w.t0) * kTopK;
+  for (int i = j0 * kTopK + tid; i < j1 * kTopK; i += kListThreads) {
+    const int32_t v = slots[i];
+    if (v == -1) continue;
+    if (v < 0 || v >= blocks) {
+      raise_paged(a.table.status, MSA_ERR_BAD_Q2K);
+      continue;
+    }
+    // at most half the places fill up, so a free one is found
+    uint32_t h = (uint32_t(v) * 2654435761u) >> 21;
+    for (;;) {
+      const int32_t old = atomicCAS(&key[h], -1, v);
+      if (old == -1 || old == v) break;
+      h = (h + 1) % kHash;
+    }
+    atomicOr(&who[h], 1ull << (i / kTopK));
+  }
+  __syncthreads();
+  for (int i = tid; i < kHash; i += kListThreads) {
+    const bool used = key[i] >= 0;
+    const uint32_t m = __ballot_sync(0xffffffffu, used);
+    int32_t at = 0;
+    if (lane == 0 && m) at = atomicAdd(&n_uniq, __popc(m));
+    at = __shfl_sync(0xffffffffu, at, 0) + __popc(m & ((1u << lane) - 1));
+    if (used) {
+      uniq[at] = key[i];
+      place[at] = i;
+    }
+  }
+  __syncthreads();
+  const int32_t n = n_uniq;
+  const int64_t base = list_base(a, row, layer, g, w.t0);
+  for (int i = tid; i < n; i += kListThreads) {
+    const int32_t v = uniq[i];
+    int32_t rank = 0;
+    for (int k = 0; k < n; ++k) rank += uniq[k] < v;
+    a.ids[base + rank] = v;
+    a.who[base + rank] = who[place[i]];
+  }
+  if (tid == 0) a.counts[item] = n + 1;  // and the drafted tokens' tile
+}
+
+// ------------------------------------------------------------ dealing out
+// The tiles before each of a CTA's stretches of layer rows (layer * rows + row).
+constexpr int kStretches = kTreeThreads;
+struct TreePrefix {
+  int32_t at[kStretches];
+  int32_t sums[kTreeThreads / 32];
+  int32_t total;
+  int32_t each;  // layer rows of a stretch
+};
+__device__ __forceinline__ int32_t item_tiles(const TreeArgs& a, const TreeRow& w, int32_t lr,
+                                              int32_t g) {
+  if (a.q2k) return a.counts[int64_t(lr) * a.kv_heads + g];
+  return lr / a.table.rows < layer_count(a, w.n) ? dense_tiles(w) : 0;
+}
+__device__ __forceinline__ int32_t layer_row_tiles(const TreeArgs& a, int32_t lr) {
+  const TreeRow w = tree_row(a, lr % a.table.rows);
+  if (!a.q2k) return item_tiles(a, w, lr, 0) * a.kv_heads;
+  int32_t n = 0;
+  for (int32_t g = 0; g < a.kv_heads; ++g) n += item_tiles(a, w, lr, g);
+  return n;
+}
+__device__ __forceinline__ void make_tree_prefix(const TreeArgs& a, TreePrefix& s) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
+  const int32_t all = a.table.rows * a.layers, threads = blockDim.x;
+  const int32_t each = (all + threads - 1) / threads;
+  const int32_t r0 = min(all, tid * each), r1 = min(all, r0 + each);
+  int32_t mine = 0;
+  for (int32_t r = r0; r < r1; ++r) mine += layer_row_tiles(a, r);
+  int32_t incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int32_t y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) s.sums[warp] = incl;
+  __syncthreads();
+  int32_t total = 0, before = 0;
+  for (int w = 0; w < warps; ++w) {
+    if (w < warp) before += s.sums[w];
+    total += s.sums[w];
+  }
+  s.at[tid] = before + incl - mine;
+  if (tid == 0) {
+    s.total = total;
+    s.each = each;
+  }
+  __syncthreads();
+}
+// Tiles of run c of `runs`: from start(c) to start(c + 1).
+__device__ __forceinline__ int32_t run_start(int32_t total, int32_t runs, int32_t c) {
+  return int32_t(int64_t(total) * c / runs);
+}
+
+// A walk over the items from tile t on.  All lanes alike.
+struct TreeWalk {
+  const TreeArgs& a;
+  int32_t lr, g;      // layer row and key head of the item
+  int32_t row, layer;
+  TreeRow w;
+  int32_t tiles;      // of the item
+  int32_t i0, i1;     // the segment
+  int32_t left;       // of the run, after the segment
+  __device__ __forceinline__ explicit TreeWalk(const TreeArgs& args) : a(args) {}
+  __device__ __forceinline__ void enter_row() {
+    row = lr % a.table.rows;
+    layer = lr / a.table.rows;
+    w = tree_row(a, row);
+  }
+  // The item that tile t lies in; i0 its place there.
+  __device__ __forceinline__ void locate(const TreePrefix& s, int32_t t) {
+    int lo = 0, hi = blockDim.x;  // the last stretch that starts at or before t
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (s.at[mid] <= t) lo = mid; else hi = mid;
+    }
+    int32_t at = s.at[lo];
+    const int32_t end = a.table.rows * a.layers - 1;
+    for (lr = lo * s.each; lr < end; ++lr) {
+      const int32_t n = layer_row_tiles(a, lr);
+      if (at + n > t) break;
+      at += n;
+    }
+    enter_row();
+    for (g = 0;; ++g) {
+      tiles = item_tiles(a, w, lr, g);
+      if (at + tiles > t || g + 1 == a.kv_heads) break;
+      at += tiles;
+    }
+    i0 = t - at;
+  }
+  __device__ __forceinline__ void begin(const TreePrefix& s, int32_t t, int32_t n) {
+    locate(s, t);
+    i1 = min(tiles, i0 + n);
+    left = n - (i1 - i0);
+  }
+  __device__ __forceinline__ bool next() {
+    if (left == 0) return false;
+    do {
+      if (++g == a.kv_heads) {
+        g = 0;
+        do {
+          if (++lr >= a.table.rows * a.layers) return false;
+          enter_row();
+        } while (layer >= layer_count(a, w.n));
+      }
+      tiles = item_tiles(a, w, lr, g);
+    } while (tiles == 0);
+    i0 = 0;
+    i1 = min(tiles, left);
+    left -= i1;
+    return true;
+  }
+  __device__ __forceinline__ int32_t rows_here() const {
+    return min(kPairRows, w.n * a.group - layer * kPairRows);
+  }
+};
+
+// ------------------------------------------------------------ the main kernel
+struct TreeBars {
+  uint64_t q_full, q_empty, k_full[kKStages], k_empty[kKStages], v_full[kVStages],
+      v_empty[kVStages], s_full[2], p_full[2], o_full[2], o_free, ml, fin;
+};
+struct TreeShared {
+  TreeBars bars;
+  uint32_t there[4][kCopyWarps];  // keys of a tile that are there; a ring of 4 tiles
+  float2 states[2][kTileRows];    // (m, l) of the slots, where they are joined
+  uint32_t tmem_base;
+  int abort;
+};
+// The prefix is done with before the first values arrive where it lies.
+template <int kDim>
+constexpr uint32_t kTreeSmem = TreeShape<kDim>::kRest + sizeof(TreeShared);
+static_assert(kTreeSmem<128> <= 227 * 1024, "shared memory of a CTA");
+static_assert(sizeof(TreePrefix) <= TreeShape<64>::kTile, "the prefix fits a stage");
+
+__device__ __forceinline__ void cp_async16_zero(uint32_t dst, const void* src, bool real) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(real ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int kN>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kN) : "memory");
+}
+
+// First key of an item's tile and the end of its keys.
+struct TileKeys {
+  int32_t first, end;
+  bool drafted;   // it may hold drafted tokens
+  uint64_t who;   // q2k: which tokens chose it
+};
+__device__ __forceinline__ TileKeys tile_keys(const TreeArgs& a, const TreeWalk& s, int64_t base,
+                                              int32_t i) {
+  if (!a.q2k) {
+    const int32_t f = i * kBlock;
+    return TileKeys{f, min(f + kBlock, s.w.len + s.w.n), true, ~0ull};
+  }
+  if (i + 1 == s.tiles) return TileKeys{s.w.len, s.w.len + s.w.n, true, 0ull};
+  const int32_t f = a.ids[base + i] * kBlock;
+  return TileKeys{f, min(f + kBlock, s.w.len), false, a.who[base + i]};
+}
+
+// The copying warps' side: fills query, key and value tiles and tells of each
+// when its copies have landed, two groups of copies later.
+template <typename T, int kDim>
+struct Copier {
+  using S = TreeShape<kDim>;
+  static constexpr int kChunks = kDim / 8;
+  static constexpr int kAtOnce = 32 / kChunks;  // rows that one copy instruction covers
+  const TreeArgs& a;
+  TreeBars& bars;
+  uint32_t sbase;
+  volatile int* abort_flag;
+  int warp, lane;                 // of the copying warps
+  uint32_t pend[2];               // barriers of groups not told of yet, oldest first
+  int n_pend;
+
+  __device__ __forceinline__ void tell(uint32_t bar) {
+    fence_proxy_async_smem();
+    mbar_arrive(bar);
+  }
+  __device__ __forceinline__ void commit(uint32_t bar) {
+    cp_async_commit();
+    if (n_pend == 2) {
+      cp_async_wait<2>();
+      tell(pend[0]);
+      pend[0] = pend[1];
+      pend[1] = bar;
+    } else {
+      pend[n_pend++] = bar;
+    }
+  }
+  __device__ __forceinline__ void flush() {
+    cp_async_wait<0>();
+    for (int i = 0; i < n_pend; ++i) tell(pend[i]);
+    n_pend = 0;
+  }
+  static __device__ __forceinline__ uint32_t at(int row, int chunk) {
+    return (chunk >> 3) * 16384u + row * 128u + (((chunk & 7) ^ (row & 7)) << 4);
+  }
+  // 128 rows of queries from matrix row r0 of the item's row on.
+  __device__ __forceinline__ void queries(const TreeWalk& s, int32_t r0, int32_t rows,
+                                          uint32_t tile) {
+    const int sub = lane / kChunks, c = lane % kChunks;
+    const int64_t width = int64_t(a.kv_heads) * a.group * kDim;
+    const T* q = static_cast<const T*>(a.q) + s.w.t0 * width + int64_t(s.g) * a.group * kDim +
+                 c * 8;
+#pragma unroll 4
+    for (int x = 0; x < 32 / kAtOnce; ++x) {
+      const int r = warp * 32 + x * kAtOnce + sub;
+      const int32_t m = r0 + r, node = m / a.group;
+      const bool real = r < rows;
+      cp_async16_zero(tile + at(r, c),
+                      real ? q + node * width + (m - node * a.group) * kDim
+                           : static_cast<const T*>(a.q),
+                      real);
+    }
+  }
+  // The pages of the warp's 32 keys of a tile, a lane each (-1: no such key).
+  __device__ __forceinline__ int32_t pages(const TreeWalk& s, const TileKeys& t) const {
+    const int32_t j = t.first + warp * 32 + lane;
+    if (j >= t.end) return -1;
+    const int32_t p = a.table.pages[int64_t(s.row) * a.table.stride + (j >> a.table.shift)];
+    if (p < 0 || p >= a.table.num_pages) {
+      raise_paged(a.table.status, MSA_ERR_BAD_PAGE);
+      return -1;
+    }
+    return p;
+  }
+  __device__ __forceinline__ void keys(const PagedPool& pool, const TreeWalk& s,
+                                       const TileKeys& t, int32_t page, uint32_t tile) {
+    const int sub = lane / kChunks, c = lane % kChunks;
+    const T* base = static_cast<const T*>(pool.base) + s.g * pool.head + c * 8;
+    const int32_t mask = (1 << a.table.shift) - 1;
+#pragma unroll 4
+    for (int x = 0; x < 32 / kAtOnce; ++x) {
+      const int key = x * kAtOnce + sub;
+      const int32_t p = __shfl_sync(0xffffffffu, page, key);
+      const int32_t slot = (t.first + warp * 32 + key) & mask;
+      const T* src = p >= 0 ? base + p * pool.page + slot * pool.token
+                            : static_cast<const T*>(pool.base);
+      cp_async16_zero(tile + at(warp * 32 + key, c), src, p >= 0);
+    }
+  }
+};
+
+template <int kRegs>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
+// P = 2^(s c2 - mref) of one tile row (tensor memory columns [cs, cs + 128) of
+// the thread's lane) as pairs of T into pk; with kMask the keys whose bit is not
+// set in words give 0.  Returns the sum of the 32-bit values; *tmax gets the
+// row's largest raw score.
+template <typename T, bool kMask>
+__device__ __forceinline__ float tree_row_exp(uint32_t cs, const uint32_t (&words)[4], float c2,
+                                              float mref, uint32_t (&pk)[64], float* tmax) {
+  const uint64_t cc = f2_pack(__float_as_uint(c2), __float_as_uint(c2));
+  const uint64_t nm = f2_pack(__float_as_uint(-mref), __float_as_uint(-mref));
+  uint64_t ls[2] = {0ull, 0ull};
+  float m0 = -INFINITY, m1 = -INFINITY;
+  auto expo = [&](const uint32_t (&r)[16], int c) {
+#pragma unroll
+    for (int j = 0; j < 16; j += 2) {
+      float x0 = __uint_as_float(r[j]), x1 = __uint_as_float(r[j + 1]);
+      const uint64_t x2 = f2_fma(f2_pack(r[j], r[j + 1]), cc, nm);
+      float p0 = fast_exp2(f2_lo(x2)), p1 = fast_exp2(f2_hi(x2));
+      if (kMask) {
+        const uint32_t w = words[c >> 1] >> ((c & 1) * 16 + j);
+        p0 = (w & 1u) ? p0 : 0.f;
+        p1 = (w & 2u) ? p1 : 0.f;
+        x0 = (w & 1u) ? x0 : -INFINITY;
+        x1 = (w & 2u) ? x1 : -INFINITY;
+      }
+      if (j & 2) m1 = fmax3(m1, x0, x1); else m0 = fmax3(m0, x0, x1);
+      ls[(j >> 1) & 1] =
+          f2_add(ls[(j >> 1) & 1], f2_pack(__float_as_uint(p0), __float_as_uint(p1)));
+      pk[8 * c + (j >> 1)] = Pair<T>::pack(p0, p1);
+    }
+  };
+  // chunk c+1 loads while chunk c is exponentiated
+  uint32_t r0[16], r1[16];
+  tmem_ld16(cs, r0);
+  tmem_ld_wait();
+  reg_fence16(r0);
+#pragma unroll
+  for (int c = 0; c < 8; c += 2) {
+    tmem_ld16(cs + 16 * c + 16, r1);
+    expo(r0, c);
+    tmem_ld_wait();
+    reg_fence16(r1);
+    if (c < 6) tmem_ld16(cs + 16 * c + 32, r0);
+    expo(r1, c + 1);
+    if (c < 6) {
+      tmem_ld_wait();
+      reg_fence16(r0);
+    }
+  }
+  *tmax = fmaxf(m0, m1);
+  const uint64_t s2 = f2_add(ls[0], ls[1]);
+  return f2_lo(s2) + f2_hi(s2);
+}
+// The row's largest raw score alone.
+template <bool kMask>
+__device__ __forceinline__ float tree_row_max(uint32_t cs, const uint32_t (&words)[4]) {
+  float m = -INFINITY;
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    uint32_t r[16];
+    tmem_ld16(cs + 16 * c, r);
+    tmem_ld_wait();
+    reg_fence16(r);
+#pragma unroll
+    for (int j = 0; j < 16; j += 2) {
+      float x0 = __uint_as_float(r[j]), x1 = __uint_as_float(r[j + 1]);
+      if (kMask) {
+        const uint32_t w = words[c >> 1] >> ((c & 1) * 16 + j);
+        x0 = (w & 1u) ? x0 : -INFINITY;
+        x1 = (w & 2u) ? x1 : -INFINITY;
+      }
+      m = fmax3(m, x0, x1);
+    }
+  }
+  return m;
+}
+
+// The tokens on the path of token `node` of a row (bit i: token i), by a warp:
+// paths of twice the length six times over.
+__device__ __forceinline__ uint64_t path_of(const TreeArgs& a, const TreeRow& w, int node) {
+  if (!a.parents) return node >= 63 ? ~0ull : (2ull << node) - 1;
+  const int lane = threadIdx.x & 31;
+  int up[2];
+  uint64_t path[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int j = lane + 32 * h;
+    up[h] = j < w.n ? a.parents[w.t0 + j] : -1;
+    if (up[h] < -1 || up[h] >= j) {
+      raise_paged(a.table.status, MSA_ERR_BAD_TREE);
+      up[h] = -1;
+    }
+    path[h] = 1ull << j;
+  }
+#pragma unroll 1
+  for (int step = 0; step < 6; ++step) {
+    uint64_t add[2];
+    int further[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint64_t p0 = __shfl_sync(0xffffffffu, path[0], up[h] & 31);
+      const uint64_t p1 = __shfl_sync(0xffffffffu, path[1], up[h] & 31);
+      const int u0 = __shfl_sync(0xffffffffu, up[0], up[h] & 31);
+      const int u1 = __shfl_sync(0xffffffffu, up[1], up[h] & 31);
+      add[h] = up[h] < 0 ? 0ull : up[h] < 32 ? p0 : p1;
+      further[h] = up[h] < 0 ? -1 : up[h] < 32 ? u0 : u1;
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      path[h] |= add[h];
+      up[h] = further[h];
+    }
+  }
+  const uint64_t p0 = __shfl_sync(0xffffffffu, path[0], node & 31);
+  const uint64_t p1 = __shfl_sync(0xffffffffu, path[1], node & 31);
+  return node < 32 ? p0 : p1;
+}
+
+// The tensor cores' side, one thread.  Step k works for slot k & 1: S of step k,
+// then P V of step k - 1.
+template <typename T, int kDim>
+__device__ __forceinline__ void tree_mma_role(const TreeArgs& a, TreeBars& bars, TreeWalk walk,
+                                           uint32_t tmem, uint32_t sbase,
+                                           volatile int* abort_flag) {
+  using S = TreeShape<kDim>;
+  constexpr bool kBf = sizeof(T) == 2 && kLift<T> == 0.f;
+  constexpr uint32_t idS = kBf ? idesc_bf16_f32(128, 128, 0, 0) : idesc_f16_f32(128, 128, 0, 0);
+  constexpr uint32_t idPV = kBf ? idesc_bf16_f32(128, kDim, 0, 1) : idesc_f16_f32(128, kDim, 0, 1);
+  auto wait = [&](uint64_t& bar, uint32_t ph) {
+    return mbar_wait(smem_u32(&bar), ph & 1, abort_flag);
+  };
+  const uint64_t dq = sdesc_sw128(sbase + S::kQ, 16u, 1024u);
+  const uint64_t dk = sdesc_sw128(sbase + S::kK, 16u, 1024u);
+  const uint64_t dv = sdesc_sw128(sbase + S::kV, 16384u, 1024u);
+  constexpr uint64_t kStage = S::kTile >> 4;
+  uint32_t nt = 0;             // key tiles before the segment
+  uint32_t nx[2] = {0, 0};     // steps of each slot
+  uint32_t segs = 0;
+  bool ok = true;
+  do {
+    const bool split = walk.rows_here() <= kTileRows;
+    const int tiles = walk.i1 - walk.i0, steps = split ? tiles : 2 * tiles;
+    bool used[2] = {false, false};
+    // P V of step k
+    auto issue_pv = [&](int k) -> bool {
+      const int x = k & 1, i = split ? k : k >> 1;
+      const uint32_t t = nt + i, stg = t % kVStages;
+      if (!wait(bars.p_full[x], nx[x])) return false;
+      if (!wait(bars.v_full[stg], t / kVStages)) return false;
+      if (!used[0] && !used[1] && segs > 0 && !wait(bars.o_free, segs - 1)) return false;
+      tc_fence_after();
+      const uint64_t bv = dv + stg * kStage;
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk)
+        umma_ts(tmem + S::kTmO + kDim * x, tmem + 128 * x + kk * 8, bv + uint64_t(kk) * 128u, idPV,
+                (used[x] || kk > 0) ? 1u : 0u);
+      used[x] = true;
+      ++nx[x];
+      if (split || x == 1) umma_commit(smem_u32(&bars.v_empty[stg]));
+      if (k + 2 >= steps) umma_commit(smem_u32(&bars.o_full[x]));
+      return true;
+    };
+    for (int k = 0; ok && k < steps; ++k) {
+      const int x = k & 1, i = split ? k : k >> 1;
+      const uint32_t t = nt + i, stg = t % kKStages;
+      if ((split || x == 0) && !wait(bars.k_full[stg], t / kKStages)) { ok = false; break; }
+      if (k == 0 && !wait(bars.q_full, segs)) { ok = false; break; }
+      tc_fence_after();
+      const uint64_t bq = dq + (split ? 0 : x) * kStage, bk = dk + stg * kStage;
+#pragma unroll
+      for (int kk = 0; kk < kDim / 16; ++kk) {
+        const uint64_t off = uint64_t((kk >> 2) * 1024 + (kk & 3) * 2);
+        umma_ss(tmem + 128 * x, bq + off, bk + off, idS, kk > 0);
+      }
+      umma_commit(smem_u32(&bars.s_full[x]));
+      if (split || x == 1) umma_commit(smem_u32(&bars.k_empty[stg]));
+      if (k + 1 == steps) umma_commit(smem_u32(&bars.q_empty));
+      if (k > 0 && !issue_pv(k - 1)) { ok = false; break; }
+    }
+    if (ok) ok = issue_pv(steps - 1);
+    nt += tiles;
+    ++segs;
+  } while (ok && walk.next());
+  umma_commit(smem_u32(&bars.fin));
+  mbar_wait_drain(smem_u32(&bars.fin), 0);
+}
+
+template <typename T, int kDim>
+__global__ void __launch_bounds__(kTreeThreads, 1)
+    k_paged_tree(const __grid_constant__ TreeArgs a) {
+  using S = TreeShape<kDim>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  TreeShared& sh = *reinterpret_cast<TreeShared*>(smem + S::kRest);
+  TreePrefix& prefix = *reinterpret_cast<TreePrefix*>(smem + S::kV);
+  TreeBars& bars = sh.bars;
+  const uint32_t sbase = smem_u32(smem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  volatile int* abort_flag = &sh.abort;
+  if (sbase & 1023u) {  // (no static shared memory, so it is aligned: the swizzle needs that)
+    if (tid == 0) raise_paged(a.table.status, MSA_ERR_TIMEOUT);
+    return;
+  }
+  if (tid == 0) {
+    sh.abort = 0;
+    auto init = [](uint64_t& b, uint32_t n) { mbar_init(smem_u32(&b), n); };
+    init(bars.q_full, kCopyWarps * 32);
+    init(bars.q_empty, 1);
+    for (int i = 0; i < kKStages; ++i) {
+      init(bars.k_full[i], kCopyWarps * 32);
+      init(bars.k_empty[i], 1);
+    }
+    for (int i = 0; i < kVStages; ++i) {
+      init(bars.v_full[i], kCopyWarps * 32);
+      init(bars.v_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      init(bars.s_full[i], 1);
+      init(bars.p_full[i], 128);
+      init(bars.o_full[i], 1);
+    }
+    init(bars.o_free, 256);
+    init(bars.ml, 256);
+    init(bars.fin, 1);
+    fence_mbar_init();
+  }
+  if (warp == kSoftWarps + kCopyWarps) {
+    tmem_alloc(smem_u32(&sh.tmem_base), 512);
+    tmem_relinquish();
+  }
+  grid_dep_wait();
+  grid_dep_release();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem_base;
+  if (blockIdx.x == 0) check_offsets(a.offs, a.table.rows, a.T, a.table.status);
+  // rows that do not fit: their tokens see nothing
+  for (int32_t r = blockIdx.x; r < a.table.rows; r += gridDim.x) {
+    const int32_t o0 = a.offs[r], o1 = a.offs[r + 1], len = a.kv_len[r], n = o1 - o0;
+    if (o0 < 0 || o1 <= o0 || o1 > a.T || row_fits(a, n, len)) continue;
+    if (tid == 0)
+      raise_paged(a.table.status, n > kNodes ? MSA_ERR_BAD_TREE : MSA_ERR_BAD_PAGE);
+    const int64_t heads = int64_t(a.kv_heads) * a.group;
+    uint4* o = reinterpret_cast<uint4*>(static_cast<T*>(a.o) + o0 * heads * kDim);
+    for (int64_t i = tid; i < n * heads * (kDim / 8); i += kTreeThreads)
+      o[i] = make_uint4(0, 0, 0, 0);
+    for (int64_t i = tid; i < n * heads; i += kTreeThreads) a.lse[o0 * heads + i] = -INFINITY;
+  }
+  make_tree_prefix(a, prefix);
+  const int32_t runs = min(prefix.total, int32_t(gridDim.x));
+  const int32_t run = blockIdx.x;
+  TreeWalk walk(a);
+  if (run < runs) {
+    const int32_t begin = run_start(prefix.total, runs, run);
+    walk.begin(prefix, begin, run_start(prefix.total, runs, run + 1) - begin);
+  }
+  __syncthreads();  // the prefix is read
+  if (run < runs) {
+    if (warp >= kSoftWarps && warp < kSoftWarps + kCopyWarps) {
+      // ---------------- copies
+      fewer_registers<kOtherRegs>();
+      Copier<T, kDim> copy{a, bars, sbase, abort_flag, warp - kSoftWarps, lane, {0, 0}, 0};
+      uint32_t nt = 0, segs = 0;
+      bool ok = true;
+      do {
+        const int32_t rows = walk.rows_here();
+        const int64_t base =
+            a.q2k ? list_base(a, walk.row, walk.layer, walk.g, walk.w.t0) : 0;
+        TileKeys t = tile_keys(a, walk, base, walk.i0);
+        int32_t page = copy.pages(walk, t);
+        for (int32_t i = walk.i0; ok && i < walk.i1; ++i, ++nt) {
+          const uint32_t ks = nt % kKStages, vs = nt % kVStages;
+          if (nt >= kKStages &&
+              !mbar_wait_warp(smem_u32(&bars.k_empty[ks]), (nt / kKStages - 1) & 1, abort_flag)) {
+            ok = false;
+            break;
+          }
+          const uint32_t seen = __ballot_sync(0xffffffffu, page >= 0);
+          if (lane == 0) sh.there[nt & 3][warp - kSoftWarps] = seen;
+          copy.keys(a.k, walk, t, page, sbase + S::kK + ks * S::kTile);
+          copy.commit(smem_u32(&bars.k_full[ks]));
+          if (i == walk.i0) {
+            // the queries, once all products with the ones before them are done
+            if (segs > 0) {
+              copy.flush();
+              if (!mbar_wait_warp(smem_u32(&bars.q_empty), (segs - 1) & 1, abort_flag)) {
+                ok = false;
+                break;
+              }
+            }
+            const int32_t r0 = walk.layer * kPairRows;
+            copy.queries(walk, r0, min(rows, kTileRows), sbase + S::kQ);
+            if (rows > kTileRows)
+              copy.queries(walk, r0 + kTileRows, rows - kTileRows, sbase + S::kQ + S::kTile);
+            copy.commit(smem_u32(&bars.q_full));
+          }
+          if (nt >= kVStages &&
+              !mbar_wait_warp(smem_u32(&bars.v_empty[vs]), (nt / kVStages - 1) & 1, abort_flag)) {
+            ok = false;
+            break;
+          }
+          copy.keys(a.v, walk, t, page, sbase + S::kV + vs * S::kTile);
+          copy.commit(smem_u32(&bars.v_full[vs]));
+          if (i + 1 < walk.i1) {
+            t = tile_keys(a, walk, base, i + 1);
+            page = copy.pages(walk, t);
+          }
+        }
+        ++segs;
+      } while (ok && walk.next());
+      copy.flush();
+    } else if (warp >= kSoftWarps + kCopyWarps) {
+      // ---------------- tensor cores
+      fewer_registers<kOtherRegs>();
+      if (warp == kSoftWarps + kCopyWarps && lane == 0)
+        tree_mma_role<T, kDim>(a, bars, walk, tmem, sbase, abort_flag);
+    } else {
+      // ---------------- softmax and results of slot x (warps 0-3: A, 4-7: B)
+      more_registers<kSoftRegs>();
+      const int x = warp >> 2, quad = warp & 3;
+      const int trow = quad * 32 + lane;  // tile row = lane of tensor memory
+      const uint32_t lane_base = uint32_t(quad * 32) << 16;
+      const uint32_t cs = tmem + lane_base + 128 * x;
+      const uint32_t co = tmem + lane_base + S::kTmO;
+      uint32_t nt = 0, nx = 0, joins = 0, no[2] = {0, 0};
+      do {
+        const int32_t rows = walk.rows_here();
+        const bool split = rows <= kTileRows;
+        const int32_t m = (split ? 0 : x * kTileRows) + trow;  // matrix row of the item
+        const bool real = m < rows;
+        const int32_t mr = walk.layer * kPairRows + (real ? m : 0);
+        const int32_t node = mr / a.group, head = mr - node * a.group;
+        const int64_t base =
+            a.q2k ? list_base(a, walk.row, walk.layer, walk.g, walk.w.t0) : 0;
+        const int tiles = walk.i1 - walk.i0;
+        const int steps = split ? (tiles + 1 - x) / 2 : tiles;
+        uint64_t path = 0;
+        // (does the segment reach the drafted tokens?)
+        if (a.q2k ? walk.i1 == walk.tiles : int64_t(walk.i1) * kBlock > walk.w.len)
+          path = path_of(a, walk.w, node);
+        float mref = -INFINITY, lsum = 0.f;
+        bool ok = true;
+        for (int k = 0; k < steps; ++k) {
+          const int i = split ? 2 * k + x : k;
+          const uint32_t t = nt + i;
+          const TileKeys tk = tile_keys(a, walk, base, walk.i0 + i);
+          // the row's keys in this tile
+          const bool chose = real && ((tk.who >> node) & 1);
+          const int32_t cached = chose ? min(max(walk.w.len - tk.first, 0), kBlock) : 0;
+          uint32_t words[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int32_t n = cached - 32 * c;
+            words[c] = n >= 32 ? 0xffffffffu : n > 0 ? (1u << n) - 1 : 0u;
+          }
+          if (tk.drafted && tk.end > walk.w.len && real) {
+            const int32_t off = walk.w.len - tk.first;  // place of drafted token 0
+            uint64_t lo, hi;
+            if (off <= 0) {
+              lo = -off < 64 ? path >> -off : 0;
+              hi = 0;
+            } else if (off < 64) {
+              lo = path << off;
+              hi = path >> (64 - off);
+            } else {
+              lo = 0;
+              hi = path << (off - 64);
+            }
+            words[0] |= uint32_t(lo);
+            words[1] |= uint32_t(lo >> 32);
+            words[2] |= uint32_t(hi);
+            words[3] |= uint32_t(hi >> 32);
+          }
+          if (!mbar_wait_warp(smem_u32(&bars.k_full[t % kKStages]), (t / kKStages) & 1,
+                              abort_flag) ||
+              !mbar_wait_warp(smem_u32(&bars.s_full[x]), nx & 1, abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < 4; ++c) words[c] &= sh.there[t & 3][c];
+          const uint32_t any = words[0] | words[1] | words[2] | words[3];
+          const uint32_t all = words[0] & words[1] & words[2] & words[3];
+          // Without masks where every row of the warp sees all of the tile or none
+          // of it: the latter are zeroed afterwards.
+          const bool plain = __all_sync(0xffffffffu, all == 0xffffffffu || any == 0);
+          if (k == 0) {  // the first tile sets the reference
+            const float mx = plain ? tree_row_max<false>(cs, words) : tree_row_max<true>(cs, words);
+            mref = any ? mx * a.scale_log2 - kLift<T> : -INFINITY;
+          }
+          uint32_t pk[64];
+          float tmax;
+          auto row_exp = [&]() {
+            if (!plain) return tree_row_exp<T, true>(cs, words, a.scale_log2, mref, pk, &tmax);
+            float l = tree_row_exp<T, false>(cs, words, a.scale_log2, mref, pk, &tmax);
+            if (any == 0) {
+#pragma unroll
+              for (int e = 0; e < 64; ++e) pk[e] = 0u;
+              l = 0.f;
+              tmax = -INFINITY;
+            }
+            return l;
+          };
+          float ls = row_exp();
+          const float top = tmax * a.scale_log2;
+          const bool raise = any != 0 && top > mref + (kRise + kLift<T>);
+          if (__any_sync(0xffffffffu, raise)) {
+            // O (complete up to the slot's step before) and the sum times 2^(mref -
+            // the new reference), then the weights again (S is still there)
+            const float to = top - kLift<T>;
+            const float f = raise ? fast_exp2(mref - to) : 1.f;
+            lsum *= f;
+            if (raise) mref = to;
+            if (k > 0) {
+#pragma unroll 1
+              for (int c = 0; c < kDim / 32; ++c) {
+                uint32_t o[32];
+                tmem_ld32(co + kDim * x + 32 * c, o);
+                tmem_ld_wait();
+                reg_fence32(o);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tmem_st32_nc(co + kDim * x + 32 * c, o);
+              }
+            }
+            ls = row_exp();
+          }
+          lsum += ls;
+          // P over the first 64 columns of S (all of S has been read)
+          tmem_st32_nc(cs, *reinterpret_cast<const uint32_t(*)[32]>(&pk[0]));
+          tmem_st32_nc(cs + 32, *reinterpret_cast<const uint32_t(*)[32]>(&pk[32]));
+          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive(smem_u32(&bars.p_full[x]));
+          ++nx;
+        }
+        if (!ok) break;
+        // ---- results.  Two states of the same rows are joined here, half of the
+        // columns by each slot's warps.
+        const bool two = split && tiles > 1;
+        float M = mref, l = lsum, f0 = x == 0 ? 1.f : 0.f, f1 = x == 1 ? 1.f : 0.f;
+        if (split) {
+          // the states before these are read (a round of the barrier for writing, one
+          // for reading)
+          if (joins > 0 && !mbar_wait_warp(smem_u32(&bars.ml), 1, abort_flag)) break;
+          sh.states[x][trow] = make_float2(mref, lsum);
+          mbar_arrive(smem_u32(&bars.ml));
+          if (!mbar_wait_warp(smem_u32(&bars.ml), 0, abort_flag)) break;
+          const float2 s0 = sh.states[0][trow], s1 = sh.states[1][trow];
+          mbar_arrive(smem_u32(&bars.ml));
+          ++joins;
+          M = fmaxf(s0.x, s1.x);
+          f0 = s0.x == -INFINITY ? 0.f : fast_exp2(s0.x - M);
+          f1 = s1.x == -INFINITY ? 0.f : fast_exp2(s1.x - M);
+          l = s0.y * f0 + s1.y * f1;
+        }
+        const bool use0 = split || x == 0, use1 = two || (!split && x == 1);
+        if (use0 && !mbar_wait_warp(smem_u32(&bars.o_full[0]), no[0] & 1, abort_flag)) break;
+        if (use1 && !mbar_wait_warp(smem_u32(&bars.o_full[1]), no[1] & 1, abort_flag)) break;
+        ++no[0];
+        if (two || !split) ++no[1];
+        tc_fence_after();
+        const bool whole = walk.i0 == 0 && walk.i1 == walk.tiles;
+        const int64_t part = (2 * int64_t(run) + (walk.i0 > 0 ? 0 : 1)) * kPairRows + m;
+        const int64_t orow =
+            (int64_t(walk.w.t0) + node) * (a.kv_heads * a.group) + walk.g * a.group + head;
+        const float inv = l == 0.f ? 0.f : 1.f / l;  // l == 0: no key was seen
+        const int c0 = split ? x * (kDim / 2) : 0, c1 = split ? c0 + kDim / 2 : kDim;
+#pragma unroll 1
+        for (int c = c0; c < c1; c += 32) {
+          uint32_t u[32], v[32];
+          float o[32];
+          if (use0) tmem_ld32(co + c, u);
+          if (use1) tmem_ld32(co + kDim + c, v);
+          tmem_ld_wait();
+          reg_fence32(u);
+          reg_fence32(v);
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            o[e] = (use0 ? __uint_as_float(u[e]) * f0 : 0.f) +
+                   (use1 ? __uint_as_float(v[e]) * f1 : 0.f);
+          if (!real) continue;
+          if (whole) {
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(a.o) + orow * kDim + c);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              dst[e] = make_uint4(Pair<T>::pack(o[8 * e] * inv, o[8 * e + 1] * inv),
+                                  Pair<T>::pack(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
+                                  Pair<T>::pack(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
+                                  Pair<T>::pack(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+          } else {
+            float4* dst = reinterpret_cast<float4*>(a.part_o + part * kDim + c);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          }
+        }
+        tc_fence_before();
+        mbar_arrive(smem_u32(&bars.o_free));
+        if (real && (!split || x == 0)) {
+          if (whole)
+            a.lse[orow] = l == 0.f ? -INFINITY : kLn2 * (M + log2f(l));
+          else
+            *reinterpret_cast<float2*>(a.part_ml + part * 2) = make_float2(M, l);
+        }
+        nt += tiles;
+      } while (walk.next());
+    }
+  }
+  // ---------------- teardown
+  if (tid == 0 && sh.abort) raise_paged(a.table.status, MSA_ERR_TIMEOUT);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kSoftWarps + kCopyWarps) tmem_dealloc(tmem, 512);
+}
+
+// ------------------------------------------------------------ joining runs
+// CTA x stands for run x + 1, if that run starts inside an item; the CTAs of an
+// item share its rows.  A warp takes a row, its lanes the channels.
+constexpr int kJoinThreads = 256;
+template <typename T, int kDim>
+__global__ void __launch_bounds__(kJoinThreads) k_paged_tree_join(const TreeArgs a) {
+  constexpr int kPer = kDim / 32, kLoads = 4;
+  struct __align__(4 * kPer) Chunk {
+    float x[kPer];
+  };
+  __shared__ TreePrefix prefix;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  grid_dep_wait();
+  grid_dep_release();
+  make_tree_prefix(a, prefix);
+  const int32_t total = prefix.total, runs = min(total, int32_t(gridDim.x) + 1);
+  const int32_t run = int32_t(blockIdx.x) + 1;
+  if (run >= runs) return;
+  const int32_t begin = run_start(total, runs, run);
+  TreeWalk walk(a);
+  walk.locate(prefix, begin);
+  if (walk.i0 == 0) return;
+  // the runs of the item's first and last tile
+  auto run_of = [&](int32_t t) {
+    int32_t c = int32_t(int64_t(t) * runs / total);
+    while (run_start(total, runs, c + 1) <= t) ++c;
+    return c;
+  };
+  const int32_t first = run_of(begin - walk.i0);
+  const int n = run_of(begin - walk.i0 + walk.tiles - 1) + 1 - first;
+  const int share = run - first - 1, shares = n - 1;
+  const int32_t rows = walk.rows_here();
+  for (int32_t m = share * (kJoinThreads / 32) + warp; m < rows;
+       m += shares * (kJoinThreads / 32)) {
+    float M = -INFINITY, l = 0.f, acc[kPer] = {};
+    for (int i0 = 0; i0 < n; i0 += kLoads) {
+      Chunk o[kLoads];
+      float2 ml[kLoads];
+#pragma unroll
+      for (int u = 0; u < kLoads; ++u) {
+        const int i = i0 + u;
+        ml[u] = make_float2(-INFINITY, 0.f);
+        o[u] = Chunk{};
+        if (i < n) {
+          const int64_t part = (2 * int64_t(first + i) + (i == 0 ? 1 : 0)) * kPairRows + m;
+          ml[u] = *reinterpret_cast<const float2*>(a.part_ml + part * 2);
+          o[u] = reinterpret_cast<const Chunk*>(a.part_o + part * kDim)[lane];
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kLoads; ++u) {
+        const float top = fmaxf(M, ml[u].x);
+        const float f = M == -INFINITY ? 0.f : fast_exp2(M - top);
+        const float g = ml[u].x == -INFINITY ? 0.f : fast_exp2(ml[u].x - top);
+        M = top;
+        l = l * f + ml[u].y * g;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) acc[e] = acc[e] * f + o[u].x[e] * g;
+      }
+    }
+    const int32_t mr = walk.layer * kPairRows + m, node = mr / a.group;
+    const int64_t orow = (int64_t(walk.w.t0) + node) * (a.kv_heads * a.group) +
+                         walk.g * a.group + mr - node * a.group;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    uint32_t* o = reinterpret_cast<uint32_t*>(static_cast<T*>(a.o) + orow * kDim + lane * kPer);
+#pragma unroll
+    for (int e = 0; e < kPer; e += 2) o[e / 2] = Pair<T>::pack(acc[e] * inv, acc[e + 1] * inv);
+    if (lane == 0) a.lse[orow] = l == 0.f ? -INFINITY : kLn2 * (M + log2f(l));
+  }
+}
+
+int32_t tree_layers(int64_t T, int32_t group) {
+  return int32_t((std::min<int64_t>(T, kNodes) * group + kPairRows - 1) / kPairRows);
+}
+// Where things lie in the workspace.
+struct TreeLayout {
+  size_t ml, o, counts, ids, who, total;
+  TreeLayout(int32_t rows, int64_t T, int32_t kv_heads, int32_t group, int32_t dim) {
+    const size_t lists = size_t(kv_heads) * (size_t(T) + 4 * size_t(rows)) * kTopK;
+    size_t at = 0;
+    auto take = [&](size_t n) {
+      const size_t was = at;
+      at = align_up(at + n, 256);
+      return was;
+    };
+    ml = take(sizeof(float) * 2 * 2 * kMaxRuns * kPairRows);
+    o = take(sizeof(float) * 2 * kMaxRuns * kPairRows * size_t(dim));
+    counts = take(sizeof(int32_t) * size_t(tree_layers(T, group)) * rows * kv_heads);
+    ids = take(sizeof(int32_t) * lists);
+    who = take(sizeof(uint64_t) * lists);
+    total = at;
+  }
+};
+
+template <typename T, int kDim>
+cudaError_t launch_tree(const TreeArgs& a, cudaStream_t s) {
+  auto kernel = k_paged_tree<T, kDim>;
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(kernel, kTreeSmem<kDim>, done);
+  if (e != cudaSuccess) return e;
+  if (a.q2k) {
+    launch_begin("paged_tree_lists", s);
+    e = launch_k(true, k_paged_tree_lists,
+                 dim3(unsigned(int64_t(a.layers) * a.table.rows * a.kv_heads)),
+                 dim3(kListThreads), 0, s, a);
+    launch_end("paged_tree_lists", s);
+    if (e != cudaSuccess) return e;
+  }
+  const int grid = std::min(device_sm_count(), kMaxRuns);
+  launch_begin("paged_tree", s);
+  e = launch_k(true, kernel, dim3(unsigned(grid)), dim3(kTreeThreads), kTreeSmem<kDim>, s, a);
+  launch_end("paged_tree", s);
+  if (e != cudaSuccess || grid == 1) return e;
+  launch_begin("paged_tree_join", s);
+  e = launch_k(true, k_paged_tree_join<T, kDim>, dim3(unsigned(grid - 1)), dim3(kJoinThreads), 0,
+               s, a);
+  launch_end("paged_tree_join", s);
+  return e;
+}
+
+bool good_tree(const msa_paged_cache* cache, int32_t rows, int64_t T, int32_t q_heads) {
+  return rows >= 1 && rows <= kMaxRows && T >= 1 && T <= kMaxTokens && q_heads >= 1 &&
+         q_heads % cache->kv_heads == 0 && q_heads / cache->kv_heads <= 16;
+}
+
+}  // namespace
+}  // namespace msa
+
+using namespace msa;
+
+extern "C" msa_status msa_paged_tree_workspace_bytes(const msa_paged_cache* cache, int32_t rows,
+                                                     int64_t T, int32_t q_heads, size_t* bytes) {
+  const msa_status st = check_cache(cache);
+  if (st != MSA_OK) return st;
+  if (!bytes || !good_tree(cache, rows, T, q_heads)) return MSA_ERR_INVALID_ARG;
+  *bytes = TreeLayout(rows, T, cache->kv_heads, q_heads / cache->kv_heads, cache->head_dim).total;
+  return MSA_OK;
+}
+
+extern "C" msa_status msa_paged_tree(const msa_paged_cache* cache, const msa_page_table* table,
+                                     const int32_t* row_offsets, const int32_t* kv_len,
+                                     const int32_t* parents, int64_t T, const void* q,
+                                     int32_t q_heads, float softmax_scale, const int32_t* q2k,
+                                     void* o, float* lse, void* workspace, size_t workspace_bytes,
+                                     msa_stream_t stream) {
+  msa_status st = check_cache(cache);
+  if (st != MSA_OK) return st;
+  st = check_table(table, cache->page_size);
+  if (st != MSA_OK) return st;
+  if (!row_offsets || !kv_len || !q || !o || !lse || !workspace ||
+      !good_tree(cache, table->rows, T, q_heads))
+    return MSA_ERR_INVALID_ARG;
+  if (!(softmax_scale > 0.f) || softmax_scale > 1e30f) return MSA_ERR_INVALID_ARG;
+  if (!paged_aligned(q) || !paged_aligned(o) || !paged_aligned(workspace) ||
+      !paged_aligned4(row_offsets) || !paged_aligned4(kv_len) || !paged_aligned4(parents) ||
+      !paged_aligned4(q2k) || !paged_aligned4(lse))
+    return MSA_ERR_ALIGNMENT;
+  const int32_t group = q_heads / cache->kv_heads, layers = tree_layers(T, group);
+  // tiles are counted in 32 bits
+  if (int64_t(table->rows) * cache->kv_heads * layers * table->width * cache->page_size >
+      (int64_t(1) << 36))
+    return MSA_ERR_INVALID_ARG;
+  const TreeLayout at(table->rows, T, cache->kv_heads, group, cache->head_dim);
+  if (workspace_bytes < at.total) return MSA_ERR_WORKSPACE;
+  st = check_device();
+  if (st != MSA_OK) return st;
+  TreeArgs a{};
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a.q = q;
+  a.k = PagedPool{cache->k, cache->k_stride[0], cache->k_stride[1], cache->k_stride[2]};
+  a.v = PagedPool{cache->v, cache->v_stride[0], cache->v_stride[1], cache->v_stride[2]};
+  a.table = table_args(table, cache->page_size, cache->num_pages, cache->status);
+  a.offs = row_offsets;
+  a.kv_len = kv_len;
+  a.parents = parents;
+  a.q2k = q2k;
+  a.o = o;
+  a.lse = lse;
+  a.T = T;
+  a.scale_log2 = softmax_scale * kLog2e;
+  a.kv_heads = cache->kv_heads;
+  a.group = group;
+  a.layers = layers;
+  a.part_ml = reinterpret_cast<float*>(ws + at.ml);
+  a.part_o = reinterpret_cast<float*>(ws + at.o);
+  a.counts = reinterpret_cast<int32_t*>(ws + at.counts);
+  a.ids = reinterpret_cast<int32_t*>(ws + at.ids);
+  a.who = reinterpret_cast<uint64_t*>(ws + at.who);
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (cache->dtype == MSA_BF16)
+    e = cache->head_dim == 128 ? launch_tree<__nv_bfloat16, 128>(a, s)
+                               : launch_tree<__nv_bfloat16, 64>(a, s);
+  else
+    e = cache->head_dim == 128 ? launch_tree<__half, 128>(a, s) : launch_tree<__half, 64>(a, s);
+  return e == cudaSuccess ? MSA_OK : MSA_ERR_CUDA;
+}

@@ -1,0 +1,392 @@
+// tree_verify.cu - which drafted tokens of a row stay, by given random
+// numbers, and the token behind them.
+//
+// Mathematics: at a token with target distribution p and drafting distribution
+// q, drafts are tried one after the other against what is left of p: r = p,
+// S = 1; draft x is kept if u q(x) < r(x) / S, else r = max(r / S - q, 0),
+// S = sum r.  Keeping with probability min(1, r(x) / (S q(x))) and going on from
+// the rest leaves p as the distribution of what is kept.  Without q a draft is
+// no random choice: kept if u S < r(x), else r(x) = 0.  The token behind the last
+// kept one is drawn from r by its running sum.
+//
+// r(x) of one token follows from p(x), q(x) and the S so far, so the walk needs
+// a pass over the vocabulary only for each S behind a rejection, and one for the
+// last draw.  All drafts' p(x) and q(x) are loaded side by side before the walk.
+//
+// A cluster of CTAs takes a row, each a run of the vocabulary, each warp a run
+// of that; all walk alike.  Sums: the running sum's steps are as narrow as 1 /
+// vocab, where 32 bits would draw a neighbour, and 64-bit additions are 1/64 as
+// fast here as 32-bit ones (they would take ten times as long as the reading).
+// So a lane adds in pairs of 32-bit numbers (the sum and what its rounding lost,
+// exact two-sums), which are put together in 64 bits once a warp: 2^-40 of the
+// sum at worst.  The drawn token's run is then added again, finer, until a warp
+// looks at 32 values at a time.
+#include <cooperative_groups.h>
+
+#include <algorithm>
+
+#include "paged.cuh"
+
+namespace msa {
+namespace {
+
+constexpr int kTree = 64;
+constexpr int kVerWarps = 16;
+constexpr int kVerThreads = kVerWarps * 32;
+constexpr int kVerCluster = 8;
+constexpr int kVerLoads = 8;  // values of each distribution that a lane has in flight
+
+struct VerifyArgs {
+  const float *target, *draft;  // draft may be null
+  int64_t target_stride, draft_stride;
+  const int32_t *tokens, *parents, *offs;
+  const float *u, *u_last;
+  int32_t *path, *count, *last;
+  int64_t T;
+  int32_t vocab, max_path, cluster;
+};
+
+// A sum in two 32-bit numbers.
+struct Pair32 {
+  float hi, lo;
+  __device__ __forceinline__ void add(float x) {  // exact but for lo's own rounding
+    const float s = __fadd_rn(hi, x);
+    const float b = __fsub_rn(s, hi);
+    lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(x, b)));
+    hi = s;
+  }
+  __device__ __forceinline__ void add(const Pair32& o) {
+    add(o.hi);
+    lo = __fadd_rn(lo, o.lo);
+  }
+  __device__ __forceinline__ double value() const { return double(hi) + double(lo); }
+};
+__device__ __forceinline__ Pair32 warp_sum(Pair32 s) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    Pair32 t{__shfl_xor_sync(0xffffffffu, s.hi, o), __shfl_xor_sync(0xffffffffu, s.lo, o)};
+    // both lanes of a pair must get the same bits: the lower lane's sum first
+    if (threadIdx.x & o) {
+      const Pair32 x = s;
+      s = t;
+      t = x;
+    }
+    s.add(t);
+  }
+  return s;
+}
+
+// What is left of a token's distribution: p's row, q's, the factors so far, the
+// tokens that were rejected (without q).
+struct Rest {
+  const float *p, *q;
+  const float* f;      // shared
+  const int32_t* out;  // shared
+  int n;               // rejections
+  bool drawn;
+  __device__ __forceinline__ float at(float p_x, float q_x, int32_t x) const {
+    float r = p_x;
+    if (drawn) {
+      for (int i = 0; i < n; ++i) r = fmaxf(__fsub_rn(__fmul_rn(r, f[i]), q_x), 0.f);
+    } else {
+      for (int i = 0; i < n; ++i) r = out[i] == x ? 0.f : r;
+    }
+    return r;
+  }
+};
+
+// Sum of r over [lo, hi), by a warp.
+__device__ __forceinline__ Pair32 run_sum(const Rest& rest, int32_t lo, int32_t hi) {
+  const int lane = threadIdx.x & 31;
+  Pair32 s{0.f, 0.f};
+  const bool two = rest.drawn && rest.n > 0;
+  for (int32_t x0 = lo + lane; x0 < hi; x0 += 32 * kVerLoads) {
+    float p[kVerLoads], q[kVerLoads];
+#pragma unroll
+    for (int i = 0; i < kVerLoads; ++i) {
+      const int32_t x = x0 + 32 * i;
+      p[i] = x < hi ? rest.p[x] : 0.f;
+      q[i] = two && x < hi ? rest.q[x] : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < kVerLoads; ++i) s.add(rest.at(p[i], q[i], x0 + 32 * i));
+  }
+  return warp_sum(s);
+}
+
+__global__ void __launch_bounds__(kVerThreads) k_tree_verify(const VerifyArgs a) {
+  namespace cg = cooperative_groups;
+  cg::cluster_group cluster = cg::this_cluster();
+  __shared__ int32_t par[kTree], tok[kTree], out[kTree];
+  __shared__ float us[kTree], pv[kTree], qv[kTree], factor[kTree];
+  __shared__ double warp_total[kVerWarps];
+  __shared__ double total[2];  // the CTA's, of this pass and the one before
+  __shared__ int32_t path[kTree];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = int(cluster.block_rank());
+  const int32_t r = blockIdx.x / a.cluster;
+  grid_dep_wait();
+  grid_dep_release();
+  const int64_t t0 = a.offs[r], t1 = a.offs[r + 1];
+  const int n = t0 >= 0 && t0 < t1 && t1 <= a.T && t1 - t0 <= kTree ? int(t1 - t0) : 0;
+  int32_t* const row_path = a.path + int64_t(r) * a.max_path;
+  if (n == 0) {
+    if (rank == 0) {
+      for (int i = tid; i < a.max_path; i += kVerThreads) row_path[i] = -1;
+      if (tid == 0) {
+        a.count[r] = 0;
+        a.last[r] = -1;
+      }
+    }
+    return;  // all CTAs of the cluster
+  }
+  if (tid < n) {
+    const int64_t t = t0 + tid;
+    const int32_t x = a.tokens[t];
+    int32_t up = a.parents ? a.parents[t] : tid - 1;
+    if (tid == 0 || up < 0 || up >= tid || x < 0 || x >= a.vocab) up = -1;
+    par[tid] = up;
+    tok[tid] = x;
+    if (up >= 0) {
+      us[tid] = a.u[t];
+      pv[tid] = a.target[(t0 + up) * a.target_stride + x];
+      qv[tid] = a.draft ? a.draft[(t0 + up) * a.draft_stride + x] : 0.f;
+    }
+  }
+  __syncthreads();
+
+  // the CTA's run of the vocabulary and the warp's
+  const int32_t V = a.vocab;
+  const int32_t c0 = int32_t(int64_t(V) * rank / a.cluster);
+  const int32_t c1 = int32_t(int64_t(V) * (rank + 1) / a.cluster);
+  const int32_t w0 = c0 + int32_t(int64_t(c1 - c0) * warp / kVerWarps);
+  const int32_t w1 = c0 + int32_t(int64_t(c1 - c0) * (warp + 1) / kVerWarps);
+  int passes = 0;
+  double before = 0.0, R = 0.0;
+  // The sum over the vocabulary, R, and over the CTAs before this one; the same
+  // in every thread of the cluster.  total[] alternates, so one barrier a pass
+  // is enough.
+  auto sum_all = [&](const Rest& rest) {
+    const Pair32 s = run_sum(rest, w0, w1);
+    if (lane == 0) warp_total[warp] = s.value();
+    __syncthreads();
+    double* mine = &total[passes & 1];
+    ++passes;
+    if (tid == 0) {
+      double v = 0.0;
+      for (int w = 0; w < kVerWarps; ++w) v += warp_total[w];
+      *mine = v;
+    }
+    cluster.sync();
+    double each[kVerCluster];
+#pragma unroll
+    for (int c = 0; c < kVerCluster; ++c)
+      each[c] = c < a.cluster ? *cluster.map_shared_rank(mine, c) : 0.0;
+    R = before = 0.0;
+#pragma unroll
+    for (int c = 0; c < kVerCluster; ++c) {
+      if (c == rank) before = R;
+      if (c < a.cluster) R += each[c];
+    }
+  };
+
+  // ---- the walk: every warp of every CTA alike
+  int cur = 0, kept = 1, out_n = 0;
+  double S = 1.0;
+  Rest rest{a.target + t0 * a.target_stride, a.draft ? a.draft + t0 * a.draft_stride : nullptr,
+            factor, out, 0, a.draft != nullptr};
+  if (tid == 0) path[0] = 0;
+  int j = 1;
+  bool summed = false;  // R is the sum of the rest
+  while (kept < a.max_path) {
+    // the next child of cur from j on
+    const bool lo = lane < n && lane >= j && par[lane] == cur;
+    const bool hi = lane + 32 < n && lane + 32 >= j && par[lane + 32] == cur;
+    const uint64_t kids = uint64_t(__ballot_sync(0xffffffffu, lo)) |
+                          uint64_t(__ballot_sync(0xffffffffu, hi)) << 32;
+    if (kids == 0) break;
+    const int kid = __ffsll(static_cast<long long>(kids)) - 1;
+    bool keep;
+    const float mine = rest.at(pv[kid], qv[kid], tok[kid]);
+    if (rest.drawn) {
+      if (rest.n > 0) {
+        if (!summed) {
+          sum_all(rest);
+          S = R;
+          summed = true;
+        }
+      }
+      const float f = S > 0.0 ? float(1.0 / S) : 0.f;
+      keep = double(us[kid]) * double(qv[kid]) < double(mine) * double(f);
+      if (!keep) {
+        __syncthreads();  // factor[] as it was is read
+        if (tid == 0) factor[rest.n] = f;
+        __syncthreads();
+        ++rest.n;
+        summed = false;
+      }
+    } else {
+      keep = mine > 0.f && double(us[kid]) * S < double(mine);
+      if (!keep) {
+        S -= double(mine);
+        __syncthreads();
+        if (tid == 0) out[out_n] = tok[kid];
+        __syncthreads();
+        rest.n = ++out_n;
+      }
+    }
+    j = kid + 1;
+    if (keep) {
+      cur = kid;
+      if (tid == 0) path[kept] = kid;
+      ++kept;
+      S = 1.0;
+      rest.n = out_n = 0;
+      summed = false;
+      rest.p = a.target + (t0 + cur) * a.target_stride;
+      if (rest.drawn) rest.q = a.draft + (t0 + cur) * a.draft_stride;
+    }
+  }
+  __syncthreads();
+  if (rank == 0) {
+    for (int i = tid; i < a.max_path; i += kVerThreads) row_path[i] = i < kept ? path[i] : -1;
+    if (tid == 0) a.count[r] = kept;
+  }
+
+  // ---- the last token
+  if (!summed) sum_all(rest);
+  if (!(R > 0.0) && rest.n > 0) {  // nothing is left: p itself
+    rest.n = 0;
+    sum_all(rest);
+  }
+  if (!(R > 0.0) || isinf(R)) {
+    if (rank == 0 && tid == 0) a.last[r] = -1;
+    cluster.sync();
+    return;
+  }
+  const double goal = double(a.u_last[r]) * R;
+  // The CTA in whose run the sum passes the goal (the last with anything in it, if
+  // the goal is not below the sum): each sees from its own and the later ones.
+  const double own = *(&total[(passes - 1) & 1]);
+  bool mine = own > 0.0 && before + own > goal;
+  if (mine) {
+    // a CTA before this one may have passed it already
+    mine = !(before > goal);
+  }
+  if (!mine && own > 0.0 && !(before + own > goal)) {
+    // no CTA passes it: the last with anything in it
+    double later = 0.0;
+    for (int c = rank + 1; c < a.cluster; ++c)
+      later += *cluster.map_shared_rank(&total[(passes - 1) & 1], c);
+    mine = !(later > 0.0);
+  }
+  cluster.sync();  // nobody reads the others' shared memory any more
+  if (!mine) return;
+  // the warp's run, then its 16th part, then 32 values at a time
+  auto choose = [&](double& base) {
+    int chosen = -1, some = -1;
+    double at = base, sum = base;
+    for (int w = 0; w < kVerWarps; ++w) {
+      const double t = warp_total[w];
+      if (t > 0.0) {
+        if (chosen < 0 || !(sum > goal)) {
+          some = w;
+          at = sum;
+        }
+        if (chosen < 0 && sum + t > goal) chosen = w;
+      }
+      if (chosen >= 0) break;
+      sum += t;
+    }
+    base = at;
+    return chosen >= 0 ? chosen : some;
+  };
+  double base = before;
+  const int w = choose(base);
+  const int32_t r0 = c0 + int32_t(int64_t(c1 - c0) * w / kVerWarps);
+  const int32_t r1 = c0 + int32_t(int64_t(c1 - c0) * (w + 1) / kVerWarps);
+  const int32_t s0 = r0 + int32_t(int64_t(r1 - r0) * warp / kVerWarps);
+  const int32_t s1 = r0 + int32_t(int64_t(r1 - r0) * (warp + 1) / kVerWarps);
+  __syncthreads();  // warp_total is read
+  const Pair32 part = run_sum(rest, s0, s1);
+  if (lane == 0) warp_total[warp] = part.value();
+  __syncthreads();
+  if (choose(base) != warp) return;
+  const bool two = rest.drawn && rest.n > 0;
+  int32_t found = -1, some = -1;
+  for (int32_t x0 = s0; x0 < s1 && found < 0; x0 += 32) {
+    const int32_t x = x0 + lane;
+    float v = 0.f;
+    if (x < s1) v = rest.at(rest.p[x], two ? rest.q[x] : 0.f, x);
+    double incl = double(v);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const double y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    const uint32_t past = __ballot_sync(0xffffffffu, v > 0.f && base + incl > goal);
+    const uint32_t any = __ballot_sync(0xffffffffu, v > 0.f);
+    if (past)
+      found = x0 + __ffs(past) - 1;
+    else if (any)
+      some = x0 + 31 - __clz(any);
+    base += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  if (lane == 0) a.last[r] = found >= 0 ? found : some;
+}
+
+}  // namespace
+}  // namespace msa
+
+using namespace msa;
+
+extern "C" msa_status msa_tree_verify(const float* target, int64_t target_stride,
+                                      const float* draft, int64_t draft_stride,
+                                      const int32_t* tokens, const int32_t* parents,
+                                      const int32_t* row_offsets, int32_t rows, int64_t T,
+                                      int32_t vocab, const float* u, const float* u_last,
+                                      int32_t max_path, int32_t* path, int32_t* count,
+                                      int32_t* last, msa_stream_t stream) {
+  if (!target || !tokens || !row_offsets || !u || !u_last || !path || !count || !last)
+    return MSA_ERR_INVALID_ARG;
+  if (rows < 1 || rows > kMaxRows || T < 1 || T > kMaxTokens || vocab < 1 ||
+      vocab > (1 << 24) || max_path < 1 || max_path > kTree || target_stride < vocab ||
+      (draft && draft_stride < vocab))
+    return MSA_ERR_INVALID_ARG;
+  if (!paged_aligned4(target) || !paged_aligned4(draft) || !paged_aligned4(tokens) ||
+      !paged_aligned4(parents) || !paged_aligned4(row_offsets) || !paged_aligned4(u) ||
+      !paged_aligned4(u_last) || !paged_aligned4(path) || !paged_aligned4(count) ||
+      !paged_aligned4(last))
+    return MSA_ERR_ALIGNMENT;
+  const msa_status st = check_device();
+  if (st != MSA_OK) return st;
+  VerifyArgs a{};
+  a.target = target;
+  a.draft = draft;
+  a.target_stride = target_stride;
+  a.draft_stride = draft_stride;
+  a.tokens = tokens;
+  a.parents = parents;
+  a.offs = row_offsets;
+  a.u = u;
+  a.u_last = u_last;
+  a.path = path;
+  a.count = count;
+  a.last = last;
+  a.T = T;
+  a.vocab = vocab;
+  a.max_path = max_path;
+  // as many CTAs a row as are on the chip at once (3 an SM), none with less than
+  // a pass of its loads to do
+  int cluster = 1;
+  while (cluster < kVerCluster && int64_t(rows) * cluster * 2 <= int64_t(device_sm_count()) * 3 &&
+         vocab >= cluster * 2 * kVerThreads * 4)
+    cluster *= 2;
+  a.cluster = cluster;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  launch_begin("tree_verify", s);
+  const cudaError_t e = launch_cluster(k_tree_verify, dim3(unsigned(rows) * cluster),
+                                       dim3(kVerThreads), 0, unsigned(cluster), s, a);
+  launch_end("tree_verify", s);
+  return e == cudaSuccess ? MSA_OK : MSA_ERR_CUDA;
+}

@@ -67,9 +67,12 @@ typedef enum msa_status {
   MSA_ERR_RANGE = 10,       /* device warning: the last backward's 16-bit dQ
                                pool overflowed (dQ holds inf / nan); rerun it
                                with MSA_DQ_ACCUM_BF16 or MSA_DQ_ACCUM_F32      */
-  MSA_ERR_BAD_PAGE = 11     /* device: a page-table entry that is needed lies
+  MSA_ERR_BAD_PAGE = 11,    /* device: a page-table entry that is needed lies
                                outside the pool, or a position or a length
                                outside its row of the page table              */
+  MSA_ERR_BAD_TREE = 12     /* device: a row of more than 64 drafted tokens, a
+                               parent that does not come before its token, or
+                               a path that does not ascend                    */
 } msa_status;
 
 /* Human-readable name of a status code (static string). */
@@ -368,12 +371,13 @@ msa_status msa_select_blocks(const void* iq, const void* ik, int64_t T, int32_t 
  * it begins at position 0 and has the shape that these calls take (64 query and
  * 4 key heads of 128 channels, bf16), the rotated queries and keys that append
  * hands back go through msa_select_blocks, msa_build_plan and msa_forward.
- * There is no call that selects or attends for all tokens of a prompt behind a
- * cached prefix at once.  Each such token can be a row of its own in select and
+ * There is no call that selects for all tokens of a prompt behind a cached
+ * prefix at once.  Each such token can be a row of its own in select and
  * decode, with the same pages and its own length, once all of them have been
  * appended and indexed; the prefix is then read once for each token.  select
  * is right for such rows with force_local alone: the mean of a token's own
- * block already holds the keys behind it.
+ * block already holds the keys behind it.  Over every key, up to 64 of them
+ * are one row of msa_paged_tree (below), which reads the prefix once.
  *
  * Rows and pages.  Token j of row r lives in page page_table[r][j / S], slot
  * j % S, S the page size.  A row's table entries past its tokens are never
@@ -547,6 +551,179 @@ msa_status msa_paged_decode(const msa_paged_cache* cache, const msa_page_table* 
                             const int32_t* kv_len, const void* q, int32_t q_heads,
                             float softmax_scale, const int32_t* q2k, void* o, float* lse,
                             void* workspace, size_t workspace_bytes, msa_stream_t stream);
+
+/*
+ * Norm and rotation of queries and keys, head by head: what stands between the
+ * projections and the attention, in training (msa_forward) and in serving
+ * (msa_paged_append without inv_freq, msa_paged_tree, msa_paged_decode).
+ *   n = 1 / sqrt(mean(x^2) + eps) over a head's channels, y = x n w,
+ * then pair i of a token at position p turns by p * inv_freq[i] as in
+ * msa_paged_append; channels from rotary_dim on are not turned.
+ *   q, k   [T][q_heads / k_heads][head_dim] of `dtype`, tokens q_stride /
+ *          k_stride elements apart (multiples of 8, a token's heads contiguous:
+ *          slices of one projection will do); head_dim 64 or 128, heads 1 .. 1024
+ *   q_weight, k_weight  [head_dim] of weight_dtype, an msa_dtype or MSA_F32
+ *   positions int32 [T] device, any values; NULL without inv_freq
+ *   inv_freq  fp32 [rotary_dim / 2], or NULL for no rotation (rotary_dim is then
+ *          ignored); rotary_dim a multiple of 16, at most head_dim
+ *   interleaved as for msa_paged_append
+ *   q_out, k_out  contiguous; may be q or k itself where that is contiguous
+ * Sums, norms and rotation are 32 bits, angles 64, and each result is rounded
+ * once.  eps >= 0, finite; 1 <= T <= 2^20.
+ *
+ * The backward takes the gradients dq_out, dk_out (contiguous) of the results,
+ * with q and k as the forward got them, and returns
+ *   g = dy turned back, dx = n (g w - u mean(g w u)), dw = sum over tokens and
+ *   heads of g u,  u = x n,
+ * dq, dk contiguous of `dtype`, dq_weight and dk_weight fp32 [head_dim].  dq, dk
+ * must not overlap the inputs.  The same call on the same device gives the same
+ * bits.  workspace: device, 16-byte aligned, >= msa_norm_rope_workspace_bytes,
+ * one for calls that may overlap in time.
+ * Errors: MSA_ERR_INVALID_ARG, MSA_ERR_ALIGNMENT (tensors 16 bytes, weights,
+ * positions and inv_freq their element), MSA_ERR_WORKSPACE, MSA_ERR_CUDA.
+ */
+#define MSA_F32 2 /* weight_dtype alone */
+typedef struct msa_norm_rope_args {
+  const void* q;
+  const void* k;
+  int64_t q_stride;
+  int64_t k_stride;
+  const void* q_weight;
+  const void* k_weight;
+  const int32_t* positions;
+  const float* inv_freq;
+  int64_t T;
+  int32_t q_heads;
+  int32_t k_heads;
+  int32_t head_dim;
+  int32_t rotary_dim;
+  int32_t interleaved;
+  int32_t dtype;        /* an msa_dtype */
+  int32_t weight_dtype;
+  float eps;
+} msa_norm_rope_args;
+msa_status msa_norm_rope(const msa_norm_rope_args* args, void* q_out, void* k_out,
+                         msa_stream_t stream);
+msa_status msa_norm_rope_workspace_bytes(int32_t head_dim, size_t* bytes);
+msa_status msa_norm_rope_backward(const msa_norm_rope_args* args, const void* dq_out,
+                                  const void* dk_out, void* dq, void* dk, float* dq_weight,
+                                  float* dk_weight, void* workspace, size_t workspace_bytes,
+                                  msa_stream_t stream);
+
+/*
+ * Drafted tokens
+ * --------------
+ * Several new tokens of a row in one step.  Row r's tokens row_offsets[r] ..
+ * row_offsets[r+1]-1 (at most 64; T in all, what lies behind row_offsets[rows]
+ * is padding) form a tree: token j continues token parents[j] of its row, a
+ * number below j, or what is cached (-1).  The row's token j lies in the cache
+ * behind the kv_len[r] tokens that are there to stay, at slot kv_len[r] + j;
+ * its position in the text is kv_len[r] plus its depth.  A step is
+ *
+ *   msa_norm_rope     (or a rotation of the caller's) with those positions
+ *   msa_paged_append  without inv_freq, start_pos = kv_len: keys and values
+ *   msa_paged_select  a row for each token, with kv_len its row's: the blocks
+ *                     of the cached tokens that it attends (q2k)
+ *   msa_paged_tree    attention
+ *   msa_tree_verify   which tokens stay, and the token behind them
+ *   msa_paged_compact moves those together; kv_len grows by their number
+ *   msa_paged_index   index keys of the tokens that stay
+ *
+ * With parents NULL every token continues the one before it: a chain of drafts,
+ * or up to 64 tokens of a prompt behind a cached prefix.
+ *
+ * msa_paged_tree: attention of such tokens.  Token t of row r sees the cached
+ * keys 0 .. kv_len[r]-1 (with q2k those in blocks of its own q2k[g][t][:]), and
+ * of the drafted ones itself, its parent, its parent's parent and so on.
+ *   q       [T][q_heads][head_dim] contiguous, of the cache's type;
+ *           q_heads = kv_heads * n, 1 <= n <= 16; query head h reads key head
+ *           h / n
+ *   row_offsets int32 [rows + 1], kv_len int32 [rows], parents int32 [T] or
+ *           NULL, all device; rows * kv_heads * width * page_size of the table,
+ *           times ceil(n / 4), <= 2^36
+ *   q2k     int32 [kv_heads][T][16] device, or NULL: every cached key.  -1 = an
+ *           unused slot; other values outside [0, blocks of the kv_len[r] cached
+ *           tokens) set MSA_ERR_BAD_Q2K and are left out
+ *   o       [T][q_heads][head_dim] contiguous, of the cache's type
+ *   lse     fp32 [T][q_heads] natural log
+ *   workspace  device, 16-byte aligned, >= msa_paged_tree_workspace_bytes for
+ *           these rows, T and q_heads;
+ *           needs no initialisation; one for each of the calls that may overlap
+ *           in time
+ * Weights are rounded to the cache's type before the product with the values
+ * (the sum under them is not); all else is 32 bits.  Results are the same from
+ * call to call on one device.
+ * Nothing is written for padding.  A row of more than 64 tokens
+ * (MSA_ERR_BAD_TREE) and a row whose kv_len plus tokens do not fit its part of
+ * the table (MSA_ERR_BAD_PAGE) get O = 0, LSE = -inf.  A bad parent is taken as
+ * -1 (MSA_ERR_BAD_TREE).  Offsets as for msa_paged_append; a row whose offsets
+ * are negative, decrease or pass T has no tokens (MSA_ERR_BAD_OFFSETS).  Keys in
+ * a bad page are left out (MSA_ERR_BAD_PAGE); a token all of whose keys are gets
+ * O = 0, LSE = -inf.  1 <= T <= 2^20.
+ */
+msa_status msa_paged_tree_workspace_bytes(const msa_paged_cache* cache, int32_t rows, int64_t T,
+                                          int32_t q_heads, size_t* bytes);
+msa_status msa_paged_tree(const msa_paged_cache* cache, const msa_page_table* table,
+                          const int32_t* row_offsets, const int32_t* kv_len,
+                          const int32_t* parents, int64_t T, const void* q, int32_t q_heads,
+                          float softmax_scale, const int32_t* q2k, void* o, float* lse,
+                          void* workspace, size_t workspace_bytes, msa_stream_t stream);
+
+/*
+ * Verification of drafted tokens against the target's probabilities.  A row's
+ * token 0 stands already; the walk begins there.  At token c it tries the tokens
+ * whose parent is c, in order of their number, and goes on from the first that it
+ * keeps.  With x = tokens[j], p = target[c], q = draft[c], S = 1 and r = p at first:
+ *   with draft     keep j if u[j] q(x) < r(x) f, f = fp32(1 / S); else
+ *                  r = max(r f - q, 0) for every token, S = sum of r
+ *   without        (drafts that were not drawn) keep j if r(x) > 0 and
+ *                  u[j] S < r(x); else S = S - r(x), r(x) = 0
+ * Where none is kept (there may be no child), the row's last token is drawn: the
+ * first x of r(0) + .. + r(x) > u_last[row] * (the sum of r).  r all zero: p itself
+ * is taken for it.  With u uniform on [0, 1) and drafts drawn from q independently
+ * of one another the row's tokens are distributed as the target's.  r is 32 bits,
+ * rounded after each operation; sums are 64 bits (up to 2^-40 of the sum), and so
+ * are the comparisons.
+ *   target  fp32 [T][vocab] device, rows target_stride elements apart: row t the
+ *           distribution behind token t, not negative, sum 1; any alignment of 4
+ *   draft   the same for the drafting model, draft_stride; or NULL
+ *   tokens  int32 [T], u fp32 [T] (entries of tokens 0 are not read)
+ *   parents int32 [T] or NULL (a chain), u_last fp32 [rows]
+ *   path    int32 [rows][max_path]: the numbers, within the row, of token 0 and the
+ *           kept ones, ascending, then -1.  1 <= max_path <= 64; a walk ends at
+ *           max_path tokens
+ *   count   int32 [rows]: how many they are
+ *   last    int32 [rows]: the token behind them; -1 if p has no positive value or
+ *           its sum is not finite
+ * A token whose parent does not come before it, or that is not in [0, vocab), is
+ * not tried.  A row without tokens, of more than 64, or with offsets that decrease
+ * or lie outside [0, T] gets count 0, path -1, last -1.
+ * 1 <= rows <= 65536, 1 <= T <= 2^20, 1 <= vocab <= 2^24.
+ * Asynchronous, no workspace, the same answer from call to call.  Errors:
+ * MSA_ERR_INVALID_ARG, MSA_ERR_ALIGNMENT, MSA_ERR_CUDA.
+ */
+msa_status msa_tree_verify(const float* target, int64_t target_stride, const float* draft,
+                           int64_t draft_stride, const int32_t* tokens, const int32_t* parents,
+                           const int32_t* row_offsets, int32_t rows, int64_t T, int32_t vocab,
+                           const float* u, const float* u_last, int32_t max_path, int32_t* path,
+                           int32_t* count, int32_t* last, msa_stream_t stream);
+
+/*
+ * Moves the kept tokens of each row together: keys and values at slot kv_len[r] +
+ * path[r][i] go to slot kv_len[r] + i, for i = 0 .. count[r]-1, within the row's
+ * pages; nothing else in the cache changes.
+ *   path    int32 [rows][path_width] device, rows contiguous, 1 <= path_width <= 64;
+ *           path[r][0 .. count[r]-1] ascend strictly from 0 or more
+ *   count   int32 [rows] device
+ *   new_len int32 [rows] device (written, not kv_len itself): kv_len[r] + count[r]
+ * A row whose count is not in [0, path_width] or whose path does not ascend
+ * (MSA_ERR_BAD_TREE), or one of whose tokens has a bad place (MSA_ERR_BAD_PAGE),
+ * is left as it is, new_len = kv_len.  No token that moves may lie in a page of
+ * another row.
+ */
+msa_status msa_paged_compact(const msa_paged_cache* cache, const msa_page_table* table,
+                             const int32_t* kv_len, const int32_t* path, int32_t path_width,
+                             const int32_t* count, int32_t* new_len, msa_stream_t stream);
 
 /*
  * Kernel timing for benchmarks.  While enabled, every kernel the library
