@@ -329,12 +329,8 @@ __device__ __forceinline__ void cp_async16_zero(uint32_t dst, const void* src, b
                "r"(real ? 16 : 0)
                : "memory");
 }
-__device__ __forceinline__ void cp_async_commit() {
-  asm volatile("cp.async.commit_group;" ::: "memory");
-}
-template <int kN>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(kN) : "memory");
+__device__ __forceinline__ void cp_async_wait_all() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 // First key of an item's tile and the end of its keys.
@@ -354,47 +350,27 @@ __device__ __forceinline__ TileKeys tile_keys(const TreeArgs& a, const TreeWalk&
   return TileKeys{f, min(f + kBlock, s.w.len), false, a.who[base + i]};
 }
 
-// The copying warps' side: fills query, key and value tiles and tells of each
-// when its copies have landed, two groups of copies later.
+// The copying warps' side: fills query, key and value tiles; each copy's landing
+// counts on the tile's barrier (the thread that issues the products orders what it
+// has waited for before them).
 template <typename T, int kDim>
 struct Copier {
   using S = TreeShape<kDim>;
   static constexpr int kChunks = kDim / 8;
   static constexpr int kAtOnce = 32 / kChunks;  // rows that one copy instruction covers
   const TreeArgs& a;
-  TreeBars& bars;
-  uint32_t sbase;
-  volatile int* abort_flag;
   int warp, lane;                 // of the copying warps
-  uint32_t pend[2];               // barriers of groups not told of yet, oldest first
-  int n_pend;
 
-  __device__ __forceinline__ void tell(uint32_t bar) {
-    fence_proxy_async_smem();
-    mbar_arrive(bar);
-  }
-  __device__ __forceinline__ void commit(uint32_t bar) {
-    cp_async_commit();
-    if (n_pend == 2) {
-      cp_async_wait<2>();
-      tell(pend[0]);
-      pend[0] = pend[1];
-      pend[1] = bar;
-    } else {
-      pend[n_pend++] = bar;
-    }
-  }
-  __device__ __forceinline__ void flush() {
-    cp_async_wait<0>();
-    for (int i = 0; i < n_pend; ++i) tell(pend[i]);
-    n_pend = 0;
+  // The barrier counts this thread once, when all its copies so far have landed.
+  static __device__ __forceinline__ void tell(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
   }
   static __device__ __forceinline__ uint32_t at(int row, int chunk) {
     return (chunk >> 3) * 16384u + row * 128u + (((chunk & 7) ^ (row & 7)) << 4);
   }
   // 128 rows of queries from matrix row r0 of the item's row on.
   __device__ __forceinline__ void queries(const TreeWalk& s, int32_t r0, int32_t rows,
-                                          uint32_t tile) {
+                                          uint32_t tile) const {
     const int sub = lane / kChunks, c = lane % kChunks;
     const int64_t width = int64_t(a.kv_heads) * a.group * kDim;
     const T* q = static_cast<const T*>(a.q) + s.w.t0 * width + int64_t(s.g) * a.group * kDim +
@@ -410,19 +386,22 @@ struct Copier {
                       real);
     }
   }
-  // The pages of the warp's 32 keys of a tile, a lane each (-1: no such key).
+  // The pages of the warp's 32 keys of a tile, a lane each, as the table has them
+  // (kNoKey: no such key).
+  static constexpr int32_t kNoKey = INT32_MIN;
   __device__ __forceinline__ int32_t pages(const TreeWalk& s, const TileKeys& t) const {
     const int32_t j = t.first + warp * 32 + lane;
-    if (j >= t.end) return -1;
-    const int32_t p = a.table.pages[int64_t(s.row) * a.table.stride + (j >> a.table.shift)];
-    if (p < 0 || p >= a.table.num_pages) {
-      raise_paged(a.table.status, MSA_ERR_BAD_PAGE);
-      return -1;
-    }
-    return p;
+    if (j >= t.end) return kNoKey;
+    return max(a.table.pages[int64_t(s.row) * a.table.stride + (j >> a.table.shift)], -1);
+  }
+  // Such a page, or -1: there is no key.
+  __device__ __forceinline__ int32_t checked(int32_t p) const {
+    if (p >= 0 && p < a.table.num_pages) return p;
+    if (p != kNoKey) raise_paged(a.table.status, MSA_ERR_BAD_PAGE);
+    return -1;
   }
   __device__ __forceinline__ void keys(const PagedPool& pool, const TreeWalk& s,
-                                       const TileKeys& t, int32_t page, uint32_t tile) {
+                                       const TileKeys& t, int32_t page, uint32_t tile) const {
     const int sub = lane / kChunks, c = lane % kChunks;
     const T* base = static_cast<const T*>(pool.base) + s.g * pool.head + c * 8;
     const int32_t mask = (1 << a.table.shift) - 1;
@@ -596,6 +575,7 @@ __device__ __forceinline__ void tree_mma_role(const TreeArgs& a, TreeBars& bars,
       if (!wait(bars.p_full[x], nx[x])) return false;
       if (!wait(bars.v_full[stg], t / kVStages)) return false;
       if (!used[0] && !used[1] && segs > 0 && !wait(bars.o_free, segs - 1)) return false;
+      fence_proxy_async_smem();
       tc_fence_after();
       const uint64_t bv = dv + stg * kStage;
 #pragma unroll
@@ -613,6 +593,7 @@ __device__ __forceinline__ void tree_mma_role(const TreeArgs& a, TreeBars& bars,
       const uint32_t t = nt + i, stg = t % kKStages;
       if ((split || x == 0) && !wait(bars.k_full[stg], t / kKStages)) { ok = false; break; }
       if (k == 0 && !wait(bars.q_full, segs)) { ok = false; break; }
+      fence_proxy_async_smem();
       tc_fence_after();
       const uint64_t bq = dq + (split ? 0 : x) * kStage, bk = dk + stg * kStage;
 #pragma unroll
@@ -654,7 +635,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     init(bars.q_full, kCopyWarps * 32);
     init(bars.q_empty, 1);
     for (int i = 0; i < kKStages; ++i) {
-      init(bars.k_full[i], kCopyWarps * 32);
+      init(bars.k_full[i], kCopyWarps * 33);
       init(bars.k_empty[i], 1);
     }
     for (int i = 0; i < kVStages; ++i) {
@@ -707,9 +688,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     if (warp >= kSoftWarps && warp < kSoftWarps + kCopyWarps) {
       // ---------------- copies
       fewer_registers<kOtherRegs>();
-      Copier<T, kDim> copy{a, bars, sbase, abort_flag, warp - kSoftWarps, lane, {0, 0}, 0};
+      const Copier<T, kDim> copy{a, warp - kSoftWarps, lane};
       uint32_t nt = 0, segs = 0;
       bool ok = true;
+      auto wait = [&](uint64_t& bar, uint32_t ph) {
+        return mbar_wait_warp(smem_u32(&bar), ph & 1, abort_flag);
+      };
       do {
         const int32_t rows = walk.rows_here();
         const int64_t base =
@@ -717,46 +701,41 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         TileKeys t = tile_keys(a, walk, base, walk.i0);
         int32_t page = copy.pages(walk, t);
         for (int32_t i = walk.i0; ok && i < walk.i1; ++i, ++nt) {
-          const uint32_t ks = nt % kKStages, vs = nt % kVStages;
-          if (nt >= kKStages &&
-              !mbar_wait_warp(smem_u32(&bars.k_empty[ks]), (nt / kKStages - 1) & 1, abort_flag)) {
-            ok = false;
-            break;
+          // the pages of the next tile, while this one's copies are started
+          TileKeys t1 = t;
+          int32_t page1 = -1;
+          if (i + 1 < walk.i1) {
+            t1 = tile_keys(a, walk, base, i + 1);
+            page1 = copy.pages(walk, t1);
           }
+          const uint32_t ks = nt % kKStages, vs = nt % kVStages;
+          if (nt >= kKStages && !wait(bars.k_empty[ks], nt / kKStages - 1)) { ok = false; break; }
+          page = copy.checked(page);
           const uint32_t seen = __ballot_sync(0xffffffffu, page >= 0);
-          if (lane == 0) sh.there[nt & 3][warp - kSoftWarps] = seen;
           copy.keys(a.k, walk, t, page, sbase + S::kK + ks * S::kTile);
-          copy.commit(smem_u32(&bars.k_full[ks]));
+          copy.tell(smem_u32(&bars.k_full[ks]));
+          if (lane == 0) {
+            sh.there[nt & 3][warp - kSoftWarps] = seen;
+            mbar_arrive(smem_u32(&bars.k_full[ks]));
+          }
           if (i == walk.i0) {
             // the queries, once all products with the ones before them are done
-            if (segs > 0) {
-              copy.flush();
-              if (!mbar_wait_warp(smem_u32(&bars.q_empty), (segs - 1) & 1, abort_flag)) {
-                ok = false;
-                break;
-              }
-            }
+            if (segs > 0 && !wait(bars.q_empty, segs - 1)) { ok = false; break; }
             const int32_t r0 = walk.layer * kPairRows;
             copy.queries(walk, r0, min(rows, kTileRows), sbase + S::kQ);
             if (rows > kTileRows)
               copy.queries(walk, r0 + kTileRows, rows - kTileRows, sbase + S::kQ + S::kTile);
-            copy.commit(smem_u32(&bars.q_full));
+            copy.tell(smem_u32(&bars.q_full));
           }
-          if (nt >= kVStages &&
-              !mbar_wait_warp(smem_u32(&bars.v_empty[vs]), (nt / kVStages - 1) & 1, abort_flag)) {
-            ok = false;
-            break;
-          }
+          if (nt >= kVStages && !wait(bars.v_empty[vs], nt / kVStages - 1)) { ok = false; break; }
           copy.keys(a.v, walk, t, page, sbase + S::kV + vs * S::kTile);
-          copy.commit(smem_u32(&bars.v_full[vs]));
-          if (i + 1 < walk.i1) {
-            t = tile_keys(a, walk, base, i + 1);
-            page = copy.pages(walk, t);
-          }
+          copy.tell(smem_u32(&bars.v_full[vs]));
+          t = t1;
+          page = page1;
         }
         ++segs;
       } while (ok && walk.next());
-      copy.flush();
+      cp_async_wait_all();
     } else if (warp >= kSoftWarps + kCopyWarps) {
       // ---------------- tensor cores
       fewer_registers<kOtherRegs>();
