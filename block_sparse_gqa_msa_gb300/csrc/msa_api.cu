@@ -168,6 +168,25 @@ CUresult make_map_kv(CUtensorMap* m, const void* base, int64_t T) {
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
+// A pool of keys or values in pages (16-bit values, strides in elements); box =
+// `rows` tokens of one head of one page x 64 channels.
+CUresult make_map_pages(CUtensorMap* m, const void* base, bool bf16, int32_t dim, int32_t heads,
+                        int32_t page_size, int64_t pages, int64_t head_stride,
+                        int64_t token_stride, int64_t page_stride, int32_t rows) {
+  auto fn = encode_fn();
+  if (!fn) return CUDA_ERROR_NOT_FOUND;
+  cuuint64_t gd[4] = {cuuint64_t(dim), cuuint64_t(heads), cuuint64_t(page_size),
+                      cuuint64_t(pages)};
+  cuuint64_t gs[3] = {cuuint64_t(head_stride) * 2, cuuint64_t(token_stride) * 2,
+                      cuuint64_t(page_stride) * 2};
+  cuuint32_t box[4] = {64, 1, cuuint32_t(rows), 1};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+            const_cast<void*>(base), gd, gs, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+
 // [rows, 128] fp32 pool (forward O accumulation) as the destination of bulk
 // tensor reductions; box = 16 rows x 32 columns (128 bytes), 128-byte swizzle,
 // so a tile row staged by one thread is spread over all shared-memory banks.

@@ -33,10 +33,13 @@
 // once.  An item within one run is finished there; otherwise each run leaves its
 // (m, l, O) in the workspace and k_paged_tree_join adds them up, in order.
 //
-// Keys come by asynchronous copies of 16 bytes into the swizzled layout that the
-// tensor cores read, three tiles of keys and two of values ahead; they take
-// pages of any size and any strides, and write zeros for keys that are not
-// there.
+// Three warps fetch keys and values, three tiles of keys and two of values ahead,
+// into the swizzled layout that the tensor cores read, in groups of 32 keys of a
+// tile.  Where all 32 of a group are there and lie in pages of 8 tokens or more, by tensor
+// copies of up to 32 tokens of a page; else by copies of 16 bytes, which take pages
+// of any size and write zeros for keys that are not there (what lies behind a
+// row's end may be anything, and 0 times it must be 0).  The latter alone, 128
+// instructions a tile, kept the tensor cores waiting two thirds of the time.
 //
 // With q2k a first kernel (k_paged_tree_lists) makes, for each item, the list of
 // the blocks that any of its tokens chose, and which tokens did.
@@ -52,11 +55,13 @@ constexpr int kNodes = 64;         // drafted tokens of a row
 constexpr int kPairRows = 256;     // matrix rows of an item
 constexpr int kTileRows = 128;
 constexpr int kMaxRuns = 160;      // CTAs: no GB300 has more SMs
-constexpr int kSoftWarps = 8, kCopyWarps = 4;
-constexpr int kTreeThreads = 512;  // and a warp that issues products, three that wait
-// Registers of a thread: 128 at launch, 512 threads; the softmax warps take over what
-// the others give up: 256 x 192 + 256 x 64 = 512 x 128.
-constexpr int kSoftRegs = 192, kOtherRegs = 64;
+// Three copying warps for four groups of 32 keys: with a fourth, 13 warps, a
+// thread would have 128 registers, and the softmax's would not do.
+constexpr int kSoftWarps = 8, kCopyWarps = 3, kGroups = 4;
+constexpr int kTreeThreads = (kSoftWarps + kCopyWarps + 1) * 32;
+// Warp 0 issues the products and the copying warps follow: a scheduler that has the
+// choice takes the lowest warp, and these have little to do but are waited for.
+constexpr int kCopyWarp0 = 1, kSoftWarp0 = 1 + kCopyWarps;
 constexpr int kKStages = 3, kVStages = 2;
 constexpr float kRise = 8.f;       // and kLift: as in paged_decode.cu
 template <typename T>
@@ -82,6 +87,7 @@ struct TreeArgs {
   uint64_t* who;        // q2k: the tokens that chose them
   float* part_ml;       // [2 runs][256][2]: m, l
   float* part_o;        // [2 runs][256][dim]
+  int32_t box;          // tokens of a tensor copy, 0: none are used
 };
 
 template <int kDim>
@@ -313,7 +319,7 @@ struct TreeBars {
 };
 struct TreeShared {
   TreeBars bars;
-  uint32_t there[4][kCopyWarps];  // keys of a tile that are there; a ring of 4 tiles
+  uint32_t there[4][kGroups];  // keys of a tile that are there; a ring of 4 tiles
   float2 states[2][kTileRows];    // (m, l) of the slots, where they are joined
   uint32_t tmem_base;
   int abort;
@@ -358,6 +364,7 @@ struct Copier {
   using S = TreeShape<kDim>;
   static constexpr int kChunks = kDim / 8;
   static constexpr int kAtOnce = 32 / kChunks;  // rows that one copy instruction covers
+  static constexpr int kMine = (kGroups + kCopyWarps - 1) / kCopyWarps;  // groups of a warp
   const TreeArgs& a;
   int warp, lane;                 // of the copying warps
 
@@ -376,8 +383,8 @@ struct Copier {
     const T* q = static_cast<const T*>(a.q) + s.w.t0 * width + int64_t(s.g) * a.group * kDim +
                  c * 8;
 #pragma unroll 4
-    for (int x = 0; x < 32 / kAtOnce; ++x) {
-      const int r = warp * 32 + x * kAtOnce + sub;
+    for (int x = warp; x < kTileRows / kAtOnce; x += kCopyWarps) {
+      const int r = x * kAtOnce + sub;
       const int32_t m = r0 + r, node = m / a.group;
       const bool real = r < rows;
       cp_async16_zero(tile + at(r, c),
@@ -386,12 +393,12 @@ struct Copier {
                       real);
     }
   }
-  // The pages of the warp's 32 keys of a tile, a lane each, as the table has them
+  // The pages of the keys of a tile's group, a lane each, as the table has them
   // (kNoKey: no such key).
   static constexpr int32_t kNoKey = INT32_MIN;
-  __device__ __forceinline__ int32_t pages(const TreeWalk& s, const TileKeys& t) const {
-    const int32_t j = t.first + warp * 32 + lane;
-    if (j >= t.end) return kNoKey;
+  __device__ __forceinline__ int32_t pages(const TreeWalk& s, const TileKeys& t, int grp) const {
+    const int32_t j = t.first + grp * 32 + lane;
+    if (grp >= kGroups || j >= t.end) return kNoKey;
     return max(a.table.pages[int64_t(s.row) * a.table.stride + (j >> a.table.shift)], -1);
   }
   // Such a page, or -1: there is no key.
@@ -400,31 +407,39 @@ struct Copier {
     if (p != kNoKey) raise_paged(a.table.status, MSA_ERR_BAD_PAGE);
     return -1;
   }
-  __device__ __forceinline__ void keys(const PagedPool& pool, const TreeWalk& s,
-                                       const TileKeys& t, int32_t page, uint32_t tile) const {
+  // Starts the copies of a group of 32 keys (or values) into a tile; its barrier
+  // counts 33 times for the group.
+  __device__ __forceinline__ void keys(const PagedPool& pool, const CUtensorMap* map,
+                                       const TreeWalk& s, const TileKeys& t, int grp,
+                                       int32_t page, uint32_t tile, uint32_t bar) const {
+    const int32_t mask = (1 << a.table.shift) - 1, j0 = t.first + grp * 32;
+    if (a.box > 0 && (j0 & (a.box - 1)) == 0 && __all_sync(0xffffffffu, page >= 0)) {
+      constexpr int kHalves = kDim / 64;
+      const int b = lane / kHalves * a.box, half = lane % kHalves;  // the lane's box
+      const int32_t p = __shfl_sync(0xffffffffu, page, b & 31);
+      if (lane == 0) mbar_arrive_expect_tx(bar, 32 * kDim * 2);
+      __syncwarp();
+      if (b < 32)
+        tma_load_4d(tile + half * 16384u + (grp * 32 + b) * 128u, map, bar, half * 64, s.g,
+                    (j0 + b) & mask, p);
+      mbar_arrive(bar);
+      return;
+    }
     const int sub = lane / kChunks, c = lane % kChunks;
     const T* base = static_cast<const T*>(pool.base) + s.g * pool.head + c * 8;
-    const int32_t mask = (1 << a.table.shift) - 1;
 #pragma unroll 4
     for (int x = 0; x < 32 / kAtOnce; ++x) {
       const int key = x * kAtOnce + sub;
       const int32_t p = __shfl_sync(0xffffffffu, page, key);
-      const int32_t slot = (t.first + warp * 32 + key) & mask;
+      const int32_t slot = (j0 + key) & mask;
       const T* src = p >= 0 ? base + p * pool.page + slot * pool.token
                             : static_cast<const T*>(pool.base);
-      cp_async16_zero(tile + at(warp * 32 + key, c), src, p >= 0);
+      cp_async16_zero(tile + at(grp * 32 + key, c), src, p >= 0);
     }
+    tell(bar);
+    if (lane == 0) mbar_arrive(bar);
   }
 };
-
-template <int kRegs>
-__device__ __forceinline__ void more_registers() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
-}
-template <int kRegs>
-__device__ __forceinline__ void fewer_registers() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
-}
 
 // P = 2^(s c2 - mref) of one tile row (tensor memory columns [cs, cs + 128) of
 // the thread's lane) as pairs of T into pk; with kMask the keys whose bit is not
@@ -543,80 +558,126 @@ __device__ __forceinline__ uint64_t path_of(const TreeArgs& a, const TreeRow& w,
   return node < 32 ? p0 : p1;
 }
 
-// The tensor cores' side, one thread.  Step k works for slot k & 1: S of step k,
+// Products and their commits by one lane of a warp that stays together: operands
+// then live in the registers that all lanes share, from which the tensor cores take
+// them.  (With lane 0 alone in a branch an instruction took 80 cycles to issue.)
+__device__ __forceinline__ void mma_ss_one(uint32_t one, uint32_t d, uint64_t a, uint64_t b,
+                                           uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "setp.ne.b32 e, %5, 0;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(one)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts_one(uint32_t one, uint32_t d, uint32_t a, uint64_t b,
+                                           uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "setp.ne.b32 e, %5, 0;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(one)
+      : "memory");
+}
+__device__ __forceinline__ void commit_one(uint32_t one, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "setp.ne.b32 e, %1, 0;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+          bar),
+      "r"(one)
+      : "memory");
+}
+
+// The tensor cores' side, one warp.  Step k works for slot k & 1: S of step k,
 // then P V of step k - 1.
 template <typename T, int kDim>
-__device__ __forceinline__ void tree_mma_role(const TreeArgs& a, TreeBars& bars, TreeWalk walk,
-                                           uint32_t tmem, uint32_t sbase,
-                                           volatile int* abort_flag) {
+__device__ __forceinline__ void tree_mma_role(const TreeArgs& a, TreeBars& bars, TreeWalk& walk,
+                                              uint32_t tmem, uint32_t sbase,
+                                              volatile int* abort_flag) {
   using S = TreeShape<kDim>;
-  constexpr bool kBf = sizeof(T) == 2 && kLift<T> == 0.f;
+  constexpr bool kBf = kLift<T> == 0.f;
   constexpr uint32_t idS = kBf ? idesc_bf16_f32(128, 128, 0, 0) : idesc_f16_f32(128, 128, 0, 0);
   constexpr uint32_t idPV = kBf ? idesc_bf16_f32(128, kDim, 0, 1) : idesc_f16_f32(128, kDim, 0, 1);
+  const uint32_t one = (threadIdx.x & 31) == 0;
   auto wait = [&](uint64_t& bar, uint32_t ph) {
-    return mbar_wait(smem_u32(&bar), ph & 1, abort_flag);
+    return mbar_wait_warp(smem_u32(&bar), ph & 1, abort_flag);
   };
   const uint64_t dq = sdesc_sw128(sbase + S::kQ, 16u, 1024u);
   const uint64_t dk = sdesc_sw128(sbase + S::kK, 16u, 1024u);
   const uint64_t dv = sdesc_sw128(sbase + S::kV, 16384u, 1024u);
   constexpr uint64_t kStage = S::kTile >> 4;
-  uint32_t nt = 0;             // key tiles before the segment
-  uint32_t nx[2] = {0, 0};     // steps of each slot
-  uint32_t segs = 0;
+  uint32_t ks = 0, kph = 0, vs = 0, vph = 0;  // stages and phases of keys and of values
+  uint32_t pph0 = 0, pph1 = 0, segs = 0;
   bool ok = true;
   do {
     const bool split = walk.rows_here() <= kTileRows;
     const int tiles = walk.i1 - walk.i0, steps = split ? tiles : 2 * tiles;
-    bool used[2] = {false, false};
-    // P V of step k
-    auto issue_pv = [&](int k) -> bool {
-      const int x = k & 1, i = split ? k : k >> 1;
-      const uint32_t t = nt + i, stg = t % kVStages;
-      if (!wait(bars.p_full[x], nx[x])) return false;
-      if (!wait(bars.v_full[stg], t / kVStages)) return false;
-      if (!used[0] && !used[1] && segs > 0 && !wait(bars.o_free, segs - 1)) return false;
+    // P V of step k: slot x, the last with its values where `frees`
+    auto issue_pv = [&](int k, int x, bool frees) -> bool {
+      uint32_t& pph = x ? pph1 : pph0;
+      if (!wait(bars.p_full[x], pph)) return false;
+      pph ^= 1;
+      if (!wait(bars.v_full[vs], vph)) return false;
+      if (k == 0 && segs > 0 && !wait(bars.o_free, segs - 1)) return false;
       fence_proxy_async_smem();
       tc_fence_after();
-      const uint64_t bv = dv + stg * kStage;
+      const uint64_t bv = dv + vs * kStage;
+      const uint32_t to = tmem + S::kTmO + kDim * x, p = tmem + 128 * x, more = k > 1;
 #pragma unroll
       for (int kk = 0; kk < 8; ++kk)
-        umma_ts(tmem + S::kTmO + kDim * x, tmem + 128 * x + kk * 8, bv + uint64_t(kk) * 128u, idPV,
-                (used[x] || kk > 0) ? 1u : 0u);
-      used[x] = true;
-      ++nx[x];
-      if (split || x == 1) umma_commit(smem_u32(&bars.v_empty[stg]));
-      if (k + 2 >= steps) umma_commit(smem_u32(&bars.o_full[x]));
+        mma_ts_one(one, to, p + kk * 8, bv + uint64_t(kk) * 128u, idPV, kk > 0 ? 1u : more);
+      if (frees) {
+        commit_one(one, smem_u32(&bars.v_empty[vs]));
+        if (++vs == kVStages) {
+          vs = 0;
+          vph ^= 1;
+        }
+      }
+      if (k + 2 >= steps) commit_one(one, smem_u32(&bars.o_full[x]));
       return true;
     };
-    for (int k = 0; ok && k < steps; ++k) {
-      const int x = k & 1, i = split ? k : k >> 1;
-      const uint32_t t = nt + i, stg = t % kKStages;
-      if ((split || x == 0) && !wait(bars.k_full[stg], t / kKStages)) { ok = false; break; }
-      if (k == 0 && !wait(bars.q_full, segs)) { ok = false; break; }
+    auto issue_s = [&](int k, int x, bool waits, bool frees) -> bool {
+      if (waits && !wait(bars.k_full[ks], kph)) return false;
+      if (k == 0 && !wait(bars.q_full, segs)) return false;
       fence_proxy_async_smem();
       tc_fence_after();
-      const uint64_t bq = dq + (split ? 0 : x) * kStage, bk = dk + stg * kStage;
+      const uint64_t bq = dq + (split ? 0 : x) * kStage, bk = dk + ks * kStage;
+      const uint32_t to = tmem + 128 * x;
 #pragma unroll
       for (int kk = 0; kk < kDim / 16; ++kk) {
         const uint64_t off = uint64_t((kk >> 2) * 1024 + (kk & 3) * 2);
-        umma_ss(tmem + 128 * x, bq + off, bk + off, idS, kk > 0);
+        mma_ss_one(one, to, bq + off, bk + off, idS, kk > 0);
       }
-      umma_commit(smem_u32(&bars.s_full[x]));
-      if (split || x == 1) umma_commit(smem_u32(&bars.k_empty[stg]));
-      if (k + 1 == steps) umma_commit(smem_u32(&bars.q_empty));
-      if (k > 0 && !issue_pv(k - 1)) { ok = false; break; }
+      commit_one(one, smem_u32(&bars.s_full[x]));
+      if (frees) {
+        commit_one(one, smem_u32(&bars.k_empty[ks]));
+        if (++ks == kKStages) {
+          ks = 0;
+          kph ^= 1;
+        }
+      }
+      if (k + 1 == steps) commit_one(one, smem_u32(&bars.q_empty));
+      return true;
+    };
+    for (int k = 0; ok && k < steps; ++k) {
+      const int x = k & 1;
+      ok = issue_s(k, x, split || x == 0, split || x == 1) &&
+           (k == 0 || issue_pv(k - 1, x ^ 1, split || x == 0));
     }
-    if (ok) ok = issue_pv(steps - 1);
-    nt += tiles;
+    ok = ok && issue_pv(steps - 1, (steps - 1) & 1, true);
     ++segs;
   } while (ok && walk.next());
-  umma_commit(smem_u32(&bars.fin));
+  commit_one(one, smem_u32(&bars.fin));
   mbar_wait_drain(smem_u32(&bars.fin), 0);
 }
 
 template <typename T, int kDim>
 __global__ void __launch_bounds__(kTreeThreads, 1)
-    k_paged_tree(const __grid_constant__ TreeArgs a) {
+    k_paged_tree(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap map_k,
+                 const __grid_constant__ CUtensorMap map_v) {
   using S = TreeShape<kDim>;
   extern __shared__ __align__(1024) uint8_t smem[];
   TreeShared& sh = *reinterpret_cast<TreeShared*>(smem + S::kRest);
@@ -635,11 +696,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     init(bars.q_full, kCopyWarps * 32);
     init(bars.q_empty, 1);
     for (int i = 0; i < kKStages; ++i) {
-      init(bars.k_full[i], kCopyWarps * 33);
+      init(bars.k_full[i], kGroups * 33);
       init(bars.k_empty[i], 1);
     }
     for (int i = 0; i < kVStages; ++i) {
-      init(bars.v_full[i], kCopyWarps * 32);
+      init(bars.v_full[i], kGroups * 33);
       init(bars.v_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -652,7 +713,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     init(bars.fin, 1);
     fence_mbar_init();
   }
-  if (warp == kSoftWarps + kCopyWarps) {
+  if (warp == 0) {
     tmem_alloc(smem_u32(&sh.tmem_base), 512);
     tmem_relinquish();
   }
@@ -685,10 +746,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   }
   __syncthreads();  // the prefix is read
   if (run < runs) {
-    if (warp >= kSoftWarps && warp < kSoftWarps + kCopyWarps) {
+    if (warp >= kCopyWarp0 && warp < kSoftWarp0) {
       // ---------------- copies
-      fewer_registers<kOtherRegs>();
-      const Copier<T, kDim> copy{a, warp - kSoftWarps, lane};
+      const Copier<T, kDim> copy{a, warp - kCopyWarp0, lane};
       uint32_t nt = 0, segs = 0;
       bool ok = true;
       auto wait = [&](uint64_t& bar, uint32_t ph) {
@@ -698,25 +758,32 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         const int32_t rows = walk.rows_here();
         const int64_t base =
             a.q2k ? list_base(a, walk.row, walk.layer, walk.g, walk.w.t0) : 0;
+        constexpr int kMine = Copier<T, kDim>::kMine;
         TileKeys t = tile_keys(a, walk, base, walk.i0);
-        int32_t page = copy.pages(walk, t);
+        int32_t page[kMine];
+#pragma unroll
+        for (int m = 0; m < kMine; ++m) page[m] = copy.pages(walk, t, copy.warp + m * kCopyWarps);
         for (int32_t i = walk.i0; ok && i < walk.i1; ++i, ++nt) {
           // the pages of the next tile, while this one's copies are started
           TileKeys t1 = t;
-          int32_t page1 = -1;
+          int32_t page1[kMine] = {};
           if (i + 1 < walk.i1) {
             t1 = tile_keys(a, walk, base, i + 1);
-            page1 = copy.pages(walk, t1);
+#pragma unroll
+            for (int m = 0; m < kMine; ++m)
+              page1[m] = copy.pages(walk, t1, copy.warp + m * kCopyWarps);
           }
           const uint32_t ks = nt % kKStages, vs = nt % kVStages;
           if (nt >= kKStages && !wait(bars.k_empty[ks], nt / kKStages - 1)) { ok = false; break; }
-          page = copy.checked(page);
-          const uint32_t seen = __ballot_sync(0xffffffffu, page >= 0);
-          copy.keys(a.k, walk, t, page, sbase + S::kK + ks * S::kTile);
-          copy.tell(smem_u32(&bars.k_full[ks]));
-          if (lane == 0) {
-            sh.there[nt & 3][warp - kSoftWarps] = seen;
-            mbar_arrive(smem_u32(&bars.k_full[ks]));
+#pragma unroll
+          for (int m = 0; m < kMine; ++m) {
+            const int grp = copy.warp + m * kCopyWarps;
+            if (grp >= kGroups) break;
+            page[m] = copy.checked(page[m]);
+            const uint32_t seen = __ballot_sync(0xffffffffu, page[m] >= 0);
+            if (lane == 0) sh.there[nt & 3][grp] = seen;
+            copy.keys(a.k, &map_k, walk, t, grp, page[m], sbase + S::kK + ks * S::kTile,
+                      smem_u32(&bars.k_full[ks]));
           }
           if (i == walk.i0) {
             // the queries, once all products with the ones before them are done
@@ -728,23 +795,31 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             copy.tell(smem_u32(&bars.q_full));
           }
           if (nt >= kVStages && !wait(bars.v_empty[vs], nt / kVStages - 1)) { ok = false; break; }
-          copy.keys(a.v, walk, t, page, sbase + S::kV + vs * S::kTile);
-          copy.tell(smem_u32(&bars.v_full[vs]));
+#pragma unroll
+          for (int m = 0; m < kMine; ++m) {
+            const int grp = copy.warp + m * kCopyWarps;
+            if (grp >= kGroups) break;
+            copy.keys(a.v, &map_v, walk, t, grp, page[m], sbase + S::kV + vs * S::kTile,
+                      smem_u32(&bars.v_full[vs]));
+            page[m] = page1[m];
+          }
           t = t1;
-          page = page1;
         }
         ++segs;
       } while (ok && walk.next());
       cp_async_wait_all();
-    } else if (warp >= kSoftWarps + kCopyWarps) {
+      if (!ok) {  // let tensor copies land before the CTA ends
+        for (uint32_t t = nt < 2 ? 0 : nt - 2; t <= nt; ++t) {
+          mbar_wait_drain(smem_u32(&bars.k_full[t % kKStages]), (t / kKStages) & 1);
+          mbar_wait_drain(smem_u32(&bars.v_full[t % kVStages]), (t / kVStages) & 1);
+        }
+      }
+    } else if (warp == 0) {
       // ---------------- tensor cores
-      fewer_registers<kOtherRegs>();
-      if (warp == kSoftWarps + kCopyWarps && lane == 0)
-        tree_mma_role<T, kDim>(a, bars, walk, tmem, sbase, abort_flag);
+      tree_mma_role<T, kDim>(a, bars, walk, tmem, sbase, abort_flag);
     } else {
-      // ---------------- softmax and results of slot x (warps 0-3: A, 4-7: B)
-      more_registers<kSoftRegs>();
-      const int x = warp >> 2, quad = warp & 3;
+      // ---------------- softmax and results of slot x (warps 4-7: A, 8-11: B)
+      const int x = (warp - kSoftWarp0) >> 2, quad = warp & 3;
       const int trow = quad * 32 + lane;  // tile row = lane of tensor memory
       const uint32_t lane_base = uint32_t(quad * 32) << 16;
       const uint32_t cs = tmem + lane_base + 128 * x;
@@ -939,7 +1014,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   if (tid == 0 && sh.abort) raise_paged(a.table.status, MSA_ERR_TIMEOUT);
   tc_fence_before();
   __syncthreads();
-  if (warp == kSoftWarps + kCopyWarps) tmem_dealloc(tmem, 512);
+  if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
 // ------------------------------------------------------------ joining runs
@@ -1036,8 +1111,14 @@ struct TreeLayout {
   }
 };
 
+}  // namespace
+CUresult make_map_pages(CUtensorMap* m, const void* base, bool bf16, int32_t dim, int32_t heads,
+                        int32_t page_size, int64_t pages, int64_t head_stride,
+                        int64_t token_stride, int64_t page_stride, int32_t rows);  // msa_api.cu
+namespace {
+
 template <typename T, int kDim>
-cudaError_t launch_tree(const TreeArgs& a, cudaStream_t s) {
+cudaError_t launch_tree(TreeArgs a, cudaStream_t s) {
   auto kernel = k_paged_tree<T, kDim>;
   static std::atomic<uint64_t> done{0};
   cudaError_t e = allow_smem(kernel, kTreeSmem<kDim>, done);
@@ -1050,9 +1131,21 @@ cudaError_t launch_tree(const TreeArgs& a, cudaStream_t s) {
     launch_end("paged_tree_lists", s);
     if (e != cudaSuccess) return e;
   }
+  // tensor copies where a page holds 8 tokens (whole rows of the swizzle) and a map
+  // can be made of the pools
+  CUtensorMap map[2] = {};
+  const int32_t page_size = 1 << a.table.shift;
+  a.box = page_size >= 8 ? std::min(page_size, 32) : 0;
+  for (int i = 0; i < 2 && a.box > 0; ++i) {
+    const PagedPool& p = i ? a.v : a.k;
+    if (make_map_pages(&map[i], p.base, kLift<T> == 0.f, kDim, a.kv_heads, page_size,
+                       a.table.num_pages, p.head, p.token, p.page, a.box) != CUDA_SUCCESS)
+      a.box = 0;
+  }
   const int grid = std::min(device_sm_count(), kMaxRuns);
   launch_begin("paged_tree", s);
-  e = launch_k(true, kernel, dim3(unsigned(grid)), dim3(kTreeThreads), kTreeSmem<kDim>, s, a);
+  e = launch_k(true, kernel, dim3(unsigned(grid)), dim3(kTreeThreads), kTreeSmem<kDim>, s, a,
+               map[0], map[1]);
   launch_end("paged_tree", s);
   if (e != cudaSuccess || grid == 1) return e;
   launch_begin("paged_tree_join", s);

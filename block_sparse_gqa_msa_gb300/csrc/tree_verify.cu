@@ -75,6 +75,16 @@ __device__ __forceinline__ Pair32 warp_sum(Pair32 s) {
   }
   return s;
 }
+// Sum of v over the lanes up to this one, of the first kLanes lanes.
+template <int kLanes>
+__device__ __forceinline__ double scan(double v) {
+#pragma unroll
+  for (int o = 1; o < kLanes; o <<= 1) {
+    const double y = __shfl_up_sync(0xffffffffu, v, o);
+    if ((threadIdx.x & 31) >= o) v += y;
+  }
+  return v;
+}
 
 // What is left of a token's distribution: p's row, q's, the factors so far, the
 // tokens that were rejected (without q).
@@ -84,42 +94,66 @@ struct Rest {
   const int32_t* out;  // shared
   int n;               // rejections
   bool drawn;
-  __device__ __forceinline__ float at(float p_x, float q_x, int32_t x) const {
-    float r = p_x;
+  // r from p for the values x0, x0 + 32, ..; factors and tokens outermost.
+  template <int kN>
+  __device__ __forceinline__ void left(float (&r)[kN], const float (&q_x)[kN], int32_t x0) const {
     if (drawn) {
-      for (int i = 0; i < n; ++i) r = fmaxf(__fsub_rn(__fmul_rn(r, f[i]), q_x), 0.f);
+      for (int i = 0; i < n; ++i) {
+        const float g = f[i];
+#pragma unroll
+        for (int e = 0; e < kN; ++e) r[e] = fmaxf(__fsub_rn(__fmul_rn(r[e], g), q_x[e]), 0.f);
+      }
     } else {
-      for (int i = 0; i < n; ++i) r = out[i] == x ? 0.f : r;
+      for (int i = 0; i < n; ++i) {
+        const int32_t d = out[i] - x0;
+#pragma unroll
+        for (int e = 0; e < kN; ++e) r[e] = d == 32 * e ? 0.f : r[e];
+      }
     }
-    return r;
+  }
+  template <int kN>
+  __device__ __forceinline__ void load(float (&r)[kN], int32_t x0, int32_t hi) const {
+    float q_x[kN] = {};
+    const bool two = drawn && n > 0;
+    if (x0 + 32 * (kN - 1) < hi) {
+#pragma unroll
+      for (int e = 0; e < kN; ++e) r[e] = p[x0 + 32 * e];
+      if (two) {
+#pragma unroll
+        for (int e = 0; e < kN; ++e) q_x[e] = q[x0 + 32 * e];
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < kN; ++e) r[e] = x0 + 32 * e < hi ? p[x0 + 32 * e] : 0.f;
+      if (two) {
+#pragma unroll
+        for (int e = 0; e < kN; ++e) q_x[e] = x0 + 32 * e < hi ? q[x0 + 32 * e] : 0.f;
+      }
+    }
+    left(r, q_x, x0);
   }
 };
 
 // Sum of r over [lo, hi), by a warp.
 __device__ __forceinline__ Pair32 run_sum(const Rest& rest, int32_t lo, int32_t hi) {
   const int lane = threadIdx.x & 31;
-  Pair32 s{0.f, 0.f};
-  const bool two = rest.drawn && rest.n > 0;
+  Pair32 s[2] = {{0.f, 0.f}, {0.f, 0.f}};
   for (int32_t x0 = lo + lane; x0 < hi; x0 += 32 * kVerLoads) {
-    float p[kVerLoads], q[kVerLoads];
+    float r[kVerLoads];
+    rest.load(r, x0, hi);
 #pragma unroll
-    for (int i = 0; i < kVerLoads; ++i) {
-      const int32_t x = x0 + 32 * i;
-      p[i] = x < hi ? rest.p[x] : 0.f;
-      q[i] = two && x < hi ? rest.q[x] : 0.f;
-    }
-#pragma unroll
-    for (int i = 0; i < kVerLoads; ++i) s.add(rest.at(p[i], q[i], x0 + 32 * i));
+    for (int e = 0; e < kVerLoads; ++e) s[e & 1].add(r[e]);
   }
-  return warp_sum(s);
+  s[0].add(s[1]);
+  return warp_sum(s[0]);
 }
 
-__global__ void __launch_bounds__(kVerThreads) k_tree_verify(const VerifyArgs a) {
+__global__ void __launch_bounds__(kVerThreads, 2) k_tree_verify(const VerifyArgs a) {
   namespace cg = cooperative_groups;
   cg::cluster_group cluster = cg::this_cluster();
   __shared__ int32_t par[kTree], tok[kTree], out[kTree];
   __shared__ float us[kTree], pv[kTree], qv[kTree], factor[kTree];
-  __shared__ double warp_total[kVerWarps];
+  __shared__ double warp_total[2][kVerWarps];
   __shared__ double total[2];  // the CTA's, of this pass and the one before
   __shared__ int32_t path[kTree];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -143,14 +177,16 @@ __global__ void __launch_bounds__(kVerThreads) k_tree_verify(const VerifyArgs a)
   if (tid < n) {
     const int64_t t = t0 + tid;
     const int32_t x = a.tokens[t];
+    const float u = a.u[t];
     int32_t up = a.parents ? a.parents[t] : tid - 1;
     if (tid == 0 || up < 0 || up >= tid || x < 0 || x >= a.vocab) up = -1;
     par[tid] = up;
     tok[tid] = x;
+    us[tid] = u;
     if (up >= 0) {
-      us[tid] = a.u[t];
-      pv[tid] = a.target[(t0 + up) * a.target_stride + x];
+      const float p = a.target[(t0 + up) * a.target_stride + x];
       qv[tid] = a.draft ? a.draft[(t0 + up) * a.draft_stride + x] : 0.f;
+      pv[tid] = p;
     }
   }
   __syncthreads();
@@ -159,65 +195,59 @@ __global__ void __launch_bounds__(kVerThreads) k_tree_verify(const VerifyArgs a)
   const int32_t V = a.vocab;
   const int32_t c0 = int32_t(int64_t(V) * rank / a.cluster);
   const int32_t c1 = int32_t(int64_t(V) * (rank + 1) / a.cluster);
-  const int32_t w0 = c0 + int32_t(int64_t(c1 - c0) * warp / kVerWarps);
-  const int32_t w1 = c0 + int32_t(int64_t(c1 - c0) * (warp + 1) / kVerWarps);
+  auto part = [](int32_t lo, int32_t hi, int w) {  // start of the w-th 16th
+    return lo + int32_t(int64_t(hi - lo) * w / kVerWarps);
+  };
   int passes = 0;
-  double before = 0.0, R = 0.0;
-  // The sum over the vocabulary, R, and over the CTAs before this one; the same
-  // in every thread of the cluster.  total[] alternates, so one barrier a pass
-  // is enough.
+  double R = 0.0, before = 0.0;  // the sum over the vocabulary, and before this CTA
+  double each = 0.0;             // a lane: the sum of the cluster's CTA number lane
+  double run = 0.0;              // a lane: the CTA's sums up to warp number lane
+  // Sums r over the vocabulary; all threads of the cluster alike.  Its shared memory
+  // alternates, so one barrier of the cluster a pass is enough.
   auto sum_all = [&](const Rest& rest) {
-    const Pair32 s = run_sum(rest, w0, w1);
-    if (lane == 0) warp_total[warp] = s.value();
-    __syncthreads();
-    double* mine = &total[passes & 1];
+    const Pair32 s = run_sum(rest, part(c0, c1, warp), part(c0, c1, warp + 1));
+    const int b = passes & 1;
     ++passes;
-    if (tid == 0) {
-      double v = 0.0;
-      for (int w = 0; w < kVerWarps; ++w) v += warp_total[w];
-      *mine = v;
-    }
+    if (lane == 0) warp_total[b][warp] = s.value();
+    __syncthreads();
+    run = scan<kVerWarps>(lane < kVerWarps ? warp_total[b][lane] : 0.0);
+    if (tid == kVerWarps - 1) total[b] = run;
     cluster.sync();
-    double each[kVerCluster];
-#pragma unroll
-    for (int c = 0; c < kVerCluster; ++c)
-      each[c] = c < a.cluster ? *cluster.map_shared_rank(mine, c) : 0.0;
-    R = before = 0.0;
-#pragma unroll
-    for (int c = 0; c < kVerCluster; ++c) {
-      if (c == rank) before = R;
-      if (c < a.cluster) R += each[c];
-    }
+    each = lane < a.cluster ? *cluster.map_shared_rank(&total[b], lane) : 0.0;
+    const double sum = scan<kVerCluster>(each);
+    R = __shfl_sync(0xffffffffu, sum, a.cluster - 1);
+    before = __shfl_sync(0xffffffffu, sum, rank > 0 ? rank - 1 : 0);
+    if (rank == 0) before = 0.0;
   };
 
   // ---- the walk: every warp of every CTA alike
-  int cur = 0, kept = 1, out_n = 0;
+  int cur = 0, kept = 1;
   double S = 1.0;
   Rest rest{a.target + t0 * a.target_stride, a.draft ? a.draft + t0 * a.draft_stride : nullptr,
             factor, out, 0, a.draft != nullptr};
   if (tid == 0) path[0] = 0;
   int j = 1;
   bool summed = false;  // R is the sum of the rest
+  const int32_t up0 = lane < n ? par[lane] : -1, up1 = lane + 32 < n ? par[lane + 32] : -1;
   while (kept < a.max_path) {
     // the next child of cur from j on
-    const bool lo = lane < n && lane >= j && par[lane] == cur;
-    const bool hi = lane + 32 < n && lane + 32 >= j && par[lane + 32] == cur;
-    const uint64_t kids = uint64_t(__ballot_sync(0xffffffffu, lo)) |
-                          uint64_t(__ballot_sync(0xffffffffu, hi)) << 32;
+    const uint64_t kids =
+        uint64_t(__ballot_sync(0xffffffffu, lane >= j && up0 == cur)) |
+        uint64_t(__ballot_sync(0xffffffffu, lane + 32 >= j && up1 == cur)) << 32;
     if (kids == 0) break;
     const int kid = __ffsll(static_cast<long long>(kids)) - 1;
     bool keep;
-    const float mine = rest.at(pv[kid], qv[kid], tok[kid]);
+    float mine[1] = {pv[kid]};
+    const float q[1] = {qv[kid]};
+    rest.left(mine, q, tok[kid]);
     if (rest.drawn) {
-      if (rest.n > 0) {
-        if (!summed) {
-          sum_all(rest);
-          S = R;
-          summed = true;
-        }
+      if (rest.n > 0 && !summed) {
+        sum_all(rest);
+        S = R;
+        summed = true;
       }
-      const float f = S > 0.0 ? float(1.0 / S) : 0.f;
-      keep = double(us[kid]) * double(qv[kid]) < double(mine) * double(f);
+      const float f = rest.n == 0 ? 1.f : S > 0.0 ? float(1.0 / S) : 0.f;
+      keep = double(us[kid]) * double(q[0]) < double(mine[0]) * double(f);
       if (!keep) {
         __syncthreads();  // factor[] as it was is read
         if (tid == 0) factor[rest.n] = f;
@@ -226,13 +256,13 @@ __global__ void __launch_bounds__(kVerThreads) k_tree_verify(const VerifyArgs a)
         summed = false;
       }
     } else {
-      keep = mine > 0.f && double(us[kid]) * S < double(mine);
+      keep = mine[0] > 0.f && double(us[kid]) * S < double(mine[0]);
       if (!keep) {
-        S -= double(mine);
+        S -= double(mine[0]);
         __syncthreads();
-        if (tid == 0) out[out_n] = tok[kid];
+        if (tid == 0) out[rest.n] = tok[kid];
         __syncthreads();
-        rest.n = ++out_n;
+        ++rest.n;
       }
     }
     j = kid + 1;
@@ -241,16 +271,11 @@ __global__ void __launch_bounds__(kVerThreads) k_tree_verify(const VerifyArgs a)
       if (tid == 0) path[kept] = kid;
       ++kept;
       S = 1.0;
-      rest.n = out_n = 0;
+      rest.n = 0;
       summed = false;
       rest.p = a.target + (t0 + cur) * a.target_stride;
       if (rest.drawn) rest.q = a.draft + (t0 + cur) * a.draft_stride;
     }
-  }
-  __syncthreads();
-  if (rank == 0) {
-    for (int i = tid; i < a.max_path; i += kVerThreads) row_path[i] = i < kept ? path[i] : -1;
-    if (tid == 0) a.count[r] = kept;
   }
 
   // ---- the last token
@@ -259,80 +284,62 @@ __global__ void __launch_bounds__(kVerThreads) k_tree_verify(const VerifyArgs a)
     rest.n = 0;
     sum_all(rest);
   }
+  cluster.barrier_arrive();  // the others' shared memory is read; theirs of this CTA, below
+  if (rank == 0) {
+    // (path[] is whole: the sums had barriers)
+    for (int i = tid; i < a.max_path; i += kVerThreads) row_path[i] = i < kept ? path[i] : -1;
+    if (tid == 0) a.count[r] = kept;
+  }
   if (!(R > 0.0) || isinf(R)) {
     if (rank == 0 && tid == 0) a.last[r] = -1;
-    cluster.sync();
+    cluster.barrier_wait();
     return;
   }
   const double goal = double(a.u_last[r]) * R;
-  // The CTA in whose run the sum passes the goal (the last with anything in it, if
-  // the goal is not below the sum): each sees from its own and the later ones.
-  const double own = *(&total[(passes - 1) & 1]);
-  bool mine = own > 0.0 && before + own > goal;
-  if (mine) {
-    // a CTA before this one may have passed it already
-    mine = !(before > goal);
-  }
-  if (!mine && own > 0.0 && !(before + own > goal)) {
-    // no CTA passes it: the last with anything in it
-    double later = 0.0;
-    for (int c = rank + 1; c < a.cluster; ++c)
-      later += *cluster.map_shared_rank(&total[(passes - 1) & 1], c);
-    mine = !(later > 0.0);
-  }
-  cluster.sync();  // nobody reads the others' shared memory any more
-  if (!mine) return;
-  // the warp's run, then its 16th part, then 32 values at a time
-  auto choose = [&](double& base) {
-    int chosen = -1, some = -1;
-    double at = base, sum = base;
-    for (int w = 0; w < kVerWarps; ++w) {
-      const double t = warp_total[w];
-      if (t > 0.0) {
-        if (chosen < 0 || !(sum > goal)) {
-          some = w;
-          at = sum;
-        }
-        if (chosen < 0 && sum + t > goal) chosen = w;
-      }
-      if (chosen >= 0) break;
-      sum += t;
-    }
-    base = at;
-    return chosen >= 0 ? chosen : some;
+  // The first of the cluster's CTAs, of its warps, of their parts, whose sum passes
+  // the goal; where rounding or a goal past the sum leaves none, the last with
+  // anything in it.  at: the sum up to the lane's part, v: of it.
+  auto choose = [&](double at, double v, int parts) {
+    const uint32_t past = __ballot_sync(0xffffffffu, lane < parts && v > 0.0 && at > goal);
+    const uint32_t some = __ballot_sync(0xffffffffu, lane < parts && v > 0.0);
+    return past ? __ffs(past) - 1 : some ? 31 - __clz(some) : 0;
   };
-  double base = before;
-  const int w = choose(base);
-  const int32_t r0 = c0 + int32_t(int64_t(c1 - c0) * w / kVerWarps);
-  const int32_t r1 = c0 + int32_t(int64_t(c1 - c0) * (w + 1) / kVerWarps);
-  const int32_t s0 = r0 + int32_t(int64_t(r1 - r0) * warp / kVerWarps);
-  const int32_t s1 = r0 + int32_t(int64_t(r1 - r0) * (warp + 1) / kVerWarps);
-  __syncthreads();  // warp_total is read
-  const Pair32 part = run_sum(rest, s0, s1);
-  if (lane == 0) warp_total[warp] = part.value();
-  __syncthreads();
-  if (choose(base) != warp) return;
-  const bool two = rest.drawn && rest.n > 0;
-  int32_t found = -1, some = -1;
-  for (int32_t x0 = s0; x0 < s1 && found < 0; x0 += 32) {
-    const int32_t x = x0 + lane;
-    float v = 0.f;
-    if (x < s1) v = rest.at(rest.p[x], two ? rest.q[x] : 0.f, x);
-    double incl = double(v);
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const double y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
+  if (choose(scan<kVerCluster>(each), each, a.cluster) == rank) {
+    // the warp's run, then its 16th part, then 32 values at a time
+    auto narrow = [&](double sums, double& base) {  // sums: up to warp number lane
+      double prev = __shfl_up_sync(0xffffffffu, sums, 1);
+      if (lane == 0) prev = 0.0;
+      const int w = choose(base + sums, sums - prev, kVerWarps);
+      base += __shfl_sync(0xffffffffu, prev, w);
+      return w;
+    };
+    double base = before;
+    const int w = narrow(run, base);
+    const int32_t r0 = part(c0, c1, w), r1 = part(c0, c1, w + 1);
+    const int32_t s0 = part(r0, r1, warp), s1 = part(r0, r1, warp + 1);
+    const int b = passes & 1;
+    const Pair32 sum = run_sum(rest, s0, s1);
+    if (lane == 0) warp_total[b][warp] = sum.value();
+    __syncthreads();
+    run = scan<kVerWarps>(lane < kVerWarps ? warp_total[b][lane] : 0.0);
+    if (narrow(run, base) == warp) {
+      int32_t found = -1, some = -1;
+      for (int32_t x0 = s0; x0 < s1 && found < 0; x0 += 32) {
+        float v[1];
+        rest.load(v, x0 + lane, s1);
+        const double incl = scan<32>(double(v[0]));
+        const uint32_t past = __ballot_sync(0xffffffffu, v[0] > 0.f && base + incl > goal);
+        const uint32_t any = __ballot_sync(0xffffffffu, v[0] > 0.f);
+        if (past)
+          found = x0 + __ffs(past) - 1;
+        else if (any)
+          some = x0 + 31 - __clz(any);
+        base += __shfl_sync(0xffffffffu, incl, 31);
+      }
+      if (lane == 0) a.last[r] = found >= 0 ? found : some;
     }
-    const uint32_t past = __ballot_sync(0xffffffffu, v > 0.f && base + incl > goal);
-    const uint32_t any = __ballot_sync(0xffffffffu, v > 0.f);
-    if (past)
-      found = x0 + __ffs(past) - 1;
-    else if (any)
-      some = x0 + 31 - __clz(any);
-    base += __shfl_sync(0xffffffffu, incl, 31);
   }
-  if (lane == 0) a.last[r] = found >= 0 ? found : some;
+  cluster.barrier_wait();
 }
 
 }  // namespace
@@ -376,10 +383,10 @@ extern "C" msa_status msa_tree_verify(const float* target, int64_t target_stride
   a.T = T;
   a.vocab = vocab;
   a.max_path = max_path;
-  // as many CTAs a row as are on the chip at once (3 an SM), none with less than
+  // as many CTAs a row as are on the chip at once (2 an SM), none with less than
   // a pass of its loads to do
   int cluster = 1;
-  while (cluster < kVerCluster && int64_t(rows) * cluster * 2 <= int64_t(device_sm_count()) * 3 &&
+  while (cluster < kVerCluster && int64_t(rows) * cluster * 2 <= int64_t(device_sm_count()) * 2 &&
          vocab >= cluster * 2 * kVerThreads * 4)
     cluster *= 2;
   a.cluster = cluster;
