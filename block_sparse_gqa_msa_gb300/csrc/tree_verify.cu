@@ -153,9 +153,10 @@ __global__ void __launch_bounds__(kVerThreads, 2) k_tree_verify(const VerifyArgs
   cg::cluster_group cluster = cg::this_cluster();
   __shared__ int32_t par[kTree], tok[kTree], out[kTree];
   __shared__ float us[kTree], pv[kTree], qv[kTree], factor[kTree];
-  __shared__ double warp_total[2][kVerWarps];
+  __shared__ double warp_total[kVerWarps];
   __shared__ double total[2];  // the CTA's, of this pass and the one before
   __shared__ int32_t path[kTree];
+  __shared__ int32_t sh_cur, sh_last, sh_n, sh_lo, sh_hi;  // what warp 0 has the others sum
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = int(cluster.block_rank());
   const int32_t r = blockIdx.x / a.cluster;
@@ -191,138 +192,157 @@ __global__ void __launch_bounds__(kVerThreads, 2) k_tree_verify(const VerifyArgs
   }
   __syncthreads();
 
-  // the CTA's run of the vocabulary and the warp's
+  // The CTA's run of the vocabulary; the w-th 16th of a run.
   const int32_t V = a.vocab;
   const int32_t c0 = int32_t(int64_t(V) * rank / a.cluster);
   const int32_t c1 = int32_t(int64_t(V) * (rank + 1) / a.cluster);
-  auto part = [](int32_t lo, int32_t hi, int w) {  // start of the w-th 16th
+  auto part = [](int32_t lo, int32_t hi, int w) {
     return lo + int32_t(int64_t(hi - lo) * w / kVerWarps);
   };
-  int passes = 0;
-  double R = 0.0, before = 0.0;  // the sum over the vocabulary, and before this CTA
-  double each = 0.0;             // a lane: the sum of the cluster's CTA number lane
-  double run = 0.0;              // a lane: the CTA's sums up to warp number lane
-  // Sums r over the vocabulary; all threads of the cluster alike.  Its shared memory
-  // alternates, so one barrier of the cluster a pass is enough.
-  auto sum_all = [&](const Rest& rest) {
-    const Pair32 s = run_sum(rest, part(c0, c1, warp), part(c0, c1, warp + 1));
-    const int b = passes & 1;
-    ++passes;
-    if (lane == 0) warp_total[b][warp] = s.value();
-    __syncthreads();
-    run = scan<kVerWarps>(lane < kVerWarps ? warp_total[b][lane] : 0.0);
-    if (tid == kVerWarps - 1) total[b] = run;
-    cluster.sync();
-    each = lane < a.cluster ? *cluster.map_shared_rank(&total[b], lane) : 0.0;
-    const double sum = scan<kVerCluster>(each);
-    R = __shfl_sync(0xffffffffu, sum, a.cluster - 1);
-    before = __shfl_sync(0xffffffffu, sum, rank > 0 ? rank - 1 : 0);
-    if (rank == 0) before = 0.0;
+  auto rest_of = [&](int cur, int rejected) {
+    return Rest{a.target + (t0 + cur) * a.target_stride,
+                a.draft ? a.draft + (t0 + cur) * a.draft_stride : nullptr, factor, out, rejected,
+                a.draft != nullptr};
   };
-
-  // ---- the walk: every warp of every CTA alike
-  int cur = 0, kept = 1;
-  double S = 1.0;
-  Rest rest{a.target + t0 * a.target_stride, a.draft ? a.draft + t0 * a.draft_stride : nullptr,
-            factor, out, 0, a.draft != nullptr};
-  if (tid == 0) path[0] = 0;
-  int j = 1;
-  bool summed = false;  // R is the sum of the rest
+  // Warp 0 walks, and has all warps sum where it needs a sum (64-bit operations of 16
+  // warps would get in one another's way): the walks of the cluster's CTAs are alike.
+  int passes = 0;
+  int cur = 0, kept = 1, rejected = 0, j = 1;
+  double S = 1.0, R = 0.0, before = 0.0;
+  double each = 0.0;     // a lane: the sum of the cluster's CTA number lane
+  double run = 0.0;      // a lane: the CTA's sums up to warp number lane
+  bool summed = false;   // R is the sum of the rest
+  bool walking = true;
   const int32_t up0 = lane < n ? par[lane] : -1, up1 = lane + 32 < n ? par[lane + 32] : -1;
-  while (kept < a.max_path) {
-    // the next child of cur from j on
-    const uint64_t kids =
-        uint64_t(__ballot_sync(0xffffffffu, lane >= j && up0 == cur)) |
-        uint64_t(__ballot_sync(0xffffffffu, lane + 32 >= j && up1 == cur)) << 32;
-    if (kids == 0) break;
-    const int kid = __ffsll(static_cast<long long>(kids)) - 1;
-    bool keep;
-    float mine[1] = {pv[kid]};
-    const float q[1] = {qv[kid]};
-    rest.left(mine, q, tok[kid]);
-    if (rest.drawn) {
-      if (rest.n > 0 && !summed) {
-        sum_all(rest);
-        S = R;
-        summed = true;
+  if (tid == 0) path[0] = 0;
+  for (;;) {
+    if (warp == 0) {
+      while (walking) {
+        // the next child of cur from j on
+        const uint64_t kids =
+            uint64_t(__ballot_sync(0xffffffffu, lane >= j && up0 == cur)) |
+            uint64_t(__ballot_sync(0xffffffffu, lane + 32 >= j && up1 == cur)) << 32;
+        if (kids == 0 || kept == a.max_path) {
+          walking = false;
+          break;
+        }
+        const int kid = __ffsll(static_cast<long long>(kids)) - 1;
+        float mine[1] = {pv[kid]};
+        const float q[1] = {qv[kid]};
+        bool keep;
+        if (a.draft) {
+          if (rejected > 0 && !summed) break;  // (to the sum, and back here)
+          if (rejected > 0) S = R;
+          const float f = rejected == 0 ? 1.f : S > 0.0 ? float(1.0 / S) : 0.f;
+          rest_of(cur, rejected).left(mine, q, tok[kid]);
+          keep = double(us[kid]) * double(q[0]) < double(mine[0]) * double(f);
+          if (!keep) {
+            __syncwarp();
+            if (lane == 0) factor[rejected] = f;
+          }
+        } else {
+          rest_of(cur, rejected).left(mine, q, tok[kid]);
+          keep = mine[0] > 0.f && double(us[kid]) * S < double(mine[0]);
+          if (!keep) {
+            S -= double(mine[0]);
+            __syncwarp();
+            if (lane == 0) out[rejected] = tok[kid];
+          }
+        }
+        __syncwarp();
+        j = kid + 1;
+        summed = false;
+        if (keep) {
+          cur = kid;
+          if (lane == 0) path[kept] = kid;
+          ++kept;
+          S = 1.0;
+          rejected = 0;
+        } else {
+          ++rejected;
+        }
       }
-      const float f = rest.n == 0 ? 1.f : S > 0.0 ? float(1.0 / S) : 0.f;
-      keep = double(us[kid]) * double(q[0]) < double(mine[0]) * double(f);
-      if (!keep) {
-        __syncthreads();  // factor[] as it was is read
-        if (tid == 0) factor[rest.n] = f;
-        __syncthreads();
-        ++rest.n;
+      if (!walking && summed && !(R > 0.0) && rejected > 0) {  // nothing is left: p itself
+        rejected = 0;
         summed = false;
       }
-    } else {
-      keep = mine[0] > 0.f && double(us[kid]) * S < double(mine[0]);
-      if (!keep) {
-        S -= double(mine[0]);
-        __syncthreads();
-        if (tid == 0) out[rest.n] = tok[kid];
-        __syncthreads();
-        ++rest.n;
+      if (lane == 0) {
+        sh_cur = summed ? -1 : cur;
+        sh_last = cur;
+        sh_n = rejected;
       }
     }
-    j = kid + 1;
-    if (keep) {
-      cur = kid;
-      if (tid == 0) path[kept] = kid;
-      ++kept;
-      S = 1.0;
-      rest.n = 0;
-      summed = false;
-      rest.p = a.target + (t0 + cur) * a.target_stride;
-      if (rest.drawn) rest.q = a.draft + (t0 + cur) * a.draft_stride;
+    __syncthreads();
+    const int at = sh_cur;
+    if (at < 0) break;
+    const int32_t w0 = part(c0, c1, warp), w1 = part(c0, c1, warp + 1);
+    const Pair32 s = run_sum(rest_of(at, sh_n), w0, w1);
+    if (lane == 0) warp_total[warp] = s.value();
+    __syncthreads();
+    const int b = passes++ & 1;
+    if (warp == 0) {
+      run = scan<kVerWarps>(lane < kVerWarps ? warp_total[lane] : 0.0);
+      if (lane == kVerWarps - 1) total[b] = run;
+    }
+    cluster.sync();  // (total[] alternates: one barrier a pass is enough)
+    if (warp == 0) {
+      each = lane < a.cluster ? *cluster.map_shared_rank(&total[b], lane) : 0.0;
+      const double sum = scan<kVerCluster>(each);
+      R = __shfl_sync(0xffffffffu, sum, a.cluster - 1);
+      before = __shfl_sync(0xffffffffu, sum, rank > 0 ? rank - 1 : 0);
+      if (rank == 0) before = 0.0;
+      summed = true;
     }
   }
 
   // ---- the last token
-  if (!summed) sum_all(rest);
-  if (!(R > 0.0) && rest.n > 0) {  // nothing is left: p itself
-    rest.n = 0;
-    sum_all(rest);
-  }
-  cluster.barrier_arrive();  // the others' shared memory is read; theirs of this CTA, below
-  if (rank == 0) {
-    // (path[] is whole: the sums had barriers)
-    for (int i = tid; i < a.max_path; i += kVerThreads) row_path[i] = i < kept ? path[i] : -1;
-    if (tid == 0) a.count[r] = kept;
-  }
-  if (!(R > 0.0) || isinf(R)) {
-    if (rank == 0 && tid == 0) a.last[r] = -1;
-    cluster.barrier_wait();
-    return;
-  }
-  const double goal = double(a.u_last[r]) * R;
+  cluster.barrier_arrive();  // this CTA has read the others' shared memory
   // The first of the cluster's CTAs, of its warps, of their parts, whose sum passes
   // the goal; where rounding or a goal past the sum leaves none, the last with
-  // anything in it.  at: the sum up to the lane's part, v: of it.
-  auto choose = [&](double at, double v, int parts) {
-    const uint32_t past = __ballot_sync(0xffffffffu, lane < parts && v > 0.0 && at > goal);
+  // anything in it.  up_to: the sum up to the lane's part, v: of it.
+  double goal = 0.0, base = before;
+  auto choose = [&](double up_to, double v, int parts) {
+    const uint32_t past = __ballot_sync(0xffffffffu, lane < parts && v > 0.0 && up_to > goal);
     const uint32_t some = __ballot_sync(0xffffffffu, lane < parts && v > 0.0);
     return past ? __ffs(past) - 1 : some ? 31 - __clz(some) : 0;
   };
-  if (choose(scan<kVerCluster>(each), each, a.cluster) == rank) {
-    // the warp's run, then its 16th part, then 32 values at a time
-    auto narrow = [&](double sums, double& base) {  // sums: up to warp number lane
-      double prev = __shfl_up_sync(0xffffffffu, sums, 1);
-      if (lane == 0) prev = 0.0;
-      const int w = choose(base + sums, sums - prev, kVerWarps);
-      base += __shfl_sync(0xffffffffu, prev, w);
-      return w;
-    };
-    double base = before;
-    const int w = narrow(run, base);
-    const int32_t r0 = part(c0, c1, w), r1 = part(c0, c1, w + 1);
-    const int32_t s0 = part(r0, r1, warp), s1 = part(r0, r1, warp + 1);
-    const int b = passes & 1;
-    const Pair32 sum = run_sum(rest, s0, s1);
-    if (lane == 0) warp_total[b][warp] = sum.value();
+  auto narrow = [&](double sums) {  // sums: up to warp number lane
+    double prev = __shfl_up_sync(0xffffffffu, sums, 1);
+    if (lane == 0) prev = 0.0;
+    const int w = choose(base + sums, sums - prev, kVerWarps);
+    base += __shfl_sync(0xffffffffu, prev, w);
+    return w;
+  };
+  if (warp == 0) {
+    const bool any = R > 0.0 && !isinf(R);
+    goal = double(a.u_last[r]) * R;
+    int32_t lo = 0, hi = 0;
+    if (any && choose(scan<kVerCluster>(each), each, a.cluster) == rank) {
+      const int w = narrow(run);
+      lo = part(c0, c1, w);
+      hi = part(c0, c1, w + 1);
+    }
+    if (lane == 0) {
+      sh_lo = lo;
+      sh_hi = hi;
+      if (rank == 0) {
+        a.count[r] = kept;
+        if (!any) a.last[r] = -1;
+      }
+    }
+    if (rank == 0)
+      for (int i = lane; i < a.max_path; i += 32) row_path[i] = i < kept ? path[i] : -1;
+  }
+  __syncthreads();
+  const int32_t r0 = sh_lo, r1 = sh_hi;
+  if (r0 < r1) {  // this CTA has it: the run's 16th part, then 32 values at a time
+    const Rest rest = rest_of(sh_last, sh_n);
+    const Pair32 s = run_sum(rest, part(r0, r1, warp), part(r0, r1, warp + 1));
+    if (lane == 0) warp_total[warp] = s.value();
     __syncthreads();
-    run = scan<kVerWarps>(lane < kVerWarps ? warp_total[b][lane] : 0.0);
-    if (narrow(run, base) == warp) {
+    if (warp == 0) {
+      const int w = narrow(scan<kVerWarps>(lane < kVerWarps ? warp_total[lane] : 0.0));
+      const int32_t s0 = part(r0, r1, w), s1 = part(r0, r1, w + 1);
       int32_t found = -1, some = -1;
       for (int32_t x0 = s0; x0 < s1 && found < 0; x0 += 32) {
         float v[1];
