@@ -11,9 +11,11 @@
 // Both are bound by HBM: x in and y out (forward), x and dy in and dx out.  A
 // lane holds 16 channels of a head (8 pairs and both of their halves), so a
 // head is 8 or 4 lanes, its sums two or three exchanges, and the rotation needs
-// none.  A warp takes a token, or a slice of its heads where tokens are few, and
-// loads several heads a lane before it works on any.  A token's angles are
-// formed once a warp.
+// none.  A warp takes an equal run of all tokens' heads and forms a token's
+// angles once.  It works alone: each lane
+// copies its own channels into its own places of a ring in shared memory, 8 KB a
+// warp ahead of the sums, across tokens; 128 KB an SM are on their way at any
+// time, and no registers are held for them.
 #include <algorithm>
 
 #include "paged.cuh"
@@ -21,10 +23,10 @@
 namespace msa {
 namespace {
 
-constexpr int kNormThreads = 256;
-constexpr int kBackThreads = 512;
-constexpr int kFwdBatch = 4;  // heads a lane that are loaded before the first is worked on
-constexpr int kBwdBatch = 2;
+constexpr int kNormThreads = 512;
+constexpr int kNormWarps = kNormThreads / 32;
+constexpr int kRing = 8192;  // bytes of a warp's ring
+constexpr int kNormSmem = kNormWarps * kRing;
 
 struct NormArgs {
   const void* x[2];       // queries, keys
@@ -38,7 +40,7 @@ struct NormArgs {
   float* dw[2];
   int64_t T;
   int32_t heads[2];
-  int32_t rot, w_type, slices, parts;
+  int32_t rot, w_type, parts;
   float eps;
 };
 
@@ -73,13 +75,12 @@ struct Place {
 
 // Angles of a token, left in the warp's shared memory, then the lane's 8.
 template <int kDim, bool kInter>
-__device__ __forceinline__ void angles(const NormArgs& a, int64_t t, float2* mine,
+__device__ __forceinline__ void angles(const NormArgs& a, int32_t pos, float2* mine,
                                        const Place<kDim, kInter>& at, float (&c)[8],
                                        float (&s)[8]) {
   const int lane = threadIdx.x & 31;
   __syncwarp();
   if (a.rot > 0) {
-    const int64_t pos = a.positions[t];
     for (int i = lane; i < a.rot / 2; i += 32) mine[i] = turn_of(pos, a.inv_freq[i]);
   }
   __syncwarp();
@@ -128,60 +129,126 @@ __device__ __forceinline__ float head_sum(float v) {
   return v;
 }
 
-// A warp's item: a token and a run of its groups.  Groups are 32 / kLanes heads
-// of queries, then of keys.
-struct Groups {
-  int q, all;
-  __device__ __forceinline__ Groups(const NormArgs& a, int per)
-      : q((a.heads[0] + per - 1) / per), all(q + (a.heads[1] + per - 1) / per) {}
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void copies_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int kN>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kN) : "memory");
+}
+
+// A warp's place in its run of groups.  A group is 32 / kLanes heads of the queries
+// or of the keys of a token, a head to kLanes lanes; the tokens' groups are dealt out
+// in equal runs.
+struct Cursor {
+  int64_t t;
+  int32_t g;
+  int32_t left;
+  int32_t groups_q, groups;
+  __device__ __forceinline__ void next() {
+    --left;
+    if (++g == groups) {
+      g = 0;
+      ++t;
+    }
+  }
 };
 
-template <typename T, int kDim, bool kInter>
-__global__ void __launch_bounds__(kNormThreads, 2) k_norm_rope(const NormArgs a) {
+// Forward, or the gradient: then each CTA's sums of dw go to the workspace,
+// k_norm_rope_join adds them up in order.
+template <typename T, int kDim, bool kInter, bool kBack>
+__global__ void __launch_bounds__(kNormThreads, 1) k_norm_rope(const NormArgs a) {
   constexpr int kLanes = kDim / 16, kPer = 32 / kLanes;
+  constexpr int kParts = kBack ? 4 : 2;             // copies of a lane in a group
+  constexpr int kDepth = kRing / (kParts * 512);    // groups on their way
+  extern __shared__ __align__(16) uint8_t ring[];
   __shared__ __align__(16) float sw[2][kDim];
-  __shared__ float2 turns[kNormThreads / 32][kDim / 2];
+  __shared__ float2 turns[kNormWarps][kDim / 2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const Place<kDim, kInter> at(lane % kLanes, a.rot);
   const int slot = lane / kLanes;
-  const Groups groups(a, kPer);
   grid_dep_wait();
   grid_dep_release();
+  Cursor work;
+  work.groups_q = (a.heads[0] + kPer - 1) / kPer;
+  work.groups = work.groups_q + (a.heads[1] + kPer - 1) / kPer;
+  {
+    const int64_t all = a.T * work.groups, runs = int64_t(gridDim.x) * kNormWarps;
+    const int64_t run = int64_t(warp) * gridDim.x + blockIdx.x;
+    const int64_t first = all * run / runs;
+    work.left = int32_t(all * (run + 1) / runs - first);
+    work.t = first / work.groups;
+    work.g = int32_t(first - work.t * work.groups);
+  }
+  Cursor ahead = work;
+  uint8_t* const mine = ring + warp * kRing + lane * 16;
+  const uint32_t mine_at = uint32_t(__cvta_generic_to_shared(mine));
+  auto fetch = [&](int stage) {
+    if (ahead.left > 0) {
+      const int kind = ahead.g >= ahead.groups_q;
+      const int h = (kind ? ahead.g - ahead.groups_q : ahead.g) * kPer + slot;
+      if (h < a.heads[kind]) {
+        const uint32_t dst = mine_at + stage * (kParts * 512);
+        const T* x = static_cast<const T*>(a.x[kind]) + ahead.t * a.stride[kind] + h * kDim;
+        copy16(dst, x + at.c0);
+        copy16(dst + 512, x + at.c1);
+        if (kBack) {
+          const T* dy = static_cast<const T*>(a.dy[kind]) + (ahead.t * a.heads[kind] + h) * kDim;
+          copy16(dst + 1024, dy + at.c0);
+          copy16(dst + 1536, dy + at.c1);
+        }
+      }
+      ahead.next();
+    }
+    copies_commit();
+  };
+#pragma unroll 1
+  for (int i = 0; i < kDepth; ++i) fetch(i);
   for (int i = threadIdx.x; i < 2 * kDim; i += kNormThreads)
     sw[i / kDim][i % kDim] = weight_at(a.w[i / kDim], a.w_type, i % kDim);
   __syncthreads();
-  const int64_t item = int64_t(blockIdx.x) * (kNormThreads / 32) + warp;
-  const int64_t t = item / a.slices;
-  const int slice = int(item % a.slices);
-  if (t >= a.T) return;
-  const int g0 = groups.all * slice / a.slices, g1 = groups.all * (slice + 1) / a.slices;
+
+  float acc[2][16] = {};
   float c[8], s[8];
-  for (int g = g0; g < g1; g += kFwdBatch) {
-    uint4 u[kFwdBatch], v[kFwdBatch];
-#pragma unroll
-    for (int b = 0; b < kFwdBatch; ++b) {
-      const int kind = g + b >= groups.q;
-      const int h = (kind ? g + b - groups.q : g + b) * kPer + slot;
-      u[b] = v[b] = make_uint4(0, 0, 0, 0);
-      if (g + b < g1 && h < a.heads[kind]) {
-        const T* x = static_cast<const T*>(a.x[kind]) + t * a.stride[kind] + h * kDim;
-        u[b] = *reinterpret_cast<const uint4*>(x + at.c0);
-        v[b] = *reinterpret_cast<const uint4*>(x + at.c1);
-      }
+  int64_t token = -1;
+  int32_t pos = a.rot > 0 ? a.positions[min(work.t, a.T - 1)] : 0;
+  int stage = 0;
+#pragma unroll 1
+  for (; work.left > 0; work.next()) {
+    if (work.t != token) {
+      token = work.t;
+      angles<kDim, kInter>(a, pos, turns[warp], at, c, s);
+      if (a.rot > 0) pos = a.positions[min(token + 1, a.T - 1)];  // the next token's
     }
-    if (g == g0) angles<kDim, kInter>(a, t, turns[warp], at, c, s);
+    const int kind = work.g >= work.groups_q;
+    const int h = (kind ? work.g - work.groups_q : work.g) * kPer + slot;
+    const bool real = h < a.heads[kind];
+    copies_wait<kDepth - 1>();
+    const uint8_t* from = mine + stage * (kParts * 512);
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    const uint4 u = real ? *reinterpret_cast<const uint4*>(from) : zero;
+    const uint4 v = real ? *reinterpret_cast<const uint4*>(from + 512) : zero;
+    float x[16];
+    unpack8<T>(u, x);
+    unpack8<T>(v, x + 8);
+    [[maybe_unused]] float d[16];
+    if (kBack) {
+      const uint4 du = real ? *reinterpret_cast<const uint4*>(from + 1024) : zero;
+      const uint4 dv = real ? *reinterpret_cast<const uint4*>(from + 1536) : zero;
+      unpack8<T>(du, d);
+      unpack8<T>(dv, d + 8);
+    }
+    fetch(stage);
+    stage = stage + 1 == kDepth ? 0 : stage + 1;
+    float ss = 0.f;
 #pragma unroll
-    for (int b = 0; b < kFwdBatch; ++b) {
-      if (g + b >= g1) break;
-      const int kind = g + b >= groups.q;
-      const int h = (kind ? g + b - groups.q : g + b) * kPer + slot;
-      float x[16];
-      unpack8<T>(u[b], x);
-      unpack8<T>(v[b], x + 8);
-      float ss = 0.f;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) ss = fmaf(x[i], x[i], ss);
-      const float n = rsqrtf(head_sum<kLanes>(ss) * (1.f / kDim) + a.eps);
+    for (int i = 0; i < 16; ++i) ss = fmaf(x[i], x[i], ss);
+    const float n = rsqrtf(head_sum<kLanes>(ss) * (1.f / kDim) + a.eps);
+    if (!kBack) {
 #pragma unroll
       for (int i = 0; i < 16; i += 4) {
         const float4 w = *reinterpret_cast<const float4*>(
@@ -192,100 +259,44 @@ __global__ void __launch_bounds__(kNormThreads, 2) k_norm_rope(const NormArgs a)
         x[i + 3] *= n * w.w;
       }
       rotate16<kInter, false>(x, c, s);
-      if (h < a.heads[kind]) {
-        T* y = static_cast<T*>(a.y[kind]) + (t * a.heads[kind] + h) * kDim;
-        *reinterpret_cast<uint4*>(y + at.c0) = pack8<T>(x);
-        *reinterpret_cast<uint4*>(y + at.c1) = pack8<T>(x + 8);
+    } else {
+      rotate16<kInter, true>(d, c, s);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] *= n;  // u
+      if (kind == 0) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[0][i] = fmaf(d[i], x[i], acc[0][i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[1][i] = fmaf(d[i], x[i], acc[1][i]);
       }
+      float dot = 0.f;
+#pragma unroll
+      for (int i = 0; i < 16; i += 4) {
+        const float4 w = *reinterpret_cast<const float4*>(
+            &sw[kind][(i < 8 ? at.c0 + i : at.c1 + i - 8)]);
+        d[i] *= w.x;
+        d[i + 1] *= w.y;
+        d[i + 2] *= w.z;
+        d[i + 3] *= w.w;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) dot = fmaf(d[i + e], x[i + e], dot);
+      }
+      const float m = head_sum<kLanes>(dot) * (1.f / kDim);  // mean(g w u)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] = n * (d[i] - x[i] * m);
+    }
+    if (real) {
+      T* y = static_cast<T*>(a.y[kind]) + (token * a.heads[kind] + h) * kDim;
+      *reinterpret_cast<uint4*>(y + at.c0) = pack8<T>(x);
+      *reinterpret_cast<uint4*>(y + at.c1) = pack8<T>(x + 8);
     }
   }
-}
-
-// Each CTA's sums of dw go to the workspace, k_norm_rope_join adds them up in
-// order.
-template <typename T, int kDim, bool kInter>
-__global__ void __launch_bounds__(kBackThreads, 1) k_norm_rope_back(const NormArgs a) {
-  constexpr int kLanes = kDim / 16, kPer = 32 / kLanes, kWarps = kBackThreads / 32;
-  __shared__ __align__(16) float sw[2][kDim];
-  __shared__ float2 turns[kWarps][kDim / 2];
-  __shared__ float sums[kWarps][2][kDim];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const Place<kDim, kInter> at(lane % kLanes, a.rot);
-  const int slot = lane / kLanes;
-  const Groups groups(a, kPer);
-  grid_dep_wait();
-  grid_dep_release();
-  for (int i = threadIdx.x; i < 2 * kDim; i += kBackThreads)
-    sw[i / kDim][i % kDim] = weight_at(a.w[i / kDim], a.w_type, i % kDim);
+  if (!kBack) return;
+  // the warp's heads, then the CTA's warps, in order; sums where the rings were
+  copies_wait<0>();
   __syncthreads();
-  float acc[2][16] = {};
-  const int64_t items = a.T * a.slices;
-  for (int64_t item = int64_t(warp) * gridDim.x + blockIdx.x; item < items;
-       item += int64_t(gridDim.x) * kWarps) {
-    const int64_t t = item / a.slices;
-    const int slice = int(item % a.slices);
-    const int g0 = groups.all * slice / a.slices, g1 = groups.all * (slice + 1) / a.slices;
-    float c[8], s[8];
-    for (int g = g0; g < g1; g += kBwdBatch) {
-      uint4 u[kBwdBatch], v[kBwdBatch], du[kBwdBatch], dv[kBwdBatch];
-#pragma unroll
-      for (int b = 0; b < kBwdBatch; ++b) {
-        const int kind = g + b >= groups.q;
-        const int h = (kind ? g + b - groups.q : g + b) * kPer + slot;
-        u[b] = v[b] = du[b] = dv[b] = make_uint4(0, 0, 0, 0);
-        if (g + b < g1 && h < a.heads[kind]) {
-          const T* x = static_cast<const T*>(a.x[kind]) + t * a.stride[kind] + h * kDim;
-          const T* dy = static_cast<const T*>(a.dy[kind]) + (t * a.heads[kind] + h) * kDim;
-          u[b] = *reinterpret_cast<const uint4*>(x + at.c0);
-          v[b] = *reinterpret_cast<const uint4*>(x + at.c1);
-          du[b] = *reinterpret_cast<const uint4*>(dy + at.c0);
-          dv[b] = *reinterpret_cast<const uint4*>(dy + at.c1);
-        }
-      }
-      if (g == g0) angles<kDim, kInter>(a, t, turns[warp], at, c, s);
-#pragma unroll
-      for (int b = 0; b < kBwdBatch; ++b) {
-        if (g + b >= g1) break;
-        const int kind = g + b >= groups.q;
-        const int h = (kind ? g + b - groups.q : g + b) * kPer + slot;
-        float x[16], d[16];
-        unpack8<T>(u[b], x);
-        unpack8<T>(v[b], x + 8);
-        unpack8<T>(du[b], d);
-        unpack8<T>(dv[b], d + 8);
-        rotate16<kInter, true>(d, c, s);
-        float ss = 0.f, dot = 0.f;
-        float w[16];
-#pragma unroll
-        for (int i = 0; i < 16; i += 4)
-          *reinterpret_cast<float4*>(w + i) = *reinterpret_cast<const float4*>(
-              &sw[kind][(i < 8 ? at.c0 + i : at.c1 + i - 8)]);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          ss = fmaf(x[i], x[i], ss);
-          dot = fmaf(d[i] * w[i], x[i], dot);
-        }
-        const float n = rsqrtf(head_sum<kLanes>(ss) * (1.f / kDim) + a.eps);
-        // mean(g w u) with u = x n
-        const float m = head_sum<kLanes>(dot) * n * (1.f / kDim);
-        if (kind == 0) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) acc[0][i] = fmaf(d[i], x[i] * n, acc[0][i]);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) acc[1][i] = fmaf(d[i], x[i] * n, acc[1][i]);
-        }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = n * (d[i] * w[i] - x[i] * n * m);
-        if (h < a.heads[kind]) {
-          T* y = static_cast<T*>(a.y[kind]) + (t * a.heads[kind] + h) * kDim;
-          *reinterpret_cast<uint4*>(y + at.c0) = pack8<T>(x);
-          *reinterpret_cast<uint4*>(y + at.c1) = pack8<T>(x + 8);
-        }
-      }
-    }
-  }
-  // the warp's heads, then the CTA's warps, in order
+  float* sums = reinterpret_cast<float*>(ring);  // [warps][2][dim]
 #pragma unroll
   for (int kind = 0; kind < 2; ++kind)
 #pragma unroll
@@ -293,13 +304,13 @@ __global__ void __launch_bounds__(kBackThreads, 1) k_norm_rope_back(const NormAr
       float v = acc[kind][i];
 #pragma unroll
       for (int o = kLanes; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-      if (slot == 0) sums[warp][kind][i < 8 ? at.c0 + i : at.c1 + i - 8] = v;
+      if (slot == 0) sums[(warp * 2 + kind) * kDim + (i < 8 ? at.c0 + i : at.c1 + i - 8)] = v;
     }
   __syncthreads();
-  for (int i = threadIdx.x; i < 2 * kDim; i += kBackThreads) {
+  for (int i = threadIdx.x; i < 2 * kDim; i += kNormThreads) {
     float v = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) v += sums[w][i / kDim][i % kDim];
+    for (int w = 0; w < kNormWarps; ++w) v += sums[w * 2 * kDim + i];
     a.part[int64_t(blockIdx.x) * 2 * kDim + i] = v;
   }
 }
@@ -325,35 +336,36 @@ __global__ void __launch_bounds__(kJoinThreads) k_norm_rope_join(const NormArgs 
   }
 }
 
-constexpr int kMaxParts = 160;  // CTAs of the backward: one an SM
+constexpr int kMaxParts = 160;  // CTAs: one an SM
 size_t norm_workspace(int32_t dim) { return sizeof(float) * kMaxParts * 2 * size_t(dim); }
 
-// Slices of a token's groups: enough warps to fill the chip where tokens are few.
-int32_t norm_slices(const NormArgs& a, int per, int warps_sm) {
+// Forward, or the gradient (a.parts: its CTAs).
+template <typename T, int kDim, bool kInter, bool kBack>
+cudaError_t launch_norm_as(NormArgs& a, cudaStream_t s) {
+  auto kernel = k_norm_rope<T, kDim, kInter, kBack>;
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(kernel, kNormSmem, done);
+  if (e != cudaSuccess) return e;
+  const int64_t per = 512 / kDim, sms = std::min(device_sm_count(), kMaxParts);
   const int64_t groups = (a.heads[0] + per - 1) / per + (a.heads[1] + per - 1) / per;
-  int64_t n = int64_t(device_sm_count()) * warps_sm / a.T;
-  if (n > groups) n = groups;
-  return int32_t(n < 1 ? 1 : n);
-}
-
-template <typename T, int kDim>
-cudaError_t launch_norm(NormArgs a, bool inter, cudaStream_t s) {
-  a.slices = norm_slices(a, 512 / kDim, 16);
-  const int64_t warps = a.T * a.slices, each = kNormThreads / 32;
-  const dim3 grid(unsigned((warps + each - 1) / each));
-  return inter ? launch_k(true, k_norm_rope<T, kDim, true>, grid, dim3(kNormThreads), 0, s, a)
-               : launch_k(true, k_norm_rope<T, kDim, false>, grid, dim3(kNormThreads), 0, s, a);
+  a.parts = int32_t(std::min<int64_t>(sms, a.T * groups));
+  return launch_k(true, kernel, dim3(unsigned(a.parts)), dim3(kNormThreads), kNormSmem, s, a);
 }
 template <typename T, int kDim>
-cudaError_t launch_norm_back(NormArgs& a, bool inter, cudaStream_t s) {
-  a.slices = norm_slices(a, 512 / kDim, kBackThreads / 32);
-  int64_t parts = std::min(device_sm_count(), kMaxParts);
-  parts = std::min<int64_t>(parts, a.T * a.slices);
-  a.parts = int32_t(parts);
-  const dim3 grid{unsigned(parts)};
-  return inter
-             ? launch_k(true, k_norm_rope_back<T, kDim, true>, grid, dim3(kBackThreads), 0, s, a)
-             : launch_k(true, k_norm_rope_back<T, kDim, false>, grid, dim3(kBackThreads), 0, s, a);
+cudaError_t launch_norm(NormArgs& a, bool inter, bool back, cudaStream_t s) {
+  if (back)
+    return inter ? launch_norm_as<T, kDim, true, true>(a, s)
+                 : launch_norm_as<T, kDim, false, true>(a, s);
+  return inter ? launch_norm_as<T, kDim, true, false>(a, s)
+               : launch_norm_as<T, kDim, false, false>(a, s);
+}
+cudaError_t launch_norm_any(NormArgs& a, const msa_norm_rope_args* p, bool back, cudaStream_t s) {
+  const bool inter = p->interleaved != 0;
+  if (p->dtype == MSA_BF16)
+    return p->head_dim == 128 ? launch_norm<__nv_bfloat16, 128>(a, inter, back, s)
+                              : launch_norm<__nv_bfloat16, 64>(a, inter, back, s);
+  return p->head_dim == 128 ? launch_norm<__half, 128>(a, inter, back, s)
+                            : launch_norm<__half, 64>(a, inter, back, s);
 }
 template <int kDim>
 cudaError_t launch_norm_join(const NormArgs& a, cudaStream_t s) {
@@ -417,15 +429,8 @@ extern "C" msa_status msa_norm_rope(const msa_norm_rope_args* args, void* q_out,
   a.y[0] = q_out;
   a.y[1] = k_out;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const bool inter = args->interleaved != 0;
   launch_begin("norm_rope", s);
-  cudaError_t e;
-  if (args->dtype == MSA_BF16)
-    e = args->head_dim == 128 ? launch_norm<__nv_bfloat16, 128>(a, inter, s)
-                              : launch_norm<__nv_bfloat16, 64>(a, inter, s);
-  else
-    e = args->head_dim == 128 ? launch_norm<__half, 128>(a, inter, s)
-                              : launch_norm<__half, 64>(a, inter, s);
+  const cudaError_t e = launch_norm_any(a, args, false, s);
   launch_end("norm_rope", s);
   return e == cudaSuccess ? MSA_OK : MSA_ERR_CUDA;
 }
@@ -460,15 +465,8 @@ extern "C" msa_status msa_norm_rope_backward(const msa_norm_rope_args* args, con
   a.dw[1] = dk_weight;
   a.part = static_cast<float*>(workspace);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const bool inter = args->interleaved != 0;
   launch_begin("norm_rope_back", s);
-  cudaError_t e;
-  if (args->dtype == MSA_BF16)
-    e = args->head_dim == 128 ? launch_norm_back<__nv_bfloat16, 128>(a, inter, s)
-                              : launch_norm_back<__nv_bfloat16, 64>(a, inter, s);
-  else
-    e = args->head_dim == 128 ? launch_norm_back<__half, 128>(a, inter, s)
-                              : launch_norm_back<__half, 64>(a, inter, s);
+  cudaError_t e = launch_norm_any(a, args, true, s);
   launch_end("norm_rope_back", s);
   if (e != cudaSuccess) return MSA_ERR_CUDA;
   launch_begin("norm_rope_join", s);
