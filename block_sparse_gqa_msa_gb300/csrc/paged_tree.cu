@@ -319,7 +319,7 @@ struct TreeBars {
 };
 struct TreeShared {
   TreeBars bars;
-  uint32_t there[4][kGroups];  // keys of a tile that are there; a ring of 4 tiles
+  uint4 there[4];               // keys of a tile that are there; a ring of 4 tiles
   float2 states[2][kTileRows];    // (m, l) of the slots, where they are joined
   uint32_t tmem_base;
   int abort;
@@ -335,10 +335,6 @@ __device__ __forceinline__ void cp_async16_zero(uint32_t dst, const void* src, b
                "r"(real ? 16 : 0)
                : "memory");
 }
-__device__ __forceinline__ void cp_async_wait_all() {
-  asm volatile("cp.async.wait_all;" ::: "memory");
-}
-
 // First key of an item's tile and the end of its keys.
 struct TileKeys {
   int32_t first, end;
@@ -357,8 +353,7 @@ __device__ __forceinline__ TileKeys tile_keys(const TreeArgs& a, const TreeWalk&
 }
 
 // The copying warps' side: fills query, key and value tiles; each copy's landing
-// counts on the tile's barrier (the thread that issues the products orders what it
-// has waited for before them).
+// counts on the tile's barrier.
 template <typename T, int kDim>
 struct Copier {
   using S = TreeShape<kDim>;
@@ -368,9 +363,15 @@ struct Copier {
   const TreeArgs& a;
   int warp, lane;                 // of the copying warps
 
-  // The barrier counts this thread once, when all its copies so far have landed.
-  static __device__ __forceinline__ void tell(uint32_t bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+  uint32_t pend;                  // barrier of 16-byte copies not told of yet, or 0
+  // Tells of them, once they have landed: before the warp waits for anything else.
+  __device__ __forceinline__ void tell() {
+    if (pend == 0) return;
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(pend);
+    pend = 0;
   }
   static __device__ __forceinline__ uint32_t at(int row, int chunk) {
     return (chunk >> 3) * 16384u + row * 128u + (((chunk & 7) ^ (row & 7)) << 4);
@@ -408,10 +409,10 @@ struct Copier {
     return -1;
   }
   // Starts the copies of a group of 32 keys (or values) into a tile; its barrier
-  // counts 33 times for the group.
+  // counts once for the group.
   __device__ __forceinline__ void keys(const PagedPool& pool, const CUtensorMap* map,
                                        const TreeWalk& s, const TileKeys& t, int grp,
-                                       int32_t page, uint32_t tile, uint32_t bar) const {
+                                       int32_t page, uint32_t tile, uint32_t bar) {
     const int32_t mask = (1 << a.table.shift) - 1, j0 = t.first + grp * 32;
     if (a.box > 0 && (j0 & (a.box - 1)) == 0 && __all_sync(0xffffffffu, page >= 0)) {
       constexpr int kHalves = kDim / 64;
@@ -422,7 +423,6 @@ struct Copier {
       if (b < 32)
         tma_load_4d(tile + half * 16384u + (grp * 32 + b) * 128u, map, bar, half * 64, s.g,
                     (j0 + b) & mask, p);
-      mbar_arrive(bar);
       return;
     }
     const int sub = lane / kChunks, c = lane % kChunks;
@@ -436,8 +436,7 @@ struct Copier {
                             : static_cast<const T*>(pool.base);
       cp_async16_zero(tile + at(grp * 32 + key, c), src, p >= 0);
     }
-    tell(bar);
-    if (lane == 0) mbar_arrive(bar);
+    pend = bar;
   }
 };
 
@@ -494,25 +493,18 @@ __device__ __forceinline__ float tree_row_exp(uint32_t cs, const uint32_t (&word
   return f2_lo(s2) + f2_hi(s2);
 }
 // The row's largest raw score alone.
-template <bool kMask>
 __device__ __forceinline__ float tree_row_max(uint32_t cs, const uint32_t (&words)[4]) {
   float m = -INFINITY;
 #pragma unroll
-  for (int c = 0; c < 8; ++c) {
-    uint32_t r[16];
-    tmem_ld16(cs + 16 * c, r);
+  for (int c = 0; c < 4; ++c) {
+    uint32_t r[32];
+    tmem_ld32(cs + 32 * c, r);
     tmem_ld_wait();
-    reg_fence16(r);
+    reg_fence32(r);
 #pragma unroll
-    for (int j = 0; j < 16; j += 2) {
-      float x0 = __uint_as_float(r[j]), x1 = __uint_as_float(r[j + 1]);
-      if (kMask) {
-        const uint32_t w = words[c >> 1] >> ((c & 1) * 16 + j);
-        x0 = (w & 1u) ? x0 : -INFINITY;
-        x1 = (w & 2u) ? x1 : -INFINITY;
-      }
-      m = fmax3(m, x0, x1);
-    }
+    for (int j = 0; j < 32; j += 2)
+      m = fmax3(m, (words[c] >> j) & 1u ? __uint_as_float(r[j]) : -INFINITY,
+                (words[c] >> j) & 2u ? __uint_as_float(r[j + 1]) : -INFINITY);
   }
   return m;
 }
@@ -622,7 +614,6 @@ __device__ __forceinline__ void tree_mma_role(const TreeArgs& a, TreeBars& bars,
       pph ^= 1;
       if (!wait(bars.v_full[vs], vph)) return false;
       if (k == 0 && segs > 0 && !wait(bars.o_free, segs - 1)) return false;
-      fence_proxy_async_smem();
       tc_fence_after();
       const uint64_t bv = dv + vs * kStage;
       const uint32_t to = tmem + S::kTmO + kDim * x, p = tmem + 128 * x, more = k > 1;
@@ -642,7 +633,6 @@ __device__ __forceinline__ void tree_mma_role(const TreeArgs& a, TreeBars& bars,
     auto issue_s = [&](int k, int x, bool waits, bool frees) -> bool {
       if (waits && !wait(bars.k_full[ks], kph)) return false;
       if (k == 0 && !wait(bars.q_full, segs)) return false;
-      fence_proxy_async_smem();
       tc_fence_after();
       const uint64_t bq = dq + (split ? 0 : x) * kStage, bk = dk + ks * kStage;
       const uint32_t to = tmem + 128 * x;
@@ -693,23 +683,23 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   if (tid == 0) {
     sh.abort = 0;
     auto init = [](uint64_t& b, uint32_t n) { mbar_init(smem_u32(&b), n); };
-    init(bars.q_full, kCopyWarps * 32);
+    init(bars.q_full, kCopyWarps);
     init(bars.q_empty, 1);
     for (int i = 0; i < kKStages; ++i) {
-      init(bars.k_full[i], kGroups * 33);
+      init(bars.k_full[i], kGroups);
       init(bars.k_empty[i], 1);
     }
     for (int i = 0; i < kVStages; ++i) {
-      init(bars.v_full[i], kGroups * 33);
+      init(bars.v_full[i], kGroups);
       init(bars.v_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       init(bars.s_full[i], 1);
-      init(bars.p_full[i], 128);
+      init(bars.p_full[i], 4);
       init(bars.o_full[i], 1);
     }
-    init(bars.o_free, 256);
-    init(bars.ml, 256);
+    init(bars.o_free, kSoftWarps);
+    init(bars.ml, kSoftWarps);
     init(bars.fin, 1);
     fence_mbar_init();
   }
@@ -748,7 +738,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   if (run < runs) {
     if (warp >= kCopyWarp0 && warp < kSoftWarp0) {
       // ---------------- copies
-      const Copier<T, kDim> copy{a, warp - kCopyWarp0, lane};
+      Copier<T, kDim> copy{a, warp - kCopyWarp0, lane, 0};
       uint32_t nt = 0, segs = 0;
       bool ok = true;
       auto wait = [&](uint64_t& bar, uint32_t ph) {
@@ -779,12 +769,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           for (int m = 0; m < kMine; ++m) {
             const int grp = copy.warp + m * kCopyWarps;
             if (grp >= kGroups) break;
+            copy.tell();
             page[m] = copy.checked(page[m]);
             const uint32_t seen = __ballot_sync(0xffffffffu, page[m] >= 0);
-            if (lane == 0) sh.there[nt & 3][grp] = seen;
+            if (lane == 0) reinterpret_cast<uint32_t*>(&sh.there[nt & 3])[grp] = seen;
             copy.keys(a.k, &map_k, walk, t, grp, page[m], sbase + S::kK + ks * S::kTile,
                       smem_u32(&bars.k_full[ks]));
           }
+          copy.tell();
           if (i == walk.i0) {
             // the queries, once all products with the ones before them are done
             if (segs > 0 && !wait(bars.q_empty, segs - 1)) { ok = false; break; }
@@ -792,22 +784,24 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             copy.queries(walk, r0, min(rows, kTileRows), sbase + S::kQ);
             if (rows > kTileRows)
               copy.queries(walk, r0 + kTileRows, rows - kTileRows, sbase + S::kQ + S::kTile);
-            copy.tell(smem_u32(&bars.q_full));
+            copy.pend = smem_u32(&bars.q_full);
+            copy.tell();
           }
           if (nt >= kVStages && !wait(bars.v_empty[vs], nt / kVStages - 1)) { ok = false; break; }
 #pragma unroll
           for (int m = 0; m < kMine; ++m) {
             const int grp = copy.warp + m * kCopyWarps;
             if (grp >= kGroups) break;
+            copy.tell();
             copy.keys(a.v, &map_v, walk, t, grp, page[m], sbase + S::kV + vs * S::kTile,
                       smem_u32(&bars.v_full[vs]));
             page[m] = page1[m];
           }
+          copy.tell();
           t = t1;
         }
         ++segs;
       } while (ok && walk.next());
-      cp_async_wait_all();
       if (!ok) {  // let tensor copies land before the CTA ends
         for (uint32_t t = nt < 2 ? 0 : nt - 2; t <= nt; ++t) {
           mbar_wait_drain(smem_u32(&bars.k_full[t % kKStages]), (t / kKStages) & 1);
@@ -830,6 +824,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         const bool split = rows <= kTileRows;
         const int32_t m = (split ? 0 : x * kTileRows) + trow;  // matrix row of the item
         const bool real = m < rows;
+        const bool used = m - lane < rows;  // a row of the warp is one
         const int32_t mr = walk.layer * kPairRows + (real ? m : 0);
         const int32_t node = mr / a.group, head = mr - node * a.group;
         const int64_t base =
@@ -846,68 +841,79 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           const int i = split ? 2 * k + x : k;
           const uint32_t t = nt + i;
           const TileKeys tk = tile_keys(a, walk, base, walk.i0 + i);
-          // the row's keys in this tile
           const bool chose = real && ((tk.who >> node) & 1);
-          const int32_t cached = chose ? min(max(walk.w.len - tk.first, 0), kBlock) : 0;
-          uint32_t words[4];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int32_t n = cached - 32 * c;
-            words[c] = n >= 32 ? 0xffffffffu : n > 0 ? (1u << n) - 1 : 0u;
-          }
-          if (tk.drafted && tk.end > walk.w.len && real) {
-            const int32_t off = walk.w.len - tk.first;  // place of drafted token 0
-            uint64_t lo, hi;
-            if (off <= 0) {
-              lo = -off < 64 ? path >> -off : 0;
-              hi = 0;
-            } else if (off < 64) {
-              lo = path << off;
-              hi = path >> (64 - off);
-            } else {
-              lo = 0;
-              hi = path << (off - 64);
-            }
-            words[0] |= uint32_t(lo);
-            words[1] |= uint32_t(lo >> 32);
-            words[2] |= uint32_t(hi);
-            words[3] |= uint32_t(hi >> 32);
-          }
           if (!mbar_wait_warp(smem_u32(&bars.k_full[t % kKStages]), (t / kKStages) & 1,
                               abort_flag) ||
               !mbar_wait_warp(smem_u32(&bars.s_full[x]), nx & 1, abort_flag)) {
             ok = false;
             break;
           }
+          ++nx;
+          if (!used) {  // no row of the warp is one: what P holds there does not matter
+            if (lane == 0) mbar_arrive(smem_u32(&bars.p_full[x]));
+            continue;
+          }
           tc_fence_after();
+          // The row's keys in this tile: where all of them are cached, all or none.
+          uint32_t words[4] = {~0u, ~0u, ~0u, ~0u};
+          bool any = chose, plain = true;
+          const uint4 there = sh.there[t & 3];
+          if (tk.first + kBlock > walk.w.len || (there.x & there.y & there.z & there.w) != ~0u) {
+            const int32_t cached = chose ? min(max(walk.w.len - tk.first, 0), kBlock) : 0;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) words[c] &= sh.there[t & 3][c];
-          const uint32_t any = words[0] | words[1] | words[2] | words[3];
-          const uint32_t all = words[0] & words[1] & words[2] & words[3];
-          // Without masks where every row of the warp sees all of the tile or none
-          // of it: the latter are zeroed afterwards.
-          const bool plain = __all_sync(0xffffffffu, all == 0xffffffffu || any == 0);
+            for (int c = 0; c < 4; ++c) {
+              const int32_t n = cached - 32 * c;
+              words[c] = n >= 32 ? ~0u : n > 0 ? (1u << n) - 1 : 0u;
+            }
+            if (tk.drafted && tk.end > walk.w.len && real) {
+              const int32_t off = walk.w.len - tk.first;  // place of drafted token 0
+              uint64_t lo, hi;
+              if (off <= 0) {
+                lo = -off < 64 ? path >> -off : 0;
+                hi = 0;
+              } else if (off < 64) {
+                lo = path << off;
+                hi = path >> (64 - off);
+              } else {
+                lo = 0;
+                hi = path << (off - 64);
+              }
+              words[0] |= uint32_t(lo);
+              words[1] |= uint32_t(lo >> 32);
+              words[2] |= uint32_t(hi);
+              words[3] |= uint32_t(hi >> 32);
+            }
+            words[0] &= there.x;
+            words[1] &= there.y;
+            words[2] &= there.z;
+            words[3] &= there.w;
+            any = (words[0] | words[1] | words[2] | words[3]) != 0;
+            const bool all = (words[0] & words[1] & words[2] & words[3]) == ~0u;
+            plain = __all_sync(0xffffffffu, all || !any);
+          }
           if (k == 0) {  // the first tile sets the reference
-            const float mx = plain ? tree_row_max<false>(cs, words) : tree_row_max<true>(cs, words);
+            const float mx = tree_row_max(cs, words);
             mref = any ? mx * a.scale_log2 - kLift<T> : -INFINITY;
           }
           uint32_t pk[64];
-          float tmax;
-          auto row_exp = [&]() {
-            if (!plain) return tree_row_exp<T, true>(cs, words, a.scale_log2, mref, pk, &tmax);
-            float l = tree_row_exp<T, false>(cs, words, a.scale_log2, mref, pk, &tmax);
-            if (any == 0) {
+          float ls;
+          for (;;) {
+            float tmax;
+            // Without masks where every row of the warp sees all of the tile or none of
+            // it: the latter are zeroed afterwards.
+            if (plain) {
+              ls = tree_row_exp<T, false>(cs, words, a.scale_log2, mref, pk, &tmax);
+              if (!any) {
 #pragma unroll
-              for (int e = 0; e < 64; ++e) pk[e] = 0u;
-              l = 0.f;
-              tmax = -INFINITY;
+                for (int e = 0; e < 64; ++e) pk[e] = 0u;
+                ls = 0.f;
+              }
+            } else {
+              ls = tree_row_exp<T, true>(cs, words, a.scale_log2, mref, pk, &tmax);
             }
-            return l;
-          };
-          float ls = row_exp();
-          const float top = tmax * a.scale_log2;
-          const bool raise = any != 0 && top > mref + (kRise + kLift<T>);
-          if (__any_sync(0xffffffffu, raise)) {
+            const float top = tmax * a.scale_log2;
+            const bool raise = any && top > mref + (kRise + kLift<T>);
+            if (!__any_sync(0xffffffffu, raise)) break;
             // O (complete up to the slot's step before) and the sum times 2^(mref -
             // the new reference), then the weights again (S is still there)
             const float to = top - kLift<T>;
@@ -926,7 +932,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 tmem_st32_nc(co + kDim * x + 32 * c, o);
               }
             }
-            ls = row_exp();
           }
           lsum += ls;
           // P over the first 64 columns of S (all of S has been read)
@@ -934,8 +939,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           tmem_st32_nc(cs + 32, *reinterpret_cast<const uint32_t(*)[32]>(&pk[32]));
           tmem_st_wait();
           tc_fence_before();
-          mbar_arrive(smem_u32(&bars.p_full[x]));
-          ++nx;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&bars.p_full[x]));
         }
         if (!ok) break;
         // ---- results.  Two states of the same rows are joined here, half of the
@@ -947,10 +952,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           // for reading)
           if (joins > 0 && !mbar_wait_warp(smem_u32(&bars.ml), 1, abort_flag)) break;
           sh.states[x][trow] = make_float2(mref, lsum);
-          mbar_arrive(smem_u32(&bars.ml));
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&bars.ml));
           if (!mbar_wait_warp(smem_u32(&bars.ml), 0, abort_flag)) break;
           const float2 s0 = sh.states[0][trow], s1 = sh.states[1][trow];
-          mbar_arrive(smem_u32(&bars.ml));
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&bars.ml));
           ++joins;
           M = fmaxf(s0.x, s1.x);
           f0 = s0.x == -INFINITY ? 0.f : fast_exp2(s0.x - M);
@@ -999,7 +1006,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           }
         }
         tc_fence_before();
-        mbar_arrive(smem_u32(&bars.o_free));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars.o_free));
         if (real && (!split || x == 0)) {
           if (whole)
             a.lse[orow] = l == 0.f ? -INFINITY : kLn2 * (M + log2f(l));
