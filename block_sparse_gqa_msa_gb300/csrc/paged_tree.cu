@@ -20,7 +20,7 @@
 //
 // Tiles.  A CTA holds two query tiles of 128 rows (slots A and B) against one
 // stream of key tiles, so that one slot's softmax runs while the tensor cores
-// work for the other: S_A, then P_B V of the step before, S_B, P_A V.  A row
+// work for the other: S, softmax, P V and the next S, by turns.  A row
 // with more than 256 matrix rows is several such items.  With 128 rows or fewer
 // slot B takes the same queries and every other key tile, and the two states
 // are joined in tensor memory's lanes at the end; the order of operations is the
@@ -33,7 +33,7 @@
 // once.  An item within one run is finished there; otherwise each run leaves its
 // (m, l, O) in the workspace and k_paged_tree_join adds them up, in order.
 //
-// Three warps fetch keys and values, three tiles of keys and two of values ahead,
+// Two warps fetch keys and values, three tiles of keys and two of values ahead,
 // into the swizzled layout that the tensor cores read, in groups of 32 keys of a
 // tile.  Where all 32 of a group are there and lie in pages of 8 tokens or more, by tensor
 // copies of up to 32 tokens of a page; else by copies of 16 bytes, which take pages
@@ -55,13 +55,12 @@ constexpr int kNodes = 64;         // drafted tokens of a row
 constexpr int kPairRows = 256;     // matrix rows of an item
 constexpr int kTileRows = 128;
 constexpr int kMaxRuns = 160;      // CTAs: no GB300 has more SMs
-// Three copying warps for four groups of 32 keys: with a fourth, 13 warps, a
-// thread would have 128 registers, and the softmax's would not do.
-constexpr int kSoftWarps = 8, kCopyWarps = 3, kGroups = 4;
-constexpr int kTreeThreads = (kSoftWarps + kCopyWarps + 1) * 32;
-// Warp 0 issues the products and the copying warps follow: a scheduler that has the
-// choice takes the lowest warp, and these have little to do but are waited for.
-constexpr int kCopyWarp0 = 1, kSoftWarp0 = 1 + kCopyWarps;
+// Warps: one a slot that issues products, two that copy, four groups of 32 keys a
+// tile between them, four a slot for the softmax.  (With more than 12 a thread would
+// have 128 registers, and the softmax's would not do.)
+constexpr int kSoftWarps = 8, kCopyWarps = 2, kGroups = 4;
+constexpr int kCopyWarp0 = 2, kSoftWarp0 = kCopyWarp0 + kCopyWarps;
+constexpr int kTreeThreads = (kSoftWarp0 + kSoftWarps) * 32;
 constexpr int kKStages = 3, kVStages = 2;
 constexpr float kRise = 8.f;       // and kLift: as in paged_decode.cu
 template <typename T>
@@ -315,7 +314,7 @@ struct TreeWalk {
 // ------------------------------------------------------------ the main kernel
 struct TreeBars {
   uint64_t q_full, q_empty, k_full[kKStages], k_empty[kKStages], v_full[kVStages],
-      v_empty[kVStages], s_full[2], p_full[2], o_full[2], o_free, ml, fin;
+      v_empty[kVStages], s_full[2], p_full[2], o_full[2], o_free, ml, fin[2];
 };
 struct TreeShared {
   TreeBars bars;
@@ -583,11 +582,14 @@ __device__ __forceinline__ void commit_one(uint32_t one, uint32_t bar) {
       : "memory");
 }
 
-// The tensor cores' side, one warp.  Step k works for slot k & 1: S of step k,
-// then P V of step k - 1.
+// The tensor cores' side of slot x, one warp: S of its first key tile, then P V of a
+// tile and S of its next one.  Issuing waits for the tensor cores, and a wait for a
+// barrier that is there already takes 100 cycles: with one warp for both slots the
+// tensor cores had nothing to do for half of the time, with one each they work for
+// one slot while the other's warp waits.
 template <typename T, int kDim>
 __device__ __forceinline__ void tree_mma_role(const TreeArgs& a, TreeBars& bars, TreeWalk& walk,
-                                              uint32_t tmem, uint32_t sbase,
+                                              int x, uint32_t tmem, uint32_t sbase,
                                               volatile int* abort_flag) {
   using S = TreeShape<kDim>;
   constexpr bool kBf = kLift<T> == 0.f;
@@ -601,67 +603,60 @@ __device__ __forceinline__ void tree_mma_role(const TreeArgs& a, TreeBars& bars,
   const uint64_t dk = sdesc_sw128(sbase + S::kK, 16u, 1024u);
   const uint64_t dv = sdesc_sw128(sbase + S::kV, 16384u, 1024u);
   constexpr uint64_t kStage = S::kTile >> 4;
-  uint32_t ks = 0, kph = 0, vs = 0, vph = 0;  // stages and phases of keys and of values
-  uint32_t pph0 = 0, pph1 = 0, segs = 0;
+  const uint32_t to_s = tmem + 128 * x, to_o = tmem + S::kTmO + kDim * x;
+  uint32_t nt = 0, np = 0, segs = 0;  // tiles, this slot's P V, segments
   bool ok = true;
   do {
     const bool split = walk.rows_here() <= kTileRows;
-    const int tiles = walk.i1 - walk.i0, steps = split ? tiles : 2 * tiles;
-    // P V of step k: slot x, the last with its values where `frees`
-    auto issue_pv = [&](int k, int x, bool frees) -> bool {
-      uint32_t& pph = x ? pph1 : pph0;
-      if (!wait(bars.p_full[x], pph)) return false;
-      pph ^= 1;
-      if (!wait(bars.v_full[vs], vph)) return false;
-      if (k == 0 && segs > 0 && !wait(bars.o_free, segs - 1)) return false;
-      tc_fence_after();
-      const uint64_t bv = dv + vs * kStage;
-      const uint32_t to = tmem + S::kTmO + kDim * x, p = tmem + 128 * x, more = k > 1;
-#pragma unroll
-      for (int kk = 0; kk < 8; ++kk)
-        mma_ts_one(one, to, p + kk * 8, bv + uint64_t(kk) * 128u, idPV, kk > 0 ? 1u : more);
-      if (frees) {
-        commit_one(one, smem_u32(&bars.v_empty[vs]));
-        if (++vs == kVStages) {
-          vs = 0;
-          vph ^= 1;
-        }
-      }
-      if (k + 2 >= steps) commit_one(one, smem_u32(&bars.o_full[x]));
-      return true;
+    const int tiles = walk.i1 - walk.i0;
+    const int step = split ? 2 : 1, first = split ? x : 0;  // the slot's tiles
+    const uint64_t bq = dq + (split ? 0 : x) * kStage;
+    // a tile's barrier counts both slots; in a tile of one slot that one counts twice
+    auto release = [&](uint64_t& bar) {
+      commit_one(one, smem_u32(&bar));
+      if (split) commit_one(one, smem_u32(&bar));
     };
-    auto issue_s = [&](int k, int x, bool waits, bool frees) -> bool {
-      if (waits && !wait(bars.k_full[ks], kph)) return false;
-      if (k == 0 && !wait(bars.q_full, segs)) return false;
+    auto issue_s = [&](int i) -> bool {
+      const uint32_t t = nt + i, stg = t % kKStages;
+      if (!wait(bars.k_full[stg], t / kKStages)) return false;
       tc_fence_after();
-      const uint64_t bq = dq + (split ? 0 : x) * kStage, bk = dk + ks * kStage;
-      const uint32_t to = tmem + 128 * x;
+      const uint64_t bk = dk + stg * kStage;
 #pragma unroll
       for (int kk = 0; kk < kDim / 16; ++kk) {
         const uint64_t off = uint64_t((kk >> 2) * 1024 + (kk & 3) * 2);
-        mma_ss_one(one, to, bq + off, bk + off, idS, kk > 0);
+        mma_ss_one(one, to_s, bq + off, bk + off, idS, kk > 0);
       }
       commit_one(one, smem_u32(&bars.s_full[x]));
-      if (frees) {
-        commit_one(one, smem_u32(&bars.k_empty[ks]));
-        if (++ks == kKStages) {
-          ks = 0;
-          kph ^= 1;
-        }
-      }
-      if (k + 1 == steps) commit_one(one, smem_u32(&bars.q_empty));
+      release(bars.k_empty[stg]);
       return true;
     };
-    for (int k = 0; ok && k < steps; ++k) {
-      const int x = k & 1;
-      ok = issue_s(k, x, split || x == 0, split || x == 1) &&
-           (k == 0 || issue_pv(k - 1, x ^ 1, split || x == 0));
+    ok = wait(bars.q_full, segs);
+    if (ok && first < tiles) ok = issue_s(first);
+    for (int i = first; ok && i < tiles; i += step) {
+      const uint32_t t = nt + i, stg = t % kVStages;
+      if (i == first && segs > 0 && !wait(bars.o_free, segs - 1)) { ok = false; break; }
+      if (!wait(bars.v_full[stg], t / kVStages) || !wait(bars.p_full[x], np)) { ok = false; break; }
+      ++np;
+      tc_fence_after();
+      const uint64_t bv = dv + stg * kStage;
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk)
+        mma_ts_one(one, to_o, to_s + kk * 8, bv + uint64_t(kk) * 128u, idPV,
+                   (kk > 0 || i > first) ? 1u : 0u);
+      release(bars.v_empty[stg]);
+      // (products of one thread run in order: S may overwrite P)
+      if (i + step < tiles)
+        ok = issue_s(i + step);
+      else
+        commit_one(one, smem_u32(&bars.o_full[x]));
     }
-    ok = ok && issue_pv(steps - 1, (steps - 1) & 1, true);
+    // this slot is done with the queries
+    commit_one(one, smem_u32(&bars.q_empty));
+    nt += tiles;
     ++segs;
   } while (ok && walk.next());
-  commit_one(one, smem_u32(&bars.fin));
-  mbar_wait_drain(smem_u32(&bars.fin), 0);
+  commit_one(one, smem_u32(&bars.fin[x]));
+  mbar_wait_drain(smem_u32(&bars.fin[x]), 0);
 }
 
 template <typename T, int kDim>
@@ -684,23 +679,23 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     sh.abort = 0;
     auto init = [](uint64_t& b, uint32_t n) { mbar_init(smem_u32(&b), n); };
     init(bars.q_full, kCopyWarps);
-    init(bars.q_empty, 1);
+    init(bars.q_empty, 2);
     for (int i = 0; i < kKStages; ++i) {
       init(bars.k_full[i], kGroups);
-      init(bars.k_empty[i], 1);
+      init(bars.k_empty[i], 2);
     }
     for (int i = 0; i < kVStages; ++i) {
       init(bars.v_full[i], kGroups);
-      init(bars.v_empty[i], 1);
+      init(bars.v_empty[i], 2);
     }
     for (int i = 0; i < 2; ++i) {
       init(bars.s_full[i], 1);
       init(bars.p_full[i], 4);
       init(bars.o_full[i], 1);
+      init(bars.fin[i], 1);
     }
     init(bars.o_free, kSoftWarps);
     init(bars.ml, kSoftWarps);
-    init(bars.fin, 1);
     fence_mbar_init();
   }
   if (warp == 0) {
@@ -808,9 +803,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           mbar_wait_drain(smem_u32(&bars.v_full[t % kVStages]), (t / kVStages) & 1);
         }
       }
-    } else if (warp == 0) {
+    } else if (warp < kCopyWarp0) {
       // ---------------- tensor cores
-      tree_mma_role<T, kDim>(a, bars, walk, tmem, sbase, abort_flag);
+      tree_mma_role<T, kDim>(a, bars, walk, warp, tmem, sbase, abort_flag);
     } else {
       // ---------------- softmax and results of slot x (warps 4-7: A, 8-11: B)
       const int x = (warp - kSoftWarp0) >> 2, quad = warp & 3;
