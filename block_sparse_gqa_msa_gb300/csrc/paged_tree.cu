@@ -351,8 +351,13 @@ __device__ __forceinline__ TileKeys tile_keys(const TreeArgs& a, const TreeWalk&
   return TileKeys{f, min(f + kBlock, s.w.len), false, a.who[base + i]};
 }
 
-// The copying warps' side: fills query, key and value tiles; each copy's landing
-// counts on the tile's barrier.
+// Offset of 16 bytes of a row in a tile that the tensor cores read.
+__device__ __forceinline__ uint32_t tile_at(int row, int chunk) {
+  return (chunk >> 3) * 16384u + row * 128u + (((chunk & 7) ^ (row & 7)) << 4);
+}
+
+// The copying warps' side: fills key and value tiles; each copy's landing counts on
+// the tile's barrier.
 template <typename T, int kDim>
 struct Copier {
   using S = TreeShape<kDim>;
@@ -371,27 +376,6 @@ struct Copier {
     __syncwarp();
     if (lane == 0) mbar_arrive(pend);
     pend = 0;
-  }
-  static __device__ __forceinline__ uint32_t at(int row, int chunk) {
-    return (chunk >> 3) * 16384u + row * 128u + (((chunk & 7) ^ (row & 7)) << 4);
-  }
-  // 128 rows of queries from matrix row r0 of the item's row on.
-  __device__ __forceinline__ void queries(const TreeWalk& s, int32_t r0, int32_t rows,
-                                          uint32_t tile) const {
-    const int sub = lane / kChunks, c = lane % kChunks;
-    const int64_t width = int64_t(a.kv_heads) * a.group * kDim;
-    const T* q = static_cast<const T*>(a.q) + s.w.t0 * width + int64_t(s.g) * a.group * kDim +
-                 c * 8;
-#pragma unroll 4
-    for (int x = warp; x < kTileRows / kAtOnce; x += kCopyWarps) {
-      const int r = x * kAtOnce + sub;
-      const int32_t m = r0 + r, node = m / a.group;
-      const bool real = r < rows;
-      cp_async16_zero(tile + at(r, c),
-                      real ? q + node * width + (m - node * a.group) * kDim
-                           : static_cast<const T*>(a.q),
-                      real);
-    }
   }
   // The pages of the keys of a tile's group, a lane each, as the table has them
   // (kNoKey: no such key).
@@ -433,7 +417,7 @@ struct Copier {
       const int32_t slot = (j0 + key) & mask;
       const T* src = p >= 0 ? base + p * pool.page + slot * pool.token
                             : static_cast<const T*>(pool.base);
-      cp_async16_zero(tile + at(grp * 32 + key, c), src, p >= 0);
+      cp_async16_zero(tile + tile_at(grp * 32 + key, c), src, p >= 0);
     }
     pend = bar;
   }
@@ -678,7 +662,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   if (tid == 0) {
     sh.abort = 0;
     auto init = [](uint64_t& b, uint32_t n) { mbar_init(smem_u32(&b), n); };
-    init(bars.q_full, kCopyWarps);
+    init(bars.q_full, kSoftWarps);
     init(bars.q_empty, 2);
     for (int i = 0; i < kKStages; ++i) {
       init(bars.k_full[i], kGroups);
@@ -734,13 +718,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     if (warp >= kCopyWarp0 && warp < kSoftWarp0) {
       // ---------------- copies
       Copier<T, kDim> copy{a, warp - kCopyWarp0, lane, 0};
-      uint32_t nt = 0, segs = 0;
+      uint32_t nt = 0;
       bool ok = true;
       auto wait = [&](uint64_t& bar, uint32_t ph) {
         return mbar_wait_warp(smem_u32(&bar), ph & 1, abort_flag);
       };
       do {
-        const int32_t rows = walk.rows_here();
         const int64_t base =
             a.q2k ? list_base(a, walk.row, walk.layer, walk.g, walk.w.t0) : 0;
         constexpr int kMine = Copier<T, kDim>::kMine;
@@ -772,16 +755,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                       smem_u32(&bars.k_full[ks]));
           }
           copy.tell();
-          if (i == walk.i0) {
-            // the queries, once all products with the ones before them are done
-            if (segs > 0 && !wait(bars.q_empty, segs - 1)) { ok = false; break; }
-            const int32_t r0 = walk.layer * kPairRows;
-            copy.queries(walk, r0, min(rows, kTileRows), sbase + S::kQ);
-            if (rows > kTileRows)
-              copy.queries(walk, r0 + kTileRows, rows - kTileRows, sbase + S::kQ + S::kTile);
-            copy.pend = smem_u32(&bars.q_full);
-            copy.tell();
-          }
           if (nt >= kVStages && !wait(bars.v_empty[vs], nt / kVStages - 1)) { ok = false; break; }
 #pragma unroll
           for (int m = 0; m < kMine; ++m) {
@@ -795,7 +768,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           copy.tell();
           t = t1;
         }
-        ++segs;
       } while (ok && walk.next());
       if (!ok) {  // let tensor copies land before the CTA ends
         for (uint32_t t = nt < 2 ? 0 : nt - 2; t <= nt; ++t) {
@@ -813,7 +785,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       const uint32_t lane_base = uint32_t(quad * 32) << 16;
       const uint32_t cs = tmem + lane_base + 128 * x;
       const uint32_t co = tmem + lane_base + S::kTmO;
-      uint32_t nt = 0, nx = 0, joins = 0, no[2] = {0, 0};
+      uint32_t nt = 0, nx = 0, segs = 0, joins = 0, no[2] = {0, 0};
       do {
         const int32_t rows = walk.rows_here();
         const bool split = rows <= kTileRows;
@@ -826,12 +798,34 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             a.q2k ? list_base(a, walk.row, walk.layer, walk.g, walk.w.t0) : 0;
         const int tiles = walk.i1 - walk.i0;
         const int steps = split ? (tiles + 1 - x) / 2 : tiles;
+        bool ok = true;
+        // The queries, once the products with the ones before them are done: each warp
+        // its own rows of its slot's tile, or half of them where both slots have one.
+        if (segs > 0) ok = mbar_wait_warp(smem_u32(&bars.q_empty), (segs - 1) & 1, abort_flag);
+        ++segs;
+        if (!ok) break;
+        const int32_t qrow = (walk.w.t0 + node) * (a.kv_heads * a.group) + walk.g * a.group + head;
+        {
+          constexpr int kChunks = kDim / 8, kAtOnce = 32 / kChunks;
+          const int sub = lane / kChunks, c = lane % kChunks;
+          const uint32_t tile = sbase + S::kQ + (split ? 0 : x) * S::kTile;
+          const T* q = static_cast<const T*>(a.q) + c * 8;
+#pragma unroll 4
+          for (int i = split ? x * 16 : 0; i < (split ? x * 16 + 16 : 32); i += kAtOnce) {
+            const int32_t from = __shfl_sync(0xffffffffu, real ? qrow : -1, i + sub);
+            cp_async16_zero(tile + tile_at(quad * 32 + i + sub, c),
+                            q + int64_t(max(from, 0)) * kDim, from >= 0);
+          }
+          asm volatile("cp.async.wait_all;" ::: "memory");
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&bars.q_full));
+        }
         uint64_t path = 0;
         // (does the segment reach the drafted tokens?)
         if (a.q2k ? walk.i1 == walk.tiles : int64_t(walk.i1) * kBlock > walk.w.len)
           path = path_of(a, walk.w, node);
         float mref = -INFINITY, lsum = 0.f;
-        bool ok = true;
         for (int k = 0; k < steps; ++k) {
           const int i = split ? 2 * k + x : k;
           const uint32_t t = nt + i;
@@ -967,8 +961,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         tc_fence_after();
         const bool whole = walk.i0 == 0 && walk.i1 == walk.tiles;
         const int64_t part = (2 * int64_t(run) + (walk.i0 > 0 ? 0 : 1)) * kPairRows + m;
-        const int64_t orow =
-            (int64_t(walk.w.t0) + node) * (a.kv_heads * a.group) + walk.g * a.group + head;
+        const int64_t orow = qrow;
         const float inv = l == 0.f ? 0.f : 1.f / l;  // l == 0: no key was seen
         const int c0 = split ? x * (kDim / 2) : 0, c1 = split ? c0 + kDim / 2 : kDim;
 #pragma unroll 1
