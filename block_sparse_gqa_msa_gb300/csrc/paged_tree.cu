@@ -33,13 +33,12 @@
 // once.  An item within one run is finished there; otherwise each run leaves its
 // (m, l, O) in the workspace and k_paged_tree_join adds them up, in order.
 //
-// Two warps fetch keys and values, three tiles of keys and two of values ahead,
-// into the swizzled layout that the tensor cores read, in groups of 32 keys of a
-// tile.  Where all 32 of a group are there and lie in pages of 8 tokens or more, by tensor
-// copies of up to 32 tokens of a page; else by copies of 16 bytes, which take pages
-// of any size and write zeros for keys that are not there (what lies behind a
-// row's end may be anything, and 0 times it must be 0).  The latter alone, 128
-// instructions a tile, kept the tensor cores waiting two thirds of the time.
+// One warp fetches keys, three tiles ahead, one values, two tiles ahead, into the
+// swizzled layout that the tensor cores read: from pages of 8 tokens or more by
+// tensor copies of up to 64 tokens of a page, a lane each; from smaller pages by
+// copies of 16 bytes.  What lies behind a row's end may be anything: as a key it
+// gives a score that a mask drops, as a value it would meet a weight of 0, so value
+// rows that are not there are zeroed.
 //
 // With q2k a first kernel (k_paged_tree_lists) makes, for each item, the list of
 // the blocks that any of its tokens chose, and which tokens did.
@@ -55,10 +54,10 @@ constexpr int kNodes = 64;         // drafted tokens of a row
 constexpr int kPairRows = 256;     // matrix rows of an item
 constexpr int kTileRows = 128;
 constexpr int kMaxRuns = 160;      // CTAs: no GB300 has more SMs
-// Warps: one a slot that issues products, two that copy, four groups of 32 keys a
-// tile between them, four a slot for the softmax.  (With more than 12 a thread would
-// have 128 registers, and the softmax's would not do.)
-constexpr int kSoftWarps = 8, kCopyWarps = 2, kGroups = 4;
+// Warps: one a slot that issues products, one that copies keys, one for values, four
+// a slot for the softmax.  (With more than 12 a thread would have 128 registers, and
+// the softmax's would not do.)
+constexpr int kSoftWarps = 8, kCopyWarps = 2;
 constexpr int kCopyWarp0 = 2, kSoftWarp0 = kCopyWarp0 + kCopyWarps;
 constexpr int kTreeThreads = (kSoftWarp0 + kSoftWarps) * 32;
 constexpr int kKStages = 3, kVStages = 2;
@@ -86,7 +85,7 @@ struct TreeArgs {
   uint64_t* who;        // q2k: the tokens that chose them
   float* part_ml;       // [2 runs][256][2]: m, l
   float* part_o;        // [2 runs][256][dim]
-  int32_t box;          // tokens of a tensor copy, 0: none are used
+  int32_t box;          // tokens of a tensor copy (a power of two), 0: none are used
 };
 
 template <int kDim>
@@ -314,11 +313,13 @@ struct TreeWalk {
 // ------------------------------------------------------------ the main kernel
 struct TreeBars {
   uint64_t q_full, q_empty, k_full[kKStages], k_empty[kKStages], v_full[kVStages],
-      v_empty[kVStages], s_full[2], p_full[2], o_full[2], o_free, ml, fin[2];
+      v_empty[kVStages], s_full[2], p_full[2], o_full[2], o_free, ml, part, fin[2];
 };
 struct TreeShared {
   TreeBars bars;
-  uint4 there[4];               // keys of a tile that are there; a ring of 4 tiles
+  // Keys of a tile whose pages are there.  A ring of 8 tiles: keys are four tiles ahead
+  // of a slot's softmax at most.
+  uint4 there[8];
   float2 states[2][kTileRows];    // (m, l) of the slots, where they are joined
   uint32_t tmem_base;
   int abort;
@@ -346,7 +347,8 @@ __device__ __forceinline__ TileKeys tile_keys(const TreeArgs& a, const TreeWalk&
     const int32_t f = i * kBlock;
     return TileKeys{f, min(f + kBlock, s.w.len + s.w.n), true, ~0ull};
   }
-  if (i + 1 == s.tiles) return TileKeys{s.w.len, s.w.len + s.w.n, true, 0ull};
+  if (i + 1 == s.tiles)  // (aligned for the copies: cached keys in it are masked)
+    return TileKeys{s.w.len & -max(a.box, 1), s.w.len + s.w.n, true, 0ull};
   const int32_t f = a.ids[base + i] * kBlock;
   return TileKeys{f, min(f + kBlock, s.w.len), false, a.who[base + i]};
 }
@@ -356,70 +358,108 @@ __device__ __forceinline__ uint32_t tile_at(int row, int chunk) {
   return (chunk >> 3) * 16384u + row * 128u + (((chunk & 7) ^ (row & 7)) << 4);
 }
 
-// The copying warps' side: fills key and value tiles; each copy's landing counts on
-// the tile's barrier.
+// The copying warps' side, of keys or of values.
 template <typename T, int kDim>
 struct Copier {
   using S = TreeShape<kDim>;
-  static constexpr int kChunks = kDim / 8;
-  static constexpr int kAtOnce = 32 / kChunks;  // rows that one copy instruction covers
-  static constexpr int kMine = (kGroups + kCopyWarps - 1) / kCopyWarps;  // groups of a warp
+  static constexpr int kHalves = kDim / 64;  // tensor copies of a box
   const TreeArgs& a;
-  int warp, lane;                 // of the copying warps
+  const PagedPool& pool;
+  const CUtensorMap* map;
+  bool values;
+  int lane;
 
-  uint32_t pend;                  // barrier of 16-byte copies not told of yet, or 0
-  // Tells of them, once they have landed: before the warp waits for anything else.
-  __device__ __forceinline__ void tell() {
-    if (pend == 0) return;
+  // With boxes: the page of the lane's box of a tile, as the table has it (kNoKey: none
+  // of its keys are in the row).  Else of key 32 grp + lane.
+  static constexpr int32_t kNoKey = INT32_MIN;
+  __device__ __forceinline__ int32_t page(const TreeWalk& s, const TileKeys& t, int grp) const {
+    const int32_t at = a.box > 0 ? lane / kHalves * a.box : 32 * grp + lane;
+    if (at >= kBlock || t.first + at >= t.end) return kNoKey;
+    return max(a.table.pages[int64_t(s.row) * a.table.stride + ((t.first + at) >> a.table.shift)],
+               -1);
+  }
+  __device__ __forceinline__ int32_t checked(int32_t p) const {
+    if (p >= 0 && p < a.table.num_pages) return p;
+    if (p != kNoKey && !values) raise_paged(a.table.status, MSA_ERR_BAD_PAGE);
+    return p == kNoKey ? kNoKey : -1;
+  }
+  // Zeros into rows r0 .. r1 - 1 of a tile.
+  __device__ __forceinline__ void zero(uint32_t tile, int r0, int r1) const {
+    constexpr int kChunks = kDim / 8;
+    for (int i = r0 * kChunks + lane; i < r1 * kChunks; i += 32)
+      st_shared_v4(tile + tile_at(i / kChunks, i % kChunks), 0, 0, 0, 0);
+  }
+  // Fills a tile and has its barrier told when all of it has landed; false: a wait gave
+  // up.  p: the lane's page; there: of keys, the mask of those that are.
+  __device__ __forceinline__ bool fill(const TreeWalk& s, const TileKeys& t, int32_t p,
+                                       uint32_t tile, uint32_t bar, uint4* there, uint64_t& part,
+                                       uint32_t& parts, volatile int* abort_flag) const {
+    const int32_t mask = (1 << a.table.shift) - 1;
+    if (a.box > 0) {
+      p = checked(p);
+      const bool bad = __any_sync(0xffffffffu, p == -1);
+      const bool mine = p >= 0;
+      const int boxes = __popc(__ballot_sync(0xffffffffu, mine)) / kHalves;
+      // values of a tile that is not whole: the rest is zeroed before it is told of
+      const bool rest = values && (t.end - t.first < kBlock || bad);
+      const uint32_t to = rest ? smem_u32(&part) : bar;
+      if (!values && lane == 0) *there = make_uint4(~0u, ~0u, ~0u, ~0u);
+      if (!values && bad) {
+        __syncwarp();
+        if (p == -1 && lane % kHalves == 0)
+          for (int k = lane / kHalves * a.box, e = k + a.box; k < e; ++k)
+            atomicAnd(reinterpret_cast<uint32_t*>(there) + k / 32, ~(1u << (k % 32)));
+        __syncwarp();
+      }
+      if (lane == 0) {
+        if (boxes > 0)
+          mbar_arrive_expect_tx(to, uint32_t(boxes * a.box) * kDim * 2);
+        else
+          mbar_arrive(to);
+      }
+      __syncwarp();
+      const int b = lane / kHalves * a.box, half = lane % kHalves;
+      if (mine)
+        tma_load_4d(tile + half * 16384u + b * 128u, map, to, half * 64, s.g, (t.first + b) & mask,
+                    p);
+      if (rest) {
+        if (!mbar_wait_warp(to, parts++ & 1, abort_flag)) return false;
+        if (bad) {
+          for (int l = 0; l < 32; l += kHalves)
+            if (__shfl_sync(0xffffffffu, p, l) == -1)
+              zero(tile, l / kHalves * a.box, (l / kHalves + 1) * a.box);
+        }
+        zero(tile, t.end - t.first, kBlock);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar);
+      }
+      return true;
+    }
+    constexpr int kChunks = kDim / 8, kAtOnce = 32 / kChunks;
+    const int sub = lane / kChunks, c = lane % kChunks;
+    const T* base = static_cast<const T*>(pool.base) + s.g * pool.head + c * 8;
+    for (int grp = 0; grp < kBlock / 32; ++grp) {
+      if (grp > 0) p = page(s, t, grp);
+      p = checked(p);
+      const uint32_t lost = __ballot_sync(0xffffffffu, p == -1);
+      if (!values && lane == 0) reinterpret_cast<uint32_t*>(there)[grp] = ~lost;
+#pragma unroll 4
+      for (int x = 0; x < 32 / kAtOnce; ++x) {
+        const int key = x * kAtOnce + sub;
+        const int32_t pg = __shfl_sync(0xffffffffu, p, key);
+        const int32_t slot = (t.first + 32 * grp + key) & mask;
+        cp_async16_zero(tile + tile_at(32 * grp + key, c),
+                        pg >= 0 ? base + pg * pool.page + slot * pool.token
+                                : static_cast<const T*>(pool.base),
+                        pg >= 0);
+      }
+    }
     asm volatile("cp.async.wait_all;" ::: "memory");
     fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0) mbar_arrive(pend);
-    pend = 0;
-  }
-  // The pages of the keys of a tile's group, a lane each, as the table has them
-  // (kNoKey: no such key).
-  static constexpr int32_t kNoKey = INT32_MIN;
-  __device__ __forceinline__ int32_t pages(const TreeWalk& s, const TileKeys& t, int grp) const {
-    const int32_t j = t.first + grp * 32 + lane;
-    if (grp >= kGroups || j >= t.end) return kNoKey;
-    return max(a.table.pages[int64_t(s.row) * a.table.stride + (j >> a.table.shift)], -1);
-  }
-  // Such a page, or -1: there is no key.
-  __device__ __forceinline__ int32_t checked(int32_t p) const {
-    if (p >= 0 && p < a.table.num_pages) return p;
-    if (p != kNoKey) raise_paged(a.table.status, MSA_ERR_BAD_PAGE);
-    return -1;
-  }
-  // Starts the copies of a group of 32 keys (or values) into a tile; its barrier
-  // counts once for the group.
-  __device__ __forceinline__ void keys(const PagedPool& pool, const CUtensorMap* map,
-                                       const TreeWalk& s, const TileKeys& t, int grp,
-                                       int32_t page, uint32_t tile, uint32_t bar) {
-    const int32_t mask = (1 << a.table.shift) - 1, j0 = t.first + grp * 32;
-    if (a.box > 0 && (j0 & (a.box - 1)) == 0 && __all_sync(0xffffffffu, page >= 0)) {
-      constexpr int kHalves = kDim / 64;
-      const int b = lane / kHalves * a.box, half = lane % kHalves;  // the lane's box
-      const int32_t p = __shfl_sync(0xffffffffu, page, b & 31);
-      if (lane == 0) mbar_arrive_expect_tx(bar, 32 * kDim * 2);
-      __syncwarp();
-      if (b < 32)
-        tma_load_4d(tile + half * 16384u + (grp * 32 + b) * 128u, map, bar, half * 64, s.g,
-                    (j0 + b) & mask, p);
-      return;
-    }
-    const int sub = lane / kChunks, c = lane % kChunks;
-    const T* base = static_cast<const T*>(pool.base) + s.g * pool.head + c * 8;
-#pragma unroll 4
-    for (int x = 0; x < 32 / kAtOnce; ++x) {
-      const int key = x * kAtOnce + sub;
-      const int32_t p = __shfl_sync(0xffffffffu, page, key);
-      const int32_t slot = (j0 + key) & mask;
-      const T* src = p >= 0 ? base + p * pool.page + slot * pool.token
-                            : static_cast<const T*>(pool.base);
-      cp_async16_zero(tile + tile_at(grp * 32 + key, c), src, p >= 0);
-    }
-    pend = bar;
+    if (lane == 0) mbar_arrive(bar);
+    return true;
   }
 };
 
@@ -665,11 +705,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     init(bars.q_full, kSoftWarps);
     init(bars.q_empty, 2);
     for (int i = 0; i < kKStages; ++i) {
-      init(bars.k_full[i], kGroups);
+      init(bars.k_full[i], 1);
       init(bars.k_empty[i], 2);
     }
     for (int i = 0; i < kVStages; ++i) {
-      init(bars.v_full[i], kGroups);
+      init(bars.v_full[i], 1);
       init(bars.v_empty[i], 2);
     }
     for (int i = 0; i < 2; ++i) {
@@ -680,6 +720,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     }
     init(bars.o_free, kSoftWarps);
     init(bars.ml, kSoftWarps);
+    init(bars.part, 1);
     fence_mbar_init();
   }
   if (warp == 0) {
@@ -716,63 +757,45 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   __syncthreads();  // the prefix is read
   if (run < runs) {
     if (warp >= kCopyWarp0 && warp < kSoftWarp0) {
-      // ---------------- copies
-      Copier<T, kDim> copy{a, warp - kCopyWarp0, lane, 0};
-      uint32_t nt = 0;
+      // ---------------- copies: one warp keys, one values
+      const bool values = warp != kCopyWarp0;
+      const Copier<T, kDim> copy{a, values ? a.v : a.k, values ? &map_v : &map_k, values, lane};
+      const uint32_t stages = values ? kVStages : kKStages;
+      uint64_t* const full = values ? bars.v_full : bars.k_full;
+      uint64_t* const empty = values ? bars.v_empty : bars.k_empty;
+      const uint32_t tiles_at = sbase + (values ? S::kV : S::kK);
+      uint32_t nt = 0, stage = 0, round = 0, parts = 0;
       bool ok = true;
-      auto wait = [&](uint64_t& bar, uint32_t ph) {
-        return mbar_wait_warp(smem_u32(&bar), ph & 1, abort_flag);
-      };
       do {
         const int64_t base =
             a.q2k ? list_base(a, walk.row, walk.layer, walk.g, walk.w.t0) : 0;
-        constexpr int kMine = Copier<T, kDim>::kMine;
         TileKeys t = tile_keys(a, walk, base, walk.i0);
-        int32_t page[kMine];
-#pragma unroll
-        for (int m = 0; m < kMine; ++m) page[m] = copy.pages(walk, t, copy.warp + m * kCopyWarps);
-        for (int32_t i = walk.i0; ok && i < walk.i1; ++i, ++nt) {
-          // the pages of the next tile, while this one's copies are started
+        int32_t page = copy.page(walk, t, 0);
+        for (int32_t i = walk.i0; i < walk.i1; ++i, ++nt) {
+          // the pages of the next tile, while this one is waited for
           TileKeys t1 = t;
-          int32_t page1[kMine] = {};
+          int32_t page1 = 0;
           if (i + 1 < walk.i1) {
             t1 = tile_keys(a, walk, base, i + 1);
-#pragma unroll
-            for (int m = 0; m < kMine; ++m)
-              page1[m] = copy.pages(walk, t1, copy.warp + m * kCopyWarps);
+            page1 = copy.page(walk, t1, 0);
           }
-          const uint32_t ks = nt % kKStages, vs = nt % kVStages;
-          if (nt >= kKStages && !wait(bars.k_empty[ks], nt / kKStages - 1)) { ok = false; break; }
-#pragma unroll
-          for (int m = 0; m < kMine; ++m) {
-            const int grp = copy.warp + m * kCopyWarps;
-            if (grp >= kGroups) break;
-            copy.tell();
-            page[m] = copy.checked(page[m]);
-            const uint32_t seen = __ballot_sync(0xffffffffu, page[m] >= 0);
-            if (lane == 0) reinterpret_cast<uint32_t*>(&sh.there[nt & 3])[grp] = seen;
-            copy.keys(a.k, &map_k, walk, t, grp, page[m], sbase + S::kK + ks * S::kTile,
-                      smem_u32(&bars.k_full[ks]));
+          ok = (round == 0 ||
+                mbar_wait_warp(smem_u32(&empty[stage]), (round - 1) & 1, abort_flag)) &&
+               copy.fill(walk, t, page, tiles_at + stage * S::kTile, smem_u32(&full[stage]),
+                         &sh.there[nt & 7], bars.part, parts, abort_flag);
+          if (!ok) break;
+          if (++stage == stages) {
+            stage = 0;
+            ++round;
           }
-          copy.tell();
-          if (nt >= kVStages && !wait(bars.v_empty[vs], nt / kVStages - 1)) { ok = false; break; }
-#pragma unroll
-          for (int m = 0; m < kMine; ++m) {
-            const int grp = copy.warp + m * kCopyWarps;
-            if (grp >= kGroups) break;
-            copy.tell();
-            copy.keys(a.v, &map_v, walk, t, grp, page[m], sbase + S::kV + vs * S::kTile,
-                      smem_u32(&bars.v_full[vs]));
-            page[m] = page1[m];
-          }
-          copy.tell();
           t = t1;
+          page = page1;
         }
       } while (ok && walk.next());
       if (!ok) {  // let tensor copies land before the CTA ends
-        for (uint32_t t = nt < 2 ? 0 : nt - 2; t <= nt; ++t) {
-          mbar_wait_drain(smem_u32(&bars.k_full[t % kKStages]), (t / kKStages) & 1);
-          mbar_wait_drain(smem_u32(&bars.v_full[t % kVStages]), (t / kVStages) & 1);
+        for (uint32_t n = 0; n < stages; ++n) {
+          const uint32_t st = (stage + n) % stages, r = st >= stage ? round - 1 : round;
+          if (st < stage || round > 0) mbar_wait_drain(smem_u32(&full[st]), r & 1);
         }
       }
     } else if (warp < kCopyWarp0) {
@@ -831,9 +854,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           const uint32_t t = nt + i;
           const TileKeys tk = tile_keys(a, walk, base, walk.i0 + i);
           const bool chose = real && ((tk.who >> node) & 1);
-          if (!mbar_wait_warp(smem_u32(&bars.k_full[t % kKStages]), (t / kKStages) & 1,
-                              abort_flag) ||
-              !mbar_wait_warp(smem_u32(&bars.s_full[x]), nx & 1, abort_flag)) {
+          if (!mbar_wait_warp(smem_u32(&bars.s_full[x]), nx & 1, abort_flag)) {
             ok = false;
             break;
           }
@@ -846,7 +867,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           // The row's keys in this tile: where all of them are cached, all or none.
           uint32_t words[4] = {~0u, ~0u, ~0u, ~0u};
           bool any = chose, plain = true;
-          const uint4 there = sh.there[t & 3];
+          const uint4 there = sh.there[t & 7];
           if (tk.first + kBlock > walk.w.len || (there.x & there.y & there.z & there.w) != ~0u) {
             const int32_t cached = chose ? min(max(walk.w.len - tk.first, 0), kBlock) : 0;
 #pragma unroll
@@ -1131,7 +1152,7 @@ cudaError_t launch_tree(TreeArgs a, cudaStream_t s) {
   // can be made of the pools
   CUtensorMap map[2] = {};
   const int32_t page_size = 1 << a.table.shift;
-  a.box = page_size >= 8 ? std::min(page_size, 32) : 0;
+  a.box = page_size >= 8 ? std::min(page_size, 64) : 0;
   for (int i = 0; i < 2 && a.box > 0; ++i) {
     const PagedPool& p = i ? a.v : a.k;
     if (make_map_pages(&map[i], p.base, kLift<T> == 0.f, kDim, a.kv_heads, page_size,
