@@ -33,7 +33,8 @@
 // once.  An item within one run is finished there; otherwise each run leaves its
 // (m, l, O) in the workspace and k_paged_tree_join adds them up, in order.
 //
-// One warp fetches keys, three tiles ahead, one values, two tiles ahead, into the
+// One warp fetches keys, three tiles ahead (heads of 64 channels: four), one values,
+// two (four) tiles ahead, into the
 // swizzled layout that the tensor cores read: from pages of 8 tokens or more by
 // tensor copies of up to 64 tokens of a page, a lane each; from smaller pages by
 // copies of 16 bytes.  What lies behind a row's end may be anything: as a key it
@@ -60,7 +61,6 @@ constexpr int kMaxRuns = 160;      // CTAs: no GB300 has more SMs
 constexpr int kSoftWarps = 8, kCopyWarps = 2;
 constexpr int kCopyWarp0 = 2, kSoftWarp0 = kCopyWarp0 + kCopyWarps;
 constexpr int kTreeThreads = (kSoftWarp0 + kSoftWarps) * 32;
-constexpr int kKStages = 3, kVStages = 2;
 constexpr float kRise = 8.f;       // and kLift: as in paged_decode.cu
 template <typename T>
 constexpr float kLift = 0.f;
@@ -91,12 +91,14 @@ struct TreeArgs {
 template <int kDim>
 struct TreeShape {
   static constexpr uint32_t kTile = kTileRows * kDim * 2;
+  static constexpr uint32_t kKStages = kDim == 128 ? 3 : 4, kVStages = kDim == 128 ? 2 : 4;
   static constexpr uint32_t kQ = 0, kK = 2 * kTile, kV = kK + kKStages * kTile;
   static constexpr uint32_t kRest = kV + kVStages * kTile;  // a TreeShared
   static constexpr uint32_t kTmO = 256;  // columns of O_A; O_B kDim further
 };
 
-// A row as the kernels see it; n == 0: nothing to attend for.
+// A row as the kernels see it; n == 0: nothing to attend for.  (Read past the
+// first-level cache: k_paged_tree_join reads it before its wait.)
 struct TreeRow {
   int32_t t0, n, len;
 };
@@ -104,7 +106,7 @@ __device__ __forceinline__ bool row_fits(const TreeArgs& a, int32_t n, int32_t l
   return n <= kNodes && len >= 0 && int64_t(len) + n <= (int64_t(a.table.width) << a.table.shift);
 }
 __device__ __forceinline__ TreeRow tree_row(const TreeArgs& a, int32_t r) {
-  const int32_t o0 = a.offs[r], o1 = a.offs[r + 1], len = a.kv_len[r];
+  const int32_t o0 = __ldcg(a.offs + r), o1 = __ldcg(a.offs + r + 1), len = __ldcg(a.kv_len + r);
   TreeRow v{o0, o1 - o0, len};
   if (o0 < 0 || o1 <= o0 || o1 > a.T || !row_fits(a, o1 - o0, len)) v.n = 0;
   return v;
@@ -204,7 +206,7 @@ struct TreePrefix {
 };
 __device__ __forceinline__ int32_t item_tiles(const TreeArgs& a, const TreeRow& w, int32_t lr,
                                               int32_t g) {
-  if (a.q2k) return a.counts[int64_t(lr) * a.kv_heads + g];
+  if (a.q2k) return __ldcg(a.counts + int64_t(lr) * a.kv_heads + g);
   return lr / a.table.rows < layer_count(a, w.n) ? dense_tiles(w) : 0;
 }
 __device__ __forceinline__ int32_t layer_row_tiles(const TreeArgs& a, int32_t lr) {
@@ -311,14 +313,15 @@ struct TreeWalk {
 };
 
 // ------------------------------------------------------------ the main kernel
+constexpr int kMaxStages = 4;
 struct TreeBars {
-  uint64_t q_full, q_empty, k_full[kKStages], k_empty[kKStages], v_full[kVStages],
-      v_empty[kVStages], s_full[2], p_full[2], o_full[2], o_free, ml, part, fin[2];
+  uint64_t q_full, q_empty, k_full[kMaxStages], k_empty[kMaxStages], v_full[kMaxStages],
+      v_empty[kMaxStages], s_full[2], p_full[2], o_full[2], o_free, ml, part, fin[2];
 };
 struct TreeShared {
   TreeBars bars;
-  // Keys of a tile whose pages are there.  A ring of 8 tiles: keys are four tiles ahead
-  // of a slot's softmax at most.
+  // Keys of a tile whose pages are there.  A ring of 8 tiles: keys are six tiles ahead
+  // of a slot's softmax at most (those of the tile after its next wait for its next S).
   uint4 there[8];
   float2 states[2][kTileRows];    // (m, l) of the slots, where they are joined
   uint32_t tmem_base;
@@ -369,19 +372,22 @@ struct Copier {
   bool values;
   int lane;
 
-  // With boxes: the page of the lane's box of a tile, as the table has it (kNoKey: none
-  // of its keys are in the row).  Else of key 32 grp + lane.
-  static constexpr int32_t kNoKey = INT32_MIN;
+  // With boxes: the page of the lane's box of a tile, else of key 32 grp + lane, as the
+  // table has it (of some key of the row, if that one is not in it: nothing here waits
+  // for the load).
   __device__ __forceinline__ int32_t page(const TreeWalk& s, const TileKeys& t, int grp) const {
     const int32_t at = a.box > 0 ? lane / kHalves * a.box : 32 * grp + lane;
-    if (at >= kBlock || t.first + at >= t.end) return kNoKey;
-    return max(a.table.pages[int64_t(s.row) * a.table.stride + ((t.first + at) >> a.table.shift)],
-               -1);
+    return a.table.pages[int64_t(s.row) * a.table.stride +
+                         (min(t.first + min(at, kBlock - 1), t.end - 1) >> a.table.shift)];
   }
-  __device__ __forceinline__ int32_t checked(int32_t p) const {
+  // Such a page; -1: not one of the pool; kNoKey: the key is not in the row.
+  static constexpr int32_t kNoKey = INT32_MIN;
+  __device__ __forceinline__ int32_t checked(const TileKeys& t, int32_t p, int grp) const {
+    const int32_t at = a.box > 0 ? lane / kHalves * a.box : 32 * grp + lane;
+    if (at >= kBlock || t.first + at >= t.end) return kNoKey;
     if (p >= 0 && p < a.table.num_pages) return p;
-    if (p != kNoKey && !values) raise_paged(a.table.status, MSA_ERR_BAD_PAGE);
-    return p == kNoKey ? kNoKey : -1;
+    if (!values) raise_paged(a.table.status, MSA_ERR_BAD_PAGE);
+    return -1;
   }
   // Zeros into rows r0 .. r1 - 1 of a tile.
   __device__ __forceinline__ void zero(uint32_t tile, int r0, int r1) const {
@@ -396,7 +402,7 @@ struct Copier {
                                        uint32_t& parts, volatile int* abort_flag) const {
     const int32_t mask = (1 << a.table.shift) - 1;
     if (a.box > 0) {
-      p = checked(p);
+      p = checked(t, p, 0);
       const bool bad = __any_sync(0xffffffffu, p == -1);
       const bool mine = p >= 0;
       const int boxes = __popc(__ballot_sync(0xffffffffu, mine)) / kHalves;
@@ -441,7 +447,7 @@ struct Copier {
     const T* base = static_cast<const T*>(pool.base) + s.g * pool.head + c * 8;
     for (int grp = 0; grp < kBlock / 32; ++grp) {
       if (grp > 0) p = page(s, t, grp);
-      p = checked(p);
+      p = checked(t, p, grp);
       const uint32_t lost = __ballot_sync(0xffffffffu, p == -1);
       if (!values && lane == 0) reinterpret_cast<uint32_t*>(there)[grp] = ~lost;
 #pragma unroll 4
@@ -641,8 +647,8 @@ __device__ __forceinline__ void tree_mma_role(const TreeArgs& a, TreeBars& bars,
       if (split) commit_one(one, smem_u32(&bar));
     };
     auto issue_s = [&](int i) -> bool {
-      const uint32_t t = nt + i, stg = t % kKStages;
-      if (!wait(bars.k_full[stg], t / kKStages)) return false;
+      const uint32_t t = nt + i, stg = t % S::kKStages;
+      if (!wait(bars.k_full[stg], t / S::kKStages)) return false;
       tc_fence_after();
       const uint64_t bk = dk + stg * kStage;
 #pragma unroll
@@ -657,9 +663,9 @@ __device__ __forceinline__ void tree_mma_role(const TreeArgs& a, TreeBars& bars,
     ok = wait(bars.q_full, segs);
     if (ok && first < tiles) ok = issue_s(first);
     for (int i = first; ok && i < tiles; i += step) {
-      const uint32_t t = nt + i, stg = t % kVStages;
+      const uint32_t t = nt + i, stg = t % S::kVStages;
       if (i == first && segs > 0 && !wait(bars.o_free, segs - 1)) { ok = false; break; }
-      if (!wait(bars.v_full[stg], t / kVStages) || !wait(bars.p_full[x], np)) { ok = false; break; }
+      if (!wait(bars.v_full[stg], t / S::kVStages) || !wait(bars.p_full[x], np)) { ok = false; break; }
       ++np;
       tc_fence_after();
       const uint64_t bv = dv + stg * kStage;
@@ -704,11 +710,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     auto init = [](uint64_t& b, uint32_t n) { mbar_init(smem_u32(&b), n); };
     init(bars.q_full, kSoftWarps);
     init(bars.q_empty, 2);
-    for (int i = 0; i < kKStages; ++i) {
+    for (int i = 0; i < kMaxStages; ++i) {
       init(bars.k_full[i], 1);
       init(bars.k_empty[i], 2);
-    }
-    for (int i = 0; i < kVStages; ++i) {
       init(bars.v_full[i], 1);
       init(bars.v_empty[i], 2);
     }
@@ -760,7 +764,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       // ---------------- copies: one warp keys, one values
       const bool values = warp != kCopyWarp0;
       const Copier<T, kDim> copy{a, values ? a.v : a.k, values ? &map_v : &map_k, values, lane};
-      const uint32_t stages = values ? kVStages : kKStages;
+      const uint32_t stages = values ? S::kVStages : S::kKStages;
       uint64_t* const full = values ? bars.v_full : bars.k_full;
       uint64_t* const empty = values ? bars.v_empty : bars.k_empty;
       const uint32_t tiles_at = sbase + (values ? S::kV : S::kK);
@@ -1035,9 +1039,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 }
 
 // ------------------------------------------------------------ joining runs
-// CTA x stands for run x + 1, if that run starts inside an item; the CTAs of an
-// item share its rows.  A warp takes a row, its lanes the channels.
-constexpr int kJoinThreads = 256;
+// CTAs (x, ..) stand for run x + 1, if that run starts inside an item; the CTAs of an
+// item share its rows.  A warp takes kJoinRows rows at a time, its lanes the channels.
+// What follows from the lengths is worked out before the wait for the runs' end.
+// (The lengths are there: k_paged_tree lets this kernel start after its own wait for
+// what came before.)
+constexpr int kJoinThreads = 256, kJoinRows = 2;
 template <typename T, int kDim>
 __global__ void __launch_bounds__(kJoinThreads) k_paged_tree_join(const TreeArgs a) {
   constexpr int kPer = kDim / 32, kLoads = 4;
@@ -1046,15 +1053,15 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_tree_join(const TreeArgs
   };
   __shared__ TreePrefix prefix;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  grid_dep_wait();
-  grid_dep_release();
   make_tree_prefix(a, prefix);
   const int32_t total = prefix.total, runs = min(total, int32_t(gridDim.x) + 1);
   const int32_t run = int32_t(blockIdx.x) + 1;
-  if (run >= runs) return;
-  const int32_t begin = run_start(total, runs, run);
+  const int32_t begin = run < runs ? run_start(total, runs, run) : 0;
   TreeWalk walk(a);
-  walk.locate(prefix, begin);
+  walk.i0 = 0;
+  if (run < runs) walk.locate(prefix, begin);
+  grid_dep_wait();  // every CTA waits: this grid must not end before the runs
+  grid_dep_release();
   if (walk.i0 == 0) return;
   // the runs of the item's first and last tile
   auto run_of = [&](int32_t t) {
@@ -1064,44 +1071,60 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_tree_join(const TreeArgs
   };
   const int32_t first = run_of(begin - walk.i0);
   const int n = run_of(begin - walk.i0 + walk.tiles - 1) + 1 - first;
-  const int share = run - first - 1, shares = n - 1;
   const int32_t rows = walk.rows_here();
-  for (int32_t m = share * (kJoinThreads / 32) + warp; m < rows;
-       m += shares * (kJoinThreads / 32)) {
-    float M = -INFINITY, l = 0.f, acc[kPer] = {};
-    for (int i0 = 0; i0 < n; i0 += kLoads) {
-      Chunk o[kLoads];
-      float2 ml[kLoads];
+  constexpr int kWarps = kJoinThreads / 32;
+  const int share = ((run - first - 1) * gridDim.y + blockIdx.y) * kWarps + warp;
+  const int shares = (n - 1) * gridDim.y * kWarps;
+  for (int32_t m0 = share * kJoinRows; m0 < rows; m0 += shares * kJoinRows) {
+    float M[kJoinRows], l[kJoinRows], acc[kJoinRows][kPer] = {};
 #pragma unroll
-      for (int u = 0; u < kLoads; ++u) {
-        const int i = i0 + u;
-        ml[u] = make_float2(-INFINITY, 0.f);
-        o[u] = Chunk{};
-        if (i < n) {
-          const int64_t part = (2 * int64_t(first + i) + (i == 0 ? 1 : 0)) * kPairRows + m;
-          ml[u] = *reinterpret_cast<const float2*>(a.part_ml + part * 2);
-          o[u] = reinterpret_cast<const Chunk*>(a.part_o + part * kDim)[lane];
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < kLoads; ++u) {
-        const float top = fmaxf(M, ml[u].x);
-        const float f = M == -INFINITY ? 0.f : fast_exp2(M - top);
-        const float g = ml[u].x == -INFINITY ? 0.f : fast_exp2(ml[u].x - top);
-        M = top;
-        l = l * f + ml[u].y * g;
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) acc[e] = acc[e] * f + o[u].x[e] * g;
-      }
+    for (int w = 0; w < kJoinRows; ++w) {
+      M[w] = -INFINITY;
+      l[w] = 0.f;
     }
-    const int32_t mr = walk.layer * kPairRows + m, node = mr / a.group;
-    const int64_t orow = (int64_t(walk.w.t0) + node) * (a.kv_heads * a.group) +
-                         walk.g * a.group + mr - node * a.group;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    uint32_t* o = reinterpret_cast<uint32_t*>(static_cast<T*>(a.o) + orow * kDim + lane * kPer);
+    for (int i0 = 0; i0 < n; i0 += kLoads) {
+      Chunk o[kJoinRows][kLoads];
+      float2 ml[kJoinRows][kLoads];
 #pragma unroll
-    for (int e = 0; e < kPer; e += 2) o[e / 2] = Pair<T>::pack(acc[e] * inv, acc[e + 1] * inv);
-    if (lane == 0) a.lse[orow] = l == 0.f ? -INFINITY : kLn2 * (M + log2f(l));
+      for (int w = 0; w < kJoinRows; ++w)
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u) {
+          const int i = i0 + u;
+          ml[w][u] = make_float2(-INFINITY, 0.f);
+          o[w][u] = Chunk{};
+          if (i < n && m0 + w < rows) {
+            const int64_t part =
+                (2 * int64_t(first + i) + (i == 0 ? 1 : 0)) * kPairRows + m0 + w;
+            ml[w][u] = *reinterpret_cast<const float2*>(a.part_ml + part * 2);
+            o[w][u] = reinterpret_cast<const Chunk*>(a.part_o + part * kDim)[lane];
+          }
+        }
+#pragma unroll
+      for (int w = 0; w < kJoinRows; ++w)
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u) {
+          const float top = fmaxf(M[w], ml[w][u].x);
+          const float f = M[w] == -INFINITY ? 0.f : fast_exp2(M[w] - top);
+          const float g = ml[w][u].x == -INFINITY ? 0.f : fast_exp2(ml[w][u].x - top);
+          M[w] = top;
+          l[w] = l[w] * f + ml[w][u].y * g;
+#pragma unroll
+          for (int e = 0; e < kPer; ++e) acc[w][e] = acc[w][e] * f + o[w][u].x[e] * g;
+        }
+    }
+#pragma unroll
+    for (int w = 0; w < kJoinRows; ++w) {
+      if (m0 + w >= rows) break;
+      const int32_t mr = walk.layer * kPairRows + m0 + w, node = mr / a.group;
+      const int64_t orow = (int64_t(walk.w.t0) + node) * (a.kv_heads * a.group) +
+                           walk.g * a.group + mr - node * a.group;
+      const float inv = l[w] == 0.f ? 0.f : 1.f / l[w];
+      uint32_t* o = reinterpret_cast<uint32_t*>(static_cast<T*>(a.o) + orow * kDim + lane * kPer);
+#pragma unroll
+      for (int e = 0; e < kPer; e += 2)
+        o[e / 2] = Pair<T>::pack(acc[w][e] * inv, acc[w][e + 1] * inv);
+      if (lane == 0) a.lse[orow] = l[w] == 0.f ? -INFINITY : kLn2 * (M[w] + log2f(l[w]));
+    }
   }
 }
 
@@ -1166,8 +1189,15 @@ cudaError_t launch_tree(TreeArgs a, cudaStream_t s) {
   launch_end("paged_tree", s);
   if (e != cudaSuccess || grid == 1) return e;
   launch_begin("paged_tree_join", s);
-  e = launch_k(true, k_paged_tree_join<T, kDim>, dim3(unsigned(grid - 1)), dim3(kJoinThreads), 0,
-               s, a);
+  // A run for each CTA, and with many items (as many as rows and key heads, of so many
+  // matrix rows) several CTAs for a run's share of an item's rows, 16 a pass (one row
+  // 29.0 us with four CTAs a run, 26.7 with one; 32 rows of up to 12000 tokens 247 us
+  // with four and 310 with one).
+  const int64_t tokens = (a.T + a.table.rows - 1) / a.table.rows;
+  const int64_t rows = int64_t(a.table.rows) * a.kv_heads * std::min<int64_t>(tokens * a.group, kPairRows);
+  const int64_t shares = std::min<int64_t>(rows / (grid * 16) + 1, 4);
+  e = launch_k(true, k_paged_tree_join<T, kDim>, dim3(unsigned(grid - 1), unsigned(shares)),
+               dim3(kJoinThreads), 0, s, a);
   launch_end("paged_tree_join", s);
   return e;
 }
