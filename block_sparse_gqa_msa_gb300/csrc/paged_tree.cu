@@ -7,7 +7,7 @@
 // against the same keys.  Over tiles of 128 keys, with a running reference m and
 // sum l in base 2 (x = scale * log2(e) * <q, k>):
 //   P = 2^(x - m), l += sum P, O += P V,
-// O and l rescaled when m has to rise (m trails the maximum by kRise at most);
+// O and l rescaled when m has to rise (see kMostSum);
 // two such states join as M = max(m1, m2), l = l1 2^(m1 - M) + l2 2^(m2 - M), O
 // likewise; at the end O / l, lse = ln2 (m + log2 l).  m, l, O are 32 bits; P is
 // rounded to the cache's type for the product with V (the tensor cores take
@@ -61,11 +61,25 @@ constexpr int kMaxRuns = 160;      // CTAs: no GB300 has more SMs
 constexpr int kSoftWarps = 8, kCopyWarps = 2;
 constexpr int kCopyWarp0 = 2, kSoftWarp0 = kCopyWarp0 + kCopyWarps;
 constexpr int kTreeThreads = (kSoftWarp0 + kSoftWarps) * 32;
-constexpr float kRise = 8.f;       // and kLift: as in paged_decode.cu
+// Registers of a thread: 168 at launch; the softmax warps take over what the first
+// four give up, 128 x 72 + 256 x 216 = 384 x 168.
+constexpr int kSoftRegs = 216, kOtherRegs = 72;
+// A row's reference m is set by its first tile, kLift below the maximum there.  In
+// whole tiles no maximum is formed: m is raised where the weights sum up to more than
+// kMostSum; in tiles with masks where the maximum is kRise above.  So the state is
+// scaled a few times in a row at most.  bf16 has the range of 32 bits: weights up to
+// 2^30 leave sums of 2^30 of them and values up to 2^60 inside it.  fp16 ends at 2^16:
+// up to 2^15, and m 7 lower than the maximum so that a key far below it keeps its bits
+// (as in paged_decode.cu).
+constexpr float kRise = 8.f;
 template <typename T>
 constexpr float kLift = 0.f;
 template <>
 constexpr float kLift<__half> = 7.f;
+template <typename T>
+constexpr float kMostSum = 1073741824.f;
+template <>
+constexpr float kMostSum<__half> = 32768.f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -316,7 +330,7 @@ struct TreeWalk {
 constexpr int kMaxStages = 4;
 struct TreeBars {
   uint64_t q_full, q_empty, k_full[kMaxStages], k_empty[kMaxStages], v_full[kMaxStages],
-      v_empty[kMaxStages], s_full[2], p_full[2], o_full[2], o_free, ml, part, fin[2];
+      v_empty[kMaxStages], s_full[2], p_full[2], o_full[2], o_free, ml, part, turn[2][4], fin[2];
 };
 struct TreeShared {
   TreeBars bars;
@@ -359,6 +373,36 @@ __device__ __forceinline__ TileKeys tile_keys(const TreeArgs& a, const TreeWalk&
 // Offset of 16 bytes of a row in a tile that the tensor cores read.
 __device__ __forceinline__ uint32_t tile_at(int row, int chunk) {
   return (chunk >> 3) * 16384u + row * 128u + (((chunk & 7) ^ (row & 7)) << 4);
+}
+
+// The keys of a tile that a row sees: those of the cached tokens, if it chose them,
+// and of the drafted ones those on its path.
+__device__ __forceinline__ uint4 tile_words(const TileKeys& t, int32_t len, bool chose,
+                                            uint64_t path) {
+  uint32_t w[4];
+  const int32_t cached = chose ? min(max(len - t.first, 0), kBlock) : 0;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const int32_t n = cached - 32 * c;
+    w[c] = n >= 32 ? ~0u : n > 0 ? (1u << n) - 1 : 0u;
+  }
+  if (t.drafted && t.end > len) {
+    const int32_t off = len - t.first;  // place of drafted token 0
+    uint64_t lo = 0, hi = 0;
+    if (off <= 0) {
+      lo = -off < 64 ? path >> -off : 0;
+    } else if (off < 64) {
+      lo = path << off;
+      hi = path >> (64 - off);
+    } else {
+      hi = path << (off - 64);
+    }
+    w[0] |= uint32_t(lo);
+    w[1] |= uint32_t(lo >> 32);
+    w[2] |= uint32_t(hi);
+    w[3] |= uint32_t(hi >> 32);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // The copying warps' side, of keys or of values.
@@ -469,31 +513,28 @@ struct Copier {
   }
 };
 
+template <int kRegs>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
 // P = 2^(s c2 - mref) of one tile row (tensor memory columns [cs, cs + 128) of
-// the thread's lane) as pairs of T into pk; with kMask the keys whose bit is not
-// set in words give 0.  Returns the sum of the 32-bit values; *tmax gets the
-// row's largest raw score.
-template <typename T, bool kMask>
-__device__ __forceinline__ float tree_row_exp(uint32_t cs, const uint32_t (&words)[4], float c2,
-                                              float mref, uint32_t (&pk)[64], float* tmax) {
+// the thread's lane) as pairs of T into pk.  Returns the sum of the 32-bit values.
+template <typename T>
+__device__ __forceinline__ float tree_row_exp(uint32_t cs, float c2, float mref,
+                                              uint32_t (&pk)[64]) {
   const uint64_t cc = f2_pack(__float_as_uint(c2), __float_as_uint(c2));
   const uint64_t nm = f2_pack(__float_as_uint(-mref), __float_as_uint(-mref));
   uint64_t ls[2] = {0ull, 0ull};
-  float m0 = -INFINITY, m1 = -INFINITY;
   auto expo = [&](const uint32_t (&r)[16], int c) {
 #pragma unroll
     for (int j = 0; j < 16; j += 2) {
-      float x0 = __uint_as_float(r[j]), x1 = __uint_as_float(r[j + 1]);
       const uint64_t x2 = f2_fma(f2_pack(r[j], r[j + 1]), cc, nm);
-      float p0 = fast_exp2(f2_lo(x2)), p1 = fast_exp2(f2_hi(x2));
-      if (kMask) {
-        const uint32_t w = words[c >> 1] >> ((c & 1) * 16 + j);
-        p0 = (w & 1u) ? p0 : 0.f;
-        p1 = (w & 2u) ? p1 : 0.f;
-        x0 = (w & 1u) ? x0 : -INFINITY;
-        x1 = (w & 2u) ? x1 : -INFINITY;
-      }
-      if (j & 2) m1 = fmax3(m1, x0, x1); else m0 = fmax3(m0, x0, x1);
+      const float p0 = fast_exp2(f2_lo(x2)), p1 = fast_exp2(f2_hi(x2));
       ls[(j >> 1) & 1] =
           f2_add(ls[(j >> 1) & 1], f2_pack(__float_as_uint(p0), __float_as_uint(p1)));
       pk[8 * c + (j >> 1)] = Pair<T>::pack(p0, p1);
@@ -517,25 +558,75 @@ __device__ __forceinline__ float tree_row_exp(uint32_t cs, const uint32_t (&word
       reg_fence16(r0);
     }
   }
-  *tmax = fmaxf(m0, m1);
   const uint64_t s2 = f2_add(ls[0], ls[1]);
   return f2_lo(s2) + f2_hi(s2);
 }
-// The row's largest raw score alone.
-__device__ __forceinline__ float tree_row_max(uint32_t cs, const uint32_t (&words)[4]) {
-  float m = -INFINITY;
-#pragma unroll
+
+// A row's state: reference and sum of weights.
+struct RowState {
+  float m, l;
+};
+// The same for tiles with masks (the keys whose bit is not set in words give 0) and
+// where the reference has to rise or is not set yet: the maximum first, O (complete
+// up to the slot's step before; there is none where `begins`) and the sum scaled,
+// then the weights, stored over the scores that have been read.  
+template <typename T, int kDim>
+__device__ __forceinline__ RowState tree_masked_tile(uint32_t cs, uint32_t co, uint4 words, float c2,
+                                                  RowState st, bool begins) {
+  float mx = -INFINITY;
+#pragma unroll 1
   for (int c = 0; c < 4; ++c) {
     uint32_t r[32];
     tmem_ld32(cs + 32 * c, r);
+    const uint32_t w = c == 0 ? words.x : c == 1 ? words.y : c == 2 ? words.z : words.w;
     tmem_ld_wait();
     reg_fence32(r);
 #pragma unroll
     for (int j = 0; j < 32; j += 2)
-      m = fmax3(m, (words[c] >> j) & 1u ? __uint_as_float(r[j]) : -INFINITY,
-                (words[c] >> j) & 2u ? __uint_as_float(r[j + 1]) : -INFINITY);
+      mx = fmax3(mx, (w >> j) & 1u ? __uint_as_float(r[j]) : -INFINITY,
+                 (w >> j) & 2u ? __uint_as_float(r[j + 1]) : -INFINITY);
   }
-  return m;
+  const float to = mx * c2 - kLift<T>;  // (-infinity without keys)
+  const bool raise = to > st.m + kRise;
+  if (__any_sync(0xffffffffu, raise)) {
+    const float f = raise ? fast_exp2(st.m - to) : 1.f;
+    st.l *= f;
+    if (raise) st.m = to;
+    if (!begins) {
+#pragma unroll 1
+      for (int c = 0; c < kDim / 32; ++c) {
+        uint32_t o[32];
+        tmem_ld32(co + 32 * c, o);
+        tmem_ld_wait();
+        reg_fence32(o);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+        tmem_st32_nc(co + 32 * c, o);
+      }
+    }
+  }
+  const float m = st.m == -INFINITY ? 0.f : st.m;
+  float sum = 0.f;
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    uint32_t r[32], p[16];
+    tmem_ld32(cs + 32 * c, r);
+    const uint32_t w = c == 0 ? words.x : c == 1 ? words.y : c == 2 ? words.z : words.w;
+    tmem_ld_wait();
+    reg_fence32(r);
+#pragma unroll
+    for (int j = 0; j < 32; j += 2) {
+      const float p0 =
+          (w >> j) & 1u ? fast_exp2(fmaf(__uint_as_float(r[j]), c2, -m)) : 0.f;
+      const float p1 =
+          (w >> j) & 2u ? fast_exp2(fmaf(__uint_as_float(r[j + 1]), c2, -m)) : 0.f;
+      sum += p0 + p1;
+      p[j >> 1] = Pair<T>::pack(p0, p1);
+    }
+    tmem_st16(cs + 16 * c, p);
+  }
+  st.l += sum;
+  return st;
 }
 
 // The tokens on the path of token `node` of a row (bit i: token i), by a warp:
@@ -725,6 +816,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     init(bars.o_free, kSoftWarps);
     init(bars.ml, kSoftWarps);
     init(bars.part, 1);
+    for (int i = 0; i < 8; ++i) init(bars.turn[i >> 2][i & 3], 1);
     fence_mbar_init();
   }
   if (warp == 0) {
@@ -762,6 +854,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   if (run < runs) {
     if (warp >= kCopyWarp0 && warp < kSoftWarp0) {
       // ---------------- copies: one warp keys, one values
+      fewer_registers<kOtherRegs>();
       const bool values = warp != kCopyWarp0;
       const Copier<T, kDim> copy{a, values ? a.v : a.k, values ? &map_v : &map_k, values, lane};
       const uint32_t stages = values ? S::kVStages : S::kKStages;
@@ -804,15 +897,28 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       }
     } else if (warp < kCopyWarp0) {
       // ---------------- tensor cores
+      fewer_registers<kOtherRegs>();
       tree_mma_role<T, kDim>(a, bars, walk, warp, tmem, sbase, abort_flag);
     } else {
       // ---------------- softmax and results of slot x (warps 4-7: A, 8-11: B)
+      more_registers<kSoftRegs>();
       const int x = (warp - kSoftWarp0) >> 2, quad = warp & 3;
       const int trow = quad * 32 + lane;  // tile row = lane of tensor memory
       const uint32_t lane_base = uint32_t(quad * 32) << 16;
       const uint32_t cs = tmem + lane_base + 128 * x;
       const uint32_t co = tmem + lane_base + S::kTmO;
       uint32_t nt = 0, nx = 0, segs = 0, joins = 0, no[2] = {0, 0};
+      // Where the slots have rows of their own, their warps on one scheduler take turns:
+      // side by side both slots would be at their softmax, and then both at the tensor
+      // cores.
+      int32_t turns = -(1 - x);  // (slot A's first needs no leave)
+      auto my_turn = [&]() {
+        const int32_t n = turns++;
+        return n < 0 || mbar_wait_warp(smem_u32(&bars.turn[x][quad]), n & 1, abort_flag);
+      };
+      auto pass_turn = [&]() {
+        if (lane == 0) mbar_arrive(smem_u32(&bars.turn[x ^ 1][quad]));
+      };
       do {
         const int32_t rows = walk.rows_here();
         const bool split = rows <= kTileRows;
@@ -852,7 +958,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         // (does the segment reach the drafted tokens?)
         if (a.q2k ? walk.i1 == walk.tiles : int64_t(walk.i1) * kBlock > walk.w.len)
           path = path_of(a, walk.w, node);
-        float mref = -INFINITY, lsum = 0.f;
+        RowState st{-INFINITY, 0.f};
         for (int k = 0; k < steps; ++k) {
           const int i = split ? 2 * k + x : k;
           const uint32_t t = nt + i;
@@ -863,94 +969,51 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             break;
           }
           ++nx;
+          if (!split && !my_turn()) {
+            ok = false;
+            break;
+          }
           if (!used) {  // no row of the warp is one: what P holds there does not matter
+            if (!split) pass_turn();
             if (lane == 0) mbar_arrive(smem_u32(&bars.p_full[x]));
             continue;
           }
           tc_fence_after();
           // The row's keys in this tile: where all of them are cached, all or none.
-          uint32_t words[4] = {~0u, ~0u, ~0u, ~0u};
-          bool any = chose, plain = true;
+          uint4 words = make_uint4(~0u, ~0u, ~0u, ~0u);
+          bool plain = k > 0;
           const uint4 there = sh.there[t & 7];
           if (tk.first + kBlock > walk.w.len || (there.x & there.y & there.z & there.w) != ~0u) {
-            const int32_t cached = chose ? min(max(walk.w.len - tk.first, 0), kBlock) : 0;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const int32_t n = cached - 32 * c;
-              words[c] = n >= 32 ? ~0u : n > 0 ? (1u << n) - 1 : 0u;
-            }
-            if (tk.drafted && tk.end > walk.w.len && real) {
-              const int32_t off = walk.w.len - tk.first;  // place of drafted token 0
-              uint64_t lo, hi;
-              if (off <= 0) {
-                lo = -off < 64 ? path >> -off : 0;
-                hi = 0;
-              } else if (off < 64) {
-                lo = path << off;
-                hi = path >> (64 - off);
-              } else {
-                lo = 0;
-                hi = path << (off - 64);
-              }
-              words[0] |= uint32_t(lo);
-              words[1] |= uint32_t(lo >> 32);
-              words[2] |= uint32_t(hi);
-              words[3] |= uint32_t(hi >> 32);
-            }
-            words[0] &= there.x;
-            words[1] &= there.y;
-            words[2] &= there.z;
-            words[3] &= there.w;
-            any = (words[0] | words[1] | words[2] | words[3]) != 0;
-            const bool all = (words[0] & words[1] & words[2] & words[3]) == ~0u;
-            plain = __all_sync(0xffffffffu, all || !any);
+            plain = false;
+            words = tile_words(tk, walk.w.len, chose, real ? path : 0ull);
+            words.x &= there.x;
+            words.y &= there.y;
+            words.z &= there.z;
+            words.w &= there.w;
+          } else if (!chose) {
+            words = make_uint4(0u, 0u, 0u, 0u);
           }
-          if (k == 0) {  // the first tile sets the reference
-            const float mx = tree_row_max(cs, words);
-            mref = any ? mx * a.scale_log2 - kLift<T> : -INFINITY;
-          }
-          uint32_t pk[64];
-          float ls;
-          for (;;) {
-            float tmax;
-            // Without masks where every row of the warp sees all of the tile or none of
-            // it: the latter are zeroed afterwards.
+          if (plain) {
+            uint32_t pk[64];
+            const float ls = tree_row_exp<T>(cs, a.scale_log2, st.m, pk);
+            // The sum tells when the reference has to rise (it is infinite where the row
+            // has seen no key so far).
+            plain = !__any_sync(0xffffffffu, chose && !(ls <= kMostSum<T>));
             if (plain) {
-              ls = tree_row_exp<T, false>(cs, words, a.scale_log2, mref, pk, &tmax);
-              if (!any) {
+              if (!chose) {
 #pragma unroll
                 for (int e = 0; e < 64; ++e) pk[e] = 0u;
-                ls = 0.f;
+              } else {
+                st.l += ls;
               }
-            } else {
-              ls = tree_row_exp<T, true>(cs, words, a.scale_log2, mref, pk, &tmax);
-            }
-            const float top = tmax * a.scale_log2;
-            const bool raise = any && top > mref + (kRise + kLift<T>);
-            if (!__any_sync(0xffffffffu, raise)) break;
-            // O (complete up to the slot's step before) and the sum times 2^(mref -
-            // the new reference), then the weights again (S is still there)
-            const float to = top - kLift<T>;
-            const float f = raise ? fast_exp2(mref - to) : 1.f;
-            lsum *= f;
-            if (raise) mref = to;
-            if (k > 0) {
-#pragma unroll 1
-              for (int c = 0; c < kDim / 32; ++c) {
-                uint32_t o[32];
-                tmem_ld32(co + kDim * x + 32 * c, o);
-                tmem_ld_wait();
-                reg_fence32(o);
-#pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                tmem_st32_nc(co + kDim * x + 32 * c, o);
-              }
+              // P over the first 64 columns of S (all of S has been read)
+              tmem_st32_nc(cs, *reinterpret_cast<const uint32_t(*)[32]>(&pk[0]));
+              tmem_st32_nc(cs + 32, *reinterpret_cast<const uint32_t(*)[32]>(&pk[32]));
             }
           }
-          lsum += ls;
-          // P over the first 64 columns of S (all of S has been read)
-          tmem_st32_nc(cs, *reinterpret_cast<const uint32_t(*)[32]>(&pk[0]));
-          tmem_st32_nc(cs + 32, *reinterpret_cast<const uint32_t(*)[32]>(&pk[32]));
+          if (!plain)
+            st = tree_masked_tile<T, kDim>(cs, co + kDim * x, words, a.scale_log2, st, k == 0);
+          if (!split) pass_turn();
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
@@ -960,12 +1023,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         // ---- results.  Two states of the same rows are joined here, half of the
         // columns by each slot's warps.
         const bool two = split && tiles > 1;
-        float M = mref, l = lsum, f0 = x == 0 ? 1.f : 0.f, f1 = x == 1 ? 1.f : 0.f;
+        float M = st.m, l = st.l, f0 = x == 0 ? 1.f : 0.f, f1 = x == 1 ? 1.f : 0.f;
         if (split) {
           // the states before these are read (a round of the barrier for writing, one
           // for reading)
           if (joins > 0 && !mbar_wait_warp(smem_u32(&bars.ml), 1, abort_flag)) break;
-          sh.states[x][trow] = make_float2(mref, lsum);
+          sh.states[x][trow] = make_float2(st.m, st.l);
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&bars.ml));
           if (!mbar_wait_warp(smem_u32(&bars.ml), 0, abort_flag)) break;
