@@ -26,7 +26,7 @@
 // are joined in tensor memory's lanes at the end; the order of operations is the
 // same.
 //
-// Split.  All items' key tiles, in order, are dealt out in equal runs to the
+// Split.  All items' key tiles, in order, are dealt out in runs of equal cost to the
 // CTAs, one an SM; a run's place is found from the lengths on the device.  Items
 // are ordered with the number of the 256-row group outermost: CTAs that read the
 // same keys for other queries then do so at about the same time, and HBM is read
@@ -210,103 +210,154 @@ __global__ void __launch_bounds__(kListThreads) k_paged_tree_lists(const TreeArg
 }
 
 // ------------------------------------------------------------ dealing out
-// The tiles before each of a CTA's stretches of layer rows (layer * rows + row).
+// Runs are equal in cost: a key tile costs 5 where both slots work on it, 3 where one
+// does (4100 and 2500 cycles), and where there are many tiles to a run an item costs
+// kItemCost beside its tiles (its queries, its first and last tile on their own, its
+// results).
+constexpr int kPairCost = 5, kSplitCost = 3, kItemCost = 6;
+constexpr int kManyTiles = 8;
 constexpr int kStretches = kTreeThreads;
 struct TreePrefix {
-  int32_t at[kStretches];
-  int32_t sums[kTreeThreads / 32];
+  int32_t at[kStretches];     // the cost of tiles before each of a CTA's stretches of
+  int32_t items[kStretches];  // layer rows (layer * rows + row), and the items there
+  int2 sums[kTreeThreads / 32];
   int32_t total;
+  int32_t item;  // an item's own cost
+  int32_t runs;
   int32_t each;  // layer rows of a stretch
 };
+__device__ __forceinline__ int32_t item_rows(const TreeArgs& a, const TreeRow& w, int32_t layer) {
+  return min(kPairRows, w.n * a.group - layer * kPairRows);
+}
+__device__ __forceinline__ int32_t tile_cost(const TreeArgs& a, const TreeRow& w, int32_t layer) {
+  return item_rows(a, w, layer) > kTileRows ? kPairCost : kSplitCost;
+}
 __device__ __forceinline__ int32_t item_tiles(const TreeArgs& a, const TreeRow& w, int32_t lr,
                                               int32_t g) {
   if (a.q2k) return __ldcg(a.counts + int64_t(lr) * a.kv_heads + g);
   return lr / a.table.rows < layer_count(a, w.n) ? dense_tiles(w) : 0;
 }
-__device__ __forceinline__ int32_t layer_row_tiles(const TreeArgs& a, int32_t lr) {
-  const TreeRow w = tree_row(a, lr % a.table.rows);
-  if (!a.q2k) return item_tiles(a, w, lr, 0) * a.kv_heads;
+// Tiles' cost and items of a layer row.
+__device__ __forceinline__ int2 layer_row_cost(const TreeArgs& a, int32_t lr) {
+  const int32_t layer = lr / a.table.rows;
+  const TreeRow w = tree_row(a, lr - layer * a.table.rows);
+  if (layer >= layer_count(a, w.n)) return make_int2(0, 0);
   int32_t n = 0;
-  for (int32_t g = 0; g < a.kv_heads; ++g) n += item_tiles(a, w, lr, g);
-  return n;
+  if (a.q2k) {
+    for (int32_t g = 0; g < a.kv_heads; ++g) n += item_tiles(a, w, lr, g);
+  } else {
+    n = dense_tiles(w) * a.kv_heads;
+  }
+  return make_int2(n * tile_cost(a, w, layer), a.kv_heads);
 }
-__device__ __forceinline__ void make_tree_prefix(const TreeArgs& a, TreePrefix& s) {
+__device__ __forceinline__ void make_tree_prefix(const TreeArgs& a, TreePrefix& s, int32_t grid) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
   const int32_t all = a.table.rows * a.layers, threads = blockDim.x;
   const int32_t each = (all + threads - 1) / threads;
   const int32_t r0 = min(all, tid * each), r1 = min(all, r0 + each);
-  int32_t mine = 0;
-  for (int32_t r = r0; r < r1; ++r) mine += layer_row_tiles(a, r);
-  int32_t incl = mine;
+  int2 mine = make_int2(0, 0);
+  for (int32_t r = r0; r < r1; ++r) {
+    const int2 c = layer_row_cost(a, r);
+    mine.x += c.x;
+    mine.y += c.y;
+  }
+  int2 incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int32_t y = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += y;
+    const int32_t x = __shfl_up_sync(0xffffffffu, incl.x, o);
+    const int32_t y = __shfl_up_sync(0xffffffffu, incl.y, o);
+    if (lane >= o) {
+      incl.x += x;
+      incl.y += y;
+    }
   }
   if (lane == 31) s.sums[warp] = incl;
   __syncthreads();
-  int32_t total = 0, before = 0;
+  int2 total = make_int2(0, 0), before = make_int2(0, 0);
   for (int w = 0; w < warps; ++w) {
-    if (w < warp) before += s.sums[w];
-    total += s.sums[w];
+    const int2 v = s.sums[w];
+    if (w < warp) {
+      before.x += v.x;
+      before.y += v.y;
+    }
+    total.x += v.x;
+    total.y += v.y;
   }
-  s.at[tid] = before + incl - mine;
+  s.at[tid] = before.x + incl.x - mine.x;
+  s.items[tid] = before.y + incl.y - mine.y;
   if (tid == 0) {
-    s.total = total;
+    const int32_t item = total.x >= kManyTiles * kPairCost * grid ? kItemCost : 0;
+    s.item = item;
+    s.total = total.x + item * total.y;
+    // no run shorter than a tile behind an item's own cost, so that none is empty
+    s.runs = min(s.total > 0 ? max(s.total / (kPairCost + item), 1) : 0, grid);
     s.each = each;
   }
   __syncthreads();
 }
-// Tiles of run c of `runs`: from start(c) to start(c + 1).
-__device__ __forceinline__ int32_t run_start(int32_t total, int32_t runs, int32_t c) {
-  return int32_t(int64_t(total) * c / runs);
+// Run c: cost run_start(c) to run_start(c + 1), the tiles that begin there.
+__device__ __forceinline__ int32_t run_start(const TreePrefix& s, int32_t c) {
+  return int32_t(int64_t(s.total) * c / s.runs);
+}
+__device__ __forceinline__ int32_t run_of(const TreePrefix& s, int32_t at) {
+  int32_t c = int32_t(int64_t(at) * s.runs / s.total);
+  while (run_start(s, c + 1) <= at) ++c;
+  return c;
 }
 
-// A walk over the items from tile t on.  All lanes alike.
+// A walk over the items of a run.  All lanes alike.
 struct TreeWalk {
   const TreeArgs& a;
   int32_t lr, g;      // layer row and key head of the item
   int32_t row, layer;
   TreeRow w;
   int32_t tiles;      // of the item
+  int32_t cost;       // of a tile
+  int32_t own;        // of an item beside its tiles
+  int32_t at;         // where the item's first tile begins
+  int32_t hi;         // the run's end
   int32_t i0, i1;     // the segment
-  int32_t left;       // of the run, after the segment
   __device__ __forceinline__ explicit TreeWalk(const TreeArgs& args) : a(args) {}
   __device__ __forceinline__ void enter_row() {
-    row = lr % a.table.rows;
     layer = lr / a.table.rows;
+    row = lr - layer * a.table.rows;
     w = tree_row(a, row);
+    cost = tile_cost(a, w, layer);
   }
-  // The item that tile t lies in; i0 its place there.
-  __device__ __forceinline__ void locate(const TreePrefix& s, int32_t t) {
-    int lo = 0, hi = blockDim.x;  // the last stretch that starts at or before t
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (s.at[mid] <= t) lo = mid; else hi = mid;
+  __device__ __forceinline__ void end_at() {
+    i1 = min(tiles, (hi - at + cost - 1) / cost);
+  }
+  // The first tile that begins at lo or later; there is one before `end`.
+  __device__ __forceinline__ void begin(const TreePrefix& s, int32_t lo, int32_t end) {
+    own = s.item;
+    hi = end;
+    int a0 = 0, a1 = blockDim.x;  // the last stretch that starts at or before lo
+    while (a1 - a0 > 1) {
+      const int mid = (a0 + a1) >> 1;
+      if (s.at[mid] + own * s.items[mid] <= lo) a0 = mid; else a1 = mid;
     }
-    int32_t at = s.at[lo];
-    const int32_t end = a.table.rows * a.layers - 1;
-    for (lr = lo * s.each; lr < end; ++lr) {
-      const int32_t n = layer_row_tiles(a, lr);
-      if (at + n > t) break;
-      at += n;
+    int32_t pos = s.at[a0] + own * s.items[a0];
+    const int32_t last = a.table.rows * a.layers - 1;
+    for (lr = a0 * s.each; lr < last; ++lr) {
+      const int2 c = layer_row_cost(a, lr);
+      if (pos + c.x + own * c.y > lo) break;
+      pos += c.x + own * c.y;
     }
     enter_row();
     for (g = 0;; ++g) {
       tiles = item_tiles(a, w, lr, g);
-      if (at + tiles > t || g + 1 == a.kv_heads) break;
-      at += tiles;
+      at = pos + own;
+      if (at + tiles * cost > lo || g + 1 == a.kv_heads) break;
+      pos = at + tiles * cost;
     }
-    i0 = t - at;
-  }
-  __device__ __forceinline__ void begin(const TreePrefix& s, int32_t t, int32_t n) {
-    locate(s, t);
-    i1 = min(tiles, i0 + n);
-    left = n - (i1 - i0);
+    i0 = lo > at ? (lo - at + cost - 1) / cost : 0;
+    end_at();
+    if (i0 >= i1) next();
   }
   __device__ __forceinline__ bool next() {
-    if (left == 0) return false;
-    do {
+    for (;;) {
+      at += tiles * cost + own;  // of the next item
+      if (at >= hi) return false;
       if (++g == a.kv_heads) {
         g = 0;
         do {
@@ -315,15 +366,12 @@ struct TreeWalk {
         } while (layer >= layer_count(a, w.n));
       }
       tiles = item_tiles(a, w, lr, g);
-    } while (tiles == 0);
-    i0 = 0;
-    i1 = min(tiles, left);
-    left -= i1;
-    return true;
+      i0 = 0;
+      end_at();
+      if (i1 > 0) return true;
+    }
   }
-  __device__ __forceinline__ int32_t rows_here() const {
-    return min(kPairRows, w.n * a.group - layer * kPairRows);
-  }
+  __device__ __forceinline__ int32_t rows_here() const { return item_rows(a, w, layer); }
 };
 
 // ------------------------------------------------------------ the main kernel
@@ -512,6 +560,33 @@ struct Copier {
     return true;
   }
 };
+
+// Tensor memory in the layout of matrix fragments: 16 lanes x 32 columns; thread t
+// gets, of each 8 columns, columns 2 (t % 4) and the next of lane t / 4 in r[4 k],
+// r[4 k + 1], of lane t / 4 + 8 in the next two.
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+// Four lanes' 4 x 4 words, transposed: word s of lane q is word q of lane s.
+__device__ __forceinline__ void transpose4(uint32_t (&r)[4]) {
+  const int q = threadIdx.x & 3;
+  const bool o1 = q & 1, o2 = q & 2;
+  const uint32_t a = __shfl_xor_sync(0xffffffffu, o1 ? r[0] : r[1], 1);
+  const uint32_t b = __shfl_xor_sync(0xffffffffu, o1 ? r[2] : r[3], 1);
+  const uint32_t s0 = o1 ? a : r[0], s1 = o1 ? r[1] : a, s2 = o1 ? b : r[2], s3 = o1 ? r[3] : b;
+  const uint32_t c = __shfl_xor_sync(0xffffffffu, o2 ? s0 : s2, 2);
+  const uint32_t d = __shfl_xor_sync(0xffffffffu, o2 ? s1 : s3, 2);
+  r[0] = o2 ? c : s0;
+  r[1] = o2 ? d : s1;
+  r[2] = o2 ? s2 : c;
+  r[3] = o2 ? s3 : d;
+}
 
 template <int kRegs>
 __device__ __forceinline__ void more_registers() {
@@ -842,14 +917,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       o[i] = make_uint4(0, 0, 0, 0);
     for (int64_t i = tid; i < n * heads; i += kTreeThreads) a.lse[o0 * heads + i] = -INFINITY;
   }
-  make_tree_prefix(a, prefix);
-  const int32_t runs = min(prefix.total, int32_t(gridDim.x));
+  make_tree_prefix(a, prefix, gridDim.x);
+  const int32_t runs = prefix.runs;
   const int32_t run = blockIdx.x;
   TreeWalk walk(a);
-  if (run < runs) {
-    const int32_t begin = run_start(prefix.total, runs, run);
-    walk.begin(prefix, begin, run_start(prefix.total, runs, run + 1) - begin);
-  }
+  if (run < runs) walk.begin(prefix, run_start(prefix, run), run_start(prefix, run + 1));
   __syncthreads();  // the prefix is read
   if (run < runs) {
     if (warp >= kCopyWarp0 && warp < kSoftWarp0) {
@@ -919,45 +991,52 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       auto pass_turn = [&]() {
         if (lane == 0) mbar_arrive(smem_u32(&bars.turn[x ^ 1][quad]));
       };
-      do {
+      // What the warp knows of its segment.
+      bool split, real, used;
+      int32_t node, qrow, tiles;
+      int64_t base;
+      uint64_t path;
+      // Enters the walk's segment and fetches its queries, once the products with the
+      // ones before them are done: each warp its own rows of its slot's tile, or half of
+      // them where both slots have one.
+      auto enter = [&]() -> bool {
         const int32_t rows = walk.rows_here();
-        const bool split = rows <= kTileRows;
+        split = rows <= kTileRows;
         const int32_t m = (split ? 0 : x * kTileRows) + trow;  // matrix row of the item
-        const bool real = m < rows;
-        const bool used = m - lane < rows;  // a row of the warp is one
+        real = m < rows;
+        used = m - lane < rows;  // a row of the warp is one
         const int32_t mr = walk.layer * kPairRows + (real ? m : 0);
-        const int32_t node = mr / a.group, head = mr - node * a.group;
-        const int64_t base =
-            a.q2k ? list_base(a, walk.row, walk.layer, walk.g, walk.w.t0) : 0;
-        const int tiles = walk.i1 - walk.i0;
-        const int steps = split ? (tiles + 1 - x) / 2 : tiles;
-        bool ok = true;
-        // The queries, once the products with the ones before them are done: each warp
-        // its own rows of its slot's tile, or half of them where both slots have one.
-        if (segs > 0) ok = mbar_wait_warp(smem_u32(&bars.q_empty), (segs - 1) & 1, abort_flag);
+        node = mr / a.group;
+        base = a.q2k ? list_base(a, walk.row, walk.layer, walk.g, walk.w.t0) : 0;
+        tiles = walk.i1 - walk.i0;
+        qrow = (walk.w.t0 + node) * (a.kv_heads * a.group) + walk.g * a.group + mr -
+               node * a.group;
+        if (segs > 0 && !mbar_wait_warp(smem_u32(&bars.q_empty), (segs - 1) & 1, abort_flag))
+          return false;
         ++segs;
-        if (!ok) break;
-        const int32_t qrow = (walk.w.t0 + node) * (a.kv_heads * a.group) + walk.g * a.group + head;
-        {
-          constexpr int kChunks = kDim / 8, kAtOnce = 32 / kChunks;
-          const int sub = lane / kChunks, c = lane % kChunks;
-          const uint32_t tile = sbase + S::kQ + (split ? 0 : x) * S::kTile;
-          const T* q = static_cast<const T*>(a.q) + c * 8;
+        constexpr int kChunks = kDim / 8, kAtOnce = 32 / kChunks;
+        const int sub = lane / kChunks, c = lane % kChunks;
+        const uint32_t tile = sbase + S::kQ + (split ? 0 : x) * S::kTile;
+        const T* q = static_cast<const T*>(a.q) + c * 8;
 #pragma unroll 4
-          for (int i = split ? x * 16 : 0; i < (split ? x * 16 + 16 : 32); i += kAtOnce) {
-            const int32_t from = __shfl_sync(0xffffffffu, real ? qrow : -1, i + sub);
-            cp_async16_zero(tile + tile_at(quad * 32 + i + sub, c),
-                            q + int64_t(max(from, 0)) * kDim, from >= 0);
-          }
-          asm volatile("cp.async.wait_all;" ::: "memory");
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&bars.q_full));
+        for (int i = split ? x * 16 : 0; i < (split ? x * 16 + 16 : 32); i += kAtOnce) {
+          const int32_t from = __shfl_sync(0xffffffffu, real ? qrow : -1, i + sub);
+          cp_async16_zero(tile + tile_at(quad * 32 + i + sub, c),
+                          q + int64_t(max(from, 0)) * kDim, from >= 0);
         }
-        uint64_t path = 0;
+        path = 0;
         // (does the segment reach the drafted tokens?)
         if (a.q2k ? walk.i1 == walk.tiles : int64_t(walk.i1) * kBlock > walk.w.len)
           path = path_of(a, walk.w, node);
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars.q_full));
+        return true;
+      };
+      bool ok = enter(), more = true;
+      while (ok && more) {
+        const int steps = split ? (tiles + 1 - x) / 2 : tiles;
         RowState st{-INFINITY, 0.f};
         for (int k = 0; k < steps; ++k) {
           const int i = split ? 2 * k + x : k;
@@ -1020,9 +1099,17 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           if (lane == 0) mbar_arrive(smem_u32(&bars.p_full[x]));
         }
         if (!ok) break;
+        nt += tiles;
         // ---- results.  Two states of the same rows are joined here, half of the
-        // columns by each slot's warps.
-        const bool two = split && tiles > 1;
+        // columns by each slot's warps.  The next segment begins before, so that its
+        // first products and softmax need not wait for this one's results.
+        const bool was_split = split, two = split && tiles > 1;
+        const bool whole = walk.i0 == 0 && walk.i1 == walk.tiles;
+        // the row's place among the results or the parts, -1: none
+        const int32_t place =
+            !real ? -1
+            : whole ? qrow
+                    : (2 * run + (walk.i0 > 0 ? 0 : 1)) * kPairRows + (split ? 0 : x * kTileRows) + trow;
         float M = st.m, l = st.l, f0 = x == 0 ? 1.f : 0.f, f1 = x == 1 ? 1.f : 0.f;
         if (split) {
           // the states before these are read (a round of the barrier for writing, one
@@ -1031,6 +1118,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           sh.states[x][trow] = make_float2(st.m, st.l);
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&bars.ml));
+        }
+        more = walk.next();
+        if (more && !(ok = enter())) break;
+        if (was_split) {
           if (!mbar_wait_warp(smem_u32(&bars.ml), 0, abort_flag)) break;
           const float2 s0 = sh.states[0][trow], s1 = sh.states[1][trow];
           __syncwarp();
@@ -1041,57 +1132,79 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           f1 = s1.x == -INFINITY ? 0.f : fast_exp2(s1.x - M);
           l = s0.y * f0 + s1.y * f1;
         }
-        const bool use0 = split || x == 0, use1 = two || (!split && x == 1);
+        const bool use0 = was_split || x == 0, use1 = two || (!was_split && x == 1);
         if (use0 && !mbar_wait_warp(smem_u32(&bars.o_full[0]), no[0] & 1, abort_flag)) break;
         if (use1 && !mbar_wait_warp(smem_u32(&bars.o_full[1]), no[1] & 1, abort_flag)) break;
         ++no[0];
-        if (two || !split) ++no[1];
+        if (two || !was_split) ++no[1];
         tc_fence_after();
-        const bool whole = walk.i0 == 0 && walk.i1 == walk.tiles;
-        const int64_t part = (2 * int64_t(run) + (walk.i0 > 0 ? 0 : 1)) * kPairRows + m;
-        const int64_t orow = qrow;
-        const float inv = l == 0.f ? 0.f : 1.f / l;  // l == 0: no key was seen
-        const int c0 = split ? x * (kDim / 2) : 0, c1 = split ? c0 + kDim / 2 : kDim;
+        if (whole) {
+          const float inv = l == 0.f ? 0.f : 1.f / l;  // l == 0: no key was seen
+          f0 *= inv;
+          f1 *= inv;
+        }
+        const int c0 = was_split ? x * (kDim / 2) : 0, c1 = was_split ? c0 + kDim / 2 : kDim;
 #pragma unroll 1
-        for (int c = c0; c < c1; c += 32) {
-          uint32_t u[32], v[32];
-          float o[32];
-          if (use0) tmem_ld32(co + c, u);
-          if (use1) tmem_ld32(co + kDim + c, v);
-          tmem_ld_wait();
-          reg_fence32(u);
-          reg_fence32(v);
+        for (int h = 0; h < 32; h += 16) {  // 16 rows at a time
+          float fa[2], fb[2];               // of lane's rows h + lane / 4 and 8 further
+          int32_t to[2];
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            o[e] = (use0 ? __uint_as_float(u[e]) * f0 : 0.f) +
-                   (use1 ? __uint_as_float(v[e]) * f1 : 0.f);
-          if (!real) continue;
-          if (whole) {
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(a.o) + orow * kDim + c);
+          for (int e = 0; e < 2; ++e) {
+            const int src = h + lane / 4 + 8 * e;
+            fa[e] = __shfl_sync(0xffffffffu, f0, src);
+            fb[e] = __shfl_sync(0xffffffffu, f1, src);
+            to[e] = __shfl_sync(0xffffffffu, place, src);
+          }
+          if (!__any_sync(0xffffffffu, to[0] >= 0 || to[1] >= 0)) continue;
+#pragma unroll 1
+          for (int c = c0; c < c1; c += 32) {
+            uint32_t u[16], v[16];
+            if (use0) tmem_ld_frag(co + (uint32_t(h) << 16) + c, u);
+            if (use1) tmem_ld_frag(co + (uint32_t(h) << 16) + kDim + c, v);
+            tmem_ld_wait();
+            reg_fence16(u);
+            reg_fence16(v);
+            // the lane's row e, columns c + 8 (lane % 4) to + 7
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              dst[e] = make_uint4(Pair<T>::pack(o[8 * e] * inv, o[8 * e + 1] * inv),
-                                  Pair<T>::pack(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
-                                  Pair<T>::pack(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
-                                  Pair<T>::pack(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
-          } else {
-            float4* dst = reinterpret_cast<float4*>(a.part_o + part * kDim + c);
+            for (int e = 0; e < 2; ++e) {
+              uint32_t lo[4], hi[4];
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+              for (int k = 0; k < 4; ++k) {
+                float o[2];
+#pragma unroll
+                for (int z = 0; z < 2; ++z)
+                  o[z] = (use0 ? __uint_as_float(u[4 * k + 2 * e + z]) * fa[e] : 0.f) +
+                         (use1 ? __uint_as_float(v[4 * k + 2 * e + z]) * fb[e] : 0.f);
+                lo[k] = whole ? Pair<T>::pack(o[0], o[1]) : __float_as_uint(o[0]);
+                hi[k] = __float_as_uint(o[1]);
+              }
+              transpose4(lo);
+              const int col = c + 8 * (lane & 3);
+              if (whole) {
+                if (to[e] >= 0)
+                  *reinterpret_cast<uint4*>(static_cast<T*>(a.o) + int64_t(to[e]) * kDim + col) =
+                      make_uint4(lo[0], lo[1], lo[2], lo[3]);
+              } else {
+                transpose4(hi);
+                if (to[e] >= 0) {
+                  uint4* dst = reinterpret_cast<uint4*>(a.part_o + int64_t(to[e]) * kDim + col);
+                  dst[0] = make_uint4(lo[0], hi[0], lo[1], hi[1]);
+                  dst[1] = make_uint4(lo[2], hi[2], lo[3], hi[3]);
+                }
+              }
+            }
           }
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&bars.o_free));
-        if (real && (!split || x == 0)) {
+        if (place >= 0 && (!was_split || x == 0)) {
           if (whole)
-            a.lse[orow] = l == 0.f ? -INFINITY : kLn2 * (M + log2f(l));
+            a.lse[place] = l == 0.f ? -INFINITY : kLn2 * (M + log2f(l));
           else
-            *reinterpret_cast<float2*>(a.part_ml + part * 2) = make_float2(M, l);
+            *reinterpret_cast<float2*>(a.part_ml + int64_t(place) * 2) = make_float2(M, l);
         }
-        nt += tiles;
-      } while (walk.next());
+      }
     }
   }
   // ---------------- teardown
@@ -1116,24 +1229,17 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_tree_join(const TreeArgs
   };
   __shared__ TreePrefix prefix;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  make_tree_prefix(a, prefix);
-  const int32_t total = prefix.total, runs = min(total, int32_t(gridDim.x) + 1);
+  make_tree_prefix(a, prefix, int32_t(gridDim.x) + 1);
   const int32_t run = int32_t(blockIdx.x) + 1;
-  const int32_t begin = run < runs ? run_start(total, runs, run) : 0;
   TreeWalk walk(a);
   walk.i0 = 0;
-  if (run < runs) walk.locate(prefix, begin);
+  if (run < prefix.runs) walk.begin(prefix, run_start(prefix, run), run_start(prefix, run + 1));
   grid_dep_wait();  // every CTA waits: this grid must not end before the runs
   grid_dep_release();
   if (walk.i0 == 0) return;
   // the runs of the item's first and last tile
-  auto run_of = [&](int32_t t) {
-    int32_t c = int32_t(int64_t(t) * runs / total);
-    while (run_start(total, runs, c + 1) <= t) ++c;
-    return c;
-  };
-  const int32_t first = run_of(begin - walk.i0);
-  const int n = run_of(begin - walk.i0 + walk.tiles - 1) + 1 - first;
+  const int32_t first = run_of(prefix, walk.at);
+  const int n = run_of(prefix, walk.at + (walk.tiles - 1) * walk.cost) + 1 - first;
   const int32_t rows = walk.rows_here();
   constexpr int kWarps = kJoinThreads / 32;
   const int share = ((run - first - 1) * gridDim.y + blockIdx.y) * kWarps + warp;
@@ -1303,9 +1409,9 @@ extern "C" msa_status msa_paged_tree(const msa_paged_cache* cache, const msa_pag
       !paged_aligned4(q2k) || !paged_aligned4(lse))
     return MSA_ERR_ALIGNMENT;
   const int32_t group = q_heads / cache->kv_heads, layers = tree_layers(T, group);
-  // tiles are counted in 32 bits
+  // tiles and their cost are counted in 32 bits
   if (int64_t(table->rows) * cache->kv_heads * layers * table->width * cache->page_size >
-      (int64_t(1) << 36))
+      (int64_t(1) << 35))
     return MSA_ERR_INVALID_ARG;
   const TreeLayout at(table->rows, T, cache->kv_heads, group, cache->head_dim);
   if (workspace_bytes < at.total) return MSA_ERR_WORKSPACE;
