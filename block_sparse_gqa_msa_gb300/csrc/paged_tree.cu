@@ -377,8 +377,8 @@ struct TreeWalk {
 // ------------------------------------------------------------ the main kernel
 constexpr int kMaxStages = 4;
 struct TreeBars {
-  uint64_t q_full, q_empty, k_full[kMaxStages], k_empty[kMaxStages], v_full[kMaxStages],
-      v_empty[kMaxStages], s_full[2], p_full[2], o_full[2], o_free, ml, part, turn[2][4], fin[2];
+  uint64_t q_full[2], q_empty, k_full[kMaxStages], k_empty[kMaxStages], v_full[kMaxStages],
+      v_empty[kMaxStages], s_full[2], p_full[2], o_full[2], o_free[2], ml, part, turn[2][4], fin[2];
 };
 struct TreeShared {
   TreeBars bars;
@@ -425,9 +425,8 @@ __device__ __forceinline__ uint32_t tile_at(int row, int chunk) {
 
 // The keys of a tile that a row sees: those of the cached tokens, if it chose them,
 // and of the drafted ones those on its path.
-__device__ __forceinline__ uint4 tile_words(const TileKeys& t, int32_t len, bool chose,
-                                            uint64_t path) {
-  uint32_t w[4];
+__device__ __forceinline__ void tile_words(const TileKeys& t, int32_t len, bool chose,
+                                           uint64_t path, uint32_t (&w)[4]) {
   const int32_t cached = chose ? min(max(len - t.first, 0), kBlock) : 0;
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
@@ -450,7 +449,6 @@ __device__ __forceinline__ uint4 tile_words(const TileKeys& t, int32_t len, bool
     w[2] |= uint32_t(hi);
     w[3] |= uint32_t(hi >> 32);
   }
-  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // The copying warps' side, of keys or of values.
@@ -641,27 +639,56 @@ __device__ __forceinline__ float tree_row_exp(uint32_t cs, float c2, float mref,
 struct RowState {
   float m, l;
 };
-// The same for tiles with masks (the keys whose bit is not set in words give 0) and
-// where the reference has to rise or is not set yet: the maximum first, O (complete
-// up to the slot's step before; there is none where `begins`) and the sum scaled,
-// then the weights, stored over the scores that have been read.  
-template <typename T, int kDim>
-__device__ __forceinline__ RowState tree_masked_tile(uint32_t cs, uint32_t co, uint4 words, float c2,
-                                                  RowState st, bool begins) {
-  float mx = -INFINITY;
+// The row's largest score.
+__device__ __forceinline__ float tree_row_max(uint32_t cs) {
+  float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll 1
   for (int c = 0; c < 4; ++c) {
     uint32_t r[32];
     tmem_ld32(cs + 32 * c, r);
-    const uint32_t w = c == 0 ? words.x : c == 1 ? words.y : c == 2 ? words.z : words.w;
     tmem_ld_wait();
     reg_fence32(r);
 #pragma unroll
-    for (int j = 0; j < 32; j += 2)
-      mx = fmax3(mx, (w >> j) & 1u ? __uint_as_float(r[j]) : -INFINITY,
-                 (w >> j) & 2u ? __uint_as_float(r[j + 1]) : -INFINITY);
+    for (int j = 0; j < 32; j += 4) {
+      m0 = fmax3(m0, __uint_as_float(r[j]), __uint_as_float(r[j + 1]));
+      m1 = fmax3(m1, __uint_as_float(r[j + 2]), __uint_as_float(r[j + 3]));
+    }
   }
-  const float to = mx * c2 - kLift<T>;  // (-infinity without keys)
+  return fmaxf(m0, m1);
+}
+// The same for tiles with masks (the keys whose bit is not set in words give 0) and
+// where the reference has to rise: the maximum first, O (complete up to the slot's step
+// before; there is none where `begins`) and the sum scaled, then the weights, stored
+// over the scores that have been read.
+template <typename T, int kDim>
+__device__ __forceinline__ RowState tree_masked_tile(uint32_t cs, uint32_t co,
+                                                     const uint32_t (&words)[4], float c2,
+                                                     RowState st, bool begins) {
+  // (rolled loops: this code runs a few times in a run, and is fetched each time)
+  uint32_t w[4] = {words[0], words[1], words[2], words[3]};
+  float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    uint32_t r[32];
+    tmem_ld32(cs + 32 * c, r);
+    tmem_ld_wait();
+    reg_fence32(r);
+#pragma unroll
+    for (int j = 0; j < 32; j += 4) {
+      float x[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        x[e] = (w[0] >> (j + e)) & 1u ? __uint_as_float(r[j + e]) : -INFINITY;
+      m0 = fmax3(m0, x[0], x[1]);
+      m1 = fmax3(m1, x[2], x[3]);
+    }
+    const uint32_t next = w[0];
+    w[0] = w[1];
+    w[1] = w[2];
+    w[2] = w[3];
+    w[3] = next;
+  }
+  const float to = fmaxf(m0, m1) * c2 - kLift<T>;  // (-infinity without keys)
   const bool raise = to > st.m + kRise;
   if (__any_sync(0xffffffffu, raise)) {
     const float f = raise ? fast_exp2(st.m - to) : 1.f;
@@ -680,27 +707,32 @@ __device__ __forceinline__ RowState tree_masked_tile(uint32_t cs, uint32_t co, u
       }
     }
   }
-  const float m = st.m == -INFINITY ? 0.f : st.m;
-  float sum = 0.f;
+  const float m = st.m == -INFINITY ? 0.f : -st.m;
+  const uint64_t cc = f2_pack(__float_as_uint(c2), __float_as_uint(c2));
+  const uint64_t nm = f2_pack(__float_as_uint(m), __float_as_uint(m));
+  uint64_t ls[2] = {0ull, 0ull};
 #pragma unroll 1
   for (int c = 0; c < 4; ++c) {
     uint32_t r[32], p[16];
     tmem_ld32(cs + 32 * c, r);
-    const uint32_t w = c == 0 ? words.x : c == 1 ? words.y : c == 2 ? words.z : words.w;
     tmem_ld_wait();
     reg_fence32(r);
 #pragma unroll
     for (int j = 0; j < 32; j += 2) {
-      const float p0 =
-          (w >> j) & 1u ? fast_exp2(fmaf(__uint_as_float(r[j]), c2, -m)) : 0.f;
-      const float p1 =
-          (w >> j) & 2u ? fast_exp2(fmaf(__uint_as_float(r[j + 1]), c2, -m)) : 0.f;
-      sum += p0 + p1;
+      const uint64_t x2 = f2_fma(f2_pack(r[j], r[j + 1]), cc, nm);
+      const float p0 = (w[0] >> j) & 1u ? fast_exp2(f2_lo(x2)) : 0.f;
+      const float p1 = (w[0] >> j) & 2u ? fast_exp2(f2_hi(x2)) : 0.f;
+      ls[(j >> 1) & 1] =
+          f2_add(ls[(j >> 1) & 1], f2_pack(__float_as_uint(p0), __float_as_uint(p1)));
       p[j >> 1] = Pair<T>::pack(p0, p1);
     }
     tmem_st16(cs + 16 * c, p);
+    w[0] = w[1];
+    w[1] = w[2];
+    w[2] = w[3];
   }
-  st.l += sum;
+  const uint64_t s2 = f2_add(ls[0], ls[1]);
+  st.l += f2_lo(s2) + f2_hi(s2);
   return st;
 }
 
@@ -824,13 +856,14 @@ __device__ __forceinline__ void tree_mma_role(const TreeArgs& a, TreeBars& bars,
       }
       commit_one(one, smem_u32(&bars.s_full[x]));
       release(bars.k_empty[stg]);
+      if (x == 0 && i + step >= tiles) commit_one(one, smem_u32(&bars.q_empty));
       return true;
     };
-    ok = wait(bars.q_full, segs);
+    ok = wait(bars.q_full[x], segs) && (!split || wait(bars.q_full[x ^ 1], segs));
     if (ok && first < tiles) ok = issue_s(first);
     for (int i = first; ok && i < tiles; i += step) {
       const uint32_t t = nt + i, stg = t % S::kVStages;
-      if (i == first && segs > 0 && !wait(bars.o_free, segs - 1)) { ok = false; break; }
+      if (i == first && segs > 0 && !wait(bars.o_free[x], segs - 1)) { ok = false; break; }
       if (!wait(bars.v_full[stg], t / S::kVStages) || !wait(bars.p_full[x], np)) { ok = false; break; }
       ++np;
       tc_fence_after();
@@ -846,8 +879,6 @@ __device__ __forceinline__ void tree_mma_role(const TreeArgs& a, TreeBars& bars,
       else
         commit_one(one, smem_u32(&bars.o_full[x]));
     }
-    // this slot is done with the queries
-    commit_one(one, smem_u32(&bars.q_empty));
     nt += tiles;
     ++segs;
   } while (ok && walk.next());
@@ -874,8 +905,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   if (tid == 0) {
     sh.abort = 0;
     auto init = [](uint64_t& b, uint32_t n) { mbar_init(smem_u32(&b), n); };
-    init(bars.q_full, kSoftWarps);
-    init(bars.q_empty, 2);
     for (int i = 0; i < kMaxStages; ++i) {
       init(bars.k_full[i], 1);
       init(bars.k_empty[i], 2);
@@ -886,11 +915,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       init(bars.s_full[i], 1);
       init(bars.p_full[i], 4);
       init(bars.o_full[i], 1);
+      init(bars.o_free[i], kSoftWarps);
+      init(bars.q_full[i], 4);
       init(bars.fin[i], 1);
     }
-    init(bars.o_free, kSoftWarps);
     init(bars.ml, kSoftWarps);
     init(bars.part, 1);
+    init(bars.q_empty, 1);
     for (int i = 0; i < 8; ++i) init(bars.turn[i >> 2][i & 3], 1);
     fence_mbar_init();
   }
@@ -999,7 +1030,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       // Enters the walk's segment and fetches its queries, once the products with the
       // ones before them are done: each warp its own rows of its slot's tile, or half of
       // them where both slots have one.
-      auto enter = [&]() -> bool {
+      auto enter = [&](bool was_split) -> bool {
         const int32_t rows = walk.rows_here();
         split = rows <= kTileRows;
         const int32_t m = (split ? 0 : x * kTileRows) + trow;  // matrix row of the item
@@ -1011,7 +1042,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         tiles = walk.i1 - walk.i0;
         qrow = (walk.w.t0 + node) * (a.kv_heads * a.group) + walk.g * a.group + mr -
                node * a.group;
-        if (segs > 0 && !mbar_wait_warp(smem_u32(&bars.q_empty), (segs - 1) & 1, abort_flag))
+        // Slot x's products with its tile are done: its softmax has read them.  Where slot
+        // B helps to fill A's tile it waits for A's; after a segment that both had on one
+        // tile they have met.
+        if (segs > 0 && x == 1 && split && !was_split &&
+            !mbar_wait_warp(smem_u32(&bars.q_empty), (segs - 1) & 1, abort_flag))
           return false;
         ++segs;
         constexpr int kChunks = kDim / 8, kAtOnce = 32 / kChunks;
@@ -1031,10 +1066,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         asm volatile("cp.async.wait_all;" ::: "memory");
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&bars.q_full));
+        if (lane == 0) mbar_arrive(smem_u32(&bars.q_full[x]));
         return true;
       };
-      bool ok = enter(), more = true;
+      bool ok = enter(false), more = true;
       while (ok && more) {
         const int steps = split ? (tiles + 1 - x) / 2 : tiles;
         RowState st{-INFINITY, 0.f};
@@ -1059,18 +1094,20 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           }
           tc_fence_after();
           // The row's keys in this tile: where all of them are cached, all or none.
-          uint4 words = make_uint4(~0u, ~0u, ~0u, ~0u);
-          bool plain = k > 0;
+          const uint32_t all = chose ? ~0u : 0u;
+          uint32_t words[4] = {all, all, all, all};
+          bool plain = true;
           const uint4 there = sh.there[t & 7];
           if (tk.first + kBlock > walk.w.len || (there.x & there.y & there.z & there.w) != ~0u) {
             plain = false;
-            words = tile_words(tk, walk.w.len, chose, real ? path : 0ull);
-            words.x &= there.x;
-            words.y &= there.y;
-            words.z &= there.z;
-            words.w &= there.w;
-          } else if (!chose) {
-            words = make_uint4(0u, 0u, 0u, 0u);
+            tile_words(tk, walk.w.len, chose, real ? path : 0ull, words);
+            words[0] &= there.x;
+            words[1] &= there.y;
+            words[2] &= there.z;
+            words[3] &= there.w;
+          } else if (k == 0) {  // the first tile sets the reference
+            const float mx = tree_row_max(cs);
+            if (chose) st.m = mx * a.scale_log2 - kLift<T>;
           }
           if (plain) {
             uint32_t pk[64];
@@ -1111,17 +1148,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             : whole ? qrow
                     : (2 * run + (walk.i0 > 0 ? 0 : 1)) * kPairRows + (split ? 0 : x * kTileRows) + trow;
         float M = st.m, l = st.l, f0 = x == 0 ? 1.f : 0.f, f1 = x == 1 ? 1.f : 0.f;
-        if (split) {
+        if (was_split) {
           // the states before these are read (a round of the barrier for writing, one
           // for reading)
           if (joins > 0 && !mbar_wait_warp(smem_u32(&bars.ml), 1, abort_flag)) break;
           sh.states[x][trow] = make_float2(st.m, st.l);
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&bars.ml));
-        }
-        more = walk.next();
-        if (more && !(ok = enter())) break;
-        if (was_split) {
           if (!mbar_wait_warp(smem_u32(&bars.ml), 0, abort_flag)) break;
           const float2 s0 = sh.states[0][trow], s1 = sh.states[1][trow];
           __syncwarp();
@@ -1132,6 +1165,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           f1 = s1.x == -INFINITY ? 0.f : fast_exp2(s1.x - M);
           l = s0.y * f0 + s1.y * f1;
         }
+        more = walk.next();
+        if (more && !(ok = enter(was_split))) break;
         const bool use0 = was_split || x == 0, use1 = two || (!was_split && x == 1);
         if (use0 && !mbar_wait_warp(smem_u32(&bars.o_full[0]), no[0] & 1, abort_flag)) break;
         if (use1 && !mbar_wait_warp(smem_u32(&bars.o_full[1]), no[1] & 1, abort_flag)) break;
@@ -1197,7 +1232,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&bars.o_free));
+        if (lane == 0) {  // O_x counts 8: all warps have read both, or slot x's its own
+          mbar_arrive(smem_u32(&bars.o_free[x]));
+          mbar_arrive(smem_u32(&bars.o_free[was_split ? x ^ 1 : x]));
+        }
         if (place >= 0 && (!was_split || x == 0)) {
           if (whole)
             a.lse[place] = l == 0.f ? -INFINITY : kLn2 * (M + log2f(l));
