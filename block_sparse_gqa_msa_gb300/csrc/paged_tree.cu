@@ -571,21 +571,6 @@ __device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[16]) 
         "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
 }
-// Four lanes' 4 x 4 words, transposed: word s of lane q is word q of lane s.
-__device__ __forceinline__ void transpose4(uint32_t (&r)[4]) {
-  const int q = threadIdx.x & 3;
-  const bool o1 = q & 1, o2 = q & 2;
-  const uint32_t a = __shfl_xor_sync(0xffffffffu, o1 ? r[0] : r[1], 1);
-  const uint32_t b = __shfl_xor_sync(0xffffffffu, o1 ? r[2] : r[3], 1);
-  const uint32_t s0 = o1 ? a : r[0], s1 = o1 ? r[1] : a, s2 = o1 ? b : r[2], s3 = o1 ? r[3] : b;
-  const uint32_t c = __shfl_xor_sync(0xffffffffu, o2 ? s0 : s2, 2);
-  const uint32_t d = __shfl_xor_sync(0xffffffffu, o2 ? s1 : s3, 2);
-  r[0] = o2 ? c : s0;
-  r[1] = o2 ? d : s1;
-  r[2] = o2 ? s2 : c;
-  r[3] = o2 ? s3 : d;
-}
-
 template <int kRegs>
 __device__ __forceinline__ void more_registers() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
@@ -1059,14 +1044,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           cp_async16_zero(tile + tile_at(quad * 32 + i + sub, c),
                           q + int64_t(max(from, 0)) * kDim, from >= 0);
         }
-        path = 0;
-        // (does the segment reach the drafted tokens?)
-        if (a.q2k ? walk.i1 == walk.tiles : int64_t(walk.i1) * kBlock > walk.w.len)
-          path = path_of(a, walk.w, node);
         asm volatile("cp.async.wait_all;" ::: "memory");
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&bars.q_full[x]));
+        path = 0;
+        // (does the segment reach the drafted tokens?)
+        if (a.q2k ? walk.i1 == walk.tiles : int64_t(walk.i1) * kBlock > walk.w.len)
+          path = path_of(a, walk.w, node);
         return true;
       };
       bool ok = enter(false), more = true;
@@ -1199,10 +1184,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             tmem_ld_wait();
             reg_fence16(u);
             reg_fence16(v);
-            // the lane's row e, columns c + 8 (lane % 4) to + 7
+            // (4 lanes' stores are a sector of 32 bytes, or half of one)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              uint32_t lo[4], hi[4];
+              const int64_t at = int64_t(to[e]) * kDim + c + 2 * (lane & 3);
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
                 float o[2];
@@ -1210,22 +1195,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 for (int z = 0; z < 2; ++z)
                   o[z] = (use0 ? __uint_as_float(u[4 * k + 2 * e + z]) * fa[e] : 0.f) +
                          (use1 ? __uint_as_float(v[4 * k + 2 * e + z]) * fb[e] : 0.f);
-                lo[k] = whole ? Pair<T>::pack(o[0], o[1]) : __float_as_uint(o[0]);
-                hi[k] = __float_as_uint(o[1]);
-              }
-              transpose4(lo);
-              const int col = c + 8 * (lane & 3);
-              if (whole) {
-                if (to[e] >= 0)
-                  *reinterpret_cast<uint4*>(static_cast<T*>(a.o) + int64_t(to[e]) * kDim + col) =
-                      make_uint4(lo[0], lo[1], lo[2], lo[3]);
-              } else {
-                transpose4(hi);
-                if (to[e] >= 0) {
-                  uint4* dst = reinterpret_cast<uint4*>(a.part_o + int64_t(to[e]) * kDim + col);
-                  dst[0] = make_uint4(lo[0], hi[0], lo[1], hi[1]);
-                  dst[1] = make_uint4(lo[2], hi[2], lo[3], hi[3]);
-                }
+                if (to[e] < 0) continue;
+                if (whole)
+                  *reinterpret_cast<uint32_t*>(static_cast<T*>(a.o) + at + 8 * k) =
+                      Pair<T>::pack(o[0], o[1]);
+                else
+                  *reinterpret_cast<float2*>(a.part_o + at + 8 * k) = make_float2(o[0], o[1]);
               }
             }
           }
