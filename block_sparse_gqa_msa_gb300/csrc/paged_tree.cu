@@ -97,6 +97,8 @@ struct TreeArgs {
   int32_t* counts;      // q2k: tiles of each item [layers][rows][kv_heads]
   int32_t* ids;         // q2k: its blocks, ascending (list_base)
   uint64_t* who;        // q2k: the tokens that chose them
+  int4* joins;          // of each run that starts inside an item: the item's first
+                        // run, its runs, layer row and key head (runs 0: it does not)
   float* part_ml;       // [2 runs][256][2]: m, l
   float* part_o;        // [2 runs][256][dim]
   int32_t box;          // tokens of a tensor copy (a power of two), 0: none are used
@@ -111,8 +113,7 @@ struct TreeShape {
   static constexpr uint32_t kTmO = 256;  // columns of O_A; O_B kDim further
 };
 
-// A row as the kernels see it; n == 0: nothing to attend for.  (Read past the
-// first-level cache: k_paged_tree_join reads it before its wait.)
+// A row as the kernels see it; n == 0: nothing to attend for.
 struct TreeRow {
   int32_t t0, n, len;
 };
@@ -120,7 +121,7 @@ __device__ __forceinline__ bool row_fits(const TreeArgs& a, int32_t n, int32_t l
   return n <= kNodes && len >= 0 && int64_t(len) + n <= (int64_t(a.table.width) << a.table.shift);
 }
 __device__ __forceinline__ TreeRow tree_row(const TreeArgs& a, int32_t r) {
-  const int32_t o0 = __ldcg(a.offs + r), o1 = __ldcg(a.offs + r + 1), len = __ldcg(a.kv_len + r);
+  const int32_t o0 = a.offs[r], o1 = a.offs[r + 1], len = a.kv_len[r];
   TreeRow v{o0, o1 - o0, len};
   if (o0 < 0 || o1 <= o0 || o1 > a.T || !row_fits(a, o1 - o0, len)) v.n = 0;
   return v;
@@ -214,7 +215,7 @@ __global__ void __launch_bounds__(kListThreads) k_paged_tree_lists(const TreeArg
 // does (4100 and 2500 cycles), and where there are many tiles to a run an item costs
 // kItemCost beside its tiles (its queries, its first and last tile on their own, its
 // results).
-constexpr int kPairCost = 5, kSplitCost = 3, kItemCost = 6;
+constexpr int kPairCost = 5, kSplitCost = 3, kItemCost = 16;
 constexpr int kManyTiles = 8;
 constexpr int kStretches = kTreeThreads;
 struct TreePrefix {
@@ -234,7 +235,7 @@ __device__ __forceinline__ int32_t tile_cost(const TreeArgs& a, const TreeRow& w
 }
 __device__ __forceinline__ int32_t item_tiles(const TreeArgs& a, const TreeRow& w, int32_t lr,
                                               int32_t g) {
-  if (a.q2k) return __ldcg(a.counts + int64_t(lr) * a.kv_heads + g);
+  if (a.q2k) return a.counts[int64_t(lr) * a.kv_heads + g];
   return lr / a.table.rows < layer_count(a, w.n) ? dense_tiles(w) : 0;
 }
 // Tiles' cost and items of a layer row.
@@ -938,6 +939,17 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   const int32_t run = blockIdx.x;
   TreeWalk walk(a);
   if (run < runs) walk.begin(prefix, run_start(prefix, run), run_start(prefix, run + 1));
+  // If the run starts inside an item: the item's first run, its runs, layer row and head.
+  if (tid == kTreeThreads - 1) {
+    int4 join = make_int4(0, 0, 0, 0);
+    if (run < runs && walk.i0 > 0) {
+      join.x = run_of(prefix, walk.at);
+      join.y = run_of(prefix, walk.at + (walk.tiles - 1) * walk.cost) + 1 - join.x;
+      join.z = walk.lr;
+      join.w = walk.g;
+    }
+    a.joins[run] = join;
+  }
   __syncthreads();  // the prefix is read
   if (run < runs) {
     if (warp >= kCopyWarp0 && warp < kSoftWarp0) {
@@ -1230,9 +1242,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 // ------------------------------------------------------------ joining runs
 // CTAs (x, ..) stand for run x + 1, if that run starts inside an item; the CTAs of an
 // item share its rows.  A warp takes kJoinRows rows at a time, its lanes the channels.
-// What follows from the lengths is worked out before the wait for the runs' end.
-// (The lengths are there: k_paged_tree lets this kernel start after its own wait for
-// what came before.)
+// (Where each worked out for itself from the lengths what it joins, that was half of
+// its time.)
 constexpr int kJoinThreads = 256, kJoinRows = 2;
 template <typename T, int kDim>
 __global__ void __launch_bounds__(kJoinThreads) k_paged_tree_join(const TreeArgs a) {
@@ -1240,20 +1251,17 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_tree_join(const TreeArgs
   struct __align__(4 * kPer) Chunk {
     float x[kPer];
   };
-  __shared__ TreePrefix prefix;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  make_tree_prefix(a, prefix, int32_t(gridDim.x) + 1);
   const int32_t run = int32_t(blockIdx.x) + 1;
-  TreeWalk walk(a);
-  walk.i0 = 0;
-  if (run < prefix.runs) walk.begin(prefix, run_start(prefix, run), run_start(prefix, run + 1));
   grid_dep_wait();  // every CTA waits: this grid must not end before the runs
   grid_dep_release();
-  if (walk.i0 == 0) return;
-  // the runs of the item's first and last tile
-  const int32_t first = run_of(prefix, walk.at);
-  const int n = run_of(prefix, walk.at + (walk.tiles - 1) * walk.cost) + 1 - first;
-  const int32_t rows = walk.rows_here();
+  const int4 join = a.joins[run];
+  const int32_t first = join.x;
+  const int n = join.y;
+  if (n == 0) return;
+  const int32_t layer = join.z / a.table.rows, g = join.w;
+  const TreeRow w_row = tree_row(a, join.z - layer * a.table.rows);
+  const int32_t rows = item_rows(a, w_row, layer);
   constexpr int kWarps = kJoinThreads / 32;
   const int share = ((run - first - 1) * gridDim.y + blockIdx.y) * kWarps + warp;
   const int shares = (n - 1) * gridDim.y * kWarps;
@@ -1297,9 +1305,9 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_tree_join(const TreeArgs
 #pragma unroll
     for (int w = 0; w < kJoinRows; ++w) {
       if (m0 + w >= rows) break;
-      const int32_t mr = walk.layer * kPairRows + m0 + w, node = mr / a.group;
-      const int64_t orow = (int64_t(walk.w.t0) + node) * (a.kv_heads * a.group) +
-                           walk.g * a.group + mr - node * a.group;
+      const int32_t mr = layer * kPairRows + m0 + w, node = mr / a.group;
+      const int64_t orow = (int64_t(w_row.t0) + node) * (a.kv_heads * a.group) + g * a.group + mr -
+                           node * a.group;
       const float inv = l[w] == 0.f ? 0.f : 1.f / l[w];
       uint32_t* o = reinterpret_cast<uint32_t*>(static_cast<T*>(a.o) + orow * kDim + lane * kPer);
 #pragma unroll
@@ -1315,7 +1323,7 @@ int32_t tree_layers(int64_t T, int32_t group) {
 }
 // Where things lie in the workspace.
 struct TreeLayout {
-  size_t ml, o, counts, ids, who, total;
+  size_t joins, ml, o, counts, ids, who, total;
   TreeLayout(int32_t rows, int64_t T, int32_t kv_heads, int32_t group, int32_t dim) {
     const size_t lists = size_t(kv_heads) * (size_t(T) + 4 * size_t(rows)) * kTopK;
     size_t at = 0;
@@ -1324,6 +1332,7 @@ struct TreeLayout {
       at = align_up(at + n, 256);
       return was;
     };
+    joins = take(sizeof(int4) * kMaxRuns);
     ml = take(sizeof(float) * 2 * 2 * kMaxRuns * kPairRows);
     o = take(sizeof(float) * 2 * kMaxRuns * kPairRows * size_t(dim));
     counts = take(sizeof(int32_t) * size_t(tree_layers(T, group)) * rows * kv_heads);
@@ -1447,6 +1456,7 @@ extern "C" msa_status msa_paged_tree(const msa_paged_cache* cache, const msa_pag
   a.kv_heads = cache->kv_heads;
   a.group = group;
   a.layers = layers;
+  a.joins = reinterpret_cast<int4*>(ws + at.joins);
   a.part_ml = reinterpret_cast<float*>(ws + at.ml);
   a.part_o = reinterpret_cast<float*>(ws + at.o);
   a.counts = reinterpret_cast<int32_t*>(ws + at.counts);
