@@ -211,19 +211,23 @@ __global__ void __launch_bounds__(kListThreads) k_paged_tree_lists(const TreeArg
 }
 
 // ------------------------------------------------------------ dealing out
-// Runs are equal in cost: a key tile costs 5 where both slots work on it, 3 where one
+// Runs are equal in cost: a key tile costs 8 where both slots work on it, 5 where one
 // does (4100 and 2500 cycles), and where there are many tiles to a run an item costs
 // kItemCost beside its tiles (its queries, its first and last tile on their own, its
-// results).
-constexpr int kPairCost = 5, kSplitCost = 3, kItemCost = 16;
+// results).  Where that leaves enough runs, a run has tiles of one item alone: items
+// are then rounded up to whole runs of 2^kShort, twice or four times as much.
+constexpr int kPairCost = 8, kSplitCost = 5, kItemCost = 26;
 constexpr int kManyTiles = 8;
+constexpr int kShort = 3, kShorts = 3;
+static_assert((1 << kShort) >= kPairCost, "no run is empty");
 constexpr int kStretches = kTreeThreads;
 struct TreePrefix {
   int32_t at[kStretches];     // the cost of tiles before each of a CTA's stretches of
   int32_t items[kStretches];  // layer rows (layer * rows + row), and the items there
-  int2 sums[kTreeThreads / 32];
+  int4 sums[kTreeThreads / 32];
   int32_t total;
   int32_t item;  // an item's own cost
+  int32_t pad;   // log2 of a run's, where items are rounded up to whole runs, or 0
   int32_t runs;
   int32_t each;  // layer rows of a stretch
 };
@@ -238,60 +242,95 @@ __device__ __forceinline__ int32_t item_tiles(const TreeArgs& a, const TreeRow& 
   if (a.q2k) return a.counts[int64_t(lr) * a.kv_heads + g];
   return lr / a.table.rows < layer_count(a, w.n) ? dense_tiles(w) : 0;
 }
-// Tiles' cost and items of a layer row.
-__device__ __forceinline__ int2 layer_row_cost(const TreeArgs& a, int32_t lr) {
+// What an item of so many tiles takes of the runs, its own cost apart.  (kFew: the page
+// table says that there are few tiles; else nothing is rounded up.)
+template <bool kFew>
+__device__ __forceinline__ int32_t item_span(int32_t tiles, int32_t cost, int32_t pad) {
+  return !kFew || pad == 0 || tiles == 0 ? tiles * cost : (((tiles - 1) * cost >> pad) + 1) << pad;
+}
+// The spans and the number of a layer row's items.
+template <bool kFew>
+__device__ __forceinline__ int2 layer_row_cost(const TreeArgs& a, int32_t lr, int32_t pad) {
   const int32_t layer = lr / a.table.rows;
   const TreeRow w = tree_row(a, lr - layer * a.table.rows);
   if (layer >= layer_count(a, w.n)) return make_int2(0, 0);
+  const int32_t cost = tile_cost(a, w, layer);
+  if (!a.q2k) return make_int2(item_span<kFew>(dense_tiles(w), cost, pad) * a.kv_heads, a.kv_heads);
   int32_t n = 0;
-  if (a.q2k) {
-    for (int32_t g = 0; g < a.kv_heads; ++g) n += item_tiles(a, w, lr, g);
-  } else {
-    n = dense_tiles(w) * a.kv_heads;
-  }
-  return make_int2(n * tile_cost(a, w, layer), a.kv_heads);
+  for (int32_t g = 0; g < a.kv_heads; ++g) n += item_span<kFew>(item_tiles(a, w, lr, g), cost, pad);
+  return make_int2(n, a.kv_heads);
 }
+template <bool kFew>
 __device__ __forceinline__ void make_tree_prefix(const TreeArgs& a, TreePrefix& s, int32_t grid) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
   const int32_t all = a.table.rows * a.layers, threads = blockDim.x;
   const int32_t each = (all + threads - 1) / threads;
   const int32_t r0 = min(all, tid * each), r1 = min(all, r0 + each);
-  int2 mine = make_int2(0, 0);
-  for (int32_t r = r0; r < r1; ++r) {
-    const int2 c = layer_row_cost(a, r);
-    mine.x += c.x;
-    mine.y += c.y;
-  }
-  int2 incl = mine;
+  int32_t pad = 0;
+  int2 total;
+  auto sum_up = [&]() {
+    int2 mine = make_int2(0, 0);
+    for (int32_t r = r0; r < r1; ++r) {
+      const int2 c = layer_row_cost<kFew>(a, r, pad);
+      mine.x += c.x;
+      mine.y += c.y;
+    }
+    int2 incl = mine;
+#pragma unroll 1
+    for (int o = 1; o < 32; o <<= 1) {
+      const int32_t x = __shfl_up_sync(0xffffffffu, incl.x, o);
+      const int32_t y = __shfl_up_sync(0xffffffffu, incl.y, o);
+      if (lane >= o) {
+        incl.x += x;
+        incl.y += y;
+      }
+    }
+    if (lane == 31) s.sums[warp] = make_int4(incl.x, incl.y, 0, 0);
+    __syncthreads();
+    int2 before = make_int2(0, 0);
+    total = before;
+    for (int w = 0; w < warps; ++w) {
+      const int4 v = s.sums[w];
+      if (w < warp) {
+        before.x += v.x;
+        before.y += v.y;
+      }
+      total.x += v.x;
+      total.y += v.y;
+    }
+    s.at[tid] = before.x + incl.x - mine.x;
+    s.items[tid] = before.y + incl.y - mine.y;
+  };
+  sum_up();
+  if (kFew && total.x <= grid << (kShort + kShorts - 1)) {
+    // how many runs there would be of each short length
+    int32_t n[kShorts] = {};
+    for (int32_t r = r0; r < r1; ++r)
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int32_t x = __shfl_up_sync(0xffffffffu, incl.x, o);
-    const int32_t y = __shfl_up_sync(0xffffffffu, incl.y, o);
-    if (lane >= o) {
-      incl.x += x;
-      incl.y += y;
+      for (int k = 0; k < kShorts; ++k) n[k] += layer_row_cost<true>(a, r, kShort + k).x >> (kShort + k);
+    __syncthreads();  // the sums are read
+#pragma unroll
+    for (int k = 0; k < kShorts; ++k) n[k] = __reduce_add_sync(0xffffffffu, n[k]);
+    if (lane == 0) s.sums[warp] = make_int4(n[0], n[1], n[2], 0);
+    __syncthreads();
+    int4 sum = make_int4(0, 0, 0, 0);
+    for (int w = 0; w < warps; ++w) {
+      sum.x += s.sums[w].x;
+      sum.y += s.sums[w].y;
+      sum.z += s.sums[w].z;
     }
+    pad = sum.x <= grid ? kShort : sum.y <= grid ? kShort + 1 : sum.z <= grid ? kShort + 2 : 0;
+    __syncthreads();
+    if (pad > 0) sum_up();
   }
-  if (lane == 31) s.sums[warp] = incl;
-  __syncthreads();
-  int2 total = make_int2(0, 0), before = make_int2(0, 0);
-  for (int w = 0; w < warps; ++w) {
-    const int2 v = s.sums[w];
-    if (w < warp) {
-      before.x += v.x;
-      before.y += v.y;
-    }
-    total.x += v.x;
-    total.y += v.y;
-  }
-  s.at[tid] = before.x + incl.x - mine.x;
-  s.items[tid] = before.y + incl.y - mine.y;
   if (tid == 0) {
-    const int32_t item = total.x >= kManyTiles * kPairCost * grid ? kItemCost : 0;
+    const int32_t item = pad == 0 && total.x >= kManyTiles * kPairCost * grid ? kItemCost : 0;
     s.item = item;
+    s.pad = pad;
     s.total = total.x + item * total.y;
     // no run shorter than a tile behind an item's own cost, so that none is empty
-    s.runs = min(s.total > 0 ? max(s.total / (kPairCost + item), 1) : 0, grid);
+    s.runs = pad > 0 ? s.total >> pad
+                     : min(s.total > 0 ? max(s.total / (kPairCost + item), 1) : 0, grid);
     s.each = each;
   }
   __syncthreads();
@@ -307,6 +346,7 @@ __device__ __forceinline__ int32_t run_of(const TreePrefix& s, int32_t at) {
 }
 
 // A walk over the items of a run.  All lanes alike.
+template <bool kFew>
 struct TreeWalk {
   const TreeArgs& a;
   int32_t lr, g;      // layer row and key head of the item
@@ -314,7 +354,7 @@ struct TreeWalk {
   TreeRow w;
   int32_t tiles;      // of the item
   int32_t cost;       // of a tile
-  int32_t own;        // of an item beside its tiles
+  int32_t own, pad;   // as in the prefix
   int32_t at;         // where the item's first tile begins
   int32_t hi;         // the run's end
   int32_t i0, i1;     // the segment
@@ -331,6 +371,7 @@ struct TreeWalk {
   // The first tile that begins at lo or later; there is one before `end`.
   __device__ __forceinline__ void begin(const TreePrefix& s, int32_t lo, int32_t end) {
     own = s.item;
+    pad = s.pad;
     hi = end;
     int a0 = 0, a1 = blockDim.x;  // the last stretch that starts at or before lo
     while (a1 - a0 > 1) {
@@ -340,7 +381,7 @@ struct TreeWalk {
     int32_t pos = s.at[a0] + own * s.items[a0];
     const int32_t last = a.table.rows * a.layers - 1;
     for (lr = a0 * s.each; lr < last; ++lr) {
-      const int2 c = layer_row_cost(a, lr);
+      const int2 c = layer_row_cost<kFew>(a, lr, pad);
       if (pos + c.x + own * c.y > lo) break;
       pos += c.x + own * c.y;
     }
@@ -348,8 +389,8 @@ struct TreeWalk {
     for (g = 0;; ++g) {
       tiles = item_tiles(a, w, lr, g);
       at = pos + own;
-      if (at + tiles * cost > lo || g + 1 == a.kv_heads) break;
-      pos = at + tiles * cost;
+      pos = at + item_span<kFew>(tiles, cost, pad);
+      if (pos > lo || g + 1 == a.kv_heads) break;
     }
     i0 = lo > at ? (lo - at + cost - 1) / cost : 0;
     end_at();
@@ -357,7 +398,7 @@ struct TreeWalk {
   }
   __device__ __forceinline__ bool next() {
     for (;;) {
-      at += tiles * cost + own;  // of the next item
+      at += item_span<kFew>(tiles, cost, pad) + own;  // of the next item
       if (at >= hi) return false;
       if (++g == a.kv_heads) {
         g = 0;
@@ -407,7 +448,8 @@ struct TileKeys {
   bool drafted;   // it may hold drafted tokens
   uint64_t who;   // q2k: which tokens chose it
 };
-__device__ __forceinline__ TileKeys tile_keys(const TreeArgs& a, const TreeWalk& s, int64_t base,
+template <typename Walk>
+__device__ __forceinline__ TileKeys tile_keys(const TreeArgs& a, const Walk& s, int64_t base,
                                               int32_t i) {
   if (!a.q2k) {
     const int32_t f = i * kBlock;
@@ -453,7 +495,7 @@ __device__ __forceinline__ void tile_words(const TileKeys& t, int32_t len, bool 
 }
 
 // The copying warps' side, of keys or of values.
-template <typename T, int kDim>
+template <typename T, int kDim, typename Walk>
 struct Copier {
   using S = TreeShape<kDim>;
   static constexpr int kHalves = kDim / 64;  // tensor copies of a box
@@ -466,7 +508,7 @@ struct Copier {
   // With boxes: the page of the lane's box of a tile, else of key 32 grp + lane, as the
   // table has it (of some key of the row, if that one is not in it: nothing here waits
   // for the load).
-  __device__ __forceinline__ int32_t page(const TreeWalk& s, const TileKeys& t, int grp) const {
+  __device__ __forceinline__ int32_t page(const Walk& s, const TileKeys& t, int grp) const {
     const int32_t at = a.box > 0 ? lane / kHalves * a.box : 32 * grp + lane;
     return a.table.pages[int64_t(s.row) * a.table.stride +
                          (min(t.first + min(at, kBlock - 1), t.end - 1) >> a.table.shift)];
@@ -488,7 +530,7 @@ struct Copier {
   }
   // Fills a tile and has its barrier told when all of it has landed; false: a wait gave
   // up.  p: the lane's page; there: of keys, the mask of those that are.
-  __device__ __forceinline__ bool fill(const TreeWalk& s, const TileKeys& t, int32_t p,
+  __device__ __forceinline__ bool fill(const Walk& s, const TileKeys& t, int32_t p,
                                        uint32_t tile, uint32_t bar, uint4* there, uint64_t& part,
                                        uint32_t& parts, volatile int* abort_flag) const {
     const int32_t mask = (1 << a.table.shift) - 1;
@@ -801,9 +843,9 @@ __device__ __forceinline__ void commit_one(uint32_t one, uint32_t bar) {
 // barrier that is there already takes 100 cycles: with one warp for both slots the
 // tensor cores had nothing to do for half of the time, with one each they work for
 // one slot while the other's warp waits.
-template <typename T, int kDim>
-__device__ __forceinline__ void tree_mma_role(const TreeArgs& a, TreeBars& bars, TreeWalk& walk,
-                                              int x, uint32_t tmem, uint32_t sbase,
+template <typename T, int kDim, typename Walk>
+__device__ __forceinline__ void tree_mma_role(const TreeArgs& a, TreeBars& bars, Walk& walk, int x,
+                                              uint32_t tmem, uint32_t sbase,
                                               volatile int* abort_flag) {
   using S = TreeShape<kDim>;
   constexpr bool kBf = kLift<T> == 0.f;
@@ -872,7 +914,7 @@ __device__ __forceinline__ void tree_mma_role(const TreeArgs& a, TreeBars& bars,
   mbar_wait_drain(smem_u32(&bars.fin[x]), 0);
 }
 
-template <typename T, int kDim>
+template <typename T, int kDim, bool kFew>
 __global__ void __launch_bounds__(kTreeThreads, 1)
     k_paged_tree(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap map_k,
                  const __grid_constant__ CUtensorMap map_v) {
@@ -934,10 +976,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       o[i] = make_uint4(0, 0, 0, 0);
     for (int64_t i = tid; i < n * heads; i += kTreeThreads) a.lse[o0 * heads + i] = -INFINITY;
   }
-  make_tree_prefix(a, prefix, gridDim.x);
+  make_tree_prefix<kFew>(a, prefix, gridDim.x);
   const int32_t runs = prefix.runs;
   const int32_t run = blockIdx.x;
-  TreeWalk walk(a);
+  TreeWalk<kFew> walk(a);
   if (run < runs) walk.begin(prefix, run_start(prefix, run), run_start(prefix, run + 1));
   // If the run starts inside an item: the item's first run, its runs, layer row and head.
   if (tid == kTreeThreads - 1) {
@@ -956,7 +998,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       // ---------------- copies: one warp keys, one values
       fewer_registers<kOtherRegs>();
       const bool values = warp != kCopyWarp0;
-      const Copier<T, kDim> copy{a, values ? a.v : a.k, values ? &map_v : &map_k, values, lane};
+      const Copier<T, kDim, TreeWalk<kFew>> copy{a, values ? a.v : a.k, values ? &map_v : &map_k, values, lane};
       const uint32_t stages = values ? S::kVStages : S::kKStages;
       uint64_t* const full = values ? bars.v_full : bars.k_full;
       uint64_t* const empty = values ? bars.v_empty : bars.k_empty;
@@ -1245,9 +1287,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 // (Where each worked out for itself from the lengths what it joins, that was half of
 // its time.)
 constexpr int kJoinThreads = 256, kJoinRows = 2;
-template <typename T, int kDim>
+template <typename T, int kDim, int kLoads>
 __global__ void __launch_bounds__(kJoinThreads) k_paged_tree_join(const TreeArgs a) {
-  constexpr int kPer = kDim / 32, kLoads = 4;
+  constexpr int kPer = kDim / 32;
   struct __align__(4 * kPer) Chunk {
     float x[kPer];
   };
@@ -1348,9 +1390,9 @@ CUresult make_map_pages(CUtensorMap* m, const void* base, bool bf16, int32_t dim
                         int64_t token_stride, int64_t page_stride, int32_t rows);  // msa_api.cu
 namespace {
 
-template <typename T, int kDim>
-cudaError_t launch_tree(TreeArgs a, cudaStream_t s) {
-  auto kernel = k_paged_tree<T, kDim>;
+template <typename T, int kDim, bool kFew>
+cudaError_t launch_tree_as(TreeArgs a, cudaStream_t s) {
+  auto kernel = k_paged_tree<T, kDim, kFew>;
   static std::atomic<uint64_t> done{0};
   cudaError_t e = allow_smem(kernel, kTreeSmem<kDim>, done);
   if (e != cudaSuccess) return e;
@@ -1387,10 +1429,22 @@ cudaError_t launch_tree(TreeArgs a, cudaStream_t s) {
   const int64_t tokens = (a.T + a.table.rows - 1) / a.table.rows;
   const int64_t rows = int64_t(a.table.rows) * a.kv_heads * std::min<int64_t>(tokens * a.group, kPairRows);
   const int64_t shares = std::min<int64_t>(rows / (grid * 16) + 1, 4);
-  e = launch_k(true, k_paged_tree_join<T, kDim>, dim3(unsigned(grid - 1), unsigned(shares)),
-               dim3(kJoinThreads), 0, s, a);
+  // (few items have many parts: eight at a time)
+  e = launch_k(true, shares == 1 ? k_paged_tree_join<T, kDim, 8> : k_paged_tree_join<T, kDim, 4>,
+               dim3(unsigned(grid - 1), unsigned(shares)), dim3(kJoinThreads), 0, s, a);
   launch_end("paged_tree_join", s);
   return e;
+}
+
+template <typename T, int kDim>
+cudaError_t launch_tree(const TreeArgs& a, cudaStream_t s) {
+  // Few tiles by the table's width: runs of one item alone may do (one row of 2900
+  // tokens 29.7 -> 26.5 us; in larger calls the question alone costs 2.5 us).
+  const int64_t tiles = (int64_t(a.table.width) << a.table.shift) / kBlock + 2;
+  const int64_t most = int64_t(a.layers) * a.table.rows * a.kv_heads * tiles;
+  return most <= int64_t(std::min(device_sm_count(), kMaxRuns)) * 8
+             ? launch_tree_as<T, kDim, true>(a, s)
+             : launch_tree_as<T, kDim, false>(a, s);
 }
 
 bool good_tree(const msa_paged_cache* cache, int32_t rows, int64_t T, int32_t q_heads) {
@@ -1433,7 +1487,7 @@ extern "C" msa_status msa_paged_tree(const msa_paged_cache* cache, const msa_pag
   const int32_t group = q_heads / cache->kv_heads, layers = tree_layers(T, group);
   // tiles and their cost are counted in 32 bits
   if (int64_t(table->rows) * cache->kv_heads * layers * table->width * cache->page_size >
-      (int64_t(1) << 35))
+      (int64_t(1) << 34))
     return MSA_ERR_INVALID_ARG;
   const TreeLayout at(table->rows, T, cache->kv_heads, group, cache->head_dim);
   if (workspace_bytes < at.total) return MSA_ERR_WORKSPACE;

@@ -640,7 +640,7 @@ msa_status msa_norm_rope_backward(const msa_norm_rope_args* args, const void* dq
  *           h / n
  *   row_offsets int32 [rows + 1], kv_len int32 [rows], parents int32 [T] or
  *           NULL, all device; rows * kv_heads * width * page_size of the table,
- *           times ceil(n / 4), <= 2^35
+ *           times ceil(n / 4), <= 2^34
  *   q2k     int32 [kv_heads][T][16] device, or NULL: every cached key.  -1 = an
  *           unused slot; other values outside [0, blocks of the kv_len[r] cached
  *           tokens) set MSA_ERR_BAD_Q2K and are left out
