@@ -835,11 +835,12 @@ def msa_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor,
                   interleaved: bool = False, q_out: torch.Tensor | None = None,
                   k_out: torch.Tensor | None = None, stream=None):
     """Every head of q [T, q_heads, head_dim] and k [T, k_heads, head_dim] (bf16 or
-    fp16, head_dim 64 or 128, each token contiguous, any token stride) scaled to
-    unit mean square, times its weight [head_dim] (fp32 or q's type), then rotated
-    by positions (int32 [T]) as ``msa_paged_append`` rotates; without inv_freq
-    nothing is rotated.  Returns (q_out, k_out), contiguous; q and k themselves
-    may be given for them where they are contiguous.  ``autograd.msa_norm_rope``
+    fp16, head_dim 64 or 128, each token contiguous, tokens any multiple of 8 apart
+    that keeps them from overlapping) scaled to unit mean square, times its weight
+    [head_dim] (fp32 or q's type), then rotated by positions (int32 [T]) as
+    ``msa_paged_append`` rotates; without inv_freq nothing is rotated.  Returns
+    (q_out, k_out), contiguous; q and k themselves may be given for them where they
+    are contiguous.  ``autograd.msa_norm_rope``
     is the differentiable form."""
     args, device, T, heads, kv, dim, dt = _norm_args(q, k, q_weight, k_weight, positions, inv_freq,
                                                      eps, interleaved)

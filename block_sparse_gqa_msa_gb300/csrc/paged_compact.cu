@@ -28,13 +28,11 @@ struct CompactArgs {
 __global__ void __launch_bounds__(kCompactThreads) k_paged_compact(const CompactArgs a) {
   // places (page, slot) of the tokens that move, from and to
   __shared__ int64_t from[2][kMaxPath], to[2][kMaxPath];  // offsets in k and in v
-  __shared__ int32_t moves;
   const int tid = threadIdx.x;
   const int32_t r = blockIdx.x;
   grid_dep_wait();
   grid_dep_release();
   // the first two warps: a token of the path a lane
-  if (tid == 0) moves = 0;
   const int32_t n = a.count[r], len = a.kv_len[r];
   const int32_t* path = a.path + int64_t(r) * a.width;
   const bool fits = n >= 0 && n <= a.width;

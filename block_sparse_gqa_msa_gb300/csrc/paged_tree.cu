@@ -39,7 +39,10 @@
 // tensor copies of up to 64 tokens of a page, a lane each; from smaller pages by
 // copies of 16 bytes.  What lies behind a row's end may be anything: as a key it
 // gives a score that a mask drops, as a value it would meet a weight of 0, so value
-// rows that are not there are zeroed.
+// rows that are not there are zeroed.  So are infinities and NaN in the values of
+// drafted tokens, which not all of the row's tokens see: those that do get them added
+// to their results.  (A look at every tile's values would take longer than its copy;
+// what all cached tokens' values hold is taken as it is.)
 //
 // With q2k a first kernel (k_paged_tree_lists) makes, for each item, the list of
 // the blocks that any of its tokens chose, and which tokens did.
@@ -427,6 +430,9 @@ struct TreeShared {
   // Keys of a tile whose pages are there.  A ring of 8 tiles: keys are six tiles ahead
   // of a slot's softmax at most (those of the tile after its next wait for its next S).
   uint4 there[8];
+  // Drafted tokens of a segment with values that are not finite.  Values are four
+  // segments ahead of one whose results are read at most.
+  uint64_t odd[8];
   float2 states[2][kTileRows];    // (m, l) of the slots, where they are joined
   uint32_t tmem_base;
   int abort;
@@ -525,22 +531,51 @@ struct Copier {
   // Zeros into rows r0 .. r1 - 1 of a tile.
   __device__ __forceinline__ void zero(uint32_t tile, int r0, int r1) const {
     constexpr int kChunks = kDim / 8;
-    for (int i = r0 * kChunks + lane; i < r1 * kChunks; i += 32)
+    for (int i = max(r0, 0) * kChunks + lane; i < r1 * kChunks; i += 32)
       st_shared_v4(tile + tile_at(i / kChunks, i % kChunks), 0, 0, 0, 0);
   }
+  // Zeros over what is not finite in the drafted tokens' values of a tile.  Returns
+  // which tokens had any.
+  __device__ __forceinline__ uint64_t clear(const Walk& s, const TileKeys& t, uint32_t tile) const {
+    constexpr int kChunks = kDim / 8;
+    // all ones in the exponent; one more makes a carry of that
+    constexpr uint32_t kExp = kLift<T> == 0.f ? 0x7f807f80u : 0x7c007c00u;
+    constexpr uint32_t kOne = kLift<T> == 0.f ? 0x00800080u : 0x04000400u;
+    const int off = s.w.len - t.first;  // row of drafted token 0
+    const int r0 = max(off, 0), r1 = min(t.end - t.first, kBlock);
+    uint32_t had[2] = {0u, 0u};
+#pragma unroll 2
+    for (int i = r0 * kChunks + lane; i < r1 * kChunks; i += 32) {
+      const uint32_t at = tile + tile_at(i / kChunks, i % kChunks);
+      uint4 v = ld_shared_v4(at);
+      auto carry = [&](uint32_t w) { return ((w & kExp) + kOne) & 0x80008000u; };
+      if (carry(v.x) | carry(v.y) | carry(v.z) | carry(v.w)) {
+        auto kept = [&](uint32_t w) { return w & ~((carry(w) >> 15) * 0xffffu); };
+        st_shared_v4(at, kept(v.x), kept(v.y), kept(v.z), kept(v.w));
+        const int j = i / kChunks - off;
+        had[j >> 5] |= 1u << (j & 31);
+      }
+    }
+    return uint64_t(__reduce_or_sync(0xffffffffu, had[0])) |
+           uint64_t(__reduce_or_sync(0xffffffffu, had[1])) << 32;
+  }
   // Fills a tile and has its barrier told when all of it has landed; false: a wait gave
-  // up.  p: the lane's page; there: of keys, the mask of those that are.
+  // up.  p: the lane's page; there: of keys, the mask of those that are; odd: of values,
+  // the segment's drafted tokens with some that are not finite.
   __device__ __forceinline__ bool fill(const Walk& s, const TileKeys& t, int32_t p,
                                        uint32_t tile, uint32_t bar, uint4* there, uint64_t& part,
-                                       uint32_t& parts, volatile int* abort_flag) const {
+                                       uint32_t& parts, uint64_t* odd,
+                                       volatile int* abort_flag) const {
     const int32_t mask = (1 << a.table.shift) - 1;
+    const bool drafted = t.drafted && t.end > s.w.len;
     if (a.box > 0) {
       p = checked(t, p, 0);
       const bool bad = __any_sync(0xffffffffu, p == -1);
       const bool mine = p >= 0;
       const int boxes = __popc(__ballot_sync(0xffffffffu, mine)) / kHalves;
-      // values of a tile that is not whole: the rest is zeroed before it is told of
-      const bool rest = values && (t.end - t.first < kBlock || bad);
+      // values of a tile that is not whole, or of drafted tokens: zeros where they belong
+      // before it is told of
+      const bool rest = values && (t.end - t.first < kBlock || bad || drafted);
       const uint32_t to = rest ? smem_u32(&part) : bar;
       if (!values && lane == 0) *there = make_uint4(~0u, ~0u, ~0u, ~0u);
       if (!values && bad) {
@@ -562,13 +597,22 @@ struct Copier {
         tma_load_4d(tile + half * 16384u + b * 128u, map, to, half * 64, s.g, (t.first + b) & mask,
                     p);
       if (rest) {
-        if (!mbar_wait_warp(to, parts++ & 1, abort_flag)) return false;
+        if (!mbar_wait_warp(to, parts++ & 1, abort_flag)) {
+          mbar_wait_drain(to, (parts - 1) & 1);
+          return false;
+        }
         if (bad) {
           for (int l = 0; l < 32; l += kHalves)
             if (__shfl_sync(0xffffffffu, p, l) == -1)
               zero(tile, l / kHalves * a.box, (l / kHalves + 1) * a.box);
         }
         zero(tile, t.end - t.first, kBlock);
+        if (drafted) {
+          if (a.q2k) zero(tile, 0, s.w.len - t.first);
+          __syncwarp();
+          const uint64_t had = clear(s, t, tile);
+          if (lane == 0) *odd |= had;
+        }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar);
@@ -595,6 +639,11 @@ struct Copier {
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
+    if (values && drafted) {
+      __syncwarp();
+      const uint64_t had = clear(s, t, tile);
+      if (lane == 0) *odd |= had;
+    }
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(bar);
@@ -1003,9 +1052,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       uint64_t* const full = values ? bars.v_full : bars.k_full;
       uint64_t* const empty = values ? bars.v_empty : bars.k_empty;
       const uint32_t tiles_at = sbase + (values ? S::kV : S::kK);
-      uint32_t nt = 0, stage = 0, round = 0, parts = 0;
+      uint32_t nt = 0, stage = 0, round = 0, parts = 0, segs = 0;
       bool ok = true;
       do {
+        uint64_t* const odd = &sh.odd[segs++ & 7];
+        if (values && lane == 0) *odd = 0;
         const int64_t base =
             a.q2k ? list_base(a, walk.row, walk.layer, walk.g, walk.w.t0) : 0;
         TileKeys t = tile_keys(a, walk, base, walk.i0);
@@ -1021,7 +1072,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           ok = (round == 0 ||
                 mbar_wait_warp(smem_u32(&empty[stage]), (round - 1) & 1, abort_flag)) &&
                copy.fill(walk, t, page, tiles_at + stage * S::kTile, smem_u32(&full[stage]),
-                         &sh.there[nt & 7], bars.part, parts, abort_flag);
+                         &sh.there[nt & 7], bars.part, parts, odd, abort_flag);
           if (!ok) break;
           if (++stage == stages) {
             stage = 0;
@@ -1204,6 +1255,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           f1 = s1.x == -INFINITY ? 0.f : fast_exp2(s1.x - M);
           l = s0.y * f0 + s1.y * f1;
         }
+        const uint64_t was_path = place >= 0 ? path : 0;
+        const uint64_t* const odd = &sh.odd[(segs - 1) & 7];
+        const int32_t was_row = walk.row, was_g = walk.g, was_len = walk.w.len;
         more = walk.next();
         if (more && !(ok = enter(was_split))) break;
         const bool use0 = was_split || x == 0, use1 = two || (!was_split && x == 1);
@@ -1255,6 +1309,31 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                       Pair<T>::pack(o[0], o[1]);
                 else
                   *reinterpret_cast<float2*>(a.part_o + at + 8 * k) = make_float2(o[0], o[1]);
+              }
+            }
+          }
+        }
+        // Values of drafted tokens on the row's path that are not finite.
+        const uint64_t seen = was_path & *odd;
+        if (__any_sync(0xffffffffu, seen != 0)) {
+          __syncwarp();
+          for (uint64_t left = seen; left != 0; left &= left - 1) {
+            const int64_t key = int64_t(was_len) + __ffsll(static_cast<long long>(left)) - 1;
+            const int32_t page =
+                a.table.pages[was_row * a.table.stride + (key >> a.table.shift)];
+            if (page < 0 || page >= a.table.num_pages) continue;
+            const T* v = static_cast<const T*>(a.v.base) + page * a.v.page + was_g * a.v.head +
+                         (key & ((int64_t(1) << a.table.shift) - 1)) * a.v.token;
+#pragma unroll 1
+            for (int c = c0; c < c1; ++c) {
+              const float add = float(v[c]);
+              if (fabsf(add) <= 3.4e38f) continue;
+              const int64_t at = int64_t(place) * kDim + c;
+              if (whole) {
+                T& o = static_cast<T*>(a.o)[at];
+                o = T(float(o) + add);
+              } else {
+                a.part_o[at] += add;
               }
             }
           }

@@ -653,6 +653,9 @@ msa_status msa_norm_rope_backward(const msa_norm_rope_args* args, const void* dq
  * Weights are rounded to the cache's type before the product with the values
  * (the sum under them is not); all else is 32 bits.  Results are the same from
  * call to call on one device.
+ * Keys that a token does not see may hold anything, and so may the values of
+ * drafted tokens that it does not see.  The cached tokens' values are finite: with
+ * q2k one that is not may reach all tokens of its row.
  * Nothing is written for padding.  A row of more than 64 tokens
  * (MSA_ERR_BAD_TREE) and a row whose kv_len plus tokens do not fit its part of
  * the table (MSA_ERR_BAD_PAGE) get O = 0, LSE = -inf.  A bad parent is taken as

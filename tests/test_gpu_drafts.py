@@ -135,6 +135,69 @@ def test_norm_in_place_and_of_zeros():
     assert (g[0] == 1000).all()
 
 
+def test_norm_strides_and_gradients_that_are_broadcast():
+    gen = _gen(17)
+    wide = _randn(gen, (50, 40, 64), BF)
+    w = (1 + 0.2 * _randn(gen, (64,))).requires_grad_()
+    q = wide[::7, 3:14].detach().requires_grad_()
+    k = wide[10:18, 37:].detach().requires_grad_()
+    pos, freq = _i32([0, -5, 2 ** 29 - 1, 7, 1, 2, -2 ** 29, 3]), _freq(32)
+    with pytest.raises(api.MSAError):  # tokens that overlap are refused
+        api.msa_norm_rope(q, k[:1].expand(8, 3, 64), w, w, pos, freq)
+    outs = autograd.msa_norm_rope(q, k, w, w, pos, freq)
+    gq, gk = _randn(gen, (1, 11, 64), BF).expand(8, 11, 64), _randn(gen, (8, 1, 64), BF).expand(8, 3, 64)
+    got = torch.autograd.grad(outs, (q, k, w), (gq, gk))
+    c = [x.detach().contiguous() for x in (q, k, gq, gk)]
+    assert all(torch.equal(x, y) for x, y in zip(outs, api.msa_norm_rope(*c[:2], w.detach(), w.detach(), pos, freq)))
+    dq, dk, wq, wk = api.msa_norm_rope_backward(c[2], c[3], c[0], c[1], w.detach(), w.detach(), pos, freq)
+    assert torch.equal(got[0], dq) and torch.equal(got[1], dk) and torch.equal(got[2], wq + wk)
+    ref = drafts.norm_rope(_np(q), _np(w), _np(pos), _np(freq), False, float(np.float32(1e-6)))
+    _within(_np(outs[0]), ref, drafts.norm_bound(_np(q), _np(w), ref, 32, False, 1e-6, HALF[BF], TINY[BF]), "y")
+
+
+def test_calls_at_once_and_in_graphs():
+    """Norm, its gradient, verification and compaction on two streams at a time and in a
+    graph whose inputs change between replays."""
+    gen, rng = _gen(18), np.random.default_rng(18)
+    q, k = _randn(gen, (900, 24, 128), BF), _randn(gen, (900, 8, 128), BF)
+    w, pos, freq = 1 + 0.1 * _randn(gen, (128,)), _i32(range(900)), _freq(64)
+    p = torch.softmax(30 * _randn(gen, (30, 9000)), 1)  # most of it in one token
+    tok, offs = _i32(rng.integers(0, 9000, 30)), _i32(range(0, 31, 6))
+    for t in range(30):  # likely drafts
+        tok[t] = p[max(t - 1, 0)].argmax()
+    u, ul = torch.rand(30, generator=gen, device=DEV), torch.rand(5, generator=gen, device=DEV)
+    kc, vc = (_randn(gen, (20, 16, 2, 64), FP) for _ in range(2))
+    tab, lens = _i32(rng.permutation(20).reshape(5, 4)), _i32([3, 40, 0, 17, 31])
+
+    def calls(stream=None):
+        out = list(api.msa_norm_rope(q, k, w, w, pos, freq, stream=stream))
+        out += api.msa_norm_rope_backward(*out, q, k, w, w, pos, freq, stream=stream)
+        path, count, last = api.msa_tree_verify(p, tok, offs, u, ul, max_path=6, stream=stream)
+        with torch.cuda.stream(stream):
+            c = api.PagedCache(kc.clone(), vc.clone())
+        new = api.msa_paged_compact(c, tab, lens, path, count, stream=stream)
+        return out + [path, count, last, new, c.k, c.v]
+
+    here = torch.cuda.current_stream()
+    want = calls(here)
+    assert int(want[7].max()) > 1
+    sides = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for got in [calls(x) for x in sides]:
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = calls(torch.cuda.current_stream())
+    for x in (q, u, kc):  # the step after
+        x.copy_(x.flip(0))
+    graph.replay()
+    torch.cuda.synchronize()
+    now = calls(here)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, now)) and not torch.equal(got[0], want[0])
+
+
 def test_norm_through_training_attention():
     """A step as trained: projection, norm with rotation, attention; the gradient of
     the projection's output is that of the two calls one after the other."""
@@ -254,6 +317,19 @@ def test_tree_rows_of_two_tokens_in_two_items():
     _tree_case(BF, 64, 1, 13, 16, [400], [63], True, seed=10)
 
 
+@pytest.mark.parametrize("seed", range(4))
+def test_tree_rows_of_all_kinds_together(seed):
+    """Rows whose items take both slots next to rows that share a tile, empty ones between
+    them, in tables of any width (few tiles or many by it) and strides."""
+    rng = np.random.default_rng(50 + seed)
+    rows = int(rng.integers(2, 60))
+    trees = [int(rng.choice([0, 1, 2, 8, 9, 16, 17, 33, 64])) for _ in range(rows)]
+    lens = [int(rng.choice([0, 1, 100, 127, 128, 129, 255, 256, 400, 1500])) for _ in range(rows)]
+    _tree_case([BF, FP][seed % 2], [128, 64][seed // 2], int(rng.integers(1, 4)),
+               int(rng.integers(1, 17)), int(rng.choice([4, 8, 16, 64])), lens, trees, seed == 3,
+               pad=seed, seed=60 + seed)
+
+
 @pytest.mark.parametrize("dt", [BF, FP])
 def test_tree_scores_that_grow_along_the_row(dt):
     _tree_case(dt, 128, 1, 16, 64, [3000, 700], [16, 4], False, seed=6, growing=True, scale=0.5)
@@ -343,6 +419,54 @@ def test_tree_bad_input_is_left_out():
     assert torch.isfinite(lse[:5]).all() and (lse[5:] == 7).all()
     o, lse = call(table, [-2, 5, 9], [100, 110], 7)
     assert (lse[:5] == 7).all() and torch.isfinite(lse[5:9]).all() and (lse[9:] == 7).all()
+
+
+@pytest.mark.parametrize("dt,dim,share,S,n,m,sparse", [
+    (BF, 128, 16, 64, 100, 40, False), (FP, 64, 3, 16, 3000, 9, False), (BF, 128, 7, 4, 250, 64, True),
+    (FP, 128, 16, 32, 0, 64, False), (BF, 64, 5, 8, 1000, 21, True), (FP, 128, 2, 256, 9000, 64, True)])
+def test_tree_values_that_are_not_finite_reach_those_who_see_them(dt, dim, share, S, n, m, sparse):
+    rng, gen, kv = np.random.default_rng(m), _gen(m + n), 2
+    lens, trees, offs = [n, 70], [m, 3], [0, m, m + 3]
+    T = m + 3
+    pool, table = _pages(rng, [a + b for a, b in zip(lens, trees)], S)
+    kc, vc = (_pool(gen, pool, S, kv, dim, dt) for _ in range(2))
+    q = _randn(gen, (T, kv * share, dim), dt)
+    parents = _random_parents(rng, m) + [-1, 0, 0]
+    q2k = _choose(rng, lens, offs, T, kv) if sparse else None
+    odd = {}  # token of row 0, key head, channel -> value
+    for i, j in enumerate(rng.choice(m, min(m, 6), replace=False)):
+        for c in rng.choice(dim, 2, replace=False):
+            odd[int(j), i % kv, int(c)] = [float("inf"), -float("inf"), float("nan")][i % 3]
+    place = lambda j: (int(table[0, (n + j) // S]), (n + j) % S)
+    for (j, g, c) in odd:
+        vc[place(j)][g, c] = 0.0
+    scale = dim ** -0.5
+    ref = drafts.tree(_np(kc), _np(vc), _np(q), table, offs, lens, parents,
+                      float(np.float32(scale)), q2k, HALF[dt], TINY[dt])
+    want, bound = ref[0].copy(), ref[2].copy()
+    # also a token that none of the others continues: its keys are not to be seen
+    leaf = [j for j in range(m) if j not in parents[:m]][-1]
+    for (j, g, c), x in odd.items():
+        vc[place(j)][g, c] = x
+        for t in range(m):
+            up = t
+            while up > j:
+                up = parents[up]
+            if up == j:
+                with np.errstate(invalid="ignore"):  # inf - inf
+                    want[t, g * share:(g + 1) * share, c] += x
+    kc[place(leaf)] = float("inf")
+    cache = api.PagedCache(kc, vc)
+    o, lse = api.msa_paged_tree(cache, q, _i32(table), _i32(offs), _i32(lens), scale,
+                                parents=_i32(parents), q2k=None if q2k is None else _i32(q2k))
+    assert api.msa_paged_read_status(cache) == 0
+    rest = [t for t in range(T) if t != leaf]
+    got, want, bound = _np(o)[rest], want[rest], bound[rest]
+    finite = np.isfinite(want)
+    assert not finite.all()
+    assert np.array_equal(got[~finite], want[~finite], equal_nan=True)
+    _within(np.where(finite, got, 0.0), np.where(finite, want, 0.0), np.where(finite, bound, 0.0), "O")
+    _within(_np(lse)[rest], ref[1][rest], ref[3][rest], "LSE")
 
 
 def test_tree_repeats_its_bits_on_streams_and_in_a_graph():
