@@ -65,8 +65,10 @@ constexpr int kSoftWarps = 8, kCopyWarps = 2;
 constexpr int kCopyWarp0 = 2, kSoftWarp0 = kCopyWarp0 + kCopyWarps;
 constexpr int kTreeThreads = (kSoftWarp0 + kSoftWarps) * 32;
 // Registers of a thread: 168 at launch; the softmax warps take over what the first
-// four give up, 128 x 72 + 256 x 216 = 384 x 168.
-constexpr int kSoftRegs = 216, kOtherRegs = 72;
+// four give up, 128 x 136 + 256 x 184 = 384 x 168: none of the roles spills then (with
+// 72 and 216 the warps that issue products do, 32 rows of up to 12000 tokens 163 -> 190
+// us).
+constexpr int kSoftRegs = 184, kOtherRegs = 136;
 // A row's reference m is set by its first tile, kLift below the maximum there.  In
 // whole tiles no maximum is formed: m is raised where the weights sum up to more than
 // kMostSum; in tiles with masks where the maximum is kRise above.  So the state is
@@ -921,10 +923,12 @@ __device__ __forceinline__ void tree_mma_role(const TreeArgs& a, TreeBars& bars,
       commit_one(one, smem_u32(&bar));
       if (split) commit_one(one, smem_u32(&bar));
     };
-    auto issue_s = [&](int i) -> bool {
+    auto key_there = [&](int i) -> bool {
+      const uint32_t t = nt + i;
+      return wait(bars.k_full[t % S::kKStages], t / S::kKStages);
+    };
+    auto issue_s = [&](int i) {
       const uint32_t t = nt + i, stg = t % S::kKStages;
-      if (!wait(bars.k_full[stg], t / S::kKStages)) return false;
-      tc_fence_after();
       const uint64_t bk = dk + stg * kStage;
 #pragma unroll
       for (int kk = 0; kk < kDim / 16; ++kk) {
@@ -934,14 +938,22 @@ __device__ __forceinline__ void tree_mma_role(const TreeArgs& a, TreeBars& bars,
       commit_one(one, smem_u32(&bars.s_full[x]));
       release(bars.k_empty[stg]);
       if (x == 0 && i + step >= tiles) commit_one(one, smem_u32(&bars.q_empty));
-      return true;
     };
     ok = wait(bars.q_full[x], segs) && (!split || wait(bars.q_full[x ^ 1], segs));
-    if (ok && first < tiles) ok = issue_s(first);
+    if (ok && first < tiles) {
+      ok = key_there(first);
+      tc_fence_after();
+      if (ok) issue_s(first);
+    }
     for (int i = first; ok && i < tiles; i += step) {
       const uint32_t t = nt + i, stg = t % S::kVStages;
       if (i == first && segs > 0 && !wait(bars.o_free[x], segs - 1)) { ok = false; break; }
-      if (!wait(bars.v_full[stg], t / S::kVStages) || !wait(bars.p_full[x], np)) { ok = false; break; }
+      // (the next keys have long been there: asked for behind P they cost their wait)
+      if (!wait(bars.v_full[stg], t / S::kVStages) ||
+          (i + step < tiles && !key_there(i + step)) || !wait(bars.p_full[x], np)) {
+        ok = false;
+        break;
+      }
       ++np;
       tc_fence_after();
       const uint64_t bv = dv + stg * kStage;
@@ -952,7 +964,7 @@ __device__ __forceinline__ void tree_mma_role(const TreeArgs& a, TreeBars& bars,
       release(bars.v_empty[stg]);
       // (products of one thread run in order: S may overwrite P)
       if (i + step < tiles)
-        ok = issue_s(i + step);
+        issue_s(i + step);
       else
         commit_one(one, smem_u32(&bars.o_full[x]));
     }
@@ -1168,57 +1180,59 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           const uint32_t t = nt + i;
           const TileKeys tk = tile_keys(a, walk, base, walk.i0 + i);
           const bool chose = real && ((tk.who >> node) & 1);
-          if (!mbar_wait_warp(smem_u32(&bars.s_full[x]), nx & 1, abort_flag)) {
+          // (the turn first: it has come before S, so that its wait costs nothing)
+          if ((!split && !my_turn()) ||
+              !mbar_wait_warp(smem_u32(&bars.s_full[x]), nx & 1, abort_flag)) {
             ok = false;
             break;
           }
           ++nx;
-          if (!split && !my_turn()) {
-            ok = false;
-            break;
-          }
           if (!used) {  // no row of the warp is one: what P holds there does not matter
             if (!split) pass_turn();
             if (lane == 0) mbar_arrive(smem_u32(&bars.p_full[x]));
             continue;
           }
           tc_fence_after();
-          // The row's keys in this tile: where all of them are cached, all or none.
-          const uint32_t all = chose ? ~0u : 0u;
-          uint32_t words[4] = {all, all, all, all};
-          bool plain = true;
+          // Tiles of cached keys alone: a row sees all of them or none.  Whether all are there
+          // is looked at behind the weights, by when it has been read.
           const uint4 there = sh.there[t & 7];
-          if (tk.first + kBlock > walk.w.len || (there.x & there.y & there.z & there.w) != ~0u) {
-            plain = false;
-            tile_words(tk, walk.w.len, chose, real ? path : 0ull, words);
-            words[0] &= there.x;
-            words[1] &= there.y;
-            words[2] &= there.z;
-            words[3] &= there.w;
-          } else if (k == 0) {  // the first tile sets the reference
-            const float mx = tree_row_max(cs);
-            if (chose) st.m = mx * a.scale_log2 - kLift<T>;
+          auto complete = [&]() { return (there.x & there.y & there.z & there.w) == ~0u; };
+          bool plain = tk.first + kBlock <= walk.w.len;
+          if (plain && k == 0) {  // the first tile sets the reference
+            plain = complete();
+            if (plain) {
+              const float mx = tree_row_max(cs);
+              if (chose) st.m = mx * a.scale_log2 - kLift<T>;
+            }
           }
           if (plain) {
             uint32_t pk[64];
             const float ls = tree_row_exp<T>(cs, a.scale_log2, st.m, pk);
             // The sum tells when the reference has to rise (it is infinite where the row
             // has seen no key so far).
-            plain = !__any_sync(0xffffffffu, chose && !(ls <= kMostSum<T>));
-            if (plain) {
-              if (!chose) {
+            const bool low = ls <= kMostSum<T>;
+            if (!__all_sync(0xffffffffu, chose && low && complete())) {
+              plain = complete() && !__any_sync(0xffffffffu, chose && !low);
 #pragma unroll
-                for (int e = 0; e < 64; ++e) pk[e] = 0u;
-              } else {
-                st.l += ls;
-              }
+              for (int e = 0; e < 64; ++e) pk[e] = chose ? pk[e] : 0u;
+            }
+            if (plain) {
+              if (chose) st.l += ls;
               // P over the first 64 columns of S (all of S has been read)
               tmem_st32_nc(cs, *reinterpret_cast<const uint32_t(*)[32]>(&pk[0]));
               tmem_st32_nc(cs + 32, *reinterpret_cast<const uint32_t(*)[32]>(&pk[32]));
             }
           }
-          if (!plain)
+          if (!plain) {
+            const uint32_t all = chose ? ~0u : 0u;
+            uint32_t words[4] = {all, all, all, all};
+            tile_words(tk, walk.w.len, chose, real ? path : 0ull, words);
+            words[0] &= there.x;
+            words[1] &= there.y;
+            words[2] &= there.z;
+            words[3] &= there.w;
             st = tree_masked_tile<T, kDim>(cs, co + kDim * x, words, a.scale_log2, st, k == 0);
+          }
           if (!split) pass_turn();
           tmem_st_wait();
           tc_fence_before();
