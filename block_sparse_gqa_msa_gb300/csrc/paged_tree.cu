@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(kListThreads) k_paged_tree_lists(const TreeArg
 // kItemCost beside its tiles (its queries, its first and last tile on their own, its
 // results).  Where that leaves enough runs, a run has tiles of one item alone: items
 // are then rounded up to whole runs of 2^kShort, twice or four times as much.
-constexpr int kPairCost = 8, kSplitCost = 5, kItemCost = 26;
+constexpr int kPairCost = 8, kSplitCost = 5, kItemCost = 34;
 constexpr int kManyTiles = 8;
 constexpr int kShort = 3, kShorts = 3;
 static_assert((1 << kShort) >= kPairCost, "no run is empty");
@@ -516,10 +516,9 @@ struct Copier {
   // With boxes: the page of the lane's box of a tile, else of key 32 grp + lane, as the
   // table has it (of some key of the row, if that one is not in it: nothing here waits
   // for the load).
-  __device__ __forceinline__ int32_t page(const Walk& s, const TileKeys& t, int grp) const {
+  __device__ __forceinline__ int32_t page(const int32_t* pages, const TileKeys& t, int grp) const {
     const int32_t at = a.box > 0 ? lane / kHalves * a.box : 32 * grp + lane;
-    return a.table.pages[int64_t(s.row) * a.table.stride +
-                         (min(t.first + min(at, kBlock - 1), t.end - 1) >> a.table.shift)];
+    return pages[min(t.first + min(at, kBlock - 1), t.end - 1) >> a.table.shift];
   }
   // Such a page; -1: not one of the pool; kNoKey: the key is not in the row.
   static constexpr int32_t kNoKey = INT32_MIN;
@@ -564,7 +563,7 @@ struct Copier {
   // Fills a tile and has its barrier told when all of it has landed; false: a wait gave
   // up.  p: the lane's page; there: of keys, the mask of those that are; odd: of values,
   // the segment's drafted tokens with some that are not finite.
-  __device__ __forceinline__ bool fill(const Walk& s, const TileKeys& t, int32_t p,
+  __device__ __forceinline__ bool fill(const Walk& s, const int32_t* pages, const TileKeys& t, int32_t p,
                                        uint32_t tile, uint32_t bar, uint4* there, uint64_t& part,
                                        uint32_t& parts, uint64_t* odd,
                                        volatile int* abort_flag) const {
@@ -599,16 +598,19 @@ struct Copier {
         tma_load_4d(tile + half * 16384u + b * 128u, map, to, half * 64, s.g, (t.first + b) & mask,
                     p);
       if (rest) {
-        if (!mbar_wait_warp(to, parts++ & 1, abort_flag)) {
-          mbar_wait_drain(to, (parts - 1) & 1);
-          return false;
-        }
+        // what no box covers now, the rest of the last one when it is there
+        const int end = t.end - t.first, covered = (end + a.box - 1) & -a.box;
+        zero(tile, covered, kBlock);
         if (bad) {
           for (int l = 0; l < 32; l += kHalves)
             if (__shfl_sync(0xffffffffu, p, l) == -1)
               zero(tile, l / kHalves * a.box, (l / kHalves + 1) * a.box);
         }
-        zero(tile, t.end - t.first, kBlock);
+        if (!mbar_wait_warp(to, parts++ & 1, abort_flag)) {
+          mbar_wait_drain(to, (parts - 1) & 1);
+          return false;
+        }
+        zero(tile, end, covered);
         if (drafted) {
           if (a.q2k) zero(tile, 0, s.w.len - t.first);
           __syncwarp();
@@ -625,7 +627,7 @@ struct Copier {
     const int sub = lane / kChunks, c = lane % kChunks;
     const T* base = static_cast<const T*>(pool.base) + s.g * pool.head + c * 8;
     for (int grp = 0; grp < kBlock / 32; ++grp) {
-      if (grp > 0) p = page(s, t, grp);
+      if (grp > 0) p = page(pages, t, grp);
       p = checked(t, p, grp);
       const uint32_t lost = __ballot_sync(0xffffffffu, p == -1);
       if (!values && lane == 0) reinterpret_cast<uint32_t*>(there)[grp] = ~lost;
@@ -1072,18 +1074,19 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         const int64_t base =
             a.q2k ? list_base(a, walk.row, walk.layer, walk.g, walk.w.t0) : 0;
         TileKeys t = tile_keys(a, walk, base, walk.i0);
-        int32_t page = copy.page(walk, t, 0);
+        const int32_t* const pages = a.table.pages + walk.row * a.table.stride;
+        int32_t page = copy.page(pages, t, 0);
         for (int32_t i = walk.i0; i < walk.i1; ++i, ++nt) {
           // the pages of the next tile, while this one is waited for
           TileKeys t1 = t;
           int32_t page1 = 0;
           if (i + 1 < walk.i1) {
             t1 = tile_keys(a, walk, base, i + 1);
-            page1 = copy.page(walk, t1, 0);
+            page1 = copy.page(pages, t1, 0);
           }
           ok = (round == 0 ||
                 mbar_wait_warp(smem_u32(&empty[stage]), (round - 1) & 1, abort_flag)) &&
-               copy.fill(walk, t, page, tiles_at + stage * S::kTile, smem_u32(&full[stage]),
+               copy.fill(walk, pages, t, page, tiles_at + stage * S::kTile, smem_u32(&full[stage]),
                          &sh.there[nt & 7], bars.part, parts, odd, abort_flag);
           if (!ok) break;
           if (++stage == stages) {
