@@ -16,6 +16,11 @@
 // copies its own channels into its own places of a ring in shared memory, 8 KB a
 // warp ahead of the sums, across tokens; 128 KB an SM are on their way at any
 // time, and no registers are held for them.
+//
+// Measured (16384 tokens of 64 + 4 heads of 128 channels): 93 us forward, 6.1 TB/s,
+// and 141 the gradient, 6.1 TB/s, of a plain copy's 6.8; 9 tokens of 24 + 8 heads
+// of 64 channels 3.1 us.  With the loads in registers, a head's at a time, the two
+// took 300 us together instead of 265.
 #include <algorithm>
 
 #include "paged.cuh"

@@ -21,6 +21,13 @@
 // exact two-sums), which are put together in 64 bits once a warp: 2^-40 of the
 // sum at worst.  The drawn token's run is then added again, finer, until a warp
 // looks at 32 values at a time.
+//
+// Measured: one row, 32000 tokens in the vocabulary, 9.5 us; 40 rows, 100003, no q,
+// 15.9; 128 rows, 151000, with q, 54 to 63 (125 MB, two passes in the longest rows).
+// A pass of a row by itself takes about 20 us there: a value costs 14 to 20
+// instructions, and eight loads of a lane are on their way at a time.  16 bytes a load
+// are as fast; a ring of asynchronous copies (80 to 100 us) and loads kept in
+// registers for the next step (84, they spill) are slower.
 #include <cooperative_groups.h>
 
 #include <algorithm>
