@@ -874,7 +874,8 @@ def msa_norm_rope_backward(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.
         ctypes.byref(args), gq, gk, dqp, dkp, dw.data_ptr(), dw.data_ptr() + 4 * dim,
         _arg(workspace, "workspace", torch.uint8, (nbytes,), device), nbytes, _stream(stream)),
         "msa_norm_rope_backward")
-    return dq, dk, dw[0], dw[1]
+    dq_weight, dk_weight = dw.unbind(0)
+    return dq, dk, dq_weight, dk_weight
 
 
 # ---------------------------------------------------------------- drafted tokens

@@ -84,7 +84,9 @@ class NormRopeFunction(torch.autograd.Function):
         dq, dk, dwq, dwk = api.msa_norm_rope_backward(
             dq_out.contiguous(), dk_out.contiguous(), q, k, q_weight, k_weight, positions,
             inv_freq, eps=ctx.eps, interleaved=ctx.interleaved)
-        return (dq, dk, dwq.to(q_weight.dtype), dwk.to(k_weight.dtype), None, None, None, None)
+        if q_weight.dtype is not torch.float32:
+            dwq, dwk = dwq.to(q_weight.dtype), dwk.to(k_weight.dtype)
+        return dq, dk, dwq, dwk, None, None, None, None
 
 
 def msa_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor,
