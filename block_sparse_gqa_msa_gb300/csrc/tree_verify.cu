@@ -23,7 +23,7 @@
 // looks at 32 values at a time.
 //
 // Measured: one row, 32000 tokens in the vocabulary, 9.5 us; 40 rows, 100003, no q,
-// 15.9; 128 rows, 151000, with q, 54 to 63 (125 MB, two passes in the longest rows).
+// 15.9; 128 rows, 151000, with q, 53 to 56 (125 MB, two passes in the longest rows).
 // A pass of a row by itself takes about 20 us there: a value costs 14 to 20
 // instructions, and eight loads of a lane are on their way at a time.  16 bytes a load
 // are as fast; a ring of asynchronous copies (80 to 100 us) and loads kept in
@@ -42,6 +42,7 @@ constexpr int kVerWarps = 16;
 constexpr int kVerThreads = kVerWarps * 32;
 constexpr int kVerCluster = 8;
 constexpr int kVerLoads = 8;  // values of each distribution that a lane has in flight
+constexpr int kVerRun = 24576;  // values of a CTA in calls of more rows than fit the chip
 
 struct VerifyArgs {
   const float *target, *draft;  // draft may be null
@@ -410,11 +411,16 @@ extern "C" msa_status msa_tree_verify(const float* target, int64_t target_stride
   a.T = T;
   a.vocab = vocab;
   a.max_path = max_path;
-  // as many CTAs a row as are on the chip at once (2 an SM), none with less than
-  // a pass of its loads to do
+  // As many CTAs a row as are on the chip at once (2 an SM), none with less than a pass
+  // of its loads to do.  With q, where rows of several passes keep the others waiting,
+  // twice as many where each still has kVerRun values: half of the rows begin as others
+  // end (100 rows, 151000 tokens: 61 -> 49 us, 200 rows, 65536: 57 -> 42; below it
+  // 128 rows, 40000: 26 -> 29; without q 128 rows, 151000: 34 -> 38).
+  auto chip = [&](int n) { return int64_t(rows) * n <= int64_t(device_sm_count()) * 2; };
   int cluster = 1;
-  while (cluster < kVerCluster && int64_t(rows) * cluster * 2 <= int64_t(device_sm_count()) * 2 &&
-         vocab >= cluster * 2 * kVerThreads * 4)
+  while (cluster < kVerCluster && vocab >= cluster * 2 * kVerThreads * 4 &&
+         (chip(cluster * 2) ||
+          (draft && chip(cluster) && vocab >= int64_t(cluster) * 2 * kVerRun)))
     cluster *= 2;
   a.cluster = cluster;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);

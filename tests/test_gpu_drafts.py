@@ -550,6 +550,7 @@ def _verify_case(rows, trees, V, drawn, chain, seed, sharp=1.0, skew=0, max_path
     (40, [5] * 40, 5000, False, 2.0, 0),
     (600, [3] * 600, 1, True, 1.0, 0),
     (200, [4] * 200, 7, False, 1.0, 1),
+    (160, [1, 3, 5, 4] * 40, 49161, False, 2.0, 1),  # more CTAs than the chip holds
 ])
 def test_verify_matches_the_definition(rows, trees, V, chain, sharp, skew, drawn):
     _verify_case(rows, trees, V, drawn, chain, rows + V, sharp, skew)
