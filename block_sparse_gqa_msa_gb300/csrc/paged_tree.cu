@@ -225,9 +225,10 @@ __global__ void __launch_bounds__(kListThreads) k_paged_tree_lists(const TreeArg
 
 // ------------------------------------------------------------ dealing out
 // Runs are equal in cost: a key tile costs 8 where both slots work on it, 5 where one
-// does (4100 and 2500 cycles), and where there are many tiles to a run an item costs
+// does (3500 and 2200 cycles), and where there are many tiles to a run an item costs
 // kItemCost beside its tiles (its queries, its first and last tile on their own, its
-// results).  Where that leaves enough runs, a run has tiles of one item alone: items
+// results; 18 for 34: 43 rows of small trees 102 -> 106 us, 32 rows of up to 12000 tokens
+// 160 -> 166).  Where that leaves enough runs, a run has tiles of one item alone: items
 // are then rounded up to whole runs of 2^kShort, twice or four times as much.
 constexpr int kPairCost = 8, kSplitCost = 5, kItemCost = 34;
 constexpr int kManyTiles = 8;
