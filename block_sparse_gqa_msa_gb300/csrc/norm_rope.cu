@@ -252,7 +252,9 @@ __global__ void __launch_bounds__(kNormThreads, 1) k_norm_rope(const NormArgs a)
     float ss = 0.f;
 #pragma unroll
     for (int i = 0; i < 16; ++i) ss = fmaf(x[i], x[i], ss);
-    const float n = rsqrtf(head_sum<kLanes>(ss) * (1.f / kDim) + a.eps);
+    // (lanes without a head add nothing to the weights' gradients, for eps = 0 neither)
+    const float mean = head_sum<kLanes>(ss) * (1.f / kDim);
+    const float n = real ? rsqrtf(mean + a.eps) : 0.f;
     if (!kBack) {
 #pragma unroll
       for (int i = 0; i < 16; i += 4) {

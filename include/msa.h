@@ -569,7 +569,8 @@ msa_status msa_paged_decode(const msa_paged_cache* cache, const msa_page_table* 
  *   interleaved as for msa_paged_append
  *   q_out, k_out  contiguous; may be q or k itself where that is contiguous
  * Sums, norms and rotation are 32 bits, angles 64, and each result is rounded
- * once.  eps >= 0, finite; 1 <= T <= 2^20.
+ * once.  eps >= 0, finite (with eps = 0 a head of zeros gives NaN, as the formula
+ * does); 1 <= T <= 2^20.
  *
  * The backward takes the gradients dq_out, dk_out (contiguous) of the results,
  * with q and k as the forward got them, and returns
