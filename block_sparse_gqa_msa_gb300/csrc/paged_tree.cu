@@ -1066,56 +1066,60 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   }
   __syncthreads();  // the prefix is read
   if (run < runs) {
-    if (warp >= kCopyWarp0 && warp < kSoftWarp0) {
-      // ---------------- copies: one warp keys, one values
+    if (warp < kSoftWarp0) {
+      // (one instruction for the group of warps, in front of its roles: PTX asks for that)
       fewer_registers<kOtherRegs>();
-      const bool values = warp != kCopyWarp0;
-      const Copier<T, kDim, TreeWalk<kFew>> copy{a, values ? a.v : a.k, values ? &map_v : &map_k, values, lane};
-      const uint32_t stages = values ? S::kVStages : S::kKStages;
-      uint64_t* const full = values ? bars.v_full : bars.k_full;
-      uint64_t* const empty = values ? bars.v_empty : bars.k_empty;
-      const uint32_t tiles_at = sbase + (values ? S::kV : S::kK);
-      uint32_t nt = 0, stage = 0, round = 0, parts = 0, segs = 0;
-      bool ok = true;
-      do {
-        uint64_t* const odd = &sh.odd[segs++ & 7];
-        if (values && lane == 0) *odd = 0;
-        const int64_t base =
-            a.q2k ? list_base(a, walk.row, walk.layer, walk.g, walk.w.t0) : 0;
-        TileKeys t = tile_keys(a, walk, base, walk.i0);
-        const int32_t* const pages = a.table.pages + walk.row * a.table.stride;
-        int32_t page = copy.page(pages, t, 0);
-        for (int32_t i = walk.i0; i < walk.i1; ++i, ++nt) {
-          // the pages of the next tile, while this one is waited for
-          TileKeys t1 = t;
-          int32_t page1 = 0;
-          if (i + 1 < walk.i1) {
-            t1 = tile_keys(a, walk, base, i + 1);
-            page1 = copy.page(pages, t1, 0);
+      if (warp >= kCopyWarp0) {
+        // ---------------- copies: one warp keys, one values
+        const bool values = warp != kCopyWarp0;
+        const Copier<T, kDim, TreeWalk<kFew>> copy{a, values ? a.v : a.k,
+                                                   values ? &map_v : &map_k, values, lane};
+        const uint32_t stages = values ? S::kVStages : S::kKStages;
+        uint64_t* const full = values ? bars.v_full : bars.k_full;
+        uint64_t* const empty = values ? bars.v_empty : bars.k_empty;
+        const uint32_t tiles_at = sbase + (values ? S::kV : S::kK);
+        uint32_t nt = 0, stage = 0, round = 0, parts = 0, segs = 0;
+        bool ok = true;
+        do {
+          uint64_t* const odd = &sh.odd[segs++ & 7];
+          if (values && lane == 0) *odd = 0;
+          const int64_t base =
+              a.q2k ? list_base(a, walk.row, walk.layer, walk.g, walk.w.t0) : 0;
+          TileKeys t = tile_keys(a, walk, base, walk.i0);
+          const int32_t* const pages = a.table.pages + walk.row * a.table.stride;
+          int32_t page = copy.page(pages, t, 0);
+          for (int32_t i = walk.i0; i < walk.i1; ++i, ++nt) {
+            // the pages of the next tile, while this one is waited for
+            TileKeys t1 = t;
+            int32_t page1 = 0;
+            if (i + 1 < walk.i1) {
+              t1 = tile_keys(a, walk, base, i + 1);
+              page1 = copy.page(pages, t1, 0);
+            }
+            ok = (round == 0 ||
+                  mbar_wait_warp(smem_u32(&empty[stage]), (round - 1) & 1, abort_flag)) &&
+                 copy.fill(walk, pages, t, page, tiles_at + stage * S::kTile,
+                           smem_u32(&full[stage]), &sh.there[nt & 7], bars.part, parts, odd,
+                           abort_flag);
+            if (!ok) break;
+            if (++stage == stages) {
+              stage = 0;
+              ++round;
+            }
+            t = t1;
+            page = page1;
           }
-          ok = (round == 0 ||
-                mbar_wait_warp(smem_u32(&empty[stage]), (round - 1) & 1, abort_flag)) &&
-               copy.fill(walk, pages, t, page, tiles_at + stage * S::kTile, smem_u32(&full[stage]),
-                         &sh.there[nt & 7], bars.part, parts, odd, abort_flag);
-          if (!ok) break;
-          if (++stage == stages) {
-            stage = 0;
-            ++round;
+        } while (ok && walk.next());
+        if (!ok) {  // let tensor copies land before the CTA ends
+          for (uint32_t n = 0; n < stages; ++n) {
+            const uint32_t st = (stage + n) % stages, r = st >= stage ? round - 1 : round;
+            if (st < stage || round > 0) mbar_wait_drain(smem_u32(&full[st]), r & 1);
           }
-          t = t1;
-          page = page1;
         }
-      } while (ok && walk.next());
-      if (!ok) {  // let tensor copies land before the CTA ends
-        for (uint32_t n = 0; n < stages; ++n) {
-          const uint32_t st = (stage + n) % stages, r = st >= stage ? round - 1 : round;
-          if (st < stage || round > 0) mbar_wait_drain(smem_u32(&full[st]), r & 1);
-        }
+      } else {
+        // ---------------- tensor cores
+        tree_mma_role<T, kDim>(a, bars, walk, warp, tmem, sbase, abort_flag);
       }
-    } else if (warp < kCopyWarp0) {
-      // ---------------- tensor cores
-      fewer_registers<kOtherRegs>();
-      tree_mma_role<T, kDim>(a, bars, walk, warp, tmem, sbase, abort_flag);
     } else {
       // ---------------- softmax and results of slot x (warps 4-7: A, 8-11: B)
       more_registers<kSoftRegs>();
