@@ -43,8 +43,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
 def build_starve(force: bool = False, verbose: bool = False) -> str:
     """A TEST-ONLY variant of the library, never used by the product: bounded
     pipeline waits give up after 2 ms instead of 1 s, and msa_test_starve(k)
-    makes CTA 0 of one kernel leave out its first Q tile, so that the tests
-    can drive the timeout path.  Built into _build/starve/."""
+    makes CTA 0 of one kernel leave out its first Q tile or a part of it, so
+    that the tests can drive the timeout path.  Built into _build/starve/."""
     d = os.path.join(BUILD, "starve")
     return _build(d, os.path.join(d, "libmsa_starve.so"),
                   ["-DMSA_TEST_STARVE", "-DMSA_WAIT_TIMEOUT_NS=2000000ull"], force, verbose)

@@ -213,13 +213,16 @@ using namespace msa;
 namespace msa {
 cudaError_t test_set_starve_fwd(int which);  // attn_fwd.cu
 cudaError_t test_set_starve_bwd(int which);  // attn_bwd.cu
+cudaError_t test_set_starve_tree(int which);  // paged_tree.cu
 }  // namespace msa
 // Test-only build: make CTA 0 of one kernel (1: fwd_group, 2: fwd_main,
-// 3: bwd_main, 0: none) leave out its first Q tile, so that a bounded
-// pipeline wait runs out and the call reports MSA_ERR_TIMEOUT.
+// 3: bwd_main, 4: paged_tree, 0: none) leave out its first Q tile or a part of
+// it, so that a bounded pipeline wait runs out and the call reports
+// MSA_ERR_TIMEOUT.
 extern "C" msa_status msa_test_starve(int32_t which) {
-  if (which < 0 || which > 3) return MSA_ERR_INVALID_ARG;
-  if (test_set_starve_fwd(which) != cudaSuccess || test_set_starve_bwd(which) != cudaSuccess)
+  if (which < 0 || which > 4) return MSA_ERR_INVALID_ARG;
+  if (test_set_starve_fwd(which) != cudaSuccess || test_set_starve_bwd(which) != cudaSuccess ||
+      test_set_starve_tree(which) != cudaSuccess)
     return MSA_ERR_CUDA;
   return MSA_OK;
 }

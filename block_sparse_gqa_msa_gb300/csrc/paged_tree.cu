@@ -60,6 +60,17 @@
 #include "sm100.cuh"
 
 namespace msa {
+
+#ifdef MSA_TEST_STARVE
+// Test-only build: when set (4), one warp of CTA 0 of k_paged_tree does not tell of its
+// part of the first queries, so that bounded waits run out and the call reports
+// MSA_ERR_TIMEOUT.  Set by msa_test_starve.
+__device__ int g_starve_tree;
+cudaError_t test_set_starve_tree(int which) {
+  return cudaMemcpyToSymbol(g_starve_tree, &which, sizeof which);
+}
+#endif
+
 namespace {
 
 constexpr int kNodes = 64;         // drafted tokens of a row
@@ -446,6 +457,7 @@ struct TreeShared {
   uint64_t odd[8];
   float2 states[2][kTileRows];    // (m, l) of the slots, where they are joined
   uint32_t tmem_base;
+  uint32_t filled[2];             // tiles of keys and of values that were copied
   int abort;
 };
 // The prefix is done with before the first values arrive where it lies.
@@ -1110,12 +1122,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             page = page1;
           }
         } while (ok && walk.next());
-        if (!ok) {  // let tensor copies land before the CTA ends
-          for (uint32_t n = 0; n < stages; ++n) {
-            const uint32_t st = (stage + n) % stages, r = st >= stage ? round - 1 : round;
-            if (st < stage || round > 0) mbar_wait_drain(smem_u32(&full[st]), r & 1);
-          }
-        }
+        if (lane == 0) sh.filled[values] = nt;
       } else {
         // ---------------- tensor cores
         tree_mma_role<T, kDim>(a, bars, walk, warp, tmem, sbase, abort_flag);
@@ -1180,6 +1187,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         asm volatile("cp.async.wait_all;" ::: "memory");
         fence_proxy_async_smem();
         __syncwarp();
+#ifdef MSA_TEST_STARVE
+        if (!(g_starve_tree == 4 && blockIdx.x == 0 && segs == 1 && warp == kSoftWarp0))
+#endif
         if (lane == 0) mbar_arrive(smem_u32(&bars.q_full[x]));
         path = 0;
         // (does the segment reach the drafted tokens?)
@@ -1384,9 +1394,20 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     }
   }
   // ---------------- teardown
-  if (tid == 0 && sh.abort) raise_paged(a.table.status, MSA_ERR_TIMEOUT);
   tc_fence_before();
   __syncthreads();
+  // (behind the barrier: any of the roles may be the last to give up)
+  if (*abort_flag) {
+    if (tid == 0) raise_paged(a.table.status, MSA_ERR_TIMEOUT);
+    // Tensor copies that nobody has waited for land before the CTA ends.
+    if (warp >= kCopyWarp0 && warp < kSoftWarp0) {
+      const bool values = warp != kCopyWarp0;
+      const uint32_t stages = values ? S::kVStages : S::kKStages, n = sh.filled[values];
+      for (uint32_t t = n > stages ? n - stages : 0; t < n; ++t)
+        mbar_wait_drain(smem_u32(&(values ? bars.v_full : bars.k_full)[t % stages]),
+                        t / stages & 1);
+    }
+  }
   if (warp == 0) tmem_dealloc(tmem, 512);
 }
 

@@ -663,7 +663,7 @@ msa_status msa_norm_rope_backward(const msa_norm_rope_args* args, const void* dq
  * -1 (MSA_ERR_BAD_TREE).  Offsets as for msa_paged_append; a row whose offsets
  * are negative, decrease or pass T has no tokens (MSA_ERR_BAD_OFFSETS).  Keys in
  * a bad page are left out (MSA_ERR_BAD_PAGE); a token all of whose keys are gets
- * O = 0, LSE = -inf.  1 <= T <= 2^20.
+ * O = 0, LSE = -inf.  MSA_ERR_TIMEOUT as for msa_paged_decode.  1 <= T <= 2^20.
  */
 msa_status msa_paged_tree_workspace_bytes(const msa_paged_cache* cache, int32_t rows, int64_t T,
                                           int32_t q_heads, size_t* bytes);
