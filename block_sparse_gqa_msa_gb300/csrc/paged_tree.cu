@@ -1399,14 +1399,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   // (behind the barrier: any of the roles may be the last to give up)
   if (*abort_flag) {
     if (tid == 0) raise_paged(a.table.status, MSA_ERR_TIMEOUT);
-    // Tensor copies that nobody has waited for land before the CTA ends.
-    if (warp >= kCopyWarp0 && warp < kSoftWarp0) {
-      const bool values = warp != kCopyWarp0;
-      const uint32_t stages = values ? S::kVStages : S::kKStages, n = sh.filled[values];
-      for (uint32_t t = n > stages ? n - stages : 0; t < n; ++t)
-        mbar_wait_drain(smem_u32(&(values ? bars.v_full : bars.k_full)[t % stages]),
-                        t / stages & 1);
-    }
+    // Tensor copies that nobody has waited for land before the CTA ends: a thread a stage,
+    // its last copy.  (With whole warps in turn heads of 64 channels spill registers.)
+    const bool values = tid >= kMaxStages;
+    const uint32_t stages = values ? S::kVStages : S::kKStages, n = sh.filled[values];
+    const uint32_t stage = tid % kMaxStages;
+    if (tid < 2 * kMaxStages && stage < stages && stage < n)
+      mbar_wait_drain(smem_u32(&(values ? bars.v_full : bars.k_full)[stage]),
+                      (n - 1 - stage) / stages & 1);
+    __syncwarp();
   }
   if (warp == 0) tmem_dealloc(tmem, 512);
 }
