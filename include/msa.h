@@ -657,6 +657,9 @@ msa_status msa_norm_rope_backward(const msa_norm_rope_args* args, const void* dq
  * Keys that a token does not see may hold anything, and so may the values of
  * drafted tokens that it does not see.  The cached tokens' values are finite: with
  * q2k one that is not may reach all tokens of its row.
+ * Values of a bf16 cache that are seen are at most 2^60 in size: weights reach 2^30
+ * before they are scaled down, and the sums of 2^30 keys have to stay inside 32 bits.
+ * Beyond, a result may be infinite where its exact value is not.
  * Nothing is written for padding.  A row of more than 64 tokens
  * (MSA_ERR_BAD_TREE) and a row whose kv_len plus tokens do not fit its part of
  * the table (MSA_ERR_BAD_PAGE) get O = 0, LSE = -inf.  A bad parent is taken as

@@ -6,7 +6,8 @@ import torch
 
 from block_sparse_gqa_msa_gb300 import api
 from oracle import drafts
-from tests.test_gpu_drafts import BF, DEV, FP, HALF, TINY, _freq, _gen, _i32, _np, _randn, _within
+from tests.test_gpu_drafts import (BF, DEV, FP, HALF, TINY, _choose, _freq, _gen, _i32, _np, _pages,
+                                   _pool, _randn, _within)
 
 pytestmark = pytest.mark.gpu
 
@@ -36,3 +37,31 @@ def test_norm_without_eps(dt, dim, hq, hk, rot, T, inter):
         bx, bw = drafts.norm_back_bounds(G, X, W, dx, sums, p, f, rot, inter, 0.0, HALF[dt], TINY[dt])
         _within(_np(back[i]), dx, bx, "dx")
         _within(_np(back[i + 2]), dw, bw, "dw")
+
+
+# ------------------------------------------------------------------ attention
+@pytest.mark.parametrize("dim,share,S,trees,sparse", [
+    (128, 16, 64, [16, 4], False), (64, 3, 16, [5, 64], False), (128, 7, 4, [9, 40], True)])
+def test_tree_values_of_the_largest_size(dim, share, S, trees, sparse):
+    """Values of 2^60 and scores that grow along the row, so that weights become large
+    before the state is scaled."""
+    rng, gen, kv = np.random.default_rng(dim), _gen(dim), 2
+    lens = [3000, 700]
+    offs = np.concatenate([[0], np.cumsum(trees)])
+    T = int(offs[-1])
+    pool, table = _pages(rng, [n + m for n, m in zip(lens, trees)], S)
+    kc = _pool(gen, pool, S, kv, dim, BF)
+    vc = _pool(gen, pool, S, kv, dim, BF)
+    vc = torch.where(vc >= 0, 2.0 ** 60, -2.0 ** 60).to(BF)
+    for r, (n, m) in enumerate(zip(lens, trees)):
+        for j in range(n + m):
+            kc[int(table[r, j // S]), j % S] *= 3.0 * j / (n + m)
+    q = _randn(gen, (T, kv * share, dim), BF)
+    q2k = _choose(rng, lens, offs, T, kv) if sparse else None
+    ref = drafts.tree(_np(kc), _np(vc), _np(q), table, offs, lens, None, 0.5, q2k, HALF[BF], TINY[BF])
+    cache = api.PagedCache(kc, vc)
+    o, lse = api.msa_paged_tree(cache, q, _i32(table), _i32(offs), _i32(lens), 0.5,
+                                q2k=None if q2k is None else _i32(q2k))
+    assert api.msa_paged_read_status(cache) == 0
+    _within(_np(o), ref[0], ref[2], "O")
+    _within(_np(lse), ref[1], ref[3], "LSE")
