@@ -18,12 +18,19 @@
 // vocab, where 32 bits would draw a neighbour, and 64-bit additions are 1/64 as
 // fast here as 32-bit ones (they would take ten times as long as the reading).
 // So a lane adds in pairs of 32-bit numbers (the sum and what its rounding lost,
-// exact two-sums), which are put together in 64 bits once a warp: 2^-40 of the
-// sum at worst.  The drawn token's run is then added again, finer, until a warp
-// looks at 32 values at a time.
+// exact two-sums).  What was lost is itself rounded at every addition, so its error
+// grows with the square of their number: in one pair for all, 151000 values of a thread
+// block were up to 2^-37 of the sum off, 2^20 values 2^-31.  Hence a pair takes 16
+// additions and then goes into a sum of three numbers.  With u = 2^-24 and s what a
+// lane's two pairs add up, the 16 are off by (1 + .. + 16) u^2 s, putting the two
+// together by 50 u^2 s, at most 1024 sums of three by 2^29 u^3 of the lane's sum, a pair
+// of that by u^2, five exchanges between lanes by 40 u^2 of the warp's: less than 2^-40
+// of the sum.  (Adding the pairs up in 64 bits: 128 rows of 151000 60.5 us, not 56.5.)
+// The drawn token's run is then added again, finer, until a warp looks at 32 values at
+// a time.
 //
 // Measured: one row, 32000 tokens in the vocabulary, 9.5 us; 40 rows, 100003, no q,
-// 15.9; 128 rows, 151000, with q, 53 to 56 (125 MB, two passes in the longest rows).
+// 16.6; 128 rows, 151000, with q, 56.5 (125 MB, two passes in the longest rows).
 // A pass of a row by itself takes about 20 us there: a value costs 14 to 20
 // instructions, and eight loads of a lane are on their way at a time.  16 bytes a load
 // are as fast; a ring of asynchronous copies (80 to 100 us) and loads kept in
@@ -54,14 +61,19 @@ struct VerifyArgs {
   int32_t vocab, max_path, cluster;
 };
 
+// a + b in a; returns what its rounding lost, exactly.
+__device__ __forceinline__ float two_sum(float& a, float b) {
+  const float s = __fadd_rn(a, b);
+  const float t = __fsub_rn(s, a);
+  const float lost = __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t));
+  a = s;
+  return lost;
+}
 // A sum in two 32-bit numbers.
 struct Pair32 {
   float hi, lo;
   __device__ __forceinline__ void add(float x) {  // exact but for lo's own rounding
-    const float s = __fadd_rn(hi, x);
-    const float b = __fsub_rn(s, hi);
-    lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(x, b)));
-    hi = s;
+    lo = __fadd_rn(lo, two_sum(hi, x));
   }
   __device__ __forceinline__ void add(const Pair32& o) {
     add(o.hi);
@@ -83,6 +95,21 @@ __device__ __forceinline__ Pair32 warp_sum(Pair32 s) {
   }
   return s;
 }
+// A sum of such sums in three numbers.
+struct Sum32 {
+  float hi, mid, lo;
+  __device__ __forceinline__ void add(const Pair32& o) {
+    const float a = two_sum(hi, o.hi);
+    const float b = two_sum(mid, a);
+    lo = __fadd_rn(lo, __fadd_rn(b, two_sum(mid, o.lo)));
+  }
+  // As a pair, lo no more than hi's rounding.
+  __device__ __forceinline__ Pair32 pair() const {
+    Pair32 s{hi, 0.f};
+    s.lo = __fadd_rn(two_sum(s.hi, mid), lo);
+    return s;
+  }
+};
 // Sum of v over the lanes up to this one, of the first kLanes lanes.
 template <int kLanes>
 __device__ __forceinline__ double scan(double v) {
@@ -143,17 +170,24 @@ struct Rest {
 };
 
 // Sum of r over [lo, hi), by a warp.
+constexpr int kVerFold = 4;  // steps of 2 x 4 additions to a pair
+static_assert(kVerFold * kVerLoads / 2 == 16, "the sums' bound");
 __device__ __forceinline__ Pair32 run_sum(const Rest& rest, int32_t lo, int32_t hi) {
   const int lane = threadIdx.x & 31;
-  Pair32 s[2] = {{0.f, 0.f}, {0.f, 0.f}};
-  for (int32_t x0 = lo + lane; x0 < hi; x0 += 32 * kVerLoads) {
-    float r[kVerLoads];
-    rest.load(r, x0, hi);
+  Sum32 sum{0.f, 0.f, 0.f};
+  for (int32_t x0 = lo + lane; x0 < hi;) {
+    Pair32 s[2] = {{0.f, 0.f}, {0.f, 0.f}};
+#pragma unroll 1
+    for (int i = 0; i < kVerFold && x0 < hi; ++i, x0 += 32 * kVerLoads) {
+      float r[kVerLoads];
+      rest.load(r, x0, hi);
 #pragma unroll
-    for (int e = 0; e < kVerLoads; ++e) s[e & 1].add(r[e]);
+      for (int e = 0; e < kVerLoads; ++e) s[e & 1].add(r[e]);
+    }
+    s[0].add(s[1]);
+    sum.add(s[0]);
   }
-  s[0].add(s[1]);
-  return warp_sum(s[0]);
+  return warp_sum(sum.pair());
 }
 
 __global__ void __launch_bounds__(kVerThreads, 2) k_tree_verify(const VerifyArgs a) {

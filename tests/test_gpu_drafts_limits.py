@@ -65,3 +65,37 @@ def test_tree_values_of_the_largest_size(dim, share, S, trees, sparse):
     assert api.msa_paged_read_status(cache) == 0
     _within(_np(o), ref[0], ref[2], "O")
     _within(_np(lse), ref[1], ref[3], "LSE")
+
+
+# ------------------------------------------------------------------ verification
+@pytest.mark.parametrize("rows,V", [(160, 151000), (160, 700001), (160, 1 << 20), (1, 1 << 22)])
+def test_verify_sums_keep_their_bits(rows, V):
+    """Few likely tokens and many of 2^-35 or so: a drawn token's place needs a sum of
+    as many bits.  Probabilities are whole numbers of 2^-59, so the place is exact."""
+    rng = np.random.default_rng(V)
+    p = np.full(V, 2.0 ** -35, np.float32)
+    p[V // 2:] = np.float32(1.9999 * 2.0 ** -35)
+    likely = np.concatenate([np.arange(64) + V * b // 16 for b in range(16)])
+    p[likely] = 2.0 ** -10
+    run = np.cumsum((p.astype(np.float64) * 2.0 ** 59).astype(np.int64))
+    total = int(run[-1])
+    small = np.setdiff1d(np.arange(V // 2), likely)
+    u, want = [], []
+    while len(u) < rows:
+        x = int(rng.choice(small))
+        g = np.float32(run[x] / total)
+        goal = int(float(g) * 2 ** 32) * total  # (exact: 24 bits from 2^-8 on)
+        if g < 2.0 ** -8:
+            continue
+        x = int(np.searchsorted(run, goal >> 32, side="right"))
+        lo, hi = int(run[x - 1]) << 32, int(run[x]) << 32
+        # the sum, the running sum and what is formed of them: 2^-40 of the sum each
+        if p[x] == p[small[0]] and min(goal - lo, hi - goal) > total << 32 >> 38:
+            u.append(g)
+            want.append(x)
+    target = torch.as_tensor(p, device=DEV).expand(rows, V).contiguous()
+    path, count, last = api.msa_tree_verify(
+        target, _i32([0] * rows), _i32(range(rows + 1)), torch.zeros(rows, device=DEV),
+        torch.as_tensor(np.array(u), device=DEV), max_path=1)
+    assert (count == 1).all() and (path == 0).all()
+    assert last.tolist() == want
