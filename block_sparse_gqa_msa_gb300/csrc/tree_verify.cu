@@ -275,7 +275,8 @@ __global__ void __launch_bounds__(kVerThreads, 2) k_tree_verify(const VerifyArgs
         if (a.draft) {
           if (rejected > 0 && !summed) break;  // (to the sum, and back here)
           if (rejected > 0) S = R;
-          const float f = rejected == 0 ? 1.f : S > 0.0 ? float(1.0 / S) : 0.f;
+          float f = rejected == 0 ? 1.f : S > 0.0 ? float(1.0 / S) : 0.f;
+          if (isinf(f)) f = 0.f;  // infinity times r would leave no distribution
           rest_of(cur, rejected).left(mine, q, tok[kid]);
           keep = double(us[kid]) * double(q[0]) < double(mine[0]) * double(f);
           if (!keep) {

@@ -682,7 +682,8 @@ msa_status msa_paged_tree(const msa_paged_cache* cache, const msa_page_table* ta
  * whose parent is c, in order of their number, and goes on from the first that it
  * keeps.  With x = tokens[j], p = target[c], q = draft[c], S = 1 and r = p at first:
  *   with draft     keep j if u[j] q(x) < r(x) f, f = fp32(1 / S); else
- *                  r = max(r f - q, 0) for every token, S = sum of r
+ *                  r = max(r f - q, 0) for every token, S = sum of r.  f = 0 where
+ *                  1 / S passes fp32's range: so little is left that it is nothing
  *   without        (drafts that were not drawn) keep j if r(x) > 0 and
  *                  u[j] S < r(x); else S = S - r(x), r(x) = 0
  * Where none is kept (there may be no child), the row's last token is drawn: the

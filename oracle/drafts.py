@@ -156,7 +156,10 @@ def verify(target, tokens, offs, u, u_last, draft=None, parents=None, max_path=6
                     continue
                 if draft is not None:
                     q = draft[t0 + cur].astype(f32)
-                    f = f32(1.0 / S) if S > 0 else f32(0)
+                    with np.errstate(over="ignore"):
+                        f = f32(1.0 / S) if S > 0 else f32(0)
+                    if np.isinf(f):  # so little is left that it is nothing
+                        f = f32(0)
                     if float(u[t0 + j]) * float(q[x]) < float(r[x]) * float(f):
                         at = j
                         break

@@ -3,6 +3,10 @@ cannot show, and the binding's."""
 import os
 import re
 
+import numpy as np
+
+from oracle import drafts
+
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
                     "block_sparse_gqa_msa_gb300", "csrc")
 
@@ -23,3 +27,23 @@ def test_a_warp_group_moves_its_registers_in_one_place():
     # and that group is whole warp groups
     roles = dict(re.findall(r"\b(kCopyWarps|kCopyWarp0) = (\d+)", code))
     assert (int(roles["kCopyWarp0"]) + int(roles["kCopyWarps"])) % 4 == 0
+
+
+def tiny_rest():
+    """Rows where the first draft is not kept and leaves 1e-40, whose reciprocal passes
+    fp32's range, or 1e-37, whose reciprocal does not; the second draft is a token
+    without probability, or the one that is left."""
+    p, q = np.zeros((12, 16), np.float32), np.zeros((12, 16), np.float32)
+    for row, left in enumerate((1e-40, 1e-37) * 2):
+        p[3 * row, 7], p[3 * row, 5], p[3 * row + 2, 9] = 0.5, left, 1.0
+        q[3 * row, 7] = 1.0
+    return dict(target=p, draft=q, tokens=[0, 7, 3] * 2 + [0, 7, 5] * 2, offs=[0, 3, 6, 9, 12],
+                parents=[-1, 0, 0] * 4, u=np.full(12, 0.75, np.float32),
+                u_last=np.full(4, 0.5, np.float32), max_path=3)
+
+
+def test_a_rest_too_small_for_fp32_is_nothing():
+    """The target itself is drawn from then: half of its sum is reached at token 7."""
+    path, count, last = drafts.verify(**tiny_rest())
+    assert path.tolist() == [[0, -1, -1]] * 3 + [[0, 2, -1]]
+    assert count.tolist() == [1, 1, 1, 2] and last.tolist() == [7, 5, 7, 9]

@@ -6,6 +6,7 @@ import torch
 
 from block_sparse_gqa_msa_gb300 import api
 from oracle import drafts
+from tests.test_drafts_rules import tiny_rest
 from tests.test_gpu_drafts import (BF, DEV, FP, HALF, TINY, _choose, _freq, _gen, _i32, _np, _pages,
                                    _pool, _randn, _within)
 
@@ -99,3 +100,13 @@ def test_verify_sums_keep_their_bits(rows, V):
         torch.as_tensor(np.array(u), device=DEV), max_path=1)
     assert (count == 1).all() and (path == 0).all()
     assert last.tolist() == want
+
+
+def test_verify_rest_too_small_for_fp32():
+    a = tiny_rest()
+    f32 = lambda x: torch.as_tensor(x, device=DEV)
+    got = api.msa_tree_verify(f32(a["target"]), _i32(a["tokens"]), _i32(a["offs"]), f32(a["u"]),
+                              f32(a["u_last"]), draft=f32(a["draft"]), parents=_i32(a["parents"]),
+                              max_path=3)
+    for x, want in zip(got, drafts.verify(**a)):
+        assert x.tolist() == want.tolist()
