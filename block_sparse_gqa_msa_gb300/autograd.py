@@ -9,17 +9,54 @@ the backward consumes them).  Argument marshalling only: every step runs in
 libmsa.so's kernels; there is no fallback.
 
 Gradients flow to Q, K and V.  LSE is returned for inspection but is not
-differentiable (the backward of the pages takes dO only).
+differentiable (the backward of the pages takes dO only).  Gradients of
+gradients are not offered: autograd cannot see into the library's kernels, so
+asking for one raises.
 """
 from __future__ import annotations
 
+import functools
 import math
 
 import torch
-
 from . import api
 
 HEAD_DIM = 128
+
+
+class _Refuse(torch.autograd.Function):
+    """Hands on the first n tensors, as results of all of them; its backward raises."""
+
+    @staticmethod
+    def forward(ctx, n, *tensors):
+        return tensors[:n]
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError("gradients of msa_attention and msa_norm_rope have no gradients of "
+                           "their own (create_graph=True)")
+
+
+def _once(backward):
+    """A backward whose results raise where they are differentiated again.  torch's own
+    once_differentiable lets them pass as constants where the gradients that come in are
+    constants, though they depend on the saved tensors."""
+
+    @functools.wraps(backward)
+    def wrapped(ctx, *grads):
+        if not torch.is_grad_enabled():  # without create_graph
+            return backward(ctx, *grads)
+        with torch.no_grad():
+            out = backward(ctx, *grads)
+        at = [i for i, x in enumerate(out) if x is not None]
+        from_ = [x for x in (*grads, *ctx.saved_tensors) if x is not None and x.requires_grad]
+        out = list(out)
+        if at and from_:
+            for i, x in zip(at, _Refuse.apply(len(at), *(out[i] for i in at), *from_)):
+                out[i] = x
+        return tuple(out)
+
+    return wrapped
 
 
 class MSAFunction(torch.autograd.Function):
@@ -35,6 +72,7 @@ class MSAFunction(torch.autograd.Function):
         return o, lse
 
     @staticmethod
+    @_once
     def backward(ctx, do, _dlse):
         q, k, v, o, lse = ctx.saved_tensors
         if do is None:
@@ -79,6 +117,7 @@ class NormRopeFunction(torch.autograd.Function):
         return q_out, k_out
 
     @staticmethod
+    @_once
     def backward(ctx, dq_out, dk_out):
         q, k, q_weight, k_weight, positions, inv_freq = ctx.saved_tensors
         dq, dk, dwq, dwk = api.msa_norm_rope_backward(

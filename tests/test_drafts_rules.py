@@ -4,7 +4,10 @@ import os
 import re
 
 import numpy as np
+import pytest
+import torch
 
+from block_sparse_gqa_msa_gb300 import api, autograd
 from oracle import drafts
 
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
@@ -47,3 +50,37 @@ def test_a_rest_too_small_for_fp32_is_nothing():
     path, count, last = drafts.verify(**tiny_rest())
     assert path.tolist() == [[0, -1, -1]] * 3 + [[0, 2, -1]]
     assert count.tolist() == [1, 1, 1, 2] and last.tolist() == [7, 5, 7, 9]
+
+
+def _stand_in_norm(q, k, q_weight, k_weight, *_, **__):
+    return q * q_weight, k * k_weight
+
+
+def _stand_in_norm_backward(dq, dk, q, k, q_weight, k_weight, *_, **__):
+    return dq * q_weight, dk * k_weight, (dq * q).sum((0, 1)), (dk * k).sum((0, 1))
+
+
+@pytest.mark.parametrize("op", ["norm", "attention"])
+def test_second_derivatives_raise(monkeypatch, op):
+    """A gradient penalty must not lose its term in silence.  (Kernels replaced by
+    arithmetic on the CPU; what is tested is what autograd does with their results.)"""
+    x = torch.randn(3, 2, 4).requires_grad_()
+    if op == "norm":
+        monkeypatch.setattr(api, "msa_norm_rope", _stand_in_norm)
+        monkeypatch.setattr(api, "msa_norm_rope_backward", _stand_in_norm_backward)
+        w = torch.randn(4).requires_grad_()
+        out = sum(y.sum() for y in autograd.msa_norm_rope(x, x, w, w))
+        leaves = (x, w)
+    else:
+        monkeypatch.setattr(api, "msa_forward", lambda p, q, k, v, s: (q * k * v, q.sum(2)))
+        monkeypatch.setattr(api, "msa_backward", lambda p, q, k, v, o, lse, do, s: (do * k * v,) * 3)
+        out = autograd.MSAFunction.apply(x, x, x, None, 1.0)[0].sum()
+        leaves = (x,)
+    # first derivatives are the same
+    plain = torch.autograd.grad(out, leaves, retain_graph=True)
+    assert not any(g.requires_grad for g in plain)
+    grads = torch.autograd.grad(out, leaves, create_graph=True)
+    assert all(torch.equal(a, b) for a, b in zip(grads, plain))
+    other = (x ** 2).sum()  # a loss that is differentiable beside it
+    with pytest.raises(RuntimeError, match="no gradients of their own"):
+        (other + sum((g ** 2).sum() for g in grads)).backward()
