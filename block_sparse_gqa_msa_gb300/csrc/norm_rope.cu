@@ -19,8 +19,9 @@
 //
 // Measured (16384 tokens of 64 + 4 heads of 128 channels): 93 us forward, 6.1 TB/s,
 // and 141 the gradient, 6.1 TB/s, of a plain copy's 6.8; 9 tokens of 24 + 8 heads
-// of 64 channels 3.1 us.  With the loads in registers, a head's at a time, the two
-// took 300 us together instead of 265.
+// of 64 channels 3.2 us.  With the loads in registers, a head's at a time, the two
+// took 300 us together instead of 265.  Few heads do not hide a token's angles: 16384
+// tokens of 16 + 2 heads of 128 channels 29 us without rotation, 42 with all turned.
 #include <algorithm>
 
 #include "paged.cuh"

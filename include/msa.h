@@ -695,7 +695,7 @@ msa_status msa_paged_tree(const msa_paged_cache* cache, const msa_page_table* ta
  *   target  fp32 [T][vocab] device, rows target_stride elements apart: row t the
  *           distribution behind token t, not negative, sum 1; any alignment of 4
  *   draft   the same for the drafting model, draft_stride; or NULL
- *   tokens  int32 [T], u fp32 [T] (entries of tokens 0 are not read)
+ *   tokens  int32 [T], u fp32 [T] (what they hold for tokens 0 does not matter)
  *   parents int32 [T] or NULL (a chain), u_last fp32 [rows]
  *   path    int32 [rows][max_path]: the numbers, within the row, of token 0 and the
  *           kept ones, ascending, then -1.  1 <= max_path <= 64; a walk ends at
