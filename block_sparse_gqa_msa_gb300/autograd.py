@@ -19,6 +19,7 @@ import functools
 import math
 
 import torch
+
 from . import api
 
 HEAD_DIM = 128

@@ -449,8 +449,8 @@ extern "C" msa_status msa_tree_verify(const float* target, int64_t target_stride
   // As many CTAs a row as are on the chip at once (2 an SM), none with less than a pass
   // of its loads to do.  With q, where rows of several passes keep the others waiting,
   // twice as many where each still has kVerRun values: half of the rows begin as others
-  // end (100 rows, 151000 tokens: 61 -> 49 us, 200 rows, 65536: 57 -> 42; below it
-  // 128 rows, 40000: 26 -> 29; without q 128 rows, 151000: 34 -> 38).
+  // end (100 rows, 151000 tokens: 63.5 -> 50.5 us, 200 rows, 65536: 58 -> 43; below it
+  // 128 rows, 40000: 26 -> 30; without q 128 rows, 151000: 34 -> 38).
   auto chip = [&](int n) { return int64_t(rows) * n <= int64_t(device_sm_count()) * 2; };
   int cluster = 1;
   while (cluster < kVerCluster && vocab >= cluster * 2 * kVerThreads * 4 &&
