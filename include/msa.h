@@ -567,7 +567,8 @@ msa_status msa_paged_decode(const msa_paged_cache* cache, const msa_page_table* 
  *   inv_freq  fp32 [rotary_dim / 2], or NULL for no rotation (rotary_dim is then
  *          ignored); rotary_dim a multiple of 16, at most head_dim
  *   interleaved as for msa_paged_append
- *   q_out, k_out  contiguous; may be q or k itself where that is contiguous
+ *   q_out, k_out  contiguous; q_out may be q itself and k_out k itself where that is
+ *          contiguous, else they must not overlap the inputs or one another
  * Sums, norms and rotation are 32 bits, angles 64, and each result is rounded
  * once.  eps >= 0, finite (with eps = 0 a head of zeros gives NaN, as the formula
  * does); 1 <= T <= 2^20.
